@@ -501,6 +501,162 @@ int luce_decode_step_paged(const luce_model* m, const luce_paged_slot* slots, co
                            int n_seq, float* x, float* logits, int32_t* argmax,
                            void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- draft trees */
+
+/*
+ * A slot's tree of drafted tokens over its cache for one layer.  The prefix
+ * is the cache's keys 0 .. len - 1; node j's K and V are at cache position
+ * len + j, and its query/output row is row0 + j.  parent (host) [n_nodes]
+ * names each node's parent, parent[j] in [-1, j) with -1 for a node that
+ * follows the prefix directly (several may: a forest); NULL is the chain
+ * -1, 0, 1, ..  Node j attends to the prefix, to its ancestors and to itself.
+ * Element (g, i, d) of K (and V) is at k[g*head_stride + i*tok_stride + d],
+ * binary16.  K, V and q that a node sees must be finite, |q| < 65504; what
+ * the cache holds at positions no row sees (other branches excepted: every
+ * node's row is its own row's key) is not used, whatever it is.
+ */
+#define LUCE_MAX_TREE 16
+typedef struct luce_treeview {
+    const uint16_t* k;      /* (device), 16-byte aligned */
+    const uint16_t* v;      /* (device), 16-byte aligned */
+    int32_t len;            /* keys of the prefix, >= 0 */
+    int32_t n_nodes;        /* 1..LUCE_MAX_TREE */
+    int32_t row0;
+    int32_t cap;            /* positions the view holds (len + n_nodes <= cap) */
+    int64_t head_stride;    /* elements, multiple of 8 */
+    int64_t tok_stride;     /* elements, multiple of 8, >= D */
+    const int32_t* parent;  /* (host) [n_nodes] or NULL */
+} luce_treeview;
+
+/*
+ * The same over pages (luce_pagedview's pools and table, which holds
+ * ceil((len + n_nodes) / LUCE_PAGE_KEYS) entries).  n_pages bounds the table's
+ * entries: a page outside [0, n_pages) is never read, its keys and values
+ * count as zero.
+ */
+typedef struct luce_pagedtreeview {
+    const uint16_t* k_pool; /* (device) [n_pages][Hkv][128][128], 16-byte aligned */
+    const uint16_t* v_pool; /* (device) same layout */
+    const int32_t* table;   /* (device) page of each 128-key span */
+    int32_t n_pages;
+    int32_t len;            /* keys of the prefix, >= 0 */
+    int32_t n_nodes;        /* 1..LUCE_MAX_TREE */
+    int32_t row0;
+    const int32_t* parent;  /* (host) [n_nodes] or NULL */
+} luce_pagedtreeview;
+
+/*
+ * Attention of every node of up to 4 slots' draft trees.  For row r of node j
+ * and query head h (KV head g = h / (Hq/Hkv)), over the keys i that j sees:
+ *   s_i = scale * q[r][h] . K[g][i],  m = max s_i,  l = sum e^(s_i - m),
+ *   out[r][h] = sum (e^(s_i - m) / l) V[g][i]
+ * The prefix is cut into chunks whose size follows from len alone; the node's
+ * own path is added to their merge in path order.  So a node's outputs depend
+ * on its prefix and its path only: it gives the same bits in any tree, in a
+ * chain of its own path, with any other slots, flat or paged.
+ *   q      (device) fp32 [T][Hq][D], 16-byte aligned; T = max(row0 + n_nodes)
+ *   out    (device) fp32 [T][Hq][D]
+ *   scores (device) fp32 [T][Hq][lds] or NULL: s_i at column i, the cache
+ *          position; -inf at the columns of [len, len + n_nodes) that the row
+ *          does not see; later columns are left as they were.  16-byte
+ *          aligned, lds a multiple of 4 and >= every len + n_nodes
+ *   stats  (device) fp32 [T][Hq][2] or NULL: (m, l); e^(s - m) / l is a key's
+ *          attention weight
+ *   ws     (device) scratch of luce_tree_attn_workspace_size(...) bytes,
+ *          256-byte aligned (no initial contents); calls that can overlap on
+ *          the GPU need scratches of their own
+ * D == 128, Hq % Hkv == 0, Hq / Hkv <= 8, 1 <= n_seq <= LUCE_MAX_SEQ, rows
+ * 0 .. T-1 belong to one view each, T <= LUCE_MAX_ROWS,
+ * len + n_nodes <= LUCE_MAX_KEYS.
+ */
+int luce_tree_attn(const float* q, const luce_treeview* views, int n_seq, int Hq, int Hkv, int D, float scale,
+                   float* out, float* scores, int64_t lds, float* stats, void* ws, size_t ws_bytes, void* stream);
+int luce_tree_attn_paged(const float* q, const luce_pagedtreeview* views, int n_seq, int Hq, int Hkv, int D,
+                         float scale, float* out, float* scores, int64_t lds, float* stats, void* ws,
+                         size_t ws_bytes, void* stream);
+
+/* Bytes of scratch luce_tree_attn needs for n_rows rows over prefixes of at
+ * most max_len keys (0 for arguments it refuses). */
+size_t luce_tree_attn_workspace_size(int n_rows, int Hq, int D, int max_len);
+
+/*
+ * A slot whose verified tree is committed: the accepted nodes path[0] <
+ * path[1] < .. (a path from the prefix, so ascending) become the keys
+ * len .. len + n_path - 1.
+ */
+typedef struct luce_commit_slot {
+    uint16_t* k;          /* (device) [n_layers][Hkv][cap][128], 16-byte aligned */
+    uint16_t* v;          /* (device) same layout */
+    int32_t len;          /* keys of the prefix */
+    int32_t cap;
+    int32_t n_path;       /* accepted nodes, 0..LUCE_MAX_TREE (0: nothing is done for the slot) */
+    int32_t row0;         /* the row of the slot's node 0 in scores */
+    const int32_t* path;  /* (host) [n_path], len + path[i] < cap */
+    float* acc;           /* (device) [n_layers][Hkv][cap] accumulated weights, or NULL */
+    int32_t* pos;         /* (device) [n_layers][Hkv][cap] positions of the keys, or NULL */
+    int32_t pos0;         /* the position of path[0] */
+} luce_commit_slot;
+
+/*
+ * Commit of up to 4 slots' accepted paths, in every layer and KV head:
+ *   K and V row len + path[i] moves to len + i (other rows are left as they were);
+ *   pos[len + i] = pos0 + i, where pos is given;
+ *   where acc is given, with w_j the sum over the accepted nodes' rows r and
+ *   the KV head's query heads h (rows in path order, heads ascending) of
+ *   e^(scores[r][h][j] - m) / l:
+ *     acc[j] += w_j for j < len,  acc[len + i] = w_(len + path[i]).
+ * A row whose l is 0 adds nothing.  The caller then continues with
+ * len + n_path keys.
+ *   scores (device) fp32 [n_layers][n_rows][Hq][lds], 16-byte aligned, lds a
+ *          multiple of 4; stats (device) fp32 [n_layers][n_rows][Hq][2]: what
+ *          luce_tree_attn gave for each layer.  Both may be NULL when no slot
+ *          has acc.
+ * No two slots share a cache, acc or pos.  D == 128, Hq % Hkv == 0,
+ * Hq / Hkv <= 8, 1 <= n_seq <= LUCE_MAX_SEQ, n_layers >= 1.
+ */
+int luce_tree_commit(const luce_commit_slot* slots, int n_seq, int n_layers, int Hq, int Hkv, int D,
+                     const float* scores, int n_rows, int64_t lds, const float* stats, void* stream);
+
+/* ---------------------------------------------------------------- eviction */
+
+/*
+ * A slot's cache with each key's accumulated attention weight and position
+ * (luce_tree_commit keeps both).
+ */
+typedef struct luce_evict_slot {
+    uint16_t* k;          /* (device) [n_layers][Hkv][cap][128], 16-byte aligned */
+    uint16_t* v;          /* (device) same layout */
+    const float* acc;     /* (device) [n_layers][Hkv][cap] */
+    const int32_t* pos;   /* (device) [n_layers][Hkv][cap] */
+    float* acc_out;       /* (device) as acc; may be acc itself */
+    int32_t* pos_out;     /* (device) as pos; may be pos itself */
+    int32_t len;          /* keys cached */
+    int32_t cap;
+    int32_t budget;       /* keys to keep, >= 1 */
+    int32_t sinks;        /* keys at positions < sinks stay */
+    int32_t recent;       /* keys at positions >= next_pos - recent stay */
+    int32_t next_pos;     /* the position of the slot's next token */
+} luce_evict_slot;
+
+/*
+ * Eviction by accumulated attention weight, in every layer and KV head of up
+ * to 4 slots by itself: of the slot's len keys the len - budget with the
+ * lowest acc leave, protected ones (sinks, recent) last; a NaN counts as
+ * lower than any weight, and of equal keys the one with the lowest index
+ * stays.  The keys that stay below index budget keep their place; the i-th
+ * (ascending) that stays at or past it moves into the i-th index below budget
+ * that was left, with its K and V rows, acc and pos - only as many rows move
+ * as must, and attention does not mind the order of its keys.  acc_out and
+ * pos_out receive the first budget entries; everything at or past index
+ * budget is left as it was.  A slot with len <= budget keeps all its keys
+ * (acc_out and pos_out receive their len entries).  The caller then continues
+ * with min(len, budget) keys.
+ * sinks >= 0, recent >= 0, sinks + recent <= budget, len <= cap,
+ * len <= LUCE_MAX_KEYS, D == 128, no two slots share an array, and an output
+ * overlaps no input but its own.
+ */
+int luce_kv_evict(const luce_evict_slot* slots, int n_seq, int n_layers, int Hkv, int D, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -22,6 +22,7 @@ MAX_ROWS_PER_SEQ = 4
 MAX_ROWS = 16
 HEAD_DIM = 128
 MAX_KEYS = 130816
+MAX_TREE = 16
 
 LUCE_OK, LUCE_EINVAL, LUCE_EUNSUPPORTED, LUCE_ECUDA, LUCE_ENOSPACE = 0, -1, -2, -3, -4
 
@@ -68,6 +69,31 @@ class PagedSlotC(ctypes.Structure):
                 ("n_pages", ctypes.c_int32), ("len", ctypes.c_int32)]
 
 
+class TreeViewC(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("len", ctypes.c_int32), ("n_nodes", ctypes.c_int32),
+                ("row0", ctypes.c_int32), ("cap", ctypes.c_int32), ("head_stride", ctypes.c_int64),
+                ("tok_stride", ctypes.c_int64), ("parent", ctypes.POINTER(ctypes.c_int32))]
+
+
+class PagedTreeViewC(ctypes.Structure):
+    _fields_ = [("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int32), ("len", ctypes.c_int32), ("n_nodes", ctypes.c_int32),
+                ("row0", ctypes.c_int32), ("parent", ctypes.POINTER(ctypes.c_int32))]
+
+
+class CommitSlotC(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("len", ctypes.c_int32), ("cap", ctypes.c_int32),
+                ("n_path", ctypes.c_int32), ("row0", ctypes.c_int32), ("path", ctypes.POINTER(ctypes.c_int32)),
+                ("acc", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("pos0", ctypes.c_int32)]
+
+
+class EvictSlotC(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("acc", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+                ("acc_out", ctypes.c_void_p), ("pos_out", ctypes.c_void_p), ("len", ctypes.c_int32),
+                ("cap", ctypes.c_int32), ("budget", ctypes.c_int32), ("sinks", ctypes.c_int32),
+                ("recent", ctypes.c_int32), ("next_pos", ctypes.c_int32)]
+
+
 _LAYOUT_FIELDS = ("xn", "xn_q", "xn_d", "qkv", "q_rot", "part", "attn", "attn_q", "attn_d", "x1",
                   "xn2", "xn2_q", "xn2_d", "gu", "h", "h_q", "h_d", "xf", "xf_q", "xf_d", "total")
 
@@ -83,7 +109,8 @@ EXPORTS = ("luce_last_error", "luce_version", "luce_launch_count", "luce_q8_quan
            "luce_decode_step_paged", "luce_wait_timeouts", "luce_decode_step_host",
            "luce_test_wait_expiry", "luce_q8_matvec_batch_path", "luce_q8_quantize_act_f16", "luce_rmsnorm_q8",
            "luce_swiglu_q8", "luce_step_graph_create", "luce_step_graph_run", "luce_step_graph_stats",
-           "luce_step_graph_destroy")
+           "luce_step_graph_destroy", "luce_tree_attn", "luce_tree_attn_paged", "luce_tree_attn_workspace_size",
+           "luce_tree_commit", "luce_kv_evict")
 
 _lib = None
 
@@ -135,9 +162,16 @@ def load_library(path: str = LIB_PATH):
     lib.luce_step_graph_stats.argtypes = [vp, ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int64),
                                           ctypes.POINTER(ctypes.c_int32)]
     lib.luce_step_graph_destroy.argtypes = [vp]
+    lib.luce_tree_attn.argtypes = [vp, ctypes.POINTER(TreeViewC), i32, i32, i32, i32, f32, vp, vp, i64, vp, vp, sz, vp]
+    lib.luce_tree_attn_paged.argtypes = [vp, ctypes.POINTER(PagedTreeViewC), i32, i32, i32, i32, f32, vp, vp, i64, vp,
+                                         vp, sz, vp]
+    lib.luce_tree_attn_workspace_size.argtypes = [i32, i32, i32, i32]
+    lib.luce_tree_attn_workspace_size.restype = sz
+    lib.luce_tree_commit.argtypes = [ctypes.POINTER(CommitSlotC), i32, i32, i32, i32, i32, vp, i32, i64, vp, vp]
+    lib.luce_kv_evict.argtypes = [ctypes.POINTER(EvictSlotC), i32, i32, i32, i32, vp]
     for name in EXPORTS:
         if name not in ("luce_last_error", "luce_version", "luce_launch_count", "luce_decode_attn_workspace_size",
-                        "luce_decode_attn_noalloc_max_bytes"):
+                        "luce_decode_attn_noalloc_max_bytes", "luce_tree_attn_workspace_size"):
             getattr(lib, name).restype = i32
     _lib = lib
     return lib
@@ -630,3 +664,327 @@ class StepGraph:
             self.close()
         except Exception:
             pass
+
+
+# ------------------------------------------------------------ draft trees and eviction
+
+@dataclass
+class TreeView:
+    """A slot's tree of drafted tokens over its cache for one layer (fp16
+    [Hkv][cap][128] K and V): ``len`` prefix keys, node j's rows at cache
+    position len + j and at row row0 + j of q/out, ``parent[j]`` in [-1, j)
+    (-1: follows the prefix).  An int n instead of a list is the chain of n."""
+    k: object
+    v: object
+    len: int
+    parent: object = 1
+    row0: int = 0
+
+
+@dataclass
+class PagedTreeView:
+    """The same over pools fp16 [n_pages][Hkv][128][128] and a device int32
+    ``table`` of the pool page of each 128-key span."""
+    k_pool: object
+    v_pool: object
+    table: object
+    len: int
+    parent: object = 1
+    row0: int = 0
+
+
+@dataclass
+class CommitSlot:
+    """A slot's cache of every layer (fp16 [n_layers][Hkv][cap][128]) whose tree's
+    nodes ``path`` (ascending) were accepted; ``row0`` is the score row of node
+    0, ``acc`` (fp32) and ``pos`` (int32), [n_layers][Hkv][cap], its keys'
+    accumulated weights and positions, ``pos0`` the first accepted node's."""
+    k: object
+    v: object
+    len: int
+    path: object
+    row0: int = 0
+    acc: object = None
+    pos: object = None
+    pos0: int = 0
+
+
+@dataclass
+class EvictSlot:
+    """A slot's cache with its keys' accumulated weights and positions (as in
+    CommitSlot), to be cut to ``budget`` keys; acc_out and pos_out default to
+    acc and pos themselves."""
+    k: object
+    v: object
+    acc: object
+    pos: object
+    len: int
+    budget: int
+    sinks: int = 0
+    recent: int = 0
+    next_pos: int = 0
+    acc_out: object = None
+    pos_out: object = None
+
+
+def _tree(parent):
+    """(n_nodes, host int32 array or None) of a parent list or a chain's length."""
+    if isinstance(parent, int):
+        return parent, None
+    p = [int(v) for v in parent]
+    return len(p), (ctypes.c_int32 * max(1, len(p)))(*p)
+
+
+def _same_device(first, *tensors):
+    for t in tensors:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}: one call works on one device")
+
+
+def _kv_pair(k, v, rank, name):
+    import torch
+    for t, w in ((k, "k"), (v, "v")):
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.float16 or not t.is_cuda:
+            raise TypeError(f"{name}.{w}: expected a CUDA float16 tensor")
+        if t.dim() != rank or t.shape[-1] != HEAD_DIM or t.stride(-1) != 1:
+            raise ValueError(f"{name}.{w}: expected {rank} dims, the last of {HEAD_DIM} contiguous values")
+    if k.shape != v.shape or k.stride() != v.stride():
+        raise ValueError(f"{name}: k and v must have the same shape and strides")
+
+
+class _Prepared:
+    """A C call with its arguments marshalled once.  The call goes to the stream
+    given at construction, else to the device's current stream at each call;
+    memory that the object allocated itself belongs to the stream of its
+    construction and is kept from reuse until a call on another one is done."""
+
+    _owned = ()
+    _home = None
+
+    def _bind(self, fn, device, stream, keep):
+        self._fn, self._device, self._stream, self._keep = fn, device, stream, keep
+
+    def _allocate(self, shape, dtype, device, stream):
+        import torch
+        home = stream if stream is not None else torch.cuda.current_stream(device)
+        with torch.cuda.stream(home):
+            t = torch.empty(shape, dtype=dtype, device=device)
+        self._home, self._owned = home, self._owned + (t,)
+        return t
+
+    def _call(self, *args):
+        import torch
+        s = self._stream if self._stream is not None else torch.cuda.current_stream(self._device)
+        if self._owned and s != self._home:
+            for t in self._owned:
+                t.record_stream(s)
+        if torch.cuda.current_device() == self._device.index:
+            _check(self._fn(*args, s.cuda_stream))
+        else:
+            with torch.cuda.device(self._device):
+                _check(self._fn(*args, s.cuda_stream))
+
+
+class TreeAttention(_Prepared):
+    """luce_tree_attn (or luce_tree_attn_paged, for PagedTreeViews) with its
+    arguments marshalled once, for repeated calls over the same buffers: q fp32
+    [T][Hq][128], ``out`` as q, ``scores`` fp32 [T][Hq][lds] and ``stats`` fp32
+    [T][Hq][2] when given.  Each call takes the views' current ``len``.  The
+    object owns its workspace (sized for the views' capacity) unless one is
+    given, so calls of one object must not overlap on the GPU."""
+
+    def __init__(self, q, views, n_kv_heads: int, scale: float, out=None, scores=None, stats=None, ws=None, stream=None):
+        import torch
+        _need(q, torch.float32, "q")
+        if q.dim() != 3:
+            raise ValueError("q: expected [T][Hq][128]")
+        T, Hq, D = q.shape
+        self.views = list(views)
+        if not self.views:
+            raise ValueError("views: expected at least one")
+        paged = isinstance(self.views[0], PagedTreeView)
+        trees = [_tree(v.parent) for v in self.views]
+        rows = max(v.row0 + n for v, (n, _) in zip(self.views, trees))
+        if rows != T:
+            raise ValueError(f"q has {T} rows, the views name {rows}")
+        self.out = self._allocate(q.shape, torch.float32, q.device, stream) if out is None else out
+        _need(self.out, torch.float32, "out")
+        if self.out.shape != q.shape:
+            raise ValueError("out: expected q's shape")
+        lds = 0
+        if scores is not None:
+            _need(scores, torch.float32, "scores")
+            if scores.dim() != 3 or scores.shape[:2] != q.shape[:2]:
+                raise ValueError("scores: expected [T][Hq][lds]")
+            lds = scores.shape[2]
+        if stats is not None:
+            _need(stats, torch.float32, "stats")
+            if stats.shape != (T, Hq, 2):
+                raise ValueError("stats: expected [T][Hq][2]")
+        n = len(self.views)
+        caps = []
+        if paged:
+            self._vc = (PagedTreeViewC * n)()
+            for i, (v, (nn, par)) in enumerate(zip(self.views, trees)):
+                _kv_pair(v.k_pool, v.v_pool, 4, f"views[{i}]")
+                _need(v.k_pool, torch.float16, f"views[{i}].k_pool")
+                _need(v.v_pool, torch.float16, f"views[{i}].v_pool")
+                _need(v.table, torch.int32, f"views[{i}].table")
+                if v.k_pool.shape[1:] != (n_kv_heads, PAGE_KEYS, HEAD_DIM):
+                    raise ValueError(f"views[{i}]: expected pools [n_pages][{n_kv_heads}][128][128]")
+                _same_device(q, v.k_pool, v.v_pool, v.table)
+                caps.append(min(v.table.numel() * PAGE_KEYS, MAX_KEYS) - nn)
+                self._vc[i] = PagedTreeViewC(v.k_pool.data_ptr(), v.v_pool.data_ptr(), v.table.data_ptr(),
+                                             v.k_pool.shape[0], v.len, nn, v.row0, par)
+            name = "luce_tree_attn_paged"
+        else:
+            self._vc = (TreeViewC * n)()
+            for i, (v, (nn, par)) in enumerate(zip(self.views, trees)):
+                _kv_pair(v.k, v.v, 3, f"views[{i}]")
+                if v.k.shape[0] != n_kv_heads:
+                    raise ValueError(f"views[{i}]: {v.k.shape[0]} heads, expected {n_kv_heads}")
+                _same_device(q, v.k, v.v)
+                caps.append(min(v.k.shape[1], MAX_KEYS) - nn)
+                self._vc[i] = TreeViewC(v.k.data_ptr(), v.v.data_ptr(), v.len, nn, v.row0, v.k.shape[1], v.k.stride(0),
+                                        v.k.stride(1), par)
+            name = "luce_tree_attn"
+        _same_device(q, self.out, scores, stats, ws)
+        self._caps = caps
+        if ws is None:
+            need = luce_tree_attn_workspace_size(T, Hq, D, max(0, *caps))
+            ws = self._allocate((max(256, need),), torch.uint8, q.device, stream)
+        _need(ws, torch.uint8, "ws")
+        self._args = (q.data_ptr(), self._vc, n, Hq, int(n_kv_heads), D, float(scale), self.out.data_ptr(), _ptr(scores),
+                      lds, _ptr(stats), ws.data_ptr(), ws.numel())
+        self._bind(getattr(load_library(), name), q.device, stream, (q, scores, stats, ws, trees))
+
+    def __call__(self):
+        for c, v, cap in zip(self._vc, self.views, self._caps):
+            if v.len > cap:
+                raise ValueError(f"len {v.len} and the tree exceed the cache")
+            c.len = v.len
+        self._call(*self._args)
+        return self.out
+
+
+def luce_tree_attn_workspace_size(n_rows: int, Hq: int, D: int, max_len: int) -> int:
+    return int(load_library().luce_tree_attn_workspace_size(n_rows, Hq, D, max_len))
+
+
+def luce_tree_attn(q, views: Sequence[TreeView], n_kv_heads: int, scale: float, out=None, scores=None, stats=None,
+                   ws=None, stream=None):
+    """Attention of the views' draft trees: fp32 q [T][Hq][128] against each
+    node's prefix, ancestors and itself.  Optional ``scores`` [T][Hq][lds] and
+    ``stats`` [T][Hq][2] receive the scaled scores and (max, sum)."""
+    return TreeAttention(q, views, n_kv_heads, scale, out, scores, stats, ws, stream)()
+
+
+def luce_tree_attn_paged(q, views: Sequence[PagedTreeView], n_kv_heads: int, scale: float, out=None, scores=None,
+                         stats=None, ws=None, stream=None):
+    """luce_tree_attn over paged caches (the same bits as a flat cache)."""
+    return TreeAttention(q, views, n_kv_heads, scale, out, scores, stats, ws, stream)()
+
+
+def _state(t, dtype, like, name):
+    _need(t, dtype, name)
+    if t.shape != like.shape[:3]:
+        raise ValueError(f"{name}: expected [n_layers][Hkv][cap] of the cache")
+
+
+class TreeCommit(_Prepared):
+    """luce_tree_commit with its arguments marshalled once: each call takes the
+    slots' current ``len``, ``path``, ``row0`` and ``pos0``.  ``scores``
+    [n_layers][n_rows][Hq][lds] and ``stats`` [n_layers][n_rows][Hq][2] (the
+    n_layers dimension may be left out for one layer) are what
+    luce_tree_attn gave."""
+
+    def __init__(self, slots: Sequence[CommitSlot], n_q_heads: int, scores=None, stats=None, stream=None):
+        import torch
+        self.slots = list(slots)
+        if not self.slots:
+            raise ValueError("slots: expected at least one")
+        L, Hkv = self.slots[0].k.shape[:2]
+        n_rows = lds = 0
+        if scores is not None:
+            _need(scores, torch.float32, "scores")
+            _need(stats, torch.float32, "stats")
+            n_rows, hq, lds = scores.shape[-3:]
+            if hq != n_q_heads or scores.numel() != L * n_rows * hq * lds or stats.numel() != L * n_rows * hq * 2:
+                raise ValueError("scores, stats: expected [n_layers][n_rows][Hq][lds] and [n_layers][n_rows][Hq][2]")
+        self._sc = (CommitSlotC * len(self.slots))()
+        for i, s in enumerate(self.slots):
+            _kv_pair(s.k, s.v, 4, f"slots[{i}]")
+            _need(s.k, torch.float16, f"slots[{i}].k")
+            _need(s.v, torch.float16, f"slots[{i}].v")
+            if s.k.shape[:2] != (L, Hkv):
+                raise ValueError("slots: expected the same layers and heads in each")
+            if s.acc is not None:
+                _state(s.acc, torch.float32, s.k, f"slots[{i}].acc")
+            if s.pos is not None:
+                _state(s.pos, torch.int32, s.k, f"slots[{i}].pos")
+            _same_device(self.slots[0].k, s.k, s.v, s.acc, s.pos, scores, stats)
+            self._sc[i] = CommitSlotC(s.k.data_ptr(), s.v.data_ptr(), s.len, s.k.shape[2], 0, s.row0, None, _ptr(s.acc),
+                                      _ptr(s.pos), s.pos0)
+        self._paths = [None] * len(self.slots)
+        self._arrays = [None] * len(self.slots)
+        self._args = (self._sc, len(self.slots), L, int(n_q_heads), Hkv, HEAD_DIM, _ptr(scores), n_rows, lds, _ptr(stats))
+        self._bind(load_library().luce_tree_commit, self.slots[0].k.device, stream, (scores, stats))
+
+    def __call__(self):
+        for i, s in enumerate(self.slots):
+            c = self._sc[i]
+            c.len, c.row0, c.pos0 = s.len, s.row0, s.pos0
+            path = tuple(s.path)
+            if path != self._paths[i]:
+                self._paths[i] = path
+                self._arrays[i] = (ctypes.c_int32 * max(1, len(path)))(*path)
+                c.path, c.n_path = self._arrays[i], len(path)
+        self._call(*self._args)
+
+
+def luce_tree_commit(slots: Sequence[CommitSlot], n_q_heads: int, scores=None, stats=None, stream=None):
+    """Make the accepted paths of verified trees the slots' next keys: their K/V
+    rows move to len, len + 1, ..; acc and pos follow where given.  The caller
+    adds the path's length to ``len``."""
+    TreeCommit(slots, n_q_heads, scores, stats, stream)()
+
+
+class KvEvict(_Prepared):
+    """luce_kv_evict with its arguments marshalled once: each call takes the
+    slots' current ``len`` and ``next_pos``."""
+
+    def __init__(self, slots: Sequence[EvictSlot], stream=None):
+        import torch
+        self.slots = list(slots)
+        if not self.slots:
+            raise ValueError("slots: expected at least one")
+        L, Hkv = self.slots[0].k.shape[:2]
+        self._sc = (EvictSlotC * len(self.slots))()
+        for i, s in enumerate(self.slots):
+            _kv_pair(s.k, s.v, 4, f"slots[{i}]")
+            _need(s.k, torch.float16, f"slots[{i}].k")
+            _need(s.v, torch.float16, f"slots[{i}].v")
+            if s.k.shape[:2] != (L, Hkv):
+                raise ValueError("slots: expected the same layers and heads in each")
+            acc_out = s.acc if s.acc_out is None else s.acc_out
+            pos_out = s.pos if s.pos_out is None else s.pos_out
+            for t, dt, w in ((s.acc, torch.float32, "acc"), (acc_out, torch.float32, "acc_out"),
+                             (s.pos, torch.int32, "pos"), (pos_out, torch.int32, "pos_out")):
+                _state(t, dt, s.k, f"slots[{i}].{w}")
+            _same_device(self.slots[0].k, s.k, s.v, s.acc, s.pos, acc_out, pos_out)
+            self._sc[i] = EvictSlotC(s.k.data_ptr(), s.v.data_ptr(), s.acc.data_ptr(), s.pos.data_ptr(),
+                                     acc_out.data_ptr(), pos_out.data_ptr(), s.len, s.k.shape[2], s.budget, s.sinks,
+                                     s.recent, s.next_pos)
+        self._args = (self._sc, len(self.slots), L, Hkv, HEAD_DIM)
+        self._bind(load_library().luce_kv_evict, self.slots[0].k.device, stream, None)
+
+    def __call__(self):
+        for c, s in zip(self._sc, self.slots):
+            c.len, c.next_pos = s.len, s.next_pos
+        self._call(*self._args)
+
+
+def luce_kv_evict(slots: Sequence[EvictSlot], stream=None):
+    """Cut the slots' caches to their budgets by accumulated attention weight,
+    per layer and KV head.  The caller continues with min(len, budget) keys."""
+    KvEvict(slots, stream)()

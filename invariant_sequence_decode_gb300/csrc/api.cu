@@ -14,6 +14,7 @@
 #include <string>
 
 #include "../../include/luce.h"
+#include "api.h"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -36,11 +37,9 @@ RopeFreq luce::rope_freq(double theta)
     return f;
 }
 
-namespace {
+static thread_local std::string g_err;
 
-thread_local std::string g_err;
-
-int fail(int code, const char* fmt, ...)
+int luce::fail(int code, const char* fmt, ...)
 {
     char buf[512];
     va_list ap;
@@ -51,24 +50,19 @@ int fail(int code, const char* fmt, ...)
     return code;
 }
 
-int ok()
+int luce::ok()
 {
     g_err.clear();
     return LUCE_OK;
 }
 
-int cuda_status(cudaError_t e, const char* what)
+int luce::cuda_status(cudaError_t e, const char* what)
 {
     if (e != cudaSuccess) return fail(LUCE_ECUDA, "%s: %s", what, cudaGetErrorString(e));
     return ok();
 }
 
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
-#define REQUIRE(cond, code, ...) \
-    do {                         \
-        if (!(cond)) return fail(code, __VA_ARGS__); \
-    } while (0)
+namespace {
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
@@ -96,7 +90,7 @@ extern "C" {
 
 const char* luce_last_error(void) { return g_err.c_str(); }
 
-int luce_version(void) { return 10000; }
+int luce_version(void) { return 10100; }
 
 uint64_t luce_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }
 

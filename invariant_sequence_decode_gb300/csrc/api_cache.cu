@@ -1,0 +1,317 @@
+// api_cache.cu - the C ABI over a slot's cache: tree attention, the commit of
+// an accepted path, eviction (see include/luce.h for the contract).
+#include <math.h>
+
+#include <algorithm>
+
+#include "../../include/luce.h"
+#include "api.h"
+#include "api_cache.h"
+#include "cache.h"
+#include "kernels.h"
+
+using namespace luce;
+
+static_assert(LUCE_MAX_TREE == kMaxTree && LUCE_MAX_ROWS == kMaxTree && LUCE_MAX_SEQ == 4, "sizes of the batches");
+
+// ------------------------------------------------------------ trees
+
+int luce::tree_path(const int32_t* parent, int n_nodes, TreeRow* rows, int view, int row0, const char* who)
+{
+    for (int j = 0; j < n_nodes; ++j) {
+        const int p = parent ? parent[j] : j - 1;
+        REQUIRE(p >= -1 && p < j, LUCE_EINVAL, "%s: view %d node %d has parent %d outside [-1, %d)", who, view, j, p, j);
+        TreeRow& r = rows[row0 + j];
+        r.view = (uint8_t)view;
+        r.node = (uint8_t)j;
+        r.n_path = 0;
+        if (p >= 0)
+            for (; r.n_path < rows[row0 + p].n_path; ++r.n_path) r.path[r.n_path] = rows[row0 + p].path[r.n_path];
+        r.path[r.n_path++] = (uint8_t)j;
+    }
+    return LUCE_OK;
+}
+
+int64_t luce::tree_chunks(TreeBatch& b, int Hq)
+{
+    int64_t part = 0;
+    for (int i = 0; i < b.n_view; ++i) {
+        TreeView& v = b.view[i];
+        v.chunk = tree_chunk_keys(v.len);
+        v.n_chunk = (v.len + v.chunk - 1) / v.chunk;
+        v.part0 = part;
+        part += (int64_t)v.n_chunk * v.n_nodes * Hq;
+    }
+    return part;
+}
+
+size_t luce_tree_attn_workspace_size(int n_rows, int Hq, int D, int max_len)
+{
+    if (n_rows < 1 || n_rows > LUCE_MAX_ROWS || Hq < 1 || D != LUCE_HEAD_DIM || max_len < 0 || max_len > LUCE_MAX_KEYS)
+        return 0;
+    return std::max<size_t>(256, tree_part_bytes((int64_t)tree_max_chunks(max_len) * n_rows * Hq));
+}
+
+static int check_tree_call(const float* q, const void* views, int n_seq, int Hq, int Hkv, int D, float scale,
+                           const float* out, const float* scores, int64_t lds, const float* stats, const void* ws,
+                           const char* who)
+{
+    REQUIRE(q && out && ws && views, LUCE_EINVAL, "%s: null q/out/ws/views", who);
+    REQUIRE(Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0, LUCE_EINVAL, "%s: Hq=%d must be a multiple of Hkv=%d", who, Hq,
+            Hkv);
+    REQUIRE(Hq / Hkv <= 8, LUCE_EUNSUPPORTED, "%s: group size %d > 8", who, Hq / Hkv);
+    REQUIRE(Hkv <= 4096, LUCE_EUNSUPPORTED, "%s: %d KV heads > 4096", who, Hkv);
+    REQUIRE(D == LUCE_HEAD_DIM, LUCE_EUNSUPPORTED, "%s: head_dim %d (only %d)", who, D, LUCE_HEAD_DIM);
+    REQUIRE(isfinite(scale), LUCE_EINVAL, "%s: scale must be finite", who);
+    REQUIRE(aligned(q, 16) && aligned(out, 4) && aligned(stats, 4) && aligned(ws, 256), LUCE_EINVAL,
+            "%s: q must be 16-byte, ws 256-byte aligned", who);
+    REQUIRE(!scores || (aligned(scores, 16) && lds >= 1 && lds % 4 == 0), LUCE_EINVAL,
+            "%s: scores must be 16-byte aligned and lds=%lld a positive multiple of 4", who, (long long)lds);
+    REQUIRE(n_seq >= 1 && n_seq <= LUCE_MAX_SEQ, LUCE_EINVAL,
+            "%s: n_seq=%d outside 1..%d (more than %d sequences are refused)", who, n_seq, LUCE_MAX_SEQ,
+            LUCE_MAX_SEQ);
+    return LUCE_OK;
+}
+
+// A view's sizes and rows, entered into the batch.
+static int add_tree_view(TreeBatch& b, int s, int len, int n_nodes, int row0, const int32_t* parent, bool* covered,
+                         const float* scores, int64_t lds, const char* who)
+{
+    REQUIRE(n_nodes >= 1 && n_nodes <= LUCE_MAX_TREE, LUCE_EINVAL, "%s: view %d has %d nodes (1..%d)", who, s, n_nodes,
+            LUCE_MAX_TREE);
+    REQUIRE(len >= 0, LUCE_EINVAL, "%s: view %d len=%d < 0", who, s, len);
+    REQUIRE(len <= LUCE_MAX_KEYS - n_nodes, LUCE_EUNSUPPORTED, "%s: view %d has %d + %d keys (at most %d)", who, s, len,
+            n_nodes, LUCE_MAX_KEYS);
+    REQUIRE(!scores || lds >= len + n_nodes, LUCE_EINVAL, "%s: lds=%lld < the %d keys of view %d", who, (long long)lds,
+            len + n_nodes, s);
+    REQUIRE(row0 >= 0 && row0 <= LUCE_MAX_ROWS - n_nodes, LUCE_EINVAL, "%s: view %d rows out of range", who, s);
+    for (int j = 0; j < n_nodes; ++j) {
+        REQUIRE(!covered[row0 + j], LUCE_EINVAL, "%s: row %d claimed twice", who, row0 + j);
+        covered[row0 + j] = true;
+    }
+    const int rc = tree_path(parent, n_nodes, b.row, s, row0, who);
+    if (rc) return rc;
+    b.view[s].len = len;
+    b.view[s].n_nodes = n_nodes;
+    b.view[s].row0 = row0;
+    b.n_view = s + 1;
+    b.n_row = std::max(b.n_row, row0 + n_nodes);
+    return LUCE_OK;
+}
+
+static int run_tree(TreeBatch& b, const bool* covered, const float* q, int Hq, int Hkv, float scale, float* out,
+                    float* scores, int64_t lds, float* stats, void* ws, size_t ws_bytes, void* stream, const char* who)
+{
+    for (int r = 0; r < b.n_row; ++r) REQUIRE(covered[r], LUCE_EINVAL, "%s: row %d belongs to no view", who, r);
+    const size_t need = tree_part_bytes(tree_chunks(b, Hq));
+    REQUIRE(ws_bytes >= need, LUCE_ENOSPACE, "%s: workspace %zu bytes < %zu needed", who, ws_bytes, need);
+    return cuda_status(launch_tree_attention(q, b, Hq, Hkv, scale, ws, out, scores, lds, stats, nullptr, nullptr,
+                                             (cudaStream_t)stream),
+                       who);
+}
+
+int luce_tree_attn(const float* q, const luce_treeview* views, int n_seq, int Hq, int Hkv, int D, float scale,
+                   float* out, float* scores, int64_t lds, float* stats, void* ws, size_t ws_bytes, void* stream)
+{
+    const char* who = "tree_attn";
+    int rc = check_tree_call(q, views, n_seq, Hq, Hkv, D, scale, out, scores, lds, stats, ws, who);
+    if (rc) return rc;
+    TreeBatch b{};
+    bool covered[LUCE_MAX_ROWS] = {};
+    for (int s = 0; s < n_seq; ++s) {
+        const luce_treeview& v = views[s];
+        REQUIRE(v.k && v.v && aligned(v.k, 16) && aligned(v.v, 16), LUCE_EINVAL,
+                "%s: view %d cache null or not 16-byte aligned", who, s);
+        if ((rc = add_tree_view(b, s, v.len, v.n_nodes, v.row0, v.parent, covered, scores, lds, who))) return rc;
+        REQUIRE(v.len + v.n_nodes <= v.cap, LUCE_EINVAL, "%s: view %d len=%d + nodes=%d exceeds cap=%d", who, s, v.len,
+                v.n_nodes, v.cap);
+        REQUIRE(v.tok_stride >= D && v.tok_stride % 8 == 0 && v.tok_stride < ((int64_t)1 << 32), LUCE_EINVAL,
+                "%s: view %d tok_stride must be a multiple of 8, at least D", who, s);
+        REQUIRE(Hkv == 1 || (v.head_stride % 8 == 0 && v.head_stride >= (int64_t)v.cap * v.tok_stride &&
+                             v.head_stride < ((int64_t)1 << 38)),
+                LUCE_EINVAL, "%s: view %d head_stride must be a multiple of 8 and keep the heads apart", who, s);
+        TreeView& t = b.view[s];
+        t.k = reinterpret_cast<const __half*>(v.k);
+        t.v = reinterpret_cast<const __half*>(v.v);
+        t.tok_stride = v.tok_stride;
+        t.head_stride = Hkv == 1 ? (int64_t)v.cap * v.tok_stride : v.head_stride;
+        t.page_stride = t.head_stride * Hkv;
+        t.n_pages = 1;
+        t.cap = v.cap;
+    }
+    return run_tree(b, covered, q, Hq, Hkv, scale, out, scores, lds, stats, ws, ws_bytes, stream, who);
+}
+
+int luce_tree_attn_paged(const float* q, const luce_pagedtreeview* views, int n_seq, int Hq, int Hkv, int D,
+                         float scale, float* out, float* scores, int64_t lds, float* stats, void* ws, size_t ws_bytes,
+                         void* stream)
+{
+    const char* who = "tree_attn_paged";
+    int rc = check_tree_call(q, views, n_seq, Hq, Hkv, D, scale, out, scores, lds, stats, ws, who);
+    if (rc) return rc;
+    TreeBatch b{};
+    bool covered[LUCE_MAX_ROWS] = {};
+    for (int s = 0; s < n_seq; ++s) {
+        const luce_pagedtreeview& v = views[s];
+        REQUIRE(v.k_pool && v.v_pool && aligned(v.k_pool, 16) && aligned(v.v_pool, 16), LUCE_EINVAL,
+                "%s: view %d pool null or not 16-byte aligned", who, s);
+        REQUIRE(v.table && aligned(v.table, 4), LUCE_EINVAL, "%s: view %d table null or misaligned", who, s);
+        REQUIRE(v.n_pages >= 1, LUCE_EINVAL, "%s: view %d n_pages=%d", who, s, v.n_pages);
+        if ((rc = add_tree_view(b, s, v.len, v.n_nodes, v.row0, v.parent, covered, scores, lds, who))) return rc;
+        TreeView& t = b.view[s];
+        t.k = reinterpret_cast<const __half*>(v.k_pool);
+        t.v = reinterpret_cast<const __half*>(v.v_pool);
+        t.pages = v.table;
+        t.n_pages = v.n_pages;
+        t.cap = LUCE_PAGE_KEYS;
+        t.tok_stride = D;
+        t.head_stride = (int64_t)LUCE_PAGE_KEYS * D;
+        t.page_stride = t.head_stride * Hkv;
+    }
+    return run_tree(b, covered, q, Hq, Hkv, scale, out, scores, lds, stats, ws, ws_bytes, stream, who);
+}
+
+// ------------------------------------------------------------ ranges
+
+int luce::check_apart(const ByteRange* r, int n, const char* who)
+{
+    for (int a = 0; a < n; ++a)
+        for (int c = 0; c < a; ++c) {
+            const bool apart = r[a].hi <= r[c].lo || r[c].hi <= r[a].lo;
+            const bool both_read = !r[a].written && !r[c].written;
+            const bool in_place = r[a].slot == r[c].slot && r[a].pair && r[a].pair == r[c].pair && r[a].lo == r[c].lo;
+            REQUIRE(apart || both_read || in_place, LUCE_EINVAL, "%s: the %s of slot %d overlaps the %s of slot %d", who,
+                    r[a].what, r[a].slot, r[c].what, r[c].slot);
+        }
+    return LUCE_OK;
+}
+
+static ByteRange range_of(const void* p, int64_t bytes, int slot, const char* what, bool written, int pair = 0)
+{
+    return ByteRange{(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes, slot, what, written, pair};
+}
+
+static int check_layers(int n_seq, int n_layers, int Hkv, int D, const void* slots, const char* who)
+{
+    REQUIRE(slots, LUCE_EINVAL, "%s: null slots", who);
+    REQUIRE(n_seq >= 1 && n_seq <= LUCE_MAX_SEQ, LUCE_EINVAL, "%s: n_seq=%d outside 1..%d", who, n_seq, LUCE_MAX_SEQ);
+    REQUIRE(D == LUCE_HEAD_DIM, LUCE_EUNSUPPORTED, "%s: head_dim %d (only %d)", who, D, LUCE_HEAD_DIM);
+    REQUIRE(n_layers >= 1 && Hkv >= 1 && (int64_t)n_layers * Hkv <= (1 << 20), LUCE_EINVAL,
+            "%s: n_layers=%d and Hkv=%d must be positive, %d heads at most in all", who, n_layers, Hkv, 1 << 20);
+    return LUCE_OK;
+}
+
+// ------------------------------------------------------------ commit
+
+int luce_tree_commit(const luce_commit_slot* slots, int n_seq, int n_layers, int Hq, int Hkv, int D,
+                     const float* scores, int n_rows, int64_t lds, const float* stats, void* stream)
+{
+    const char* who = "tree_commit";
+    int rc = check_layers(n_seq, n_layers, Hkv, D, slots, who);
+    if (rc) return rc;
+    REQUIRE(Hq >= Hkv && Hq % Hkv == 0, LUCE_EINVAL, "%s: Hq=%d must be a multiple of Hkv=%d", who, Hq, Hkv);
+    REQUIRE(Hq / Hkv <= 8, LUCE_EUNSUPPORTED, "%s: group size %d > 8", who, Hq / Hkv);
+    CommitBatch b{};
+    b.n_slot = n_seq;
+    ByteRange r[4 * LUCE_MAX_SEQ + 2];
+    int nr = 0;
+    bool any_acc = false, any = false;
+    const int64_t heads = (int64_t)n_layers * Hkv;
+    for (int s = 0; s < n_seq; ++s) {
+        const luce_commit_slot& c = slots[s];
+        REQUIRE(c.k && c.v && aligned(c.k, 16) && aligned(c.v, 16), LUCE_EINVAL,
+                "%s: slot %d cache null or not 16-byte aligned", who, s);
+        REQUIRE(aligned(c.acc, 4) && aligned(c.pos, 4), LUCE_EINVAL, "%s: slot %d acc or pos misaligned", who, s);
+        REQUIRE(c.n_path >= 0 && c.n_path <= LUCE_MAX_TREE, LUCE_EINVAL, "%s: slot %d n_path=%d outside 0..%d", who, s,
+                c.n_path, LUCE_MAX_TREE);
+        REQUIRE(c.n_path == 0 || c.path, LUCE_EINVAL, "%s: slot %d has a null path", who, s);
+        REQUIRE(c.len >= 0 && c.cap >= 1 && c.len <= c.cap, LUCE_EINVAL, "%s: slot %d len=%d outside [0, cap=%d]", who, s,
+                c.len, c.cap);
+        REQUIRE(c.pos0 >= 0 && c.pos0 <= INT32_MAX - LUCE_MAX_TREE, LUCE_EINVAL, "%s: slot %d pos0=%d", who, s, c.pos0);
+        int last = -1;
+        for (int i = 0; i < c.n_path; ++i) {
+            REQUIRE(c.path[i] > last && c.path[i] < LUCE_MAX_TREE && (int64_t)c.len + c.path[i] < c.cap, LUCE_EINVAL,
+                    "%s: slot %d path[%d]=%d must ascend, below %d and within the cache", who, s, i, c.path[i],
+                    LUCE_MAX_TREE);
+            last = c.path[i];
+            b.slot[s].path[i] = (uint8_t)last;
+        }
+        if (c.acc && c.n_path > 0) {
+            any_acc = true;
+            REQUIRE(scores && stats, LUCE_EINVAL, "%s: slot %d has acc, but scores or stats is null", who, s);
+            REQUIRE(c.row0 >= 0 && (int64_t)c.row0 + last < n_rows, LUCE_EINVAL,
+                    "%s: slot %d rows %d + %d outside the %d score rows", who, s, c.row0, last, n_rows);
+            REQUIRE(lds > (int64_t)c.len + last, LUCE_EINVAL, "%s: lds=%lld does not reach slot %d's key %d", who,
+                    (long long)lds, s, c.len + last);
+        }
+        any = any || c.n_path > 0;
+        b.slot[s].k = reinterpret_cast<__half*>(c.k);
+        b.slot[s].v = reinterpret_cast<__half*>(c.v);
+        b.slot[s].acc = c.acc;
+        b.slot[s].pos = c.pos;
+        b.slot[s].len = c.len;
+        b.slot[s].cap = c.cap;
+        b.slot[s].row0 = c.row0;
+        b.slot[s].pos0 = c.pos0;
+        b.slot[s].n_path = c.n_path;
+        r[nr++] = range_of(c.k, heads * c.cap * D * 2, s, "K cache", true);
+        r[nr++] = range_of(c.v, heads * c.cap * D * 2, s, "V cache", true);
+        if (c.acc) r[nr++] = range_of(c.acc, heads * c.cap * 4, s, "acc", true);
+        if (c.pos) r[nr++] = range_of(c.pos, heads * c.cap * 4, s, "pos", true);
+    }
+    if (any_acc) {
+        REQUIRE(n_rows >= 1 && n_rows <= LUCE_MAX_ROWS, LUCE_EINVAL, "%s: n_rows=%d outside 1..%d", who, n_rows,
+                LUCE_MAX_ROWS);
+        REQUIRE(aligned(scores, 16) && lds % 4 == 0 && lds < ((int64_t)1 << 31) && aligned(stats, 4), LUCE_EINVAL,
+                "%s: scores must be 16-byte aligned and lds=%lld a multiple of 4", who, (long long)lds);
+        r[nr++] = range_of(scores, (int64_t)n_layers * n_rows * Hq * lds * 4, -1, "scores", false);
+        r[nr++] = range_of(stats, (int64_t)n_layers * n_rows * Hq * 8, -1, "stats", false);
+    }
+    if ((rc = check_apart(r, nr, who))) return rc;
+    if (!any) return ok();
+    return cuda_status(launch_tree_commit(b, n_layers, Hq, Hkv, scores, n_rows, lds, stats, (cudaStream_t)stream), who);
+}
+
+// ------------------------------------------------------------ eviction
+
+int luce_kv_evict(const luce_evict_slot* slots, int n_seq, int n_layers, int Hkv, int D, void* stream)
+{
+    const char* who = "kv_evict";
+    int rc = check_layers(n_seq, n_layers, Hkv, D, slots, who);
+    if (rc) return rc;
+    EvictBatch b{};
+    b.n_slot = n_seq;
+    ByteRange r[6 * LUCE_MAX_SEQ];
+    int nr = 0;
+    bool any = false;
+    const int64_t heads = (int64_t)n_layers * Hkv;
+    for (int s = 0; s < n_seq; ++s) {
+        const luce_evict_slot& e = slots[s];
+        REQUIRE(e.k && e.v && aligned(e.k, 16) && aligned(e.v, 16), LUCE_EINVAL,
+                "%s: slot %d cache null or not 16-byte aligned", who, s);
+        REQUIRE(e.acc && e.pos && e.acc_out && e.pos_out && aligned(e.acc, 4) && aligned(e.pos, 4) &&
+                    aligned(e.acc_out, 4) && aligned(e.pos_out, 4),
+                LUCE_EINVAL, "%s: slot %d acc or pos null or misaligned", who, s);
+        REQUIRE(e.cap >= 1 && e.len >= 0 && e.len <= e.cap, LUCE_EINVAL, "%s: slot %d len=%d outside [0, cap=%d]", who, s,
+                e.len, e.cap);
+        REQUIRE(e.len <= LUCE_MAX_KEYS, LUCE_EUNSUPPORTED, "%s: slot %d has %d keys (at most %d)", who, s, e.len,
+                LUCE_MAX_KEYS);
+        REQUIRE(e.budget >= 1 && e.sinks >= 0 && e.recent >= 0 && (int64_t)e.sinks + e.recent <= e.budget, LUCE_EINVAL,
+                "%s: slot %d needs 1 <= budget and sinks + recent <= budget (%d, %d, %d)", who, s, e.budget, e.sinks,
+                e.recent);
+        REQUIRE(e.next_pos >= 0, LUCE_EINVAL, "%s: slot %d next_pos=%d", who, s, e.next_pos);
+        b.slot[s] = EvictSlot{reinterpret_cast<__half*>(e.k), reinterpret_cast<__half*>(e.v), e.acc, e.pos, e.acc_out,
+                              e.pos_out, e.len, e.cap, e.budget, e.sinks, e.recent, e.next_pos};
+        const bool copies = e.acc_out != e.acc || e.pos_out != e.pos;
+        any = any || e.len > e.budget || (copies && e.len > 0);
+        r[nr++] = range_of(e.k, heads * e.cap * D * 2, s, "K cache", true);
+        r[nr++] = range_of(e.v, heads * e.cap * D * 2, s, "V cache", true);
+        r[nr++] = range_of(e.acc, heads * e.cap * 4, s, "acc", false, 1);
+        r[nr++] = range_of(e.pos, heads * e.cap * 4, s, "pos", false, 2);
+        r[nr++] = range_of(e.acc_out, heads * e.cap * 4, s, "acc_out", true, 1);
+        r[nr++] = range_of(e.pos_out, heads * e.cap * 4, s, "pos_out", true, 2);
+    }
+    if ((rc = check_apart(r, nr, who))) return rc;
+    if (!any) return ok();
+    return cuda_status(launch_kv_evict(b, n_layers, Hkv, (cudaStream_t)stream), who);
+}

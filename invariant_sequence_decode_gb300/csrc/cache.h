@@ -1,0 +1,105 @@
+// cache.h - launchers of the kernels over a slot's cache: tree attention, the
+// commit of an accepted path, eviction (internal).
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace luce {
+
+constexpr int kMaxTree = 16;  // nodes of a slot's tree, and rows of a call
+
+// A slot's tree over its cache for one layer.  Flat cache (pages == nullptr):
+// element d of key j of KV head g is k[g*head_stride + j*tok_stride + d].
+// Paged cache: key j lives in page pages[j / 128], page p at k + p*page_stride;
+// an entry outside [0, n_pages) names no page.
+struct TreeView {
+    const __half* k;
+    const __half* v;
+    const int32_t* pages;
+    int64_t head_stride;
+    int64_t tok_stride;
+    int64_t page_stride;
+    int64_t part0;  // the view's first row of partial results
+    int32_t n_pages;
+    int32_t cap;
+    int32_t len;
+    int32_t n_nodes;
+    int32_t row0;
+    int32_t chunk;    // keys of a chunk: tree_chunk_keys(len)
+    int32_t n_chunk;  // chunks of the prefix
+};
+
+// A row's node: its path from the prefix (ascending, the node itself last).
+struct TreeRow {
+    uint8_t view;
+    uint8_t node;
+    uint8_t n_path;
+    uint8_t path[kMaxTree];
+};
+
+struct TreeBatch {
+    TreeView view[4];
+    TreeRow row[kMaxTree];
+    int32_t n_view;
+    int32_t n_row;
+};
+
+// Keys of a chunk of a prefix of len keys: a function of len alone, so that
+// a row's sums are cut the same way whatever else is in the call.
+int tree_chunk_keys(int len);
+
+// The most chunks of a prefix of at most max_len keys.
+int tree_max_chunks(int max_len);
+
+// Bytes of partial results of n_part rows (view chunks x KV heads x the rows
+// of a KV head).
+size_t tree_part_bytes(int64_t n_part);
+
+// out [T][Hq][128]; scores [T][Hq][lds] and stats [T][Hq][2] nullable; out_q,
+// out_d (nullable): out's q8_0 codes and scales.
+cudaError_t launch_tree_attention(const float* q, const TreeBatch& b, int Hq, int Hkv, float scale, void* part,
+                                  float* out, float* scores, int64_t lds, float* stats, int8_t* out_q, float* out_d,
+                                  cudaStream_t s);
+
+struct CommitSlot {
+    __half* k;
+    __half* v;
+    float* acc;
+    int32_t* pos;
+    int32_t len;
+    int32_t cap;
+    int32_t row0;
+    int32_t pos0;
+    int32_t n_path;
+    uint8_t path[kMaxTree];
+};
+struct CommitBatch {
+    CommitSlot slot[4];
+    int32_t n_slot;
+};
+cudaError_t launch_tree_commit(const CommitBatch& b, int n_layers, int Hq, int Hkv, const float* scores, int n_rows,
+                               int64_t lds, const float* stats, cudaStream_t s);
+
+struct EvictSlot {
+    __half* k;
+    __half* v;
+    const float* acc;
+    const int32_t* pos;
+    float* acc_out;
+    int32_t* pos_out;
+    int32_t len;
+    int32_t cap;
+    int32_t budget;
+    int32_t sinks;
+    int32_t recent;
+    int32_t next_pos;
+};
+struct EvictBatch {
+    EvictSlot slot[4];
+    int32_t n_slot;
+};
+cudaError_t launch_kv_evict(const EvictBatch& b, int n_layers, int Hkv, cudaStream_t s);
+
+}  // namespace luce

@@ -1,0 +1,157 @@
+"""The entry points over a slot's cache refuse invalid calls with a status
+before anything is enqueued (no device needed: validation precedes launches)."""
+import ctypes
+
+import pytest
+
+import invariant_sequence_decode_gb300 as luce
+from invariant_sequence_decode_gb300 import build
+
+P = 0x10000
+BIG = 0x100000000
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return luce.load_library()
+
+
+def ints(values):
+    return (ctypes.c_int32 * max(1, len(values)))(*values)
+
+
+def view(length=10, nodes=2, row0=0, cap=4096, head=4096 * 128, tok=128, parent=None, k=P, v=P + BIG):
+    return luce.TreeViewC(k, v, length, nodes, row0, cap, head, tok, None if parent is None else ints(parent))
+
+
+def attn(lib, views, q=P, Hq=8, Hkv=2, D=128, scale=0.1, out=P, scores=None, lds=0, stats=None, ws=P, ws_bytes=1 << 40, n=None):
+    arr = (luce.TreeViewC * max(1, len(views)))(*views)
+    return lib.luce_tree_attn(q, arr, len(views) if n is None else n, Hq, Hkv, D, scale, out, scores, lds, stats, ws,
+                              ws_bytes, None)
+
+
+E, U, S = luce.LUCE_EINVAL, luce.LUCE_EUNSUPPORTED, luce.LUCE_ENOSPACE
+
+
+@pytest.mark.parametrize("want,kw", [
+    (E, dict(q=0)), (E, dict(q=P + 8)), (E, dict(out=0)), (E, dict(ws=0)), (E, dict(ws=P + 16)),
+    (E, dict(Hq=9)), (E, dict(Hkv=0)), (E, dict(Hq=0)), (U, dict(Hq=18)), (U, dict(D=64)),
+    (E, dict(scale=float("nan"))), (E, dict(scale=float("inf"))),
+    (E, dict(scores=P, lds=0)), (E, dict(scores=P, lds=14)), (E, dict(scores=P + 4, lds=16)), (E, dict(scores=P, lds=8)),
+    (E, dict(stats=P + 2)), (S, dict(ws_bytes=16)),
+])
+def test_tree_attention_refuses_arguments(lib, want, kw):
+    assert attn(lib, [view()], **kw) == want and lib.luce_last_error()
+
+
+@pytest.mark.parametrize("want,views", [
+    (E, []), (E, [view(row0=2 * i) for i in range(5)]),
+    (E, [view(nodes=0)]), (E, [view(nodes=17)]), (E, [view(nodes=-1)]),
+    (E, [view(length=-1)]), (E, [view(length=4095)]), (U, [view(length=130815, cap=1 << 20, head=1 << 27)]),
+    (E, [view(row0=1)]), (E, [view(row0=-1)]), (E, [view(nodes=4, row0=13)]),
+    (E, [view(), view()]), (E, [view(nodes=8), view(nodes=9, row0=8)]),
+    (E, [view(parent=[0, 0])]), (E, [view(parent=[-1, 1])]), (E, [view(parent=[-2, 0])]), (E, [view(parent=[-1, 5])]),
+    (E, [view(k=0)]), (E, [view(v=0)]), (E, [view(k=P + 8)]),
+    (E, [view(tok=120)]), (E, [view(tok=132)]), (E, [view(head=4096 * 128 - 8)]), (E, [view(head=4096 * 128 + 4)]),
+    (E, [view(tok=1 << 33, head=1 << 37)]),
+])
+def test_tree_attention_refuses_views(lib, want, views):
+    assert attn(lib, views) == want and lib.luce_last_error()
+
+
+def test_tree_attention_null_views(lib):
+    assert lib.luce_tree_attn(P, None, 1, 8, 2, 128, 0.1, P, None, 0, None, P, 1 << 30, None) == E
+
+
+@pytest.mark.parametrize("want,kw", [
+    (E, dict(k=0)), (E, dict(v=P + 2)), (E, dict(table=0)), (E, dict(table=P + 2)), (E, dict(pages=0)), (E, dict(length=-1)),
+    (U, dict(length=130815)), (E, dict(nodes=0)), (E, dict(nodes=17)), (E, dict(row0=1)), (E, dict(parent=[1, 0])),
+])
+def test_paged_tree_attention_refusals(lib, want, kw):
+    a = dict(k=P, v=P, table=P, pages=4, length=10, nodes=2, row0=0, parent=None)
+    a.update(kw)
+    v = luce.PagedTreeViewC(a["k"], a["v"], a["table"], a["pages"], a["length"], a["nodes"], a["row0"],
+                            None if a["parent"] is None else ints(a["parent"]))
+    arr = (luce.PagedTreeViewC * 1)(v)
+    assert lib.luce_tree_attn_paged(P, arr, 1, 8, 2, 128, 0.1, P, None, 0, None, P, 1 << 40, None) == want
+
+
+def test_tree_workspace_sizes(lib):
+    size = lib.luce_tree_attn_workspace_size
+    assert size(0, 8, 128, 10) == size(17, 8, 128, 10) == size(1, 8, 64, 10) == size(1, 8, 128, 200000) == 0
+    assert size(1, 0, 128, 10) == size(1, 8, 128, -1) == 0
+    assert size(1, 8, 128, 0) >= 256
+    last = 0
+    for n in (1, 128, 129, 1000, 8192, 8193, 32768, 32769, 100000, 130816):
+        assert size(4, 40, 128, n) >= last  # a workspace for longer prefixes serves shorter ones
+        last = size(4, 40, 128, n)
+
+
+def slot(k=P, v=P + BIG, length=10, cap=64, path=(0, 2), row0=0, acc=None, pos=None, pos0=10, n=None):
+    return luce.CommitSlotC(k, v, length, cap, len(path) if n is None else n, row0, ints(path), acc, pos, pos0)
+
+
+def commit(lib, slots, L=2, Hq=8, Hkv=2, D=128, scores=None, rows=0, lds=0, stats=None, n=None):
+    arr = (luce.CommitSlotC * max(1, len(slots)))(*slots)
+    return lib.luce_tree_commit(arr, len(slots) if n is None else n, L, Hq, Hkv, D, scores, rows, lds, stats, None)
+
+
+ACC, POS, SC, ST = P + 2 * BIG, P + 3 * BIG, P + 4 * BIG, P + 5 * BIG
+
+
+@pytest.mark.parametrize("want,slots,kw", [
+    (E, [], {}), (E, [slot()] * 5, {}), (E, [slot()], dict(L=0)), (E, [slot()], dict(Hkv=0)), (U, [slot()], dict(D=64)),
+    (E, [slot()], dict(Hq=9)), (U, [slot()], dict(Hq=32)), (E, [slot()], dict(L=1 << 20)),
+    (E, [slot(k=0)], {}), (E, [slot(v=P + BIG + 8)], {}), (E, [slot(length=-1)], {}), (E, [slot(length=65)], {}),
+    (E, [slot(n=17)], {}), (E, [slot(n=-1)], {}), (E, [slot(path=(2, 0))], {}), (E, [slot(path=(1, 1))], {}),
+    (E, [slot(path=(0, 16))], {}), (E, [slot(path=(-1,))], {}), (E, [slot(length=60, path=(0, 4))], {}),
+    (E, [slot(pos0=-1)], {}), (E, [slot(v=P)], {}), (E, [slot(), slot()], {}),
+    (E, [slot(acc=ACC)], {}), (E, [slot(acc=ACC)], dict(scores=SC, rows=4, lds=16)),
+    (E, [slot(acc=ACC)], dict(scores=SC, rows=2, lds=16, stats=ST)),     # row 2 outside two rows
+    (E, [slot(acc=ACC)], dict(scores=SC, rows=17, lds=16, stats=ST)),
+    (E, [slot(acc=ACC)], dict(scores=SC, rows=4, lds=12, stats=ST)),     # column 12 outside
+    (E, [slot(acc=ACC)], dict(scores=SC, rows=4, lds=15, stats=ST)),
+    (E, [slot(acc=ACC)], dict(scores=SC + 4, rows=4, lds=16, stats=ST)),
+    (E, [slot(acc=ACC, row0=-1)], dict(scores=SC, rows=4, lds=16, stats=ST)),
+    (E, [slot(acc=ACC, pos=ACC)], dict(scores=SC, rows=4, lds=16, stats=ST)),
+    (E, [slot(acc=SC)], dict(scores=SC, rows=4, lds=16, stats=ST)),
+    (E, [slot(acc=ACC + 2)], dict(scores=SC, rows=4, lds=16, stats=ST)),
+])
+def test_commit_refusals(lib, want, slots, kw):
+    assert commit(lib, slots, **kw) == want and lib.luce_last_error()
+
+
+def test_commit_of_nothing_enqueues_nothing(lib):
+    before = luce.launch_count()
+    assert commit(lib, [slot(path=()), slot(k=P + 6 * BIG, v=P + 7 * BIG, path=())]) == luce.LUCE_OK
+    assert luce.launch_count() == before
+
+
+def eslot(k=P, v=P + BIG, acc=ACC, pos=POS, acc_out=ACC, pos_out=POS, length=20, cap=64, budget=10, sinks=1, recent=4, nxt=20):
+    return luce.EvictSlotC(k, v, acc, pos, acc_out, pos_out, length, cap, budget, sinks, recent, nxt)
+
+
+def evict(lib, slots, L=2, Hkv=2, D=128):
+    arr = (luce.EvictSlotC * max(1, len(slots)))(*slots)
+    return lib.luce_kv_evict(arr, len(slots), L, Hkv, D, None)
+
+
+@pytest.mark.parametrize("want,slots,kw", [
+    (E, [], {}), (E, [eslot()] * 5, {}), (E, [eslot()], dict(L=0)), (U, [eslot()], dict(D=64)),
+    (E, [eslot(k=0)], {}), (E, [eslot(k=P + 8)], {}), (E, [eslot(acc=0)], {}), (E, [eslot(pos_out=0)], {}),
+    (E, [eslot(acc=ACC + 1)], {}), (E, [eslot(length=65)], {}), (E, [eslot(length=-1)], {}),
+    (U, [eslot(length=130817, cap=130900)], {}), (E, [eslot(budget=0)], {}), (E, [eslot(sinks=-1)], {}),
+    (E, [eslot(recent=-1)], {}), (E, [eslot(sinks=6, recent=5)], {}), (E, [eslot(sinks=2**31 - 1, recent=2**31 - 1)], {}),
+    (E, [eslot(nxt=-1)], {}), (E, [eslot(), eslot()], {}), (E, [eslot(v=P)], {}),
+    (E, [eslot(acc_out=ACC + 4)], {}), (E, [eslot(acc_out=POS)], {}), (E, [eslot(pos_out=POS + 64)], {}),
+])
+def test_evict_refusals(lib, want, slots, kw):
+    assert evict(lib, slots, **kw) == want and lib.luce_last_error()
+
+
+def test_evict_within_budget_in_place_enqueues_nothing(lib):
+    before = luce.launch_count()
+    assert evict(lib, [eslot(budget=20), eslot(P + 6 * BIG, P + 7 * BIG, P + 8 * BIG, P + 9 * BIG, P + 8 * BIG, P + 9 * BIG,
+                                               length=0)]) == luce.LUCE_OK
+    assert luce.launch_count() == before
