@@ -560,7 +560,7 @@ typedef struct luce_pagedtreeview {
  *          position; -inf at the columns of [len, len + n_nodes) that the row
  *          does not see; later columns are left as they were.  16-byte
  *          aligned, lds a multiple of 4 and >= every len + n_nodes
- *   stats  (device) fp32 [T][Hq][2] or NULL: (m, l); e^(s - m) / l is a key's
+ *   stats  (device) fp32 [T][Hq][2] or NULL, 8-byte aligned: (m, l); e^(s - m) / l is a key's
  *          attention weight
  *   ws     (device) scratch of luce_tree_attn_workspace_size(...) bytes,
  *          256-byte aligned (no initial contents); calls that can overlap on

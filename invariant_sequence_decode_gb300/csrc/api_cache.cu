@@ -63,8 +63,8 @@ static int check_tree_call(const float* q, const void* views, int n_seq, int Hq,
     REQUIRE(Hkv <= 4096, LUCE_EUNSUPPORTED, "%s: %d KV heads > 4096", who, Hkv);
     REQUIRE(D == LUCE_HEAD_DIM, LUCE_EUNSUPPORTED, "%s: head_dim %d (only %d)", who, D, LUCE_HEAD_DIM);
     REQUIRE(isfinite(scale), LUCE_EINVAL, "%s: scale must be finite", who);
-    REQUIRE(aligned(q, 16) && aligned(out, 4) && aligned(stats, 4) && aligned(ws, 256), LUCE_EINVAL,
-            "%s: q must be 16-byte, ws 256-byte aligned", who);
+    REQUIRE(aligned(q, 16) && aligned(out, 4) && aligned(stats, 8) && aligned(ws, 256), LUCE_EINVAL,
+            "%s: q must be 16-byte, stats 8-byte, ws 256-byte aligned", who);
     REQUIRE(!scores || (aligned(scores, 16) && lds >= 1 && lds % 4 == 0), LUCE_EINVAL,
             "%s: scores must be 16-byte aligned and lds=%lld a positive multiple of 4", who, (long long)lds);
     REQUIRE(n_seq >= 1 && n_seq <= LUCE_MAX_SEQ, LUCE_EINVAL,

@@ -25,9 +25,8 @@
 // thread issues the products, and 256 threads (two to a row, 64 keys each)
 // turn S into P in place in tensor memory and add each tile's O into registers
 // with the running maximum's correction.
-#include <math.h>
-
 #include <algorithm>
+#include <cmath>
 
 #include "cache.h"
 #include "common.cuh"
@@ -67,8 +66,8 @@ __device__ __forceinline__ const __half* tree_key(const TreeView& v, const __hal
 
 // ---------------------------------------------------------------- chunks
 
-// 8 warps on S, P and O; a warpgroup of which one warp feeds the tiles and one
-// issues the products.  384 threads get 168 registers each (64,512 in all);
+// 8 warps on S, P and O; a warpgroup of which one warp feeds the tiles, one
+// issues S, one P V.  384 threads get 168 registers each (64,512 in all);
 // the second kind gives up to 40, the first then has 232: 256 * 232 + 128 * 40.
 constexpr int kTreeThreads = 384;
 constexpr int kTreeStages = 3;     // tiles of K in flight, and of V
@@ -76,7 +75,7 @@ constexpr int kTreeTileBytes = kTreeTile * kHeadDim * 2;
 constexpr int kTreeSmem = 2 * kTreeStages * kTreeTileBytes + 1024;
 // tensor memory, 512 columns: S/P twice, O, q's two parts
 constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384;
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ unsigned int g_tree_wait_timeouts;
 
@@ -84,14 +83,22 @@ struct TreeMaps {
     CUtensorMap k[4], v[4];
 };
 
+// The scale of the scores.  The sign goes into q (exactly), so that a tile's
+// largest product is its largest score; weights are powers of two,
+// e^(s - m) = 2^(log2 dot - max), log2 = |scale| log2 e.
+struct TreeScale {
+    float sign, abs, log2;
+    float natural;  // of a maximum: ln 2 (0 for a scale of 0)
+};
+
 struct TreeBars {
     uint64_t k_full[kTreeStages], k_empty[kTreeStages], v_full[kTreeStages], v_empty[kTreeStages];
     uint64_t s_full[2];    // S of a tile is complete
     uint64_t p_full[2];    // and its P is in place
+    uint64_t p_read[2];    // and that P has been multiplied
     uint64_t o_full;       // O of a tile is complete
     uint64_t o_free;       // and has been read
     uint64_t q_full;       // q's parts are in place
-    uint64_t x_full[4];    // the maxima of a row quarter's two halves are exchanged
 };
 
 // A chunk of a (view, KV head), in the order view, head, chunk.
@@ -134,18 +141,31 @@ __device__ __forceinline__ uint64_t tree_desc(uint32_t addr, uint32_t lbo, uint3
            (2ull << 61);
 }
 
-// D[128][128] (+)= A (tensor memory, f16) * B (shared memory); one 16-wide step.
-__device__ __forceinline__ void tree_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate)
+// D[128][128] (+)= A (tensor memory, f16) * B (shared memory), one 16-wide
+// step, by the lane whose `elected` is set.  The whole warp comes here: issued
+// from a branch of one thread, each product cost 152 cycles (its descriptor
+// goes through registers that only a converged warp has at hand) against 64.
+__device__ __forceinline__ void tree_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate,
+                                         uint32_t elected)
 {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-                 "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate));
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+                 " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(elected));
 }
 
-__device__ __forceinline__ void tree_commit_mma(uint64_t* bar)
+__device__ __forceinline__ void tree_commit_mma(uint64_t* bar, uint32_t elected)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+                 " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_addr(bar)),
+                 "r"(elected)
                  : "memory");
+}
+
+__device__ __forceinline__ uint32_t elect_one()
+{
+    uint32_t e;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(e));
+    return e;
 }
 __device__ __forceinline__ void tm_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tm_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -200,22 +220,49 @@ __device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t* r)
 }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// e^x = 2^(x log2 e), within about 2^-22 for the x <= 0 that it is given.
-__device__ __forceinline__ float tree_exp(float x)
+__device__ __forceinline__ float tree_exp2(float x)
 {
     float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(__fmul_rn(x, kLog2e)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Pairs of fp32 values: two sums or fused multiply-adds per instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
 
 // Two fp32 values as f16 pairs, x = hi + lo; the first in the low half.
 __device__ __forceinline__ void tree_split(float x0, float x1, uint32_t& hi, uint32_t& lo)
 {
-    const __half2 h = __floats2half2_rn(x0, x1);
-    const float2 f = __half22float2(h);
-    const __half2 l = __floats2half2_rn(__fsub_rn(x0, f.x), __fsub_rn(x1, f.y));
-    hi = *reinterpret_cast<const uint32_t*>(&h);
-    lo = *reinterpret_cast<const uint32_t*>(&l);
+    float l0, l1;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(x1), "f"(x0));
+    asm("{\n .reg .f16 a, b, n;\n mov.b32 {a, b}, %2;\n mov.b16 n, 0xBC00;\n"  // x - hi, exactly
+        " fma.rn.f32.f16 %0, a, n, %3;\n fma.rn.f32.f16 %1, b, n, %4;\n}"
+        : "=f"(l0), "=f"(l1)
+        : "r"(hi), "f"(x0), "f"(x1));
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(l1), "f"(l0));
 }
 
 __device__ __forceinline__ void st_v8(float* p, const float* v)
@@ -261,32 +308,18 @@ __device__ int tree_produce(const TreeMaps& maps, const TreeBatch& b, int Hkv, i
     return i;
 }
 
-// The products: S of tile i is issued before P V of tile i - 1, so the tensor
-// cores work on one tile while the other's softmax runs.
-__device__ void tree_products(const TreeBatch& b, int Hkv, int u0, int u1, uint32_t tiles, uint32_t tmem, TreeBars& bar)
+// S = Q K^T of the CTA's tiles, issued by one warp; P V by another, so that
+// the tensor cores work on one tile's product while the other warp waits for
+// the next one's operands.  The issue loops stay loops: unrolled, their code
+// (4 KB each) fell out of the instruction cache at every chunk's end and cost
+// 8,000 cycles to fetch again.
+__device__ void tree_s(const TreeBatch& b, int Hkv, int u0, int u1, uint32_t tiles, uint32_t tmem, TreeBars& bar)
 {
-    // D f32, A and B f16, 128 x 128; P V's B (V) is N-major
-    constexpr uint32_t idesc_s = (1u << 4) | (16u << 17) | (8u << 24), idesc_o = idesc_s | (1u << 16);
+    // D f32, A and B f16, 128 x 128
+    constexpr uint32_t idesc = (1u << 4) | (16u << 17) | (8u << 24);
+    const uint32_t elected = elect_one();
     unsigned int* late = &g_tree_wait_timeouts;
     int i = 0, heads = 0, last = -1;
-    auto values = [&](int j) {
-        const int st = j % kTreeStages;
-        if (!mbar_wait(&bar.p_full[j & 1], (j >> 1) & 1, late) || !mbar_wait(&bar.v_full[st], (j / kTreeStages) & 1, late) ||
-            (j > 0 && !mbar_wait(&bar.o_free, (j - 1) & 1, late)))
-            return false;
-        tm_after();
-        const uint32_t vt = tiles + (kTreeStages + st) * kTreeTileBytes, p = tmem + kColS + 128 * (j & 1);
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-            const uint64_t d = tree_desc(vt + 2048 * ks, kTreeTileBytes / 2, 1024);
-            const uint32_t a = p + 64 * (ks >> 2) + 8 * (ks & 3);
-            tree_mma(tmem + kColO, a, d, idesc_o, ks > 0);
-            tree_mma(tmem + kColO, a + 32, d, idesc_o, true);
-        }
-        tree_commit_mma(&bar.v_empty[st]);
-        tree_commit_mma(&bar.o_full);
-        return true;
-    };
     for (int u = u0; u < u1; ++u) {
         const TreeUnit t = tree_unit(b, Hkv, u);
         if (t.view * Hkv + t.g != last) {
@@ -295,30 +328,56 @@ __device__ void tree_products(const TreeBatch& b, int Hkv, int u0, int u1, uint3
         }
         for (int k = 0; k < t.tiles; ++k, ++i) {
             const int st = i % kTreeStages;
-            // P of tile i - 2 is read, its S and P may be overwritten
-            if ((i > 1 && !mbar_wait(&bar.o_full, (i - 2) & 1, late)) ||
+            // (the first two buffers are free)
+            if (!mbar_wait(&bar.p_read[i & 1], ((i >> 1) & 1) ^ 1, late) ||
                 !mbar_wait(&bar.k_full[st], (i / kTreeStages) & 1, late))
                 return;
             tm_after();
-            const uint32_t kt = tiles + st * kTreeTileBytes, s = tmem + kColS + 128 * (i & 1);
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-                const uint64_t d = tree_desc(kt + (ks >> 2) * (kTreeTileBytes / 2) + 32 * (ks & 3), 16, 1024);
-                tree_mma(s, tmem + kColQ + 8 * ks, d, idesc_s, ks > 0);
-                tree_mma(s, tmem + kColQ + 64 + 8 * ks, d, idesc_s, true);
-            }
-            tree_commit_mma(&bar.k_empty[st]);
-            tree_commit_mma(&bar.s_full[i & 1]);
-            if (i > 0 && !values(i - 1)) return;
+            const uint32_t s = tmem + kColS + 128 * (i & 1);
+            const uint64_t d = tree_desc(tiles + st * kTreeTileBytes, 16, 1024);
+            // the low parts first: an accumulation loses digits by the sum's
+            // size, and theirs is small
+#pragma unroll 1
+            for (int ks = 0; ks < 16; ++ks)
+                tree_mma(s, tmem + kColQ + 8 * (ks ^ 8), d + (ks >> 2 & 1) * (kTreeTileBytes / 32) + 2 * (ks & 3), idesc,
+                         ks > 0, elected);
+            tree_commit_mma(&bar.s_full[i & 1], elected);
+            tree_commit_mma(&bar.k_empty[st], elected);
         }
     }
-    if (i > 0) values(i - 1);
+}
+
+__device__ void tree_pv(const TreeBatch& b, int Hkv, int u0, int u1, uint32_t tiles, uint32_t tmem, TreeBars& bar)
+{
+    constexpr uint32_t idesc = (1u << 4) | (1u << 16) | (16u << 17) | (8u << 24);  // B = V is N-major
+    const uint32_t elected = elect_one();
+    unsigned int* late = &g_tree_wait_timeouts;
+    int i = 0;
+    for (int u = u0; u < u1; ++u) {
+        const int n = tree_unit(b, Hkv, u).tiles;
+        for (int k = 0; k < n; ++k, ++i) {
+            const int st = i % kTreeStages;
+            if (!mbar_wait(&bar.v_full[st], (i / kTreeStages) & 1, late) ||
+                !mbar_wait(&bar.p_full[i & 1], (i >> 1) & 1, late) || (i > 0 && !mbar_wait(&bar.o_free, (i - 1) & 1, late)))
+                return;
+            tm_after();
+            const uint32_t p = tmem + kColS + 128 * (i & 1) + 32;
+            const uint64_t d = tree_desc(tiles + (kTreeStages + st) * kTreeTileBytes, kTreeTileBytes / 2, 1024);
+#pragma unroll 1
+            for (int ks = 0; ks < 16; ++ks)
+                tree_mma(tmem + kColO, p + 64 * (ks >> 2 & 1) + 8 * (ks & 3) - 32 * (ks >> 3), d + 128 * (ks & 7), idesc,
+                         ks > 0, elected);
+            tree_commit_mma(&bar.o_full, elected);
+            tree_commit_mma(&bar.p_read[i & 1], elected);
+            tree_commit_mma(&bar.v_empty[st], elected);
+        }
+    }
 }
 
 // One CTA an SM; CTA c takes the chunks that begin in its share of all tiles.
 __global__ void __launch_bounds__(kTreeThreads, 1)
 tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* __restrict__ q, const __grid_constant__ TreeBatch b,
-                  int Hq, int Hkv, int all_tiles, float scale, float* __restrict__ part_o, float* __restrict__ part_ml,
+                  int Hq, int Hkv, int all_tiles, TreeScale scale, float* __restrict__ part_o, float* __restrict__ part_ml,
                   float* __restrict__ scores, int64_t lds)
 {
     extern __shared__ uint8_t tree_smem[];
@@ -326,6 +385,7 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* __restrict
     __shared__ TreeBars bar;
     __shared__ uint32_t tmem_at;
     __shared__ float mx[2][2][kTreeTile];  // a row's maxima of a tile's two halves, by tile parity
+    __shared__ volatile int bail[4];       // a wait of the row quarter's warps expired
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_trigger();
     if (warp == 9) {
@@ -343,11 +403,12 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* __restrict
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.s_full[i], 1);
             mbar_init(&bar.p_full[i], 256);
+            mbar_init(&bar.p_read[i], 1);
         }
         mbar_init(&bar.o_full, 1);
         mbar_init(&bar.o_free, 256);
         mbar_init(&bar.q_full, 256);
-        for (int i = 0; i < 4; ++i) mbar_init(&bar.x_full[i], 64);
+        for (int i = 0; i < 4; ++i) bail[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     tm_before();
@@ -367,55 +428,66 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* __restrict
             ring_drain<kTreeStages>(bar.k_full, n, late);
             ring_drain<kTreeStages>(bar.v_full, n, late);
         }
-        if (warp == 9 && lane == 0) tree_products(b, Hkv, u0, u1, smem_addr(tiles), tmem, bar);
+        if (warp == 9) tree_s(b, Hkv, u0, u1, smem_addr(tiles), tmem, bar);
+        if (warp == 10) tree_pv(b, Hkv, u0, u1, smem_addr(tiles), tmem, bar);
         __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         const int half = warp >> 2, quad = warp & 3, row = 32 * quad + lane, GQ = Hq / Hkv;
         const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
-        float o[64];                            // the chunk's sum, dims 64 half .. 64 half + 63
-        int i = 0, last = -1, R = 0, xn = 0;
-        bool ok = true;
+        uint64_t o[32];                         // the chunk's sum, dims 64 half .. 64 half + 63
+        int i = 0, last = -1, R = 0;
+        bool ok = true, left = false;
         // the tile whose O is still to come: its correction of the sum before
-        // it, whether the warp has rows in it, where the sum goes after it
+        // it (none: the chunk's first), whether the warp has rows in it, where
+        // the sum goes after it
         float prev_alpha = 0.0f;
-        bool prev_live = false;
+        bool prev_first = true, prev_live = false;
         float* prev_out = nullptr;
         auto take = [&](int j) {
-            if (!mbar_wait(&bar.o_full, j & 1, late)) return false;
+            const bool done = mbar_wait(&bar.o_full, j & 1, late);
             tm_after();
-            if (prev_live) {
+            if (prev_live && done) {
+                if (prev_first) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0;
+                }
+                const uint64_t al = pair(prev_alpha, prev_alpha);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     float x[32];
                     tm_ld32(lanes + kColO + 64 * half + 32 * c, x);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        o[32 * c + e] = prev_alpha == 0.0f ? x[e] : __fmaf_rn(o[32 * c + e], prev_alpha, x[e]);
+                    for (int e = 0; e < 16; ++e) o[16 * c + e] = fma2(o[16 * c + e], al, pair(x[2 * e], x[2 * e + 1]));
                 }
             }
             tm_before();
             mbar_arrive(&bar.o_free);
-            if (prev_out) {
+            if (prev_out && done) {
 #pragma unroll
-                for (int e = 0; e < 64; e += 8) st_v8(prev_out + e, o + e);
+                for (int e = 0; e < 32; e += 4) {
+                    const float2 a = unpair(o[e]), c = unpair(o[e + 1]), d = unpair(o[e + 2]), f = unpair(o[e + 3]);
+                    const float x[8] = {a.x, a.y, c.x, c.y, d.x, d.y, f.x, f.y};
+                    st_v8(prev_out + 2 * e, x);
+                }
             }
-            return true;
+            return done;
         };
-        for (int u = u0; ok && u < u1; ++u) {
+        for (int u = u0; !left && u < u1; ++u) {
             const TreeUnit t = tree_unit(b, Hkv, u);
             const TreeView& v = b.view[t.view];
+            const size_t at_row = (size_t)(v.row0 + row / GQ) * Hq + t.g * GQ + row % GQ;
             if (t.view * Hkv + t.g != last) {  // (S of every tile of the last head is complete: its q is free)
                 last = t.view * Hkv + t.g;
                 R = v.n_nodes * GQ;
                 if (32 * quad < R) {
                     uint32_t hi[32], lo[32];
-                    const float* qr = q + ((size_t)(v.row0 + row / GQ) * Hq + t.g * GQ + row % GQ) * kHeadDim + 64 * half;
+                    const float* qr = q + at_row * kHeadDim + 64 * half;
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const float4 x = row < R ? *reinterpret_cast<const float4*>(qr + 4 * e) : make_float4(0, 0, 0, 0);
-                        tree_split(x.x, x.y, hi[2 * e], lo[2 * e]);
-                        tree_split(x.z, x.w, hi[2 * e + 1], lo[2 * e + 1]);
+                        tree_split(__fmul_rn(x.x, scale.sign), __fmul_rn(x.y, scale.sign), hi[2 * e], lo[2 * e]);
+                        tree_split(__fmul_rn(x.z, scale.sign), __fmul_rn(x.w, scale.sign), hi[2 * e + 1], lo[2 * e + 1]);
                     }
                     tm_st32(lanes + kColQ + 32 * half, hi);
                     tm_st32(lanes + kColQ + 64 + 32 * half, lo);
@@ -426,77 +498,88 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* __restrict
             }
             const bool live = 32 * quad < R, valid = row < R;
             const int64_t pr = v.part0 + ((int64_t)t.c * Hkv + t.g) * R + row;
-            float* sc = scores && valid ? scores + ((size_t)(v.row0 + row / GQ) * Hq + t.g * GQ + row % GQ) * lds + t.key0 +
-                                              64 * half
-                                        : nullptr;
-            float m = -INFINITY, l = 0.0f;
+            float* sc = scores && valid ? scores + at_row * lds + t.key0 + 64 * half : nullptr;
+            float m = -INFINITY, l = 0.0f;  // m: a power of two's exponent
             for (int k = 0; k < t.tiles; ++k, ++i) {
                 const int n = min(kTreeTile, t.nkey - k * kTreeTile);  // keys of the tile
-                if (!(ok = mbar_wait(&bar.s_full[i & 1], (i >> 1) & 1, late))) break;
+                ok = ok && mbar_wait(&bar.s_full[i & 1], (i >> 1) & 1, late);
                 tm_after();
                 if (n < kTreeTile) {
                     // what lies behind the last key may be anything: its weight
                     // is 0, but 0 times a NaN would not be
                     const int st = i % kTreeStages;
-                    if (!(ok = mbar_wait(&bar.v_full[st], (i / kTreeStages) & 1, late))) break;
+                    ok = ok && mbar_wait(&bar.v_full[st], (i / kTreeStages) & 1, late);
                     uint8_t* vt = tiles + (kTreeStages + st) * kTreeTileBytes;
-                    for (int e = tid; e < (kTreeTile - n) * 16; e += 256)
+                    for (int e = tid; ok && e < (kTreeTile - n) * 16; e += 256)
                         *reinterpret_cast<uint4*>(vt + (e & 8) * (kTreeTileBytes / 16) + (n + (e >> 4)) * 128 + (e & 7) * 16) =
                             make_uint4(0, 0, 0, 0);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 float alpha = 0.0f;
+                if (!ok) bail[quad] = 1;
                 if (live) {
                     float s[64];
                     tm_ld64(lanes + kColS + 128 * (i & 1) + 64 * half, s);
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int e = 0; e < 64; ++e) s[e] = __fmul_rn(s[e], scale);
                     if (n < kTreeTile) {
 #pragma unroll
                         for (int e = 0; e < 64; ++e)
                             if (64 * half + e >= n) s[e] = -INFINITY;
                     }
+                    float tops[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                    for (int e = 4; e < 64; e += 8) {
+#pragma unroll
+                        for (int f = 0; f < 4; ++f)
+                            tops[f] = fmaxf(tops[f], e + 4 < 64 ? fmaxf(s[e + f], s[e + 4 + f]) : s[e + f]);
+                    }
+                    mx[i & 1][half][row] = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                    // the two warps of a row quarter always meet here (and
+                    // below), an expired wait or not, and leave together
+                    asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
+                    if ((left = bail[quad])) break;
+                    const float top = fmaxf(m, __fmul_rn(fmaxf(mx[i & 1][0][row], mx[i & 1][1][row]), scale.log2));
+                    const float at = top == -INFINITY ? 0.0f : top;
+                    alpha = tree_exp2(__fsub_rn(m, at));  // 0 for m = -inf
+                    m = top;
                     if (sc) {
                         float* to = sc + k * kTreeTile;
 #pragma unroll
                         for (int e = 0; e < 64; e += 4) {
-                            if (64 * half + e + 3 < n)
-                                *reinterpret_cast<float4*>(to + e) = make_float4(s[e], s[e + 1], s[e + 2], s[e + 3]);
-                            else
-#pragma unroll
-                                for (int f = e; f < e + 4; ++f)
-                                    if (64 * half + f < n) to[f] = s[f];
+                            const float4 x = make_float4(__fmul_rn(s[e], scale.abs), __fmul_rn(s[e + 1], scale.abs),
+                                                         __fmul_rn(s[e + 2], scale.abs), __fmul_rn(s[e + 3], scale.abs));
+                            if (64 * half + e + 3 < n) {
+                                *reinterpret_cast<float4*>(to + e) = x;
+                            } else {
+                                if (64 * half + e < n) to[e] = x.x;
+                                if (64 * half + e + 1 < n) to[e + 1] = x.y;
+                                if (64 * half + e + 2 < n) to[e + 2] = x.z;
+                            }
                         }
                     }
-#pragma unroll
-                    for (int e = 0; e < 64; ++e) top = fmaxf(top, s[e]);
-                    mx[xn & 1][half][row] = top;
-                    mbar_arrive(&bar.x_full[quad]);
-                    if (!(ok = mbar_wait(&bar.x_full[quad], xn & 1, late))) break;
-                    top = fmaxf(m, fmaxf(mx[xn & 1][0][row], mx[xn & 1][1][row]));
-                    ++xn;
-                    const float at = top == -INFINITY ? 0.0f : top;
-                    if (k > 0) alpha = tree_exp(__fsub_rn(m, at));  // 0 for m = -inf
-                    m = top;
-                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    const uint64_t c2 = pair(scale.log2, scale.log2), m2 = pair(-at, -at);
+                    uint64_t sum[4] = {0, 0, 0, 0};
                     uint32_t hi[32], lo[32];
 #pragma unroll
-                    for (int e = 0; e < 64; e += 2) {
-                        const float p0 = tree_exp(__fsub_rn(s[e], at)), p1 = tree_exp(__fsub_rn(s[e + 1], at));
-                        sum[e & 2] = __fadd_rn(sum[e & 2], p0);
-                        sum[(e & 2) + 1] = __fadd_rn(sum[(e & 2) + 1], p1);
-                        tree_split(p0, p1, hi[e / 2], lo[e / 2]);
+                    for (int e = 0; e < 32; ++e) {
+                        const float2 x = unpair(fma2(pair(s[2 * e], s[2 * e + 1]), c2, m2));
+                        const float p0 = tree_exp2(x.x), p1 = tree_exp2(x.y);
+                        sum[e & 3] = add2(sum[e & 3], pair(p0, p1));
+                        tree_split(p0, p1, hi[e], lo[e]);
                     }
-                    l = __fmaf_rn(l, alpha, __fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3])));
+                    const float2 ls = unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+                    l = __fmaf_rn(l, alpha, __fadd_rn(ls.x, ls.y));
                     tm_st32(lanes + kColS + 128 * (i & 1) + 64 * half, hi);
                     tm_st32(lanes + kColS + 128 * (i & 1) + 64 * half + 32, lo);
                     tm_wait_st();
+                } else {
+                    asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
+                    if ((left = bail[quad])) break;
                 }
                 tm_before();
                 mbar_arrive(&bar.p_full[i & 1]);
-                if (i > 0 && !(ok = take(i - 1))) break;
+                if (i > 0) ok = take(i - 1);
                 prev_alpha = alpha;
+                prev_first = k == 0;
                 prev_live = live;
                 prev_out = valid && k + 1 == t.tiles ? part_o + pr * kHeadDim + 64 * half : nullptr;
                 if (prev_out) {
@@ -505,10 +588,10 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* __restrict
                 }
             }
         }
-        if (ok && i > 0) ok = take(i - 1);
+        if (!left && i > 0) ok = take(i - 1) && ok;
         // after an expired wait products may still be running: wait once more
         // (bounded) for the last of them before tensor memory is freed
-        if (!ok && tid == 0 && i > 0) mbar_wait(&bar.o_full, (i - 1) & 1, late);
+        if (!(ok && !left) && tid == 0 && i > 0) mbar_wait(&bar.o_full, (i - 1) & 1, late);
     }
     tm_before();
     __syncthreads();
@@ -545,92 +628,134 @@ static bool tree_maps(const TreeBatch& b, int Hkv, TreeMaps* maps)
     return true;
 }
 
-// Merge of one (row, query head): the prefix's chunks in order, then the
-// node's path from the prefix down.  One thread per dim.
+// Merge of one (row, query head): the prefix's chunks and the node's path.
+// One CTA of 4 warps, 4 dims a lane.  Warp w sums chunks w, w + 4, .. in order
+// and then path keys w, w + 4, ..; the four sums are added in order.  It is
+// bound by latency, not bytes (R 528 bytes a chunk), so everything it reads is
+// asked for before anything is used: statistics, the first chunks' sums, the
+// path's K and V.
+constexpr int kMergeAhead = 8;  // chunk sums in flight per warp
+
+__device__ __forceinline__ float4 half4(uint2 x)
+{
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&x.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&x.y));
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+
+__device__ __forceinline__ void axpy4(float4& o, float4 x, float a)
+{
+    o.x = __fmaf_rn(x.x, a, o.x);
+    o.y = __fmaf_rn(x.y, a, o.y);
+    o.z = __fmaf_rn(x.z, a, o.z);
+    o.w = __fmaf_rn(x.w, a, o.w);
+}
+
 __global__ void __launch_bounds__(kHeadDim)
-tree_merge_kernel(const float* __restrict__ q, const __grid_constant__ TreeBatch b, int Hq, int Hkv, float scale,
+tree_merge_kernel(const float* __restrict__ q, const __grid_constant__ TreeBatch b, int Hq, int Hkv, TreeScale scale,
                   const float* __restrict__ part_o, const float* __restrict__ part_ml, float* __restrict__ out,
                   float* __restrict__ scores, int64_t lds, float* __restrict__ stats, int8_t* __restrict__ out_q,
                   float* __restrict__ out_d)
 {
-    __shared__ float w[kMaxTreeChunks];
-    __shared__ float ps[kMaxTree];
-    __shared__ float Ls;
+    __shared__ float ps[kMaxTree];            // the path's products
+    __shared__ float4 os[4][kHeadDim / 4];    // the warps' sums
     pdl_trigger();
-    const int h = blockIdx.x, r = blockIdx.y, d = threadIdx.x, lane = d & 31, warp = d >> 5;
+    const int h = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const TreeRow& row = b.row[r];
     const TreeView& v = b.view[row.view];
     const int GQ = Hq / Hkv, g = h / GQ, R = v.n_nodes * GQ, np = row.n_path, nch = v.n_chunk;
     const int64_t pr0 = v.part0 + (int64_t)g * R + row.node * GQ + h % GQ, pstep = (int64_t)Hkv * R;
+    const size_t rh = (size_t)r * Hq + h;
     pdl_wait();
-    const float* qr = q + ((size_t)r * Hq + h) * kHeadDim;
-    const float4 qv = *reinterpret_cast<const float4*>(qr + 4 * lane);
-    for (int a = warp; a < np; a += 4) {
-        const __half* k = tree_key(v, v.k, g, v.len + row.path[a]);
-        float acc = 0.0f;
-        if (k) {
-            const uint2 kv = *reinterpret_cast<const uint2*>(k + 4 * lane);
-            const float2 k0 = __half22float2(*reinterpret_cast<const __half2*>(&kv.x));
-            const float2 k1 = __half22float2(*reinterpret_cast<const __half2*>(&kv.y));
-            acc = __fmaf_rn(qv.w, k1.y, __fmaf_rn(qv.z, k1.x, __fmaf_rn(qv.y, k0.y, __fmul_rn(qv.x, k0.x))));
+    const float4 qv = *reinterpret_cast<const float4*>(q + rh * kHeadDim + 4 * lane);
+    uint2 kx[4], vx[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        kx[i] = vx[i] = make_uint2(0, 0);
+        if (warp + 4 * i < np) {
+            const int key = v.len + row.path[warp + 4 * i];
+            const __half* kp = tree_key(v, v.k, g, key);
+            const __half* vp = tree_key(v, v.v, g, key);
+            if (kp) kx[i] = *reinterpret_cast<const uint2*>(kp + 4 * lane);
+            if (vp) vx[i] = *reinterpret_cast<const uint2*>(vp + 4 * lane);
         }
-        acc = warp_sum_butterfly(acc);
-        if (lane == 0) ps[a] = __fmul_rn(acc, scale);
+    }
+    // every warp has all chunks' statistics: chunk lane + 32 j in its lane
+    float w[4], L = 0.0f, M = -INFINITY;
+    float2 ls[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int c = lane + 32 * j;
+        w[j] = -INFINITY;
+        ls[j] = make_float2(0.0f, 0.0f);
+        if (c < nch) {
+            const float4 ml = __ldcg(reinterpret_cast<const float4*>(part_ml + 4 * (pr0 + c * pstep)));
+            w[j] = ml.x;
+            ls[j] = make_float2(ml.y, ml.z);
+        }
+    }
+    float4 ov[kMergeAhead];
+    const float4* po = reinterpret_cast<const float4*>(part_o) + pr0 * (kHeadDim / 4) + lane;
+#pragma unroll
+    for (int j = 0; j < kMergeAhead; ++j)
+        if (warp + 4 * j < nch) ov[j] = __ldcg(po + (int64_t)(warp + 4 * j) * pstep * (kHeadDim / 4));
+
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 k = half4(kx[i]);
+        const float dot = warp_sum_butterfly(
+            __fmaf_rn(qv.w, k.w, __fmaf_rn(qv.z, k.z, __fmaf_rn(qv.y, k.y, __fmul_rn(qv.x, k.x)))));
+        if (lane == 0 && warp + 4 * i < np) ps[warp + 4 * i] = __fmul_rn(dot, scale.sign);
     }
     __syncthreads();
-    float* sc = scores ? scores + ((size_t)r * Hq + h) * lds + v.len : nullptr;
-    if (sc && d < v.n_nodes) {
+    if (scores && tid < v.n_nodes) {
         float x = -INFINITY;
         for (int a = 0; a < np; ++a)
-            if (row.path[a] == d) x = ps[a];
-        sc[d] = x;
+            if (row.path[a] == tid) x = __fmul_rn(ps[a], scale.abs);
+        scores[rh * lds + v.len + tid] = x;
     }
-    __syncthreads();  // the scores are read before the path's become weights
-    if (warp == 0) {
-        float M = -INFINITY;
-        for (int c = lane; c < nch; c += 32) {
-            const float m = __ldcg(part_ml + 4 * (pr0 + c * pstep));
-            w[c] = m;
-            M = fmaxf(M, m);
-        }
-        const float mine = lane < np ? ps[lane] : -INFINITY;
-        M = warp_max(fmaxf(M, mine));
-        const float ref = M == -INFINITY ? 0.0f : M;
-        float L = 0.0f;
-        for (int c = lane; c < nch; c += 32) {
-            const float f = expf(__fsub_rn(w[c], ref));
-            w[c] = f;
-            const float* ml = part_ml + 4 * (pr0 + c * pstep);
-            L = __fmaf_rn(__fadd_rn(__ldcg(ml + 1), __ldcg(ml + 2)), f, L);
-        }
-        L = warp_sum_butterfly(L);
-        __syncwarp();
-        if (lane < np) ps[lane] = expf(__fsub_rn(mine, ref));
-        __syncwarp();
-        for (int a = 0; a < np; ++a) L = __fadd_rn(L, ps[a]);
-        if (lane == 0) {
-            Ls = L;
-            if (stats) {
-                stats[2 * ((size_t)r * Hq + h)] = M;
-                stats[2 * ((size_t)r * Hq + h) + 1] = L;
-            }
-        }
+    float p = lane < np ? __fmul_rn(ps[lane], scale.log2) : -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) M = fmaxf(M, w[j]);
+    M = warp_max(fmaxf(M, p));
+    const float ref = M == -INFINITY ? 0.0f : M;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        w[j] = tree_exp2(__fsub_rn(w[j], ref));
+        L = __fmaf_rn(__fadd_rn(ls[j].x, ls[j].y), w[j], L);
     }
+    p = tree_exp2(__fsub_rn(p, ref));
+    L = __fadd_rn(warp_sum_butterfly(L), warp_sum_butterfly(p));
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {  // chunk 4 j + warp: its weight is in lane (4 j + warp) & 31's w[j >> 3]
+        const int c = 4 * j + warp;
+        if ((j & (kMergeAhead - 1)) == 0 && j > 0) {
+            if (4 * j >= nch) break;
+#pragma unroll
+            for (int e = 0; e < kMergeAhead; ++e)
+                if (c + 4 * e < nch) ov[e] = __ldcg(po + (int64_t)(c + 4 * e) * pstep * (kHeadDim / 4));
+        }
+        const float f = __shfl_sync(0xffffffffu, w[j >> 3], c & 31);
+        if (c < nch) axpy4(o, ov[j & (kMergeAhead - 1)], f);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float f = __shfl_sync(0xffffffffu, p, warp + 4 * i);
+        if (warp + 4 * i < np) axpy4(o, half4(vx[i]), f);
+    }
+    os[warp][lane] = o;
     __syncthreads();
-    float O = 0.0f;
-    for (int c = 0; c < nch; ++c) O = __fmaf_rn(__ldcg(part_o + (pr0 + c * pstep) * kHeadDim + d), w[c], O);
-    for (int a = 0; a < np; ++a) {
-        const __half* x = tree_key(v, v.v, g, v.len + row.path[a]);
-        if (x) O = __fmaf_rn(ps[a], __half2float(x[d]), O);
-    }
-    const float val = __fdiv_rn(O, Ls);
-    const size_t oi = ((size_t)r * Hq + h) * kHeadDim + d;
-    out[oi] = val;
+    const float* of = &os[0][0].x;
+    const float O = __fadd_rn(__fadd_rn(of[tid], of[kHeadDim + tid]), __fadd_rn(of[2 * kHeadDim + tid], of[3 * kHeadDim + tid]));
+    const float val = __fdiv_rn(O, L);
+    out[rh * kHeadDim + tid] = val;
+    if (stats && tid == 0) *reinterpret_cast<float2*>(stats + 2 * rh) = make_float2(__fmul_rn(M, scale.natural), L);
     if (out_q) {
         float dd;
         const int code = q8_quantize_lane(val, &dd);
-        out_q[oi] = (int8_t)code;
-        if (lane == 0) out_d[oi / 32] = dd;
+        out_q[rh * kHeadDim + tid] = (int8_t)code;
+        if (lane == 0) out_d[(rh * kHeadDim + tid) / 32] = dd;
     }
 }
 
@@ -645,6 +770,10 @@ cudaError_t launch_tree_attention(const float* q, const TreeBatch& b, int Hq, in
     }
     float* part_o = (float*)part;
     float* part_ml = part_o + n_part * kHeadDim;
+    // (a scale of 0 weighs all keys alike: its exponents are 0 to within 2^-100)
+    const TreeScale sc = {scale < 0 ? -1.0f : 1.0f, std::fabs(scale),
+                          std::max((float)(std::fabs((double)scale) * 1.4426950408889634), 1e-37f),
+                          scale == 0 ? 0.0f : kLn2};
     if (tiles > 0) {
         TreeMaps maps{};
         if (!tree_maps(b, Hkv, &maps)) return cudaErrorInvalidValue;
@@ -654,12 +783,12 @@ cudaError_t launch_tree_attention(const float* q, const TreeBatch& b, int Hq, in
         cudaError_t e = set_smem_once(tree_chunk_kernel, kTreeSmem, done);
         if (e == cudaSuccess)
             e = launch_pdl_smem(tree_chunk_kernel, dim3((unsigned)std::min<int64_t>(sms, tiles)), dim3(kTreeThreads),
-                                kTreeSmem, s, maps, q, b, Hq, Hkv, (int)tiles, scale, part_o, part_ml, scores, lds);
+                                kTreeSmem, s, maps, q, b, Hq, Hkv, (int)tiles, sc, part_o, part_ml, scores, lds);
         if (e != cudaSuccess) return e;
         count_launches(1);
     }
     const cudaError_t e =
-        launch_pdl(tree_merge_kernel, dim3(Hq, b.n_row), dim3(kHeadDim), s, q, b, Hq, Hkv, scale,
+        launch_pdl(tree_merge_kernel, dim3(Hq, b.n_row), dim3(kHeadDim), s, q, b, Hq, Hkv, sc,
                    (const float*)part_o, (const float*)part_ml, out, scores, lds, stats, out_q, out_d);
     count_launches(1);
     return e;

@@ -244,6 +244,25 @@ def test_large_scores_and_a_dominant_key():
     assert np.abs(out.cpu().numpy() - o).max() <= do
 
 
+@pytest.mark.parametrize("scale", [-0.09, 0.0, 1e-30, 1.0, 3.0])
+def test_scales(scale):
+    rng = np.random.default_rng(16)
+    s = Slot(rng, 8, 2, 700, tree_of("random", 5, 2))
+    q = cuda(s.q)
+    sc, st = torch.zeros(5, 8, 720, device="cuda"), torch.zeros(5, 8, 2, device="cuda")
+    out = luce.luce_tree_attn(q, [s.flat(0)], 2, scale, scores=sc, stats=st)
+    o, x, ml = ref.tree_attention(s.q, s.k, s.v, s.len, s.parent, scale)
+    ds, do, dl = ref.tree_tolerance(s.q, s.k, s.v, s.len, 5, scale, 128)
+    assert np.abs(out.cpu().numpy() - o).max() <= do
+    got, seen = sc[:, :, :705].cpu().numpy(), np.isfinite(x)
+    assert np.array_equal(np.isneginf(got), ~seen) and np.abs(got[seen] - x[seen]).max() <= ds
+    assert np.abs(st[..., 0].cpu().numpy() - ml[..., 0]).max() <= ds
+    # a weight from the scores and statistics is the weight of the definition
+    w = np.exp(got.astype(np.float64) - st[..., :1].cpu().numpy()) / st[..., 1:].cpu().numpy()
+    want = np.exp(x - ml[..., :1]) / ml[..., 1:]
+    assert np.abs(w - want)[seen].max() <= (4 * ds + 2.0 ** -23 * (700 + 300 + 88)) * want.max()
+
+
 def test_prepared_call_follows_len_streams_and_graphs():
     rng = np.random.default_rng(14)
     s = Slot(rng, 8, 2, 300, ref.chain(2), slack=40)
