@@ -1,10 +1,12 @@
 // cache.cu - what happens to a slot's cache between steps: the commit of a
 // verified tree's accepted path, and eviction by accumulated attention weight.
-#include <math.h>
+#include <algorithm>
+#include <cmath>
 
 #include "cache.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "ring.cuh"
 
 namespace luce {
 
@@ -15,24 +17,26 @@ namespace luce {
 // are all read before any is written and a path may move onto itself.
 //
 // Weights: acc_j += sum over accepted rows r and the group's heads h of
-// e^(s_rhj - m_rh) / l_rh; a stream over the scores (4 A GQ bytes per key
-// against 8 of acc), four keys per thread.
-constexpr int kCommitThreads = 256;
+// e^(s_rhj - m_rh) / l_rh: a stream over the scores (4 A GQ bytes per key
+// against 8 of acc), four keys per thread, eight rows of scores in flight.
+constexpr int kCommitThreads = 128;
 constexpr int kCommitKeys = 4 * kCommitThreads;
+constexpr int kCommitAhead = 8;
 
-__device__ __forceinline__ float commit_weight(const float* __restrict__ sc, int64_t lds, int64_t col, const float2* ml,
-                                               int n)
+__device__ __forceinline__ float commit_exp(float x)
 {
-    float w = 0.0f;
-    for (int i = 0; i < n; ++i) w = __fmaf_rn(expf(__fsub_rn(sc[i * lds + col], ml[i].x)), ml[i].y, w);
-    return w;
+    // e^x = 2^(x log2 e): x <= 0 but for rounding, off by at most |x| 2^-24 more
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(__fmul_rn(x, 1.4426950408889634f)));
+    return y;
 }
 
 __global__ void __launch_bounds__(kCommitThreads)
-tree_commit_kernel(CommitBatch b, int n_layers, int Hq, int Hkv, const float* __restrict__ scores, int n_rows,
-                   int64_t lds, const float* __restrict__ stats, int move_ctas)
+tree_commit_kernel(const __grid_constant__ CommitBatch b, int n_layers, int Hq, int Hkv, const float* __restrict__ scores,
+                   int n_rows, int64_t lds, const float* __restrict__ stats, int move_ctas)
 {
-    __shared__ float2 ml[kMaxTree * 8];  // (m, 1 / l) of the accepted rows' heads
+    __shared__ float2 ml[kMaxTree * 8];   // (m, 1 / l) of the accepted rows' heads
+    __shared__ int64_t at[kMaxTree * 8];  // and where their scores begin
     pdl_trigger();
     const CommitSlot& sl = b.slot[blockIdx.y];
     const int tid = threadIdx.x, A = sl.n_path, heads = n_layers * Hkv;
@@ -51,30 +55,48 @@ tree_commit_kernel(CommitBatch b, int n_layers, int Hq, int Hkv, const float* __
         if (sl.pos && lane < A) sl.pos[(int64_t)lh * sl.cap + sl.len + lane] = sl.pos0 + lane;
         return;
     }
-    const int64_t tiles = (sl.len + A + kCommitKeys - 1) / kCommitKeys;
-    int64_t at = blockIdx.x - move_ctas;
+    const int tiles = max(1, (sl.len + kCommitKeys - 1) / kCommitKeys);  // (the first also takes the new keys)
+    const int GQ = Hq / Hkv, part = blockIdx.x - move_ctas, lh = part / tiles, tile = part - lh * tiles, n = A * GQ;
+    if (!sl.acc || A == 0 || lh >= heads) return;
     pdl_wait();
-    if (!sl.acc || A == 0) return;
-    const int GQ = Hq / Hkv, lh = (int)(at / tiles);
-    if (lh >= heads) return;
     const int l = lh / Hkv, g = lh % Hkv;
-    for (int i = tid; i < A * GQ; i += kCommitThreads) {
-        const int64_t r = (int64_t)l * n_rows + sl.row0 + sl.path[i / GQ];
-        const float* st = stats + 2 * (r * Hq + g * GQ + i % GQ);
-        ml[i] = make_float2(st[0] == -INFINITY ? 0.0f : st[0], st[1] == 0.0f ? 0.0f : __fdiv_rn(1.0f, st[1]));
+    for (int i = tid; i < n; i += kCommitThreads) {
+        const int64_t rh = ((int64_t)l * n_rows + sl.row0 + sl.path[i / GQ]) * Hq + g * GQ + i % GQ;
+        const float m = stats[2 * rh], sum = stats[2 * rh + 1];
+        ml[i] = make_float2(m == -INFINITY ? 0.0f : m, sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum));
+        at[i] = rh * lds;
     }
     __syncthreads();
     float* acc = sl.acc + (int64_t)lh * sl.cap;
-    const int j0 = (int)(at % tiles) * kCommitKeys;
-    for (int j = j0 + tid; j < min(j0 + kCommitKeys, sl.len + A); j += kCommitThreads) {
-        const int col = j < sl.len ? j : sl.len + sl.path[j - sl.len];
+    if (tile == 0 && tid < A) {
         float w = 0.0f;
-        for (int a = 0; a < A; ++a) {
-            const int64_t r = (int64_t)l * n_rows + sl.row0 + sl.path[a];
-            w = __fadd_rn(w, commit_weight(scores + (r * Hq + g * GQ) * lds, lds, col, ml + a * GQ, GQ));
-        }
-        acc[j] = j < sl.len ? __fadd_rn(acc[j], w) : w;
+        for (int i = 0; i < n; ++i)
+            w = __fmaf_rn(commit_exp(__fsub_rn(scores[at[i] + sl.len + sl.path[tid]], ml[i].x)), ml[i].y, w);
+        acc[sl.len + tid] = w;
     }
+    const int j = tile * kCommitKeys + 4 * tid;
+    if (j >= sl.len) return;
+    float old[4], w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) old[e] = j + e < sl.len ? acc[j + e] : 0.0f;
+    for (int i0 = 0; i0 < n; i0 += kCommitAhead) {
+        float4 s[kCommitAhead];
+#pragma unroll
+        for (int e = 0; e < kCommitAhead; ++e)
+            if (i0 + e < n) s[e] = __ldcs(reinterpret_cast<const float4*>(scores + at[i0 + e] + j));
+#pragma unroll
+        for (int e = 0; e < kCommitAhead; ++e)
+            if (i0 + e < n) {
+                const float2 t = ml[i0 + e];
+                w[0] = __fmaf_rn(commit_exp(__fsub_rn(s[e].x, t.x)), t.y, w[0]);
+                w[1] = __fmaf_rn(commit_exp(__fsub_rn(s[e].y, t.x)), t.y, w[1]);
+                w[2] = __fmaf_rn(commit_exp(__fsub_rn(s[e].z, t.x)), t.y, w[2]);
+                w[3] = __fmaf_rn(commit_exp(__fsub_rn(s[e].w, t.x)), t.y, w[3]);
+            }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (j + e < sl.len) acc[j + e] = __fadd_rn(old[e], w[e]);
 }
 
 cudaError_t launch_tree_commit(const CommitBatch& b, int n_layers, int Hq, int Hkv, const float* scores, int n_rows,
@@ -84,7 +106,7 @@ cudaError_t launch_tree_commit(const CommitBatch& b, int n_layers, int Hq, int H
     int64_t tiles = 0;
     for (int i = 0; i < b.n_slot; ++i)
         if (b.slot[i].acc && b.slot[i].n_path > 0)
-            tiles = max(tiles, (int64_t)(b.slot[i].len + b.slot[i].n_path + kCommitKeys - 1) / kCommitKeys);
+            tiles = std::max<int64_t>(tiles, std::max(1, (b.slot[i].len + kCommitKeys - 1) / kCommitKeys));
     const int64_t move = (heads + kCommitThreads / 32 - 1) / (kCommitThreads / 32);
     const cudaError_t e = launch_pdl(tree_commit_kernel, dim3((unsigned)(move + heads * tiles), b.n_slot),
                                      dim3(kCommitThreads), s, b, n_layers, Hq, Hkv, scores, n_rows, lds, stats,
@@ -95,13 +117,25 @@ cudaError_t launch_tree_commit(const CommitBatch& b, int n_layers, int Hq, int H
 
 // ---------------------------------------------------------------- eviction
 //
-// One CTA per (slot, layer, KV head).  The n = len - budget keys that leave
-// are the lowest of an ordered 32-bit form of acc (NaN lowest, protected keys
-// highest): a radix selection finds the n-th lowest value T, 8 bits at a pass
-// over a 256-bin histogram, and how many keys equal to T leave; of those the
-// ones with the highest indexes do.  Then holes (index < budget, leaving) and
-// comers (index >= budget, staying) are found in ascending order and paired.
-constexpr int kEvictThreads = 1024;
+// One cluster of C CTAs per (slot, layer, KV head), each with a slice of the
+// head's keys in shared memory as an ordered 32-bit rank (NaN 0, weights by
+// value, protected keys highest).  The n = len - budget lowest leave:
+//   1. a radix selection finds the n-th lowest rank T and how many keys equal
+//      to T leave: three passes over the slice (11, 11, 10 bits), each a
+//      histogram in shared memory that every CTA adds up over the cluster;
+//   2. of the keys equal to T the first `stay` stay, counted through the
+//      cluster in index order;
+//   3. holes (index < budget, leaving) and comers (index >= budget, staying)
+//      are listed in index order by each CTA; the i-th hole of the cluster
+//      gets the i-th comer's rows, 32 pairs at a time per warp.
+// No atomics but integer counts, so nothing depends on their order.
+// Bound by latency while few keys leave (each step is a cluster barrier), by
+// the moved rows' bytes where a prompt is cut.
+constexpr int kEvictThreads = 512;
+constexpr int kEvictWarps = kEvictThreads / 32;
+constexpr int kEvictBins = 2048;
+constexpr int kEvictSlice = 16352;  // most keys of a CTA: 8 CTAs hold 130,816
+constexpr int kEvictMove = 4;  // pairs of rows in flight per warp
 
 __device__ __forceinline__ uint32_t evict_rank(float a, int pos, const EvictSlot& sl)
 {
@@ -111,140 +145,277 @@ __device__ __forceinline__ uint32_t evict_rank(float a, int pos, const EvictSlot
     return u >> 31 ? ~u : u | 0x80000000u;  // at most 0xff800000
 }
 
-// Exclusive prefix of flag over the CTA's threads, and their number.
-__device__ __forceinline__ int evict_prefix(bool flag, int* warp_n, int* total)
+__device__ __forceinline__ void cluster_sync()
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t m = __ballot_sync(0xffffffffu, flag);
-    __syncthreads();
-    if (lane == 0) warp_n[warp] = __popc(m);
-    __syncthreads();
-    int before = 0, all = 0;
-    for (int i = 0; i < kEvictThreads / 32; ++i) {
-        if (i < warp) before += warp_n[i];
-        all += warp_n[i];
-    }
-    *total = all;
-    return before + __popc(m & ((1u << lane) - 1));
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// A word of CTA r's shared memory at this CTA's address p.
+__device__ __forceinline__ uint32_t far_addr(const void* p, int r)
+{
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(r));
+    return a;
+}
+__device__ __forceinline__ int far_ld(uint32_t a)
+{
+    int v;
+    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ int4 far_ld4(uint32_t a)
+{
+    int4 v;
+    asm volatile("ld.shared::cluster.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
 }
 
-__global__ void __launch_bounds__(kEvictThreads)
-kv_evict_kernel(EvictBatch b)
+// Exclusive prefix of v over the CTA's threads; *total the sum.
+__device__ __forceinline__ int block_prefix(int v, int* warp_sum, int* total)
 {
-    __shared__ int hist[256];
-    __shared__ int warp_n[kEvictThreads / 32];
-    __shared__ int digit, below;
-    __shared__ int hole[2 * kEvictThreads], come[2 * kEvictThreads];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    int s = lane < kEvictWarps ? warp_sum[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < kEvictWarps; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
+    }
+    *total = __shfl_sync(0xffffffffu, s, kEvictWarps - 1);
+    const int before = __shfl_sync(0xffffffffu, s, max(warp - 1, 0));
+    return x - v + (warp ? before : 0);
+}
+
+template <int C>
+__global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kEvictThreads)
+kv_evict_kernel(const __grid_constant__ EvictBatch b, int slice)
+{
+    extern __shared__ uint32_t evict_smem[];  // ranks [slice], then the lists [slice]
+    __shared__ __align__(16) int hist[2][kEvictBins];
+    __shared__ int warp_sum[kEvictWarps];
+    __shared__ int digit, below, equal;
+    __shared__ int n_eq, n_hole, n_come;  // this CTA's, for the cluster
     pdl_trigger();
     const EvictSlot& sl = b.slot[blockIdx.y];
-    const int64_t lh = blockIdx.x;
+    const int64_t lh = blockIdx.x / C;
+    const int me = C > 1 ? (int)cluster_rank() : 0;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const float* acc = sl.acc + lh * sl.cap;
     const int32_t* pos = sl.pos + lh * sl.cap;
     float* acc_out = sl.acc_out + lh * sl.cap;
     int32_t* pos_out = sl.pos_out + lh * sl.cap;
-    pdl_wait();
-    const int keep = min(sl.len, sl.budget);
-    for (int j = tid; j < keep; j += kEvictThreads) {  // (holes are overwritten below)
-        if (acc_out != acc) acc_out[j] = acc[j];
-        if (pos_out != pos) pos_out[j] = pos[j];
-    }
+    uint32_t* rank = evict_smem;
+    uint32_t* list = evict_smem + slice;
+    const int j0 = min(me * slice, sl.len), nj = min(slice, sl.len - j0);  // this CTA's keys
     const int n = sl.len - sl.budget;
-    if (n <= 0) return;
-    uint32_t T = 0;
-    int left = n;  // keys that leave among those sharing T's leading digits
-    for (int sh = 24; sh >= 0; sh -= 8) {
-        __syncthreads();
-        if (tid < 256) hist[tid] = 0;
-        __syncthreads();
-        for (int j = tid; j < sl.len; j += kEvictThreads) {
-            const uint32_t u = evict_rank(acc[j], pos[j], sl);
-            if (sh == 24 || (u >> (sh + 8)) == (T >> (sh + 8))) atomicAdd(&hist[(u >> sh) & 255], 1);
+    for (int i = tid; i < 2 * kEvictBins; i += kEvictThreads) (&hist[0][0])[i] = 0;
+    __syncthreads();
+    pdl_wait();
+    for (int i = tid; i < nj; i += kEvictThreads) {
+        const int j = j0 + i;
+        const float a = acc[j];
+        const int p = pos[j];
+        if (j < sl.budget) {  // (holes are overwritten below)
+            if (acc_out != acc) acc_out[j] = a;
+            if (pos_out != pos) pos_out[j] = p;
         }
-        __syncthreads();
-        if (tid == 0) {
-            int at = 0, d = 0;
-            while (d < 255 && at + hist[d] < left) at += hist[d++];
-            digit = d;
+        const uint32_t u = evict_rank(a, p, sl);
+        rank[i] = u;
+        if (n > 0) atomicAdd(&hist[0][u >> 21], 1);
+    }
+    if (n <= 0) return;  // (the whole cluster)
+
+    // 1. T, `left` keys equal to it leave
+    uint32_t T = 0;
+    int left = n, same = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+        const int sh = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+        int* mine = hist[pass & 1];
+        if (pass > 0) {
+            const int width = pass == 1 ? 11 : 10;
+            for (int i = tid; i < nj; i += kEvictThreads) {
+                const uint32_t u = rank[i];
+                if (u >> (sh + width) == T >> (sh + width)) atomicAdd(&mine[(u >> sh) & ((1u << width) - 1)], 1);
+            }
+        }
+        if (C > 1) cluster_sync(); else __syncthreads();
+        // four bins a thread, over the cluster
+        int4 c = make_int4(0, 0, 0, 0);
+        if (C == 1) {
+            c = reinterpret_cast<const int4*>(mine)[tid];
+        } else {
+#pragma unroll
+            for (int r = 0; r < C; ++r) {
+                const int4 x = far_ld4(far_addr(mine + 4 * tid, r));
+                c.x += x.x;
+                c.y += x.y;
+                c.z += x.z;
+                c.w += x.w;
+            }
+        }
+        int all;
+        const int before = block_prefix(c.x + c.y + c.z + c.w, warp_sum, &all);
+        if (before < left && left <= before + c.x + c.y + c.z + c.w) {
+            int at = before, d = 0;
+            const int cs[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (d == e && at + cs[e] < left) {
+                    at += cs[e];
+                    ++d;
+                }
+            digit = 4 * tid + d;
             below = at;
+            equal = cs[d];
         }
         __syncthreads();
         T |= (uint32_t)digit << sh;
         left -= below;
-    }
-    __syncthreads();
-    // keys equal to T: the first `stay` of them stay
-    const int stay = hist[T & 255] - left;
-    __half* kb = sl.k + lh * sl.cap * (int64_t)kHeadDim;
-    __half* vb = sl.v + lh * sl.cap * (int64_t)kHeadDim;
-    int eq_h = 0;  // keys equal to T before the hole cursor
-    int eq_c = 0;  // and before the comer cursor
-    for (int j0 = 0; j0 < sl.budget; j0 += kEvictThreads) {
-        const int j = j0 + tid;
-        int all;
-        evict_prefix(j < sl.budget && evict_rank(acc[min(j, sl.len - 1)], pos[min(j, sl.len - 1)], sl) == T, warp_n, &all);
-        eq_c += all;
-    }
-    int jh = 0, jc = sl.budget, nh = 0, nc = 0;
-    for (;;) {
-        while (nh < kEvictThreads && jh < sl.budget) {
-            const int j = jh + tid;
-            const uint32_t u = j < sl.budget ? evict_rank(acc[j], pos[j], sl) : 0xffffffffu;
-            int all;
-            const int e = eq_h + evict_prefix(j < sl.budget && u == T, warp_n, &all);
-            eq_h += all;
-            const bool f = j < sl.budget && (u < T || (u == T && e >= stay));
-            const int at = nh + evict_prefix(f, warp_n, &all);
-            if (f) hole[at] = j;
-            nh += all;
-            jh += kEvictThreads;
-        }
-        while (nc < kEvictThreads && jc < sl.len) {
-            const int j = jc + tid;
-            const uint32_t u = j < sl.len ? evict_rank(acc[j], pos[j], sl) : 0;
-            int all;
-            const int e = eq_c + evict_prefix(j < sl.len && u == T, warp_n, &all);
-            eq_c += all;
-            const bool f = j < sl.len && (u > T || (u == T && e < stay));
-            const int at = nc + evict_prefix(f, warp_n, &all);
-            if (f) come[at] = j;
-            nc += all;
-            jc += kEvictThreads;
+        same = equal;
+        // pass 2 counts in hist[0] again, which the other CTAs have read by
+        // now only if they are past pass 1's barrier: it is cleared behind that
+        if (pass == 1) {
+            for (int i = tid; i < kEvictBins; i += kEvictThreads) hist[0][i] = 0;
         }
         __syncthreads();
-        const int m = min(nh, nc);
-        if (m == 0) return;
-        for (int i = warp; i < m; i += kEvictThreads / 32) {
-            uint4* base = reinterpret_cast<uint4*>(lane < 16 ? kb : vb) + (lane & 15);
-            base[(int64_t)hole[i] * 16] = base[(int64_t)come[i] * 16];
-        }
-        for (int i = tid; i < m; i += kEvictThreads) {
-            acc_out[hole[i]] = acc[come[i]];
-            pos_out[hole[i]] = pos[come[i]];
-        }
-        // the unpaired ones move to the front of their list
-        int h0 = 0, h1 = 0, c0 = 0, c1 = 0;
-        const int i0 = m + tid, i1 = m + tid + kEvictThreads;
-        if (i0 < nh) h0 = hole[i0];
-        if (i1 < nh) h1 = hole[i1];
-        if (i0 < nc) c0 = come[i0];
-        if (i1 < nc) c1 = come[i1];
-        __syncthreads();
-        if (i0 < nh) hole[tid] = h0;
-        if (i1 < nh) hole[tid + kEvictThreads] = h1;
-        if (i0 < nc) come[tid] = c0;
-        if (i1 < nc) come[tid + kEvictThreads] = c1;
-        nh -= m;
-        nc -= m;
-        __syncthreads();
     }
+    const int stay = same - left;  // the first keys equal to T, in index order
+
+    // 2. each thread's run of the slice: keys equal to T before it
+    const int run = (nj + kEvictThreads - 1) / kEvictThreads, r0 = min(tid * run, nj), r1 = min(r0 + run, nj);
+    int eq = 0;
+    for (int i = r0; i < r1; ++i) eq += rank[i] == T;
+    int all;
+    int eq_at = block_prefix(eq, warp_sum, &all);
+    if (C > 1) {
+        if (tid == 0) n_eq = all;
+        cluster_sync();
+#pragma unroll
+        for (int r = 0; r < C; ++r)
+            if (r < me) eq_at += far_ld(far_addr(&n_eq, r));
+    }
+
+    // 3. holes from the list's front, comers from its back
+    int holes = 0, comes = 0, e = eq_at;
+    for (int i = r0; i < r1; ++i) {
+        const uint32_t u = rank[i];
+        const bool leaves = u < T || (u == T && e >= stay);
+        e += u == T;
+        if (j0 + i < sl.budget) holes += leaves;
+        else comes += !leaves;
+    }
+    int nh, nc;
+    int h_at = block_prefix(holes, warp_sum, &nh), c_at = block_prefix(comes, warp_sum, &nc);
+    e = eq_at;
+    for (int i = r0; i < r1; ++i) {
+        const uint32_t u = rank[i];
+        const bool leaves = u < T || (u == T && e >= stay);
+        e += u == T;
+        if (j0 + i < sl.budget) {
+            if (leaves) list[h_at++] = j0 + i;
+        } else if (!leaves) {
+            list[slice - 1 - c_at++] = j0 + i;
+        }
+    }
+    if (tid == 0) {
+        n_hole = nh;
+        n_come = nc;
+    }
+    if (C > 1) cluster_sync(); else __syncthreads();
+    int h_before[C], c_before[C], m = 0, mc = 0;
+#pragma unroll
+    for (int r = 0; r < C; ++r) {
+        h_before[r] = m;
+        c_before[r] = mc;
+        m += C > 1 ? far_ld(far_addr(&n_hole, r)) : n_hole;
+        mc += C > 1 ? far_ld(far_addr(&n_come, r)) : n_come;
+    }
+    const int64_t rows = lh * sl.cap * 16;
+    uint4* base = reinterpret_cast<uint4*>(lane < 16 ? sl.k : sl.v) + rows + (lane & 15);
+    for (int i0 = 32 * (me * kEvictWarps + warp); i0 < m; i0 += 32 * C * kEvictWarps) {
+        const int i = i0 + lane, cnt = min(32, m - i0);
+        int to = 0, from = 0;
+        if (i < m) {
+            int rh = 0, rc = 0;
+#pragma unroll
+            for (int r = 1; r < C; ++r) {
+                if (i >= h_before[r]) rh = r;
+                if (i >= c_before[r]) rc = r;
+            }
+            int hb = 0, cb = 0;
+#pragma unroll
+            for (int r = 0; r < C; ++r) {
+                if (r == rh) hb = h_before[r];
+                if (r == rc) cb = c_before[r];
+            }
+            if (C > 1) {
+                to = far_ld(far_addr(list + (i - hb), rh));
+                from = far_ld(far_addr(list + (slice - 1 - (i - cb)), rc));
+            } else {
+                to = (int)list[i];
+                from = (int)list[slice - 1 - i];
+            }
+            acc_out[to] = acc[from];
+            pos_out[to] = pos[from];
+        }
+        for (int k = 0; k < cnt; k += kEvictMove) {
+            uint4 x[kEvictMove];
+#pragma unroll
+            for (int d = 0; d < kEvictMove; ++d) {
+                const int f = __shfl_sync(0xffffffffu, from, (k + d) & 31);
+                if (k + d < cnt) x[d] = __ldcs(base + (int64_t)f * 16);
+            }
+#pragma unroll
+            for (int d = 0; d < kEvictMove; ++d) {
+                const int t = __shfl_sync(0xffffffffu, to, (k + d) & 31);
+                if (k + d < cnt) base[(int64_t)t * 16] = x[d];
+            }
+        }
+    }
+    if (C > 1) cluster_sync();  // the others still read this CTA's list
+}
+
+template <int C>
+static cudaError_t launch_evict(const EvictBatch& b, int heads, int max_len, cudaStream_t s)
+{
+    const int slice = std::max(1, (max_len + C - 1) / C);
+    static std::atomic<bool> done[kMaxDevices];
+    cudaError_t e = set_smem_once(kv_evict_kernel<C>, 8 * kEvictSlice, done);
+    if (e == cudaSuccess)
+        e = launch_pdl_smem(kv_evict_kernel<C>, dim3((unsigned)heads * C, b.n_slot), dim3(kEvictThreads), 8 * (size_t)slice, s,
+                            b, slice);
+    count_launches(1);
+    return e;
 }
 
 cudaError_t launch_kv_evict(const EvictBatch& b, int n_layers, int Hkv, cudaStream_t s)
 {
-    const cudaError_t e = launch_pdl(kv_evict_kernel, dim3((unsigned)n_layers * Hkv, b.n_slot), dim3(kEvictThreads), s, b);
-    count_launches(1);
-    return e;
+    int max_len = 0;
+    for (int i = 0; i < b.n_slot; ++i) max_len = std::max(max_len, b.slot[i].len);
+    const int heads = n_layers * Hkv;
+    int c = 1;
+    while (c < 8 && ((max_len + c - 1) / c > kEvictSlice || (max_len / c > 4096 && (int64_t)heads * b.n_slot * c < 304)))
+        c *= 2;
+    switch (c) {
+        case 1: return launch_evict<1>(b, heads, max_len, s);
+        case 2: return launch_evict<2>(b, heads, max_len, s);
+        case 4: return launch_evict<4>(b, heads, max_len, s);
+        default: return launch_evict<8>(b, heads, max_len, s);
+    }
 }
 
 }  // namespace luce
