@@ -550,7 +550,7 @@ typedef struct luce_pagedtreeview {
  * and query head h (KV head g = h / (Hq/Hkv)), over the keys i that j sees:
  *   s_i = scale * q[r][h] . K[g][i],  m = max s_i,  l = sum e^(s_i - m),
  *   out[r][h] = sum (e^(s_i - m) / l) V[g][i]
- * The prefix is cut into chunks whose size follows from len alone; the node's
+ * The prefix is cut into chunks whose size follows from len and Hkv; the node's
  * own path is added to their merge in path order.  So a node's outputs depend
  * on its prefix and its path only: it gives the same bits in any tree, in a
  * chain of its own path, with any other slots, flat or paged.
@@ -577,7 +577,7 @@ int luce_tree_attn_paged(const float* q, const luce_pagedtreeview* views, int n_
 
 /* Bytes of scratch luce_tree_attn needs for n_rows rows over prefixes of at
  * most max_len keys (0 for arguments it refuses). */
-size_t luce_tree_attn_workspace_size(int n_rows, int Hq, int D, int max_len);
+size_t luce_tree_attn_workspace_size(int n_rows, int Hq, int Hkv, int D, int max_len);
 
 /*
  * A slot whose verified tree is committed: the accepted nodes path[0] <

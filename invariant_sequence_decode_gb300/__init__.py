@@ -165,7 +165,7 @@ def load_library(path: str = LIB_PATH):
     lib.luce_tree_attn.argtypes = [vp, ctypes.POINTER(TreeViewC), i32, i32, i32, i32, f32, vp, vp, i64, vp, vp, sz, vp]
     lib.luce_tree_attn_paged.argtypes = [vp, ctypes.POINTER(PagedTreeViewC), i32, i32, i32, i32, f32, vp, vp, i64, vp,
                                          vp, sz, vp]
-    lib.luce_tree_attn_workspace_size.argtypes = [i32, i32, i32, i32]
+    lib.luce_tree_attn_workspace_size.argtypes = [i32, i32, i32, i32, i32]
     lib.luce_tree_attn_workspace_size.restype = sz
     lib.luce_tree_commit.argtypes = [ctypes.POINTER(CommitSlotC), i32, i32, i32, i32, i32, vp, i32, i64, vp, vp]
     lib.luce_kv_evict.argtypes = [ctypes.POINTER(EvictSlotC), i32, i32, i32, i32, vp]
@@ -760,29 +760,45 @@ class _Prepared:
 
     _owned = ()
     _home = None
+    _lent = frozenset()
 
     def _bind(self, fn, device, stream, keep):
-        self._fn, self._device, self._stream, self._keep = fn, device, stream, keep
+        import torch
+        self._fn, self._index, self._keep = fn, device.index, (stream, keep)
+        self._stream = None if stream is None else stream.cuda_stream
+        self._device_now, self._stream_now = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
     def _allocate(self, shape, dtype, device, stream):
         import torch
-        home = stream if stream is not None else torch.cuda.current_stream(device)
-        with torch.cuda.stream(home):
+        if stream is None:
             t = torch.empty(shape, dtype=dtype, device=device)
-        self._home, self._owned = home, self._owned + (t,)
+            self._home = torch._C._cuda_getCurrentRawStream(device.index)
+        else:
+            with torch.cuda.stream(stream):
+                t = torch.empty(shape, dtype=dtype, device=device)
+            self._home = stream.cuda_stream
+        self._owned = self._owned + (t,)
         return t
 
-    def _call(self, *args):
+    def _lend(self, stream):
+        """The object's own memory is used on another stream than its own."""
         import torch
-        s = self._stream if self._stream is not None else torch.cuda.current_stream(self._device)
-        if self._owned and s != self._home:
-            for t in self._owned:
-                t.record_stream(s)
-        if torch.cuda.current_device() == self._device.index:
-            _check(self._fn(*args, s.cuda_stream))
+        for t in self._owned:
+            t.record_stream(torch.cuda.ExternalStream(stream, device=t.device))
+        self._lent = self._lent | {stream}
+
+    def _call(self, *args):
+        s = self._stream if self._stream is not None else self._stream_now(self._index)
+        if s != self._home and self._owned and s not in self._lent:
+            self._lend(s)
+        if self._device_now() == self._index:
+            rc = self._fn(*args, s)
         else:
-            with torch.cuda.device(self._device):
-                _check(self._fn(*args, s.cuda_stream))
+            import torch
+            with torch.cuda.device(self._index):
+                rc = self._fn(*args, s)
+        if rc != LUCE_OK:
+            _check(rc)
 
 
 class TreeAttention(_Prepared):
@@ -803,6 +819,8 @@ class TreeAttention(_Prepared):
         if not self.views:
             raise ValueError("views: expected at least one")
         paged = isinstance(self.views[0], PagedTreeView)
+        if not all(isinstance(v, PagedTreeView if paged else TreeView) for v in self.views):
+            raise TypeError("views: expected TreeViews or PagedTreeViews, of one kind")
         trees = [_tree(v.parent) for v in self.views]
         rows = max(v.row0 + n for v, (n, _) in zip(self.views, trees))
         if rows != T:
@@ -849,26 +867,33 @@ class TreeAttention(_Prepared):
                                         v.k.stride(1), par)
             name = "luce_tree_attn"
         _same_device(q, self.out, scores, stats, ws)
-        self._caps = caps
+        self._caps, self._items, self._lens = caps, [self._vc[i] for i in range(n)], [v.len for v in self.views]
+        for v, cap in zip(self.views, caps):
+            self._fits(v.len, cap)
         if ws is None:
-            need = luce_tree_attn_workspace_size(T, Hq, D, max(0, *caps))
+            need = luce_tree_attn_workspace_size(T, Hq, int(n_kv_heads), D, max(0, *caps))
             ws = self._allocate((max(256, need),), torch.uint8, q.device, stream)
         _need(ws, torch.uint8, "ws")
         self._args = (q.data_ptr(), self._vc, n, Hq, int(n_kv_heads), D, float(scale), self.out.data_ptr(), _ptr(scores),
                       lds, _ptr(stats), ws.data_ptr(), ws.numel())
         self._bind(getattr(load_library(), name), q.device, stream, (q, scores, stats, ws, trees))
 
+    @staticmethod
+    def _fits(length, cap):
+        if length > cap:
+            raise ValueError(f"len {length} and the tree exceed the cache")
+
     def __call__(self):
-        for c, v, cap in zip(self._vc, self.views, self._caps):
-            if v.len > cap:
-                raise ValueError(f"len {v.len} and the tree exceed the cache")
-            c.len = v.len
+        for i, v in enumerate(self.views):
+            if v.len != self._lens[i]:
+                self._fits(v.len, self._caps[i])
+                self._items[i].len = self._lens[i] = v.len
         self._call(*self._args)
         return self.out
 
 
-def luce_tree_attn_workspace_size(n_rows: int, Hq: int, D: int, max_len: int) -> int:
-    return int(load_library().luce_tree_attn_workspace_size(n_rows, Hq, D, max_len))
+def luce_tree_attn_workspace_size(n_rows: int, Hq: int, Hkv: int, D: int, max_len: int) -> int:
+    return int(load_library().luce_tree_attn_workspace_size(n_rows, Hq, Hkv, D, max_len))
 
 
 def luce_tree_attn(q, views: Sequence[TreeView], n_kv_heads: int, scale: float, out=None, scores=None, stats=None,
@@ -925,20 +950,20 @@ class TreeCommit(_Prepared):
             _same_device(self.slots[0].k, s.k, s.v, s.acc, s.pos, scores, stats)
             self._sc[i] = CommitSlotC(s.k.data_ptr(), s.v.data_ptr(), s.len, s.k.shape[2], 0, s.row0, None, _ptr(s.acc),
                                       _ptr(s.pos), s.pos0)
-        self._paths = [None] * len(self.slots)
+        self._now = [None] * len(self.slots)
         self._arrays = [None] * len(self.slots)
         self._args = (self._sc, len(self.slots), L, int(n_q_heads), Hkv, HEAD_DIM, _ptr(scores), n_rows, lds, _ptr(stats))
         self._bind(load_library().luce_tree_commit, self.slots[0].k.device, stream, (scores, stats))
 
     def __call__(self):
         for i, s in enumerate(self.slots):
-            c = self._sc[i]
-            c.len, c.row0, c.pos0 = s.len, s.row0, s.pos0
-            path = tuple(s.path)
-            if path != self._paths[i]:
-                self._paths[i] = path
+            now = (s.len, s.row0, s.pos0, *s.path)
+            if now != self._now[i]:
+                path = now[3:]
                 self._arrays[i] = (ctypes.c_int32 * max(1, len(path)))(*path)
-                c.path, c.n_path = self._arrays[i], len(path)
+                c = self._sc[i]
+                c.len, c.row0, c.pos0, c.path, c.n_path = s.len, s.row0, s.pos0, self._arrays[i], len(path)
+                self._now[i] = now
         self._call(*self._args)
 
 
@@ -975,12 +1000,16 @@ class KvEvict(_Prepared):
             self._sc[i] = EvictSlotC(s.k.data_ptr(), s.v.data_ptr(), s.acc.data_ptr(), s.pos.data_ptr(),
                                      acc_out.data_ptr(), pos_out.data_ptr(), s.len, s.k.shape[2], s.budget, s.sinks,
                                      s.recent, s.next_pos)
+        self._now = [None] * len(self.slots)
         self._args = (self._sc, len(self.slots), L, Hkv, HEAD_DIM)
         self._bind(load_library().luce_kv_evict, self.slots[0].k.device, stream, None)
 
     def __call__(self):
-        for c, s in zip(self._sc, self.slots):
-            c.len, c.next_pos = s.len, s.next_pos
+        for i, s in enumerate(self.slots):
+            now = (s.len, s.next_pos)
+            if now != self._now[i]:
+                self._sc[i].len, self._sc[i].next_pos = now
+                self._now[i] = now
         self._call(*self._args)
 
 

@@ -32,12 +32,12 @@ int luce::tree_path(const int32_t* parent, int n_nodes, TreeRow* rows, int view,
     return LUCE_OK;
 }
 
-int64_t luce::tree_chunks(TreeBatch& b, int Hq)
+int64_t luce::tree_chunks(TreeBatch& b, int Hq, int Hkv)
 {
     int64_t part = 0;
     for (int i = 0; i < b.n_view; ++i) {
         TreeView& v = b.view[i];
-        v.chunk = tree_chunk_keys(v.len);
+        v.chunk = tree_chunk_keys(v.len, Hkv);
         v.n_chunk = (v.len + v.chunk - 1) / v.chunk;
         v.part0 = part;
         part += (int64_t)v.n_chunk * v.n_nodes * Hq;
@@ -45,11 +45,12 @@ int64_t luce::tree_chunks(TreeBatch& b, int Hq)
     return part;
 }
 
-size_t luce_tree_attn_workspace_size(int n_rows, int Hq, int D, int max_len)
+size_t luce_tree_attn_workspace_size(int n_rows, int Hq, int Hkv, int D, int max_len)
 {
-    if (n_rows < 1 || n_rows > LUCE_MAX_ROWS || Hq < 1 || D != LUCE_HEAD_DIM || max_len < 0 || max_len > LUCE_MAX_KEYS)
+    if (n_rows < 1 || n_rows > LUCE_MAX_ROWS || Hkv < 1 || Hq < Hkv || Hq % Hkv || Hq / Hkv > 8 || Hkv > 4096 ||
+        D != LUCE_HEAD_DIM || max_len < 0 || max_len > LUCE_MAX_KEYS)
         return 0;
-    return std::max<size_t>(256, tree_part_bytes((int64_t)tree_max_chunks(max_len) * n_rows * Hq));
+    return std::max<size_t>(256, tree_part_bytes((int64_t)tree_max_chunks(max_len, Hkv) * n_rows * Hq));
 }
 
 static int check_tree_call(const float* q, const void* views, int n_seq, int Hq, int Hkv, int D, float scale,
@@ -103,7 +104,7 @@ static int run_tree(TreeBatch& b, const bool* covered, const float* q, int Hq, i
                     float* scores, int64_t lds, float* stats, void* ws, size_t ws_bytes, void* stream, const char* who)
 {
     for (int r = 0; r < b.n_row; ++r) REQUIRE(covered[r], LUCE_EINVAL, "%s: row %d belongs to no view", who, r);
-    const size_t need = tree_part_bytes(tree_chunks(b, Hq));
+    const size_t need = tree_part_bytes(tree_chunks(b, Hq, Hkv));
     REQUIRE(ws_bytes >= need, LUCE_ENOSPACE, "%s: workspace %zu bytes < %zu needed", who, ws_bytes, need);
     return cuda_status(launch_tree_attention(q, b, Hq, Hkv, scale, ws, out, scores, lds, stats, nullptr, nullptr,
                                              (cudaStream_t)stream),

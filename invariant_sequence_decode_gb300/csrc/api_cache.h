@@ -12,7 +12,7 @@ namespace luce {
 int tree_path(const int32_t* parent, int n_nodes, TreeRow* rows, int view, int row0, const char* who);
 
 // Cuts the views' prefixes into chunks; returns the rows of partial results.
-int64_t tree_chunks(TreeBatch& b, int Hq);
+int64_t tree_chunks(TreeBatch& b, int Hq, int Hkv);
 
 // A byte range that a call reads or writes.  Two that overlap are refused
 // unless both are read, or they are the same slot's input and output of one

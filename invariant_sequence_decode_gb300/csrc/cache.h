@@ -27,7 +27,7 @@ struct TreeView {
     int32_t len;
     int32_t n_nodes;
     int32_t row0;
-    int32_t chunk;    // keys of a chunk: tree_chunk_keys(len)
+    int32_t chunk;    // keys of a chunk: tree_chunk_keys(len, Hkv)
     int32_t n_chunk;  // chunks of the prefix
 };
 
@@ -46,12 +46,13 @@ struct TreeBatch {
     int32_t n_row;
 };
 
-// Keys of a chunk of a prefix of len keys: a function of len alone, so that
-// a row's sums are cut the same way whatever else is in the call.
-int tree_chunk_keys(int len);
+// Keys of a chunk of a prefix of len keys: a function of len and the model's KV
+// heads alone, so that a row's sums are cut the same way whatever else is in
+// the call.
+int tree_chunk_keys(int len, int Hkv);
 
 // The most chunks of a prefix of at most max_len keys.
-int tree_max_chunks(int max_len);
+int tree_max_chunks(int max_len, int Hkv);
 
 // Bytes of partial results of n_part rows (view chunks x KV heads x the rows
 // of a KV head).

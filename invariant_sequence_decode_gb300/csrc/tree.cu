@@ -5,7 +5,7 @@
 // prefix at len + node.  For row r of node j and query head h
 //   out = sum_i e^(s_i - m) v_i / l,  s_i = scale q.k_i,  m = max s_i,  l = sum e^(s_i - m).
 // The prefix, which every node of the tree sees, is cut into chunks of
-// tree_chunk_keys(len) keys; each chunk yields (m, l, sum e^(s - m) v) per row
+// tree_chunk_keys(len, Hkv) keys; each chunk yields (m, l, sum e^(s - m) v) per row
 // and the merge adds the chunks in order, then the node's own path, key by key
 // from the prefix down to the node.  A node's bits so follow from its prefix
 // and its path alone: the other branches of its tree, which lie between its
@@ -25,6 +25,8 @@
 // thread issues the products, and 256 threads (two to a row, 64 keys each)
 // turn S into P in place in tensor memory and add each tile's O into registers
 // with the running maximum's correction.
+#include <limits.h>
+
 #include <algorithm>
 #include <cmath>
 
@@ -35,21 +37,37 @@
 
 namespace luce {
 
-// Prefixes up to kTreeShort keys take 128-key chunks, up to kTreeMid 512, longer ones 1,024.
-constexpr int kTreeShort = 8192, kTreeMid = 32768;
+constexpr int kTreeTile = 128;  // keys of a tile, and rows of the products
+constexpr int kMaxTreeChunks = 160;
+constexpr int kTreeCtas = 152;  // the CTAs that a cut aims at: one per multiprocessor
 
-int tree_chunk_keys(int len) { return len <= kTreeShort ? 128 : (len <= kTreeMid ? 512 : 1024); }
-
-int tree_max_chunks(int max_len)
+// Tiles of a chunk for a prefix of nt tiles.  A chunk costs its tiles and about
+// one more (its q, its results); one view's chunks, Hkv heads, go to kTreeCtas
+// CTAs in rounds.  Of the cuts that fill 1, 2, 3 or 4 rounds the cheapest is
+// taken, the one with fewer chunks of equals: 130,800 keys of 8 heads make 19
+// chunks of 54 tiles (8-tile chunks, 128 a head: 117 against 93 us).
+static int tree_chunk_tiles(int nt, int Hkv)
 {
-    int most = 0;
-    for (int len : {std::min(max_len, kTreeShort), std::min(max_len, kTreeMid), max_len})
-        most = std::max(most, (len + tree_chunk_keys(len) - 1) / tree_chunk_keys(len));
-    return most;
+    int best = nt, least = INT_MAX;
+    for (int rounds = 1; rounds <= 4; ++rounds) {
+        const int n = std::min({kTreeCtas * rounds / Hkv, nt, kMaxTreeChunks});
+        if (n < 1) continue;
+        const int tiles = (nt + n - 1) / n;
+        const int cost = (Hkv * n + kTreeCtas - 1) / kTreeCtas * (tiles + 1);
+        if (cost < least) {
+            least = cost;
+            best = tiles;
+        }
+    }
+    return std::max(best, 1);
 }
 
-constexpr int kMaxTreeChunks = 128;
-constexpr int kTreeTile = 128;  // keys of a tile, and rows of the products
+int tree_chunk_keys(int len, int Hkv) { return kTreeTile * tree_chunk_tiles((len + kTreeTile - 1) / kTreeTile, Hkv); }
+
+int tree_max_chunks(int max_len, int Hkv)
+{
+    return std::min({(max_len + kTreeTile - 1) / kTreeTile, kMaxTreeChunks, std::max(1, 4 * kTreeCtas / Hkv)});
+}
 
 // A view chunk's partial results: part_o [row][128] and part_ml [row][4] = (m,
 // l of the keys 0..63 of its tiles, l of the keys 64..127, unused), with
@@ -66,8 +84,8 @@ __device__ __forceinline__ const __half* tree_key(const TreeView& v, const __hal
 
 // ---------------------------------------------------------------- chunks
 
-// 8 warps on S, P and O; a warpgroup of which one warp feeds the tiles, one
-// issues S, one P V.  384 threads get 168 registers each (64,512 in all);
+// 8 warps on S, P and O; a warpgroup of which one warp feeds the tiles and one
+// issues the products.  384 threads get 168 registers each (64,512 in all);
 // the second kind gives up to 40, the first then has 232: 256 * 232 + 128 * 40.
 constexpr int kTreeThreads = 384;
 constexpr int kTreeStages = 3;     // tiles of K in flight, and of V
@@ -118,20 +136,6 @@ __device__ __forceinline__ TreeUnit tree_unit(const TreeBatch& b, int Hkv, int u
     t.nkey = min(v.chunk, v.len - t.key0);
     t.tiles = (t.nkey + kTreeTile - 1) / kTreeTile;
     return t;
-}
-
-// The first chunk that begins at or behind tile `at` of all tiles.
-__device__ __forceinline__ int tree_first_unit(const TreeBatch& b, int Hkv, int at)
-{
-    int u = 0;
-    for (int i = 0; i < b.n_view; ++i) {
-        const TreeView& v = b.view[i];
-        const int nt = (v.len + kTreeTile - 1) / kTreeTile, ct = v.chunk / kTreeTile;
-        if (at < nt * Hkv) return u + at / nt * v.n_chunk + (at % nt + ct - 1) / ct;
-        at -= nt * Hkv;
-        u += Hkv * v.n_chunk;
-    }
-    return u;
 }
 
 __device__ __forceinline__ uint64_t tree_desc(uint32_t addr, uint32_t lbo, uint32_t sbo)
@@ -274,10 +278,10 @@ __device__ __forceinline__ void st_v8(float* p, const float* v)
 
 // The producer: K and V tiles of the CTA's chunks, in order.  Returns the
 // tiles issued.
-__device__ int tree_produce(const TreeMaps& maps, const TreeBatch& b, int Hkv, int u0, int u1, uint8_t* tiles, TreeBars& bar)
+__device__ int tree_produce(const TreeMaps& maps, const TreeBatch& b, int Hkv, int u0, int u1, int step, uint8_t* tiles, TreeBars& bar)
 {
     int i = 0;
-    for (int u = u0; u < u1; ++u) {
+    for (int u = u0; u < u1; u += step) {
         const TreeUnit t = tree_unit(b, Hkv, u);
         const TreeView& v = b.view[t.view];
         for (int k = 0; k < t.tiles; ++k, ++i) {
@@ -308,76 +312,106 @@ __device__ int tree_produce(const TreeMaps& maps, const TreeBatch& b, int Hkv, i
     return i;
 }
 
-// S = Q K^T of the CTA's tiles, issued by one warp; P V by another, so that
-// the tensor cores work on one tile's product while the other warp waits for
-// the next one's operands.  The issue loops stay loops: unrolled, their code
-// (4 KB each) fell out of the instruction cache at every chunk's end and cost
-// 8,000 cycles to fetch again.
-__device__ void tree_s(const TreeBatch& b, int Hkv, int u0, int u1, uint32_t tiles, uint32_t tmem, TreeBars& bar)
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity)
 {
-    // D f32, A and B f16, 128 x 128
-    constexpr uint32_t idesc = (1u << 4) | (16u << 17) | (8u << 24);
+    uint32_t done;
+    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(done)
+                 : "r"(smem_addr(bar)), "r"(parity)
+                 : "memory");
+    return done;
+}
+
+// The products, issued by one warp: S = Q K^T of the next tile as soon as its K
+// is there and its buffer free, else P V of the next tile whose P is there.
+// One warp for both, each product's 16 steps in one go: issued by a warp each
+// the steps of S and P V alternate on the tensor cores and both take twice
+// their time, with the softmax waiting for the one and the buffer for the other
+// (3,050 cycles a tile).  The issue loops stay loops: unrolled, their code (4 KB
+// each) fell out of the instruction cache at every chunk's end and cost 8,000
+// cycles to fetch again.  The warp sits in the scheduler of the last row quarter,
+// which has rows to work on in the widest calls only.
+__device__ void tree_products(const TreeBatch& b, int Hkv, int u0, int u1, int step, uint32_t tiles, uint32_t tmem,
+                              TreeBars& bar)
+{
+    // D f32, A and B f16, 128 x 128; P V's B (V) is N-major
+    constexpr uint32_t idesc_s = (1u << 4) | (16u << 17) | (8u << 24), idesc_o = idesc_s | (1u << 16);
     const uint32_t elected = elect_one();
-    unsigned int* late = &g_tree_wait_timeouts;
-    int i = 0, heads = 0, last = -1;
-    for (int u = u0; u < u1; ++u) {
-        const TreeUnit t = tree_unit(b, Hkv, u);
-        if (t.view * Hkv + t.g != last) {
-            last = t.view * Hkv + t.g;
-            if (!mbar_wait(&bar.q_full, heads++ & 1, late)) return;
-        }
-        for (int k = 0; k < t.tiles; ++k, ++i) {
+    int left = 0;  // tiles whose S is still to come
+    for (int u = u0; u < u1; u += step) left += tree_unit(b, Hkv, u).tiles;
+    int i = 0, j = 0, u = u0, k = 0, heads = 0, last = -1;
+    bool fresh = left > 0;  // the tile is its head's first: q is not there yet
+    TreeUnit t = left > 0 ? tree_unit(b, Hkv, u0) : TreeUnit{};
+    if (left > 0) last = t.view * Hkv + t.g;
+    uint64_t since = 0;
+    for (uint32_t polls = 0; left > 0 || j < i;) {
+        if (left > 0) {
             const int st = i % kTreeStages;
-            // (the first two buffers are free)
-            if (!mbar_wait(&bar.p_read[i & 1], ((i >> 1) & 1) ^ 1, late) ||
-                !mbar_wait(&bar.k_full[st], (i / kTreeStages) & 1, late))
+            const bool q_there = !fresh || mbar_test(&bar.q_full, heads & 1);
+            const bool free = mbar_test(&bar.p_read[i & 1], ((i >> 1) & 1) ^ 1);
+            const bool k_there = mbar_test(&bar.k_full[st], (i / kTreeStages) & 1);
+            if (__all_sync(0xffffffffu, q_there && free && k_there)) {
+                tm_after();
+                if (fresh) ++heads;
+                const uint32_t s = tmem + kColS + 128 * (i & 1);
+                const uint64_t d = tree_desc(tiles + st * kTreeTileBytes, 16, 1024);
+                // the low parts first: an accumulation loses digits by the
+                // sum's size, and theirs is small
+#pragma unroll 4
+                for (int ks = 0; ks < 16; ++ks)
+                    tree_mma(s, tmem + kColQ + 8 * (ks ^ 8), d + (ks >> 2 & 1) * (kTreeTileBytes / 32) + 2 * (ks & 3),
+                             idesc_s, ks > 0, elected);
+                tree_commit_mma(&bar.s_full[i & 1], elected);
+                tree_commit_mma(&bar.k_empty[st], elected);
+                ++i;
+                fresh = false;
+                if (++k == t.tiles && --left > 0) {
+                    k = 0;
+                    t = tree_unit(b, Hkv, u += step);
+                    fresh = t.view * Hkv + t.g != last;
+                    last = t.view * Hkv + t.g;
+                } else if (k < t.tiles) {
+                    --left;
+                }
+                polls = 0;
+            }
+        }
+        if (j < i) {
+            const int st = j % kTreeStages;
+            const bool p_there = mbar_test(&bar.p_full[j & 1], (j >> 1) & 1);
+            const bool free = j == 0 || mbar_test(&bar.o_free, (j - 1) & 1);
+            const bool v_there = mbar_test(&bar.v_full[st], (j / kTreeStages) & 1);
+            if (__all_sync(0xffffffffu, p_there && free && v_there)) {
+                tm_after();
+                const uint32_t p = tmem + kColS + 128 * (j & 1) + 32;
+                const uint64_t d = tree_desc(tiles + (kTreeStages + st) * kTreeTileBytes, kTreeTileBytes / 2, 1024);
+#pragma unroll 4
+                for (int ks = 0; ks < 16; ++ks)
+                    tree_mma(tmem + kColO, p + 64 * (ks >> 2 & 1) + 8 * (ks & 3) - 32 * (ks >> 3), d + 128 * (ks & 7),
+                             idesc_o, ks > 0, elected);
+                tree_commit_mma(&bar.o_full, elected);
+                tree_commit_mma(&bar.p_read[j & 1], elected);
+                tree_commit_mma(&bar.v_empty[st], elected);
+                ++j;
+                polls = 0;
+            }
+        }
+        // bounded: about a second without a product (or 2^26 polls) and the
+        // warp gives up; the clock is only looked at every 256 polls
+        if ((++polls & 255) == 0) {
+            if (polls == 256) since = global_ns();
+            if (__any_sync(0xffffffffu, global_ns() - since > kWaitLimitNs || polls >= (1u << 26))) {
+                if (elected) atomicAdd(&g_tree_wait_timeouts, 1u);
                 return;
-            tm_after();
-            const uint32_t s = tmem + kColS + 128 * (i & 1);
-            const uint64_t d = tree_desc(tiles + st * kTreeTileBytes, 16, 1024);
-            // the low parts first: an accumulation loses digits by the sum's
-            // size, and theirs is small
-#pragma unroll 1
-            for (int ks = 0; ks < 16; ++ks)
-                tree_mma(s, tmem + kColQ + 8 * (ks ^ 8), d + (ks >> 2 & 1) * (kTreeTileBytes / 32) + 2 * (ks & 3), idesc,
-                         ks > 0, elected);
-            tree_commit_mma(&bar.s_full[i & 1], elected);
-            tree_commit_mma(&bar.k_empty[st], elected);
+            }
         }
     }
 }
 
-__device__ void tree_pv(const TreeBatch& b, int Hkv, int u0, int u1, uint32_t tiles, uint32_t tmem, TreeBars& bar)
-{
-    constexpr uint32_t idesc = (1u << 4) | (1u << 16) | (16u << 17) | (8u << 24);  // B = V is N-major
-    const uint32_t elected = elect_one();
-    unsigned int* late = &g_tree_wait_timeouts;
-    int i = 0;
-    for (int u = u0; u < u1; ++u) {
-        const int n = tree_unit(b, Hkv, u).tiles;
-        for (int k = 0; k < n; ++k, ++i) {
-            const int st = i % kTreeStages;
-            if (!mbar_wait(&bar.v_full[st], (i / kTreeStages) & 1, late) ||
-                !mbar_wait(&bar.p_full[i & 1], (i >> 1) & 1, late) || (i > 0 && !mbar_wait(&bar.o_free, (i - 1) & 1, late)))
-                return;
-            tm_after();
-            const uint32_t p = tmem + kColS + 128 * (i & 1) + 32;
-            const uint64_t d = tree_desc(tiles + (kTreeStages + st) * kTreeTileBytes, kTreeTileBytes / 2, 1024);
-#pragma unroll 1
-            for (int ks = 0; ks < 16; ++ks)
-                tree_mma(tmem + kColO, p + 64 * (ks >> 2 & 1) + 8 * (ks & 3) - 32 * (ks >> 3), d + 128 * (ks & 7), idesc,
-                         ks > 0, elected);
-            tree_commit_mma(&bar.o_full, elected);
-            tree_commit_mma(&bar.p_read[i & 1], elected);
-            tree_commit_mma(&bar.v_empty[st], elected);
-        }
-    }
-}
-
-// One CTA an SM; CTA c takes the chunks that begin in its share of all tiles.
+// One CTA an SM, each with its share of all chunks.
 __global__ void __launch_bounds__(kTreeThreads, 1)
 tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* __restrict__ q, const __grid_constant__ TreeBatch b,
-                  int Hq, int Hkv, int all_tiles, TreeScale scale, float* __restrict__ part_o, float* __restrict__ part_ml,
+                  int Hq, int Hkv, int units, bool runs, TreeScale scale, float* __restrict__ part_o, float* __restrict__ part_ml,
                   float* __restrict__ scores, int64_t lds)
 {
     extern __shared__ uint8_t tree_smem[];
@@ -415,21 +449,29 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* __restrict
     __syncthreads();
     tm_after();
     const uint32_t tmem = tmem_at;
-    const int u0 = tree_first_unit(b, Hkv, (int)((int64_t)all_tiles * blockIdx.x / gridDim.x));
-    const int u1 = tree_first_unit(b, Hkv, (int)((int64_t)all_tiles * (blockIdx.x + 1) / gridDim.x));
+    if (tid < 2 * b.n_view) {
+        const CUtensorMap* m = tid < b.n_view ? &maps.k[tid] : &maps.v[tid - b.n_view];
+        asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+    }
+    // one-tile chunks: a run of them each (a run's heads change least); longer
+    // ones: every gridDim.x-th, as chunks of unlike views then spread evenly
+    int u0 = blockIdx.x, u1 = units, step = gridDim.x;
+    if (runs) {
+        u0 = (int)((int64_t)units * blockIdx.x / gridDim.x);
+        u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
+        step = 1;
+    }
     unsigned int* late = &g_tree_wait_timeouts;
     pdl_wait();
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 8 && lane == 0) {
-            asm volatile("fence.proxy.async;" ::: "memory");  // the step's own rows were written by plain stores
-            const int n = tree_produce(maps, b, Hkv, u0, u1, tiles, bar);
+            const int n = tree_produce(maps, b, Hkv, u0, u1, step, tiles, bar);
             ring_drain<kTreeStages>(bar.k_full, n, late);
             ring_drain<kTreeStages>(bar.v_full, n, late);
         }
-        if (warp == 9) tree_s(b, Hkv, u0, u1, smem_addr(tiles), tmem, bar);
-        if (warp == 10) tree_pv(b, Hkv, u0, u1, smem_addr(tiles), tmem, bar);
+        if (warp == 11) tree_products(b, Hkv, u0, u1, step, smem_addr(tiles), tmem, bar);
         __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
@@ -473,7 +515,7 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* __restrict
             }
             return done;
         };
-        for (int u = u0; !left && u < u1; ++u) {
+        for (int u = u0; !left && u < u1; u += step) {
             const TreeUnit t = tree_unit(b, Hkv, u);
             const TreeView& v = b.view[t.view];
             const size_t at_row = (size_t)(v.row0 + row / GQ) * Hq + t.g * GQ + row % GQ;
@@ -681,10 +723,11 @@ tree_merge_kernel(const float* __restrict__ q, const __grid_constant__ TreeBatch
         }
     }
     // every warp has all chunks' statistics: chunk lane + 32 j in its lane
-    float w[4], L = 0.0f, M = -INFINITY;
-    float2 ls[4];
+    constexpr int kStats = kMaxTreeChunks / 32;
+    float w[kStats], L = 0.0f, M = -INFINITY;
+    float2 ls[kStats];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kStats; ++j) {
         const int c = lane + 32 * j;
         w[j] = -INFINITY;
         ls[j] = make_float2(0.0f, 0.0f);
@@ -716,11 +759,11 @@ tree_merge_kernel(const float* __restrict__ q, const __grid_constant__ TreeBatch
     }
     float p = lane < np ? __fmul_rn(ps[lane], scale.log2) : -INFINITY;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) M = fmaxf(M, w[j]);
+    for (int j = 0; j < kStats; ++j) M = fmaxf(M, w[j]);
     M = warp_max(fmaxf(M, p));
     const float ref = M == -INFINITY ? 0.0f : M;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kStats; ++j) {
         w[j] = tree_exp2(__fsub_rn(w[j], ref));
         L = __fmaf_rn(__fadd_rn(ls[j].x, ls[j].y), w[j], L);
     }
@@ -728,7 +771,7 @@ tree_merge_kernel(const float* __restrict__ q, const __grid_constant__ TreeBatch
     L = __fadd_rn(warp_sum_butterfly(L), warp_sum_butterfly(p));
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {  // chunk 4 j + warp: its weight is in lane (4 j + warp) & 31's w[j >> 3]
+    for (int j = 0; j < kMaxTreeChunks / 4; ++j) {  // chunk 4 j + warp: its weight is in lane (4 j + warp) & 31's w[j >> 3]
         const int c = 4 * j + warp;
         if ((j & (kMergeAhead - 1)) == 0 && j > 0) {
             if (4 * j >= nch) break;
@@ -763,9 +806,11 @@ cudaError_t launch_tree_attention(const float* q, const TreeBatch& b, int Hq, in
                                   float* out, float* scores, int64_t lds, float* stats, int8_t* out_q, float* out_d,
                                   cudaStream_t s)
 {
-    int64_t tiles = 0, n_part = 0;
+    int64_t units = 0, n_part = 0;
+    bool runs = true;
     for (int i = 0; i < b.n_view; ++i) {
-        tiles += (int64_t)((b.view[i].len + kTreeTile - 1) / kTreeTile) * Hkv;
+        units += (int64_t)b.view[i].n_chunk * Hkv;
+        runs = runs && b.view[i].chunk == kTreeTile;
         n_part += (int64_t)b.view[i].n_chunk * b.view[i].n_nodes * Hq;
     }
     float* part_o = (float*)part;
@@ -774,7 +819,7 @@ cudaError_t launch_tree_attention(const float* q, const TreeBatch& b, int Hq, in
     const TreeScale sc = {scale < 0 ? -1.0f : 1.0f, std::fabs(scale),
                           std::max((float)(std::fabs((double)scale) * 1.4426950408889634), 1e-37f),
                           scale == 0 ? 0.0f : kLn2};
-    if (tiles > 0) {
+    if (units > 0) {
         TreeMaps maps{};
         if (!tree_maps(b, Hkv, &maps)) return cudaErrorInvalidValue;
         const int sms = sm_count();
@@ -782,8 +827,8 @@ cudaError_t launch_tree_attention(const float* q, const TreeBatch& b, int Hq, in
         static std::atomic<bool> done[kMaxDevices];
         cudaError_t e = set_smem_once(tree_chunk_kernel, kTreeSmem, done);
         if (e == cudaSuccess)
-            e = launch_pdl_smem(tree_chunk_kernel, dim3((unsigned)std::min<int64_t>(sms, tiles)), dim3(kTreeThreads),
-                                kTreeSmem, s, maps, q, b, Hq, Hkv, (int)tiles, sc, part_o, part_ml, scores, lds);
+            e = launch_pdl_smem(tree_chunk_kernel, dim3((unsigned)std::min<int64_t>(sms, units)), dim3(kTreeThreads),
+                                kTreeSmem, s, maps, q, b, Hq, Hkv, (int)units, runs, sc, part_o, part_ml, scores, lds);
         if (e != cudaSuccess) return e;
         count_launches(1);
     }

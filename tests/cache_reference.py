@@ -42,13 +42,14 @@ def tree_tolerance(q, k, v, length, n, scale, chunks):
     products (q in two f16 parts, together within 2^-22 of q) and one product
     with scale; e^x of a score off by d is off by a factor of 1 + d, once in the
     weight and once in their sum, plus 4 units of exp and its argument's (times
-    |x| <= 88: weights below e^-88 are nothing); sums run over at most 1,024
-    keys of a chunk, the chunks and the path."""
+    |x| <= 88: weights below e^-88 are nothing); a chunk's sums run over 128
+    keys of a tile and at most 1,024 tiles, the merge's over the chunks and the
+    path."""
     u = 2.0 ** -23
     a = np.abs(q.astype(np.float64)).max(axis=(0, 1))
     b = np.abs(np.nan_to_num(k[:, :length + n].astype(np.float64))).max(axis=(0, 1))
     ds = u * (256 + 4) * abs(scale) * float((a * b).sum())
-    rel = 2 * ds + u * (4 + 88 + min(length, 1024) + 2 * chunks + 2 * n + 8)
+    rel = 2 * ds + u * (4 + 88 + min(length, 128) + -(-length // 128) + 2 * chunks + 2 * n + 8)
     vmax = float(np.abs(np.nan_to_num(v[:, :length + n].astype(np.float64))).max())
     return ds, 2 * rel * vmax, rel * (length + n)
 

@@ -39,7 +39,7 @@ E, U, S = luce.LUCE_EINVAL, luce.LUCE_EUNSUPPORTED, luce.LUCE_ENOSPACE
     (E, dict(Hq=9)), (E, dict(Hkv=0)), (E, dict(Hq=0)), (U, dict(Hq=18)), (U, dict(D=64)),
     (E, dict(scale=float("nan"))), (E, dict(scale=float("inf"))),
     (E, dict(scores=P, lds=0)), (E, dict(scores=P, lds=14)), (E, dict(scores=P + 4, lds=16)), (E, dict(scores=P, lds=8)),
-    (E, dict(stats=P + 2)), (S, dict(ws_bytes=16)),
+    (E, dict(stats=P + 4)), (S, dict(ws_bytes=16)),
 ])
 def test_tree_attention_refuses_arguments(lib, want, kw):
     assert attn(lib, [view()], **kw) == want and lib.luce_last_error()
@@ -79,13 +79,14 @@ def test_paged_tree_attention_refusals(lib, want, kw):
 
 def test_tree_workspace_sizes(lib):
     size = lib.luce_tree_attn_workspace_size
-    assert size(0, 8, 128, 10) == size(17, 8, 128, 10) == size(1, 8, 64, 10) == size(1, 8, 128, 200000) == 0
-    assert size(1, 0, 128, 10) == size(1, 8, 128, -1) == 0
-    assert size(1, 8, 128, 0) >= 256
-    last = 0
-    for n in (1, 128, 129, 1000, 8192, 8193, 32768, 32769, 100000, 130816):
-        assert size(4, 40, 128, n) >= last  # a workspace for longer prefixes serves shorter ones
-        last = size(4, 40, 128, n)
+    assert size(0, 8, 2, 128, 10) == size(17, 8, 2, 128, 10) == size(1, 8, 2, 64, 10) == size(1, 8, 2, 128, 200000) == 0
+    assert size(1, 0, 1, 128, 10) == size(1, 8, 0, 128, 10) == size(1, 8, 3, 128, 10) == size(1, 18, 2, 128, 10) == 0
+    assert size(1, 8, 2, 128, -1) == 0 and size(1, 8, 2, 128, 0) >= 256
+    for hkv in (1, 2, 3, 8, 40, 200, 700):
+        last = 0
+        for n in (1, 128, 129, 1000, 8192, 8193, 32768, 32769, 100000, 130816):
+            assert size(4, 4 * hkv, hkv, 128, n) >= last  # a workspace for longer prefixes serves shorter ones
+            last = size(4, 4 * hkv, hkv, 128, n)
 
 
 def slot(k=P, v=P + BIG, length=10, cap=64, path=(0, 2), row0=0, acc=None, pos=None, pos0=10, n=None):

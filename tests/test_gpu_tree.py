@@ -109,7 +109,7 @@ def check(slots, out, sc, st, Hkv, fill=0.0):
     (8, 2, 0, "chain", 1), (8, 2, 0, "random", 9), (8, 2, 1, "star", 2), (4, 4, 2, "chain", 3), (40, 8, 127, "random", 16),
     (40, 8, 128, "random", 5), (8, 1, 129, "forest", 16), (7, 1, 255, "random", 7), (6, 2, 256, "chain", 4),
     (5, 1, 1000, "random", 13), (16, 2, 1001, "star", 16), (2, 2, 4097, "random", 3), (3, 1, 8191, "random", 11),
-    (8, 2, 8192, "chain", 2), (8, 2, 8193, "random", 16), (4, 2, 16500, "random", 6), (2, 1, 40003, "random", 4),
+    (70, 70, 300, "random", 3), (200, 200, 1300, "chain", 2), (8, 2, 8192, "chain", 2), (8, 2, 8193, "random", 16), (4, 2, 16500, "random", 6), (2, 1, 40003, "random", 4),
 ])
 def test_one_slot(Hq, Hkv, length, kind, n, paged):
     rng = np.random.default_rng(length * 31 + n)
@@ -307,7 +307,7 @@ def test_calls_behind_one_another_share_a_workspace():
     slots = [Slot(rng, 40, 8, L, tree_of("random", 8, L)) for L in (2051, 900)]
     views = [s.flat(0) for s in slots]
     want = [bits(luce.luce_tree_attn(cuda(s.q), [v], 8, SCALE)) for s, v in zip(slots, views)]
-    ws = torch.full((luce.luce_tree_attn_workspace_size(8, 40, 128, 2100),), 255, dtype=torch.uint8, device="cuda")
+    ws = torch.full((luce.luce_tree_attn_workspace_size(8, 40, 8, 128, 2100),), 255, dtype=torch.uint8, device="cuda")
     calls = [luce.TreeAttention(cuda(s.q), [v], 8, SCALE, ws=ws) for s, v in zip(slots, views)]
     for _ in range(20):
         for c in calls:
