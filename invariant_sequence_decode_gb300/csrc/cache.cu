@@ -122,7 +122,9 @@ cudaError_t launch_tree_commit(const CommitBatch& b, int n_layers, int Hq, int H
 // value, protected keys highest).  The n = len - budget lowest leave:
 //   1. a radix selection finds the n-th lowest rank T and how many keys equal
 //      to T leave: three passes over the slice (11, 11, 10 bits), each a
-//      histogram in shared memory that every CTA adds up over the cluster;
+//      histogram in shared memory; every CTA finds the digit by adding up over
+//      the cluster first the sums of 32 bins, then the 32 bins that matter
+//      (reading whole histograms of 8 CTAs took 4,000 cycles a pass);
 //   2. of the keys equal to T the first `stay` stay, counted through the
 //      cluster in index order;
 //   3. holes (index < budget, leaving) and comers (index >= budget, staying)
@@ -135,7 +137,8 @@ constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictBins = 2048;
 constexpr int kEvictSlice = 16352;  // most keys of a CTA: 8 CTAs hold 130,816
-constexpr int kEvictMove = 4;  // pairs of rows in flight per warp
+constexpr int kEvictMove = 8;   // pairs of rows in flight per warp
+constexpr int kEvictAhead = 8;  // keys in flight per thread
 
 __device__ __forceinline__ uint32_t evict_rank(float a, int pos, const EvictSlot& sl)
 {
@@ -155,7 +158,6 @@ __device__ __forceinline__ uint32_t cluster_rank()
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-// A word of CTA r's shared memory at this CTA's address p.
 __device__ __forceinline__ uint32_t far_addr(const void* p, int r)
 {
     uint32_t a;
@@ -168,13 +170,6 @@ __device__ __forceinline__ int far_ld(uint32_t a)
     asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
     return v;
 }
-__device__ __forceinline__ int4 far_ld4(uint32_t a)
-{
-    int4 v;
-    asm volatile("ld.shared::cluster.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-    return v;
-}
-
 // Exclusive prefix of v over the CTA's threads; *total the sum.
 __device__ __forceinline__ int block_prefix(int v, int* warp_sum, int* total)
 {
@@ -199,15 +194,36 @@ __device__ __forceinline__ int block_prefix(int v, int* warp_sum, int* total)
     return x - v + (warp ? before : 0);
 }
 
+// A word of CTA r's shared memory at this CTA's address p.
 template <int C>
-__global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kEvictThreads)
+__device__ __forceinline__ int evict_word(const int* p, int r)
+{
+    return C > 1 ? far_ld(far_addr(p, r)) : *p;
+}
+
+// Exclusive prefix of v over the warp.
+__device__ __forceinline__ int warp_prefix(int v)
+{
+    const int lane = threadIdx.x & 31;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    return x - v;
+}
+
+template <int C>
+__global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kEvictThreads, 2)
 kv_evict_kernel(const __grid_constant__ EvictBatch b, int slice)
 {
     extern __shared__ uint32_t evict_smem[];  // ranks [slice], then the lists [slice]
     __shared__ __align__(16) int hist[2][kEvictBins];
     __shared__ int warp_sum[kEvictWarps];
+    __shared__ int coarse[2][kEvictBins / 32];
     __shared__ int digit, below, equal;
-    __shared__ int n_eq, n_hole, n_come;  // this CTA's, for the cluster
+    __shared__ int n_hole, n_come;  // this CTA's, for the cluster
     pdl_trigger();
     const EvictSlot& sl = b.slot[blockIdx.y];
     const int64_t lh = blockIdx.x / C;
@@ -224,17 +240,29 @@ kv_evict_kernel(const __grid_constant__ EvictBatch b, int slice)
     for (int i = tid; i < 2 * kEvictBins; i += kEvictThreads) (&hist[0][0])[i] = 0;
     __syncthreads();
     pdl_wait();
-    for (int i = tid; i < nj; i += kEvictThreads) {
-        const int j = j0 + i;
-        const float a = acc[j];
-        const int p = pos[j];
-        if (j < sl.budget) {  // (holes are overwritten below)
-            if (acc_out != acc) acc_out[j] = a;
-            if (pos_out != pos) pos_out[j] = p;
+    for (int i0 = tid; i0 < nj; i0 += kEvictAhead * kEvictThreads) {
+        float a[kEvictAhead];
+        int p[kEvictAhead];
+#pragma unroll
+        for (int e = 0; e < kEvictAhead; ++e) {
+            const int i = i0 + e * kEvictThreads;
+            if (i < nj) {
+                a[e] = acc[j0 + i];
+                p[e] = pos[j0 + i];
+            }
         }
-        const uint32_t u = evict_rank(a, p, sl);
-        rank[i] = u;
-        if (n > 0) atomicAdd(&hist[0][u >> 21], 1);
+#pragma unroll
+        for (int e = 0; e < kEvictAhead; ++e) {
+            const int i = i0 + e * kEvictThreads, j = j0 + i;
+            if (i >= nj) break;
+            if (j < sl.budget) {  // (holes are overwritten below)
+                if (acc_out != acc) acc_out[j] = a[e];
+                if (pos_out != pos) pos_out[j] = p[e];
+            }
+            const uint32_t u = evict_rank(a[e], p[e], sl);
+            rank[i] = u;
+            if (n > 0) atomicAdd(&hist[0][u >> 21], 1);
+        }
     }
     if (n <= 0) return;  // (the whole cluster)
 
@@ -252,35 +280,41 @@ kv_evict_kernel(const __grid_constant__ EvictBatch b, int slice)
                 if (u >> (sh + width) == T >> (sh + width)) atomicAdd(&mine[(u >> sh) & ((1u << width) - 1)], 1);
             }
         }
+        __syncthreads();
+        // sums of 32 bins, for the cluster
+        {
+            const int4 c = reinterpret_cast<const int4*>(mine)[tid];
+            int v = c.x + c.y + c.z + c.w;
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            if ((lane & 7) == 0) coarse[pass & 1][tid >> 3] = v;
+        }
         if (C > 1) cluster_sync(); else __syncthreads();
-        // four bins a thread, over the cluster
-        int4 c = make_int4(0, 0, 0, 0);
-        if (C == 1) {
-            c = reinterpret_cast<const int4*>(mine)[tid];
-        } else {
+        if (warp == 0) {
+            // the 32 bins, then the bin, in which the n-th lowest falls
+            int c0 = 0, c1 = 0;
 #pragma unroll
             for (int r = 0; r < C; ++r) {
-                const int4 x = far_ld4(far_addr(mine + 4 * tid, r));
-                c.x += x.x;
-                c.y += x.y;
-                c.z += x.z;
-                c.w += x.w;
+                c0 += evict_word<C>(&coarse[pass & 1][2 * lane], r);
+                c1 += evict_word<C>(&coarse[pass & 1][2 * lane + 1], r);
             }
-        }
-        int all;
-        const int before = block_prefix(c.x + c.y + c.z + c.w, warp_sum, &all);
-        if (before < left && left <= before + c.x + c.y + c.z + c.w) {
-            int at = before, d = 0;
-            const int cs[4] = {c.x, c.y, c.z, c.w};
+            int at = warp_prefix(c0 + c1);
+            uint32_t in = __ballot_sync(0xffffffffu, at < left && left <= at + c0 + c1);
+            int src = __ffs(in) - 1;
+            const int second = at + c0 < left;
+            const int group = __shfl_sync(0xffffffffu, 2 * lane + second, src);
+            const int base = __shfl_sync(0xffffffffu, at + (second ? c0 : 0), src);
+            c0 = 0;
 #pragma unroll
-            for (int e = 0; e < 3; ++e)
-                if (d == e && at + cs[e] < left) {
-                    at += cs[e];
-                    ++d;
-                }
-            digit = 4 * tid + d;
-            below = at;
-            equal = cs[d];
+            for (int r = 0; r < C; ++r) c0 += evict_word<C>(&mine[32 * group + lane], r);
+            at = base + warp_prefix(c0);
+            in = __ballot_sync(0xffffffffu, at < left && left <= at + c0);
+            src = __ffs(in) - 1;
+            if (lane == src) {
+                digit = 32 * group + lane;
+                below = at;
+                equal = c0;
+            }
         }
         __syncthreads();
         T |= (uint32_t)digit << sh;
@@ -295,31 +329,29 @@ kv_evict_kernel(const __grid_constant__ EvictBatch b, int slice)
     }
     const int stay = same - left;  // the first keys equal to T, in index order
 
-    // 2. each thread's run of the slice: keys equal to T before it
-    const int run = (nj + kEvictThreads - 1) / kEvictThreads, r0 = min(tid * run, nj), r1 = min(r0 + run, nj);
-    int eq = 0;
-    for (int i = r0; i < r1; ++i) eq += rank[i] == T;
-    int all;
-    int eq_at = block_prefix(eq, warp_sum, &all);
-    if (C > 1) {
-        if (tid == 0) n_eq = all;
-        cluster_sync();
+    // 2. each thread's run of the slice: keys equal to T before it (those of
+    // the CTAs before this one are a bin of their last histogram)
+    // (runs of odd length: their words fall into different banks)
+    const int run = ((nj + kEvictThreads - 1) / kEvictThreads) | 1, r0 = min(tid * run, nj), r1 = min(r0 + run, nj);
+    int eq_far = 0;
 #pragma unroll
-        for (int r = 0; r < C; ++r)
-            if (r < me) eq_at += far_ld(far_addr(&n_eq, r));
-    }
+    for (int r = 0; r < C - 1; ++r)
+        if (r < me) eq_far += evict_word<C>(&hist[0][T & 1023], r);
+    int eq = 0, all;
+    for (int i = r0; i < r1; ++i) eq += rank[i] == T;
+    const int eq_at = eq_far + block_prefix(eq, warp_sum, &all);
 
     // 3. holes from the list's front, comers from its back
-    int holes = 0, comes = 0, e = eq_at;
+    int found = 0, e = eq_at;  // holes + 65536 comers, each at most kEvictSlice
     for (int i = r0; i < r1; ++i) {
         const uint32_t u = rank[i];
         const bool leaves = u < T || (u == T && e >= stay);
         e += u == T;
-        if (j0 + i < sl.budget) holes += leaves;
-        else comes += !leaves;
+        if (j0 + i < sl.budget) found += leaves;
+        else found += leaves ? 0 : 65536;
     }
-    int nh, nc;
-    int h_at = block_prefix(holes, warp_sum, &nh), c_at = block_prefix(comes, warp_sum, &nc);
+    const int found_at = block_prefix(found, warp_sum, &all);
+    int h_at = found_at & 65535, c_at = found_at >> 16;
     e = eq_at;
     for (int i = r0; i < r1; ++i) {
         const uint32_t u = rank[i];
@@ -332,17 +364,20 @@ kv_evict_kernel(const __grid_constant__ EvictBatch b, int slice)
         }
     }
     if (tid == 0) {
-        n_hole = nh;
-        n_come = nc;
+        n_hole = all & 65535;
+        n_come = all >> 16;
     }
     if (C > 1) cluster_sync(); else __syncthreads();
     int h_before[C], c_before[C], m = 0, mc = 0;
+    {
+        const int hs = lane < C ? evict_word<C>(&n_hole, lane) : 0, cs = lane < C ? evict_word<C>(&n_come, lane) : 0;
 #pragma unroll
-    for (int r = 0; r < C; ++r) {
-        h_before[r] = m;
-        c_before[r] = mc;
-        m += C > 1 ? far_ld(far_addr(&n_hole, r)) : n_hole;
-        mc += C > 1 ? far_ld(far_addr(&n_come, r)) : n_come;
+        for (int r = 0; r < C; ++r) {
+            h_before[r] = m;
+            c_before[r] = mc;
+            m += __shfl_sync(0xffffffffu, hs, r);
+            mc += __shfl_sync(0xffffffffu, cs, r);
+        }
     }
     const int64_t rows = lh * sl.cap * 16;
     uint4* base = reinterpret_cast<uint4*>(lane < 16 ? sl.k : sl.v) + rows + (lane & 15);
@@ -389,6 +424,123 @@ kv_evict_kernel(const __grid_constant__ EvictBatch b, int slice)
     if (C > 1) cluster_sync();  // the others still read this CTA's list
 }
 
+// Few keys leave (a step's new ones): one CTA per head keeps its keys' ranks in
+// registers and takes out the lowest, of equals the last, n times: a round is
+// a minimum over registers, warps and CTA, against the selection's three passes
+// over a histogram.  2,051 keys to 2,048 in 512 heads: 8.5 us, 16.6 through the selection.
+constexpr int kFewThreads = 256;
+constexpr int kFewWarps = kFewThreads / 32;
+constexpr int kFewKeys = 16;                                  // most that leave
+constexpr int kFewPer = 16, kFewMax = kFewPer * kFewThreads;  // longest cache
+
+__device__ __forceinline__ uint32_t redux_min(uint32_t x)
+{
+    uint32_t r;
+    asm volatile("redux.sync.min.u32 %0, %1, 0xffffffff;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t redux_max(uint32_t x)
+{
+    uint32_t r;
+    asm volatile("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+__global__ void __launch_bounds__(kFewThreads)
+kv_evict_few_kernel(const __grid_constant__ EvictBatch b)
+{
+    __shared__ uint32_t low[2][kFewWarps], at[2][kFewWarps];  // a round's lowest rank of each warp, and its last index
+    __shared__ int hole[kFewKeys], come[kFewKeys];
+    pdl_trigger();
+    const EvictSlot& sl = b.slot[blockIdx.y];
+    const int64_t lh = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const float* acc = sl.acc + lh * sl.cap;
+    const int32_t* pos = sl.pos + lh * sl.cap;
+    float* acc_out = sl.acc_out + lh * sl.cap;
+    int32_t* pos_out = sl.pos_out + lh * sl.cap;
+    const int n = sl.len - sl.budget;
+    uint32_t rank[kFewPer];
+    pdl_wait();
+    {
+        float a[kFewPer];
+        int p[kFewPer];
+#pragma unroll
+        for (int e = 0; e < kFewPer; ++e) {
+            const int j = tid + e * kFewThreads;
+            if (j < sl.len) {
+                a[e] = acc[j];
+                p[e] = pos[j];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < kFewPer; ++e) {
+            const int j = tid + e * kFewThreads;
+            rank[e] = 0xffffffffu;
+            if (j < sl.len) {
+                if (j < sl.budget) {
+                    if (acc_out != acc) acc_out[j] = a[e];
+                    if (pos_out != pos) pos_out[j] = p[e];
+                }
+                rank[e] = evict_rank(a[e], p[e], sl);
+            }
+        }
+    }
+    if (n <= 0) return;
+    uint32_t gone = 0;      // this thread's keys that left, a bit each
+    int left = 0x7fffffff;  // warp 0, lane r: the key that left in round r
+    for (int r = 0; r < n; ++r) {
+        uint32_t m = 0xffffffffu;
+        int mj = -1;
+#pragma unroll
+        for (int e = 0; e < kFewPer; ++e) {
+            const int j = tid + e * kFewThreads;
+            if (j < sl.len && !(gone >> e & 1) && rank[e] <= m) {  // (of equals the last)
+                m = rank[e];
+                mj = j;
+            }
+        }
+        const uint32_t wm = redux_min(mj < 0 ? 0xffffffffu : m);
+        const uint32_t wj = redux_max(mj >= 0 && m == wm ? (uint32_t)mj + 1 : 0u);  // 0: no key left
+        if (lane == 0) {
+            low[r & 1][warp] = wm;
+            at[r & 1][warp] = wj;
+        }
+        __syncthreads();
+        const uint32_t cm = lane < kFewWarps ? low[r & 1][lane] : 0xffffffffu, cj = lane < kFewWarps ? at[r & 1][lane] : 0u;
+        const uint32_t bm = redux_min(cj ? cm : 0xffffffffu);
+        const int bj = (int)redux_max(cj && cm == bm ? cj : 0u) - 1;
+        if (bj % kFewThreads == tid) gone |= 1u << (bj / kFewThreads);
+        if (warp == 0 && lane == r) left = bj;
+    }
+    // holes and comers in ascending order: each key's place is the number of
+    // its kind below it
+    if (warp == 0) {
+        bool stays = lane < n;  // key budget + lane
+        int below = 0;
+        for (int r = 0; r < n; ++r) {
+            const int j = __shfl_sync(0xffffffffu, left, r);
+            if (j == sl.budget + lane) stays = false;
+            if (j < left) ++below;
+        }
+        if (left < sl.budget) hole[below] = left;
+        const uint32_t mask = __ballot_sync(0xffffffffu, stays);
+        if (stays) come[__popc(mask & ((1u << lane) - 1))] = sl.budget + lane;
+        if (lane == 0) low[0][0] = __popc(mask);
+    }
+    __syncthreads();
+    const int m = (int)low[0][0];
+    uint4* base = reinterpret_cast<uint4*>(lane < 16 ? sl.k : sl.v) + lh * sl.cap * 16 + (lane & 15);
+    for (int i = warp; i < m; i += kFewWarps) {
+        const int to = hole[i], from = come[i];
+        base[(int64_t)to * 16] = base[(int64_t)from * 16];
+        if (lane == 0) {
+            acc_out[to] = acc[from];
+            pos_out[to] = pos[from];
+        }
+    }
+}
+
 template <int C>
 static cudaError_t launch_evict(const EvictBatch& b, int heads, int max_len, cudaStream_t s)
 {
@@ -407,8 +559,16 @@ cudaError_t launch_kv_evict(const EvictBatch& b, int n_layers, int Hkv, cudaStre
     int max_len = 0;
     for (int i = 0; i < b.n_slot; ++i) max_len = std::max(max_len, b.slot[i].len);
     const int heads = n_layers * Hkv;
+    int most = 0;
+    for (int i = 0; i < b.n_slot; ++i) most = std::max(most, b.slot[i].len - b.slot[i].budget);
+    if (most <= kFewKeys && max_len <= kFewMax) {
+        const cudaError_t e =
+            launch_pdl(kv_evict_few_kernel, dim3((unsigned)heads, b.n_slot), dim3(kFewThreads), s, b);
+        count_launches(1);
+        return e;
+    }
     int c = 1;
-    while (c < 8 && ((max_len + c - 1) / c > kEvictSlice || (max_len / c > 4096 && (int64_t)heads * b.n_slot * c < 304)))
+    while (c < 8 && ((max_len + c - 1) / c > kEvictSlice || (max_len / c > 4096 && (int64_t)heads * b.n_slot * c <= 152)))
         c *= 2;
     switch (c) {
         case 1: return launch_evict<1>(b, heads, max_len, s);
