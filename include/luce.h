@@ -580,6 +580,37 @@ int luce_tree_attn_paged(const float* q, const luce_pagedtreeview* views, int n_
 size_t luce_tree_attn_workspace_size(int n_rows, int Hq, int Hkv, int D, int max_len);
 
 /*
+ * A slot of a step over draft trees: its caches of every layer, its prefix and
+ * its tree (parent as in luce_treeview).
+ */
+typedef struct luce_tree_slot {
+    uint16_t* k;            /* (device) [n_layers][n_kv_heads][cap][head_dim], 16-byte aligned */
+    uint16_t* v;            /* (device) same layout */
+    int32_t len;            /* keys cached before this step */
+    int32_t cap;
+    int32_t pos0;           /* position of a node that follows the prefix: len, or more once keys were evicted */
+    int32_t n_nodes;        /* >= 1, LUCE_MAX_ROWS over all slots */
+    const int32_t* parent;  /* (host) [n_nodes] or NULL */
+} luce_tree_slot;
+
+/*
+ * luce_decode_step over draft trees (and over caches whose keys were evicted,
+ * whose length is not their next position): slot s owns n_nodes consecutive
+ * rows of x, in call order; node j is at position pos0 + the number of its
+ * ancestors, its K/V rows are written at cache position len + j in every
+ * layer, and it attends as in luce_tree_attn.  A node's outputs are the bits
+ * of a step over its own path alone.  scores and stats (each nullable) are
+ * luce_tree_attn's, a layer behind the other: fp32 [n_layers][T][Hq][lds] and
+ * [n_layers][T][Hq][2], as luce_tree_commit takes them.  Other arguments and
+ * errors as luce_decode_step; ws is sized by luce_decode_step_tree_layout with
+ * max_ctx >= every len (the same fields as luce_decode_step_layout).
+ */
+int luce_decode_step_tree(const luce_model* m, const luce_tree_slot* slots, int n_seq, float* x, float* logits,
+                          int32_t* argmax, float* scores, int64_t lds, float* stats, void* ws, size_t ws_bytes,
+                          void* stream);
+int luce_decode_step_tree_layout(const luce_model* m, int n_rows, int max_ctx, luce_step_layout* out);
+
+/*
  * A slot whose verified tree is committed: the accepted nodes path[0] <
  * path[1] < .. (a path from the prefix, so ascending) become the keys
  * len .. len + n_path - 1.

@@ -81,6 +81,11 @@ class PagedTreeViewC(ctypes.Structure):
                 ("row0", ctypes.c_int32), ("parent", ctypes.POINTER(ctypes.c_int32))]
 
 
+class TreeSlotC(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("len", ctypes.c_int32), ("cap", ctypes.c_int32),
+                ("pos0", ctypes.c_int32), ("n_nodes", ctypes.c_int32), ("parent", ctypes.POINTER(ctypes.c_int32))]
+
+
 class CommitSlotC(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("len", ctypes.c_int32), ("cap", ctypes.c_int32),
                 ("n_path", ctypes.c_int32), ("row0", ctypes.c_int32), ("path", ctypes.POINTER(ctypes.c_int32)),
@@ -110,7 +115,7 @@ EXPORTS = ("luce_last_error", "luce_version", "luce_launch_count", "luce_q8_quan
            "luce_test_wait_expiry", "luce_q8_matvec_batch_path", "luce_q8_quantize_act_f16", "luce_rmsnorm_q8",
            "luce_swiglu_q8", "luce_step_graph_create", "luce_step_graph_run", "luce_step_graph_stats",
            "luce_step_graph_destroy", "luce_tree_attn", "luce_tree_attn_paged", "luce_tree_attn_workspace_size",
-           "luce_tree_commit", "luce_kv_evict")
+           "luce_tree_commit", "luce_kv_evict", "luce_decode_step_tree", "luce_decode_step_tree_layout")
 
 _lib = None
 
@@ -167,6 +172,9 @@ def load_library(path: str = LIB_PATH):
                                          vp, sz, vp]
     lib.luce_tree_attn_workspace_size.argtypes = [i32, i32, i32, i32, i32]
     lib.luce_tree_attn_workspace_size.restype = sz
+    lib.luce_decode_step_tree.argtypes = [ctypes.POINTER(ModelC), ctypes.POINTER(TreeSlotC), i32, vp, vp, vp, vp, i64, vp,
+                                          vp, sz, vp]
+    lib.luce_decode_step_tree_layout.argtypes = [ctypes.POINTER(ModelC), i32, i32, ctypes.POINTER(StepLayoutC)]
     lib.luce_tree_commit.argtypes = [ctypes.POINTER(CommitSlotC), i32, i32, i32, i32, i32, vp, i32, i64, vp, vp]
     lib.luce_kv_evict.argtypes = [ctypes.POINTER(EvictSlotC), i32, i32, i32, i32, vp]
     for name in EXPORTS:
@@ -461,6 +469,16 @@ class Model:
         import torch
         return torch.empty(self.layout(n_rows, max_ctx)["total"], dtype=torch.uint8, device=device)
 
+    def tree_layout(self, n_rows: int, max_ctx: int) -> dict:
+        """The workspace layout of luce_decode_step_tree for prefixes of at most max_ctx keys."""
+        out = StepLayoutC()
+        _check(load_library().luce_decode_step_tree_layout(ctypes.byref(self.c), n_rows, max_ctx, ctypes.byref(out)))
+        return {n: getattr(out, n) for n in _LAYOUT_FIELDS}
+
+    def tree_workspace(self, n_rows: int, max_ctx: int, device="cuda"):
+        import torch
+        return torch.empty(self.tree_layout(n_rows, max_ctx)["total"], dtype=torch.uint8, device=device)
+
 
 @dataclass
 class Slot:
@@ -694,6 +712,18 @@ class PagedTreeView:
 
 
 @dataclass
+class TreeSlot:
+    """A slot of luce_decode_step_tree: its K/V cache for every layer (fp16
+    [n_layers][Hkv][cap][128]), ``len`` keys cached, ``pos0`` the position of a
+    node that follows them (default len), ``parent`` as in TreeView."""
+    k: object
+    v: object
+    len: int
+    parent: object = 1
+    pos0: Optional[int] = None
+
+
+@dataclass
 class CommitSlot:
     """A slot's cache of every layer (fp16 [n_layers][Hkv][cap][128]) whose tree's
     nodes ``path`` (ascending) were accepted; ``row0`` is the score row of node
@@ -908,6 +938,45 @@ def luce_tree_attn_paged(q, views: Sequence[PagedTreeView], n_kv_heads: int, sca
                          stats=None, ws=None, stream=None):
     """luce_tree_attn over paged caches (the same bits as a flat cache)."""
     return TreeAttention(q, views, n_kv_heads, scale, out, scores, stats, ws, stream)()
+
+
+def luce_decode_step_tree(model: "Model", slots: Sequence[TreeSlot], x, ws, logits=None, argmax=None, scores=None,
+                          stats=None, stream=None):
+    """One batched decode step over the slots' draft trees (luce_decode_step for
+    rows that are nodes of trees, or whose caches had keys evicted).  x: fp32
+    [T][hidden] in/out, a slot's nodes in consecutive rows; scores
+    [n_layers][T][Hq][lds] and stats [n_layers][T][Hq][2] are what
+    luce_tree_commit takes."""
+    import torch
+    _need(x, torch.float32, "x")
+    n, T = len(slots), x.shape[0]
+    sc, trees = (TreeSlotC * max(1, n))(), [_tree(s.parent) for s in slots]
+    if sum(t[0] for t in trees) != T:
+        raise ValueError(f"x has {T} rows, the trees {sum(t[0] for t in trees)}")
+    for i, (s, (nn, par)) in enumerate(zip(slots, trees)):
+        _kv_pair(s.k, s.v, 4, f"slots[{i}]")
+        _need(s.k, torch.float16, f"slots[{i}].k")
+        _need(s.v, torch.float16, f"slots[{i}].v")
+        if s.k.shape[:2] != (len(model.layers), model.n_kv_heads):
+            raise ValueError(f"slots[{i}]: expected caches [n_layers][n_kv_heads][cap][128] of the model")
+        _same_device(x, s.k, s.v)
+        sc[i] = TreeSlotC(s.k.data_ptr(), s.v.data_ptr(), s.len, s.k.shape[2], s.len if s.pos0 is None else s.pos0, nn, par)
+    lds = 0
+    if scores is not None:
+        _need(scores, torch.float32, "scores")
+        lds = scores.shape[-1]
+        if scores.numel() != len(model.layers) * T * model.n_q_heads * lds:
+            raise ValueError("scores: expected [n_layers][T][Hq][lds]")
+    if stats is not None:
+        _need(stats, torch.float32, "stats")
+        if stats.numel() != len(model.layers) * T * model.n_q_heads * 2:
+            raise ValueError("stats: expected [n_layers][T][Hq][2]")
+    _same_device(x, ws, logits, argmax, scores, stats)
+    with torch.cuda.device(x.device):
+        _check(load_library().luce_decode_step_tree(ctypes.byref(model.c), sc, n, x.data_ptr(), _ptr(logits), _ptr(argmax),
+                                                    _ptr(scores), lds, _ptr(stats), ws.data_ptr(), ws.numel(),
+                                                    _stream(stream)))
+    return x
 
 
 def _state(t, dtype, like, name):

@@ -15,6 +15,8 @@
 
 #include "../../include/luce.h"
 #include "api.h"
+#include "api_cache.h"
+#include "cache.h"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -457,7 +459,8 @@ static int check_model(const luce_model* m, const char* who)
     return LUCE_OK;
 }
 
-static void layout_of(const luce_model* m, int T, int max_ctx, luce_step_layout* L)
+// part_bytes: the attention's scratch.
+static void layout_of(const luce_model* m, int T, size_t part_bytes, luce_step_layout* L)
 {
     const size_t H = m->hidden, Hq = m->n_q_heads, Hkv = m->n_kv_heads, D = m->head_dim, F = m->ffn;
     size_t o = 0;
@@ -487,8 +490,19 @@ static void layout_of(const luce_model* m, int T, int max_ctx, luce_step_layout*
     L->xf_d = take(T * H / 32 * 4);
     // The split-K scratch comes last so that the offsets above do not depend
     // on the context bound.
-    L->part = take(attn_part_floats(T * max_chunks_upto(std::max(max_ctx, 1)), (int)Hq) * 4);
+    L->part = take(part_bytes);
     L->total = o;
+}
+
+static size_t step_part_bytes(const luce_model* m, int T, int max_ctx)
+{
+    return attn_part_floats(T * max_chunks_upto(std::max(max_ctx, 1)), m->n_q_heads) * 4;
+}
+
+// The scratch of a step over draft trees, whose prefixes hold at most max_ctx keys.
+static size_t tree_step_part_bytes(const luce_model* m, int T, int max_ctx)
+{
+    return tree_part_bytes((int64_t)tree_max_chunks(max_ctx, m->n_kv_heads) * T * m->n_q_heads);
 }
 
 int luce_decode_step_layout(const luce_model* m, int n_rows, int max_ctx, luce_step_layout* out)
@@ -499,7 +513,21 @@ int luce_decode_step_layout(const luce_model* m, int n_rows, int max_ctx, luce_s
     REQUIRE(n_rows >= 1 && n_rows <= LUCE_MAX_ROWS, LUCE_EINVAL, "decode_step_layout: n_rows=%d outside 1..%d",
             n_rows, LUCE_MAX_ROWS);
     REQUIRE(max_ctx >= 1, LUCE_EINVAL, "decode_step_layout: max_ctx=%d", max_ctx);
-    layout_of(m, n_rows, max_ctx, out);
+    layout_of(m, n_rows, step_part_bytes(m, n_rows, max_ctx), out);
+    return ok();
+}
+
+int luce_decode_step_tree_layout(const luce_model* m, int n_rows, int max_ctx, luce_step_layout* out)
+{
+    const char* who = "decode_step_tree_layout";
+    int rc = check_model(m, who);
+    if (rc) return rc;
+    REQUIRE(out, LUCE_EINVAL, "%s: null out", who);
+    REQUIRE(n_rows >= 1 && n_rows <= LUCE_MAX_ROWS, LUCE_EINVAL, "%s: n_rows=%d outside 1..%d", who, n_rows,
+            LUCE_MAX_ROWS);
+    REQUIRE(max_ctx >= 0 && max_ctx <= LUCE_MAX_KEYS, LUCE_EINVAL, "%s: max_ctx=%d outside 0..%d", who, max_ctx,
+            LUCE_MAX_KEYS);
+    layout_of(m, n_rows, tree_step_part_bytes(m, n_rows, max_ctx), out);
     return ok();
 }
 
@@ -582,12 +610,22 @@ static void resolve_outputs(HostIO* io, int T, int H)
     io->outputs_resolved = true;
 }
 
+// The draft trees of luce_decode_step_tree: the rows' paths, the positions of
+// nodes that follow the prefix, where each layer's scores and statistics go.
+struct StepTree {
+    TreeBatch batch;
+    int pos0[LUCE_MAX_SEQ];
+    float* scores;
+    int64_t lds;
+    float* stats;
+};
+
 // The step's own argument checks (the slots are checked by the callers):
 // buffers, weights, row count and workspace size.  On success *L is the
 // workspace layout and *T the row count.
 static int check_step(const luce_model* m, const StepSlot* slots, const int32_t* rows_per_slot, int n_seq, float* x,
                       float* logits, int32_t* argmax, void* ws, size_t ws_bytes, const char* who, const HostIO& io,
-                      luce_step_layout* L, int* T_out)
+                      const StepTree* tree, luce_step_layout* L, int* T_out)
 {
     REQUIRE(x && ws, LUCE_EINVAL, "%s: null x/ws", who);
     REQUIRE(aligned(x, 16) && aligned(ws, 256), LUCE_EINVAL, "%s: x must be 16-byte and ws 256-byte aligned", who);
@@ -595,10 +633,10 @@ static int check_step(const luce_model* m, const StepSlot* slots, const int32_t*
             "%s: logits/argmax need vocab > 0 and the head weights", who);
     REQUIRE(!argmax || logits, LUCE_EINVAL, "%s: argmax needs the logits buffer", who);
     REQUIRE(!io.argmax_out || argmax, LUCE_EINVAL, "%s: argmax_out needs the argmax buffer", who);
-    int T = 0, max_len = 1;
+    int T = 0, max_len = tree ? 0 : 1;  // (a tree's own keys are not in its prefix)
     for (int s = 0; s < n_seq; ++s) {
         T += rows_per_slot[s];
-        max_len = std::max(max_len, slots[s].len + rows_per_slot[s]);
+        max_len = std::max(max_len, slots[s].len + (tree ? 0 : rows_per_slot[s]));
     }
     REQUIRE(T <= LUCE_MAX_ROWS, LUCE_EINVAL, "%s: %d rows > %d", who, T, LUCE_MAX_ROWS);
     for (int l = 0; l < m->n_layers; ++l) {
@@ -611,7 +649,7 @@ static int check_step(const luce_model* m, const StepSlot* slots, const int32_t*
     }
     REQUIRE(!logits || aligned(m->head_q, 32), LUCE_EINVAL, "%s: head weights must be 32-byte aligned", who);
 
-    layout_of(m, T, max_len, L);
+    layout_of(m, T, tree ? tree_step_part_bytes(m, T, max_len) : step_part_bytes(m, T, max_len), L);
     REQUIRE(ws_bytes >= L->total, LUCE_ENOSPACE, "%s: workspace %zu bytes < %zu needed", who, ws_bytes, L->total);
     *T_out = T;
     return LUCE_OK;
@@ -619,11 +657,12 @@ static int check_step(const luce_model* m, const StepSlot* slots, const int32_t*
 
 static int decode_step_impl(const luce_model* m, const StepSlot* slots, const int32_t* rows_per_slot, int n_seq,
                             float* x, float* logits, int32_t* argmax, void* ws, size_t ws_bytes, void* stream,
-                            const char* who, const HostIO& io = HostIO{nullptr, nullptr, nullptr})
+                            const char* who, const HostIO& io = HostIO{nullptr, nullptr, nullptr},
+                            const StepTree* tree = nullptr)
 {
     luce_step_layout L;
     int T = 0;
-    const int rc = check_step(m, slots, rows_per_slot, n_seq, x, logits, argmax, ws, ws_bytes, who, io, &L, &T);
+    const int rc = check_step(m, slots, rows_per_slot, n_seq, x, logits, argmax, ws, ws_bytes, who, io, tree, &L, &T);
     if (rc) return rc;
     const int H = m->hidden, Hq = m->n_q_heads, Hkv = m->n_kv_heads, D = m->head_dim, F = m->ffn;
 
@@ -650,15 +689,18 @@ static int decode_step_impl(const luce_model* m, const StepSlot* slots, const in
     // Row bookkeeping (host): positions, K/V destinations, attention rows.
     RowPos pos{};
     pos.n_rows = T;
-    int slot_of[LUCE_MAX_ROWS];
+    int slot_of[LUCE_MAX_ROWS], key_of[LUCE_MAX_ROWS];
     {
         int r = 0;
         for (int s = 0; s < n_seq; ++s)
             for (int j = 0; j < rows_per_slot[s]; ++j, ++r) {
                 slot_of[r] = s;
-                pos.pos[r] = slots[s].len + j;
+                key_of[r] = slots[s].len + j;
+                pos.pos[r] = tree ? tree->pos0[s] + tree->batch.row[r].n_path - 1 : key_of[r];
             }
     }
+    TreeBatch tb;
+    if (tree) tb = tree->batch;
     // the 64 inverse frequencies of the model's theta, formed once per thread and theta
     thread_local double freq_theta = -1.0;
     thread_local RopeFreq freq;
@@ -684,7 +726,7 @@ static int decode_step_impl(const luce_model* m, const StepSlot* slots, const in
         kv.n_rows = ar.n_rows = T;
         for (int r = 0; r < T; ++r) {
             const StepSlot& sl = slots[slot_of[r]];
-            const int p = pos.pos[r];
+            const int p = key_of[r];
             if (sl.table) {
                 const int64_t at = (int64_t)sl.table_host[p / kPageKeys] * page_stride + (int64_t)l * page_elems +
                                    (int64_t)(p % kPageKeys) * D;
@@ -728,9 +770,20 @@ static int decode_step_impl(const luce_model* m, const StepSlot* slots, const in
         if ((e = launch_qkv_rope(w.wqkv_q, (const __half*)w.wqkv_d, H, xn_q, xn_d, T, qkv, Hq, Hkv, pos, freq, q_rot,
                                  kv, st)))
             break;
-        if ((e = launch_attention(q_rot, (int64_t)Hq * D, ar, Hq, Hkv, scale, part, attn, (int64_t)Hq * D,
-                                  attn_q, attn_d, st)))
-            break;
+        if (tree) {
+            const int64_t at = (int64_t)l * T * Hq;
+            for (int s = 0; s < n_seq; ++s) {
+                tb.view[s].k = slots[s].k + (int64_t)l * Hkv * tb.view[s].head_stride;
+                tb.view[s].v = slots[s].v + (int64_t)l * Hkv * tb.view[s].head_stride;
+            }
+            e = launch_tree_attention(q_rot, tb, Hq, Hkv, scale, part, attn,
+                                      tree->scores ? tree->scores + at * tree->lds : nullptr, tree->lds,
+                                      tree->stats ? tree->stats + 2 * at : nullptr, attn_q, attn_d, st);
+        } else {
+            e = launch_attention(q_rot, (int64_t)Hq * D, ar, Hq, Hkv, scale, part, attn, (int64_t)Hq * D, attn_q, attn_d,
+                                 st);
+        }
+        if (e) break;
         if ((e = launch_matvec(w.wo_q, (const __half*)w.wo_d, H, Hq * D, attn_q, attn_d, T, x1, H, x, H, st)))
             break;
         if ((e = launch_rmsnorm_quant(x1, T, H, w.ffn_norm, m->rms_eps, xn2, xn2_q, xn2_d, false, st))) break;
@@ -835,6 +888,73 @@ int luce_decode_step(const luce_model* m, const luce_slot* slots, const int32_t*
     const int rc = flat_slots(m, slots, rows_per_slot, n_seq, ss, who);
     if (rc) return rc;
     return decode_step_impl(m, ss, rows_per_slot, n_seq, x, logits, argmax, ws, ws_bytes, stream, who);
+}
+
+int luce_decode_step_tree(const luce_model* m, const luce_tree_slot* slots, int n_seq, float* x, float* logits,
+                          int32_t* argmax, float* scores, int64_t lds, float* stats, void* ws, size_t ws_bytes,
+                          void* stream)
+{
+    const char* who = "decode_step_tree";
+    int rc = check_model(m, who);
+    if (rc) return rc;
+    REQUIRE(slots, LUCE_EINVAL, "%s: null slots", who);
+    REQUIRE(n_seq >= 1 && n_seq <= LUCE_MAX_SEQ, LUCE_EINVAL,
+            "%s: n_seq=%d outside 1..%d (more than %d slots are refused)", who, n_seq, LUCE_MAX_SEQ, LUCE_MAX_SEQ);
+    REQUIRE(m->n_kv_heads <= 4096, LUCE_EUNSUPPORTED, "%s: %d KV heads > 4096", who, m->n_kv_heads);
+    REQUIRE(!scores || (aligned(scores, 16) && lds >= 1 && lds % 4 == 0 && lds < ((int64_t)1 << 31)), LUCE_EINVAL,
+            "%s: scores must be 16-byte aligned and lds=%lld a positive multiple of 4", who, (long long)lds);
+    REQUIRE(aligned(stats, 8), LUCE_EINVAL, "%s: stats must be 8-byte aligned", who);
+    StepSlot ss[LUCE_MAX_SEQ];
+    StepTree tree{};
+    int32_t rows[LUCE_MAX_SEQ];
+    ByteRange r[2 * LUCE_MAX_SEQ + 2];
+    const int64_t heads = (int64_t)m->n_layers * m->n_kv_heads;
+    int T = 0;
+    for (int s = 0; s < n_seq; ++s) {
+        const luce_tree_slot& sl = slots[s];
+        REQUIRE(sl.k && sl.v && aligned(sl.k, 16) && aligned(sl.v, 16), LUCE_EINVAL,
+                "%s: slot %d cache null or not 16-byte aligned", who, s);
+        REQUIRE(sl.n_nodes >= 1 && sl.n_nodes <= LUCE_MAX_TREE - T, LUCE_EINVAL,
+                "%s: slot %d has %d nodes (at least 1, %d in all)", who, s, sl.n_nodes, LUCE_MAX_ROWS);
+        REQUIRE(sl.len >= 0 && sl.cap >= 1 && (int64_t)sl.len + sl.n_nodes <= sl.cap, LUCE_EINVAL,
+                "%s: slot %d len=%d + nodes=%d exceeds cap=%d", who, s, sl.len, sl.n_nodes, sl.cap);
+        REQUIRE(sl.len <= kMaxKeys - sl.n_nodes, LUCE_EUNSUPPORTED, "%s: slot %d would hold %d keys (at most %d)", who, s,
+                sl.len + sl.n_nodes, kMaxKeys);
+        REQUIRE(sl.pos0 >= 0 && sl.pos0 <= INT32_MAX - LUCE_MAX_TREE, LUCE_EINVAL, "%s: slot %d pos0=%d", who, s, sl.pos0);
+        REQUIRE(!scores || lds >= sl.len + sl.n_nodes, LUCE_EINVAL, "%s: lds=%lld < the %d keys of slot %d", who,
+                (long long)lds, sl.len + sl.n_nodes, s);
+        if ((rc = tree_path(sl.parent, sl.n_nodes, tree.batch.row, s, T, who))) return rc;
+        TreeView& v = tree.batch.view[s];
+        v.tok_stride = LUCE_HEAD_DIM;
+        v.head_stride = (int64_t)sl.cap * LUCE_HEAD_DIM;
+        v.page_stride = v.head_stride * m->n_kv_heads;
+        v.n_pages = 1;
+        v.cap = sl.cap;
+        v.len = sl.len;
+        v.n_nodes = sl.n_nodes;
+        v.row0 = T;
+        ss[s] = StepSlot{reinterpret_cast<__half*>(sl.k), reinterpret_cast<__half*>(sl.v), sl.len, sl.cap, nullptr,
+                         nullptr};
+        tree.pos0[s] = sl.pos0;
+        rows[s] = sl.n_nodes;
+        T += sl.n_nodes;
+        const uintptr_t bytes = (uintptr_t)(heads * sl.cap * LUCE_HEAD_DIM * 2);
+        r[2 * s] = ByteRange{(uintptr_t)sl.k, (uintptr_t)sl.k + bytes, s, "K cache", true, 0};
+        r[2 * s + 1] = ByteRange{(uintptr_t)sl.v, (uintptr_t)sl.v + bytes, s, "V cache", true, 0};
+    }
+    int nr = 2 * n_seq;
+    const uintptr_t out_rows = (uintptr_t)m->n_layers * T * m->n_q_heads;
+    if (scores) r[nr++] = ByteRange{(uintptr_t)scores, (uintptr_t)scores + out_rows * lds * 4, -1, "scores", true, 0};
+    if (stats) r[nr++] = ByteRange{(uintptr_t)stats, (uintptr_t)stats + out_rows * 8, -1, "stats", true, 0};
+    if ((rc = check_apart(r, nr, who))) return rc;
+    tree.batch.n_view = n_seq;
+    tree.batch.n_row = T;
+    tree_chunks(tree.batch, m->n_q_heads, m->n_kv_heads);
+    tree.scores = scores;
+    tree.lds = lds;
+    tree.stats = stats;
+    return decode_step_impl(m, ss, rows, n_seq, x, logits, argmax, ws, ws_bytes, stream, who,
+                            HostIO{nullptr, nullptr, nullptr}, &tree);
 }
 
 int luce_decode_step_host(const luce_model* m, const luce_slot* slots, const int32_t* rows_per_slot, int n_seq,
@@ -1031,7 +1151,7 @@ int luce_step_graph_create(const luce_model* m, const luce_slot* slots, const in
     luce_step_layout L;
     int T = 0;
     if ((rc = check_step(m, ss, rows_per_slot, n_seq, x, logits, argmax, ws, ws_bytes, who,
-                         HostIO{x_in, x_out, argmax_out}, &L, &T)))
+                         HostIO{x_in, x_out, argmax_out}, nullptr, &L, &T)))
         return rc;
     luce_step_graph* g = new (std::nothrow) luce_step_graph();
     REQUIRE(g, LUCE_ENOSPACE, "%s: out of host memory", who);

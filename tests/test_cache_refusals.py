@@ -156,3 +156,45 @@ def test_evict_within_budget_in_place_enqueues_nothing(lib):
     assert evict(lib, [eslot(budget=20), eslot(P + 6 * BIG, P + 7 * BIG, P + 8 * BIG, P + 9 * BIG, P + 8 * BIG, P + 9 * BIG,
                                                length=0)]) == luce.LUCE_OK
     assert luce.launch_count() == before
+
+
+def model(n_layers=2, vocab=0, hq=4, hkv=2):
+    layers = (luce.LayerC * n_layers)(*[luce.LayerC(*([P] * 10)) for _ in range(n_layers)])
+    m = luce.ModelC(n_layers, 256, hq, hkv, 128, 512, vocab, 1e-6, 1e6, layers, P, P, P)
+    return m
+
+
+def tslot(k=P, v=P + BIG, length=10, cap=64, pos0=10, nodes=2, parent=None):
+    return luce.TreeSlotC(k, v, length, cap, pos0, nodes, None if parent is None else ints(parent))
+
+
+def step(lib, slots, m=None, x=P, logits=None, argmax=None, scores=None, lds=0, stats=None, ws=0x100000, ws_bytes=1 << 40, n=None):
+    arr = (luce.TreeSlotC * max(1, len(slots)))(*slots)
+    return lib.luce_decode_step_tree(ctypes.byref(m or model()), arr, len(slots) if n is None else n, x, logits, argmax,
+                                     scores, lds, stats, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("want,slots,kw", [
+    (E, [], {}), (E, [tslot()] * 5, {}), (E, [tslot(k=0)], {}), (E, [tslot(v=P + BIG + 8)], {}), (E, [tslot(nodes=0)], {}),
+    (E, [tslot(nodes=17)], {}), (E, [tslot(nodes=9), tslot(P + 2 * BIG, P + 3 * BIG, nodes=8)], {}), (E, [tslot(length=63)], {}),
+    (E, [tslot(length=-1)], {}), (U, [tslot(length=130815, cap=1 << 20)], {}), (E, [tslot(pos0=-1)], {}),
+    (E, [tslot(pos0=2 ** 31 - 1)], {}), (E, [tslot(parent=[0, 0])], {}), (E, [tslot(parent=[-1, 1])], {}),
+    (E, [tslot(), tslot()], {}), (E, [tslot(v=P)], {}), (E, [tslot()], dict(scores=SC, lds=10)),
+    (E, [tslot()], dict(scores=SC, lds=8)), (E, [tslot()], dict(scores=SC + 8, lds=12)), (E, [tslot()], dict(stats=ST + 4)),
+    (E, [tslot()], dict(scores=P, lds=12)), (E, [tslot()], dict(x=0)), (E, [tslot()], dict(ws=0)), (E, [tslot()], dict(logits=P)),
+    (S, [tslot()], dict(ws_bytes=1024)),
+])
+def test_tree_step_refusals(lib, want, slots, kw):
+    assert step(lib, slots, **kw) == want and lib.luce_last_error()
+
+
+def test_tree_step_layout(lib):
+    m, a, b = model(), luce.StepLayoutC(), luce.StepLayoutC()
+    assert lib.luce_decode_step_tree_layout(ctypes.byref(m), 0, 10, ctypes.byref(a)) == E
+    assert lib.luce_decode_step_tree_layout(ctypes.byref(m), 17, 10, ctypes.byref(a)) == E
+    assert lib.luce_decode_step_tree_layout(ctypes.byref(m), 4, -1, ctypes.byref(a)) == E
+    assert lib.luce_decode_step_tree_layout(ctypes.byref(m), 4, 130817, ctypes.byref(a)) == E
+    assert lib.luce_decode_step_tree_layout(ctypes.byref(m), 4, 10, None) == E
+    assert lib.luce_decode_step_tree_layout(ctypes.byref(m), 4, 1000, ctypes.byref(a)) == luce.LUCE_OK
+    assert lib.luce_decode_step_layout(ctypes.byref(m), 4, 1000, ctypes.byref(b)) == luce.LUCE_OK
+    assert all(getattr(a, f) == getattr(b, f) for f in luce._LAYOUT_FIELDS if f != "total")
