@@ -284,6 +284,10 @@ __device__ int tree_produce(const TreeMaps& maps, const TreeBatch& b, int Hkv, i
     for (int u = u0; u < u1; u += step) {
         const TreeUnit t = tree_unit(b, Hkv, u);
         const TreeView& v = b.view[t.view];
+        if (u == u0) {
+            pdl_wait();
+            pdl_trigger();
+        }
         for (int k = 0; k < t.tiles; ++k, ++i) {
             const int st = i % kTreeStages;
             const uint32_t free = ((i / kTreeStages) & 1) ^ 1;
@@ -421,7 +425,6 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* __restrict
     __shared__ float mx[2][2][kTreeTile];  // a row's maxima of a tile's two halves, by tile parity
     __shared__ volatile int bail[4];       // a wait of the row quarter's warps expired
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    pdl_trigger();
     if (warp == 9) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_at)),
                      "r"(512u));
@@ -462,8 +465,10 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* __restrict
         step = 1;
     }
     unsigned int* late = &g_tree_wait_timeouts;
-    pdl_wait();
 
+    // Each role waits for the kernels before this one right before it first
+    // needs what they wrote.  The producer's thread then lets the merge start:
+    // by then everything but this kernel's results is in place for it.
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 8 && lane == 0) {
@@ -522,6 +527,7 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* __restrict
             if (t.view * Hkv + t.g != last) {  // (S of every tile of the last head is complete: its q is free)
                 last = t.view * Hkv + t.g;
                 R = v.n_nodes * GQ;
+                if (u == u0) pdl_wait();
                 if (32 * quad < R) {
                     uint32_t hi[32], lo[32];
                     const float* qr = q + at_row * kHeadDim + 64 * half;
@@ -674,8 +680,8 @@ static bool tree_maps(const TreeBatch& b, int Hkv, TreeMaps* maps)
 // One CTA of 4 warps, 4 dims a lane.  Warp w sums chunks w, w + 4, .. in order
 // and then path keys w, w + 4, ..; the four sums are added in order.  It is
 // bound by latency, not bytes (R 528 bytes a chunk), so everything it reads is
-// asked for before anything is used: statistics, the first chunks' sums, the
-// path's K and V.
+// asked for before anything is used: the path's K and V, and its scores, before
+// the wait for the chunks, then statistics and the first chunks' sums together.
 constexpr int kMergeAhead = 8;  // chunk sums in flight per warp
 
 __device__ __forceinline__ float4 half4(uint2 x)
@@ -697,7 +703,7 @@ __global__ void __launch_bounds__(kHeadDim)
 tree_merge_kernel(const float* __restrict__ q, const __grid_constant__ TreeBatch b, int Hq, int Hkv, TreeScale scale,
                   const float* __restrict__ part_o, const float* __restrict__ part_ml, float* __restrict__ out,
                   float* __restrict__ scores, int64_t lds, float* __restrict__ stats, int8_t* __restrict__ out_q,
-                  float* __restrict__ out_d)
+                  float* __restrict__ out_d, int nch_all)
 {
     __shared__ float ps[kMaxTree];            // the path's products
     __shared__ float4 os[4][kHeadDim / 4];    // the warps' sums
@@ -708,7 +714,8 @@ tree_merge_kernel(const float* __restrict__ q, const __grid_constant__ TreeBatch
     const int GQ = Hq / Hkv, g = h / GQ, R = v.n_nodes * GQ, np = row.n_path, nch = v.n_chunk;
     const int64_t pr0 = v.part0 + (int64_t)g * R + row.node * GQ + h % GQ, pstep = (int64_t)Hkv * R;
     const size_t rh = (size_t)r * Hq + h;
-    pdl_wait();
+    // behind a chunk kernel, q and the path's rows are in place already
+    if (nch_all == 0) pdl_wait();
     const float4 qv = *reinterpret_cast<const float4*>(q + rh * kHeadDim + 4 * lane);
     uint2 kx[4], vx[4];
 #pragma unroll
@@ -722,6 +729,14 @@ tree_merge_kernel(const float* __restrict__ q, const __grid_constant__ TreeBatch
             if (vp) vx[i] = *reinterpret_cast<const uint2*>(vp + 4 * lane);
         }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 k = half4(kx[i]);
+        const float dot = warp_sum_butterfly(
+            __fmaf_rn(qv.w, k.w, __fmaf_rn(qv.z, k.z, __fmaf_rn(qv.y, k.y, __fmul_rn(qv.x, k.x)))));
+        if (lane == 0 && warp + 4 * i < np) ps[warp + 4 * i] = __fmul_rn(dot, scale.sign);
+    }
+    if (nch_all > 0) pdl_wait();
     // every warp has all chunks' statistics: chunk lane + 32 j in its lane
     constexpr int kStats = kMaxTreeChunks / 32;
     float w[kStats], L = 0.0f, M = -INFINITY;
@@ -742,14 +757,6 @@ tree_merge_kernel(const float* __restrict__ q, const __grid_constant__ TreeBatch
 #pragma unroll
     for (int j = 0; j < kMergeAhead; ++j)
         if (warp + 4 * j < nch) ov[j] = __ldcg(po + (int64_t)(warp + 4 * j) * pstep * (kHeadDim / 4));
-
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 k = half4(kx[i]);
-        const float dot = warp_sum_butterfly(
-            __fmaf_rn(qv.w, k.w, __fmaf_rn(qv.z, k.z, __fmaf_rn(qv.y, k.y, __fmul_rn(qv.x, k.x)))));
-        if (lane == 0 && warp + 4 * i < np) ps[warp + 4 * i] = __fmul_rn(dot, scale.sign);
-    }
     __syncthreads();
     if (scores && tid < v.n_nodes) {
         float x = -INFINITY;
@@ -834,7 +841,7 @@ cudaError_t launch_tree_attention(const float* q, const TreeBatch& b, int Hq, in
     }
     const cudaError_t e =
         launch_pdl(tree_merge_kernel, dim3(Hq, b.n_row), dim3(kHeadDim), s, q, b, Hq, Hkv, sc,
-                   (const float*)part_o, (const float*)part_ml, out, scores, lds, stats, out_q, out_d);
+                   (const float*)part_o, (const float*)part_ml, out, scores, lds, stats, out_q, out_d, (int)units);
     count_launches(1);
     return e;
 }
