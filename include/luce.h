@@ -639,7 +639,7 @@ typedef struct luce_commit_slot {
  * A row whose l is 0 adds nothing.  The caller then continues with
  * len + n_path keys.
  *   scores (device) fp32 [n_layers][n_rows][Hq][lds], 16-byte aligned, lds a
- *          multiple of 4; stats (device) fp32 [n_layers][n_rows][Hq][2]: what
+ *          multiple of 4; stats (device) fp32 [n_layers][n_rows][Hq][2], 8-byte aligned: what
  *          luce_tree_attn gave for each layer.  Both may be NULL when no slot
  *          has acc.
  * No two slots share a cache, acc or pos.  D == 128, Hq % Hkv == 0,

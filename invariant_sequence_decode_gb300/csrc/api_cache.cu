@@ -263,8 +263,8 @@ int luce_tree_commit(const luce_commit_slot* slots, int n_seq, int n_layers, int
     if (any_acc) {
         REQUIRE(n_rows >= 1 && n_rows <= LUCE_MAX_ROWS, LUCE_EINVAL, "%s: n_rows=%d outside 1..%d", who, n_rows,
                 LUCE_MAX_ROWS);
-        REQUIRE(aligned(scores, 16) && lds % 4 == 0 && lds < ((int64_t)1 << 31) && aligned(stats, 4), LUCE_EINVAL,
-                "%s: scores must be 16-byte aligned and lds=%lld a multiple of 4", who, (long long)lds);
+        REQUIRE(aligned(scores, 16) && lds % 4 == 0 && lds < ((int64_t)1 << 31) && aligned(stats, 8), LUCE_EINVAL,
+                "%s: scores must be 16-byte, stats 8-byte aligned and lds=%lld a multiple of 4", who, (long long)lds);
         r[nr++] = range_of(scores, (int64_t)n_layers * n_rows * Hq * lds * 4, -1, "scores", false);
         r[nr++] = range_of(stats, (int64_t)n_layers * n_rows * Hq * 8, -1, "stats", false);
     }

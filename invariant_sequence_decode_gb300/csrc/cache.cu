@@ -32,8 +32,8 @@ __device__ __forceinline__ float commit_exp(float x)
 }
 
 __global__ void __launch_bounds__(kCommitThreads)
-tree_commit_kernel(const __grid_constant__ CommitBatch b, int n_layers, int Hq, int Hkv, const float* __restrict__ scores,
-                   int n_rows, int64_t lds, const float* __restrict__ stats, int move_ctas)
+tree_commit_kernel(const __grid_constant__ CommitBatch b, int n_layers, int Hq, int Hkv, const float* scores, int n_rows, int64_t lds,
+                   const float* stats, int move_ctas)
 {
     __shared__ float2 ml[kMaxTree * 8];   // (m, 1 / l) of the accepted rows' heads
     __shared__ int64_t at[kMaxTree * 8];  // and where their scores begin
@@ -48,7 +48,7 @@ tree_commit_kernel(const __grid_constant__ CommitBatch b, int n_layers, int Hq, 
         uint4 x[kMaxTree];
 #pragma unroll
         for (int i = 0; i < kMaxTree; ++i)
-            if (i < A && sl.path[i] != i) x[i] = p[sl.path[i] * 16];
+            if (i < A && sl.path[i] != i) x[i] = ld_placed_u4(p + sl.path[i] * 16);
 #pragma unroll
         for (int i = 0; i < kMaxTree; ++i)
             if (i < A && sl.path[i] != i) p[i * 16] = x[i];
@@ -62,7 +62,8 @@ tree_commit_kernel(const __grid_constant__ CommitBatch b, int n_layers, int Hq, 
     const int l = lh / Hkv, g = lh % Hkv;
     for (int i = tid; i < n; i += kCommitThreads) {
         const int64_t rh = ((int64_t)l * n_rows + sl.row0 + sl.path[i / GQ]) * Hq + g * GQ + i % GQ;
-        const float m = stats[2 * rh], sum = stats[2 * rh + 1];
+        const float2 st = ld_placed_f2(stats + 2 * rh);
+        const float m = st.x, sum = st.y;
         ml[i] = make_float2(m == -INFINITY ? 0.0f : m, sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum));
         at[i] = rh * lds;
     }
@@ -71,19 +72,19 @@ tree_commit_kernel(const __grid_constant__ CommitBatch b, int n_layers, int Hq, 
     if (tile == 0 && tid < A) {
         float w = 0.0f;
         for (int i = 0; i < n; ++i)
-            w = __fmaf_rn(commit_exp(__fsub_rn(scores[at[i] + sl.len + sl.path[tid]], ml[i].x)), ml[i].y, w);
+            w = __fmaf_rn(commit_exp(__fsub_rn(ld_placed_f(scores + at[i] + sl.len + sl.path[tid]), ml[i].x)), ml[i].y, w);
         acc[sl.len + tid] = w;
     }
     const int j = tile * kCommitKeys + 4 * tid;
     if (j >= sl.len) return;
     float old[4], w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) old[e] = j + e < sl.len ? acc[j + e] : 0.0f;
+    for (int e = 0; e < 4; ++e) old[e] = j + e < sl.len ? ld_placed_f(acc + j + e) : 0.0f;
     for (int i0 = 0; i0 < n; i0 += kCommitAhead) {
         float4 s[kCommitAhead];
 #pragma unroll
         for (int e = 0; e < kCommitAhead; ++e)
-            if (i0 + e < n) s[e] = __ldcs(reinterpret_cast<const float4*>(scores + at[i0 + e] + j));
+            if (i0 + e < n) s[e] = ld_placed_cs_f4(scores + at[i0 + e] + j);
 #pragma unroll
         for (int e = 0; e < kCommitAhead; ++e)
             if (i0 + e < n) {
@@ -247,8 +248,8 @@ kv_evict_kernel(const __grid_constant__ EvictBatch b, int slice)
         for (int e = 0; e < kEvictAhead; ++e) {
             const int i = i0 + e * kEvictThreads;
             if (i < nj) {
-                a[e] = acc[j0 + i];
-                p[e] = pos[j0 + i];
+                a[e] = ld_placed_f(acc + j0 + i);
+                p[e] = ld_placed_i(pos + j0 + i);
             }
         }
 #pragma unroll
@@ -404,15 +405,15 @@ kv_evict_kernel(const __grid_constant__ EvictBatch b, int slice)
                 to = (int)list[i];
                 from = (int)list[slice - 1 - i];
             }
-            acc_out[to] = acc[from];
-            pos_out[to] = pos[from];
+            acc_out[to] = ld_placed_f(acc + from);
+            pos_out[to] = ld_placed_i(pos + from);
         }
         for (int k = 0; k < cnt; k += kEvictMove) {
             uint4 x[kEvictMove];
 #pragma unroll
             for (int d = 0; d < kEvictMove; ++d) {
                 const int f = __shfl_sync(0xffffffffu, from, (k + d) & 31);
-                if (k + d < cnt) x[d] = __ldcs(base + (int64_t)f * 16);
+                if (k + d < cnt) x[d] = ld_placed_cs_u4(base + (int64_t)f * 16);
             }
 #pragma unroll
             for (int d = 0; d < kEvictMove; ++d) {
@@ -469,8 +470,8 @@ kv_evict_few_kernel(const __grid_constant__ EvictBatch b)
         for (int e = 0; e < kFewPer; ++e) {
             const int j = tid + e * kFewThreads;
             if (j < sl.len) {
-                a[e] = acc[j];
-                p[e] = pos[j];
+                a[e] = ld_placed_f(acc + j);
+                p[e] = ld_placed_i(pos + j);
             }
         }
 #pragma unroll
@@ -533,10 +534,10 @@ kv_evict_few_kernel(const __grid_constant__ EvictBatch b)
     uint4* base = reinterpret_cast<uint4*>(lane < 16 ? sl.k : sl.v) + lh * sl.cap * 16 + (lane & 15);
     for (int i = warp; i < m; i += kFewWarps) {
         const int to = hole[i], from = come[i];
-        base[(int64_t)to * 16] = base[(int64_t)from * 16];
+        base[(int64_t)to * 16] = ld_placed_u4(base + (int64_t)from * 16);
         if (lane == 0) {
-            acc_out[to] = acc[from];
-            pos_out[to] = pos[from];
+            acc_out[to] = ld_placed_f(acc + from);
+            pos_out[to] = ld_placed_i(pos + from);
         }
     }
 }

@@ -8,6 +8,75 @@
 
 namespace luce {
 
+#ifdef __CUDACC__
+// Loads of what an earlier kernel may still be writing when this one starts:
+// none may move ahead of the wait for it (pdl_wait).  A load through a const
+// __restrict__ pointer, __ldg or __ldcg may be, as what it reads counts as
+// constant for the kernel's whole life; these keep their place.
+__device__ __forceinline__ float4 ld_placed_f4(const void* p)
+{
+    float4 r;
+    asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w) : "l"(p) : "memory");
+    return r;
+}
+// The same past L1: data that other kernels wrote and that is read once.
+__device__ __forceinline__ float4 ld_placed_cg_f4(const void* p)
+{
+    float4 r;
+    asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w)
+                 : "l"(p)
+                 : "memory");
+    return r;
+}
+// The same, first to leave the caches.
+__device__ __forceinline__ float4 ld_placed_cs_f4(const void* p)
+{
+    float4 r;
+    asm volatile("ld.global.cs.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w)
+                 : "l"(p)
+                 : "memory");
+    return r;
+}
+__device__ __forceinline__ float2 ld_placed_f2(const void* p)
+{
+    float2 r;
+    asm volatile("ld.global.v2.f32 {%0, %1}, [%2];" : "=f"(r.x), "=f"(r.y) : "l"(p) : "memory");
+    return r;
+}
+__device__ __forceinline__ float ld_placed_f(const void* p)
+{
+    float r;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(r) : "l"(p) : "memory");
+    return r;
+}
+__device__ __forceinline__ int ld_placed_i(const void* p)
+{
+    int r;
+    asm volatile("ld.global.s32 %0, [%1];" : "=r"(r) : "l"(p) : "memory");
+    return r;
+}
+__device__ __forceinline__ uint2 ld_placed_u2(const void* p)
+{
+    uint2 r;
+    asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p) : "memory");
+    return r;
+}
+__device__ __forceinline__ uint4 ld_placed_cs_u4(const void* p)
+{
+    uint4 r;
+    asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+    return r;
+}
+__device__ __forceinline__ uint4 ld_placed_u4(const void* p)
+{
+    uint4 r;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+    return r;
+}
+#endif
+
 constexpr int kMaxTree = 16;  // nodes of a slot's tree, and rows of a call
 
 // A slot's tree over its cache for one layer.  Flat cache (pages == nullptr):

@@ -77,7 +77,7 @@ size_t tree_part_bytes(int64_t n_part) { return (size_t)n_part * (kHeadDim + 4) 
 __device__ __forceinline__ const __half* tree_key(const TreeView& v, const __half* base, int g, int key)
 {
     if (!v.pages) return base + (int64_t)g * v.head_stride + (int64_t)key * v.tok_stride;
-    const int p = __ldg(v.pages + (key >> 7));
+    const int p = ld_placed_i(v.pages + (key >> 7));
     if (p < 0 || p >= v.n_pages) return nullptr;
     return base + (int64_t)p * v.page_stride + (int64_t)g * v.head_stride + (int64_t)(key & 127) * v.tok_stride;
 }
@@ -174,22 +174,7 @@ __device__ __forceinline__ uint32_t elect_one()
 __device__ __forceinline__ void tm_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tm_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// 32 or 64 columns of this warp's 32 lanes of tensor memory, waited for.
-__device__ __forceinline__ void tm_ld32(uint32_t addr, float* v)
-{
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-        " tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(addr));
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
+// 64 columns of this warp's 32 lanes of tensor memory, waited for.
 __device__ __forceinline__ void tm_ld64(uint32_t addr, float* v)
 {
     uint32_t r[64];
@@ -294,7 +279,7 @@ __device__ int tree_produce(const TreeMaps& maps, const TreeBatch& b, int Hkv, i
             const int key = t.key0 + k * kTreeTile;
             int page = 0, y = key;
             if (v.pages) {
-                page = __ldg(v.pages + (key >> 7));
+                page = ld_placed_i(v.pages + (key >> 7));
                 if (page < 0 || page >= v.n_pages) page = v.n_pages;  // outside the map: zeros
                 y = 0;
             }
@@ -316,105 +301,74 @@ __device__ int tree_produce(const TreeMaps& maps, const TreeBatch& b, int Hkv, i
     return i;
 }
 
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity)
-{
-    uint32_t done;
-    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-                 : "=r"(done)
-                 : "r"(smem_addr(bar)), "r"(parity)
-                 : "memory");
-    return done;
-}
-
-// The products, issued by one warp: S = Q K^T of the next tile as soon as its K
-// is there and its buffer free, else P V of the next tile whose P is there.
-// One warp for both, each product's 16 steps in one go: issued by a warp each
-// the steps of S and P V alternate on the tensor cores and both take twice
-// their time, with the softmax waiting for the one and the buffer for the other
-// (3,050 cycles a tile).  The issue loops stay loops: unrolled, their code (4 KB
-// each) fell out of the instruction cache at every chunk's end and cost 8,000
-// cycles to fetch again.  The warp sits in the scheduler of the last row quarter,
-// which has rows to work on in the widest calls only.
+// The products, issued by one warp in the order S of tile i, P V of tile i - 1:
+// while a tile's softmax runs the tensor cores have the other product of the
+// tiles beside it.  One warp for both, each product's 16 steps in one go:
+// issued by a warp each, the steps of S and P V alternated on the tensor cores
+// and both took twice their time, with the softmax waiting for the one and the
+// buffer for the other (3,050 cycles a tile against 2,650).  The issue loops
+// stay loops: unrolled whole, their code (4 KB each) fell out of the
+// instruction cache at every chunk's end and cost 8,000 cycles to fetch again.
+// The warp sits in the scheduler of the last row quarter, which has rows to
+// work on in the widest calls only.
 __device__ void tree_products(const TreeBatch& b, int Hkv, int u0, int u1, int step, uint32_t tiles, uint32_t tmem,
                               TreeBars& bar)
 {
     // D f32, A and B f16, 128 x 128; P V's B (V) is N-major
     constexpr uint32_t idesc_s = (1u << 4) | (16u << 17) | (8u << 24), idesc_o = idesc_s | (1u << 16);
     const uint32_t elected = elect_one();
-    int left = 0;  // tiles whose S is still to come
-    for (int u = u0; u < u1; u += step) left += tree_unit(b, Hkv, u).tiles;
-    int i = 0, j = 0, u = u0, k = 0, heads = 0, last = -1;
-    bool fresh = left > 0;  // the tile is its head's first: q is not there yet
-    TreeUnit t = left > 0 ? tree_unit(b, Hkv, u0) : TreeUnit{};
-    if (left > 0) last = t.view * Hkv + t.g;
-    uint64_t since = 0;
-    for (uint32_t polls = 0; left > 0 || j < i;) {
-        if (left > 0) {
+    unsigned int* late = &g_tree_wait_timeouts;
+    int i = 0, heads = 0, last = -1;
+    auto values = [&](int j) {
+        const int st = j % kTreeStages;
+        const bool there = mbar_wait(&bar.v_full[st], (j / kTreeStages) & 1, late) &&
+                           mbar_wait(&bar.p_full[j & 1], (j >> 1) & 1, late) &&
+                           (j == 0 || mbar_wait(&bar.o_free, (j - 1) & 1, late));
+        if (!__all_sync(0xffffffffu, there)) return false;  // (the warp leaves as one)
+        tm_after();
+        const uint32_t p = tmem + kColS + 128 * (j & 1) + 32;
+        const uint64_t d = tree_desc(tiles + (kTreeStages + st) * kTreeTileBytes, kTreeTileBytes / 2, 1024);
+        // the low parts first: an accumulation loses digits by the sum's size,
+        // and theirs is small
+#pragma unroll 4
+        for (int ks = 0; ks < 16; ++ks)
+            tree_mma(tmem + kColO, p + 64 * (ks >> 2 & 1) + 8 * (ks & 3) - 32 * (ks >> 3), d + 128 * (ks & 7), idesc_o,
+                     ks > 0, elected);
+        tree_commit_mma(&bar.o_full, elected);
+        tree_commit_mma(&bar.p_read[j & 1], elected);
+        tree_commit_mma(&bar.v_empty[st], elected);
+        return true;
+    };
+    for (int u = u0; u < u1; u += step) {
+        const TreeUnit t = tree_unit(b, Hkv, u);
+        if (t.view * Hkv + t.g != last) {
+            last = t.view * Hkv + t.g;
+            if (!__all_sync(0xffffffffu, mbar_wait(&bar.q_full, heads++ & 1, late))) return;
+        }
+        for (int k = 0; k < t.tiles; ++k, ++i) {
             const int st = i % kTreeStages;
-            const bool q_there = !fresh || mbar_test(&bar.q_full, heads & 1);
-            const bool free = mbar_test(&bar.p_read[i & 1], ((i >> 1) & 1) ^ 1);
-            const bool k_there = mbar_test(&bar.k_full[st], (i / kTreeStages) & 1);
-            if (__all_sync(0xffffffffu, q_there && free && k_there)) {
-                tm_after();
-                if (fresh) ++heads;
-                const uint32_t s = tmem + kColS + 128 * (i & 1);
-                const uint64_t d = tree_desc(tiles + st * kTreeTileBytes, 16, 1024);
-                // the low parts first: an accumulation loses digits by the
-                // sum's size, and theirs is small
+            // (the first two buffers are free)
+            const bool there = mbar_wait(&bar.k_full[st], (i / kTreeStages) & 1, late) &&
+                               mbar_wait(&bar.p_read[i & 1], ((i >> 1) & 1) ^ 1, late);
+            if (!__all_sync(0xffffffffu, there)) return;
+            tm_after();
+            const uint32_t s = tmem + kColS + 128 * (i & 1);
+            const uint64_t d = tree_desc(tiles + st * kTreeTileBytes, 16, 1024);
 #pragma unroll 4
-                for (int ks = 0; ks < 16; ++ks)
-                    tree_mma(s, tmem + kColQ + 8 * (ks ^ 8), d + (ks >> 2 & 1) * (kTreeTileBytes / 32) + 2 * (ks & 3),
-                             idesc_s, ks > 0, elected);
-                tree_commit_mma(&bar.s_full[i & 1], elected);
-                tree_commit_mma(&bar.k_empty[st], elected);
-                ++i;
-                fresh = false;
-                if (++k == t.tiles && --left > 0) {
-                    k = 0;
-                    t = tree_unit(b, Hkv, u += step);
-                    fresh = t.view * Hkv + t.g != last;
-                    last = t.view * Hkv + t.g;
-                } else if (k < t.tiles) {
-                    --left;
-                }
-                polls = 0;
-            }
-        }
-        if (j < i) {
-            const int st = j % kTreeStages;
-            const bool p_there = mbar_test(&bar.p_full[j & 1], (j >> 1) & 1);
-            const bool free = j == 0 || mbar_test(&bar.o_free, (j - 1) & 1);
-            const bool v_there = mbar_test(&bar.v_full[st], (j / kTreeStages) & 1);
-            if (__all_sync(0xffffffffu, p_there && free && v_there)) {
-                tm_after();
-                const uint32_t p = tmem + kColS + 128 * (j & 1) + 32;
-                const uint64_t d = tree_desc(tiles + (kTreeStages + st) * kTreeTileBytes, kTreeTileBytes / 2, 1024);
-#pragma unroll 4
-                for (int ks = 0; ks < 16; ++ks)
-                    tree_mma(tmem + kColO, p + 64 * (ks >> 2 & 1) + 8 * (ks & 3) - 32 * (ks >> 3), d + 128 * (ks & 7),
-                             idesc_o, ks > 0, elected);
-                tree_commit_mma(&bar.o_full, elected);
-                tree_commit_mma(&bar.p_read[j & 1], elected);
-                tree_commit_mma(&bar.v_empty[st], elected);
-                ++j;
-                polls = 0;
-            }
-        }
-        // bounded: about a second without a product (or 2^26 polls) and the
-        // warp gives up; the clock is only looked at every 256 polls
-        if ((++polls & 255) == 0) {
-            if (polls == 256) since = global_ns();
-            if (__any_sync(0xffffffffu, global_ns() - since > kWaitLimitNs || polls >= (1u << 26))) {
-                if (elected) atomicAdd(&g_tree_wait_timeouts, 1u);
-                return;
-            }
+            for (int ks = 0; ks < 16; ++ks)  // the low parts first, as above
+                tree_mma(s, tmem + kColQ + 8 * (ks ^ 8), d + (ks >> 2 & 1) * (kTreeTileBytes / 32) + 2 * (ks & 3), idesc_s,
+                         ks > 0, elected);
+            tree_commit_mma(&bar.s_full[i & 1], elected);
+            tree_commit_mma(&bar.k_empty[st], elected);
+            if (i > 0 && !values(i - 1)) return;
         }
     }
+    if (i > 0) values(i - 1);
 }
 
 // One CTA an SM, each with its share of all chunks.
 __global__ void __launch_bounds__(kTreeThreads, 1)
-tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* __restrict__ q, const __grid_constant__ TreeBatch b,
+tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const __grid_constant__ TreeBatch b,
                   int Hq, int Hkv, int units, bool runs, TreeScale scale, float* __restrict__ part_o, float* __restrict__ part_ml,
                   float* __restrict__ scores, int64_t lds)
 {
@@ -492,7 +446,7 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* __restrict
         bool prev_first = true, prev_live = false;
         float* prev_out = nullptr;
         auto take = [&](int j) {
-            const bool done = mbar_wait(&bar.o_full, j & 1, late);
+            const bool done = __all_sync(0xffffffffu, mbar_wait(&bar.o_full, j & 1, late));
             tm_after();
             if (prev_live && done) {
                 if (prev_first) {
@@ -500,16 +454,16 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* __restrict
                     for (int e = 0; e < 32; ++e) o[e] = 0;
                 }
                 const uint64_t al = pair(prev_alpha, prev_alpha);
+                float x[64];
+                tm_ld64(lanes + kColO + 64 * half, x);
+                tm_before();
+                mbar_arrive(&bar.o_free);  // (the next tile's P V waits for this)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float x[32];
-                    tm_ld32(lanes + kColO + 64 * half + 32 * c, x);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[16 * c + e] = fma2(o[16 * c + e], al, pair(x[2 * e], x[2 * e + 1]));
-                }
+                for (int e = 0; e < 32; ++e) o[e] = fma2(o[e], al, pair(x[2 * e], x[2 * e + 1]));
+            } else {
+                tm_before();
+                mbar_arrive(&bar.o_free);
             }
-            tm_before();
-            mbar_arrive(&bar.o_free);
             if (prev_out && done) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 4) {
@@ -533,7 +487,7 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* __restrict
                     const float* qr = q + at_row * kHeadDim + 64 * half;
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const float4 x = row < R ? *reinterpret_cast<const float4*>(qr + 4 * e) : make_float4(0, 0, 0, 0);
+                        const float4 x = row < R ? ld_placed_f4(qr + 4 * e) : make_float4(0, 0, 0, 0);
                         tree_split(__fmul_rn(x.x, scale.sign), __fmul_rn(x.y, scale.sign), hi[2 * e], lo[2 * e]);
                         tree_split(__fmul_rn(x.z, scale.sign), __fmul_rn(x.w, scale.sign), hi[2 * e + 1], lo[2 * e + 1]);
                     }
@@ -700,8 +654,8 @@ __device__ __forceinline__ void axpy4(float4& o, float4 x, float a)
 }
 
 __global__ void __launch_bounds__(kHeadDim)
-tree_merge_kernel(const float* __restrict__ q, const __grid_constant__ TreeBatch b, int Hq, int Hkv, TreeScale scale,
-                  const float* __restrict__ part_o, const float* __restrict__ part_ml, float* __restrict__ out,
+tree_merge_kernel(const float* q, const __grid_constant__ TreeBatch b, int Hq, int Hkv, TreeScale scale,
+                  const float* part_o, const float* part_ml, float* __restrict__ out,
                   float* __restrict__ scores, int64_t lds, float* __restrict__ stats, int8_t* __restrict__ out_q,
                   float* __restrict__ out_d, int nch_all)
 {
@@ -716,7 +670,7 @@ tree_merge_kernel(const float* __restrict__ q, const __grid_constant__ TreeBatch
     const size_t rh = (size_t)r * Hq + h;
     // behind a chunk kernel, q and the path's rows are in place already
     if (nch_all == 0) pdl_wait();
-    const float4 qv = *reinterpret_cast<const float4*>(q + rh * kHeadDim + 4 * lane);
+    const float4 qv = ld_placed_f4(q + rh * kHeadDim + 4 * lane);
     uint2 kx[4], vx[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -725,8 +679,8 @@ tree_merge_kernel(const float* __restrict__ q, const __grid_constant__ TreeBatch
             const int key = v.len + row.path[warp + 4 * i];
             const __half* kp = tree_key(v, v.k, g, key);
             const __half* vp = tree_key(v, v.v, g, key);
-            if (kp) kx[i] = *reinterpret_cast<const uint2*>(kp + 4 * lane);
-            if (vp) vx[i] = *reinterpret_cast<const uint2*>(vp + 4 * lane);
+            if (kp) kx[i] = ld_placed_u2(kp + 4 * lane);
+            if (vp) vx[i] = ld_placed_u2(vp + 4 * lane);
         }
     }
 #pragma unroll
@@ -747,7 +701,7 @@ tree_merge_kernel(const float* __restrict__ q, const __grid_constant__ TreeBatch
         w[j] = -INFINITY;
         ls[j] = make_float2(0.0f, 0.0f);
         if (c < nch) {
-            const float4 ml = __ldcg(reinterpret_cast<const float4*>(part_ml + 4 * (pr0 + c * pstep)));
+            const float4 ml = ld_placed_cg_f4(part_ml + 4 * (pr0 + c * pstep));
             w[j] = ml.x;
             ls[j] = make_float2(ml.y, ml.z);
         }
@@ -756,7 +710,7 @@ tree_merge_kernel(const float* __restrict__ q, const __grid_constant__ TreeBatch
     const float4* po = reinterpret_cast<const float4*>(part_o) + pr0 * (kHeadDim / 4) + lane;
 #pragma unroll
     for (int j = 0; j < kMergeAhead; ++j)
-        if (warp + 4 * j < nch) ov[j] = __ldcg(po + (int64_t)(warp + 4 * j) * pstep * (kHeadDim / 4));
+        if (warp + 4 * j < nch) ov[j] = ld_placed_cg_f4(po + (int64_t)(warp + 4 * j) * pstep * (kHeadDim / 4));
     __syncthreads();
     if (scores && tid < v.n_nodes) {
         float x = -INFINITY;
@@ -784,7 +738,7 @@ tree_merge_kernel(const float* __restrict__ q, const __grid_constant__ TreeBatch
             if (4 * j >= nch) break;
 #pragma unroll
             for (int e = 0; e < kMergeAhead; ++e)
-                if (c + 4 * e < nch) ov[e] = __ldcg(po + (int64_t)(c + 4 * e) * pstep * (kHeadDim / 4));
+                if (c + 4 * e < nch) ov[e] = ld_placed_cg_f4(po + (int64_t)(c + 4 * e) * pstep * (kHeadDim / 4));
         }
         const float f = __shfl_sync(0xffffffffu, w[j >> 3], c & 31);
         if (c < nch) axpy4(o, ov[j & (kMergeAhead - 1)], f);

@@ -96,6 +96,23 @@ def test_a_node_gives_the_bits_of_its_path_alone(model, lens, trees, pos0):
         row0 += len(tree)
 
 
+@pytest.mark.parametrize("length", [0, 130, 700])
+def test_repeated_steps_give_the_same_bits(model, length):
+    """Kernels of a step overlap at their ends; none may read ahead of what it waits for."""
+    k, v = cache(0, length, length + 20)
+    xh = wl.acts(3, 8, wl.TINY_LAYER.hidden, sub=6)
+    ws, first = model.tree_workspace(8, length), None
+    for it in range(60):
+        ws.fill_(255 * (it & 1))
+        sl = luce.TreeSlot(cuda(k), cuda(v), length, [-1, 0, 0, 1, 1, 2, 5, -1])
+        x, logits, am = cuda(xh), torch.empty(8, VOCAB, device="cuda"), torch.empty(8, dtype=torch.int32, device="cuda")
+        luce.luce_decode_step_tree(model, [sl], x, ws, logits, am)
+        torch.cuda.synchronize()
+        got = [bits(x), bits(logits), sl.k.view(torch.int16).cpu().numpy(), sl.v.view(torch.int16).cpu().numpy()]
+        first = first or got
+        assert all(np.array_equal(a, b) for a, b in zip(got, first))
+
+
 def test_chains_agree_with_the_plain_step(model):
     lens, rows, cap = [3, 40, 200, 255], [1, 2, 3, 4], 300
     host = [cache(s, n, cap) for s, n in enumerate(lens)]
