@@ -611,6 +611,27 @@ int luce_decode_step_tree(const luce_model* m, const luce_tree_slot* slots, int 
 int luce_decode_step_tree_layout(const luce_model* m, int n_rows, int max_ctx, luce_step_layout* out);
 
 /*
+ * The same over paged slots (luce_paged_slot's pools and tables; the pages that
+ * receive this step's rows are referenced by no other slot of the call): the
+ * bits of flat caches that hold the same keys.
+ */
+typedef struct luce_paged_tree_slot {
+    uint16_t* k_pool;              /* (device) [n_pages][n_layers][Hkv][128][128] */
+    uint16_t* v_pool;              /* (device) */
+    const int32_t* table;          /* (device) [n_table] */
+    const int32_t* table_host;     /* (host)   [n_table], equal to table */
+    int32_t n_table;               /* >= ceil((len + n_nodes) / 128) */
+    int32_t n_pages;
+    int32_t len;
+    int32_t pos0;
+    int32_t n_nodes;
+    const int32_t* parent;         /* (host) [n_nodes] or NULL */
+} luce_paged_tree_slot;
+int luce_decode_step_tree_paged(const luce_model* m, const luce_paged_tree_slot* slots, int n_seq, float* x,
+                                float* logits, int32_t* argmax, float* scores, int64_t lds, float* stats, void* ws,
+                                size_t ws_bytes, void* stream);
+
+/*
  * A slot whose verified tree is committed: the accepted nodes path[0] <
  * path[1] < .. (a path from the prefix, so ascending) become the keys
  * len .. len + n_path - 1.
@@ -647,6 +668,28 @@ typedef struct luce_commit_slot {
  */
 int luce_tree_commit(const luce_commit_slot* slots, int n_seq, int n_layers, int Hq, int Hkv, int D,
                      const float* scores, int n_rows, int64_t lds, const float* stats, void* stream);
+
+/*
+ * The same over paged slots: rows move between the pages that table_host names.
+ * No page is named by two slots of the call at indexes that it writes.
+ */
+typedef struct luce_paged_commit_slot {
+    uint16_t* k_pool;           /* (device) [n_pages][n_layers][Hkv][128][128], 16-byte aligned */
+    uint16_t* v_pool;           /* (device) same layout */
+    const int32_t* table_host;  /* (host) [n_table] */
+    int32_t n_table;            /* >= ceil((len + path[n_path - 1] + 1) / 128) */
+    int32_t n_pages;
+    int32_t len;
+    int32_t cap;                /* keys of a head in acc and pos */
+    int32_t n_path;
+    int32_t row0;
+    const int32_t* path;        /* (host) [n_path] */
+    float* acc;                 /* (device) [n_layers][Hkv][cap] or NULL */
+    int32_t* pos;               /* (device) [n_layers][Hkv][cap] or NULL */
+    int32_t pos0;
+} luce_paged_commit_slot;
+int luce_tree_commit_paged(const luce_paged_commit_slot* slots, int n_seq, int n_layers, int Hq, int Hkv, int D,
+                           const float* scores, int n_rows, int64_t lds, const float* stats, void* stream);
 
 /* ---------------------------------------------------------------- eviction */
 
@@ -687,6 +730,30 @@ typedef struct luce_evict_slot {
  * overlaps no input but its own.
  */
 int luce_kv_evict(const luce_evict_slot* slots, int n_seq, int n_layers, int Hkv, int D, void* stream);
+
+/*
+ * The same over paged slots; the pages of indexes >= budget are free
+ * afterwards.  table (device) holds ceil(len / 128) entries; a row of a page
+ * outside [0, n_pages) is neither read nor written.  No page below index budget
+ * is named twice in the call.
+ */
+typedef struct luce_paged_evict_slot {
+    uint16_t* k_pool;     /* (device) [n_pages][n_layers][Hkv][128][128], 16-byte aligned */
+    uint16_t* v_pool;     /* (device) same layout */
+    const int32_t* table; /* (device) page of each 128-key span */
+    const float* acc;     /* (device) [n_layers][Hkv][cap] */
+    const int32_t* pos;   /* (device) [n_layers][Hkv][cap] */
+    float* acc_out;       /* (device) as acc; may be acc itself */
+    int32_t* pos_out;     /* (device) as pos; may be pos itself */
+    int32_t n_pages;
+    int32_t len;          /* keys cached */
+    int32_t cap;          /* keys of a head in acc and pos */
+    int32_t budget;
+    int32_t sinks;
+    int32_t recent;
+    int32_t next_pos;
+} luce_paged_evict_slot;
+int luce_kv_evict_paged(const luce_paged_evict_slot* slots, int n_seq, int n_layers, int Hkv, int D, void* stream);
 
 #ifdef __cplusplus
 }

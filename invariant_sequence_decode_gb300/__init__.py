@@ -86,8 +86,23 @@ class TreeSlotC(ctypes.Structure):
                 ("pos0", ctypes.c_int32), ("n_nodes", ctypes.c_int32), ("parent", ctypes.POINTER(ctypes.c_int32))]
 
 
+class PagedTreeSlotC(ctypes.Structure):
+    _fields_ = [("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("table_host", ctypes.POINTER(ctypes.c_int32)), ("n_table", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("len", ctypes.c_int32), ("pos0", ctypes.c_int32),
+                ("n_nodes", ctypes.c_int32), ("parent", ctypes.POINTER(ctypes.c_int32))]
+
+
 class CommitSlotC(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("len", ctypes.c_int32), ("cap", ctypes.c_int32),
+                ("n_path", ctypes.c_int32), ("row0", ctypes.c_int32), ("path", ctypes.POINTER(ctypes.c_int32)),
+                ("acc", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("pos0", ctypes.c_int32)]
+
+
+class PagedCommitSlotC(ctypes.Structure):
+    _fields_ = [("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p),
+                ("table_host", ctypes.POINTER(ctypes.c_int32)), ("n_table", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("len", ctypes.c_int32), ("cap", ctypes.c_int32),
                 ("n_path", ctypes.c_int32), ("row0", ctypes.c_int32), ("path", ctypes.POINTER(ctypes.c_int32)),
                 ("acc", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("pos0", ctypes.c_int32)]
 
@@ -95,6 +110,14 @@ class CommitSlotC(ctypes.Structure):
 class EvictSlotC(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("acc", ctypes.c_void_p), ("pos", ctypes.c_void_p),
                 ("acc_out", ctypes.c_void_p), ("pos_out", ctypes.c_void_p), ("len", ctypes.c_int32),
+                ("cap", ctypes.c_int32), ("budget", ctypes.c_int32), ("sinks", ctypes.c_int32),
+                ("recent", ctypes.c_int32), ("next_pos", ctypes.c_int32)]
+
+
+class PagedEvictSlotC(ctypes.Structure):
+    _fields_ = [("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("acc", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("acc_out", ctypes.c_void_p),
+                ("pos_out", ctypes.c_void_p), ("n_pages", ctypes.c_int32), ("len", ctypes.c_int32),
                 ("cap", ctypes.c_int32), ("budget", ctypes.c_int32), ("sinks", ctypes.c_int32),
                 ("recent", ctypes.c_int32), ("next_pos", ctypes.c_int32)]
 
@@ -115,7 +138,8 @@ EXPORTS = ("luce_last_error", "luce_version", "luce_launch_count", "luce_q8_quan
            "luce_test_wait_expiry", "luce_q8_matvec_batch_path", "luce_q8_quantize_act_f16", "luce_rmsnorm_q8",
            "luce_swiglu_q8", "luce_step_graph_create", "luce_step_graph_run", "luce_step_graph_stats",
            "luce_step_graph_destroy", "luce_tree_attn", "luce_tree_attn_paged", "luce_tree_attn_workspace_size",
-           "luce_tree_commit", "luce_kv_evict", "luce_decode_step_tree", "luce_decode_step_tree_layout")
+           "luce_tree_commit", "luce_kv_evict", "luce_decode_step_tree", "luce_decode_step_tree_layout",
+           "luce_decode_step_tree_paged", "luce_tree_commit_paged", "luce_kv_evict_paged")
 
 _lib = None
 
@@ -174,6 +198,10 @@ def load_library(path: str = LIB_PATH):
     lib.luce_tree_attn_workspace_size.restype = sz
     lib.luce_decode_step_tree.argtypes = [ctypes.POINTER(ModelC), ctypes.POINTER(TreeSlotC), i32, vp, vp, vp, vp, i64, vp,
                                           vp, sz, vp]
+    lib.luce_decode_step_tree_paged.argtypes = [ctypes.POINTER(ModelC), ctypes.POINTER(PagedTreeSlotC), i32, vp, vp, vp,
+                                                vp, i64, vp, vp, sz, vp]
+    lib.luce_tree_commit_paged.argtypes = [ctypes.POINTER(PagedCommitSlotC), i32, i32, i32, i32, i32, vp, i32, i64, vp, vp]
+    lib.luce_kv_evict_paged.argtypes = [ctypes.POINTER(PagedEvictSlotC), i32, i32, i32, i32, vp]
     lib.luce_decode_step_tree_layout.argtypes = [ctypes.POINTER(ModelC), i32, i32, ctypes.POINTER(StepLayoutC)]
     lib.luce_tree_commit.argtypes = [ctypes.POINTER(CommitSlotC), i32, i32, i32, i32, i32, vp, i32, i64, vp, vp]
     lib.luce_kv_evict.argtypes = [ctypes.POINTER(EvictSlotC), i32, i32, i32, i32, vp]
@@ -724,6 +752,25 @@ class TreeSlot:
 
 
 @dataclass
+class PagedTreeSlot:
+    """The same in pages of 128 tokens: pools fp16 [n_pages][n_layers][Hkv][128][128]
+    and ``table``, the pool page of each 128-token span (a host int32 array,
+    mirrored on the device as table_dev)."""
+    k_pool: object
+    v_pool: object
+    table: object  # numpy int32
+    len: int
+    parent: object = 1
+    pos0: Optional[int] = None
+
+    def __post_init__(self):
+        import numpy as np
+        import torch
+        self.table = np.ascontiguousarray(self.table, dtype=np.int32)
+        self.table_dev = torch.from_numpy(self.table).to(self.k_pool.device)
+
+
+@dataclass
 class CommitSlot:
     """A slot's cache of every layer (fp16 [n_layers][Hkv][cap][128]) whose tree's
     nodes ``path`` (ascending) were accepted; ``row0`` is the score row of node
@@ -740,12 +787,45 @@ class CommitSlot:
 
 
 @dataclass
+class PagedCommitSlot:
+    """The same over pools fp16 [n_pages][n_layers][Hkv][128][128] and a host
+    int32 ``table``; acc and pos are [n_layers][Hkv][keys]."""
+    k_pool: object
+    v_pool: object
+    table: object  # numpy int32
+    len: int
+    path: object
+    row0: int = 0
+    acc: object = None
+    pos: object = None
+    pos0: int = 0
+
+
+@dataclass
 class EvictSlot:
     """A slot's cache with its keys' accumulated weights and positions (as in
     CommitSlot), to be cut to ``budget`` keys; acc_out and pos_out default to
     acc and pos themselves."""
     k: object
     v: object
+    acc: object
+    pos: object
+    len: int
+    budget: int
+    sinks: int = 0
+    recent: int = 0
+    next_pos: int = 0
+    acc_out: object = None
+    pos_out: object = None
+
+
+@dataclass
+class PagedEvictSlot:
+    """The same over pools fp16 [n_pages][n_layers][Hkv][128][128] and a device
+    int32 ``table``; the pages of indexes >= budget are free afterwards."""
+    k_pool: object
+    v_pool: object
+    table: object
     acc: object
     pos: object
     len: int
@@ -949,18 +1029,26 @@ def luce_decode_step_tree(model: "Model", slots: Sequence[TreeSlot], x, ws, logi
     luce_tree_commit takes."""
     import torch
     _need(x, torch.float32, "x")
-    n, T = len(slots), x.shape[0]
-    sc, trees = (TreeSlotC * max(1, n))(), [_tree(s.parent) for s in slots]
+    n, T, L, Hkv = len(slots), x.shape[0], len(model.layers), model.n_kv_heads
+    paged = n > 0 and isinstance(slots[0], PagedTreeSlot)
+    if not all(isinstance(s, PagedTreeSlot if paged else TreeSlot) for s in slots):
+        raise TypeError("slots: expected TreeSlots or PagedTreeSlots, of one kind")
+    trees = [_tree(s.parent) for s in slots]
     if sum(t[0] for t in trees) != T:
         raise ValueError(f"x has {T} rows, the trees {sum(t[0] for t in trees)}")
+    sc = ((PagedTreeSlotC if paged else TreeSlotC) * max(1, n))()
     for i, (s, (nn, par)) in enumerate(zip(slots, trees)):
-        _kv_pair(s.k, s.v, 4, f"slots[{i}]")
-        _need(s.k, torch.float16, f"slots[{i}].k")
-        _need(s.v, torch.float16, f"slots[{i}].v")
-        if s.k.shape[:2] != (len(model.layers), model.n_kv_heads):
-            raise ValueError(f"slots[{i}]: expected caches [n_layers][n_kv_heads][cap][128] of the model")
-        _same_device(x, s.k, s.v)
-        sc[i] = TreeSlotC(s.k.data_ptr(), s.v.data_ptr(), s.len, s.k.shape[2], s.len if s.pos0 is None else s.pos0, nn, par)
+        pos0 = s.len if s.pos0 is None else s.pos0
+        if paged:
+            _pools(s.k_pool, s.v_pool, L, Hkv, f"slots[{i}]")
+            _same_device(x, s.k_pool, s.v_pool, s.table_dev)
+            sc[i] = PagedTreeSlotC(s.k_pool.data_ptr(), s.v_pool.data_ptr(), s.table_dev.data_ptr(),
+                                   s.table.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)), len(s.table),
+                                   s.k_pool.shape[0], s.len, pos0, nn, par)
+        else:
+            _caches(s.k, s.v, L, Hkv, f"slots[{i}]")
+            _same_device(x, s.k, s.v)
+            sc[i] = TreeSlotC(s.k.data_ptr(), s.v.data_ptr(), s.len, s.k.shape[2], pos0, nn, par)
     lds = 0
     if scores is not None:
         _need(scores, torch.float32, "scores")
@@ -972,32 +1060,62 @@ def luce_decode_step_tree(model: "Model", slots: Sequence[TreeSlot], x, ws, logi
         if stats.numel() != len(model.layers) * T * model.n_q_heads * 2:
             raise ValueError("stats: expected [n_layers][T][Hq][2]")
     _same_device(x, ws, logits, argmax, scores, stats)
+    lib = load_library()
+    fn = lib.luce_decode_step_tree_paged if paged else lib.luce_decode_step_tree
     with torch.cuda.device(x.device):
-        _check(load_library().luce_decode_step_tree(ctypes.byref(model.c), sc, n, x.data_ptr(), _ptr(logits), _ptr(argmax),
-                                                    _ptr(scores), lds, _ptr(stats), ws.data_ptr(), ws.numel(),
-                                                    _stream(stream)))
+        _check(fn(ctypes.byref(model.c), sc, n, x.data_ptr(), _ptr(logits), _ptr(argmax), _ptr(scores), lds, _ptr(stats),
+                  ws.data_ptr(), ws.numel(), _stream(stream)))
     return x
 
 
-def _state(t, dtype, like, name):
+def _caches(k, v, L, Hkv, name):
+    import torch
+    _kv_pair(k, v, 4, name)
+    _need(k, torch.float16, name + ".k")
+    _need(v, torch.float16, name + ".v")
+    if k.shape[:2] != (L, Hkv):
+        raise ValueError(f"{name}: expected caches [{L} layers][{Hkv} KV heads][cap][128]")
+
+
+def _pools(k, v, L, Hkv, name):
+    import torch
+    _kv_pair(k, v, 5, name)
+    _need(k, torch.float16, name + ".k_pool")
+    _need(v, torch.float16, name + ".v_pool")
+    if k.shape[1:4] != (L, Hkv, PAGE_KEYS):
+        raise ValueError(f"{name}: expected pools [n_pages][{L} layers][{Hkv} KV heads][128][128]")
+
+
+def _state(t, dtype, L, Hkv, cap, name):
     _need(t, dtype, name)
-    if t.shape != like.shape[:3]:
-        raise ValueError(f"{name}: expected [n_layers][Hkv][cap] of the cache")
+    if t.dim() != 3 or t.shape[:2] != (L, Hkv) or (cap is not None and t.shape[2] != cap):
+        raise ValueError(f"{name}: expected [{L} layers][{Hkv} KV heads][cap]")
+
+
+def _kind(slots, flat, paged):
+    """Whether the slots are paged ones; they are all of one kind."""
+    if not slots:
+        raise ValueError("slots: expected at least one")
+    is_paged = isinstance(slots[0], paged)
+    if not all(isinstance(s, paged if is_paged else flat) for s in slots):
+        raise TypeError(f"slots: expected {flat.__name__}s or {paged.__name__}s, of one kind")
+    return is_paged
 
 
 class TreeCommit(_Prepared):
-    """luce_tree_commit with its arguments marshalled once: each call takes the
-    slots' current ``len``, ``path``, ``row0`` and ``pos0``.  ``scores``
-    [n_layers][n_rows][Hq][lds] and ``stats`` [n_layers][n_rows][Hq][2] (the
-    n_layers dimension may be left out for one layer) are what
-    luce_tree_attn gave."""
+    """luce_tree_commit (or luce_tree_commit_paged, for PagedCommitSlots) with its
+    arguments marshalled once: each call takes the slots' current ``len``,
+    ``path``, ``row0`` and ``pos0``.  ``scores`` [n_layers][n_rows][Hq][lds] and
+    ``stats`` [n_layers][n_rows][Hq][2] (the n_layers dimension may be left out
+    for one layer) are what luce_tree_attn gave."""
 
     def __init__(self, slots: Sequence[CommitSlot], n_q_heads: int, scores=None, stats=None, stream=None):
+        import numpy as np
         import torch
         self.slots = list(slots)
-        if not self.slots:
-            raise ValueError("slots: expected at least one")
-        L, Hkv = self.slots[0].k.shape[:2]
+        paged = _kind(self.slots, CommitSlot, PagedCommitSlot)
+        first = self.slots[0].k_pool if paged else self.slots[0].k
+        L, Hkv = first.shape[1:3] if paged else first.shape[:2]
         n_rows = lds = 0
         if scores is not None:
             _need(scores, torch.float32, "scores")
@@ -1005,32 +1123,43 @@ class TreeCommit(_Prepared):
             n_rows, hq, lds = scores.shape[-3:]
             if hq != n_q_heads or scores.numel() != L * n_rows * hq * lds or stats.numel() != L * n_rows * hq * 2:
                 raise ValueError("scores, stats: expected [n_layers][n_rows][Hq][lds] and [n_layers][n_rows][Hq][2]")
-        self._sc = (CommitSlotC * len(self.slots))()
+        n = len(self.slots)
+        self._sc = ((PagedCommitSlotC if paged else CommitSlotC) * n)()
+        tables = []
         for i, s in enumerate(self.slots):
-            _kv_pair(s.k, s.v, 4, f"slots[{i}]")
-            _need(s.k, torch.float16, f"slots[{i}].k")
-            _need(s.v, torch.float16, f"slots[{i}].v")
-            if s.k.shape[:2] != (L, Hkv):
-                raise ValueError("slots: expected the same layers and heads in each")
+            if paged:
+                _pools(s.k_pool, s.v_pool, L, Hkv, f"slots[{i}]")
+                k, v, cap = s.k_pool, s.v_pool, next((t.shape[-1] for t in (s.acc, s.pos) if t is not None), MAX_KEYS)
+            else:
+                _caches(s.k, s.v, L, Hkv, f"slots[{i}]")
+                k, v, cap = s.k, s.v, s.k.shape[2]
             if s.acc is not None:
-                _state(s.acc, torch.float32, s.k, f"slots[{i}].acc")
+                _state(s.acc, torch.float32, L, Hkv, cap, f"slots[{i}].acc")
             if s.pos is not None:
-                _state(s.pos, torch.int32, s.k, f"slots[{i}].pos")
-            _same_device(self.slots[0].k, s.k, s.v, s.acc, s.pos, scores, stats)
-            self._sc[i] = CommitSlotC(s.k.data_ptr(), s.v.data_ptr(), s.len, s.k.shape[2], 0, s.row0, None, _ptr(s.acc),
-                                      _ptr(s.pos), s.pos0)
-        self._now = [None] * len(self.slots)
-        self._arrays = [None] * len(self.slots)
-        self._args = (self._sc, len(self.slots), L, int(n_q_heads), Hkv, HEAD_DIM, _ptr(scores), n_rows, lds, _ptr(stats))
-        self._bind(load_library().luce_tree_commit, self.slots[0].k.device, stream, (scores, stats))
+                _state(s.pos, torch.int32, L, Hkv, cap, f"slots[{i}].pos")
+            _same_device(first, k, v, s.acc, s.pos, scores, stats)
+            if paged:
+                table = np.ascontiguousarray(s.table, dtype=np.int32)
+                tables.append(table)
+                self._sc[i] = PagedCommitSlotC(k.data_ptr(), v.data_ptr(),
+                                               table.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)), len(table),
+                                               k.shape[0], s.len, cap, 0, s.row0, None, _ptr(s.acc), _ptr(s.pos), s.pos0)
+            else:
+                self._sc[i] = CommitSlotC(k.data_ptr(), v.data_ptr(), s.len, cap, 0, s.row0, None, _ptr(s.acc),
+                                          _ptr(s.pos), s.pos0)
+        self._items = [self._sc[i] for i in range(n)]
+        self._now, self._arrays = [None] * n, [None] * n
+        self._args = (self._sc, n, L, int(n_q_heads), Hkv, HEAD_DIM, _ptr(scores), n_rows, lds, _ptr(stats))
+        lib = load_library()
+        self._bind(lib.luce_tree_commit_paged if paged else lib.luce_tree_commit, first.device, stream,
+                   (scores, stats, tables))
 
     def __call__(self):
         for i, s in enumerate(self.slots):
             now = (s.len, s.row0, s.pos0, *s.path)
             if now != self._now[i]:
-                path = now[3:]
+                path, c = now[3:], self._items[i]
                 self._arrays[i] = (ctypes.c_int32 * max(1, len(path)))(*path)
-                c = self._sc[i]
                 c.len, c.row0, c.pos0, c.path, c.n_path = s.len, s.row0, s.pos0, self._arrays[i], len(path)
                 self._now[i] = now
         self._call(*self._args)
@@ -1044,40 +1173,55 @@ def luce_tree_commit(slots: Sequence[CommitSlot], n_q_heads: int, scores=None, s
 
 
 class KvEvict(_Prepared):
-    """luce_kv_evict with its arguments marshalled once: each call takes the
-    slots' current ``len`` and ``next_pos``."""
+    """luce_kv_evict (or luce_kv_evict_paged, for PagedEvictSlots) with its
+    arguments marshalled once: each call takes the slots' current ``len`` and
+    ``next_pos``."""
 
     def __init__(self, slots: Sequence[EvictSlot], stream=None):
         import torch
         self.slots = list(slots)
-        if not self.slots:
-            raise ValueError("slots: expected at least one")
-        L, Hkv = self.slots[0].k.shape[:2]
-        self._sc = (EvictSlotC * len(self.slots))()
+        paged = _kind(self.slots, EvictSlot, PagedEvictSlot)
+        first = self.slots[0].k_pool if paged else self.slots[0].k
+        L, Hkv = first.shape[1:3] if paged else first.shape[:2]
+        n = len(self.slots)
+        self._sc = ((PagedEvictSlotC if paged else EvictSlotC) * n)()
         for i, s in enumerate(self.slots):
-            _kv_pair(s.k, s.v, 4, f"slots[{i}]")
-            _need(s.k, torch.float16, f"slots[{i}].k")
-            _need(s.v, torch.float16, f"slots[{i}].v")
-            if s.k.shape[:2] != (L, Hkv):
-                raise ValueError("slots: expected the same layers and heads in each")
+            if paged:
+                _pools(s.k_pool, s.v_pool, L, Hkv, f"slots[{i}]")
+                _need(s.table, torch.int32, f"slots[{i}].table")
+                k, v, cap = s.k_pool, s.v_pool, s.acc.shape[-1]
+                if s.table.numel() * PAGE_KEYS < min(s.len, cap):
+                    raise ValueError(f"slots[{i}].table: {s.table.numel()} pages do not hold {s.len} keys")
+            else:
+                _caches(s.k, s.v, L, Hkv, f"slots[{i}]")
+                k, v, cap = s.k, s.v, s.k.shape[2]
             acc_out = s.acc if s.acc_out is None else s.acc_out
             pos_out = s.pos if s.pos_out is None else s.pos_out
             for t, dt, w in ((s.acc, torch.float32, "acc"), (acc_out, torch.float32, "acc_out"),
                              (s.pos, torch.int32, "pos"), (pos_out, torch.int32, "pos_out")):
-                _state(t, dt, s.k, f"slots[{i}].{w}")
-            _same_device(self.slots[0].k, s.k, s.v, s.acc, s.pos, acc_out, pos_out)
-            self._sc[i] = EvictSlotC(s.k.data_ptr(), s.v.data_ptr(), s.acc.data_ptr(), s.pos.data_ptr(),
-                                     acc_out.data_ptr(), pos_out.data_ptr(), s.len, s.k.shape[2], s.budget, s.sinks,
-                                     s.recent, s.next_pos)
-        self._now = [None] * len(self.slots)
-        self._args = (self._sc, len(self.slots), L, Hkv, HEAD_DIM)
-        self._bind(load_library().luce_kv_evict, self.slots[0].k.device, stream, None)
+                _state(t, dt, L, Hkv, cap, f"slots[{i}].{w}")
+            _same_device(first, k, v, s.acc, s.pos, acc_out, pos_out, s.table if paged else None)
+            if paged:
+                self._sc[i] = PagedEvictSlotC(k.data_ptr(), v.data_ptr(), s.table.data_ptr(), s.acc.data_ptr(),
+                                              s.pos.data_ptr(), acc_out.data_ptr(), pos_out.data_ptr(), k.shape[0], s.len,
+                                              cap, s.budget, s.sinks, s.recent, s.next_pos)
+            else:
+                self._sc[i] = EvictSlotC(k.data_ptr(), v.data_ptr(), s.acc.data_ptr(), s.pos.data_ptr(),
+                                         acc_out.data_ptr(), pos_out.data_ptr(), s.len, cap, s.budget, s.sinks, s.recent,
+                                         s.next_pos)
+        self._items, self._now = [self._sc[i] for i in range(n)], [None] * n
+        self._pages = [s.table.numel() * PAGE_KEYS if paged else None for s in self.slots]
+        self._args = (self._sc, n, L, Hkv, HEAD_DIM)
+        lib = load_library()
+        self._bind(lib.luce_kv_evict_paged if paged else lib.luce_kv_evict, first.device, stream, None)
 
     def __call__(self):
         for i, s in enumerate(self.slots):
             now = (s.len, s.next_pos)
             if now != self._now[i]:
-                self._sc[i].len, self._sc[i].next_pos = now
+                if self._pages[i] is not None and s.len > self._pages[i]:
+                    raise ValueError(f"slots[{i}].table does not hold {s.len} keys")
+                self._items[i].len, self._items[i].next_pos = now
                 self._now[i] = now
         self._call(*self._args)
 

@@ -890,12 +890,12 @@ int luce_decode_step(const luce_model* m, const luce_slot* slots, const int32_t*
     return decode_step_impl(m, ss, rows_per_slot, n_seq, x, logits, argmax, ws, ws_bytes, stream, who);
 }
 
-int luce_decode_step_tree(const luce_model* m, const luce_tree_slot* slots, int n_seq, float* x, float* logits,
-                          int32_t* argmax, float* scores, int64_t lds, float* stats, void* ws, size_t ws_bytes,
-                          void* stream)
+// The checks of a step over draft trees that do not depend on how the cache is
+// laid out.
+static int check_tree_step(const luce_model* m, const void* slots, int n_seq, const float* scores, int64_t lds,
+                           const float* stats, const char* who)
 {
-    const char* who = "decode_step_tree";
-    int rc = check_model(m, who);
+    const int rc = check_model(m, who);
     if (rc) return rc;
     REQUIRE(slots, LUCE_EINVAL, "%s: null slots", who);
     REQUIRE(n_seq >= 1 && n_seq <= LUCE_MAX_SEQ, LUCE_EINVAL,
@@ -904,6 +904,54 @@ int luce_decode_step_tree(const luce_model* m, const luce_tree_slot* slots, int 
     REQUIRE(!scores || (aligned(scores, 16) && lds >= 1 && lds % 4 == 0 && lds < ((int64_t)1 << 31)), LUCE_EINVAL,
             "%s: scores must be 16-byte aligned and lds=%lld a positive multiple of 4", who, (long long)lds);
     REQUIRE(aligned(stats, 8), LUCE_EINVAL, "%s: stats must be 8-byte aligned", who);
+    return LUCE_OK;
+}
+
+// Slot s's tree and sizes; *T counts the rows so far.
+static int add_tree_slot(StepTree& tree, int32_t* rows, int s, int len, int pos0, int n_nodes, const int32_t* parent,
+                         const float* scores, int64_t lds, int* T, const char* who)
+{
+    REQUIRE(n_nodes >= 1 && n_nodes <= LUCE_MAX_ROWS - *T, LUCE_EINVAL, "%s: slot %d has %d nodes (at least 1, %d in all)",
+            who, s, n_nodes, LUCE_MAX_ROWS);
+    REQUIRE(len >= 0, LUCE_EINVAL, "%s: slot %d len=%d", who, s, len);
+    REQUIRE(len <= kMaxKeys - n_nodes, LUCE_EUNSUPPORTED, "%s: slot %d would hold %d + %d keys (at most %d)", who, s, len,
+            n_nodes, kMaxKeys);
+    REQUIRE(pos0 >= 0 && pos0 <= INT32_MAX - LUCE_MAX_TREE, LUCE_EINVAL, "%s: slot %d pos0=%d", who, s, pos0);
+    REQUIRE(!scores || lds >= len + n_nodes, LUCE_EINVAL, "%s: lds=%lld < the %d keys of slot %d", who, (long long)lds,
+            len + n_nodes, s);
+    const int rc = tree_path(parent, n_nodes, tree.batch.row, s, *T, who);
+    if (rc) return rc;
+    tree.batch.view[s].len = len;
+    tree.batch.view[s].n_nodes = n_nodes;
+    tree.batch.view[s].row0 = *T;
+    tree.batch.view[s].tok_stride = LUCE_HEAD_DIM;
+    tree.batch.n_view = s + 1;
+    tree.pos0[s] = pos0;
+    rows[s] = n_nodes;
+    *T += n_nodes;
+    tree.batch.n_row = *T;
+    return LUCE_OK;
+}
+
+static int run_tree_step(const luce_model* m, const StepSlot* ss, StepTree& tree, const int32_t* rows, int n_seq, float* x,
+                         float* logits, int32_t* argmax, float* scores, int64_t lds, float* stats, void* ws,
+                         size_t ws_bytes, void* stream, const char* who)
+{
+    tree_chunks(tree.batch, m->n_q_heads, m->n_kv_heads);
+    tree.scores = scores;
+    tree.lds = lds;
+    tree.stats = stats;
+    return decode_step_impl(m, ss, rows, n_seq, x, logits, argmax, ws, ws_bytes, stream, who,
+                            HostIO{nullptr, nullptr, nullptr}, &tree);
+}
+
+int luce_decode_step_tree(const luce_model* m, const luce_tree_slot* slots, int n_seq, float* x, float* logits,
+                          int32_t* argmax, float* scores, int64_t lds, float* stats, void* ws, size_t ws_bytes,
+                          void* stream)
+{
+    const char* who = "decode_step_tree";
+    int rc = check_tree_step(m, slots, n_seq, scores, lds, stats, who);
+    if (rc) return rc;
     StepSlot ss[LUCE_MAX_SEQ];
     StepTree tree{};
     int32_t rows[LUCE_MAX_SEQ];
@@ -914,30 +962,16 @@ int luce_decode_step_tree(const luce_model* m, const luce_tree_slot* slots, int 
         const luce_tree_slot& sl = slots[s];
         REQUIRE(sl.k && sl.v && aligned(sl.k, 16) && aligned(sl.v, 16), LUCE_EINVAL,
                 "%s: slot %d cache null or not 16-byte aligned", who, s);
-        REQUIRE(sl.n_nodes >= 1 && sl.n_nodes <= LUCE_MAX_TREE - T, LUCE_EINVAL,
-                "%s: slot %d has %d nodes (at least 1, %d in all)", who, s, sl.n_nodes, LUCE_MAX_ROWS);
-        REQUIRE(sl.len >= 0 && sl.cap >= 1 && (int64_t)sl.len + sl.n_nodes <= sl.cap, LUCE_EINVAL,
-                "%s: slot %d len=%d + nodes=%d exceeds cap=%d", who, s, sl.len, sl.n_nodes, sl.cap);
-        REQUIRE(sl.len <= kMaxKeys - sl.n_nodes, LUCE_EUNSUPPORTED, "%s: slot %d would hold %d keys (at most %d)", who, s,
-                sl.len + sl.n_nodes, kMaxKeys);
-        REQUIRE(sl.pos0 >= 0 && sl.pos0 <= INT32_MAX - LUCE_MAX_TREE, LUCE_EINVAL, "%s: slot %d pos0=%d", who, s, sl.pos0);
-        REQUIRE(!scores || lds >= sl.len + sl.n_nodes, LUCE_EINVAL, "%s: lds=%lld < the %d keys of slot %d", who,
-                (long long)lds, sl.len + sl.n_nodes, s);
-        if ((rc = tree_path(sl.parent, sl.n_nodes, tree.batch.row, s, T, who))) return rc;
+        if ((rc = add_tree_slot(tree, rows, s, sl.len, sl.pos0, sl.n_nodes, sl.parent, scores, lds, &T, who))) return rc;
+        REQUIRE(sl.cap >= 1 && sl.len + sl.n_nodes <= sl.cap, LUCE_EINVAL, "%s: slot %d len=%d + nodes=%d exceeds cap=%d",
+                who, s, sl.len, sl.n_nodes, sl.cap);
         TreeView& v = tree.batch.view[s];
-        v.tok_stride = LUCE_HEAD_DIM;
         v.head_stride = (int64_t)sl.cap * LUCE_HEAD_DIM;
         v.page_stride = v.head_stride * m->n_kv_heads;
         v.n_pages = 1;
         v.cap = sl.cap;
-        v.len = sl.len;
-        v.n_nodes = sl.n_nodes;
-        v.row0 = T;
         ss[s] = StepSlot{reinterpret_cast<__half*>(sl.k), reinterpret_cast<__half*>(sl.v), sl.len, sl.cap, nullptr,
                          nullptr};
-        tree.pos0[s] = sl.pos0;
-        rows[s] = sl.n_nodes;
-        T += sl.n_nodes;
         const uintptr_t bytes = (uintptr_t)(heads * sl.cap * LUCE_HEAD_DIM * 2);
         r[2 * s] = ByteRange{(uintptr_t)sl.k, (uintptr_t)sl.k + bytes, s, "K cache", true, 0};
         r[2 * s + 1] = ByteRange{(uintptr_t)sl.v, (uintptr_t)sl.v + bytes, s, "V cache", true, 0};
@@ -947,14 +981,7 @@ int luce_decode_step_tree(const luce_model* m, const luce_tree_slot* slots, int 
     if (scores) r[nr++] = ByteRange{(uintptr_t)scores, (uintptr_t)scores + out_rows * lds * 4, -1, "scores", true, 0};
     if (stats) r[nr++] = ByteRange{(uintptr_t)stats, (uintptr_t)stats + out_rows * 8, -1, "stats", true, 0};
     if ((rc = check_apart(r, nr, who))) return rc;
-    tree.batch.n_view = n_seq;
-    tree.batch.n_row = T;
-    tree_chunks(tree.batch, m->n_q_heads, m->n_kv_heads);
-    tree.scores = scores;
-    tree.lds = lds;
-    tree.stats = stats;
-    return decode_step_impl(m, ss, rows, n_seq, x, logits, argmax, ws, ws_bytes, stream, who,
-                            HostIO{nullptr, nullptr, nullptr}, &tree);
+    return run_tree_step(m, ss, tree, rows, n_seq, x, logits, argmax, scores, lds, stats, ws, ws_bytes, stream, who);
 }
 
 int luce_decode_step_host(const luce_model* m, const luce_slot* slots, const int32_t* rows_per_slot, int n_seq,
@@ -1236,20 +1263,12 @@ int luce_step_graph_destroy(luce_step_graph* g)
     return ok();
 }
 
-int luce_decode_step_paged(const luce_model* m, const luce_paged_slot* slots, const int32_t* rows_per_slot,
-                           int n_seq, float* x, float* logits, int32_t* argmax, void* ws, size_t ws_bytes,
-                           void* stream)
+// Validates paged slots into ss; LUCE_OK or the refusal.
+static int paged_slots(const luce_paged_slot* slots, const int32_t* rows_per_slot, int n_seq, StepSlot* ss,
+                       const char* who)
 {
-    const char* who = "decode_step_paged";
-    int rc = check_model(m, who);
-    if (rc) return rc;
-    REQUIRE(slots && rows_per_slot, LUCE_EINVAL, "%s: null slots/rows", who);
-    REQUIRE(n_seq >= 1 && n_seq <= LUCE_MAX_SEQ, LUCE_EINVAL,
-            "%s: n_seq=%d outside 1..%d (more than %d slots are refused)", who, n_seq, LUCE_MAX_SEQ, LUCE_MAX_SEQ);
-    StepSlot ss[LUCE_MAX_SEQ];
     for (int s = 0; s < n_seq; ++s) {
         const luce_paged_slot& sl = slots[s];
-        if ((rc = check_rows(rows_per_slot, s, who))) return rc;
         const int n = rows_per_slot[s];
         REQUIRE(sl.k_pool && sl.v_pool && aligned(sl.k_pool, 16) && aligned(sl.v_pool, 16), LUCE_EINVAL,
                 "%s: slot %d pool null or not 16-byte aligned", who, s);
@@ -1280,7 +1299,52 @@ int luce_decode_step_paged(const luce_model* m, const luce_paged_slot* slots, co
                             a.table_host[pg], s, o);
             }
     }
+    return LUCE_OK;
+}
+
+int luce_decode_step_paged(const luce_model* m, const luce_paged_slot* slots, const int32_t* rows_per_slot,
+                           int n_seq, float* x, float* logits, int32_t* argmax, void* ws, size_t ws_bytes,
+                           void* stream)
+{
+    const char* who = "decode_step_paged";
+    int rc = check_model(m, who);
+    if (rc) return rc;
+    REQUIRE(slots && rows_per_slot, LUCE_EINVAL, "%s: null slots/rows", who);
+    REQUIRE(n_seq >= 1 && n_seq <= LUCE_MAX_SEQ, LUCE_EINVAL,
+            "%s: n_seq=%d outside 1..%d (more than %d slots are refused)", who, n_seq, LUCE_MAX_SEQ, LUCE_MAX_SEQ);
+    StepSlot ss[LUCE_MAX_SEQ];
+    for (int s = 0; s < n_seq; ++s)
+        if ((rc = check_rows(rows_per_slot, s, who))) return rc;
+    if ((rc = paged_slots(slots, rows_per_slot, n_seq, ss, who))) return rc;
     return decode_step_impl(m, ss, rows_per_slot, n_seq, x, logits, argmax, ws, ws_bytes, stream, who);
+}
+
+int luce_decode_step_tree_paged(const luce_model* m, const luce_paged_tree_slot* slots, int n_seq, float* x,
+                                float* logits, int32_t* argmax, float* scores, int64_t lds, float* stats, void* ws,
+                                size_t ws_bytes, void* stream)
+{
+    const char* who = "decode_step_tree_paged";
+    int rc = check_tree_step(m, slots, n_seq, scores, lds, stats, who);
+    if (rc) return rc;
+    StepSlot ss[LUCE_MAX_SEQ];
+    StepTree tree{};
+    int32_t rows[LUCE_MAX_SEQ];
+    luce_paged_slot ps[LUCE_MAX_SEQ];
+    int T = 0;
+    for (int s = 0; s < n_seq; ++s) {
+        const luce_paged_tree_slot& sl = slots[s];
+        if ((rc = add_tree_slot(tree, rows, s, sl.len, sl.pos0, sl.n_nodes, sl.parent, scores, lds, &T, who))) return rc;
+        REQUIRE(sl.k_pool != sl.v_pool, LUCE_EINVAL, "%s: slot %d has one pool for K and V", who, s);
+        ps[s] = luce_paged_slot{sl.k_pool, sl.v_pool, sl.table, sl.table_host, sl.n_table, sl.n_pages, sl.len};
+        TreeView& v = tree.batch.view[s];
+        v.head_stride = (int64_t)kPageKeys * LUCE_HEAD_DIM;
+        v.page_stride = (int64_t)m->n_layers * m->n_kv_heads * v.head_stride;
+        v.n_pages = sl.n_pages;
+        v.cap = kPageKeys;
+        v.pages = sl.table;
+    }
+    if ((rc = paged_slots(ps, rows, n_seq, ss, who))) return rc;
+    return run_tree_step(m, ss, tree, rows, n_seq, x, logits, argmax, scores, lds, stats, ws, ws_bytes, stream, who);
 }
 
 }  // extern "C"

@@ -204,62 +204,69 @@ static int check_layers(int n_seq, int n_layers, int Hkv, int D, const void* slo
 
 // ------------------------------------------------------------ commit
 
-int luce_tree_commit(const luce_commit_slot* slots, int n_seq, int n_layers, int Hq, int Hkv, int D,
-                     const float* scores, int n_rows, int64_t lds, const float* stats, void* stream)
+namespace {
+
+// What a commit's flat and paged slots share, entered into the batch.
+struct CommitArgs {
+    int len, cap, n_path, row0;
+    const int32_t* path;
+    float* acc;
+    int32_t* pos;
+    int pos0;
+};
+
+}  // namespace
+
+static int check_commit_call(int n_seq, int n_layers, int Hq, int Hkv, int D, const void* slots, const char* who)
 {
-    const char* who = "tree_commit";
-    int rc = check_layers(n_seq, n_layers, Hkv, D, slots, who);
+    const int rc = check_layers(n_seq, n_layers, Hkv, D, slots, who);
     if (rc) return rc;
     REQUIRE(Hq >= Hkv && Hq % Hkv == 0, LUCE_EINVAL, "%s: Hq=%d must be a multiple of Hkv=%d", who, Hq, Hkv);
     REQUIRE(Hq / Hkv <= 8, LUCE_EUNSUPPORTED, "%s: group size %d > 8", who, Hq / Hkv);
-    CommitBatch b{};
-    b.n_slot = n_seq;
-    ByteRange r[4 * LUCE_MAX_SEQ + 2];
-    int nr = 0;
-    bool any_acc = false, any = false;
-    const int64_t heads = (int64_t)n_layers * Hkv;
-    for (int s = 0; s < n_seq; ++s) {
-        const luce_commit_slot& c = slots[s];
-        REQUIRE(c.k && c.v && aligned(c.k, 16) && aligned(c.v, 16), LUCE_EINVAL,
-                "%s: slot %d cache null or not 16-byte aligned", who, s);
-        REQUIRE(aligned(c.acc, 4) && aligned(c.pos, 4), LUCE_EINVAL, "%s: slot %d acc or pos misaligned", who, s);
-        REQUIRE(c.n_path >= 0 && c.n_path <= LUCE_MAX_TREE, LUCE_EINVAL, "%s: slot %d n_path=%d outside 0..%d", who, s,
-                c.n_path, LUCE_MAX_TREE);
-        REQUIRE(c.n_path == 0 || c.path, LUCE_EINVAL, "%s: slot %d has a null path", who, s);
-        REQUIRE(c.len >= 0 && c.cap >= 1 && c.len <= c.cap, LUCE_EINVAL, "%s: slot %d len=%d outside [0, cap=%d]", who, s,
-                c.len, c.cap);
-        REQUIRE(c.pos0 >= 0 && c.pos0 <= INT32_MAX - LUCE_MAX_TREE, LUCE_EINVAL, "%s: slot %d pos0=%d", who, s, c.pos0);
-        int last = -1;
-        for (int i = 0; i < c.n_path; ++i) {
-            REQUIRE(c.path[i] > last && c.path[i] < LUCE_MAX_TREE && (int64_t)c.len + c.path[i] < c.cap, LUCE_EINVAL,
-                    "%s: slot %d path[%d]=%d must ascend, below %d and within the cache", who, s, i, c.path[i],
-                    LUCE_MAX_TREE);
-            last = c.path[i];
-            b.slot[s].path[i] = (uint8_t)last;
-        }
-        if (c.acc && c.n_path > 0) {
-            any_acc = true;
-            REQUIRE(scores && stats, LUCE_EINVAL, "%s: slot %d has acc, but scores or stats is null", who, s);
-            REQUIRE(c.row0 >= 0 && (int64_t)c.row0 + last < n_rows, LUCE_EINVAL,
-                    "%s: slot %d rows %d + %d outside the %d score rows", who, s, c.row0, last, n_rows);
-            REQUIRE(lds > (int64_t)c.len + last, LUCE_EINVAL, "%s: lds=%lld does not reach slot %d's key %d", who,
-                    (long long)lds, s, c.len + last);
-        }
-        any = any || c.n_path > 0;
-        b.slot[s].k = reinterpret_cast<__half*>(c.k);
-        b.slot[s].v = reinterpret_cast<__half*>(c.v);
-        b.slot[s].acc = c.acc;
-        b.slot[s].pos = c.pos;
-        b.slot[s].len = c.len;
-        b.slot[s].cap = c.cap;
-        b.slot[s].row0 = c.row0;
-        b.slot[s].pos0 = c.pos0;
-        b.slot[s].n_path = c.n_path;
-        r[nr++] = range_of(c.k, heads * c.cap * D * 2, s, "K cache", true);
-        r[nr++] = range_of(c.v, heads * c.cap * D * 2, s, "V cache", true);
-        if (c.acc) r[nr++] = range_of(c.acc, heads * c.cap * 4, s, "acc", true);
-        if (c.pos) r[nr++] = range_of(c.pos, heads * c.cap * 4, s, "pos", true);
+    return LUCE_OK;
+}
+
+static int add_commit_slot(CommitSlot& o, const CommitArgs& c, int s, int64_t heads, const float* scores, int n_rows,
+                           int64_t lds, const float* stats, ByteRange* r, int* nr, bool* any_acc, const char* who)
+{
+    REQUIRE(aligned(c.acc, 4) && aligned(c.pos, 4), LUCE_EINVAL, "%s: slot %d acc or pos misaligned", who, s);
+    REQUIRE(c.n_path >= 0 && c.n_path <= LUCE_MAX_TREE, LUCE_EINVAL, "%s: slot %d n_path=%d outside 0..%d", who, s,
+            c.n_path, LUCE_MAX_TREE);
+    REQUIRE(c.n_path == 0 || c.path, LUCE_EINVAL, "%s: slot %d has a null path", who, s);
+    REQUIRE(c.len >= 0 && c.cap >= 1 && c.len <= c.cap, LUCE_EINVAL, "%s: slot %d len=%d outside [0, cap=%d]", who, s,
+            c.len, c.cap);
+    REQUIRE(c.pos0 >= 0 && c.pos0 <= INT32_MAX - LUCE_MAX_TREE, LUCE_EINVAL, "%s: slot %d pos0=%d", who, s, c.pos0);
+    int last = -1;
+    for (int i = 0; i < c.n_path; ++i) {
+        REQUIRE(c.path[i] > last && c.path[i] < LUCE_MAX_TREE && (int64_t)c.len + c.path[i] < c.cap, LUCE_EINVAL,
+                "%s: slot %d path[%d]=%d must ascend, below %d and within the cache", who, s, i, c.path[i],
+                LUCE_MAX_TREE);
+        last = c.path[i];
+        o.path[i] = (uint8_t)last;
     }
+    if (c.acc && c.n_path > 0) {
+        *any_acc = true;
+        REQUIRE(scores && stats, LUCE_EINVAL, "%s: slot %d has acc, but scores or stats is null", who, s);
+        REQUIRE(c.row0 >= 0 && (int64_t)c.row0 + last < n_rows, LUCE_EINVAL,
+                "%s: slot %d rows %d + %d outside the %d score rows", who, s, c.row0, last, n_rows);
+        REQUIRE(lds > (int64_t)c.len + last, LUCE_EINVAL, "%s: lds=%lld does not reach slot %d's key %d", who,
+                (long long)lds, s, c.len + last);
+    }
+    o.acc = c.acc;
+    o.pos = c.pos;
+    o.len = c.len;
+    o.cap = c.cap;
+    o.row0 = c.row0;
+    o.pos0 = c.pos0;
+    o.n_path = c.n_path;
+    if (c.acc) r[(*nr)++] = range_of(c.acc, heads * c.cap * 4, s, "acc", true);
+    if (c.pos) r[(*nr)++] = range_of(c.pos, heads * c.cap * 4, s, "pos", true);
+    return LUCE_OK;
+}
+
+static int run_commit(const CommitBatch& b, int n_layers, int Hq, int Hkv, const float* scores, int n_rows, int64_t lds,
+                      const float* stats, ByteRange* r, int nr, bool any_acc, void* stream, const char* who)
+{
     if (any_acc) {
         REQUIRE(n_rows >= 1 && n_rows <= LUCE_MAX_ROWS, LUCE_EINVAL, "%s: n_rows=%d outside 1..%d", who, n_rows,
                 LUCE_MAX_ROWS);
@@ -268,12 +275,136 @@ int luce_tree_commit(const luce_commit_slot* slots, int n_seq, int n_layers, int
         r[nr++] = range_of(scores, (int64_t)n_layers * n_rows * Hq * lds * 4, -1, "scores", false);
         r[nr++] = range_of(stats, (int64_t)n_layers * n_rows * Hq * 8, -1, "stats", false);
     }
-    if ((rc = check_apart(r, nr, who))) return rc;
+    const int rc = check_apart(r, nr, who);
+    if (rc) return rc;
+    bool any = false;
+    for (int s = 0; s < b.n_slot; ++s) any = any || b.slot[s].n_path > 0;
     if (!any) return ok();
     return cuda_status(launch_tree_commit(b, n_layers, Hq, Hkv, scores, n_rows, lds, stats, (cudaStream_t)stream), who);
 }
 
+int luce_tree_commit(const luce_commit_slot* slots, int n_seq, int n_layers, int Hq, int Hkv, int D,
+                     const float* scores, int n_rows, int64_t lds, const float* stats, void* stream)
+{
+    const char* who = "tree_commit";
+    int rc = check_commit_call(n_seq, n_layers, Hq, Hkv, D, slots, who);
+    if (rc) return rc;
+    CommitBatch b{};
+    b.n_slot = n_seq;
+    ByteRange r[4 * LUCE_MAX_SEQ + 2];
+    int nr = 0;
+    bool any_acc = false;
+    const int64_t heads = (int64_t)n_layers * Hkv;
+    for (int s = 0; s < n_seq; ++s) {
+        const luce_commit_slot& c = slots[s];
+        REQUIRE(c.k && c.v && aligned(c.k, 16) && aligned(c.v, 16), LUCE_EINVAL,
+                "%s: slot %d cache null or not 16-byte aligned", who, s);
+        const CommitArgs a{c.len, c.cap, c.n_path, c.row0, c.path, c.acc, c.pos, c.pos0};
+        CommitSlot& o = b.slot[s];
+        if ((rc = add_commit_slot(o, a, s, heads, scores, n_rows, lds, stats, r, &nr, &any_acc, who))) return rc;
+        o.k = reinterpret_cast<__half*>(c.k);
+        o.v = reinterpret_cast<__half*>(c.v);
+        o.head_step = (int64_t)c.cap * D;
+        for (int i = 0; i < c.n_path; ++i) {
+            o.from[i] = (int64_t)(c.len + c.path[i]) * D;
+            o.to[i] = (int64_t)(c.len + i) * D;
+        }
+        r[nr++] = range_of(c.k, heads * c.cap * D * 2, s, "K cache", true);
+        r[nr++] = range_of(c.v, heads * c.cap * D * 2, s, "V cache", true);
+    }
+    return run_commit(b, n_layers, Hq, Hkv, scores, n_rows, lds, stats, r, nr, any_acc, stream, who);
+}
+
+int luce_tree_commit_paged(const luce_paged_commit_slot* slots, int n_seq, int n_layers, int Hq, int Hkv, int D,
+                           const float* scores, int n_rows, int64_t lds, const float* stats, void* stream)
+{
+    const char* who = "tree_commit_paged";
+    int rc = check_commit_call(n_seq, n_layers, Hq, Hkv, D, slots, who);
+    if (rc) return rc;
+    CommitBatch b{};
+    b.n_slot = n_seq;
+    ByteRange r[2 * LUCE_MAX_SEQ + 2];
+    int nr = 0;
+    bool any_acc = false;
+    const int64_t heads = (int64_t)n_layers * Hkv, page = heads * LUCE_PAGE_KEYS * D;
+    for (int s = 0; s < n_seq; ++s) {
+        const luce_paged_commit_slot& c = slots[s];
+        REQUIRE(c.k_pool && c.v_pool && aligned(c.k_pool, 16) && aligned(c.v_pool, 16), LUCE_EINVAL,
+                "%s: slot %d pool null or not 16-byte aligned", who, s);
+        REQUIRE(c.k_pool != c.v_pool, LUCE_EINVAL, "%s: slot %d has one pool for K and V", who, s);
+        REQUIRE(c.n_pages >= 1 && c.n_table >= 0 && (c.table_host || c.n_path == 0), LUCE_EINVAL,
+                "%s: slot %d has no pages or no table", who, s);
+        const CommitArgs a{c.len, c.cap, c.n_path, c.row0, c.path, c.acc, c.pos, c.pos0};
+        CommitSlot& o = b.slot[s];
+        if ((rc = add_commit_slot(o, a, s, heads, scores, n_rows, lds, stats, r, &nr, &any_acc, who))) return rc;
+        o.k = reinterpret_cast<__half*>(c.k_pool);
+        o.v = reinterpret_cast<__half*>(c.v_pool);
+        o.head_step = (int64_t)LUCE_PAGE_KEYS * D;
+        for (int i = 0; i < c.n_path; ++i)
+            for (int to = 0; to < 2; ++to) {
+                const int key = c.len + (to ? i : c.path[i]), at = key / LUCE_PAGE_KEYS;
+                REQUIRE(at < c.n_table && c.table_host[at] >= 0 && c.table_host[at] < c.n_pages, LUCE_EINVAL,
+                        "%s: slot %d key %d has no page in [0, %d)", who, s, key, c.n_pages);
+                (to ? o.to : o.from)[i] = c.table_host[at] * page + (int64_t)(key % LUCE_PAGE_KEYS) * D;
+            }
+    }
+    // a row that one slot writes is no other slot's row
+    for (int s = 0; s < n_seq; ++s)
+        for (int t = 0; t < n_seq; ++t)
+            for (int i = 0; i < b.slot[s].n_path && s != t; ++i)
+                for (int j = 0; j < b.slot[t].n_path; ++j)
+                    REQUIRE((b.slot[s].k != b.slot[t].k && b.slot[s].v != b.slot[t].v) ||
+                                (b.slot[s].to[i] != b.slot[t].to[j] && b.slot[s].to[i] != b.slot[t].from[j]),
+                            LUCE_EINVAL, "%s: slots %d and %d share a row", who, s, t);
+    return run_commit(b, n_layers, Hq, Hkv, scores, n_rows, lds, stats, r, nr, any_acc, stream, who);
+}
+
 // ------------------------------------------------------------ eviction
+
+namespace {
+
+struct EvictArgs {
+    const float* acc;
+    const int32_t* pos;
+    float* acc_out;
+    int32_t* pos_out;
+    int len, cap, budget, sinks, recent, next_pos;
+};
+
+}  // namespace
+
+static int add_evict_slot(EvictSlot& o, const EvictArgs& e, int s, int64_t heads, ByteRange* r, int* nr, bool* any,
+                          const char* who)
+{
+    REQUIRE(e.acc && e.pos && e.acc_out && e.pos_out && aligned(e.acc, 4) && aligned(e.pos, 4) && aligned(e.acc_out, 4) &&
+                aligned(e.pos_out, 4),
+            LUCE_EINVAL, "%s: slot %d acc or pos null or misaligned", who, s);
+    REQUIRE(e.cap >= 1 && e.len >= 0 && e.len <= e.cap, LUCE_EINVAL, "%s: slot %d len=%d outside [0, cap=%d]", who, s, e.len,
+            e.cap);
+    REQUIRE(e.len <= LUCE_MAX_KEYS, LUCE_EUNSUPPORTED, "%s: slot %d has %d keys (at most %d)", who, s, e.len,
+            LUCE_MAX_KEYS);
+    REQUIRE(e.budget >= 1 && e.sinks >= 0 && e.recent >= 0 && (int64_t)e.sinks + e.recent <= e.budget, LUCE_EINVAL,
+            "%s: slot %d needs 1 <= budget and sinks + recent <= budget (%d, %d, %d)", who, s, e.budget, e.sinks,
+            e.recent);
+    REQUIRE(e.next_pos >= 0, LUCE_EINVAL, "%s: slot %d next_pos=%d", who, s, e.next_pos);
+    o.acc = e.acc;
+    o.pos = e.pos;
+    o.acc_out = e.acc_out;
+    o.pos_out = e.pos_out;
+    o.len = e.len;
+    o.cap = e.cap;
+    o.budget = e.budget;
+    o.sinks = e.sinks;
+    o.recent = e.recent;
+    o.next_pos = e.next_pos;
+    const bool copies = e.acc_out != e.acc || e.pos_out != e.pos;
+    *any = *any || e.len > e.budget || (copies && e.len > 0);
+    r[(*nr)++] = range_of(e.acc, heads * e.cap * 4, s, "acc", false, 1);
+    r[(*nr)++] = range_of(e.pos, heads * e.cap * 4, s, "pos", false, 2);
+    r[(*nr)++] = range_of(e.acc_out, heads * e.cap * 4, s, "acc_out", true, 1);
+    r[(*nr)++] = range_of(e.pos_out, heads * e.cap * 4, s, "pos_out", true, 2);
+    return LUCE_OK;
+}
 
 int luce_kv_evict(const luce_evict_slot* slots, int n_seq, int n_layers, int Hkv, int D, void* stream)
 {
@@ -290,27 +421,49 @@ int luce_kv_evict(const luce_evict_slot* slots, int n_seq, int n_layers, int Hkv
         const luce_evict_slot& e = slots[s];
         REQUIRE(e.k && e.v && aligned(e.k, 16) && aligned(e.v, 16), LUCE_EINVAL,
                 "%s: slot %d cache null or not 16-byte aligned", who, s);
-        REQUIRE(e.acc && e.pos && e.acc_out && e.pos_out && aligned(e.acc, 4) && aligned(e.pos, 4) &&
-                    aligned(e.acc_out, 4) && aligned(e.pos_out, 4),
-                LUCE_EINVAL, "%s: slot %d acc or pos null or misaligned", who, s);
-        REQUIRE(e.cap >= 1 && e.len >= 0 && e.len <= e.cap, LUCE_EINVAL, "%s: slot %d len=%d outside [0, cap=%d]", who, s,
-                e.len, e.cap);
-        REQUIRE(e.len <= LUCE_MAX_KEYS, LUCE_EUNSUPPORTED, "%s: slot %d has %d keys (at most %d)", who, s, e.len,
-                LUCE_MAX_KEYS);
-        REQUIRE(e.budget >= 1 && e.sinks >= 0 && e.recent >= 0 && (int64_t)e.sinks + e.recent <= e.budget, LUCE_EINVAL,
-                "%s: slot %d needs 1 <= budget and sinks + recent <= budget (%d, %d, %d)", who, s, e.budget, e.sinks,
-                e.recent);
-        REQUIRE(e.next_pos >= 0, LUCE_EINVAL, "%s: slot %d next_pos=%d", who, s, e.next_pos);
-        b.slot[s] = EvictSlot{reinterpret_cast<__half*>(e.k), reinterpret_cast<__half*>(e.v), e.acc, e.pos, e.acc_out,
-                              e.pos_out, e.len, e.cap, e.budget, e.sinks, e.recent, e.next_pos};
-        const bool copies = e.acc_out != e.acc || e.pos_out != e.pos;
-        any = any || e.len > e.budget || (copies && e.len > 0);
+        const EvictArgs a{e.acc, e.pos, e.acc_out, e.pos_out, e.len, e.cap, e.budget, e.sinks, e.recent, e.next_pos};
+        EvictSlot& o = b.slot[s];
+        if ((rc = add_evict_slot(o, a, s, heads, r, &nr, &any, who))) return rc;
+        o.k = reinterpret_cast<__half*>(e.k);
+        o.v = reinterpret_cast<__half*>(e.v);
+        o.head_step = (int64_t)e.cap * D;
         r[nr++] = range_of(e.k, heads * e.cap * D * 2, s, "K cache", true);
         r[nr++] = range_of(e.v, heads * e.cap * D * 2, s, "V cache", true);
-        r[nr++] = range_of(e.acc, heads * e.cap * 4, s, "acc", false, 1);
-        r[nr++] = range_of(e.pos, heads * e.cap * 4, s, "pos", false, 2);
-        r[nr++] = range_of(e.acc_out, heads * e.cap * 4, s, "acc_out", true, 1);
-        r[nr++] = range_of(e.pos_out, heads * e.cap * 4, s, "pos_out", true, 2);
+    }
+    if ((rc = check_apart(r, nr, who))) return rc;
+    if (!any) return ok();
+    return cuda_status(launch_kv_evict(b, n_layers, Hkv, (cudaStream_t)stream), who);
+}
+
+int luce_kv_evict_paged(const luce_paged_evict_slot* slots, int n_seq, int n_layers, int Hkv, int D, void* stream)
+{
+    const char* who = "kv_evict_paged";
+    int rc = check_layers(n_seq, n_layers, Hkv, D, slots, who);
+    if (rc) return rc;
+    EvictBatch b{};
+    b.n_slot = n_seq;
+    ByteRange r[4 * LUCE_MAX_SEQ];
+    int nr = 0;
+    bool any = false;
+    const int64_t heads = (int64_t)n_layers * Hkv;
+    for (int s = 0; s < n_seq; ++s) {
+        const luce_paged_evict_slot& e = slots[s];
+        REQUIRE(e.k_pool && e.v_pool && aligned(e.k_pool, 16) && aligned(e.v_pool, 16), LUCE_EINVAL,
+                "%s: slot %d pool null or not 16-byte aligned", who, s);
+        REQUIRE(e.k_pool != e.v_pool, LUCE_EINVAL, "%s: slot %d has one pool for K and V", who, s);
+        REQUIRE(e.table && aligned(e.table, 4) && e.n_pages >= 1, LUCE_EINVAL, "%s: slot %d has no pages or no table", who,
+                s);
+        const EvictArgs a{e.acc, e.pos, e.acc_out, e.pos_out, e.len, e.cap, e.budget, e.sinks, e.recent, e.next_pos};
+        EvictSlot& o = b.slot[s];
+        if ((rc = add_evict_slot(o, a, s, heads, r, &nr, &any, who))) return rc;
+        o.k = reinterpret_cast<__half*>(e.k_pool);
+        o.v = reinterpret_cast<__half*>(e.v_pool);
+        o.pages = e.table;
+        o.n_pages = e.n_pages;
+        o.head_step = (int64_t)LUCE_PAGE_KEYS * D;
+        REQUIRE(heads * LUCE_PAGE_KEYS * e.n_pages < ((int64_t)1 << 31), LUCE_EUNSUPPORTED,
+                "%s: slot %d pool has 2^31 rows or more", who, s);
+        o.page_rows = (int32_t)(heads * LUCE_PAGE_KEYS);
     }
     if ((rc = check_apart(r, nr, who))) return rc;
     if (!any) return ok();

@@ -44,14 +44,14 @@ tree_commit_kernel(const __grid_constant__ CommitBatch b, int n_layers, int Hq, 
         const int lane = tid & 31, lh = blockIdx.x * (kCommitThreads / 32) + (tid >> 5);
         pdl_wait();
         if (lh >= heads || A == 0) return;
-        uint4* p = reinterpret_cast<uint4*>(lane < 16 ? sl.k : sl.v) + ((int64_t)lh * sl.cap + sl.len) * 16 + (lane & 15);
+        __half* p = (lane < 16 ? sl.k : sl.v) + lh * sl.head_step + 8 * (lane & 15);
         uint4 x[kMaxTree];
 #pragma unroll
         for (int i = 0; i < kMaxTree; ++i)
-            if (i < A && sl.path[i] != i) x[i] = ld_placed_u4(p + sl.path[i] * 16);
+            if (i < A && sl.path[i] != i) x[i] = ld_placed_u4(p + sl.from[i]);
 #pragma unroll
         for (int i = 0; i < kMaxTree; ++i)
-            if (i < A && sl.path[i] != i) p[i * 16] = x[i];
+            if (i < A && sl.path[i] != i) *reinterpret_cast<uint4*>(p + sl.to[i]) = x[i];
         if (sl.pos && lane < A) sl.pos[(int64_t)lh * sl.cap + sl.len + lane] = sl.pos0 + lane;
         return;
     }
@@ -171,6 +171,15 @@ __device__ __forceinline__ int far_ld(uint32_t a)
     asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
     return v;
 }
+// Key j's row, in rows from the (layer, KV head)'s first; -1 for a page outside
+// the pool.
+__device__ __forceinline__ int evict_row(const EvictSlot& sl, int j)
+{
+    if (!sl.pages) return j;
+    const int p = ld_placed_i(sl.pages + (j >> 7));
+    return p < 0 || p >= sl.n_pages ? -1 : p * sl.page_rows + (j & 127);
+}
+
 // Exclusive prefix of v over the CTA's threads; *total the sum.
 __device__ __forceinline__ int block_prefix(int v, int* warp_sum, int* total)
 {
@@ -380,8 +389,7 @@ kv_evict_kernel(const __grid_constant__ EvictBatch b, int slice)
             mc += __shfl_sync(0xffffffffu, cs, r);
         }
     }
-    const int64_t rows = lh * sl.cap * 16;
-    uint4* base = reinterpret_cast<uint4*>(lane < 16 ? sl.k : sl.v) + rows + (lane & 15);
+    uint4* base = reinterpret_cast<uint4*>((lane < 16 ? sl.k : sl.v) + lh * sl.head_step) + (lane & 15);
     for (int i0 = 32 * (me * kEvictWarps + warp); i0 < m; i0 += 32 * C * kEvictWarps) {
         const int i = i0 + lane, cnt = min(32, m - i0);
         int to = 0, from = 0;
@@ -408,17 +416,20 @@ kv_evict_kernel(const __grid_constant__ EvictBatch b, int slice)
             acc_out[to] = ld_placed_f(acc + from);
             pos_out[to] = ld_placed_i(pos + from);
         }
+        int dst = i < m ? evict_row(sl, to) : -1;
+        const int src = i < m ? evict_row(sl, from) : -1;
+        if (src < 0) dst = -1;
         for (int k = 0; k < cnt; k += kEvictMove) {
             uint4 x[kEvictMove];
 #pragma unroll
             for (int d = 0; d < kEvictMove; ++d) {
-                const int f = __shfl_sync(0xffffffffu, from, (k + d) & 31);
-                if (k + d < cnt) x[d] = ld_placed_cs_u4(base + (int64_t)f * 16);
+                const int f = __shfl_sync(0xffffffffu, src, (k + d) & 31);
+                if (k + d < cnt && f >= 0) x[d] = ld_placed_cs_u4(base + (int64_t)f * 16);
             }
 #pragma unroll
             for (int d = 0; d < kEvictMove; ++d) {
-                const int t = __shfl_sync(0xffffffffu, to, (k + d) & 31);
-                if (k + d < cnt) base[(int64_t)t * 16] = x[d];
+                const int t = __shfl_sync(0xffffffffu, dst, (k + d) & 31);
+                if (k + d < cnt && t >= 0) base[(int64_t)t * 16] = x[d];
             }
         }
     }
@@ -531,10 +542,11 @@ kv_evict_few_kernel(const __grid_constant__ EvictBatch b)
     }
     __syncthreads();
     const int m = (int)low[0][0];
-    uint4* base = reinterpret_cast<uint4*>(lane < 16 ? sl.k : sl.v) + lh * sl.cap * 16 + (lane & 15);
+    uint4* base = reinterpret_cast<uint4*>((lane < 16 ? sl.k : sl.v) + lh * sl.head_step) + (lane & 15);
     for (int i = warp; i < m; i += kFewWarps) {
         const int to = hole[i], from = come[i];
-        base[(int64_t)to * 16] = ld_placed_u4(base + (int64_t)from * 16);
+        const int src = evict_row(sl, from), dst = evict_row(sl, to);
+        if (src >= 0 && dst >= 0) base[(int64_t)dst * 16] = ld_placed_u4(base + (int64_t)src * 16);
         if (lane == 0) {
             acc_out[to] = ld_placed_f(acc + from);
             pos_out[to] = ld_placed_i(pos + from);

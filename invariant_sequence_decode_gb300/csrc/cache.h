@@ -133,11 +133,15 @@ cudaError_t launch_tree_attention(const float* q, const TreeBatch& b, int Hq, in
                                   float* out, float* scores, int64_t lds, float* stats, int8_t* out_q, float* out_d,
                                   cudaStream_t s);
 
+// Offsets are in elements from k and v: path row i moves from from[i] to to[i]
+// in each (layer, KV head), head_step apart.
 struct CommitSlot {
     __half* k;
     __half* v;
     float* acc;
     int32_t* pos;
+    int64_t head_step;
+    int64_t from[kMaxTree], to[kMaxTree];
     int32_t len;
     int32_t cap;
     int32_t row0;
@@ -152,6 +156,8 @@ struct CommitBatch {
 cudaError_t launch_tree_commit(const CommitBatch& b, int n_layers, int Hq, int Hkv, const float* scores, int n_rows,
                                int64_t lds, const float* stats, cudaStream_t s);
 
+// Key j of (layer, KV head) lh is at lh * head_step + j * 128 elements, or, in
+// pages, at lh * head_step + (pages[j / 128] * page_rows + j % 128) * 128.
 struct EvictSlot {
     __half* k;
     __half* v;
@@ -159,6 +165,10 @@ struct EvictSlot {
     const int32_t* pos;
     float* acc_out;
     int32_t* pos_out;
+    const int32_t* pages;
+    int64_t head_step;
+    int32_t page_rows;
+    int32_t n_pages;
     int32_t len;
     int32_t cap;
     int32_t budget;

@@ -198,3 +198,57 @@ def test_tree_step_layout(lib):
     assert lib.luce_decode_step_tree_layout(ctypes.byref(m), 4, 1000, ctypes.byref(a)) == luce.LUCE_OK
     assert lib.luce_decode_step_layout(ctypes.byref(m), 4, 1000, ctypes.byref(b)) == luce.LUCE_OK
     assert all(getattr(a, f) == getattr(b, f) for f in luce._LAYOUT_FIELDS if f != "total")
+
+
+def pslot(k=P, v=P + BIG, table=(0, 1, 2), n_pages=4, length=130, cap=400, path=(0, 2), row0=0, acc=None, pos=None, pos0=10):
+    return luce.PagedCommitSlotC(k, v, ints(table) if table is not None else None, len(table or ()), n_pages, length, cap,
+                                 len(path), row0, ints(path), acc, pos, pos0)
+
+
+def pcommit(lib, slots, L=2, Hq=8, Hkv=2, D=128, scores=None, rows=0, lds=0, stats=None):
+    arr = (luce.PagedCommitSlotC * max(1, len(slots)))(*slots)
+    return lib.luce_tree_commit_paged(arr, len(slots), L, Hq, Hkv, D, scores, rows, lds, stats, None)
+
+
+@pytest.mark.parametrize("want,slots,kw", [
+    (E, [], {}), (U, [pslot()], dict(D=64)), (E, [pslot(k=0)], {}), (E, [pslot(v=P)], {}), (E, [pslot(k=P + 8)], {}),
+    (E, [pslot(table=None)], {}), (E, [pslot(n_pages=0)], {}), (E, [pslot(table=(0, 4))], {}), (E, [pslot(table=(0, -1))], {}),
+    (E, [pslot(table=(0,))], {}), (E, [pslot(length=126, path=(0, 2), table=(0, 9))], {}), (E, [pslot(path=(2, 1))], {}),
+    (E, [pslot(length=399, path=(0, 1))], {}), (E, [pslot(), pslot()], {}), (E, [pslot(acc=ACC)], {}),
+    (E, [pslot(path=(1, 3)), pslot(table=(3, 1), length=133, path=(0,))], {}),   # writes key 133's row, which the other reads
+    (E, [pslot(acc=ACC, pos=ACC)], dict(scores=SC, rows=4, lds=136, stats=ST)),
+])
+def test_paged_commit_refusals(lib, want, slots, kw):
+    assert pcommit(lib, slots, **kw) == want and lib.luce_last_error()
+
+
+def peslot(k=P, v=P + BIG, table=P, acc=ACC, pos=POS, acc_out=ACC, pos_out=POS, n_pages=4, length=20, cap=64, budget=10, sinks=1,
+           recent=4, nxt=20):
+    return luce.PagedEvictSlotC(k, v, table, acc, pos, acc_out, pos_out, n_pages, length, cap, budget, sinks, recent, nxt)
+
+
+@pytest.mark.parametrize("want,slot,kw", [
+    (U, peslot(), dict(D=64)), (E, peslot(k=0), {}), (E, peslot(v=P), {}), (E, peslot(table=0), {}), (E, peslot(table=P + 2), {}),
+    (E, peslot(n_pages=0), {}), (E, peslot(acc=0), {}), (E, peslot(length=65), {}), (E, peslot(budget=0), {}),
+    (E, peslot(sinks=6, recent=5), {}), (E, peslot(acc_out=POS), {}), (U, peslot(length=130817, cap=130900), {}),
+])
+def test_paged_evict_refusals(lib, want, slot, kw):
+    arr = (luce.PagedEvictSlotC * 1)(slot)
+    assert lib.luce_kv_evict_paged(arr, 1, 2, 2, kw.get("D", 128), None) == want and lib.luce_last_error()
+
+
+def ptslot(k=P, v=P + BIG, table=P, host=(0, 1), n_pages=4, length=10, pos0=10, nodes=2, parent=None):
+    return luce.PagedTreeSlotC(k, v, table, ints(host), len(host), n_pages, length, pos0, nodes,
+                               None if parent is None else ints(parent))
+
+
+@pytest.mark.parametrize("want,slots", [
+    (E, []), (E, [ptslot(k=0)]), (E, [ptslot(v=P)]), (E, [ptslot(table=0)]), (E, [ptslot(host=(4, 0))]), (E, [ptslot(host=())]),
+    (E, [ptslot(length=255)]), (E, [ptslot(nodes=0)]), (E, [ptslot(nodes=17)]), (E, [ptslot(parent=[0, 0])]), (E, [ptslot(pos0=-1)]),
+    (E, [ptslot(), ptslot()]), (U, [ptslot(length=130815)]),
+])
+def test_paged_tree_step_refusals(lib, want, slots):
+    arr = (luce.PagedTreeSlotC * max(1, len(slots)))(*slots)
+    assert lib.luce_decode_step_tree_paged(ctypes.byref(model()), arr, len(slots), P, None, None, None, 0, None, 0x100000,
+                                           1 << 40, None) == want
+    assert lib.luce_last_error()

@@ -249,6 +249,79 @@ def test_evict_python_refusals():
         luce.luce_kv_evict([luce.EvictSlot(k, k, acc, pos, 4, 2)])
 
 
+# ------------------------------------------------------------------ pages
+
+def pool_of(rng, x, extra=2):
+    """x [L][Hkv][cap][128] laid out in pages: (pool [n_pages][L][Hkv][128][128], table); unused rows hold NaN."""
+    L, Hkv, cap, _ = x.shape
+    per = -(-cap // 128)
+    table = rng.permutation(per + extra)[:per].astype(np.int32)
+    pool = np.full((per + extra, L, Hkv, 128, 128), np.nan, dtype=np.float16)
+    for i, p in enumerate(table):
+        part = x[:, :, 128 * i:128 * (i + 1)]
+        pool[p, :, :, :part.shape[2]] = part
+    return pool, table
+
+
+@pytest.mark.parametrize("lens,paths", [([126], [[1, 2, 5]]), ([0, 300], [[0, 3], [2, 7]]), ([383, 128, 1], [[3], [0, 1, 4], []])])
+def test_paged_commit(lens, paths):
+    rng = np.random.default_rng(sum(lens))
+    L, Hq, Hkv = 2, 6, 3
+    per = 16 // len(lens)
+    lds = -(-(max(lens) + 16) // 4) * 4
+    scores = rng.standard_normal((L, len(lens) * per, Hq, lds)).astype(np.float32)
+    stats = np.ones((L, len(lens) * per, Hq, 2), dtype=np.float32)
+    slots, flat, spare = [], [], []
+    for s, (n, path) in enumerate(zip(lens, paths)):
+        k, v = caches(rng, L, Hkv, n + 16)
+        acc, pos = rng.random((L, Hkv, n + 16)).astype(np.float32), np.zeros((L, Hkv, n + 16), dtype=np.int32)
+        seed = int(rng.integers(1 << 30))
+        pools = [pool_of(np.random.default_rng(seed), x) for x in (k, v)]
+        flat.append(luce.CommitSlot(cuda(k), cuda(v), n, path, s * per, cuda(acc), cuda(pos), 7))
+        slots.append(luce.PagedCommitSlot(cuda(pools[0][0]), cuda(pools[1][0]), pools[0][1], n, path, s * per, cuda(acc),
+                                          cuda(pos), 7))
+        spare.append(seed)
+    luce.luce_tree_commit(flat, Hq, cuda(scores), cuda(stats))
+    luce.luce_tree_commit(slots, Hq, cuda(scores), cuda(stats))
+    torch.cuda.synchronize()
+    for f, p, seed in zip(flat, slots, spare):
+        for a, b in ((f.k, p.k_pool), (f.v, p.v_pool)):
+            assert same(b, pool_of(np.random.default_rng(seed), a.cpu().numpy())[0])
+        assert same(p.acc, f.acc.cpu().numpy()) and same(p.pos, f.pos.cpu().numpy())
+
+
+@pytest.mark.parametrize("length,budget", [(130, 127), (300, 290), (700, 100), (5000, 2000)])
+def test_paged_evict(length, budget):
+    rng = np.random.default_rng(length)
+    L, Hkv = 2, 2
+    k, v = caches(rng, L, Hkv, length)
+    acc, pos = weights(rng, "odd", (L, Hkv, length)), np.tile(np.arange(length, dtype=np.int32), (L, Hkv, 1))
+    wk, wv, wa, wp = ref.evict(k, v, acc, pos, length, budget, 2, 20, length)
+    (pk, table), (pv, _) = (pool_of(np.random.default_rng(5), x) for x in (k, v))
+    sl = luce.PagedEvictSlot(cuda(pk), cuda(pv), cuda(table), cuda(acc), cuda(pos), length, budget, 2, 20, length)
+    luce.luce_kv_evict([sl])
+    torch.cuda.synchronize()
+    assert same(sl.k_pool, pool_of(np.random.default_rng(5), wk)[0]) and same(sl.v_pool, pool_of(np.random.default_rng(5), wv)[0])
+    assert same(sl.acc, wa) and same(sl.pos, wp)
+
+
+@pytest.mark.parametrize("length,budget", [(300, 290), (700, 300)])
+def test_paged_evict_leaves_rows_of_bad_pages(length, budget):
+    rng = np.random.default_rng(length + 1)
+    k, v = caches(rng, 1, 2, length)
+    acc, pos = weights(rng, "plain", (1, 2, length)), np.tile(np.arange(length, dtype=np.int32), (1, 2, 1))
+    wk, wv, wa, wp = ref.evict(k, v, acc, pos, length, budget, 0, 0, length)
+    (pk, table), (pv, _) = (pool_of(np.random.default_rng(5), x) for x in (k, v))
+    bad = table.copy()
+    bad[1] = 2 ** 31 - 1                                                # rows 128..255: neither read nor written
+    wk[:, :, 128:256], wv[:, :, 128:256] = k[:, :, 128:256], v[:, :, 128:256]
+    sl = luce.PagedEvictSlot(cuda(pk), cuda(pv), cuda(bad), cuda(acc), cuda(pos), length, budget, 0, 0, length)
+    luce.luce_kv_evict([sl])
+    torch.cuda.synchronize()
+    assert same(sl.k_pool, pool_of(np.random.default_rng(5), wk)[0]) and same(sl.v_pool, pool_of(np.random.default_rng(5), wv)[0])
+    assert same(sl.acc, wa) and same(sl.pos, wp)
+
+
 # ------------------------------------------------------------------ together
 
 def test_decode_loop_with_trees_commits_and_eviction():

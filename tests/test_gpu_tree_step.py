@@ -130,6 +130,34 @@ def test_chains_agree_with_the_plain_step(model):
         assert err.max().item() <= 2e-3
 
 
+def test_pages_give_the_bits_of_flat_caches(model):
+    lens, trees, pos0 = [120, 0, 300], [[-1, 0, 0, 1, 3, 4, 0, 2, 1], [-1, 0], [-1, 0, 1]], [200, 0, 300]
+    rng = np.random.default_rng(3)
+    xh = wl.acts(3, sum(len(t) for t in trees), wl.TINY_LAYER.hidden, sub=7)
+    flat, paged = [], []
+    for s, (n, tree, p0) in enumerate(zip(lens, trees, pos0)):
+        k, v = cache(s, n, n + len(tree))
+        flat.append(luce.TreeSlot(cuda(k), cuda(v), n, tree, p0))
+        per = -(-(n + len(tree)) // 128)
+        table, pools = rng.permutation(per + 2)[:per], []
+        for x in (k, v):
+            pool = np.full((per + 2, LAYERS, x.shape[1], 128, 128), np.nan, dtype=np.float16)
+            for i, p in enumerate(table):
+                part = x[:, :, 128 * i:128 * (i + 1)]
+                pool[p, :, :, :part.shape[2]] = part
+            pools.append(cuda(pool))
+        paged.append(luce.PagedTreeSlot(*pools, table, n, tree, p0))
+    sc = [torch.zeros(LAYERS, xh.shape[0], 4, 320, device="cuda") for _ in range(2)]
+    st = [torch.zeros(LAYERS, xh.shape[0], 4, 2, device="cuda") for _ in range(2)]
+    a, b = step(model, flat, cuda(xh), sc[0], st[0]), step(model, paged, cuda(xh), sc[1], st[1])
+    for x, y in zip((*a, sc[0], st[0]), (*b, sc[1], st[1])):
+        assert np.array_equal(bits(x), bits(y))
+    for f, p in zip(flat, paged):
+        for j in range(f.len, f.len + len(f.parent)):
+            for x, y in ((f.k, p.k_pool), (f.v, p.v_pool)):
+                assert torch.equal(x[:, :, j].view(torch.int16), y[p.table[j // 128], :, :, j % 128].view(torch.int16))
+
+
 def test_decode_loop(model):
     """Two slots decode with trees of 8; keys past 48 are evicted.  What the loop
     keeps is checked against its own inputs: the accepted rows' K/V, the
