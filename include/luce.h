@@ -653,9 +653,9 @@ typedef struct luce_commit_slot {
  * Commit of up to 4 slots' accepted paths, in every layer and KV head:
  *   K and V row len + path[i] moves to len + i (other rows are left as they were);
  *   pos[len + i] = pos0 + i, where pos is given;
- *   where acc is given, with w_j the sum over the accepted nodes' rows r and
- *   the KV head's query heads h (rows in path order, heads ascending) of
- *   e^(scores[r][h][j] - m) / l:
+ *   where acc is given, with w_j the sum (in an order that depends on n_path
+ *   and Hq / Hkv only) over the accepted nodes' rows r and the KV head's query
+ *   heads h of e^(scores[r][h][j] - m) / l:
  *     acc[j] += w_j for j < len,  acc[len + i] = w_(len + path[i]).
  * A row whose l is 0 adds nothing.  The caller then continues with
  * len + n_path keys.

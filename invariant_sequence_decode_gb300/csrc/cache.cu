@@ -36,7 +36,7 @@ tree_commit_kernel(const __grid_constant__ CommitBatch b, int n_layers, int Hq, 
                    const float* stats, int move_ctas)
 {
     __shared__ float2 ml[kMaxTree * 8];   // (m, 1 / l) of the accepted rows' heads
-    __shared__ int64_t at[kMaxTree * 8];  // and where their scores begin
+    __shared__ int64_t at[kMaxTree * 8];  // and their index in stats and scores
     pdl_trigger();
     const CommitSlot& sl = b.slot[blockIdx.y];
     const int tid = threadIdx.x, A = sl.n_path, heads = n_layers * Hkv;
@@ -58,33 +58,44 @@ tree_commit_kernel(const __grid_constant__ CommitBatch b, int n_layers, int Hq, 
     const int tiles = max(1, (sl.len + kCommitKeys - 1) / kCommitKeys);  // (the first also takes the new keys)
     const int GQ = Hq / Hkv, part = blockIdx.x - move_ctas, lh = part / tiles, tile = part - lh * tiles, n = A * GQ;
     if (!sl.acc || A == 0 || lh >= heads) return;
-    pdl_wait();
     const int l = lh / Hkv, g = lh % Hkv;
-    for (int i = tid; i < n; i += kCommitThreads) {
-        const int64_t rh = ((int64_t)l * n_rows + sl.row0 + sl.path[i / GQ]) * Hq + g * GQ + i % GQ;
-        const float2 st = ld_placed_f2(stats + 2 * rh);
-        const float m = st.x, sum = st.y;
-        ml[i] = make_float2(m == -INFINITY ? 0.0f : m, sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum));
-        at[i] = rh * lds;
-    }
+    for (int i = tid; i < n; i += kCommitThreads)
+        at[i] = ((int64_t)l * n_rows + sl.row0 + sl.path[i / GQ]) * Hq + g * GQ + i % GQ;
     __syncthreads();
-    float* acc = sl.acc + (int64_t)lh * sl.cap;
-    if (tile == 0 && tid < A) {
-        float w = 0.0f;
-        for (int i = 0; i < n; ++i)
-            w = __fmaf_rn(commit_exp(__fsub_rn(ld_placed_f(scores + at[i] + sl.len + sl.path[tid]), ml[i].x)), ml[i].y, w);
-        acc[sl.len + tid] = w;
+    pdl_wait();
+    for (int i = tid; i < n; i += kCommitThreads) {
+        const float2 st = ld_placed_f2(stats + 2 * at[i]);
+        ml[i] = make_float2(st.x == -INFINITY ? 0.0f : st.x, st.y == 0.0f ? 0.0f : __fdiv_rn(1.0f, st.y));
     }
+    float* acc = sl.acc + (int64_t)lh * sl.cap;
     const int j = tile * kCommitKeys + 4 * tid;
-    if (j >= sl.len) return;
     float old[4], w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) old[e] = j + e < sl.len ? ld_placed_f(acc + j + e) : 0.0f;
-    for (int i0 = 0; i0 < n; i0 += kCommitAhead) {
-        float4 s[kCommitAhead];
+    float4 s[kCommitAhead];
+    // the first rows are on their way while the statistics settle
+    auto fetch = [&](int i0) {
 #pragma unroll
         for (int e = 0; e < kCommitAhead; ++e)
-            if (i0 + e < n) s[e] = ld_placed_cs_f4(scores + at[i0 + e] + j);
+            if (i0 + e < n) s[e] = ld_placed_cs_f4(scores + at[i0 + e] * lds + j);
+    };
+    if (j < sl.len) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) old[e] = j + e < sl.len ? ld_placed_f(acc + j + e) : 0.0f;
+        fetch(0);
+    }
+    __syncthreads();
+    if (tile == 0)  // a warp per new key
+        for (int k = tid >> 5; k < A; k += kCommitThreads / 32) {
+            float x = 0.0f;
+            for (int i = tid & 31; i < n; i += 32) {
+                const float t = ld_placed_f(scores + at[i] * lds + sl.len + sl.path[k]);
+                x = __fmaf_rn(commit_exp(__fsub_rn(t, ml[i].x)), ml[i].y, x);
+            }
+            x = warp_sum_butterfly(x);
+            if ((tid & 31) == 0) acc[sl.len + k] = x;
+        }
+    if (j >= sl.len) return;
+    for (int i0 = 0; i0 < n; i0 += kCommitAhead) {
+        if (i0 > 0) fetch(i0);
 #pragma unroll
         for (int e = 0; e < kCommitAhead; ++e)
             if (i0 + e < n) {
