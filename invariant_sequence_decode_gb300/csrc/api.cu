@@ -99,7 +99,11 @@ uint64_t luce_launch_count(void) { return g_launches.load(std::memory_order_rela
 int luce_wait_timeouts(uint32_t* count, int reset)
 {
     REQUIRE(count, LUCE_EINVAL, "wait_timeouts: null count");
-    return cuda_status(read_wait_timeouts(count, reset != 0), "wait_timeouts");
+    uint32_t rings = 0, trees = 0;
+    cudaError_t e = read_wait_timeouts(&rings, reset != 0);
+    if (e == cudaSuccess) e = read_tree_wait_timeouts(&trees, reset != 0);
+    if (e == cudaSuccess) *count = rings + trees;
+    return cuda_status(e, "wait_timeouts");
 }
 
 int luce_test_wait_expiry(int64_t limit_ns, void* stream)

@@ -133,6 +133,9 @@ cudaError_t launch_tree_attention(const float* q, const TreeBatch& b, int Hq, in
                                   float* out, float* scores, int64_t lds, float* stats, int8_t* out_q, float* out_d,
                                   cudaStream_t s);
 
+// Bounded waits of the tree attention that expired on the current device.
+cudaError_t read_tree_wait_timeouts(uint32_t* count, bool reset);
+
 // Offsets are in elements from k and v: path row i moves from from[i] to to[i]
 // in each (layer, KV head), head_step apart.
 struct CommitSlot {

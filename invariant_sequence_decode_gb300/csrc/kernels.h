@@ -101,12 +101,11 @@ cudaError_t launch_qkv_rope_tma(const int8_t* wq, const __half* wd, int K, const
                                 const KvRows& kv, cudaStream_t s);
 
 // Bounded waits that expired on the current device (synchronous; the dp4a
-// ring's, the tensor-core ring's, the slot attention's and the tree attention's counters summed);
+// ring's, the tensor-core ring's and the slot attention's counters summed);
 // reset clears the counters.
 cudaError_t read_wait_timeouts(uint32_t* count, bool reset);
 cudaError_t read_mma_wait_timeouts(uint32_t* count, bool reset);
 cudaError_t read_attn_wait_timeouts(uint32_t* count, bool reset);
-cudaError_t read_tree_wait_timeouts(uint32_t* count, bool reset);
 
 // One bounded wait that nothing completes (limit_ns), counted as expired.
 cudaError_t launch_wait_expiry(uint64_t limit_ns, cudaStream_t s);

@@ -564,16 +564,6 @@ bool encode_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* ba
     return true;
 }
 
-bool encode_map_once(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base, const cuuint64_t* dims,
-                     const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle)
-{
-    const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-    const cuuint32_t es[4] = {1, 1, 1, 1};
-    return enc && enc(m, dt, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, es,
-                      CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 int current_device()
 {
     int dev = 0;
@@ -797,7 +787,7 @@ cudaError_t launch_wait_expiry(uint64_t limit_ns, cudaStream_t s)
 
 cudaError_t read_wait_timeouts(uint32_t* count, bool reset)
 {
-    uint32_t mine = 0, mma = 0, attn = 0, tree = 0;
+    uint32_t mine = 0, mma = 0, attn = 0;
     cudaError_t e = cudaMemcpyFromSymbol(&mine, g_wait_timeouts, sizeof(uint32_t));
     if (e == cudaSuccess && reset) {
         const uint32_t zero = 0;
@@ -805,8 +795,7 @@ cudaError_t read_wait_timeouts(uint32_t* count, bool reset)
     }
     if (e == cudaSuccess) e = read_mma_wait_timeouts(&mma, reset);
     if (e == cudaSuccess) e = read_attn_wait_timeouts(&attn, reset);
-    if (e == cudaSuccess) e = read_tree_wait_timeouts(&tree, reset);
-    if (e == cudaSuccess) *count = mine + mma + attn + tree;
+    if (e == cudaSuccess) *count = mine + mma + attn;
     return e;
 }
 

@@ -103,15 +103,6 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, int
         : "memory");
 }
 
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, int x, int y, int z, int w, uint64_t* bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-        "[%6];" ::"r"(smem_addr(dst)),
-        "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
-        : "memory");
-}
-
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, int x, int y, uint64_t* bar)
 {
     asm volatile(
@@ -145,11 +136,6 @@ int sm_count();
 bool encode_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base, const cuuint64_t* dims,
                 const cuuint64_t* strides, const cuuint32_t* box,
                 CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE);
-
-// encode_map of 2 to 4 dims without the table: for maps whose base, sizes and
-// strides are a caller's per call.
-bool encode_map_once(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base, const cuuint64_t* dims,
-                     const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle);
 
 // Raises `kernel`'s dynamic shared-memory limit to `bytes` once per device;
 // `done` is the kernel's own per-device flag table.

@@ -261,6 +261,16 @@ __device__ __forceinline__ void st_v8(float* p, const float* v)
                  : "memory");
 }
 
+// A box of the (d, key, head, page) map.
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, int x, int y, int z, int w, uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(smem_addr(dst)),
+        "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+        : "memory");
+}
+
 // The producer: K and V tiles of the CTA's chunks, in order.  Returns the
 // tiles issued.
 __device__ int tree_produce(const TreeMaps& maps, const TreeBatch& b, int Hkv, int u0, int u1, int step, uint8_t* tiles, TreeBars& bar)
@@ -610,22 +620,37 @@ cudaError_t read_tree_wait_timeouts(uint32_t* count, bool reset)
     return e;
 }
 
+static PFN_cuTensorMapEncodeTiled_v12000 tree_map_encoder()
+{
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
+}
+
 // The maps of the views' K and V: dims (d, key, head, page), boxes of 64 dims
-// by 128 keys.
+// by 128 keys, zeros outside.  Made anew by each call: two of them take 0.1 us.
 static bool tree_maps(const TreeBatch& b, int Hkv, TreeMaps* maps)
 {
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = tree_map_encoder();
+    if (!enc) return false;
     for (int i = 0; i < b.n_view; ++i) {
         const TreeView& v = b.view[i];
         if (v.n_chunk == 0) continue;
         const cuuint64_t dims[4] = {kHeadDim, (cuuint64_t)v.cap, (cuuint64_t)Hkv, (cuuint64_t)v.n_pages};
         const cuuint64_t strides[3] = {(cuuint64_t)v.tok_stride * 2, (cuuint64_t)v.head_stride * 2,
                                        (cuuint64_t)(v.pages ? v.page_stride : v.head_stride) * 2};
-        const cuuint32_t box[4] = {kHeadDim / 2, kTreeTile, 1, 1};
-        if (!encode_map_once(&maps->k[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, v.k, dims, strides, box,
-                             CU_TENSOR_MAP_SWIZZLE_128B) ||
-            !encode_map_once(&maps->v[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, v.v, dims, strides, box,
-                             CU_TENSOR_MAP_SWIZZLE_128B))
-            return false;
+        const cuuint32_t box[4] = {kHeadDim / 2, kTreeTile, 1, 1}, step[4] = {1, 1, 1, 1};
+        for (int kv = 0; kv < 2; ++kv)
+            if (enc(kv ? &maps->v[i] : &maps->k[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<__half*>(kv ? v.v : v.k),
+                    dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+                return false;
     }
     return true;
 }
