@@ -917,7 +917,8 @@ class TreeAttention(_Prepared):
     [T][Hq][128], ``out`` as q, ``scores`` fp32 [T][Hq][lds] and ``stats`` fp32
     [T][Hq][2] when given.  Each call takes the views' current ``len``.  The
     object owns its workspace (sized for the views' capacity) unless one is
-    given, so calls of one object must not overlap on the GPU."""
+    given, so calls of one object must not overlap on the GPU, and a graph that
+    captured a call needs the object alive."""
 
     def __init__(self, q, views, n_kv_heads: int, scale: float, out=None, scores=None, stats=None, ws=None, stream=None):
         import torch

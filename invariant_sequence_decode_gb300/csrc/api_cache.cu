@@ -38,10 +38,14 @@ int64_t luce::tree_chunks(TreeBatch& b, int Hq, int Hkv)
     for (int i = 0; i < b.n_view; ++i) {
         TreeView& v = b.view[i];
         v.chunk = tree_chunk_keys(v.len, Hkv);
-        v.n_chunk = (v.len + v.chunk - 1) / v.chunk;
+        v.n_chunk = tree_is_short(v.len) ? 0 : (v.len + v.chunk - 1) / v.chunk;
         v.part0 = part;
         part += (int64_t)v.n_chunk * v.n_nodes * Hq;
     }
+    b.n_short = b.n_long = 0;
+    for (int r = 0; r < b.n_row; ++r)
+        if (b.view[b.row[r].view].n_chunk == 0) b.short_row[b.n_short++] = (uint8_t)r;
+        else b.long_row[b.n_long++] = (uint8_t)r;
     return part;
 }
 
@@ -131,6 +135,8 @@ int luce_tree_attn(const float* q, const luce_treeview* views, int n_seq, int Hq
         REQUIRE(Hkv == 1 || (v.head_stride % 8 == 0 && v.head_stride >= (int64_t)v.cap * v.tok_stride &&
                              v.head_stride < ((int64_t)1 << 38)),
                 LUCE_EINVAL, "%s: view %d head_stride must be a multiple of 8 and keep the heads apart", who, s);
+        REQUIRE((int64_t)v.cap * v.tok_stride < ((int64_t)1 << 38), LUCE_EINVAL, "%s: view %d spans 2^38 elements or more",
+                who, s);
         TreeView& t = b.view[s];
         t.k = reinterpret_cast<const __half*>(v.k);
         t.v = reinterpret_cast<const __half*>(v.v);

@@ -11,7 +11,8 @@ namespace luce {
 // refusal.  parent: nullptr for a chain.
 int tree_path(const int32_t* parent, int n_nodes, TreeRow* rows, int view, int row0, const char* who);
 
-// Cuts the views' prefixes into chunks; returns the rows of partial results.
+// Cuts the views' prefixes into chunks and tells their rows apart by it;
+// returns the rows of partial results.
 int64_t tree_chunks(TreeBatch& b, int Hq, int Hkv);
 
 // A byte range that a call reads or writes.  Two that overlap are refused

@@ -97,7 +97,7 @@ struct TreeView {
     int32_t n_nodes;
     int32_t row0;
     int32_t chunk;    // keys of a chunk: tree_chunk_keys(len, Hkv)
-    int32_t n_chunk;  // chunks of the prefix
+    int32_t n_chunk;  // chunks of the prefix; 0: it is short
 };
 
 // A row's node: its path from the prefix (ascending, the node itself last).
@@ -113,7 +113,12 @@ struct TreeBatch {
     TreeRow row[kMaxTree];
     int32_t n_view;
     int32_t n_row;
+    int32_t n_short, n_long;  // rows whose prefix is short, or cut into chunks
+    uint8_t short_row[kMaxTree], long_row[kMaxTree];
 };
+
+// Whether a prefix is taken whole rather than cut into chunks.
+bool tree_is_short(int len);
 
 // Keys of a chunk of a prefix of len keys: a function of len and the model's KV
 // heads alone, so that a row's sums are cut the same way whatever else is in

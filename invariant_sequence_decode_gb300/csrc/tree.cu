@@ -9,7 +9,8 @@
 // and the merge adds the chunks in order, then the node's own path, key by key
 // from the prefix down to the node.  A node's bits so follow from its prefix
 // and its path alone: the other branches of its tree, which lie between its
-// ancestors in the cache, take no part in any of its sums.
+// ancestors in the cache, take no part in any of its sums.  Prefixes of at most
+// kTreeShort keys take tree_short_kernel, which has no chunks and no merge.
 //
 // Prefix chunks (tree_chunk_kernel).  A tree's n nodes and a KV head's GQ query
 // heads make R = n GQ <= 128 rows that share every key, so both products run
@@ -39,6 +40,11 @@ namespace luce {
 
 constexpr int kTreeTile = 128;  // keys of a tile, and rows of the products
 constexpr int kMaxTreeChunks = 160;
+// Longest prefix that tree_short_kernel takes.  It reads the prefix once per row
+// and head, the chunks once per KV head: at 64 keys it takes 3.2 us for one row
+// of 8 heads and 7.3 for 16 rows of 40, through chunks 6.1 and 9.4; at 128 keys
+// 4.5 and 13.2 against 5.7 and 8.8.
+constexpr int kTreeShort = 64;
 constexpr int kTreeCtas = 152;  // the CTAs that a cut aims at: one per multiprocessor
 
 // Tiles of a chunk for a prefix of nt tiles.  A chunk costs its tiles and about
@@ -62,10 +68,13 @@ static int tree_chunk_tiles(int nt, int Hkv)
     return std::max(best, 1);
 }
 
+bool tree_is_short(int len) { return len <= kTreeShort; }
+
 int tree_chunk_keys(int len, int Hkv) { return kTreeTile * tree_chunk_tiles((len + kTreeTile - 1) / kTreeTile, Hkv); }
 
 int tree_max_chunks(int max_len, int Hkv)
 {
+    if (tree_is_short(max_len)) return 0;
     return std::min({(max_len + kTreeTile - 1) / kTreeTile, kMaxTreeChunks, std::max(1, 4 * kTreeCtas / Hkv)});
 }
 
@@ -682,19 +691,18 @@ __global__ void __launch_bounds__(kHeadDim)
 tree_merge_kernel(const float* q, const __grid_constant__ TreeBatch b, int Hq, int Hkv, TreeScale scale,
                   const float* part_o, const float* part_ml, float* __restrict__ out,
                   float* __restrict__ scores, int64_t lds, float* __restrict__ stats, int8_t* __restrict__ out_q,
-                  float* __restrict__ out_d, int nch_all)
+                  float* __restrict__ out_d)
 {
     __shared__ float ps[kMaxTree];            // the path's products
     __shared__ float4 os[4][kHeadDim / 4];    // the warps' sums
     pdl_trigger();
-    const int h = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int h = blockIdx.x, r = b.long_row[blockIdx.y], tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const TreeRow& row = b.row[r];
     const TreeView& v = b.view[row.view];
     const int GQ = Hq / Hkv, g = h / GQ, R = v.n_nodes * GQ, np = row.n_path, nch = v.n_chunk;
     const int64_t pr0 = v.part0 + (int64_t)g * R + row.node * GQ + h % GQ, pstep = (int64_t)Hkv * R;
     const size_t rh = (size_t)r * Hq + h;
-    // behind a chunk kernel, q and the path's rows are in place already
-    if (nch_all == 0) pdl_wait();
+    // (behind the chunk kernel, q and the path's rows are in place already)
     const float4 qv = ld_placed_f4(q + rh * kHeadDim + 4 * lane);
     uint2 kx[4], vx[4];
 #pragma unroll
@@ -715,7 +723,7 @@ tree_merge_kernel(const float* q, const __grid_constant__ TreeBatch b, int Hq, i
             __fmaf_rn(qv.w, k.w, __fmaf_rn(qv.z, k.z, __fmaf_rn(qv.y, k.y, __fmul_rn(qv.x, k.x)))));
         if (lane == 0 && warp + 4 * i < np) ps[warp + 4 * i] = __fmul_rn(dot, scale.sign);
     }
-    if (nch_all > 0) pdl_wait();
+    pdl_wait();
     // every warp has all chunks' statistics: chunk lane + 32 j in its lane
     constexpr int kStats = kMaxTreeChunks / 32;
     float w[kStats], L = 0.0f, M = -INFINITY;
@@ -788,6 +796,120 @@ tree_merge_kernel(const float* q, const __grid_constant__ TreeBatch b, int Hq, i
     }
 }
 
+// Short prefixes: one CTA of 8 warps per (row, query head) over the keys that
+// the row sees, prefix then path.  Scores: eight lanes to a key, 16 dims each,
+// key 32 i + 4 warp + lane / 8 in step i; values: four dims a lane, warp w sums
+// keys w, w + 8, .. in order and the eight sums are added in order.  Bound by
+// latency: K and V of all steps are asked for at once.
+constexpr int kShortThreads = 256;
+constexpr int kShortKeys = kTreeShort + kMaxTree;
+constexpr int kShortSteps = (kShortKeys + 31) / 32;
+
+__global__ void __launch_bounds__(kShortThreads)
+tree_short_kernel(const float* q, const __grid_constant__ TreeBatch b, int Hq, int Hkv, TreeScale scale,
+                  float* __restrict__ out, float* __restrict__ scores, int64_t lds, float* __restrict__ stats,
+                  int8_t* __restrict__ out_q, float* __restrict__ out_d)
+{
+    __shared__ float ps[32 * kShortSteps];    // the keys' products
+    __shared__ float4 os[8][kHeadDim / 4];    // the warps' sums
+    pdl_trigger();
+    const int h = blockIdx.x, r = b.short_row[blockIdx.y], tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const TreeRow& row = b.row[r];
+    const TreeView& v = b.view[row.view];
+    const int g = h / (Hq / Hkv), n = v.len + row.n_path;
+    const size_t rh = (size_t)r * Hq + h;
+    auto key_at = [&](int a) { return a < v.len ? a : v.len + row.path[a - v.len]; };
+    pdl_wait();
+    const int part = lane & 7;  // dims 16 part .. 16 part + 15
+    float4 qv[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) qv[e] = ld_placed_f4(q + rh * kHeadDim + 16 * part + 4 * e);
+    uint4 kx[kShortSteps][2];
+#pragma unroll
+    for (int i = 0; i < kShortSteps; ++i) {
+        const int a = 32 * i + 4 * warp + (lane >> 3);
+        kx[i][0] = kx[i][1] = make_uint4(0, 0, 0, 0);
+        const __half* kp = a < n ? tree_key(v, v.k, g, key_at(a)) : nullptr;
+        if (kp) {
+            kx[i][0] = ld_placed_u4(kp + 16 * part);
+            kx[i][1] = ld_placed_u4(kp + 16 * part + 8);
+        }
+    }
+    constexpr int kPer = (kShortKeys + 7) / 8;
+    uint2 vx[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int a = warp + 8 * i;
+        vx[i] = make_uint2(0, 0);
+        const __half* vp = a < n ? tree_key(v, v.v, g, key_at(a)) : nullptr;
+        if (vp) vx[i] = ld_placed_u2(vp + 4 * lane);
+    }
+#pragma unroll
+    for (int i = 0; i < kShortSteps; ++i) {
+        const int a = 32 * i + 4 * warp + (lane >> 3);
+        float dot = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint4 x = kx[i][e >> 1];
+            const float4 k = half4(e & 1 ? make_uint2(x.z, x.w) : make_uint2(x.x, x.y));
+            dot = __fmaf_rn(qv[e].w, k.w, __fmaf_rn(qv[e].z, k.z, __fmaf_rn(qv[e].y, k.y, __fmaf_rn(qv[e].x, k.x, dot))));
+        }
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) dot = __fadd_rn(dot, __shfl_xor_sync(0xffffffffu, dot, o));
+        if (part == 0) ps[a] = a < n ? __fmul_rn(dot, scale.sign) : -INFINITY;
+    }
+    __syncthreads();
+    if (scores) {
+        float* sc = scores + rh * lds;
+        if (tid < v.len) sc[tid] = __fmul_rn(ps[tid], scale.abs);
+        if (tid >= kShortThreads - kMaxTree && tid - (kShortThreads - kMaxTree) < v.n_nodes) {
+            const int node = tid - (kShortThreads - kMaxTree);
+            float x = -INFINITY;
+            for (int a = 0; a < row.n_path; ++a)
+                if (row.path[a] == node) x = __fmul_rn(ps[v.len + a], scale.abs);
+            sc[v.len + node] = x;
+        }
+    }
+    // every warp has all keys' weights: key lane + 32 i in its lane
+    float p[kShortSteps], M = -INFINITY, L = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kShortSteps; ++i) {
+        p[i] = 32 * i + lane < n ? __fmul_rn(ps[32 * i + lane], scale.log2) : -INFINITY;
+        M = fmaxf(M, p[i]);
+    }
+    M = warp_max(M);
+    const float ref = M == -INFINITY ? 0.0f : M;
+#pragma unroll
+    for (int i = 0; i < kShortSteps; ++i) {
+        p[i] = tree_exp2(__fsub_rn(p[i], ref));
+        L = __fadd_rn(L, p[i]);
+    }
+    L = warp_sum_butterfly(L);
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const float f = __shfl_sync(0xffffffffu, p[i >> 2], (warp + 8 * i) & 31);
+        if (warp + 8 * i < n) axpy4(o, half4(vx[i]), f);
+    }
+    os[warp][lane] = o;
+    __syncthreads();
+    if (tid < kHeadDim) {
+        const float* of = &os[0][0].x + tid;
+        float O = of[0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) O = __fadd_rn(O, of[e * kHeadDim]);
+        const float val = __fdiv_rn(O, L);
+        out[rh * kHeadDim + tid] = val;
+        if (stats && tid == 0) *reinterpret_cast<float2*>(stats + 2 * rh) = make_float2(__fmul_rn(M, scale.natural), L);
+        if (out_q) {
+            float dd;
+            const int code = q8_quantize_lane(val, &dd);
+            out_q[rh * kHeadDim + tid] = (int8_t)code;
+            if (lane == 0) out_d[(rh * kHeadDim + tid) / 32] = dd;
+        }
+    }
+}
+
 cudaError_t launch_tree_attention(const float* q, const TreeBatch& b, int Hq, int Hkv, float scale, void* part,
                                   float* out, float* scores, int64_t lds, float* stats, int8_t* out_q, float* out_d,
                                   cudaStream_t s)
@@ -817,12 +939,19 @@ cudaError_t launch_tree_attention(const float* q, const TreeBatch& b, int Hq, in
                                 kTreeSmem, s, maps, q, b, Hq, Hkv, (int)units, runs, sc, part_o, part_ml, scores, lds);
         if (e != cudaSuccess) return e;
         count_launches(1);
+        // right behind the chunks: it starts on what their launch waited for
+        e = launch_pdl(tree_merge_kernel, dim3(Hq, b.n_long), dim3(kHeadDim), s, q, b, Hq, Hkv, sc, (const float*)part_o,
+                       (const float*)part_ml, out, scores, lds, stats, out_q, out_d);
+        if (e != cudaSuccess) return e;
+        count_launches(1);
     }
-    const cudaError_t e =
-        launch_pdl(tree_merge_kernel, dim3(Hq, b.n_row), dim3(kHeadDim), s, q, b, Hq, Hkv, sc,
-                   (const float*)part_o, (const float*)part_ml, out, scores, lds, stats, out_q, out_d, (int)units);
-    count_launches(1);
-    return e;
+    if (b.n_short > 0) {
+        const cudaError_t e = launch_pdl(tree_short_kernel, dim3(Hq, b.n_short), dim3(kShortThreads), s, q, b, Hq, Hkv, sc,
+                                         out, scores, lds, stats, out_q, out_d);
+        if (e != cudaSuccess) return e;
+        count_launches(1);
+    }
+    return cudaSuccess;
 }
 
 }  // namespace luce

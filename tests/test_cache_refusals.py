@@ -54,10 +54,14 @@ def test_tree_attention_refuses_arguments(lib, want, kw):
     (E, [view(parent=[0, 0])]), (E, [view(parent=[-1, 1])]), (E, [view(parent=[-2, 0])]), (E, [view(parent=[-1, 5])]),
     (E, [view(k=0)]), (E, [view(v=0)]), (E, [view(k=P + 8)]),
     (E, [view(tok=120)]), (E, [view(tok=132)]), (E, [view(head=4096 * 128 - 8)]), (E, [view(head=4096 * 128 + 4)]),
-    (E, [view(tok=1 << 33, head=1 << 37)]),
+    (E, [view(tok=1 << 33, head=1 << 37)]), (E, [view(tok=1 << 31, cap=1 << 10, head=1 << 41)]),
 ])
 def test_tree_attention_refuses_views(lib, want, views):
     assert attn(lib, views) == want and lib.luce_last_error()
+
+
+def test_tree_attention_refuses_a_span_beyond_the_maps(lib):
+    assert attn(lib, [view(tok=1 << 30, cap=1 << 9)], Hkv=1) == E and b"2^38" in lib.luce_last_error()
 
 
 def test_tree_attention_null_views(lib):
