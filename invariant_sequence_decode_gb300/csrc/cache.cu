@@ -150,7 +150,7 @@ constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictBins = 2048;
 constexpr int kEvictSlice = 16352;  // most keys of a CTA: 8 CTAs hold 130,816
 constexpr int kEvictMove = 8;   // pairs of rows in flight per warp
-constexpr int kEvictAhead = 8;  // keys in flight per thread
+constexpr int kEvictAhead = 16;  // keys in flight per thread
 
 __device__ __forceinline__ uint32_t evict_rank(float a, int pos, const EvictSlot& sl)
 {
@@ -296,9 +296,11 @@ kv_evict_kernel(const __grid_constant__ EvictBatch b, int slice)
         int* mine = hist[pass & 1];
         if (pass > 0) {
             const int width = pass == 1 ? 11 : 10;
+            const uint32_t want = T >> (sh + width), bits = (1u << width) - 1;
+#pragma unroll 8
             for (int i = tid; i < nj; i += kEvictThreads) {
                 const uint32_t u = rank[i];
-                if (u >> (sh + width) == T >> (sh + width)) atomicAdd(&mine[(u >> sh) & ((1u << width) - 1)], 1);
+                if (u >> (sh + width) == want) atomicAdd(&mine[(u >> sh) & bits], 1);
             }
         }
         __syncthreads();
@@ -359,31 +361,27 @@ kv_evict_kernel(const __grid_constant__ EvictBatch b, int slice)
     for (int r = 0; r < C - 1; ++r)
         if (r < me) eq_far += evict_word<C>(&hist[0][T & 1023], r);
     int eq = 0, all;
-    for (int i = r0; i < r1; ++i) eq += rank[i] == T;
+    uint64_t low = 0, same_as = 0;  // the run's keys below T and equal to it, a bit each
+    static_assert(((kEvictSlice + kEvictThreads - 1) / kEvictThreads | 1) <= 64, "a run's keys are bits of a word");
+#pragma unroll 8
+    for (int i = r0; i < r1; ++i) {
+        const uint32_t u = rank[i];
+        low |= (uint64_t)(u < T) << (i - r0);
+        same_as |= (uint64_t)(u == T) << (i - r0);
+    }
+    eq = __popcll(same_as);
     const int eq_at = eq_far + block_prefix(eq, warp_sum, &all);
 
     // 3. holes from the list's front, comers from its back
-    int found = 0, e = eq_at;  // holes + 65536 comers, each at most kEvictSlice
-    for (int i = r0; i < r1; ++i) {
-        const uint32_t u = rank[i];
-        const bool leaves = u < T || (u == T && e >= stay);
-        e += u == T;
-        if (j0 + i < sl.budget) found += leaves;
-        else found += leaves ? 0 : 65536;
-    }
-    const int found_at = block_prefix(found, warp_sum, &all);
-    int h_at = found_at & 65535, c_at = found_at >> 16;
-    e = eq_at;
-    for (int i = r0; i < r1; ++i) {
-        const uint32_t u = rank[i];
-        const bool leaves = u < T || (u == T && e >= stay);
-        e += u == T;
-        if (j0 + i < sl.budget) {
-            if (leaves) list[h_at++] = j0 + i;
-        } else if (!leaves) {
-            list[slice - 1 - c_at++] = j0 + i;
-        }
-    }
+    // of the run's keys equal to T the first stay - eq_at stay
+    for (int k = min(max(stay - eq_at, 0), eq); k > 0; --k) same_as &= same_as - 1;
+    const uint64_t leave = low | same_as, in = r1 - r0 == 64 ? ~0ull : (1ull << (r1 - r0)) - 1;
+    const int split = min(max(sl.budget - (j0 + r0), 0), 64);  // the run's keys below the budget
+    const uint64_t below_budget = split == 64 ? ~0ull : (1ull << split) - 1;
+    uint64_t hs = leave & below_budget & in, cs = ~leave & ~below_budget & in;
+    const int found_at = block_prefix(__popcll(hs) + (__popcll(cs) << 16), warp_sum, &all);  // each at most kEvictSlice
+    for (int at = found_at & 65535; hs; hs &= hs - 1) list[at++] = j0 + r0 + __ffsll(hs) - 1;
+    for (int at = slice - 1 - (found_at >> 16); cs; cs &= cs - 1) list[at--] = j0 + r0 + __ffsll(cs) - 1;
     if (tid == 0) {
         n_hole = all & 65535;
         n_come = all >> 16;
