@@ -106,6 +106,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ unsigned int g_tree_wait_timeouts;
 
+constexpr int kStageRow = 20;  // floats from row to row: 16-byte pieces of eight rows in different banks
+
 struct TreeMaps {
     CUtensorMap k[4], v[4];
 };
@@ -397,6 +399,10 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
     __shared__ uint32_t tmem_at;
     __shared__ float mx[2][2][kTreeTile];  // a row's maxima of a tile's two halves, by tile parity
     __shared__ volatile int bail[4];       // a wait of the row quarter's warps expired
+    // A warp's 32 rows, 16 columns at a time, on their way between a row per
+    // thread and 64 bytes of a row per four threads: global loads and stores by
+    // a row per thread touch 32 lines an instruction (q's took 3,000 cycles)
+    __shared__ __align__(16) float stage[8][32 * kStageRow];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (warp == 9) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_at)),
@@ -456,11 +462,19 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
         const int half = warp >> 2, quad = warp & 3, row = 32 * quad + lane, GQ = Hq / Hkv;
         const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
         uint64_t o[32];                         // the chunk's sum, dims 64 half .. 64 half + 63
+        float* st = stage[warp];
+        const int piece = 4 * (lane & 3);       // of the row 8 i + lane / 4, i = 0..3, that this thread loads and stores
+        int far_row[4];                         // those rows' place in q and scores, from the view's head
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int rr = 32 * quad + 8 * e + (lane >> 2);
+            far_row[e] = rr / GQ * Hq + rr % GQ;
+        }
         int i = 0, last = -1, R = 0;
         bool ok = true, left = false;
         // the tile whose O is still to come: its correction of the sum before
         // it (none: the chunk's first), whether the warp has rows in it, where
-        // the sum goes after it
+        // the sums go after it
         float prev_alpha = 0.0f;
         bool prev_first = true, prev_live = false;
         float* prev_out = nullptr;
@@ -496,19 +510,34 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
         for (int u = u0; !left && u < u1; u += step) {
             const TreeUnit t = tree_unit(b, Hkv, u);
             const TreeView& v = b.view[t.view];
-            const size_t at_row = (size_t)(v.row0 + row / GQ) * Hq + t.g * GQ + row % GQ;
+            const int64_t head = (int64_t)v.row0 * Hq + t.g * GQ;
             if (t.view * Hkv + t.g != last) {  // (S of every tile of the last head is complete: its q is free)
                 last = t.view * Hkv + t.g;
                 R = v.n_nodes * GQ;
                 if (u == u0) pdl_wait();
                 if (32 * quad < R) {
-                    uint32_t hi[32], lo[32];
-                    const float* qr = q + at_row * kHeadDim + 64 * half;
+                    float4 x[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const float4 x = row < R ? ld_placed_f4(qr + 4 * e) : make_float4(0, 0, 0, 0);
-                        tree_split(__fmul_rn(x.x, scale.sign), __fmul_rn(x.y, scale.sign), hi[2 * e], lo[2 * e]);
-                        tree_split(__fmul_rn(x.z, scale.sign), __fmul_rn(x.w, scale.sign), hi[2 * e + 1], lo[2 * e + 1]);
+                        const bool in = 32 * quad + 8 * (e & 3) + (lane >> 2) < R;
+                        x[e] = in ? ld_placed_f4(q + (head + far_row[e & 3]) * kHeadDim + 64 * half + 16 * (e >> 2) + piece)
+                                  : make_float4(0, 0, 0, 0);
+                    }
+                    uint32_t hi[32], lo[32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            *reinterpret_cast<float4*>(st + (8 * e + (lane >> 2)) * kStageRow + piece) = x[4 * c + e];
+                        __syncwarp();
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float4 y = *reinterpret_cast<const float4*>(st + lane * kStageRow + 4 * e);
+                            const int at = 8 * c + 2 * e;
+                            tree_split(__fmul_rn(y.x, scale.sign), __fmul_rn(y.y, scale.sign), hi[at], lo[at]);
+                            tree_split(__fmul_rn(y.z, scale.sign), __fmul_rn(y.w, scale.sign), hi[at + 1], lo[at + 1]);
+                        }
+                        __syncwarp();
                     }
                     tm_st32(lanes + kColQ + 32 * half, hi);
                     tm_st32(lanes + kColQ + 64 + 32 * half, lo);
@@ -517,9 +546,9 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
                 tm_before();
                 mbar_arrive(&bar.q_full);
             }
-            const bool live = 32 * quad < R, valid = row < R;
-            const int64_t pr = v.part0 + ((int64_t)t.c * Hkv + t.g) * R + row;
-            float* sc = scores && valid ? scores + at_row * lds + t.key0 + 64 * half : nullptr;
+            const bool live = 32 * quad < R;
+            const int64_t pr = v.part0 + ((int64_t)t.c * Hkv + t.g) * R;  // the chunk's first row of results
+            float* sc = scores && live ? scores + head * lds + t.key0 + 64 * half : nullptr;
             float m = -INFINITY, l = 0.0f;  // m: a power of two's exponent
             for (int k = 0; k < t.tiles; ++k, ++i) {
                 const int n = min(kTreeTile, t.nkey - k * kTreeTile);  // keys of the tile
@@ -563,18 +592,32 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
                     alpha = tree_exp2(__fsub_rn(m, at));  // 0 for m = -inf
                     m = top;
                     if (sc) {
-                        float* to = sc + k * kTreeTile;
 #pragma unroll
-                        for (int e = 0; e < 64; e += 4) {
-                            const float4 x = make_float4(__fmul_rn(s[e], scale.abs), __fmul_rn(s[e + 1], scale.abs),
-                                                         __fmul_rn(s[e + 2], scale.abs), __fmul_rn(s[e + 3], scale.abs));
-                            if (64 * half + e + 3 < n) {
-                                *reinterpret_cast<float4*>(to + e) = x;
-                            } else {
-                                if (64 * half + e < n) to[e] = x.x;
-                                if (64 * half + e + 1 < n) to[e + 1] = x.y;
-                                if (64 * half + e + 2 < n) to[e + 2] = x.z;
+                        for (int c = 0; c < 4; ++c) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float* x = s + 16 * c + 4 * e;
+                                *reinterpret_cast<float4*>(st + lane * kStageRow + 4 * e) =
+                                    make_float4(__fmul_rn(x[0], scale.abs), __fmul_rn(x[1], scale.abs),
+                                                __fmul_rn(x[2], scale.abs), __fmul_rn(x[3], scale.abs));
                             }
+                            __syncwarp();
+                            const int at = 16 * c + piece, in = n - 64 * half - at;  // keys of the tile from this piece on
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int rr = 8 * e + (lane >> 2);
+                                if (32 * quad + rr >= R) break;
+                                const float4 x = *reinterpret_cast<const float4*>(st + rr * kStageRow + piece);
+                                float* to = sc + far_row[e] * lds + k * kTreeTile + at;
+                                if (in >= 4) {
+                                    *reinterpret_cast<float4*>(to) = x;
+                                } else {
+                                    if (in > 0) to[0] = x.x;
+                                    if (in > 1) to[1] = x.y;
+                                    if (in > 2) to[2] = x.z;
+                                }
+                            }
+                            __syncwarp();
                         }
                     }
                     const uint64_t c2 = pair(scale.log2, scale.log2), m2 = pair(-at, -at);
@@ -602,10 +645,11 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
                 prev_alpha = alpha;
                 prev_first = k == 0;
                 prev_live = live;
-                prev_out = valid && k + 1 == t.tiles ? part_o + pr * kHeadDim + 64 * half : nullptr;
-                if (prev_out) {
-                    if (half == 0) part_ml[4 * pr] = m;
-                    part_ml[4 * pr + 1 + half] = l;
+                prev_out = nullptr;
+                if (row < R && k + 1 == t.tiles) {
+                    prev_out = part_o + (pr + row) * kHeadDim + 64 * half;
+                    if (half == 0) part_ml[4 * (pr + row)] = m;
+                    part_ml[4 * (pr + row) + 1 + half] = l;
                 }
             }
         }
