@@ -130,21 +130,25 @@ struct TreeBars {
     uint64_t q_full;       // q's parts are in place
 };
 
-// A chunk of a (view, KV head), in the order view, head, chunk.
-struct TreeUnit {
-    int view, g, c, tiles, key0, nkey;
+// Chunks of one (view, KV head) that a CTA takes one after the other: `chunks`
+// of them from number c on, in the order view, head, chunk.
+struct TreeRun {
+    int view, g, c, chunks, tiles, key0, nkey;
 };
 
-__device__ __forceinline__ TreeUnit tree_unit(const TreeBatch& b, int Hkv, int u)
+// The run at chunk u of all: up to chunk `end` of all, or of one chunk.
+__device__ __forceinline__ TreeRun tree_run(const TreeBatch& b, int Hkv, int u, int end)
 {
-    TreeUnit t;
+    TreeRun t;
+    const int u0 = u;
     t.view = 0;
     while (t.view + 1 < b.n_view && u >= Hkv * b.view[t.view].n_chunk) u -= Hkv * b.view[t.view++].n_chunk;
     const TreeView& v = b.view[t.view];
     t.g = u / v.n_chunk;
     t.c = u - t.g * v.n_chunk;
+    t.chunks = min(v.n_chunk - t.c, end - u0);
     t.key0 = t.c * v.chunk;
-    t.nkey = min(v.chunk, v.len - t.key0);
+    t.nkey = min(t.chunks * v.chunk, v.len - t.key0);
     t.tiles = (t.nkey + kTreeTile - 1) / kTreeTile;
     return t;
 }
@@ -287,8 +291,9 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, int
 __device__ int tree_produce(const TreeMaps& maps, const TreeBatch& b, int Hkv, int u0, int u1, int step, uint8_t* tiles, TreeBars& bar)
 {
     int i = 0;
-    for (int u = u0; u < u1; u += step) {
-        const TreeUnit t = tree_unit(b, Hkv, u);
+    for (int u = u0, next; u < u1; u = next) {
+        const TreeRun t = tree_run(b, Hkv, u, step ? u + 1 : u1);
+        next = step ? u + step : u + t.chunks;
         const TreeView& v = b.view[t.view];
         if (u == u0) {
             pdl_wait();
@@ -360,8 +365,9 @@ __device__ void tree_products(const TreeBatch& b, int Hkv, int u0, int u1, int s
         tree_commit_mma(&bar.v_empty[st], elected);
         return true;
     };
-    for (int u = u0; u < u1; u += step) {
-        const TreeUnit t = tree_unit(b, Hkv, u);
+    for (int u = u0, next; u < u1; u = next) {
+        const TreeRun t = tree_run(b, Hkv, u, step ? u + 1 : u1);
+        next = step ? u + step : u + t.chunks;
         if (t.view * Hkv + t.g != last) {
             last = t.view * Hkv + t.g;
             if (!__all_sync(0xffffffffu, mbar_wait(&bar.q_full, heads++ & 1, late))) return;
@@ -441,7 +447,7 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
     if (runs) {
         u0 = (int)((int64_t)units * blockIdx.x / gridDim.x);
         u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
-        step = 1;
+        step = 0;
     }
     unsigned int* late = &g_tree_wait_timeouts;
 
@@ -507,8 +513,9 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
             }
             return done;
         };
-        for (int u = u0; !left && u < u1; u += step) {
-            const TreeUnit t = tree_unit(b, Hkv, u);
+        for (int u = u0, next; !left && u < u1; u = next) {
+            const TreeRun t = tree_run(b, Hkv, u, step ? u + 1 : u1);
+            next = step ? u + step : u + t.chunks;
             const TreeView& v = b.view[t.view];
             const int64_t head = (int64_t)v.row0 * Hq + t.g * GQ;
             if (t.view * Hkv + t.g != last) {  // (S of every tile of the last head is complete: its q is free)
@@ -547,11 +554,17 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
                 mbar_arrive(&bar.q_full);
             }
             const bool live = 32 * quad < R;
-            const int64_t pr = v.part0 + ((int64_t)t.c * Hkv + t.g) * R;  // the chunk's first row of results
+            const int ct = v.chunk / kTreeTile;
+            int kc = 0;                                                   // the chunk's tiles so far
+            int64_t pr = v.part0 + ((int64_t)t.c * Hkv + t.g) * R + row;  // the chunk's row of results
             float* sc = scores && live ? scores + head * lds + t.key0 + 64 * half : nullptr;
             float m = -INFINITY, l = 0.0f;  // m: a power of two's exponent
             for (int k = 0; k < t.tiles; ++k, ++i) {
                 const int n = min(kTreeTile, t.nkey - k * kTreeTile);  // keys of the tile
+                if (kc == 0) {
+                    m = -INFINITY;
+                    l = 0.0f;
+                }
                 ok = ok && mbar_wait(&bar.s_full[i & 1], (i >> 1) & 1, late);
                 tm_after();
                 if (n < kTreeTile) {
@@ -643,13 +656,17 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
                 mbar_arrive(&bar.p_full[i & 1]);
                 if (i > 0) ok = take(i - 1);
                 prev_alpha = alpha;
-                prev_first = k == 0;
+                prev_first = kc == 0;
                 prev_live = live;
                 prev_out = nullptr;
-                if (row < R && k + 1 == t.tiles) {
-                    prev_out = part_o + (pr + row) * kHeadDim + 64 * half;
-                    if (half == 0) part_ml[4 * (pr + row)] = m;
-                    part_ml[4 * (pr + row) + 1 + half] = l;
+                if (++kc == ct || k + 1 == t.tiles) {  // the chunk's last tile
+                    kc = 0;
+                    if (row < R) {
+                        prev_out = part_o + pr * kHeadDim + 64 * half;
+                        if (half == 0) part_ml[4 * pr] = m;
+                        part_ml[4 * pr + 1 + half] = l;
+                    }
+                    pr += (int64_t)Hkv * R;
                 }
             }
         }
