@@ -180,6 +180,15 @@ __device__ __forceinline__ void tree_commit_mma(uint64_t* bar, uint32_t elected)
                  : "memory");
 }
 
+// One arrival for the warp, behind what all of its threads have done to tensor
+// memory (32 arrivals of their own would queue at the barrier's word).
+__device__ __forceinline__ void warp_arrive(uint64_t* bar)
+{
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 __device__ __forceinline__ uint32_t elect_one()
 {
     uint32_t e;
@@ -424,12 +433,12 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.s_full[i], 1);
-            mbar_init(&bar.p_full[i], 256);
+            mbar_init(&bar.p_full[i], 8);
             mbar_init(&bar.p_read[i], 1);
         }
         mbar_init(&bar.o_full, 1);
-        mbar_init(&bar.o_free, 256);
-        mbar_init(&bar.q_full, 256);
+        mbar_init(&bar.o_free, 8);
+        mbar_init(&bar.q_full, 8);
         for (int i = 0; i < 4; ++i) bail[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -495,13 +504,11 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
                 const uint64_t al = pair(prev_alpha, prev_alpha);
                 float x[64];
                 tm_ld64(lanes + kColO + 64 * half, x);
-                tm_before();
-                mbar_arrive(&bar.o_free);  // (the next tile's P V waits for this)
+                warp_arrive(&bar.o_free);  // (the next tile's P V waits for this)
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] = fma2(o[e], al, pair(x[2 * e], x[2 * e + 1]));
             } else {
-                tm_before();
-                mbar_arrive(&bar.o_free);
+                warp_arrive(&bar.o_free);
             }
             if (prev_out && done) {
 #pragma unroll
@@ -548,10 +555,15 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
                     }
                     tm_st32(lanes + kColQ + 32 * half, hi);
                     tm_st32(lanes + kColQ + 64 + 32 * half, lo);
-                    tm_wait_st();
+                } else {
+                    // no rows here: products of zeros draw less power than of
+                    // what happens to lie there
+                    uint32_t zero[32] = {};
+                    tm_st32(lanes + kColQ + 32 * half, zero);
+                    tm_st32(lanes + kColQ + 64 + 32 * half, zero);
                 }
-                tm_before();
-                mbar_arrive(&bar.q_full);
+                tm_wait_st();
+                warp_arrive(&bar.q_full);
             }
             const bool live = 32 * quad < R;
             const int ct = v.chunk / kTreeTile;
@@ -652,8 +664,7 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
                     asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
                     if ((left = bail[quad])) break;
                 }
-                tm_before();
-                mbar_arrive(&bar.p_full[i & 1]);
+                warp_arrive(&bar.p_full[i & 1]);
                 if (i > 0) ok = take(i - 1);
                 prev_alpha = alpha;
                 prev_first = kc == 0;
