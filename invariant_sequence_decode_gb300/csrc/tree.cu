@@ -19,13 +19,16 @@
 // two f16 parts each, x = hi + lo, both parts multiplied in: the products then
 // carry 2^-22 of q and p, the size of an fp32 sum's own error, where one f16
 // part would lose 2^-11.
-// The kernel is bound by reading K and V (64 KB a tile; at full rate an SM gets
-// one in about 2,800 cycles, the four products take about 1,024), so what
-// matters is that loads never pause: one CTA an SM walks its share of all
-// chunks, a producer warp keeps up to six 32 KB tiles in flight by TMA, one
-// thread issues the products, and 256 threads (two to a row, 64 keys each)
-// turn S into P in place in tensor memory and add each tile's O into registers
-// with the running maximum's correction.
+// Long prefixes are bound by reading K and V (64 KB a tile: at full rate an SM
+// gets one in about 2,860 cycles), with the products (2,080 cycles) and the
+// softmax (1,050 of them exponentials) close behind, so what matters is that
+// none of the three pauses: one CTA an SM walks its share of all chunks, a
+// producer warp keeps up to six 32 KB tiles in flight by TMA, one warp issues
+// the products, and 256 threads (two to a row, 64 keys each) turn S into P in
+// place in tensor memory and add each tile's O into registers with the running
+// maximum's correction; a tile takes 2,650 cycles.  16 nodes of 40 heads over
+// 130,800 keys of 8 heads: 102 us, 86 alone at 6.2 TB/s.  Short ones are bound by
+// one tile's chain (K, S, softmax, P V, O: 6 us) and the merge (3.5 us).
 #include <limits.h>
 
 #include <algorithm>
@@ -51,7 +54,7 @@ constexpr int kTreeCtas = 152;  // the CTAs that a cut aims at: one per multipro
 // one more (its q, its results); one view's chunks, Hkv heads, go to kTreeCtas
 // CTAs in rounds.  Of the cuts that fill 1, 2, 3 or 4 rounds the cheapest is
 // taken, the one with fewer chunks of equals: 130,800 keys of 8 heads make 19
-// chunks of 54 tiles (8-tile chunks, 128 a head: 117 against 93 us).
+// chunks of 54 tiles (8-tile chunks, 128 a head: 117 against 97 us).
 static int tree_chunk_tiles(int nt, int Hkv)
 {
     int best = nt, least = INT_MAX;
@@ -128,6 +131,7 @@ struct TreeBars {
     uint64_t o_full;       // O of a tile is complete
     uint64_t o_free;       // and has been read
     uint64_t q_full;       // q's parts are in place
+    uint64_t done;         // every product that was issued is complete
 };
 
 // Chunks of one (view, KV head) that a CTA takes one after the other: `chunks`
@@ -374,32 +378,38 @@ __device__ void tree_products(const TreeBatch& b, int Hkv, int u0, int u1, int s
         tree_commit_mma(&bar.v_empty[st], elected);
         return true;
     };
-    for (int u = u0, next; u < u1; u = next) {
-        const TreeRun t = tree_run(b, Hkv, u, step ? u + 1 : u1);
-        next = step ? u + step : u + t.chunks;
-        if (t.view * Hkv + t.g != last) {
-            last = t.view * Hkv + t.g;
-            if (!__all_sync(0xffffffffu, mbar_wait(&bar.q_full, heads++ & 1, late))) return;
-        }
-        for (int k = 0; k < t.tiles; ++k, ++i) {
-            const int st = i % kTreeStages;
-            // (the first two buffers are free)
-            const bool there = mbar_wait(&bar.k_full[st], (i / kTreeStages) & 1, late) &&
-                               mbar_wait(&bar.p_read[i & 1], ((i >> 1) & 1) ^ 1, late);
-            if (!__all_sync(0xffffffffu, there)) return;
-            tm_after();
-            const uint32_t s = tmem + kColS + 128 * (i & 1);
-            const uint64_t d = tree_desc(tiles + st * kTreeTileBytes, 16, 1024);
+    auto all = [&] {
+        for (int u = u0, next; u < u1; u = next) {
+            const TreeRun t = tree_run(b, Hkv, u, step ? u + 1 : u1);
+            next = step ? u + step : u + t.chunks;
+            if (t.view * Hkv + t.g != last) {
+                last = t.view * Hkv + t.g;
+                if (!__all_sync(0xffffffffu, mbar_wait(&bar.q_full, heads++ & 1, late))) return;
+            }
+            for (int k = 0; k < t.tiles; ++k, ++i) {
+                const int st = i % kTreeStages;
+                // (the first two buffers are free)
+                const bool there = mbar_wait(&bar.k_full[st], (i / kTreeStages) & 1, late) &&
+                                   mbar_wait(&bar.p_read[i & 1], ((i >> 1) & 1) ^ 1, late);
+                if (!__all_sync(0xffffffffu, there)) return;
+                tm_after();
+                const uint32_t s = tmem + kColS + 128 * (i & 1);
+                const uint64_t d = tree_desc(tiles + st * kTreeTileBytes, 16, 1024);
 #pragma unroll 4
-            for (int ks = 0; ks < 16; ++ks)  // the low parts first, as above
-                tree_mma(s, tmem + kColQ + 8 * (ks ^ 8), d + (ks >> 2 & 1) * (kTreeTileBytes / 32) + 2 * (ks & 3), idesc_s,
-                         ks > 0, elected);
-            tree_commit_mma(&bar.s_full[i & 1], elected);
-            tree_commit_mma(&bar.k_empty[st], elected);
-            if (i > 0 && !values(i - 1)) return;
+                for (int ks = 0; ks < 16; ++ks)  // the low parts first, as above
+                    tree_mma(s, tmem + kColQ + 8 * (ks ^ 8), d + (ks >> 2 & 1) * (kTreeTileBytes / 32) + 2 * (ks & 3),
+                             idesc_s, ks > 0, elected);
+                tree_commit_mma(&bar.s_full[i & 1], elected);
+                tree_commit_mma(&bar.k_empty[st], elected);
+                if (i > 0 && !values(i - 1)) return;
+            }
         }
-    }
-    if (i > 0) values(i - 1);
+        if (i > 0) values(i - 1);
+    };
+    all();
+    // also after an expired wait, tensor memory is not freed under a product
+    tree_commit_mma(&bar.done, elected);
+    mbar_wait(&bar.done, 0, late);
 }
 
 // One CTA an SM, each with its share of all chunks.
@@ -439,6 +449,7 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
         mbar_init(&bar.o_full, 1);
         mbar_init(&bar.o_free, 8);
         mbar_init(&bar.q_full, 8);
+        mbar_init(&bar.done, 1);
         for (int i = 0; i < 4; ++i) bail[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -582,9 +593,9 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
                 if (n < kTreeTile) {
                     // what lies behind the last key may be anything: its weight
                     // is 0, but 0 times a NaN would not be
-                    const int st = i % kTreeStages;
-                    ok = ok && mbar_wait(&bar.v_full[st], (i / kTreeStages) & 1, late);
-                    uint8_t* vt = tiles + (kTreeStages + st) * kTreeTileBytes;
+                    const int slot = i % kTreeStages;
+                    ok = ok && mbar_wait(&bar.v_full[slot], (i / kTreeStages) & 1, late);
+                    uint8_t* vt = tiles + (kTreeStages + slot) * kTreeTileBytes;
                     for (int e = tid; ok && e < (kTreeTile - n) * 16; e += 256)
                         *reinterpret_cast<uint4*>(vt + (e & 8) * (kTreeTileBytes / 16) + (n + (e >> 4)) * 128 + (e & 7) * 16) =
                             make_uint4(0, 0, 0, 0);
@@ -682,9 +693,6 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
             }
         }
         if (!left && i > 0) ok = take(i - 1) && ok;
-        // after an expired wait products may still be running: wait once more
-        // (bounded) for the last of them before tensor memory is freed
-        if (!(ok && !left) && tid == 0 && i > 0) mbar_wait(&bar.o_full, (i - 1) & 1, late);
     }
     tm_before();
     __syncthreads();
