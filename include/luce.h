@@ -665,7 +665,8 @@ typedef struct luce_commit_slot {
  *          luce_tree_attn gave for each layer.  Both may be NULL when no slot
  *          has acc.
  * No two slots share a cache, acc or pos.  D == 128, Hq % Hkv == 0,
- * Hq / Hkv <= 8, 1 <= n_seq <= LUCE_MAX_SEQ, n_layers >= 1.
+ * Hq / Hkv <= 8, 1 <= n_seq <= LUCE_MAX_SEQ, n_layers >= 1,
+ * len + n_path <= LUCE_MAX_KEYS.
  */
 int luce_tree_commit(const luce_commit_slot* slots, int n_seq, int n_layers, int Hq, int Hkv, int D,
                      const float* scores, int n_rows, int64_t lds, const float* stats, void* stream);

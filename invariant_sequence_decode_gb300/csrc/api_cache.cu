@@ -108,7 +108,7 @@ static int run_tree(TreeBatch& b, const bool* covered, const float* q, int Hq, i
                     float* scores, int64_t lds, float* stats, void* ws, size_t ws_bytes, void* stream, const char* who)
 {
     for (int r = 0; r < b.n_row; ++r) REQUIRE(covered[r], LUCE_EINVAL, "%s: row %d belongs to no view", who, r);
-    const size_t need = tree_part_bytes(tree_chunks(b, Hq, Hkv));
+    const size_t need = std::max<size_t>(256, tree_part_bytes(tree_chunks(b, Hq, Hkv)));
     REQUIRE(ws_bytes >= need, LUCE_ENOSPACE, "%s: workspace %zu bytes < %zu needed", who, ws_bytes, need);
     return cuda_status(launch_tree_attention(q, b, Hq, Hkv, scale, ws, out, scores, lds, stats, nullptr, nullptr,
                                              (cudaStream_t)stream),
@@ -198,6 +198,22 @@ static ByteRange range_of(const void* p, int64_t bytes, int slot, const char* wh
     return ByteRange{(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes, slot, what, written, pair};
 }
 
+static const char* const kPoolK = "K pool";
+static const char* const kPoolV = "V pool";
+
+// Slots may share a pool, each with its own rows; pools that are not one overlap
+// nothing.
+static void add_pool(ByteRange* r, int* nr, const void* p, int64_t bytes, int slot, const char* what)
+{
+    const ByteRange n = range_of(p, bytes, slot, what, true);
+    for (int i = 0; i < *nr; ++i)
+        if (r[i].what == what && r[i].lo == n.lo) {
+            r[i].hi = std::max(r[i].hi, n.hi);
+            return;
+        }
+    r[(*nr)++] = n;
+}
+
 static int check_layers(int n_seq, int n_layers, int Hkv, int D, const void* slots, const char* who)
 {
     REQUIRE(slots, LUCE_EINVAL, "%s: null slots", who);
@@ -241,6 +257,8 @@ static int add_commit_slot(CommitSlot& o, const CommitArgs& c, int s, int64_t he
     REQUIRE(c.n_path == 0 || c.path, LUCE_EINVAL, "%s: slot %d has a null path", who, s);
     REQUIRE(c.len >= 0 && c.cap >= 1 && c.len <= c.cap, LUCE_EINVAL, "%s: slot %d len=%d outside [0, cap=%d]", who, s,
             c.len, c.cap);
+    REQUIRE(c.len <= LUCE_MAX_KEYS - c.n_path, LUCE_EUNSUPPORTED, "%s: slot %d would hold %d + %d keys (at most %d)", who, s,
+            c.len, c.n_path, LUCE_MAX_KEYS);
     REQUIRE(c.pos0 >= 0 && c.pos0 <= INT32_MAX - LUCE_MAX_TREE, LUCE_EINVAL, "%s: slot %d pos0=%d", who, s, c.pos0);
     int last = -1;
     for (int i = 0; i < c.n_path; ++i) {
@@ -329,7 +347,7 @@ int luce_tree_commit_paged(const luce_paged_commit_slot* slots, int n_seq, int n
     if (rc) return rc;
     CommitBatch b{};
     b.n_slot = n_seq;
-    ByteRange r[2 * LUCE_MAX_SEQ + 2];
+    ByteRange r[4 * LUCE_MAX_SEQ + 2];
     int nr = 0;
     bool any_acc = false;
     const int64_t heads = (int64_t)n_layers * Hkv, page = heads * LUCE_PAGE_KEYS * D;
@@ -337,7 +355,6 @@ int luce_tree_commit_paged(const luce_paged_commit_slot* slots, int n_seq, int n
         const luce_paged_commit_slot& c = slots[s];
         REQUIRE(c.k_pool && c.v_pool && aligned(c.k_pool, 16) && aligned(c.v_pool, 16), LUCE_EINVAL,
                 "%s: slot %d pool null or not 16-byte aligned", who, s);
-        REQUIRE(c.k_pool != c.v_pool, LUCE_EINVAL, "%s: slot %d has one pool for K and V", who, s);
         REQUIRE(c.n_pages >= 1 && c.n_table >= 0 && (c.table_host || c.n_path == 0), LUCE_EINVAL,
                 "%s: slot %d has no pages or no table", who, s);
         const CommitArgs a{c.len, c.cap, c.n_path, c.row0, c.path, c.acc, c.pos, c.pos0};
@@ -346,6 +363,8 @@ int luce_tree_commit_paged(const luce_paged_commit_slot* slots, int n_seq, int n
         o.k = reinterpret_cast<__half*>(c.k_pool);
         o.v = reinterpret_cast<__half*>(c.v_pool);
         o.head_step = (int64_t)LUCE_PAGE_KEYS * D;
+        add_pool(r, &nr, c.k_pool, page * c.n_pages * 2, s, kPoolK);
+        add_pool(r, &nr, c.v_pool, page * c.n_pages * 2, s, kPoolV);
         for (int i = 0; i < c.n_path; ++i)
             for (int to = 0; to < 2; ++to) {
                 const int key = c.len + (to ? i : c.path[i]), at = key / LUCE_PAGE_KEYS;
@@ -448,7 +467,7 @@ int luce_kv_evict_paged(const luce_paged_evict_slot* slots, int n_seq, int n_lay
     if (rc) return rc;
     EvictBatch b{};
     b.n_slot = n_seq;
-    ByteRange r[4 * LUCE_MAX_SEQ];
+    ByteRange r[6 * LUCE_MAX_SEQ];
     int nr = 0;
     bool any = false;
     const int64_t heads = (int64_t)n_layers * Hkv;
@@ -456,7 +475,6 @@ int luce_kv_evict_paged(const luce_paged_evict_slot* slots, int n_seq, int n_lay
         const luce_paged_evict_slot& e = slots[s];
         REQUIRE(e.k_pool && e.v_pool && aligned(e.k_pool, 16) && aligned(e.v_pool, 16), LUCE_EINVAL,
                 "%s: slot %d pool null or not 16-byte aligned", who, s);
-        REQUIRE(e.k_pool != e.v_pool, LUCE_EINVAL, "%s: slot %d has one pool for K and V", who, s);
         REQUIRE(e.table && aligned(e.table, 4) && e.n_pages >= 1, LUCE_EINVAL, "%s: slot %d has no pages or no table", who,
                 s);
         const EvictArgs a{e.acc, e.pos, e.acc_out, e.pos_out, e.len, e.cap, e.budget, e.sinks, e.recent, e.next_pos};
@@ -470,6 +488,8 @@ int luce_kv_evict_paged(const luce_paged_evict_slot* slots, int n_seq, int n_lay
         REQUIRE(heads * LUCE_PAGE_KEYS * e.n_pages < ((int64_t)1 << 31), LUCE_EUNSUPPORTED,
                 "%s: slot %d pool has 2^31 rows or more", who, s);
         o.page_rows = (int32_t)(heads * LUCE_PAGE_KEYS);
+        add_pool(r, &nr, e.k_pool, heads * LUCE_PAGE_KEYS * D * 2 * e.n_pages, s, kPoolK);
+        add_pool(r, &nr, e.v_pool, heads * LUCE_PAGE_KEYS * D * 2 * e.n_pages, s, kPoolV);
     }
     if ((rc = check_apart(r, nr, who))) return rc;
     if (!any) return ok();

@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kFewThreads)
 kv_evict_few_kernel(const __grid_constant__ EvictBatch b)
 {
     __shared__ uint32_t low[2][kFewWarps], at[2][kFewWarps];  // a round's lowest rank of each warp, and its last index
-    __shared__ int hole[kFewKeys], come[kFewKeys];
+    __shared__ int hole[kFewKeys], come[kFewKeys], n_come;
     pdl_trigger();
     const EvictSlot& sl = b.slot[blockIdx.y];
     const int64_t lh = blockIdx.x;
@@ -547,10 +547,10 @@ kv_evict_few_kernel(const __grid_constant__ EvictBatch b)
         if (left < sl.budget) hole[below] = left;
         const uint32_t mask = __ballot_sync(0xffffffffu, stays);
         if (stays) come[__popc(mask & ((1u << lane) - 1))] = sl.budget + lane;
-        if (lane == 0) low[0][0] = __popc(mask);
+        if (lane == 0) n_come = __popc(mask);
     }
     __syncthreads();
-    const int m = (int)low[0][0];
+    const int m = n_come;
     uint4* base = reinterpret_cast<uint4*>((lane < 16 ? sl.k : sl.v) + lh * sl.head_step) + (lane & 15);
     for (int i = warp; i < m; i += kFewWarps) {
         const int to = hole[i], from = come[i];

@@ -121,7 +121,8 @@ ACC, POS, SC, ST = P + 2 * BIG, P + 3 * BIG, P + 4 * BIG, P + 5 * BIG
     (E, [slot(acc=ACC, row0=-1)], dict(scores=SC, rows=4, lds=16, stats=ST)),
     (E, [slot(acc=ACC, pos=ACC)], dict(scores=SC, rows=4, lds=16, stats=ST)),
     (E, [slot(acc=SC)], dict(scores=SC, rows=4, lds=16, stats=ST)),
-    (E, [slot(acc=ACC + 2)], dict(scores=SC, rows=4, lds=16, stats=ST)),
+    (E, [slot(acc=ACC + 2)], dict(scores=SC, rows=4, lds=16, stats=ST)), (E, [slot(acc=ACC)], dict(scores=SC, rows=4, lds=16, stats=ST + 4)),
+    (U, [slot(length=130815, cap=130900)], {}), (U, [slot(length=2 ** 30, cap=2 ** 31 - 1)], {}),
 ])
 def test_commit_refusals(lib, want, slots, kw):
     assert commit(lib, slots, **kw) == want and lib.luce_last_error()
@@ -221,6 +222,9 @@ def pcommit(lib, slots, L=2, Hq=8, Hkv=2, D=128, scores=None, rows=0, lds=0, sta
     (E, [pslot(length=399, path=(0, 1))], {}), (E, [pslot(), pslot()], {}), (E, [pslot(acc=ACC)], {}),
     (E, [pslot(path=(1, 3)), pslot(table=(3, 1), length=133, path=(0,))], {}),   # writes key 133's row, which the other reads
     (E, [pslot(acc=ACC, pos=ACC)], dict(scores=SC, rows=4, lds=136, stats=ST)),
+    (E, [pslot(pos=P + 256)], {}), (E, [pslot(acc=P + BIG)], dict(scores=SC, rows=4, lds=136, stats=ST)),       # within a pool
+    (E, [pslot(), pslot(k=P + 2 * 2 * 128 * 256, table=(3, 3, 3))], {}), (E, [pslot(), pslot(P + BIG, P, (3, 3, 3))], {}),
+    (U, [pslot(length=130815, cap=1 << 20, table=(0,) * 1023)], {}),
 ])
 def test_paged_commit_refusals(lib, want, slots, kw):
     assert pcommit(lib, slots, **kw) == want and lib.luce_last_error()
@@ -235,6 +239,7 @@ def peslot(k=P, v=P + BIG, table=P, acc=ACC, pos=POS, acc_out=ACC, pos_out=POS, 
     (U, peslot(), dict(D=64)), (E, peslot(k=0), {}), (E, peslot(v=P), {}), (E, peslot(table=0), {}), (E, peslot(table=P + 2), {}),
     (E, peslot(n_pages=0), {}), (E, peslot(acc=0), {}), (E, peslot(length=65), {}), (E, peslot(budget=0), {}),
     (E, peslot(sinks=6, recent=5), {}), (E, peslot(acc_out=POS), {}), (U, peslot(length=130817, cap=130900), {}),
+    (E, peslot(acc_out=P + 256), {}), (E, peslot(pos=P + BIG, pos_out=P + BIG), {}), (U, peslot(n_pages=1 << 22), {}),
 ])
 def test_paged_evict_refusals(lib, want, slot, kw):
     arr = (luce.PagedEvictSlotC * 1)(slot)
