@@ -987,7 +987,8 @@ class TreeAttention(_Prepared):
         _need(ws, torch.uint8, "ws")
         self._args = (q.data_ptr(), self._vc, n, Hq, int(n_kv_heads), D, float(scale), self.out.data_ptr(), _ptr(scores),
                       lds, _ptr(stats), ws.data_ptr(), ws.numel())
-        self._bind(getattr(load_library(), name), q.device, stream, (q, scores, stats, ws, trees))
+        caches = [(v.k_pool, v.v_pool, v.table) if paged else (v.k, v.v) for v in self.views]
+        self._bind(getattr(load_library(), name), q.device, stream, (q, scores, stats, ws, trees, caches))
 
     @staticmethod
     def _fits(length, cap):
@@ -1106,12 +1107,11 @@ def _kind(slots, flat, paged):
 class TreeCommit(_Prepared):
     """luce_tree_commit (or luce_tree_commit_paged, for PagedCommitSlots) with its
     arguments marshalled once: each call takes the slots' current ``len``,
-    ``path``, ``row0`` and ``pos0``.  ``scores`` [n_layers][n_rows][Hq][lds] and
+    ``path``, ``row0``, ``pos0`` and ``table``.  ``scores`` [n_layers][n_rows][Hq][lds] and
     ``stats`` [n_layers][n_rows][Hq][2] (the n_layers dimension may be left out
     for one layer) are what luce_tree_attn gave."""
 
     def __init__(self, slots: Sequence[CommitSlot], n_q_heads: int, scores=None, stats=None, stream=None):
-        import numpy as np
         import torch
         self.slots = list(slots)
         paged = _kind(self.slots, CommitSlot, PagedCommitSlot)
@@ -1126,7 +1126,7 @@ class TreeCommit(_Prepared):
                 raise ValueError("scores, stats: expected [n_layers][n_rows][Hq][lds] and [n_layers][n_rows][Hq][2]")
         n = len(self.slots)
         self._sc = ((PagedCommitSlotC if paged else CommitSlotC) * n)()
-        tables = []
+        caches = []
         for i, s in enumerate(self.slots):
             if paged:
                 _pools(s.k_pool, s.v_pool, L, Hkv, f"slots[{i}]")
@@ -1139,12 +1139,10 @@ class TreeCommit(_Prepared):
             if s.pos is not None:
                 _state(s.pos, torch.int32, L, Hkv, cap, f"slots[{i}].pos")
             _same_device(first, k, v, s.acc, s.pos, scores, stats)
+            caches.append((k, v, s.acc, s.pos))
             if paged:
-                table = np.ascontiguousarray(s.table, dtype=np.int32)
-                tables.append(table)
-                self._sc[i] = PagedCommitSlotC(k.data_ptr(), v.data_ptr(),
-                                               table.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)), len(table),
-                                               k.shape[0], s.len, cap, 0, s.row0, None, _ptr(s.acc), _ptr(s.pos), s.pos0)
+                self._sc[i] = PagedCommitSlotC(k.data_ptr(), v.data_ptr(), None, 0, k.shape[0], s.len, cap, 0, s.row0, None,
+                                               _ptr(s.acc), _ptr(s.pos), s.pos0)
             else:
                 self._sc[i] = CommitSlotC(k.data_ptr(), v.data_ptr(), s.len, cap, 0, s.row0, None, _ptr(s.acc),
                                           _ptr(s.pos), s.pos0)
@@ -1153,9 +1151,21 @@ class TreeCommit(_Prepared):
         self._args = (self._sc, n, L, int(n_q_heads), Hkv, HEAD_DIM, _ptr(scores), n_rows, lds, _ptr(stats))
         lib = load_library()
         self._bind(lib.luce_tree_commit_paged if paged else lib.luce_tree_commit, first.device, stream,
-                   (scores, stats, tables))
+                   (scores, stats, caches))
+        self._tables = [None] * n if paged else None
+
+    def _take_tables(self):
+        import numpy as np
+        for i, s in enumerate(self.slots):
+            t = np.asarray(s.table)
+            if self._tables[i] is None or not np.array_equal(t, self._tables[i]):
+                self._tables[i] = t = np.array(t, dtype=np.int32)
+                self._items[i].table_host = t.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))
+                self._items[i].n_table = t.size
 
     def __call__(self):
+        if self._tables is not None:
+            self._take_tables()
         for i, s in enumerate(self.slots):
             now = (s.len, s.row0, s.pos0, *s.path)
             if now != self._now[i]:
@@ -1175,8 +1185,8 @@ def luce_tree_commit(slots: Sequence[CommitSlot], n_q_heads: int, scores=None, s
 
 class KvEvict(_Prepared):
     """luce_kv_evict (or luce_kv_evict_paged, for PagedEvictSlots) with its
-    arguments marshalled once: each call takes the slots' current ``len`` and
-    ``next_pos``."""
+    arguments marshalled once: each call takes the slots' current ``len``,
+    ``budget``, ``sinks``, ``recent`` and ``next_pos``."""
 
     def __init__(self, slots: Sequence[EvictSlot], stream=None):
         import torch
@@ -1186,6 +1196,7 @@ class KvEvict(_Prepared):
         L, Hkv = first.shape[1:3] if paged else first.shape[:2]
         n = len(self.slots)
         self._sc = ((PagedEvictSlotC if paged else EvictSlotC) * n)()
+        caches = []
         for i, s in enumerate(self.slots):
             if paged:
                 _pools(s.k_pool, s.v_pool, L, Hkv, f"slots[{i}]")
@@ -1202,6 +1213,7 @@ class KvEvict(_Prepared):
                              (s.pos, torch.int32, "pos"), (pos_out, torch.int32, "pos_out")):
                 _state(t, dt, L, Hkv, cap, f"slots[{i}].{w}")
             _same_device(first, k, v, s.acc, s.pos, acc_out, pos_out, s.table if paged else None)
+            caches.append((k, v, s.acc, s.pos, acc_out, pos_out, s.table if paged else None))
             if paged:
                 self._sc[i] = PagedEvictSlotC(k.data_ptr(), v.data_ptr(), s.table.data_ptr(), s.acc.data_ptr(),
                                               s.pos.data_ptr(), acc_out.data_ptr(), pos_out.data_ptr(), k.shape[0], s.len,
@@ -1214,15 +1226,16 @@ class KvEvict(_Prepared):
         self._pages = [s.table.numel() * PAGE_KEYS if paged else None for s in self.slots]
         self._args = (self._sc, n, L, Hkv, HEAD_DIM)
         lib = load_library()
-        self._bind(lib.luce_kv_evict_paged if paged else lib.luce_kv_evict, first.device, stream, None)
+        self._bind(lib.luce_kv_evict_paged if paged else lib.luce_kv_evict, first.device, stream, caches)
 
     def __call__(self):
         for i, s in enumerate(self.slots):
-            now = (s.len, s.next_pos)
+            now = (s.len, s.next_pos, s.budget, s.sinks, s.recent)
             if now != self._now[i]:
                 if self._pages[i] is not None and s.len > self._pages[i]:
                     raise ValueError(f"slots[{i}].table does not hold {s.len} keys")
-                self._items[i].len, self._items[i].next_pos = now
+                c = self._items[i]
+                c.len, c.next_pos, c.budget, c.sinks, c.recent = now
                 self._now[i] = now
         self._call(*self._args)
 

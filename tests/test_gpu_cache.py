@@ -108,6 +108,35 @@ def test_a_row_that_saw_nothing_adds_nothing():
     assert (acc[0, 0] - want).abs().max().item() <= 6 * 2 ** -24
 
 
+def test_prepared_commit_follows_its_slots_in_streams_and_graphs():
+    rng = np.random.default_rng(17)
+    k, v = caches(rng, 2, 2, 64)
+    scores = rng.standard_normal((2, 4, 4, 64)).astype(np.float32)
+    stats = np.stack([scores.max(-1), np.full(scores.shape[:-1], 9.0, dtype=np.float32)], -1)
+    acc, pos = np.zeros((2, 2, 64), dtype=np.float32), np.zeros((2, 2, 64), dtype=np.int32)
+    sl = luce.CommitSlot(cuda(k), cuda(v), 10, [1, 3], 0, cuda(acc), cuda(pos), 10)
+    call = luce.TreeCommit([sl], 4, cuda(scores), cuda(stats))
+    want = [k, v, acc, pos]
+    side = torch.cuda.Stream()
+    for length, path, pos0 in ((10, [1, 3], 10), (12, [0], 40), (13, [0, 1, 2], 41)):
+        sl.len, sl.path, sl.pos0 = length, path, pos0
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            call()
+        torch.cuda.current_stream().wait_stream(side)
+        want = list(ref.commit(want[0], want[1], length, path, want[2], want[3], pos0, scores, stats))
+    sl.len, sl.path, sl.pos0 = 16, [2], 44
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(2):                                                   # replayed: the same commit twice
+        graph.replay()
+        want = list(ref.commit(want[0], want[1], 16, [2], want[2], want[3], 44, scores, stats))
+    torch.cuda.synchronize()
+    assert same(sl.k, want[0]) and same(sl.v, want[1]) and same(sl.pos, want[3])
+    assert np.abs(sl.acc.cpu().numpy() - want[2]).max() <= 5 * weight_tolerance(want[2], 2, 3)
+
+
 def test_commit_python_refusals():
     k = torch.zeros(2, 2, 24, 128, dtype=torch.float16, device="cuda")
     with pytest.raises(ValueError):
@@ -320,6 +349,40 @@ def test_paged_evict_leaves_rows_of_bad_pages(length, budget):
     torch.cuda.synchronize()
     assert same(sl.k_pool, pool_of(np.random.default_rng(5), wk)[0]) and same(sl.v_pool, pool_of(np.random.default_rng(5), wv)[0])
     assert same(sl.acc, wa) and same(sl.pos, wp)
+
+
+def test_prepared_calls_follow_a_replaced_table_and_budget():
+    rng = np.random.default_rng(23)
+    k, v = caches(rng, 1, 2, 300)
+    (pk, table), (pv, _) = (pool_of(np.random.default_rng(9), x) for x in (k, v))
+    sl = luce.PagedCommitSlot(cuda(pk), cuda(pv), table, 120, [2])
+    call = luce.TreeCommit([sl], 4)
+    call()
+    k, v = ref.commit(k, v, 120, [2])[:2]
+    assert same(sl.k_pool, pool_of(np.random.default_rng(9), k)[0])
+    other = np.setdiff1d(np.arange(len(pk)), table)[:1]                  # its second page moves elsewhere
+    sl.k_pool[int(other[0])] = sl.k_pool[int(table[1])]
+    sl.v_pool[int(other[0])] = sl.v_pool[int(table[1])]
+    old = sl.k_pool[int(table[1])].clone()
+    sl.table = np.array([table[0], other[0], table[2]], dtype=np.int32)
+    sl.len, sl.path = 127, [0, 3]
+    call()
+    k, v = ref.commit(k, v, 127, [0, 3])[:2]
+    got = sl.k_pool.cpu().numpy()[sl.table]                             # [3][1][2][128][128]
+    assert np.array_equal(np.concatenate(list(got), axis=2)[:, :, :300].view(np.uint16), k.view(np.uint16))
+    assert same(sl.k_pool[int(table[1])], old.cpu().numpy())
+
+    k, v = caches(rng, 1, 2, 64)
+    acc, pos = rng.random((1, 2, 64)).astype(np.float32), np.tile(np.arange(64, dtype=np.int32), (1, 2, 1))
+    sl = luce.EvictSlot(cuda(k), cuda(v), cuda(acc), cuda(pos), 60, 50, 0, 0, 60)
+    call = luce.KvEvict([sl])
+    call()
+    sl.len, sl.budget, sl.sinks, sl.recent = 50, 40, 3, 5
+    call()
+    for n, cut, sinks, recent in ((60, 50, 0, 0), (50, 40, 3, 5)):
+        k, v, acc, pos = ref.evict(k, v, acc, pos, n, cut, sinks, recent, 60)
+    torch.cuda.synchronize()
+    assert same(sl.k, k) and same(sl.v, v) and same(sl.acc, acc) and same(sl.pos, pos)
 
 
 # ------------------------------------------------------------------ together
