@@ -141,7 +141,7 @@ cudaError_t launch_tree_commit(const CommitBatch& b, int n_layers, int Hq, int H
 //      cluster in index order;
 //   3. holes (index < budget, leaving) and comers (index >= budget, staying)
 //      are listed in index order by each CTA; the i-th hole of the cluster
-//      gets the i-th comer's rows, 32 pairs at a time per warp.
+//      gets the i-th comer's rows, an equal run of the pairs per warp.
 // No atomics but integer counts, so nothing depends on their order.
 // Bound by latency while few keys leave (each step is a cluster barrier), by
 // the moved rows' bytes where a prompt is cut.
@@ -356,11 +356,7 @@ kv_evict_kernel(const __grid_constant__ EvictBatch b, int slice)
     // the CTAs before this one are a bin of their last histogram)
     // (runs of odd length: their words fall into different banks)
     const int run = ((nj + kEvictThreads - 1) / kEvictThreads) | 1, r0 = min(tid * run, nj), r1 = min(r0 + run, nj);
-    int eq_far = 0;
-#pragma unroll
-    for (int r = 0; r < C - 1; ++r)
-        if (r < me) eq_far += evict_word<C>(&hist[0][T & 1023], r);
-    int eq = 0, all;
+    int all;
     uint64_t low = 0, same_as = 0;  // the run's keys below T and equal to it, a bit each
     static_assert(((kEvictSlice + kEvictThreads - 1) / kEvictThreads | 1) <= 64, "a run's keys are bits of a word");
 #pragma unroll 8
@@ -369,12 +365,17 @@ kv_evict_kernel(const __grid_constant__ EvictBatch b, int slice)
         low |= (uint64_t)(u < T) << (i - r0);
         same_as |= (uint64_t)(u == T) << (i - r0);
     }
-    eq = __popcll(same_as);
-    const int eq_at = eq_far + block_prefix(eq, warp_sum, &all);
+    if (stay > 0) {  // (the cluster alike)
+        int eq_far = 0;
+#pragma unroll
+        for (int r = 0; r < C - 1; ++r)
+            if (r < me) eq_far += evict_word<C>(&hist[0][T & 1023], r);
+        const int eq = __popcll(same_as), eq_at = eq_far + block_prefix(eq, warp_sum, &all);
+        // of the run's keys equal to T the first stay - eq_at stay
+        for (int k = min(max(stay - eq_at, 0), eq); k > 0; --k) same_as &= same_as - 1;
+    }
 
     // 3. holes from the list's front, comers from its back
-    // of the run's keys equal to T the first stay - eq_at stay
-    for (int k = min(max(stay - eq_at, 0), eq); k > 0; --k) same_as &= same_as - 1;
     const uint64_t leave = low | same_as, in = r1 - r0 == 64 ? ~0ull : (1ull << (r1 - r0)) - 1;
     const int split = min(max(sl.budget - (j0 + r0), 0), 64);  // the run's keys below the budget
     const uint64_t below_budget = split == 64 ? ~0ull : (1ull << split) - 1;
@@ -399,10 +400,12 @@ kv_evict_kernel(const __grid_constant__ EvictBatch b, int slice)
         }
     }
     uint4* base = reinterpret_cast<uint4*>((lane < 16 ? sl.k : sl.v) + lh * sl.head_step) + (lane & 15);
-    for (int i0 = 32 * (me * kEvictWarps + warp); i0 < m; i0 += 32 * C * kEvictWarps) {
-        const int i = i0 + lane, cnt = min(32, m - i0);
+    // every warp of the cluster takes an equal run of the pairs
+    const int mover = me * kEvictWarps + warp, end = (int)((int64_t)m * (mover + 1) / (C * kEvictWarps));
+    for (int i0 = (int)((int64_t)m * mover / (C * kEvictWarps)); i0 < end; i0 += 32) {
+        const int i = i0 + lane, cnt = min(32, end - i0);
         int to = 0, from = 0;
-        if (i < m) {
+        if (i < end) {
             int rh = 0, rc = 0;
 #pragma unroll
             for (int r = 1; r < C; ++r) {
@@ -425,8 +428,8 @@ kv_evict_kernel(const __grid_constant__ EvictBatch b, int slice)
             acc_out[to] = ld_placed_f(acc + from);
             pos_out[to] = ld_placed_i(pos + from);
         }
-        int dst = i < m ? evict_row(sl, to) : -1;
-        const int src = i < m ? evict_row(sl, from) : -1;
+        int dst = i < end ? evict_row(sl, to) : -1;
+        const int src = i < end ? evict_row(sl, from) : -1;
         if (src < 0) dst = -1;
         for (int k = 0; k < cnt; k += kEvictMove) {
             uint4 x[kEvictMove];
