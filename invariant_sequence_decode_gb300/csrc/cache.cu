@@ -1,5 +1,7 @@
 // cache.cu - what happens to a slot's cache between steps: the commit of a
 // verified tree's accepted path, and eviction by accumulated attention weight.
+#include <limits.h>
+
 #include <algorithm>
 #include <cmath>
 
@@ -448,33 +450,30 @@ kv_evict_kernel(const __grid_constant__ EvictBatch b, int slice)
     if (C > 1) cluster_sync();  // the others still read this CTA's list
 }
 
-// Few keys leave (a step's new ones): one CTA per head keeps its keys' ranks in
-// registers and takes out the lowest, of equals the last, n times: a round is
-// a minimum over registers, warps and CTA, against the selection's three passes
-// over a histogram.  2,051 keys to 2,048 in 512 heads: 8.5 us, 16.6 through the selection.
+// Few keys leave (a step's new ones): one CTA per head keeps its keys in
+// registers as 64-bit numbers in the order in which they leave (the rank, of
+// equals the last index first), no two alike.  The n-th lowest of 64 groups'
+// lowest keys bounds the n lowest keys of all from above, and only the n groups
+// up to it hold keys below it, so the few keys up to the bound go to a list,
+// where each counts the lower ones.
 constexpr int kFewThreads = 256;
 constexpr int kFewWarps = kFewThreads / 32;
-constexpr int kFewKeys = 16;                                  // most that leave
+constexpr int kFewKeys = 32;                                  // most that leave: a lane each
 constexpr int kFewPer = 16, kFewMax = kFewPer * kFewThreads;  // longest cache
+constexpr int kFewGroups = 64;                                // of 4 threads, more than may leave
+constexpr int kFewList = kFewKeys * (kFewMax / kFewGroups);
 
-__device__ __forceinline__ uint32_t redux_min(uint32_t x)
+__device__ __forceinline__ uint64_t shfl_xor_u64(uint64_t x, int o)
 {
-    uint32_t r;
-    asm volatile("redux.sync.min.u32 %0, %1, 0xffffffff;" : "=r"(r) : "r"(x));
-    return r;
-}
-__device__ __forceinline__ uint32_t redux_max(uint32_t x)
-{
-    uint32_t r;
-    asm volatile("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(r) : "r"(x));
-    return r;
+    return __shfl_xor_sync(0xffffffffu, (unsigned long long)x, o);
 }
 
 __global__ void __launch_bounds__(kFewThreads)
 kv_evict_few_kernel(const __grid_constant__ EvictBatch b)
 {
-    __shared__ uint32_t low[2][kFewWarps], at[2][kFewWarps];  // a round's lowest rank of each warp, and its last index
-    __shared__ int hole[kFewKeys], come[kFewKeys], n_come;
+    __shared__ __align__(16) uint64_t low[kFewGroups], list[kFewList];
+    __shared__ uint64_t bound;
+    __shared__ int gone[kFewKeys], hole[kFewKeys], come[kFewKeys], n_list, n_come;
     pdl_trigger();
     const EvictSlot& sl = b.slot[blockIdx.y];
     const int64_t lh = blockIdx.x;
@@ -484,7 +483,11 @@ kv_evict_few_kernel(const __grid_constant__ EvictBatch b)
     float* acc_out = sl.acc_out + lh * sl.cap;
     int32_t* pos_out = sl.pos_out + lh * sl.cap;
     const int n = sl.len - sl.budget;
-    uint32_t rank[kFewPer];
+    uint64_t key[kFewPer];
+    if (tid == 0) {
+        bound = ~0ull;
+        n_list = 0;
+    }
     pdl_wait();
     {
         float a[kFewPer];
@@ -500,46 +503,63 @@ kv_evict_few_kernel(const __grid_constant__ EvictBatch b)
 #pragma unroll
         for (int e = 0; e < kFewPer; ++e) {
             const int j = tid + e * kFewThreads;
-            rank[e] = 0xffffffffu;
+            key[e] = ~0ull;
             if (j < sl.len) {
                 if (j < sl.budget) {
                     if (acc_out != acc) acc_out[j] = a[e];
                     if (pos_out != pos) pos_out[j] = p[e];
                 }
-                rank[e] = evict_rank(a[e], p[e], sl);
+                key[e] = (uint64_t)evict_rank(a[e], p[e], sl) << 32 | (uint32_t)(INT_MAX - j);
             }
         }
     }
     if (n <= 0) return;
-    uint32_t gone = 0;      // this thread's keys that left, a bit each
-    int left = 0x7fffffff;  // warp 0, lane r: the key that left in round r
-    for (int r = 0; r < n; ++r) {
-        uint32_t m = 0xffffffffu;
-        int mj = -1;
+    uint64_t m = key[0];
 #pragma unroll
-        for (int e = 0; e < kFewPer; ++e) {
-            const int j = tid + e * kFewThreads;
-            if (j < sl.len && !(gone >> e & 1) && rank[e] <= m) {  // (of equals the last)
-                m = rank[e];
-                mj = j;
-            }
+    for (int e = 1; e < kFewPer; ++e) m = min(m, key[e]);
+    m = min(m, shfl_xor_u64(m, 1));
+    m = min(m, shfl_xor_u64(m, 2));
+    if ((tid & 3) == 0) low[tid >> 2] = m;
+    __syncthreads();
+    if (n == 1) {
+        if (warp == 0) {
+            m = min(low[lane], low[lane + 32]);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = min(m, shfl_xor_u64(m, o));
+            if (lane == 0) gone[0] = INT_MAX - (int)(uint32_t)m;
+            __syncwarp();
         }
-        const uint32_t wm = redux_min(mj < 0 ? 0xffffffffu : m);
-        const uint32_t wj = redux_max(mj >= 0 && m == wm ? (uint32_t)mj + 1 : 0u);  // 0: no key left
-        if (lane == 0) {
-            low[r & 1][warp] = wm;
-            at[r & 1][warp] = wj;
+    } else {
+        int below = 0;  // a group's four threads count together
+#pragma unroll
+        for (int i = 0; i < kFewGroups / 4; ++i) below += low[4 * i + (tid & 3)] < m;
+        below += __shfl_xor_sync(0xffffffffu, below, 1);
+        below += __shfl_xor_sync(0xffffffffu, below, 2);
+        if (below == n - 1 && m != ~0ull) bound = m;  // (fewer groups with keys: every key is listed)
+        __syncthreads();
+        if (m <= bound) {
+#pragma unroll
+            for (int e = 0; e < kFewPer; ++e)
+                if (key[e] <= bound && key[e] != ~0ull) list[atomicAdd(&n_list, 1)] = key[e];
         }
         __syncthreads();
-        const uint32_t cm = lane < kFewWarps ? low[r & 1][lane] : 0xffffffffu, cj = lane < kFewWarps ? at[r & 1][lane] : 0u;
-        const uint32_t bm = redux_min(cj ? cm : 0xffffffffu);
-        const int bj = (int)redux_max(cj && cm == bm ? cj : 0u) - 1;
-        if (bj % kFewThreads == tid) gone |= 1u << (bj / kFewThreads);
-        if (warp == 0 && lane == r) left = bj;
+        const int found = n_list;
+        for (int i0 = 8 * warp; i0 < found; i0 += 8 * kFewWarps) {  // and a key's four
+            const int i = i0 + (lane >> 2);
+            const uint64_t mine = list[min(i, found - 1)];
+            below = 0;
+#pragma unroll 4
+            for (int k = tid & 3; k < found; k += 4) below += list[k] < mine;
+            below += __shfl_xor_sync(0xffffffffu, below, 1);
+            below += __shfl_xor_sync(0xffffffffu, below, 2);
+            if (i < found && below < n) gone[below] = INT_MAX - (int)(uint32_t)mine;
+        }
+        __syncthreads();
     }
     // holes and comers in ascending order: each key's place is the number of
     // its kind below it
     if (warp == 0) {
+        const int left = lane < n ? gone[lane] : INT_MAX;
         bool stays = lane < n;  // key budget + lane
         int below = 0;
         for (int r = 0; r < n; ++r) {
@@ -553,17 +573,26 @@ kv_evict_few_kernel(const __grid_constant__ EvictBatch b)
         if (lane == 0) n_come = __popc(mask);
     }
     __syncthreads();
-    const int m = n_come;
+    const int moves = n_come;
     uint4* base = reinterpret_cast<uint4*>((lane < 16 ? sl.k : sl.v) + lh * sl.head_step) + (lane & 15);
-    for (int i = warp; i < m; i += kFewWarps) {
-        const int to = hole[i], from = come[i];
-        const int src = evict_row(sl, from), dst = evict_row(sl, to);
-        if (src >= 0 && dst >= 0) base[(int64_t)dst * 16] = ld_placed_u4(base + (int64_t)src * 16);
-        if (lane == 0) {
-            acc_out[to] = ld_placed_f(acc + from);
-            pos_out[to] = ld_placed_i(pos + from);
+    uint4 x[kFewKeys / kFewWarps];
+    int dst[kFewKeys / kFewWarps];
+#pragma unroll
+    for (int e = 0; e < kFewKeys / kFewWarps; ++e) {
+        const int i = warp + e * kFewWarps;
+        dst[e] = -1;
+        if (i >= moves) continue;
+        const int to = hole[i], from = come[i], src = evict_row(sl, from);
+        if (src >= 0) {
+            dst[e] = evict_row(sl, to);
+            x[e] = ld_placed_u4(base + (int64_t)src * 16);
         }
+        if (lane == 0) acc_out[to] = ld_placed_f(acc + from);
+        if (lane == 1) pos_out[to] = ld_placed_i(pos + from);
     }
+#pragma unroll
+    for (int e = 0; e < kFewKeys / kFewWarps; ++e)
+        if (dst[e] >= 0) base[(int64_t)dst[e] * 16] = x[e];
 }
 
 template <int C>
