@@ -351,6 +351,41 @@ def test_paged_evict_leaves_rows_of_bad_pages(length, budget):
     assert same(sl.acc, wa) and same(sl.pos, wp)
 
 
+@pytest.mark.parametrize("kind", ["plain", "ties", "equal", "odd"])
+@pytest.mark.parametrize("length,leave", [(3, 2), (33, 32), (34, 33), (257, 32), (4096, 32), (4096, 1), (4097, 1), (4097, 32), (4097, 33),
+                                          (8193, 2), (30011, 17)])
+def test_evict_few(length, leave, kind):
+    rng = np.random.default_rng(length + leave)
+    k, v = caches(rng, 1, 2, length + 3)
+    acc = weights(rng, kind, (1, 2, length + 3))
+    pos = np.tile(rng.permutation(length + 3).astype(np.int32), (1, 2, 1))
+    out = [np.full_like(acc, 5.0), np.full_like(pos, 5)]
+    sinks, recent = min(2, length - leave - 1), min(7, max(length - leave - 3, 0))
+    wk, wv, wa, wp = ref.evict(k, v, acc, pos, length, length - leave, sinks, recent, length)
+    sl = luce.EvictSlot(cuda(k), cuda(v), cuda(acc), cuda(pos), length, length - leave, sinks, recent, length, cuda(out[0]), cuda(out[1]))
+    luce.luce_kv_evict([sl])
+    torch.cuda.synchronize()
+    n = length - leave
+    assert same(sl.k, wk) and same(sl.v, wv) and same(sl.acc, acc) and same(sl.pos, pos)
+    assert same(sl.acc_out[..., :n], wa[..., :n]) and same(sl.pos_out[..., :n], wp[..., :n])
+    assert bool((sl.acc_out[..., n:] == 5).all()) and bool((sl.pos_out[..., n:] == 5).all())
+
+
+@pytest.mark.parametrize("length,leave,period,low", [(4000, 12, 256, 40), (4096, 32, 256, 60), (70001, 2, 512, 4), (70001, 32, 512, 60)])
+def test_evict_few_when_low_weights_lie_close(length, leave, period, low):
+    """The lowest keys share a few places of a period: more lie below the bound than the list holds."""
+    rng = np.random.default_rng(length + low)
+    k, v = caches(rng, 1, 1, length)
+    acc = rng.random((1, 1, length)).astype(np.float32)
+    acc = np.where(np.arange(length) % period < low, acc * np.float32(2.0 ** -20), acc + 1).astype(np.float32)
+    pos = np.tile(np.arange(length, dtype=np.int32), (1, 1, 1))
+    wk, wv, wa, wp = ref.evict(k, v, acc, pos, length, length - leave, 0, 3, length)
+    sl = luce.EvictSlot(cuda(k), cuda(v), cuda(acc), cuda(pos), length, length - leave, 0, 3, length)
+    luce.luce_kv_evict([sl])
+    torch.cuda.synchronize()
+    assert same(sl.k, wk) and same(sl.v, wv) and same(sl.acc, wa) and same(sl.pos, wp)
+
+
 def test_prepared_calls_follow_a_replaced_table_and_budget():
     rng = np.random.default_rng(23)
     k, v = caches(rng, 1, 2, 300)
