@@ -75,9 +75,14 @@ tree_commit_kernel(const __grid_constant__ CommitBatch b, int n_layers, int Hq, 
     float4 s[kCommitAhead];
     // the first rows are on their way while the statistics settle
     auto fetch = [&](int i0) {
+        if (i0 + kCommitAhead <= n) {  // (a batch without branches)
 #pragma unroll
-        for (int e = 0; e < kCommitAhead; ++e)
-            if (i0 + e < n) s[e] = ld_placed_cs_f4(scores + at[i0 + e] * lds + j);
+            for (int e = 0; e < kCommitAhead; ++e) s[e] = ld_placed_cs_f4(scores + at[i0 + e] * lds + j);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kCommitAhead; ++e)
+                if (i0 + e < n) s[e] = ld_placed_cs_f4(scores + at[i0 + e] * lds + j);
+        }
     };
     if (j < sl.len) {
 #pragma unroll
