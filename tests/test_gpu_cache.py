@@ -319,6 +319,10 @@ def test_paged_commit(lens, paths):
         assert same(p.acc, f.acc.cpu().numpy()) and same(p.pos, f.pos.cpu().numpy())
 
 
+def test_paged_evict_few_of_many():
+    test_paged_evict(9000, 8990)
+
+
 @pytest.mark.parametrize("length,budget", [(130, 127), (300, 290), (700, 100), (5000, 2000)])
 def test_paged_evict(length, budget):
     rng = np.random.default_rng(length)
@@ -384,6 +388,27 @@ def test_evict_few_when_low_weights_lie_close(length, leave, period, low):
     luce.luce_kv_evict([sl])
     torch.cuda.synchronize()
     assert same(sl.k, wk) and same(sl.v, wv) and same(sl.acc, wa) and same(sl.pos, wp)
+
+
+@pytest.mark.parametrize("shapes", [[(9000, 8990), (5, 5), (4097, 4096), (100, 120)], [(3000, 2990), (1, 1), (0, 4), (40, 9)],
+                                    [(20000, 19968), (7000, 7000), (4100, 5000)]])
+def test_evict_few_slots_of_different_lengths(shapes):
+    """Slots that keep all keys next to slots that lose a few, into arrays of their own."""
+    rng = np.random.default_rng(sum(n for n, _ in shapes))
+    slots, want = [], []
+    for n, budget in shapes:
+        k, v = caches(rng, 2, 2, n + 2)
+        acc, pos = weights(rng, "odd", (2, 2, n + 2)), np.tile(rng.permutation(n + 2).astype(np.int32), (2, 2, 1))
+        want.append((acc, pos) + tuple(ref.evict(k, v, acc, pos, n, budget, 1, 0, n + 2)))
+        out = torch.full((2, 2, n + 2), 5.0, device="cuda"), torch.full((2, 2, n + 2), 5, dtype=torch.int32, device="cuda")
+        slots.append(luce.EvictSlot(cuda(k), cuda(v), cuda(acc), cuda(pos), n, budget, 1, 0, n + 2, *out))
+    luce.luce_kv_evict(slots)
+    torch.cuda.synchronize()
+    for sl, (acc, pos, wk, wv, wa, wp) in zip(slots, want):
+        keep = min(sl.len, sl.budget)
+        assert same(sl.k, wk) and same(sl.v, wv) and same(sl.acc, acc) and same(sl.pos, pos)
+        assert same(sl.acc_out[..., :keep], wa[..., :keep]) and same(sl.pos_out[..., :keep], wp[..., :keep])
+        assert bool((sl.acc_out[..., keep:] == 5).all()) and bool((sl.pos_out[..., keep:] == 5).all())
 
 
 def test_prepared_calls_follow_a_replaced_table_and_budget():
