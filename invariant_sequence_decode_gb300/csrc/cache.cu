@@ -364,6 +364,10 @@ kv_evict_kernel(const __grid_constant__ EvictBatch b, int slice)
             for (int i = tid; i < kEvictBins; i += kEvictThreads) hist[0][i] = 0;
         }
         __syncthreads();
+        if (left == same) {  // the whole bin leaves: its other bits need not be known
+            T |= (1u << sh) - 1;
+            break;
+        }
     }
     const int stay = same - left;  // the first keys equal to T, in index order
 
