@@ -20,7 +20,9 @@ namespace luce {
 //
 // Weights: acc_j += sum over accepted rows r and the group's heads h of
 // e^(s_rhj - m_rh) / l_rh: a stream over the scores (4 A GQ bytes per key
-// against 8 of acc), four keys per thread, eight rows of scores in flight.
+// against 8 of acc), four keys per thread, eight rows of scores in flight (12 or
+// 16: 46.5 and 56.7 us on four slots of 8 layers with 16,385 to 32,757 keys, where 8 take
+// 40.1, 6.1 TB/s; two keys per thread 61.7).
 constexpr int kCommitThreads = 128;
 constexpr int kCommitKeys = 4 * kCommitThreads;
 constexpr int kCommitAhead = 8;
@@ -151,7 +153,8 @@ cudaError_t launch_tree_commit(const CommitBatch& b, int n_layers, int Hq, int H
 //      gets the i-th comer's rows, an equal run of the pairs per warp.
 // No atomics but integer counts, so nothing depends on their order.
 // Bound by latency while few keys leave (each step is a cluster barrier), by
-// the moved rows' bytes where a prompt is cut.
+// the moved rows' bytes where a prompt is cut: 64 heads from 32,757 keys to
+// 4,096 in 54.5 us, of which the rows take 36 (6.5 TB/s).
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictBins = 2048;
