@@ -872,10 +872,16 @@ class _Prepared:
     _home = None
     _lent = frozenset()
 
-    def _bind(self, fn, device, stream, keep):
+    def _bind(self, name, args, device, stream, keep):
+        """The C function and its arguments but the stream, as C values: converting
+        them at every call takes ctypes 0.7 us."""
         import torch
-        self._fn, self._index, self._keep = fn, device.index, (stream, keep)
+        lib = load_library()
+        self._fn = lib[name]  # (a function object of its own, without argument types)
+        self._args = tuple(v if isinstance(v, ctypes.Array) else t(v) for t, v in zip(getattr(lib, name).argtypes, args))
+        self._index, self._keep = device.index, (stream, keep)
         self._stream = None if stream is None else stream.cuda_stream
+        self._at = self._at_arg = None  # the last call's stream
         self._device_now, self._stream_now = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
     def _allocate(self, shape, dtype, device, stream):
@@ -897,16 +903,18 @@ class _Prepared:
             t.record_stream(torch.cuda.ExternalStream(stream, device=t.device))
         self._lent = self._lent | {stream}
 
-    def _call(self, *args):
+    def _call(self):
         s = self._stream if self._stream is not None else self._stream_now(self._index)
-        if s != self._home and self._owned and s not in self._lent:
-            self._lend(s)
+        if s != self._at:
+            if s != self._home and self._owned and s not in self._lent:
+                self._lend(s)
+            self._at, self._at_arg = s, ctypes.c_void_p(s)
         if self._device_now() == self._index:
-            rc = self._fn(*args, s)
+            rc = self._fn(*self._args, self._at_arg)
         else:
             import torch
             with torch.cuda.device(self._index):
-                rc = self._fn(*args, s)
+                rc = self._fn(*self._args, self._at_arg)
         if rc != LUCE_OK:
             _check(rc)
 
@@ -985,10 +993,10 @@ class TreeAttention(_Prepared):
             need = luce_tree_attn_workspace_size(T, Hq, int(n_kv_heads), D, max(0, *caps))
             ws = self._allocate((max(256, need),), torch.uint8, q.device, stream)
         _need(ws, torch.uint8, "ws")
-        self._args = (q.data_ptr(), self._vc, n, Hq, int(n_kv_heads), D, float(scale), self.out.data_ptr(), _ptr(scores),
-                      lds, _ptr(stats), ws.data_ptr(), ws.numel())
+        args = (q.data_ptr(), self._vc, n, Hq, int(n_kv_heads), D, float(scale), self.out.data_ptr(), _ptr(scores), lds,
+                _ptr(stats), ws.data_ptr(), ws.numel())
         caches = [(v.k_pool, v.v_pool, v.table) if paged else (v.k, v.v) for v in self.views]
-        self._bind(getattr(load_library(), name), q.device, stream, (q, scores, stats, ws, trees, caches))
+        self._bind(name, args, q.device, stream, (q, scores, stats, ws, trees, caches))
 
     @staticmethod
     def _fits(length, cap):
@@ -1000,7 +1008,7 @@ class TreeAttention(_Prepared):
             if v.len != self._lens[i]:
                 self._fits(v.len, self._caps[i])
                 self._items[i].len = self._lens[i] = v.len
-        self._call(*self._args)
+        self._call()
         return self.out
 
 
@@ -1148,10 +1156,8 @@ class TreeCommit(_Prepared):
                                           _ptr(s.pos), s.pos0)
         self._items = [self._sc[i] for i in range(n)]
         self._now, self._arrays = [None] * n, [None] * n
-        self._args = (self._sc, n, L, int(n_q_heads), Hkv, HEAD_DIM, _ptr(scores), n_rows, lds, _ptr(stats))
-        lib = load_library()
-        self._bind(lib.luce_tree_commit_paged if paged else lib.luce_tree_commit, first.device, stream,
-                   (scores, stats, caches))
+        args = (self._sc, n, L, int(n_q_heads), Hkv, HEAD_DIM, _ptr(scores), n_rows, lds, _ptr(stats))
+        self._bind("luce_tree_commit_paged" if paged else "luce_tree_commit", args, first.device, stream, (scores, stats, caches))
         self._tables = [None] * n if paged else None
 
     def _take_tables(self):
@@ -1173,7 +1179,7 @@ class TreeCommit(_Prepared):
                 self._arrays[i] = (ctypes.c_int32 * max(1, len(path)))(*path)
                 c.len, c.row0, c.pos0, c.path, c.n_path = s.len, s.row0, s.pos0, self._arrays[i], len(path)
                 self._now[i] = now
-        self._call(*self._args)
+        self._call()
 
 
 def luce_tree_commit(slots: Sequence[CommitSlot], n_q_heads: int, scores=None, stats=None, stream=None):
@@ -1224,9 +1230,8 @@ class KvEvict(_Prepared):
                                          s.next_pos)
         self._items, self._now = [self._sc[i] for i in range(n)], [None] * n
         self._pages = [s.table.numel() * PAGE_KEYS if paged else None for s in self.slots]
-        self._args = (self._sc, n, L, Hkv, HEAD_DIM)
-        lib = load_library()
-        self._bind(lib.luce_kv_evict_paged if paged else lib.luce_kv_evict, first.device, stream, caches)
+        args = (self._sc, n, L, Hkv, HEAD_DIM)
+        self._bind("luce_kv_evict_paged" if paged else "luce_kv_evict", args, first.device, stream, caches)
 
     def __call__(self):
         for i, s in enumerate(self.slots):
@@ -1237,7 +1242,7 @@ class KvEvict(_Prepared):
                 c = self._items[i]
                 c.len, c.next_pos, c.budget, c.sinks, c.recent = now
                 self._now[i] = now
-        self._call(*self._args)
+        self._call()
 
 
 def luce_kv_evict(slots: Sequence[EvictSlot], stream=None):

@@ -329,10 +329,7 @@ int luce_tree_commit(const luce_commit_slot* slots, int n_seq, int n_layers, int
         o.k = reinterpret_cast<__half*>(c.k);
         o.v = reinterpret_cast<__half*>(c.v);
         o.head_step = (int64_t)c.cap * D;
-        for (int i = 0; i < c.n_path; ++i) {
-            o.from[i] = (int64_t)(c.len + c.path[i]) * D;
-            o.to[i] = (int64_t)(c.len + i) * D;
-        }
+        for (int e = 0; e < 2; ++e) o.span[e] = (int64_t)(c.len / LUCE_PAGE_KEYS + e) * LUCE_PAGE_KEYS * D;
         r[nr++] = range_of(c.k, heads * c.cap * D * 2, s, "K cache", true);
         r[nr++] = range_of(c.v, heads * c.cap * D * 2, s, "V cache", true);
     }
@@ -370,17 +367,19 @@ int luce_tree_commit_paged(const luce_paged_commit_slot* slots, int n_seq, int n
                 const int key = c.len + (to ? i : c.path[i]), at = key / LUCE_PAGE_KEYS;
                 REQUIRE(at < c.n_table && c.table_host[at] >= 0 && c.table_host[at] < c.n_pages, LUCE_EINVAL,
                         "%s: slot %d key %d has no page in [0, %d)", who, s, key, c.n_pages);
-                (to ? o.to : o.from)[i] = c.table_host[at] * page + (int64_t)(key % LUCE_PAGE_KEYS) * D;
+                o.span[at - c.len / LUCE_PAGE_KEYS] = c.table_host[at] * page;
             }
     }
     // a row that one slot writes is no other slot's row
     for (int s = 0; s < n_seq; ++s)
         for (int t = 0; t < n_seq; ++t)
             for (int i = 0; i < b.slot[s].n_path && s != t; ++i)
-                for (int j = 0; j < b.slot[t].n_path; ++j)
-                    REQUIRE((b.slot[s].k != b.slot[t].k && b.slot[s].v != b.slot[t].v) ||
-                                (b.slot[s].to[i] != b.slot[t].to[j] && b.slot[s].to[i] != b.slot[t].from[j]),
-                            LUCE_EINVAL, "%s: slots %d and %d share a row", who, s, t);
+                for (int j = 0; j < b.slot[t].n_path; ++j) {
+                    const CommitSlot &a = b.slot[s], &o = b.slot[t];
+                    const int64_t to = a.at(a.len + i);
+                    REQUIRE((a.k != o.k && a.v != o.v) || (to != o.at(o.len + j) && to != o.at(o.len + o.path[j])), LUCE_EINVAL,
+                            "%s: slots %d and %d share a row", who, s, t);
+                }
     return run_commit(b, n_layers, Hq, Hkv, scores, n_rows, lds, stats, r, nr, any_acc, stream, who);
 }
 

@@ -52,10 +52,10 @@ tree_commit_kernel(const __grid_constant__ CommitBatch b, int n_layers, int Hq, 
         uint4 x[kMaxTree];
 #pragma unroll
         for (int i = 0; i < kMaxTree; ++i)
-            if (i < A && sl.path[i] != i) x[i] = ld_placed_u4(p + sl.from[i]);
+            if (i < A && sl.path[i] != i) x[i] = ld_placed_u4(p + sl.at(sl.len + sl.path[i]));
 #pragma unroll
         for (int i = 0; i < kMaxTree; ++i)
-            if (i < A && sl.path[i] != i) *reinterpret_cast<uint4*>(p + sl.to[i]) = x[i];
+            if (i < A && sl.path[i] != i) *reinterpret_cast<uint4*>(p + sl.at(sl.len + i)) = x[i];
         if (sl.pos && lane < A) sl.pos[(int64_t)lh * sl.cap + sl.len + lane] = sl.pos0 + lane;
         return;
     }

@@ -149,13 +149,16 @@ struct CommitSlot {
     float* acc;
     int32_t* pos;
     int64_t head_step;
-    int64_t from[kMaxTree], to[kMaxTree];
+    int64_t span[2];  // rows of the 128 keys that hold key len, and of the next 128, in elements
     int32_t len;
     int32_t cap;
     int32_t row0;
     int32_t pos0;
     int32_t n_path;
     uint8_t path[kMaxTree];
+
+    // key's row of a head: nodes lie less than 128 keys behind len
+    __host__ __device__ int64_t at(int key) const { return span[(key >> 7) - (len >> 7)] + (int64_t)(key & 127) * 128; }
 };
 struct CommitBatch {
     CommitSlot slot[4];
