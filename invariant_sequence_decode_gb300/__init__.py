@@ -1163,9 +1163,9 @@ class TreeCommit(_Prepared):
     def _take_tables(self):
         import numpy as np
         for i, s in enumerate(self.slots):
-            t = np.asarray(s.table)
-            if self._tables[i] is None or not np.array_equal(t, self._tables[i]):
-                self._tables[i] = t = np.array(t, dtype=np.int32)
+            if s.table is not self._tables[i]:  # (an int32 array is read where it lies, anything else copied at every call)
+                t = np.ascontiguousarray(s.table, dtype=np.int32)
+                self._tables[i] = t
                 self._items[i].table_host = t.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))
                 self._items[i].n_table = t.size
 

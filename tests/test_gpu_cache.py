@@ -431,6 +431,16 @@ def test_prepared_calls_follow_a_replaced_table_and_budget():
     got = sl.k_pool.cpu().numpy()[sl.table]                             # [3][1][2][128][128]
     assert np.array_equal(np.concatenate(list(got), axis=2)[:, :, :300].view(np.uint16), k.view(np.uint16))
     assert same(sl.k_pool[int(table[1])], old.cpu().numpy())
+    sl.k_pool[int(table[1])], sl.v_pool[int(table[1])] = sl.k_pool[int(other[0])], sl.v_pool[int(other[0])]
+    sl.table[1] = table[1]                                              # in place: back to the first page
+    sl.len, sl.path = 129, [1, 2]
+    call()
+    k, v = ref.commit(k, v, 129, [1, 2])[:2]
+    assert same(sl.k_pool[int(table[1])], np.ascontiguousarray(k[:, :, 128:256]))
+    sl.table, sl.len, sl.path = [int(p) for p in table], 131, [4]
+    call()
+    k, v = ref.commit(k, v, 131, [4])[:2]
+    assert same(sl.v_pool[int(table[1])], np.ascontiguousarray(v[:, :, 128:256]))
 
     k, v = caches(rng, 1, 2, 64)
     acc, pos = rng.random((1, 2, 64)).astype(np.float32), np.tile(np.arange(64, dtype=np.int32), (1, 2, 1))
