@@ -20,9 +20,9 @@ namespace luce {
 //
 // Weights: acc_j += sum over accepted rows r and the group's heads h of
 // e^(s_rhj - m_rh) / l_rh: a stream over the scores (4 A GQ bytes per key
-// against 8 of acc), four keys per thread, eight rows of scores in flight (12 or
-// 16: 46.5 and 56.7 us on four slots of 8 layers with 16,385 to 32,757 keys, where 8 take
-// 40.1, 6.1 TB/s; two keys per thread 61.7).
+// against 8 of acc), four keys per thread, always eight rows of scores in flight
+// (four slots of 8 layers with 16,385 to 32,757 keys: 39.9 us, 6.2 TB/s; 4, 6 or
+// 10 in flight 42.9, 44.2 and 41.5; two keys per thread 61.7).
 constexpr int kCommitThreads = 128;
 constexpr int kCommitKeys = 4 * kCommitThreads;
 constexpr int kCommitAhead = 8;
@@ -75,21 +75,26 @@ tree_commit_kernel(const __grid_constant__ CommitBatch b, int n_layers, int Hq, 
     const int j = tile * kCommitKeys + 4 * tid;
     float old[4], w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     float4 s[kCommitAhead];
-    // the first rows are on their way while the statistics settle
-    auto fetch = [&](int i0) {
-        if (i0 + kCommitAhead <= n) {  // (a batch without branches)
-#pragma unroll
-            for (int e = 0; e < kCommitAhead; ++e) s[e] = ld_placed_cs_f4(scores + at[i0 + e] * lds + j);
-        } else {
-#pragma unroll
-            for (int e = 0; e < kCommitAhead; ++e)
-                if (i0 + e < n) s[e] = ld_placed_cs_f4(scores + at[i0 + e] * lds + j);
-        }
+    auto get = [&](int i) { return ld_placed_cs_f4(scores + at[i] * lds + j); };
+    auto add = [&](int i, float4 x) {
+        const float2 t = ml[i];
+        w[0] = __fmaf_rn(commit_exp(__fsub_rn(x.x, t.x)), t.y, w[0]);
+        w[1] = __fmaf_rn(commit_exp(__fsub_rn(x.y, t.x)), t.y, w[1]);
+        w[2] = __fmaf_rn(commit_exp(__fsub_rn(x.z, t.x)), t.y, w[2]);
+        w[3] = __fmaf_rn(commit_exp(__fsub_rn(x.w, t.x)), t.y, w[3]);
     };
     if (j < sl.len) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) old[e] = j + e < sl.len ? ld_placed_f(acc + j + e) : 0.0f;
-        fetch(0);
+        // the first rows are on their way while the statistics settle
+        if (n >= kCommitAhead) {  // (without branches)
+#pragma unroll
+            for (int e = 0; e < kCommitAhead; ++e) s[e] = get(e);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kCommitAhead; ++e)
+                if (e < n) s[e] = get(e);
+        }
     }
     __syncthreads();
     if (tile == 0)  // a warp per new key
@@ -103,18 +108,26 @@ tree_commit_kernel(const __grid_constant__ CommitBatch b, int n_layers, int Hq, 
             if ((tid & 31) == 0) acc[sl.len + k] = x;
         }
     if (j >= sl.len) return;
-    for (int i0 = 0; i0 < n; i0 += kCommitAhead) {
-        if (i0 > 0) fetch(i0);
+    // a row's place is taken by the one that is eight on
+    int i0 = 0;
+    for (; i0 + 2 * kCommitAhead <= n; i0 += kCommitAhead) {
 #pragma unroll
-        for (int e = 0; e < kCommitAhead; ++e)
-            if (i0 + e < n) {
-                const float2 t = ml[i0 + e];
-                w[0] = __fmaf_rn(commit_exp(__fsub_rn(s[e].x, t.x)), t.y, w[0]);
-                w[1] = __fmaf_rn(commit_exp(__fsub_rn(s[e].y, t.x)), t.y, w[1]);
-                w[2] = __fmaf_rn(commit_exp(__fsub_rn(s[e].z, t.x)), t.y, w[2]);
-                w[3] = __fmaf_rn(commit_exp(__fsub_rn(s[e].w, t.x)), t.y, w[3]);
-            }
+        for (int e = 0; e < kCommitAhead; ++e) {
+            add(i0 + e, s[e]);
+            s[e] = get(i0 + kCommitAhead + e);
+        }
     }
+    if (i0 + kCommitAhead < n) {
+#pragma unroll
+        for (int e = 0; e < kCommitAhead; ++e) {
+            add(i0 + e, s[e]);
+            if (i0 + kCommitAhead + e < n) s[e] = get(i0 + kCommitAhead + e);
+        }
+        i0 += kCommitAhead;
+    }
+#pragma unroll
+    for (int e = 0; e < kCommitAhead; ++e)
+        if (i0 + e < n) add(i0 + e, s[e]);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
         if (j + e < sl.len) acc[j + e] = __fadd_rn(old[e], w[e]);
