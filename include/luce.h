@@ -673,7 +673,8 @@ int luce_tree_commit(const luce_commit_slot* slots, int n_seq, int n_layers, int
 
 /*
  * The same over paged slots: rows move between the pages that table_host names.
- * No page is named by two slots of the call at indexes that it writes.
+ * No page is named by two slots of the call at indexes that it writes.  Slots
+ * may share a pool; pools that are not one, acc and pos overlap nothing.
  */
 typedef struct luce_paged_commit_slot {
     uint16_t* k_pool;           /* (device) [n_pages][n_layers][Hkv][128][128], 16-byte aligned */
@@ -737,7 +738,8 @@ int luce_kv_evict(const luce_evict_slot* slots, int n_seq, int n_layers, int Hkv
  * The same over paged slots; the pages of indexes >= budget are free
  * afterwards.  table (device) holds ceil(len / 128) entries; a row of a page
  * outside [0, n_pages) is neither read nor written.  No page below index budget
- * is named twice in the call.
+ * is named twice in the call.  Slots may share a pool; pools that are not one
+ * and the other arrays overlap nothing.
  */
 typedef struct luce_paged_evict_slot {
     uint16_t* k_pool;     /* (device) [n_pages][n_layers][Hkv][128][128], 16-byte aligned */
