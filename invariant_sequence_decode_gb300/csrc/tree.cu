@@ -27,7 +27,7 @@
 // the products, and 256 threads (two to a row, 64 keys each) turn S into P in
 // place in tensor memory and add each tile's O into registers with the running
 // maximum's correction; a tile takes 2,650 cycles.  16 nodes of 40 heads over
-// 130,800 keys of 8 heads: 100 us, 86 alone at 6.2 TB/s.  Short ones are bound by
+// 130,800 keys of 8 heads: 98 us, 86 alone at 6.2 TB/s.  Short ones are bound by
 // one tile's chain (K, S, softmax, P V, O: 6 us) and the merge (3.5 us).
 #include <limits.h>
 
