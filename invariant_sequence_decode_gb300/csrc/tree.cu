@@ -458,8 +458,10 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
     tm_after();
     const uint32_t tmem = tmem_at;
     if (tid < 2 * b.n_view) {
-        const CUtensorMap* m = tid < b.n_view ? &maps.k[tid] : &maps.v[tid - b.n_view];
-        asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+        const int view = tid % b.n_view;
+        const CUtensorMap* m = tid < b.n_view ? &maps.k[view] : &maps.v[view];
+        if (b.view[view].n_chunk > 0)  // (a short prefix has no map)
+            asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
     }
     // one-tile chunks: a run of them each (a run's heads change least); longer
     // ones: every gridDim.x-th, as chunks of unlike views then spread evenly

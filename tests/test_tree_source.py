@@ -1,0 +1,26 @@
+"""Rules that tree.cu keeps where breaking them could fault or race on a GPU:
+they are read off the source, no run of the broken form shows them."""
+import os
+import re
+
+SOURCE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "invariant_sequence_decode_gb300", "csrc",
+                      "tree.cu")
+
+
+def kernel(name):
+    """The kernel's body, without comments."""
+    text = re.sub(r"//[^\n]*", "", open(SOURCE).read())
+    body = text[re.search(r"\b" + name + r"\([^;]*?\)\s*\{", text).end():]
+    depth = 1
+    for i, c in enumerate(body):
+        depth += (c == "{") - (c == "}")
+        if depth == 0:
+            return body[:i]
+    raise AssertionError(name)
+
+
+def test_only_encoded_maps_are_prefetched():
+    """A short prefix's view has no tensor map: its place holds zeros."""
+    body = kernel("tree_chunk_kernel")
+    at = body.index("prefetch.tensormap")
+    assert re.search(r"if \(b\.view\[view\]\.n_chunk > 0\)\s*asm volatile\(\"$", body[:at])
