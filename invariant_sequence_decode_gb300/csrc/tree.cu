@@ -474,8 +474,8 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
     unsigned int* late = &g_tree_wait_timeouts;
 
     // Each role waits for the kernels before this one right before it first
-    // needs what they wrote.  The producer's thread then lets the merge start:
-    // by then everything but this kernel's results is in place for it.
+    // needs what they wrote.  The producer's thread then lets the merge be
+    // launched, which waits for this kernel before it reads anything.
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 8 && lane == 0) {
@@ -750,8 +750,10 @@ static bool tree_maps(const TreeBatch& b, int Hkv, TreeMaps* maps)
 // One CTA of 4 warps, 4 dims a lane.  Warp w sums chunks w, w + 4, .. in order
 // and then path keys w, w + 4, ..; the four sums are added in order.  It is
 // bound by latency, not bytes (R 528 bytes a chunk), so everything it reads is
-// asked for before anything is used: the path's K and V, and its scores, before
-// the wait for the chunks, then statistics and the first chunks' sums together.
+// asked for before anything is used: q, the path's K and V, the statistics and
+// the first chunks' sums together.  All of it behind this kernel's own wait: q
+// and the path's rows are by the kernels before the chunks, for which the chunk
+// kernel has waited, but that orders nothing for the reader here.
 constexpr int kMergeAhead = 8;  // chunk sums in flight per warp
 
 __device__ __forceinline__ float4 half4(uint2 x)
@@ -784,7 +786,7 @@ tree_merge_kernel(const float* q, const __grid_constant__ TreeBatch b, int Hq, i
     const int GQ = Hq / Hkv, g = h / GQ, R = v.n_nodes * GQ, np = row.n_path, nch = v.n_chunk;
     const int64_t pr0 = v.part0 + (int64_t)g * R + row.node * GQ + h % GQ, pstep = (int64_t)Hkv * R;
     const size_t rh = (size_t)r * Hq + h;
-    // (behind the chunk kernel, q and the path's rows are in place already)
+    pdl_wait();
     const float4 qv = ld_placed_f4(q + rh * kHeadDim + 4 * lane);
     uint2 kx[4], vx[4];
 #pragma unroll
@@ -798,14 +800,6 @@ tree_merge_kernel(const float* q, const __grid_constant__ TreeBatch b, int Hq, i
             if (vp) vx[i] = ld_placed_u2(vp + 4 * lane);
         }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 k = half4(kx[i]);
-        const float dot = warp_sum_butterfly(
-            __fmaf_rn(qv.w, k.w, __fmaf_rn(qv.z, k.z, __fmaf_rn(qv.y, k.y, __fmul_rn(qv.x, k.x)))));
-        if (lane == 0 && warp + 4 * i < np) ps[warp + 4 * i] = __fmul_rn(dot, scale.sign);
-    }
-    pdl_wait();
     // every warp has all chunks' statistics: chunk lane + 32 j in its lane
     constexpr int kStats = kMaxTreeChunks / 32;
     float w[kStats], L = 0.0f, M = -INFINITY;
@@ -826,6 +820,13 @@ tree_merge_kernel(const float* q, const __grid_constant__ TreeBatch b, int Hq, i
 #pragma unroll
     for (int j = 0; j < kMergeAhead; ++j)
         if (warp + 4 * j < nch) ov[j] = ld_placed_cg_f4(po + (int64_t)(warp + 4 * j) * pstep * (kHeadDim / 4));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 k = half4(kx[i]);
+        const float dot = warp_sum_butterfly(
+            __fmaf_rn(qv.w, k.w, __fmaf_rn(qv.z, k.z, __fmaf_rn(qv.y, k.y, __fmul_rn(qv.x, k.x)))));
+        if (lane == 0 && warp + 4 * i < np) ps[warp + 4 * i] = __fmul_rn(dot, scale.sign);
+    }
     __syncthreads();
     if (scores && tid < v.n_nodes) {
         float x = -INFINITY;
@@ -1021,7 +1022,6 @@ cudaError_t launch_tree_attention(const float* q, const TreeBatch& b, int Hq, in
                                 kTreeSmem, s, maps, q, b, Hq, Hkv, (int)units, runs, sc, part_o, part_ml, scores, lds);
         if (e != cudaSuccess) return e;
         count_launches(1);
-        // right behind the chunks: it starts on what their launch waited for
         e = launch_pdl(tree_merge_kernel, dim3(Hq, b.n_long), dim3(kHeadDim), s, q, b, Hq, Hkv, sc, (const float*)part_o,
                        (const float*)part_ml, out, scores, lds, stats, out_q, out_d);
         if (e != cudaSuccess) return e;

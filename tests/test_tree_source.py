@@ -3,6 +3,8 @@ they are read off the source, no run of the broken form shows them."""
 import os
 import re
 
+import pytest
+
 SOURCE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "invariant_sequence_decode_gb300", "csrc",
                       "tree.cu")
 
@@ -24,3 +26,12 @@ def test_only_encoded_maps_are_prefetched():
     body = kernel("tree_chunk_kernel")
     at = body.index("prefetch.tensormap")
     assert re.search(r"if \(b\.view\[view\]\.n_chunk > 0\)\s*asm volatile\(\"$", body[:at])
+
+
+@pytest.mark.parametrize("name", ["tree_merge_kernel", "tree_short_kernel"])
+def test_nothing_is_read_ahead_of_the_wait(name):
+    """What earlier kernels wrote is visible to a kernel behind its own wait, whatever
+    the kernel between them has waited for."""
+    body = kernel(name)
+    ahead = body[:body.index("pdl_wait()")]
+    assert not re.search(r"ld_\w+\(|tree_key\(|__ldg|__ldcg|\bq\[|part_(o|ml)\b", ahead)
