@@ -521,21 +521,46 @@ class Slot:
         return self.k.shape[2]
 
 
+class _TableMirror:
+    """A slot whose host int32 ``table`` may be replaced or edited between calls;
+    ``table_dev`` is its copy on the device."""
+
+    def __post_init__(self):
+        import numpy as np
+        self.table, self._mirrored, self._captured = np.ascontiguousarray(self.table, dtype=np.int32), None, []
+        self.mirror_table()
+
+    def mirror_table(self, stream=None):
+        """Bring table_dev up to date for a call on ``stream`` and return the host
+        table.  A changed table gets a new device copy (calls under way and
+        captured ones keep theirs), which cannot be made during a capture."""
+        import numpy as np
+        import torch
+        table, device = np.ascontiguousarray(self.table, dtype=np.int32), self.k_pool.device
+        now = None if device.type != "cuda" else stream or torch.cuda.current_stream(device)
+        capturing = now is not None and torch.cuda.is_current_stream_capturing()
+        if self._mirrored is None or not np.array_equal(table, self._mirrored):
+            if capturing:
+                raise RuntimeError("the slot's table changed: call mirror_table() before the capture")
+            self._mirrored = table.copy()
+            self.table_dev = torch.from_numpy(table.copy()).to(device)
+            self._home = None if now is None else torch.cuda.current_stream(device).cuda_stream
+        if capturing:
+            self._captured.append(self.table_dev)
+        elif now is not None and now.cuda_stream != self._home:
+            self.table_dev.record_stream(now)
+        return table
+
+
 @dataclass
-class PagedSlot:
+class PagedSlot(_TableMirror):
     """A slot in pages of 128 tokens: pools fp16 [n_pages][n_layers][Hkv][128][128];
-    ``table`` lists the pool page of each 128-token span (kept as a host int32
-    array and mirrored on the device)."""
+    ``table`` lists the pool page of each 128-token span (a host int32 array,
+    mirrored on the device; each call takes what it holds by then)."""
     k_pool: object
     v_pool: object
     table: object  # numpy int32
     len: int
-
-    def __post_init__(self):
-        import numpy as np
-        import torch
-        self.table = np.ascontiguousarray(self.table, dtype=np.int32)
-        self.table_dev = torch.from_numpy(self.table).to(self.k_pool.device)
 
 
 def luce_decode_step_paged(model: "Model", slots: Sequence[PagedSlot], rows_per_slot: Sequence[int], x, ws,
@@ -545,10 +570,10 @@ def luce_decode_step_paged(model: "Model", slots: Sequence[PagedSlot], rows_per_
     _need(x, torch.float32, "x")
     n = len(slots)
     sc = (PagedSlotC * max(1, n))()
-    for i, s in enumerate(slots):
+    tables = [s.mirror_table(stream) for s in slots]
+    for i, (s, t) in enumerate(zip(slots, tables)):
         sc[i] = PagedSlotC(s.k_pool.data_ptr(), s.v_pool.data_ptr(), s.table_dev.data_ptr(),
-                           s.table.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)), len(s.table),
-                           s.k_pool.shape[0], s.len)
+                           t.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)), t.size, s.k_pool.shape[0], s.len)
     rows = (ctypes.c_int32 * max(1, n))(*rows_per_slot)
     _check(load_library().luce_decode_step_paged(ctypes.byref(model.c), sc, rows, n, x.data_ptr(), _ptr(logits),
                                                  _ptr(argmax), ws.data_ptr(), ws.numel(), _stream(stream)))
@@ -752,22 +777,16 @@ class TreeSlot:
 
 
 @dataclass
-class PagedTreeSlot:
+class PagedTreeSlot(_TableMirror):
     """The same in pages of 128 tokens: pools fp16 [n_pages][n_layers][Hkv][128][128]
     and ``table``, the pool page of each 128-token span (a host int32 array,
-    mirrored on the device as table_dev)."""
+    mirrored on the device as table_dev; each call takes what it holds by then)."""
     k_pool: object
     v_pool: object
     table: object  # numpy int32
     len: int
     parent: object = 1
     pos0: Optional[int] = None
-
-    def __post_init__(self):
-        import numpy as np
-        import torch
-        self.table = np.ascontiguousarray(self.table, dtype=np.int32)
-        self.table_dev = torch.from_numpy(self.table).to(self.k_pool.device)
 
 
 @dataclass
@@ -1047,14 +1066,15 @@ def luce_decode_step_tree(model: "Model", slots: Sequence[TreeSlot], x, ws, logi
     if sum(t[0] for t in trees) != T:
         raise ValueError(f"x has {T} rows, the trees {sum(t[0] for t in trees)}")
     sc = ((PagedTreeSlotC if paged else TreeSlotC) * max(1, n))()
-    for i, (s, (nn, par)) in enumerate(zip(slots, trees)):
+    tables = [s.mirror_table(stream) if paged else None for s in slots]
+    for i, (s, (nn, par), t) in enumerate(zip(slots, trees, tables)):
         pos0 = s.len if s.pos0 is None else s.pos0
         if paged:
             _pools(s.k_pool, s.v_pool, L, Hkv, f"slots[{i}]")
             _same_device(x, s.k_pool, s.v_pool, s.table_dev)
             sc[i] = PagedTreeSlotC(s.k_pool.data_ptr(), s.v_pool.data_ptr(), s.table_dev.data_ptr(),
-                                   s.table.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)), len(s.table),
-                                   s.k_pool.shape[0], s.len, pos0, nn, par)
+                                   t.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)), t.size, s.k_pool.shape[0], s.len,
+                                   pos0, nn, par)
         else:
             _caches(s.k, s.v, L, Hkv, f"slots[{i}]")
             _same_device(x, s.k, s.v)

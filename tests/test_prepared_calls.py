@@ -1,0 +1,76 @@
+"""What the Python calls hand to the library, seen by a stand-in for it: no
+device needed, the tensors lie on the host."""
+import contextlib
+import ctypes
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+import invariant_sequence_decode_gb300 as luce  # noqa: E402
+
+
+def ints(p, n):
+    return np.ctypeslib.as_array(ctypes.cast(p, ctypes.POINTER(ctypes.c_int32)), (n,)).tolist()
+
+
+@pytest.fixture
+def library(monkeypatch):
+    """Stands in for the library: names' functions are set by the tests."""
+    class Library:
+        luce_last_error = staticmethod(lambda: b"refused")
+
+        def __getitem__(self, name):
+            return getattr(self, name)
+
+    lib = Library()
+    monkeypatch.setattr(luce, "load_library", lambda *a: lib)
+    monkeypatch.setattr(luce, "_need", lambda *a: None)
+    monkeypatch.setattr(luce, "_kv_pair", lambda *a: None)
+    monkeypatch.setattr(luce, "_stream", lambda stream=None: 0)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    return lib
+
+
+class TinyModel:
+    layers, n_kv_heads, n_q_heads, vocab = [None], 2, 4, 0
+    c = luce.ModelC()
+
+
+def paged_steps(library):
+    """(make a slot, step over it): what a step sees as its host and its device table."""
+    seen = []
+
+    def step(model, slots, *rest):
+        s = slots[0]
+        seen.append((ints(s.table_host, s.n_table), ints(s.table, s.n_table)))
+        return 0
+
+    library.luce_decode_step_paged = library.luce_decode_step_tree_paged = step
+    pool = lambda: torch.zeros(8, 1, 2, 128, 128, dtype=torch.float16)  # noqa: E731
+    x, ws = torch.zeros(1, 256), torch.zeros(1024, dtype=torch.uint8)
+    return seen, {
+        "tree": (lambda t: luce.PagedTreeSlot(pool(), pool(), t, 130, 1),
+                 lambda s: luce.luce_decode_step_tree(TinyModel, [s], x, ws)),
+        "plain": (lambda t: luce.PagedSlot(pool(), pool(), t, 130),
+                  lambda s: luce.luce_decode_step_paged(TinyModel, [s], [1], x, ws)),
+    }
+
+
+@pytest.mark.parametrize("kind", ["tree", "plain"])
+def test_a_paged_step_reads_the_table_it_was_given_last(library, kind):
+    seen, steps = paged_steps(library)
+    make, step = steps[kind]
+    slot = make([3, 1])
+    step(slot)
+    first = slot.table_dev
+    step(slot)
+    assert slot.table_dev is first                       # nothing changed, nothing copied
+    slot.table[1] = 5                                    # a page was remapped
+    step(slot)
+    slot.table = np.array([3, 5, 7, 0])                  # the cache grew
+    step(slot)
+    slot.table = [2, 6]
+    step(slot)
+    want = [[3, 1], [3, 1], [3, 5], [3, 5, 7, 0], [2, 6]]
+    assert seen == [(t, t) for t in want]
