@@ -86,9 +86,15 @@ int tree_max_chunks(int max_len, int Hkv)
 // row = part0 + (chunk * Hkv + g) * R + i, i = node * GQ + head of the group.
 size_t tree_part_bytes(int64_t n_part) { return (size_t)n_part * (kHeadDim + 4) * sizeof(float); }
 
+__device__ __forceinline__ const __half* flat_key(const TreeView& v, const __half* base, int g, int key)
+{
+    return base + (int64_t)g * v.head_stride + (int64_t)key * v.tok_stride;
+}
+
+// The key's row; nullptr for a page outside the pool.
 __device__ __forceinline__ const __half* tree_key(const TreeView& v, const __half* base, int g, int key)
 {
-    if (!v.pages) return base + (int64_t)g * v.head_stride + (int64_t)key * v.tok_stride;
+    if (!v.pages) return flat_key(v, base, g, key);
     const int p = ld_placed_i(v.pages + (key >> 7));
     if (p < 0 || p >= v.n_pages) return nullptr;
     return base + (int64_t)p * v.page_stride + (int64_t)g * v.head_stride + (int64_t)(key & 127) * v.tok_stride;
@@ -753,7 +759,9 @@ static bool tree_maps(const TreeBatch& b, int Hkv, TreeMaps* maps)
 // asked for before anything is used: q, the path's K and V, the statistics and
 // the first chunks' sums together.  All of it behind this kernel's own wait: q
 // and the path's rows are by the kernels before the chunks, for which the chunk
-// kernel has waited, but that orders nothing for the reader here.
+// kernel has waited, but that orders nothing for the reader here.  Ahead of the
+// wait only addresses are formed and lines of flat caches asked for in L2 (16
+// nodes with scores 12.3 us, 13.2 without that).
 constexpr int kMergeAhead = 8;  // chunk sums in flight per warp
 
 __device__ __forceinline__ float4 half4(uint2 x)
@@ -771,6 +779,9 @@ __device__ __forceinline__ void axpy4(float4& o, float4 x, float a)
     o.w = __fmaf_rn(x.w, a, o.w);
 }
 
+// Asks for a line in L2; no value is read.
+__device__ __forceinline__ void fetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory"); }
+
 __global__ void __launch_bounds__(kHeadDim)
 tree_merge_kernel(const float* q, const __grid_constant__ TreeBatch b, int Hq, int Hkv, TreeScale scale,
                   const float* part_o, const float* part_ml, float* __restrict__ out,
@@ -786,22 +797,45 @@ tree_merge_kernel(const float* q, const __grid_constant__ TreeBatch b, int Hq, i
     const int GQ = Hq / Hkv, g = h / GQ, R = v.n_nodes * GQ, np = row.n_path, nch = v.n_chunk;
     const int64_t pr0 = v.part0 + (int64_t)g * R + row.node * GQ + h % GQ, pstep = (int64_t)Hkv * R;
     const size_t rh = (size_t)r * Hq + h;
+    const float* qp = q + rh * kHeadDim + 4 * lane;
+    fetch_l2(qp);
+    const __half *kp[4], *vp[4];
+    if (!v.pages) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (warp + 4 * i < np) {
+                const int key = v.len + row.path[warp + 4 * i];
+                kp[i] = flat_key(v, v.k, g, key) + 4 * lane;
+                vp[i] = flat_key(v, v.v, g, key) + 4 * lane;
+                fetch_l2(kp[i]);
+                fetch_l2(vp[i]);
+            }
+    }
+    constexpr int kStats = kMaxTreeChunks / 32;
+    const float* mlp = part_ml + 4 * (pr0 + lane * pstep);
+    const float4* po = reinterpret_cast<const float4*>(part_o) + (pr0 + warp * pstep) * (kHeadDim / 4) + lane;
+    int64_t ml_step = 32 * 4 * pstep, po_step = 4 * pstep * (kHeadDim / 4);
+    int chunks = nch;
+    asm volatile("" : "+l"(mlp), "+l"(po), "+l"(ml_step), "+l"(po_step), "+r"(chunks));  // (formed by now)
     pdl_wait();
-    const float4 qv = ld_placed_f4(q + rh * kHeadDim + 4 * lane);
+    const float4 qv = ld_placed_f4(qp);
     uint2 kx[4], vx[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         kx[i] = vx[i] = make_uint2(0, 0);
-        if (warp + 4 * i < np) {
+        if (warp + 4 * i >= np) continue;
+        if (v.pages) {
             const int key = v.len + row.path[warp + 4 * i];
-            const __half* kp = tree_key(v, v.k, g, key);
-            const __half* vp = tree_key(v, v.v, g, key);
-            if (kp) kx[i] = ld_placed_u2(kp + 4 * lane);
-            if (vp) vx[i] = ld_placed_u2(vp + 4 * lane);
+            const __half* base = tree_key(v, v.k, g, key);
+            kp[i] = base ? base + 4 * lane : nullptr;
+            vp[i] = base ? v.v + (kp[i] - v.k) : nullptr;
+        }
+        if (kp[i]) {
+            kx[i] = ld_placed_u2(kp[i]);
+            vx[i] = ld_placed_u2(vp[i]);
         }
     }
     // every warp has all chunks' statistics: chunk lane + 32 j in its lane
-    constexpr int kStats = kMaxTreeChunks / 32;
     float w[kStats], L = 0.0f, M = -INFINITY;
     float2 ls[kStats];
 #pragma unroll
@@ -809,23 +843,23 @@ tree_merge_kernel(const float* q, const __grid_constant__ TreeBatch b, int Hq, i
         const int c = lane + 32 * j;
         w[j] = -INFINITY;
         ls[j] = make_float2(0.0f, 0.0f);
-        if (c < nch) {
-            const float4 ml = ld_placed_cg_f4(part_ml + 4 * (pr0 + c * pstep));
+        if (c < chunks) {
+            const float4 ml = ld_placed_cg_f4(mlp + j * ml_step);
             w[j] = ml.x;
             ls[j] = make_float2(ml.y, ml.z);
         }
     }
     float4 ov[kMergeAhead];
-    const float4* po = reinterpret_cast<const float4*>(part_o) + pr0 * (kHeadDim / 4) + lane;
 #pragma unroll
     for (int j = 0; j < kMergeAhead; ++j)
-        if (warp + 4 * j < nch) ov[j] = ld_placed_cg_f4(po + (int64_t)(warp + 4 * j) * pstep * (kHeadDim / 4));
+        if (warp + 4 * j < chunks) ov[j] = ld_placed_cg_f4(po + j * po_step);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+        if (warp + 4 * i >= np) break;
         const float4 k = half4(kx[i]);
         const float dot = warp_sum_butterfly(
             __fmaf_rn(qv.w, k.w, __fmaf_rn(qv.z, k.z, __fmaf_rn(qv.y, k.y, __fmul_rn(qv.x, k.x)))));
-        if (lane == 0 && warp + 4 * i < np) ps[warp + 4 * i] = __fmul_rn(dot, scale.sign);
+        if (lane == 0) ps[warp + 4 * i] = __fmul_rn(dot, scale.sign);
     }
     __syncthreads();
     if (scores && tid < v.n_nodes) {
@@ -851,13 +885,13 @@ tree_merge_kernel(const float* q, const __grid_constant__ TreeBatch b, int Hq, i
     for (int j = 0; j < kMaxTreeChunks / 4; ++j) {  // chunk 4 j + warp: its weight is in lane (4 j + warp) & 31's w[j >> 3]
         const int c = 4 * j + warp;
         if ((j & (kMergeAhead - 1)) == 0 && j > 0) {
-            if (4 * j >= nch) break;
+            if (4 * j >= chunks) break;
 #pragma unroll
             for (int e = 0; e < kMergeAhead; ++e)
-                if (c + 4 * e < nch) ov[e] = ld_placed_cg_f4(po + (int64_t)(c + 4 * e) * pstep * (kHeadDim / 4));
+                if (c + 4 * e < chunks) ov[e] = ld_placed_cg_f4(po + (j + e) * po_step);
         }
         const float f = __shfl_sync(0xffffffffu, w[j >> 3], c & 31);
-        if (c < nch) axpy4(o, ov[j & (kMergeAhead - 1)], f);
+        if (c < chunks) axpy4(o, ov[j & (kMergeAhead - 1)], f);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
