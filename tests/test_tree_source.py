@@ -34,4 +34,4 @@ def test_nothing_is_read_ahead_of_the_wait(name):
     the kernel between them has waited for."""
     body = kernel(name)
     ahead = body[:body.index("pdl_wait()")]
-    assert not re.search(r"ld_\w+\(|tree_key\(|__ldg|__ldcg|\bq\[|part_(o|ml)\b", ahead)
+    assert not re.search(r"ld_\w+\(|tree_key\(|__ldg|__ldcg|\b(q|part_o|part_ml|qp|mlp|po)\[|\*\s*(q|qp|mlp|po)\s*;", ahead)
