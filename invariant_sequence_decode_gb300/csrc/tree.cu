@@ -16,9 +16,10 @@
 // heads make R = n GQ <= 128 rows that share every key, so both products run
 // as 128-row tcgen05.mma tiles, row = tensor-memory lane: S = Q K^T over tiles
 // of 128 keys, then O = P V.  K and V are f16; q and p are fp32 and go in as
-// two f16 parts each, x = hi + lo, both parts multiplied in: the products then
-// carry 2^-22 of q and p, the size of an fp32 sum's own error, where one f16
-// part would lose 2^-11.
+// two f16 parts each, x = hi + lo, both parts multiplied in.  The parts hold x
+// to within 2^-22, the size of an fp32 sum's own error (one f16 part would lose
+// 2^-11), or to within 2^-25 where that is more; p is 2^15 e^(s - m), so a weight
+// is off by 2^-22 of itself or by 2^-40 of the largest one so far.
 // Long prefixes are bound by reading K and V (64 KB a tile: at full rate an SM
 // gets one in about 2,860 cycles), with the products (2,080 cycles) and the
 // softmax (1,050 of them exponentials) close behind, so what matters is that
@@ -82,7 +83,8 @@ int tree_max_chunks(int max_len, int Hkv)
 }
 
 // A view chunk's partial results: part_o [row][128] and part_ml [row][4] = (m,
-// l of the keys 0..63 of its tiles, l of the keys 64..127, unused), with
+// l of the keys 0..63 of its tiles, l of the keys 64..127, unused), the sums
+// times 2^15, with
 // row = part0 + (chunk * Hkv + g) * R + i, i = node * GQ + head of the group.
 size_t tree_part_bytes(int64_t n_part) { return (size_t)n_part * (kHeadDim + 4) * sizeof(float); }
 
@@ -112,6 +114,9 @@ constexpr int kTreeSmem = 2 * kTreeStages * kTreeTileBytes + 1024;
 // tensor memory, 512 columns: S/P twice, O, q's two parts
 constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384;
 constexpr float kLn2 = 0.6931471805599453f;
+// A chunk's weights (and so its sums) are 2^kTreeUp e^(s - m): f16 has no digits
+// below 2^-24, and one dominant key would take those of the chunk's others.
+constexpr float kTreeUp = 15.0f, kTreeDown = 1.0f / 32768.0f;
 
 __device__ unsigned int g_tree_wait_timeouts;
 
@@ -631,8 +636,9 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
                     // below), an expired wait or not, and leave together
                     asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
                     if ((left = bail[quad])) break;
-                    const float top = fmaxf(m, __fmul_rn(fmaxf(mx[i & 1][0][row], mx[i & 1][1][row]), scale.log2));
-                    const float at = top == -INFINITY ? 0.0f : top;
+                    // rounded up, and the weights' shift below down: none is above 2^kTreeUp
+                    const float top = fmaxf(m, __fmul_ru(fmaxf(mx[i & 1][0][row], mx[i & 1][1][row]), scale.log2));
+                    const float at = top == -INFINITY ? 0.0f : top, up = __fsub_rd(kTreeUp, at);
                     alpha = tree_exp2(__fsub_rn(m, at));  // 0 for m = -inf
                     m = top;
                     if (sc) {
@@ -664,7 +670,7 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
                             __syncwarp();
                         }
                     }
-                    const uint64_t c2 = pair(scale.log2, scale.log2), m2 = pair(-at, -at);
+                    const uint64_t c2 = pair(scale.log2, scale.log2), m2 = pair(up, up);
                     uint64_t sum[4] = {0, 0, 0, 0};
                     uint32_t hi[32], lo[32];
 #pragma unroll
@@ -875,7 +881,7 @@ tree_merge_kernel(const float* q, const __grid_constant__ TreeBatch b, int Hq, i
     const float ref = M == -INFINITY ? 0.0f : M;
 #pragma unroll
     for (int j = 0; j < kStats; ++j) {
-        w[j] = tree_exp2(__fsub_rn(w[j], ref));
+        w[j] = __fmul_rn(tree_exp2(__fsub_rn(w[j], ref)), kTreeDown);
         L = __fmaf_rn(__fadd_rn(ls[j].x, ls[j].y), w[j], L);
     }
     p = tree_exp2(__fsub_rn(p, ref));
