@@ -18,8 +18,10 @@
 // of 128 keys, then O = P V.  K and V are f16; q and p are fp32 and go in as
 // two f16 parts each, x = hi + lo, both parts multiplied in.  The parts hold x
 // to within 2^-22, the size of an fp32 sum's own error (one f16 part would lose
-// 2^-11), or to within 2^-25 where that is more; p is 2^15 e^(s - m), so a weight
-// is off by 2^-22 of itself or by 2^-40 of the largest one so far.
+// 2^-11), or to within 2^-25 where that is more; so q is held in units of a power
+// of two that puts its row's largest element into [2^14, 2^15), and p is
+// 2^15 e^(s - m): an element of q is off by 2^-22 of itself or 2^-39 of its row's
+// largest, a weight by 2^-22 of itself or 2^-40 of the largest one so far.
 // Long prefixes are bound by reading K and V (64 KB a tile: at full rate an SM
 // gets one in about 2,860 cycles), with the products (2,080 cycles) and the
 // softmax (1,050 of them exponentials) close behind, so what matters is that
@@ -434,6 +436,7 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
     __shared__ TreeBars bar;
     __shared__ uint32_t tmem_at;
     __shared__ float mx[2][2][kTreeTile];  // a row's maxima of a tile's two halves, by tile parity
+    __shared__ float qmx[2][kTreeTile];    // and of |q|'s two halves
     __shared__ volatile int bail[4];       // a wait of the row quarter's warps expired
     // A warp's 32 rows, 16 columns at a time, on their way between a row per
     // thread and 64 bytes of a row per four threads: global loads and stores by
@@ -510,6 +513,7 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
             far_row[e] = rr / GQ * Hq + rr % GQ;
         }
         int i = 0, last = -1, R = 0;
+        float unit = 0.0f;                      // the row's power of two: q is held in units of it
         bool ok = true, left = false;
         // the tile whose O is still to come: its correction of the sum before
         // it (none: the chunk's first), whether the warp has rows in it, where
@@ -561,6 +565,23 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
                         x[e] = in ? ld_placed_f4(q + (head + far_row[e & 3]) * kHeadDim + 64 * half + 16 * (e >> 2) + piece)
                                   : make_float4(0, 0, 0, 0);
                     }
+                    // the row's unit puts its largest element into [2^14, 2^15)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float big = 0.0f;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const float4 y = x[4 * c + e];
+                            big = fmaxf(big, fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w))));
+                        }
+                        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                        if ((lane & 3) == 0) qmx[half][32 * quad + 8 * e + (lane >> 2)] = big;
+                    }
+                    asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
+                    const int exp = max((__float_as_int(fmaxf(qmx[0][row], qmx[1][row])) >> 23) - 127 - 14, -112);
+                    unit = __int_as_float((127 + exp) << 23);
+                    const float into = __fmul_rn(scale.sign, __int_as_float((127 - exp) << 23));
                     uint32_t hi[32], lo[32];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
@@ -572,8 +593,8 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
                         for (int e = 0; e < 4; ++e) {
                             const float4 y = *reinterpret_cast<const float4*>(st + lane * kStageRow + 4 * e);
                             const int at = 8 * c + 2 * e;
-                            tree_split(__fmul_rn(y.x, scale.sign), __fmul_rn(y.y, scale.sign), hi[at], lo[at]);
-                            tree_split(__fmul_rn(y.z, scale.sign), __fmul_rn(y.w, scale.sign), hi[at + 1], lo[at + 1]);
+                            tree_split(__fmul_rn(y.x, into), __fmul_rn(y.y, into), hi[at], lo[at]);
+                            tree_split(__fmul_rn(y.z, into), __fmul_rn(y.w, into), hi[at + 1], lo[at + 1]);
                         }
                         __syncwarp();
                     }
@@ -637,19 +658,20 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
                     asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
                     if ((left = bail[quad])) break;
                     // rounded up, and the weights' shift below down: none is above 2^kTreeUp
-                    const float top = fmaxf(m, __fmul_ru(fmaxf(mx[i & 1][0][row], mx[i & 1][1][row]), scale.log2));
+                    const float log2 = __fmul_rn(scale.log2, unit);
+                    const float top = fmaxf(m, __fmul_ru(fmaxf(mx[i & 1][0][row], mx[i & 1][1][row]), log2));
                     const float at = top == -INFINITY ? 0.0f : top, up = __fsub_rd(kTreeUp, at);
                     alpha = tree_exp2(__fsub_rn(m, at));  // 0 for m = -inf
                     m = top;
                     if (sc) {
+                        const float f = __fmul_rn(scale.abs, unit);
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 const float* x = s + 16 * c + 4 * e;
                                 *reinterpret_cast<float4*>(st + lane * kStageRow + 4 * e) =
-                                    make_float4(__fmul_rn(x[0], scale.abs), __fmul_rn(x[1], scale.abs),
-                                                __fmul_rn(x[2], scale.abs), __fmul_rn(x[3], scale.abs));
+                                    make_float4(__fmul_rn(x[0], f), __fmul_rn(x[1], f), __fmul_rn(x[2], f), __fmul_rn(x[3], f));
                             }
                             __syncwarp();
                             const int at = 16 * c + piece, in = n - 64 * half - at;  // keys of the tile from this piece on
@@ -670,7 +692,7 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
                             __syncwarp();
                         }
                     }
-                    const uint64_t c2 = pair(scale.log2, scale.log2), m2 = pair(up, up);
+                    const uint64_t c2 = pair(log2, log2), m2 = pair(up, up);
                     uint64_t sum[4] = {0, 0, 0, 0};
                     uint32_t hi[32], lo[32];
 #pragma unroll

@@ -56,3 +56,38 @@ def test_small_weights_keep_their_digits_beside_a_dominant_key(Hkv, length, at, 
         p = np.exp(score[:, keys].astype(np.float64) - gap)
         want = np.einsum("gk,gkd->gd", p, v[:, keys].astype(np.float64)) / p.sum(1, keepdims=True)
         assert (np.abs(got[j] - want) / want).max() <= tol
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-10, 1e-6, 1e-5, 1e-3, 1.0, 6e4])
+@pytest.mark.parametrize("Hq,Hkv,length", [(40, 8, 300), (3, 1, 1000), (8, 8, 70)])
+def test_q_keeps_its_digits_whatever_its_size(Hq, Hkv, length, size):
+    """Scores of about 1 from small q and large K, or the other way round.
+
+    A score is two times 128 products in fp32 sums (a unit each) and one with scale; an element of q is held within
+    2^-22 of itself or 2^-39 of its row's largest.  K's own error is none: the reference takes the binary16 values.
+    """
+    rng = np.random.default_rng(length)
+    n, cap = 3, length + 3
+    kscale = 1.0 if size >= 1 else 4000.0
+    q = (size * (rng.random((n, Hq, 128)) - 0.5)).astype(np.float32)
+    q[1, :, 5] = size                                         # small elements beside a large one
+    q[1, :, 6:] *= np.float32(2.0 ** -12)
+    k = (kscale * (rng.random((Hkv, cap, 128)) - 0.5)).astype(np.float16)
+    v = rng.standard_normal((Hkv, cap, 128)).astype(np.float16)
+    scale = 1.0 / (size * kscale)
+    lds = -(-cap // 4) * 4
+    sc, st = torch.zeros(n, Hq, lds, device="cuda"), torch.zeros(n, Hq, 2, device="cuda")
+    out = luce.luce_tree_attn(cuda(q), [luce.TreeView(cuda(k), cuda(v), length, n)], Hkv, scale, scores=sc, stats=st)
+    out, sc = out.cpu().numpy().astype(np.float64), sc.cpu().numpy().astype(np.float64)
+    scale = float(np.float32(scale))
+    for j in range(n):
+        for h in range(Hq):
+            K, V, Q = (x.astype(np.float64) for x in (k[h // (Hq // Hkv), :length + j + 1], v[h // (Hq // Hkv), :length + j + 1], q[j, h]))
+            size_of = scale * (np.abs(K) @ np.abs(Q))
+            tol = size_of * (260 * U + 2.0 ** -22) + 2.0 ** -39 * scale * np.abs(Q).max() * np.abs(K).sum(1)
+            s = scale * (K @ Q)
+            assert (np.abs(sc[j, h, :length + j + 1] - s) <= tol).all()
+            p = np.exp(s - s.max())
+            want = p @ V / p.sum()
+            rel = 2 * tol.max() + sums(length) + 2.0 ** -22
+            assert (np.abs(out[j, h] - want) <= rel * (p @ np.abs(V)) / p.sum() * 2).all()
