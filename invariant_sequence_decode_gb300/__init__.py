@@ -23,6 +23,7 @@ MAX_ROWS = 16
 HEAD_DIM = 128
 MAX_KEYS = 130816
 MAX_TREE = 16
+LAST_POS = 2 ** 31 - 1  # no key is this far
 
 LUCE_OK, LUCE_EINVAL, LUCE_EUNSUPPORTED, LUCE_ECUDA, LUCE_ENOSPACE = 0, -1, -2, -3, -4
 
@@ -823,8 +824,10 @@ class PagedCommitSlot:
 @dataclass
 class EvictSlot:
     """A slot's cache with its keys' accumulated weights and positions (as in
-    CommitSlot), to be cut to ``budget`` keys; acc_out and pos_out default to
-    acc and pos themselves."""
+    CommitSlot), to be cut to ``budget`` keys; keys at positions < sinks and
+    >= next_pos - recent stay (``recent`` needs ``next_pos``, the position of
+    the slot's next token); acc_out and pos_out default to acc and pos
+    themselves."""
     k: object
     v: object
     acc: object
@@ -833,7 +836,7 @@ class EvictSlot:
     budget: int
     sinks: int = 0
     recent: int = 0
-    next_pos: int = 0
+    next_pos: Optional[int] = None
     acc_out: object = None
     pos_out: object = None
 
@@ -851,7 +854,7 @@ class PagedEvictSlot:
     budget: int
     sinks: int = 0
     recent: int = 0
-    next_pos: int = 0
+    next_pos: Optional[int] = None
     acc_out: object = None
     pos_out: object = None
 
@@ -1243,11 +1246,10 @@ class KvEvict(_Prepared):
             if paged:
                 self._sc[i] = PagedEvictSlotC(k.data_ptr(), v.data_ptr(), s.table.data_ptr(), s.acc.data_ptr(),
                                               s.pos.data_ptr(), acc_out.data_ptr(), pos_out.data_ptr(), k.shape[0], s.len,
-                                              cap, s.budget, s.sinks, s.recent, s.next_pos)
+                                              cap, s.budget, s.sinks, s.recent, 0)
             else:
                 self._sc[i] = EvictSlotC(k.data_ptr(), v.data_ptr(), s.acc.data_ptr(), s.pos.data_ptr(),
-                                         acc_out.data_ptr(), pos_out.data_ptr(), s.len, cap, s.budget, s.sinks, s.recent,
-                                         s.next_pos)
+                                         acc_out.data_ptr(), pos_out.data_ptr(), s.len, cap, s.budget, s.sinks, s.recent, 0)
         self._items, self._now = [self._sc[i] for i in range(n)], [None] * n
         self._pages = [s.table.numel() * PAGE_KEYS if paged else None for s in self.slots]
         args = (self._sc, n, L, Hkv, HEAD_DIM)
@@ -1259,8 +1261,11 @@ class KvEvict(_Prepared):
             if now != self._now[i]:
                 if self._pages[i] is not None and s.len > self._pages[i]:
                     raise ValueError(f"slots[{i}].table does not hold {s.len} keys")
+                if s.next_pos is None and s.recent:
+                    raise ValueError(f"slots[{i}]: recent={s.recent} needs next_pos, the position of the next token")
                 c = self._items[i]
-                c.len, c.next_pos, c.budget, c.sinks, c.recent = now
+                c.len, c.budget, c.sinks, c.recent = s.len, s.budget, s.sinks, s.recent
+                c.next_pos = LAST_POS if s.next_pos is None else s.next_pos
                 self._now[i] = now
         self._call()
 

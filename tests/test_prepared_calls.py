@@ -74,3 +74,46 @@ def test_a_paged_step_reads_the_table_it_was_given_last(library, kind):
     step(slot)
     want = [[3, 1], [3, 1], [3, 5], [3, 5, 7, 0], [2, 6]]
     assert seen == [(t, t) for t in want]
+
+
+def state(dtype, cap=40):
+    return torch.zeros(1, 2, cap, dtype=dtype)
+
+
+def evict_slot(**kw):
+    kv = lambda: torch.zeros(1, 2, 40, 128, dtype=torch.float16)  # noqa: E731
+    return luce.EvictSlot(kv(), kv(), state(torch.float32), state(torch.int32), 30, 20, **kw)
+
+
+def record(library, name, fields, argtypes):
+    """The named function as one that notes its first slot's fields."""
+    seen = []
+
+    def call(slots, n, *rest):
+        seen.append(tuple(getattr(slots[0], f) for f in fields))
+        return 0
+
+    call.argtypes = argtypes
+    setattr(library, name, call)
+    return seen
+
+
+@pytest.fixture
+def evictions(library, monkeypatch):
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: None, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 0, raising=False)
+    i32 = ctypes.c_int32
+    for name in ("luce_kv_evict", "luce_kv_evict_paged"):
+        seen = record(library, name, ("len", "budget", "sinks", "recent", "next_pos"), [None, i32, i32, i32, i32, None])
+        setattr(library, name + "_seen", seen)
+    return library.luce_kv_evict_seen
+
+
+def test_eviction_without_a_next_position_protects_none_as_recent(evictions):
+    luce.luce_kv_evict([evict_slot()])
+    luce.luce_kv_evict([evict_slot(sinks=2)])
+    assert evictions == [(30, 20, 0, 0, 2 ** 31 - 1), (30, 20, 2, 0, 2 ** 31 - 1)]
+    with pytest.raises(ValueError, match="next_pos"):
+        luce.luce_kv_evict([evict_slot(recent=4)])
+    luce.luce_kv_evict([evict_slot(recent=4, next_pos=31)])
+    assert evictions[2:] == [(30, 20, 0, 4, 31)]
