@@ -795,7 +795,8 @@ class CommitSlot:
     """A slot's cache of every layer (fp16 [n_layers][Hkv][cap][128]) whose tree's
     nodes ``path`` (ascending) were accepted; ``row0`` is the score row of node
     0, ``acc`` (fp32) and ``pos`` (int32), [n_layers][Hkv][cap], its keys'
-    accumulated weights and positions, ``pos0`` the first accepted node's."""
+    accumulated weights and positions, ``pos0`` the first accepted node's
+    (default len, as in TreeSlot)."""
     k: object
     v: object
     len: int
@@ -803,7 +804,7 @@ class CommitSlot:
     row0: int = 0
     acc: object = None
     pos: object = None
-    pos0: int = 0
+    pos0: Optional[int] = None
 
 
 @dataclass
@@ -818,7 +819,7 @@ class PagedCommitSlot:
     row0: int = 0
     acc: object = None
     pos: object = None
-    pos0: int = 0
+    pos0: Optional[int] = None
 
 
 @dataclass
@@ -1173,10 +1174,9 @@ class TreeCommit(_Prepared):
             caches.append((k, v, s.acc, s.pos))
             if paged:
                 self._sc[i] = PagedCommitSlotC(k.data_ptr(), v.data_ptr(), None, 0, k.shape[0], s.len, cap, 0, s.row0, None,
-                                               _ptr(s.acc), _ptr(s.pos), s.pos0)
+                                               _ptr(s.acc), _ptr(s.pos), 0)
             else:
-                self._sc[i] = CommitSlotC(k.data_ptr(), v.data_ptr(), s.len, cap, 0, s.row0, None, _ptr(s.acc),
-                                          _ptr(s.pos), s.pos0)
+                self._sc[i] = CommitSlotC(k.data_ptr(), v.data_ptr(), s.len, cap, 0, s.row0, None, _ptr(s.acc), _ptr(s.pos), 0)
         self._items = [self._sc[i] for i in range(n)]
         self._now, self._arrays = [None] * n, [None] * n
         args = (self._sc, n, L, int(n_q_heads), Hkv, HEAD_DIM, _ptr(scores), n_rows, lds, _ptr(stats))
@@ -1200,7 +1200,8 @@ class TreeCommit(_Prepared):
             if now != self._now[i]:
                 path, c = now[3:], self._items[i]
                 self._arrays[i] = (ctypes.c_int32 * max(1, len(path)))(*path)
-                c.len, c.row0, c.pos0, c.path, c.n_path = s.len, s.row0, s.pos0, self._arrays[i], len(path)
+                c.len, c.row0, c.path, c.n_path = s.len, s.row0, self._arrays[i], len(path)
+                c.pos0 = s.len if s.pos0 is None else s.pos0
                 self._now[i] = now
         self._call()
 

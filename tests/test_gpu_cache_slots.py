@@ -33,3 +33,19 @@ def test_eviction_without_positions_of_its_own_goes_by_weight(length, budget, fi
     torch.cuda.synchronize()
     for t, w in zip((slot.k, slot.v, slot.acc, slot.pos), want):
         assert same(t[:, :, :budget], w[:, :, :budget])
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_a_commit_without_pos0_continues_the_cache(paged):
+    rng = np.random.default_rng(3)
+    L, Hkv, length, path = 2, 2, 200, [0, 3, 4]
+    pos = cuda(np.tile(np.arange(256, dtype=np.int32), (L, Hkv, 1)))
+    pos[:, :, length:] = -1
+    if paged:
+        pool = [cuda(rng.standard_normal((3, L, Hkv, 128, 128)).astype(np.float16)) for _ in range(2)]
+        slot = luce.PagedCommitSlot(*pool, np.array([2, 0], dtype=np.int32), length, path, pos=pos)
+    else:
+        slot = luce.CommitSlot(*(cuda(rng.standard_normal((L, Hkv, 256, 128)).astype(np.float16)) for _ in range(2)), length, path, pos=pos)
+    luce.luce_tree_commit([slot], 4)
+    torch.cuda.synchronize()
+    assert (pos[:, :, :length + 3].cpu() == torch.arange(length + 3)).all() and (pos[:, :, length + 3:] == -1).all()

@@ -99,10 +99,16 @@ def record(library, name, fields, argtypes):
 
 
 @pytest.fixture
-def evictions(library, monkeypatch):
+def prepared(library, monkeypatch):
+    """The library for prepared calls, whose device and stream are the host's."""
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: None, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 0, raising=False)
-    i32 = ctypes.c_int32
+    return library
+
+
+@pytest.fixture
+def evictions(prepared):
+    library, i32 = prepared, ctypes.c_int32
     for name in ("luce_kv_evict", "luce_kv_evict_paged"):
         seen = record(library, name, ("len", "budget", "sinks", "recent", "next_pos"), [None, i32, i32, i32, i32, None])
         setattr(library, name + "_seen", seen)
@@ -117,3 +123,19 @@ def test_eviction_without_a_next_position_protects_none_as_recent(evictions):
         luce.luce_kv_evict([evict_slot(recent=4)])
     luce.luce_kv_evict([evict_slot(recent=4, next_pos=31)])
     assert evictions[2:] == [(30, 20, 0, 4, 31)]
+
+
+def test_a_commit_takes_len_as_its_first_position_unless_told(prepared):
+    i32, vp = ctypes.c_int32, ctypes.c_void_p
+    seen = record(prepared, "luce_tree_commit", ("len", "pos0", "n_path"), [None, i32, i32, i32, i32, i32, vp, i32, ctypes.c_int64, vp, vp])
+    kv = lambda: torch.zeros(1, 2, 40, 128, dtype=torch.float16)  # noqa: E731
+    slot = luce.CommitSlot(kv(), kv(), 30, [0, 2], pos=state(torch.int32))
+    call = luce.TreeCommit([slot], 4)
+    call()
+    slot.len = 32
+    call()
+    slot.pos0 = 0
+    call()
+    slot.pos0 = 70
+    call()
+    assert seen == [(30, 30, 2), (32, 32, 2), (32, 0, 2), (32, 70, 2)]
