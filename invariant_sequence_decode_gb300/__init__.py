@@ -1138,15 +1138,15 @@ def _kind(slots, flat, paged):
 
 class TreeCommit(_Prepared):
     """luce_tree_commit (or luce_tree_commit_paged, for PagedCommitSlots) with its
-    arguments marshalled once: each call takes the slots' current ``len``,
-    ``path``, ``row0``, ``pos0`` and ``table``.  ``scores`` [n_layers][n_rows][Hq][lds] and
+    arguments marshalled once: each call takes what the slots hold by then, and
+    checks tensors that were replaced.  ``scores`` [n_layers][n_rows][Hq][lds] and
     ``stats`` [n_layers][n_rows][Hq][2] (the n_layers dimension may be left out
     for one layer) are what luce_tree_attn gave."""
 
     def __init__(self, slots: Sequence[CommitSlot], n_q_heads: int, scores=None, stats=None, stream=None):
         import torch
         self.slots = list(slots)
-        paged = _kind(self.slots, CommitSlot, PagedCommitSlot)
+        self._paged = paged = _kind(self.slots, CommitSlot, PagedCommitSlot)
         first = self.slots[0].k_pool if paged else self.slots[0].k
         L, Hkv = first.shape[1:3] if paged else first.shape[:2]
         n_rows = lds = 0
@@ -1157,45 +1157,54 @@ class TreeCommit(_Prepared):
             if hq != n_q_heads or scores.numel() != L * n_rows * hq * lds or stats.numel() != L * n_rows * hq * 2:
                 raise ValueError("scores, stats: expected [n_layers][n_rows][Hq][lds] and [n_layers][n_rows][Hq][2]")
         n = len(self.slots)
+        self._first, self._heads = first, (L, Hkv)
+        _same_device(first, scores, stats)
         self._sc = ((PagedCommitSlotC if paged else CommitSlotC) * n)()
-        caches = []
+        self._items, self._tensors = [self._sc[i] for i in range(n)], [None] * n
+        self._now, self._arrays, self._tables = [None] * n, [None] * n, [None] * n
         for i, s in enumerate(self.slots):
-            if paged:
-                _pools(s.k_pool, s.v_pool, L, Hkv, f"slots[{i}]")
-                k, v, cap = s.k_pool, s.v_pool, next((t.shape[-1] for t in (s.acc, s.pos) if t is not None), MAX_KEYS)
-            else:
-                _caches(s.k, s.v, L, Hkv, f"slots[{i}]")
-                k, v, cap = s.k, s.v, s.k.shape[2]
-            if s.acc is not None:
-                _state(s.acc, torch.float32, L, Hkv, cap, f"slots[{i}].acc")
-            if s.pos is not None:
-                _state(s.pos, torch.int32, L, Hkv, cap, f"slots[{i}].pos")
-            _same_device(first, k, v, s.acc, s.pos, scores, stats)
-            caches.append((k, v, s.acc, s.pos))
-            if paged:
-                self._sc[i] = PagedCommitSlotC(k.data_ptr(), v.data_ptr(), None, 0, k.shape[0], s.len, cap, 0, s.row0, None,
-                                               _ptr(s.acc), _ptr(s.pos), 0)
-            else:
-                self._sc[i] = CommitSlotC(k.data_ptr(), v.data_ptr(), s.len, cap, 0, s.row0, None, _ptr(s.acc), _ptr(s.pos), 0)
-        self._items = [self._sc[i] for i in range(n)]
-        self._now, self._arrays = [None] * n, [None] * n
+            self._take(i, s)
         args = (self._sc, n, L, int(n_q_heads), Hkv, HEAD_DIM, _ptr(scores), n_rows, lds, _ptr(stats))
-        self._bind("luce_tree_commit_paged" if paged else "luce_tree_commit", args, first.device, stream, (scores, stats, caches))
-        self._tables = [None] * n if paged else None
+        self._bind("luce_tree_commit_paged" if paged else "luce_tree_commit", args, first.device, stream, (scores, stats))
 
-    def _take_tables(self):
+    def _take(self, i, s):
+        """Slot i's tensors."""
+        import torch
+        (L, Hkv), c = self._heads, self._items[i]
+        if self._paged:
+            _pools(s.k_pool, s.v_pool, L, Hkv, f"slots[{i}]")
+            k, v, cap = s.k_pool, s.v_pool, next((t.shape[-1] for t in (s.acc, s.pos) if t is not None), MAX_KEYS)
+        else:
+            _caches(s.k, s.v, L, Hkv, f"slots[{i}]")
+            k, v, cap = s.k, s.v, s.k.shape[2]
+        if s.acc is not None:
+            _state(s.acc, torch.float32, L, Hkv, cap, f"slots[{i}].acc")
+        if s.pos is not None:
+            _state(s.pos, torch.int32, L, Hkv, cap, f"slots[{i}].pos")
+        _same_device(self._first, k, v, s.acc, s.pos)
+        if self._paged:
+            c.k_pool, c.v_pool, c.n_pages = k.data_ptr(), v.data_ptr(), k.shape[0]
+        else:
+            c.k, c.v = k.data_ptr(), v.data_ptr()
+        c.cap, c.acc, c.pos = cap, _ptr(s.acc), _ptr(s.pos)
+        self._tensors[i] = (k, v, s.acc, s.pos)
+
+    def _take_table(self, i, s):
         import numpy as np
-        for i, s in enumerate(self.slots):
-            if s.table is not self._tables[i]:  # (an int32 array is read where it lies, anything else copied at every call)
-                t = np.ascontiguousarray(s.table, dtype=np.int32)
-                self._tables[i] = t
-                self._items[i].table_host = t.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))
-                self._items[i].n_table = t.size
+        t = np.ascontiguousarray(s.table, dtype=np.int32)
+        self._tables[i] = t  # (an int32 array is read where it lies, anything else copied at every call)
+        self._items[i].table_host = t.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))
+        self._items[i].n_table = t.size
 
     def __call__(self):
-        if self._tables is not None:
-            self._take_tables()
+        paged = self._paged
         for i, s in enumerate(self.slots):
+            t = self._tensors[i]
+            if not ((s.k_pool is t[0] and s.v_pool is t[1]) if paged else (s.k is t[0] and s.v is t[1])) or \
+                    s.acc is not t[2] or s.pos is not t[3]:
+                self._take(i, s)
+            if paged and s.table is not self._tables[i]:
+                self._take_table(i, s)
             now = (s.len, s.row0, s.pos0, *s.path)
             if now != self._now[i]:
                 path, c = now[3:], self._items[i]
@@ -1215,52 +1224,62 @@ def luce_tree_commit(slots: Sequence[CommitSlot], n_q_heads: int, scores=None, s
 
 class KvEvict(_Prepared):
     """luce_kv_evict (or luce_kv_evict_paged, for PagedEvictSlots) with its
-    arguments marshalled once: each call takes the slots' current ``len``,
-    ``budget``, ``sinks``, ``recent`` and ``next_pos``."""
+    arguments marshalled once: each call takes what the slots hold by then, and
+    checks tensors that were replaced."""
 
     def __init__(self, slots: Sequence[EvictSlot], stream=None):
-        import torch
         self.slots = list(slots)
-        paged = _kind(self.slots, EvictSlot, PagedEvictSlot)
+        self._paged = paged = _kind(self.slots, EvictSlot, PagedEvictSlot)
         first = self.slots[0].k_pool if paged else self.slots[0].k
         L, Hkv = first.shape[1:3] if paged else first.shape[:2]
         n = len(self.slots)
+        self._first, self._heads = first, (L, Hkv)
         self._sc = ((PagedEvictSlotC if paged else EvictSlotC) * n)()
-        caches = []
+        self._items, self._now, self._tensors, self._pages = [self._sc[i] for i in range(n)], [None] * n, [None] * n, [0] * n
         for i, s in enumerate(self.slots):
-            if paged:
-                _pools(s.k_pool, s.v_pool, L, Hkv, f"slots[{i}]")
-                _need(s.table, torch.int32, f"slots[{i}].table")
-                k, v, cap = s.k_pool, s.v_pool, s.acc.shape[-1]
-                if s.table.numel() * PAGE_KEYS < min(s.len, cap):
-                    raise ValueError(f"slots[{i}].table: {s.table.numel()} pages do not hold {s.len} keys")
-            else:
-                _caches(s.k, s.v, L, Hkv, f"slots[{i}]")
-                k, v, cap = s.k, s.v, s.k.shape[2]
-            acc_out = s.acc if s.acc_out is None else s.acc_out
-            pos_out = s.pos if s.pos_out is None else s.pos_out
-            for t, dt, w in ((s.acc, torch.float32, "acc"), (acc_out, torch.float32, "acc_out"),
-                             (s.pos, torch.int32, "pos"), (pos_out, torch.int32, "pos_out")):
-                _state(t, dt, L, Hkv, cap, f"slots[{i}].{w}")
-            _same_device(first, k, v, s.acc, s.pos, acc_out, pos_out, s.table if paged else None)
-            caches.append((k, v, s.acc, s.pos, acc_out, pos_out, s.table if paged else None))
-            if paged:
-                self._sc[i] = PagedEvictSlotC(k.data_ptr(), v.data_ptr(), s.table.data_ptr(), s.acc.data_ptr(),
-                                              s.pos.data_ptr(), acc_out.data_ptr(), pos_out.data_ptr(), k.shape[0], s.len,
-                                              cap, s.budget, s.sinks, s.recent, 0)
-            else:
-                self._sc[i] = EvictSlotC(k.data_ptr(), v.data_ptr(), s.acc.data_ptr(), s.pos.data_ptr(),
-                                         acc_out.data_ptr(), pos_out.data_ptr(), s.len, cap, s.budget, s.sinks, s.recent, 0)
-        self._items, self._now = [self._sc[i] for i in range(n)], [None] * n
-        self._pages = [s.table.numel() * PAGE_KEYS if paged else None for s in self.slots]
+            self._take(i, s)
         args = (self._sc, n, L, Hkv, HEAD_DIM)
-        self._bind("luce_kv_evict_paged" if paged else "luce_kv_evict", args, first.device, stream, caches)
+        self._bind("luce_kv_evict_paged" if paged else "luce_kv_evict", args, first.device, stream, None)
+
+    def _take(self, i, s):
+        """Slot i's tensors."""
+        import torch
+        (L, Hkv), c, table = self._heads, self._items[i], None
+        if self._paged:
+            _pools(s.k_pool, s.v_pool, L, Hkv, f"slots[{i}]")
+            _need(s.table, torch.int32, f"slots[{i}].table")
+            k, v, cap, table = s.k_pool, s.v_pool, s.acc.shape[-1], s.table
+            if table.numel() * PAGE_KEYS < min(s.len, cap):
+                raise ValueError(f"slots[{i}].table: {table.numel()} pages do not hold {s.len} keys")
+        else:
+            _caches(s.k, s.v, L, Hkv, f"slots[{i}]")
+            k, v, cap = s.k, s.v, s.k.shape[2]
+        acc_out = s.acc if s.acc_out is None else s.acc_out
+        pos_out = s.pos if s.pos_out is None else s.pos_out
+        for t, dt, w in ((s.acc, torch.float32, "acc"), (acc_out, torch.float32, "acc_out"),
+                         (s.pos, torch.int32, "pos"), (pos_out, torch.int32, "pos_out")):
+            _state(t, dt, L, Hkv, cap, f"slots[{i}].{w}")
+        _same_device(self._first, k, v, s.acc, s.pos, acc_out, pos_out, table)
+        if self._paged:
+            c.k_pool, c.v_pool, c.n_pages, c.table = k.data_ptr(), v.data_ptr(), k.shape[0], table.data_ptr()
+            self._pages[i] = table.numel() * PAGE_KEYS
+        else:
+            c.k, c.v = k.data_ptr(), v.data_ptr()
+        c.acc, c.pos, c.acc_out, c.pos_out = s.acc.data_ptr(), s.pos.data_ptr(), acc_out.data_ptr(), pos_out.data_ptr()
+        c.cap = cap
+        self._tensors[i] = (k, v, s.acc, s.pos, s.acc_out, s.pos_out, table)
+        self._now[i] = None
 
     def __call__(self):
+        paged = self._paged
         for i, s in enumerate(self.slots):
+            t = self._tensors[i]
+            if not ((s.k_pool is t[0] and s.v_pool is t[1] and s.table is t[6]) if paged else (s.k is t[0] and s.v is t[1])) or \
+                    not (s.acc is t[2] and s.pos is t[3] and s.acc_out is t[4] and s.pos_out is t[5]):
+                self._take(i, s)
             now = (s.len, s.next_pos, s.budget, s.sinks, s.recent)
             if now != self._now[i]:
-                if self._pages[i] is not None and s.len > self._pages[i]:
+                if paged and s.len > self._pages[i]:
                     raise ValueError(f"slots[{i}].table does not hold {s.len} keys")
                 if s.next_pos is None and s.recent:
                     raise ValueError(f"slots[{i}]: recent={s.recent} needs next_pos, the position of the next token")

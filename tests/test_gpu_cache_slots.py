@@ -49,3 +49,28 @@ def test_a_commit_without_pos0_continues_the_cache(paged):
     luce.luce_tree_commit([slot], 4)
     torch.cuda.synchronize()
     assert (pos[:, :, :length + 3].cpu() == torch.arange(length + 3)).all() and (pos[:, :, length + 3:] == -1).all()
+
+
+@pytest.mark.parametrize("length,budget", [(300, 290), (700, 300)])
+def test_a_prepared_eviction_follows_a_replaced_table(length, budget):
+    """The same keys in other pages, by the same prepared call."""
+    rng = np.random.default_rng(length)
+    L, Hkv, per = 2, 2, -(-length // 128)
+    k, v = (rng.standard_normal((L, Hkv, per * 128, 128)).astype(np.float16) for _ in range(2))
+    acc = rng.random((L, Hkv, length)).astype(np.float32)
+    pos = np.tile(np.arange(length, dtype=np.int32), (L, Hkv, 1))
+    pools = [torch.zeros(2 * per, L, Hkv, 128, 128, dtype=torch.float16, device="cuda") for _ in range(2)]
+    want = ref.evict(k, v, acc, pos, length, budget, 0, 0, length)
+    slot = luce.PagedEvictSlot(*pools, cuda(np.arange(per, dtype=np.int32)), cuda(acc), cuda(pos), length, budget, next_pos=length,
+                               acc_out=torch.zeros_like(cuda(acc)), pos_out=torch.zeros_like(cuda(pos)))
+    call = luce.KvEvict([slot])
+    for pages in (range(per), range(2 * per - 1, per - 1, -1)):
+        table = np.array(list(pages), dtype=np.int32)
+        slot.table = cuda(table)
+        for pool, x in zip(pools, (k, v)):
+            pool[torch.from_numpy(table).long()] = cuda(x.reshape(L, Hkv, per, 128, 128).transpose(2, 0, 1, 3, 4))
+        call()
+        torch.cuda.synchronize()
+        for pool, w in zip(pools, want[:2]):
+            got = pool[torch.from_numpy(table).long()].cpu().numpy().transpose(1, 2, 0, 3, 4).reshape(L, Hkv, per * 128, 128)
+            assert np.array_equal(got.view(np.uint16), w.view(np.uint16))

@@ -139,3 +139,42 @@ def test_a_commit_takes_len_as_its_first_position_unless_told(prepared):
     slot.pos0 = 70
     call()
     assert seen == [(30, 30, 2), (32, 32, 2), (32, 0, 2), (32, 70, 2)]
+
+
+def test_prepared_evictions_and_commits_follow_replaced_tensors(prepared, monkeypatch):
+    monkeypatch.setattr(luce, "_state", lambda *a: None)
+    monkeypatch.setattr(luce, "_pools", lambda *a: None)
+    i32, vp, i64 = ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64
+    evict_fields = ("k_pool", "v_pool", "table", "acc", "pos", "acc_out", "pos_out", "n_pages", "cap")
+    seen = record(prepared, "luce_kv_evict_paged", evict_fields, [None, i32, i32, i32, i32, vp])
+    pool = lambda n=3: torch.zeros(n, 1, 2, 128, 128, dtype=torch.float16)  # noqa: E731
+    table = lambda n=2: torch.zeros(n, dtype=torch.int32)  # noqa: E731
+    s = luce.PagedEvictSlot(pool(), pool(), table(), state(torch.float32, 256), state(torch.int32, 256), 200, 100)
+    call = luce.KvEvict([s])
+
+    def want():
+        outs = (s.acc if s.acc_out is None else s.acc_out, s.pos if s.pos_out is None else s.pos_out)
+        return tuple(t.data_ptr() for t in (s.k_pool, s.v_pool, s.table, s.acc, s.pos, *outs)) + (len(s.k_pool), s.acc.shape[-1])
+
+    for change in ({}, {"table": table()}, {"k_pool": pool(5), "v_pool": pool(5)}, {"acc_out": state(torch.float32, 256)},
+                   {"acc": state(torch.float32, 256)}, {"pos": state(torch.int32, 256)}, {"table": table(4)}):
+        for name, t in change.items():
+            setattr(s, name, t)
+        call()
+        assert seen[-1] == want()
+    s.len = 513
+    with pytest.raises(ValueError, match="does not hold"):
+        call()
+    s.len, s.table = 300, table(2)
+    with pytest.raises(ValueError):
+        call()
+    commit_fields = ("k", "v", "acc", "pos", "cap")
+    seen = record(prepared, "luce_tree_commit", commit_fields, [None, i32, i32, i32, i32, i32, vp, i32, i64, vp, vp])
+    kv = lambda n=40: torch.zeros(1, 2, n, 128, dtype=torch.float16)  # noqa: E731
+    c = luce.CommitSlot(kv(), kv(), 30, [0, 2], acc=state(torch.float32), pos=state(torch.int32))
+    call = luce.TreeCommit([c], 4)
+    for change in ({}, {"k": kv(), "v": kv()}, {"acc": state(torch.float32)}, {"pos": None}, {"k": kv(50), "v": kv(50), "acc": None}):
+        for name, t in change.items():
+            setattr(c, name, t)
+        call()
+        assert seen[-1] == tuple(None if t is None else t.data_ptr() for t in (c.k, c.v, c.acc, c.pos)) + (c.k.shape[2],)
