@@ -911,12 +911,13 @@ class _Prepared:
         import torch
         if stream is None:
             t = torch.empty(shape, dtype=dtype, device=device)
-            self._home = torch._C._cuda_getCurrentRawStream(device.index)
+            home = torch._C._cuda_getCurrentRawStream(device.index)
         else:
             with torch.cuda.stream(stream):
                 t = torch.empty(shape, dtype=dtype, device=device)
-            self._home = stream.cuda_stream
-        self._owned = self._owned + (t,)
+            home = stream.cuda_stream
+        self._home = home if self._home in (None, home) else -1  # (of several streams: every call lends)
+        self._owned, self._lent, self._at = self._owned + (t,), frozenset(), None
         return t
 
     def _lend(self, stream):
@@ -946,10 +947,11 @@ class TreeAttention(_Prepared):
     """luce_tree_attn (or luce_tree_attn_paged, for PagedTreeViews) with its
     arguments marshalled once, for repeated calls over the same buffers: q fp32
     [T][Hq][128], ``out`` as q, ``scores`` fp32 [T][Hq][lds] and ``stats`` fp32
-    [T][Hq][2] when given.  Each call takes the views' current ``len``.  The
-    object owns its workspace (sized for the views' capacity) unless one is
-    given, so calls of one object must not overlap on the GPU, and a graph that
-    captured a call needs the object alive."""
+    [T][Hq][2] when given.  Each call takes what the views hold by then (another
+    tree, other rows of the T, a longer cache) and checks tensors that were
+    replaced.  The object owns its workspace (sized for the views' capacity)
+    unless one is given, so calls of one object must not overlap on the GPU, and
+    a graph that captured a call needs the object and the call's caches alive."""
 
     def __init__(self, q, views, n_kv_heads: int, scale: float, out=None, scores=None, stats=None, ws=None, stream=None):
         import torch
@@ -963,10 +965,6 @@ class TreeAttention(_Prepared):
         paged = isinstance(self.views[0], PagedTreeView)
         if not all(isinstance(v, PagedTreeView if paged else TreeView) for v in self.views):
             raise TypeError("views: expected TreeViews or PagedTreeViews, of one kind")
-        trees = [_tree(v.parent) for v in self.views]
-        rows = max(v.row0 + n for v, (n, _) in zip(self.views, trees))
-        if rows != T:
-            raise ValueError(f"q has {T} rows, the views name {rows}")
         self.out = self._allocate(q.shape, torch.float32, q.device, stream) if out is None else out
         _need(self.out, torch.float32, "out")
         if self.out.shape != q.shape:
@@ -982,44 +980,72 @@ class TreeAttention(_Prepared):
             if stats.shape != (T, Hq, 2):
                 raise ValueError("stats: expected [T][Hq][2]")
         n = len(self.views)
-        caps = []
-        if paged:
-            self._vc = (PagedTreeViewC * n)()
-            for i, (v, (nn, par)) in enumerate(zip(self.views, trees)):
-                _kv_pair(v.k_pool, v.v_pool, 4, f"views[{i}]")
-                _need(v.k_pool, torch.float16, f"views[{i}].k_pool")
-                _need(v.v_pool, torch.float16, f"views[{i}].v_pool")
-                _need(v.table, torch.int32, f"views[{i}].table")
-                if v.k_pool.shape[1:] != (n_kv_heads, PAGE_KEYS, HEAD_DIM):
-                    raise ValueError(f"views[{i}]: expected pools [n_pages][{n_kv_heads}][128][128]")
-                _same_device(q, v.k_pool, v.v_pool, v.table)
-                caps.append(min(v.table.numel() * PAGE_KEYS, MAX_KEYS) - nn)
-                self._vc[i] = PagedTreeViewC(v.k_pool.data_ptr(), v.v_pool.data_ptr(), v.table.data_ptr(),
-                                             v.k_pool.shape[0], v.len, nn, v.row0, par)
-            name = "luce_tree_attn_paged"
-        else:
-            self._vc = (TreeViewC * n)()
-            for i, (v, (nn, par)) in enumerate(zip(self.views, trees)):
-                _kv_pair(v.k, v.v, 3, f"views[{i}]")
-                if v.k.shape[0] != n_kv_heads:
-                    raise ValueError(f"views[{i}]: {v.k.shape[0]} heads, expected {n_kv_heads}")
-                _same_device(q, v.k, v.v)
-                caps.append(min(v.k.shape[1], MAX_KEYS) - nn)
-                self._vc[i] = TreeViewC(v.k.data_ptr(), v.v.data_ptr(), v.len, nn, v.row0, v.k.shape[1], v.k.stride(0),
-                                        v.k.stride(1), par)
-            name = "luce_tree_attn"
+        self._paged, self._q, self._shape = paged, q, (T, Hq, int(n_kv_heads), D)
+        self._vc = ((PagedTreeViewC if paged else TreeViewC) * n)()
+        self._items, self._lens = [self._vc[i] for i in range(n)], [v.len for v in self.views]
+        self._caps, self._seen = [0] * n, [None] * n
+        for i, v in enumerate(self.views):
+            self._take(i, v)
+        self._check_rows()
         _same_device(q, self.out, scores, stats, ws)
-        self._caps, self._items, self._lens = caps, [self._vc[i] for i in range(n)], [v.len for v in self.views]
-        for v, cap in zip(self.views, caps):
-            self._fits(v.len, cap)
+        self._own_ws = ws is None
         if ws is None:
-            need = luce_tree_attn_workspace_size(T, Hq, int(n_kv_heads), D, max(0, *caps))
-            ws = self._allocate((max(256, need),), torch.uint8, q.device, stream)
+            ws = self._allocate((self._ws_bytes(),), torch.uint8, q.device, stream)
         _need(ws, torch.uint8, "ws")
         args = (q.data_ptr(), self._vc, n, Hq, int(n_kv_heads), D, float(scale), self.out.data_ptr(), _ptr(scores), lds,
                 _ptr(stats), ws.data_ptr(), ws.numel())
-        caches = [(v.k_pool, v.v_pool, v.table) if paged else (v.k, v.v) for v in self.views]
-        self._bind(name, args, q.device, stream, (q, scores, stats, ws, trees, caches))
+        self._ws_args = len(args) - 2
+        self._bind("luce_tree_attn_paged" if paged else "luce_tree_attn", args, q.device, stream, (q, scores, stats, ws))
+
+    def _take(self, i, v):
+        """View i's tensors, tree and rows."""
+        import torch
+        c, Hkv = self._items[i], self._shape[2]
+        nn, par = _tree(v.parent)
+        if self._paged:
+            _kv_pair(v.k_pool, v.v_pool, 4, f"views[{i}]")
+            _need(v.k_pool, torch.float16, f"views[{i}].k_pool")
+            _need(v.v_pool, torch.float16, f"views[{i}].v_pool")
+            _need(v.table, torch.int32, f"views[{i}].table")
+            if v.k_pool.shape[1:] != (Hkv, PAGE_KEYS, HEAD_DIM):
+                raise ValueError(f"views[{i}]: expected pools [n_pages][{Hkv}][128][128]")
+            _same_device(self._q, v.k_pool, v.v_pool, v.table)
+            cap, tensors = v.table.numel() * PAGE_KEYS, (v.k_pool, v.v_pool, v.table)
+            c.k_pool, c.v_pool, c.table, c.n_pages = *(t.data_ptr() for t in tensors), v.k_pool.shape[0]
+        else:
+            _kv_pair(v.k, v.v, 3, f"views[{i}]")
+            if v.k.shape[0] != Hkv:
+                raise ValueError(f"views[{i}]: {v.k.shape[0]} heads, expected {Hkv}")
+            _same_device(self._q, v.k, v.v)
+            cap, tensors = v.k.shape[1], (v.k, v.v, None)
+            c.k, c.v, c.cap = v.k.data_ptr(), v.v.data_ptr(), cap
+            c.head_stride, c.tok_stride = v.k.stride(0), v.k.stride(1)
+        self._caps[i] = min(cap, MAX_KEYS) - nn
+        self._fits(v.len, self._caps[i])
+        c.len, c.n_nodes, c.row0, c.parent = v.len, nn, v.row0, par
+        self._lens[i] = v.len
+        # the tree as given, to tell whether it changed (one that has no == of its own is taken at every call)
+        kind = type(v.parent) if type(v.parent) in (int, list, tuple) else None
+        self._seen[i] = (*tensors, v.row0, kind, list(v.parent) if kind is list else v.parent, par)
+        self._rows = None
+
+    def _check_rows(self):
+        rows, T = max(c.row0 + c.n_nodes for c in self._items), self._shape[0]
+        if rows != T:
+            raise ValueError(f"q has {T} rows, the views name {rows}")
+        self._rows = rows
+
+    def _ws_bytes(self):
+        return max(256, luce_tree_attn_workspace_size(*self._shape, max(0, *self._caps)))
+
+    def _retake(self, i, v):
+        """View i changed: more room is asked for where its cache grew."""
+        import torch
+        self._take(i, v)
+        at = self._ws_args
+        if self._own_ws and self._ws_bytes() > self._args[at + 1].value:
+            ws = self._allocate((self._ws_bytes(),), torch.uint8, self._q.device, self._keep[0])
+            self._args = (*self._args[:at], ctypes.c_void_p(ws.data_ptr()), ctypes.c_size_t(ws.numel()))
 
     @staticmethod
     def _fits(length, cap):
@@ -1027,10 +1053,17 @@ class TreeAttention(_Prepared):
             raise ValueError(f"len {length} and the tree exceed the cache")
 
     def __call__(self):
+        paged = self._paged
         for i, v in enumerate(self.views):
+            k, vv, table, row0, kind, parent, _ = self._seen[i]
+            if not ((v.k_pool is k and v.v_pool is vv and v.table is table) if paged else (v.k is k and v.v is vv)) or \
+                    v.row0 != row0 or type(v.parent) is not kind or v.parent != parent:
+                self._retake(i, v)
             if v.len != self._lens[i]:
                 self._fits(v.len, self._caps[i])
                 self._items[i].len = self._lens[i] = v.len
+        if self._rows is None:
+            self._check_rows()
         self._call()
         return self.out
 

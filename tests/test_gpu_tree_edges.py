@@ -26,3 +26,24 @@ def test_short_and_cut_prefixes_in_one_call(lens):
     for i, s in enumerate(slots):
         alone, _, _ = run([s], [s.flat(0)], 2)
         assert np.array_equal(bits(alone), bits(out[3 * i:3 * i + 3]))
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_a_prepared_call_follows_the_trees_of_a_loop(paged):
+    rng = np.random.default_rng(21)
+    views = []
+    for L in (300, 40, 9000):                               # each cache holds six rows behind its prefix
+        s = Slot(rng, 8, 2, L, tree_of("random", 6, L), slack=0)
+        views.append(s.paged(0, rng) if paged else s.flat(0))
+    *views, longer = views
+    views[1].parent, views[1].row0 = 2, 6
+    q = torch.randn(8, 8, 128, device="cuda")
+    call, fn = luce.TreeAttention(q, views, 2, 0.09), luce.luce_tree_attn_paged if paged else luce.luce_tree_attn
+    for step, sizes in enumerate(([6, 2], [4, 4], [4, 4], [2, 6], [5, 3], [5, 3])):
+        if step == 4:                                       # the first slot goes on with a longer cache
+            for name in vars(longer):
+                setattr(views[0], name, getattr(longer, name))
+        for i, (v, n) in enumerate(zip(views, sizes)):
+            v.parent, v.row0 = tree_of("random", n, 10 * step + i), sum(sizes[:i])
+        got = call().clone()
+        assert np.array_equal(bits(got), bits(fn(q, views, 2, 0.09)))

@@ -178,3 +178,68 @@ def test_prepared_evictions_and_commits_follow_replaced_tensors(prepared, monkey
             setattr(c, name, t)
         call()
         assert seen[-1] == tuple(None if t is None else t.data_ptr() for t in (c.k, c.v, c.acc, c.pos)) + (c.k.shape[2],)
+
+
+@pytest.fixture
+def attention(prepared):
+    """Notes each call's views as (k, parents or None, len, row0, nodes), and the workspace's bytes."""
+    i32, i64, f32, vp, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
+    seen = []
+
+    def call(q, views, n, Hq, Hkv, D, scale, out, scores, lds, stats, ws, ws_bytes, stream):
+        seen.append([(v.k, ints(v.parent, v.n_nodes) if v.parent else None, v.len, v.row0, v.n_nodes) for v in views])
+        prepared.ws_bytes = ws_bytes.value
+        return 0
+
+    call.argtypes = [vp, None, i32, i32, i32, i32, f32, vp, vp, i64, vp, vp, sz, vp]
+    prepared.luce_tree_attn = call
+    prepared.luce_tree_attn_workspace_size = lambda T, Hq, Hkv, D, max_len: max_len * 10
+    return seen
+
+
+def test_a_prepared_tree_attention_follows_trees_rows_and_caches(attention, prepared):
+    kv = lambda cap=64: torch.zeros(2, cap, 128, dtype=torch.float16)  # noqa: E731
+    a, b = luce.TreeView(kv(), kv(), 10, [-1, 0, 0], 0), luce.TreeView(kv(), kv(), 20, 2, 3)
+    call = luce.TreeAttention(torch.zeros(5, 4, 128), [a, b], 2, 0.1)
+
+    def check():
+        call()
+        for v, got in zip((a, b), attention[-1]):
+            tree = None if isinstance(v.parent, int) else list(v.parent)
+            assert got == (v.k.data_ptr(), tree, v.len, v.row0, v.parent if tree is None else len(tree))
+
+    check()
+    a.parent = [-1, -1, 1]                       # the next step's tree
+    check()
+    a.parent[2] = 0                              # edited where it lies
+    check()
+    a.parent, b.parent, b.row0 = (-1, 0), [-1, 0, 1], 2
+    check()
+    a.parent = np.array([-1, -1])
+    check()
+    a.parent[1] = 0
+    check()
+    b.row0, a.row0 = 0, 3
+    check()
+    a.k, a.v, a.len = kv(), kv(), 30
+    check()
+    first = prepared.ws_bytes
+    b.k, b.v, b.len = kv(500), kv(500), 400      # a longer cache asks for more workspace
+    check()
+    assert prepared.ws_bytes > first and prepared.ws_bytes >= 10 * 400
+    calls = len(attention)
+    for bad in ({"parent": [-1] * 3}, {"parent": [-1]}, {"parent": 2, "row0": 4}):
+        keep = {name: getattr(a, name) for name in bad}
+        for name, x in bad.items():
+            setattr(a, name, x)
+        for _ in range(2):                       # refused until it is put right
+            with pytest.raises(ValueError, match="rows"):
+                call()
+        for name, x in keep.items():
+            setattr(a, name, x)
+    b.len = 498
+    with pytest.raises(ValueError, match="exceed"):
+        call()
+    assert len(attention) == calls
+    b.len = 497
+    check()
