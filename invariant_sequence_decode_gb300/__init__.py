@@ -904,7 +904,7 @@ class _Prepared:
         self._args = tuple(v if isinstance(v, ctypes.Array) else t(v) for t, v in zip(getattr(lib, name).argtypes, args))
         self._index, self._keep = device.index, (stream, keep)
         self._stream = None if stream is None else stream.cuda_stream
-        self._at = self._at_arg = None  # the last call's stream
+        self._at = (None, None)  # the last call's stream, also as a C value
         self._device_now, self._stream_now = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
     def _allocate(self, shape, dtype, device, stream):
@@ -917,7 +917,7 @@ class _Prepared:
                 t = torch.empty(shape, dtype=dtype, device=device)
             home = stream.cuda_stream
         self._home = home if self._home in (None, home) else -1  # (of several streams: every call lends)
-        self._owned, self._lent, self._at = self._owned + (t,), frozenset(), None
+        self._owned, self._lent, self._at = self._owned + (t,), frozenset(), (None, None)
         return t
 
     def _lend(self, stream):
@@ -929,16 +929,17 @@ class _Prepared:
 
     def _call(self):
         s = self._stream if self._stream is not None else self._stream_now(self._index)
-        if s != self._at:
+        at = self._at  # (read once: another thread's call may put its own there)
+        if s != at[0]:
             if s != self._home and self._owned and s not in self._lent:
                 self._lend(s)
-            self._at, self._at_arg = s, ctypes.c_void_p(s)
+            at = self._at = (s, ctypes.c_void_p(s))
         if self._device_now() == self._index:
-            rc = self._fn(*self._args, self._at_arg)
+            rc = self._fn(*self._args, at[1])
         else:
             import torch
             with torch.cuda.device(self._index):
-                rc = self._fn(*self._args, self._at_arg)
+                rc = self._fn(*self._args, at[1])
         if rc != LUCE_OK:
             _check(rc)
 

@@ -243,3 +243,29 @@ def test_a_prepared_tree_attention_follows_trees_rows_and_caches(attention, prep
     assert len(attention) == calls
     b.len = 497
     check()
+
+
+def test_two_threads_on_two_streams_keep_to_their_own(prepared, monkeypatch):
+    """A second call comes between a call's look at its stream and its launch, as another thread's may."""
+    i32, vp, streams, launched, between = ctypes.c_int32, ctypes.c_void_p, [11], [], [True]
+
+    def evict(slots, n, L, Hkv, D, stream):
+        launched.append(stream.value)
+        return 0
+
+    evict.argtypes = [None, i32, i32, i32, i32, vp]
+    prepared.luce_kv_evict = evict
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: streams[-1], raising=False)
+
+    def device():
+        if between.pop() if between else False:
+            streams.append(22)
+            call()
+            streams.pop()
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", device, raising=False)
+    call = luce.KvEvict([evict_slot()])
+    call()
+    assert launched == [22, 11]
+    call()
+    assert launched == [22, 11, 11]
