@@ -568,7 +568,8 @@ typedef struct luce_pagedtreeview {
  *          the GPU need scratches of their own
  * D == 128, Hq % Hkv == 0, Hq / Hkv <= 8, 1 <= n_seq <= LUCE_MAX_SEQ, rows
  * 0 .. T-1 belong to one view each, T <= LUCE_MAX_ROWS,
- * len + n_nodes <= LUCE_MAX_KEYS.
+ * len + n_nodes <= LUCE_MAX_KEYS.  out, scores, stats and ws overlap nothing
+ * that the call reads or writes (LUCE_EINVAL), but out may be q itself.
  */
 int luce_tree_attn(const float* q, const luce_treeview* views, int n_seq, int Hq, int Hkv, int D, float scale,
                    float* out, float* scores, int64_t lds, float* stats, void* ws, size_t ws_bytes, void* stream);
@@ -604,7 +605,8 @@ typedef struct luce_tree_slot {
  * luce_tree_attn's, a layer behind the other: fp32 [n_layers][T][Hq][lds] and
  * [n_layers][T][Hq][2], as luce_tree_commit takes them.  Other arguments and
  * errors as luce_decode_step; ws is sized by luce_decode_step_tree_layout with
- * max_ctx >= every len (the same fields as luce_decode_step_layout).
+ * max_ctx >= every len (the same fields as luce_decode_step_layout).  scores
+ * and stats overlap neither each other nor the caches.
  */
 int luce_decode_step_tree(const luce_model* m, const luce_tree_slot* slots, int n_seq, float* x, float* logits,
                           int32_t* argmax, float* scores, int64_t lds, float* stats, void* ws, size_t ws_bytes,

@@ -937,6 +937,15 @@ static int add_tree_slot(StepTree& tree, int32_t* rows, int s, int len, int pos0
     return LUCE_OK;
 }
 
+// The scores and statistics of a step's layers.
+static void add_step_outputs(ByteRange* r, int* nr, const luce_model* m, int T, const float* scores, int64_t lds,
+                             const float* stats)
+{
+    const uintptr_t rows = (uintptr_t)m->n_layers * T * m->n_q_heads;
+    if (scores) r[(*nr)++] = ByteRange{(uintptr_t)scores, (uintptr_t)scores + rows * lds * 4, -1, "scores", true, 0};
+    if (stats) r[(*nr)++] = ByteRange{(uintptr_t)stats, (uintptr_t)stats + rows * 8, -1, "stats", true, 0};
+}
+
 static int run_tree_step(const luce_model* m, const StepSlot* ss, StepTree& tree, const int32_t* rows, int n_seq, float* x,
                          float* logits, int32_t* argmax, float* scores, int64_t lds, float* stats, void* ws,
                          size_t ws_bytes, void* stream, const char* who)
@@ -981,9 +990,7 @@ int luce_decode_step_tree(const luce_model* m, const luce_tree_slot* slots, int 
         r[2 * s + 1] = ByteRange{(uintptr_t)sl.v, (uintptr_t)sl.v + bytes, s, "V cache", true, 0};
     }
     int nr = 2 * n_seq;
-    const uintptr_t out_rows = (uintptr_t)m->n_layers * T * m->n_q_heads;
-    if (scores) r[nr++] = ByteRange{(uintptr_t)scores, (uintptr_t)scores + out_rows * lds * 4, -1, "scores", true, 0};
-    if (stats) r[nr++] = ByteRange{(uintptr_t)stats, (uintptr_t)stats + out_rows * 8, -1, "stats", true, 0};
+    add_step_outputs(r, &nr, m, T, scores, lds, stats);
     if ((rc = check_apart(r, nr, who))) return rc;
     return run_tree_step(m, ss, tree, rows, n_seq, x, logits, argmax, scores, lds, stats, ws, ws_bytes, stream, who);
 }
@@ -1348,6 +1355,16 @@ int luce_decode_step_tree_paged(const luce_model* m, const luce_paged_tree_slot*
         v.pages = sl.table;
     }
     if ((rc = paged_slots(ps, rows, n_seq, ss, who))) return rc;
+    // scores and stats overlap no pool (slots may share pools, so those are not told apart here)
+    ByteRange r[2 * LUCE_MAX_SEQ + 2];
+    int nr = 0;
+    for (int s = 0; s < n_seq; ++s) {
+        const uintptr_t bytes = (uintptr_t)(tree.batch.view[s].page_stride * slots[s].n_pages * 2);
+        r[nr++] = ByteRange{(uintptr_t)slots[s].k_pool, (uintptr_t)slots[s].k_pool + bytes, s, "K pool", false, 0};
+        r[nr++] = ByteRange{(uintptr_t)slots[s].v_pool, (uintptr_t)slots[s].v_pool + bytes, s, "V pool", false, 0};
+    }
+    add_step_outputs(r, &nr, m, T, scores, lds, stats);
+    if ((rc = check_apart(r, nr, who))) return rc;
     return run_tree_step(m, ss, tree, rows, n_seq, x, logits, argmax, scores, lds, stats, ws, ws_bytes, stream, who);
 }
 

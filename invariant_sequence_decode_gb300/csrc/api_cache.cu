@@ -1,6 +1,7 @@
 // api_cache.cu - the C ABI over a slot's cache: tree attention, the commit of
 // an accepted path, eviction (see include/luce.h for the contract).
 #include <math.h>
+#include <stdio.h>
 
 #include <algorithm>
 
@@ -13,6 +14,29 @@
 using namespace luce;
 
 static_assert(LUCE_MAX_TREE == kMaxTree && LUCE_MAX_ROWS == kMaxTree && LUCE_MAX_SEQ == 4, "sizes of the batches");
+
+// ------------------------------------------------------------ ranges
+
+int luce::check_apart(const ByteRange* r, int n, const char* who)
+{
+    for (int a = 0; a < n; ++a)
+        for (int c = 0; c < a; ++c) {
+            const bool apart = r[a].hi <= r[c].lo || r[c].hi <= r[a].lo;
+            const bool both_read = !r[a].written && !r[c].written;
+            const bool in_place = r[a].slot == r[c].slot && r[a].pair && r[a].pair == r[c].pair && r[a].lo == r[c].lo;
+            if (apart || both_read || in_place) continue;
+            char at[2][24] = {"", ""};  // (-1: no slot's own)
+            if (r[a].slot >= 0) snprintf(at[0], sizeof at[0], " of slot %d", r[a].slot);
+            if (r[c].slot >= 0) snprintf(at[1], sizeof at[1], " of slot %d", r[c].slot);
+            return fail(LUCE_EINVAL, "%s: the %s%s overlaps the %s%s", who, r[a].what, at[0], r[c].what, at[1]);
+        }
+    return LUCE_OK;
+}
+
+static ByteRange range_of(const void* p, int64_t bytes, int slot, const char* what, bool written, int pair = 0)
+{
+    return ByteRange{(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes, slot, what, written, pair};
+}
 
 // ------------------------------------------------------------ trees
 
@@ -104,12 +128,35 @@ static int add_tree_view(TreeBatch& b, int s, int len, int n_nodes, int row0, co
     return LUCE_OK;
 }
 
+// What a view's rows read.  (Tiles reach further, but use nothing of it.)
+static void add_view_ranges(ByteRange* r, int* nr, const TreeView& v, int s, int Hkv)
+{
+    const int64_t keys = v.len + v.n_nodes;
+    const int64_t elems = v.pages ? v.page_stride * v.n_pages
+                                  : v.head_stride * (Hkv - 1) + v.tok_stride * (keys - 1) + LUCE_HEAD_DIM;
+    r[(*nr)++] = range_of(v.k, elems * 2, s, "K", false);
+    r[(*nr)++] = range_of(v.v, elems * 2, s, "V", false);
+    if (v.pages) r[(*nr)++] = range_of(v.pages, (keys + LUCE_PAGE_KEYS - 1) / LUCE_PAGE_KEYS * 4, s, "table", false);
+}
+
 static int run_tree(TreeBatch& b, const bool* covered, const float* q, int Hq, int Hkv, float scale, float* out,
                     float* scores, int64_t lds, float* stats, void* ws, size_t ws_bytes, void* stream, const char* who)
 {
     for (int r = 0; r < b.n_row; ++r) REQUIRE(covered[r], LUCE_EINVAL, "%s: row %d belongs to no view", who, r);
     const size_t need = std::max<size_t>(256, tree_part_bytes(tree_chunks(b, Hq, Hkv)));
     REQUIRE(ws_bytes >= need, LUCE_ENOSPACE, "%s: workspace %zu bytes < %zu needed", who, ws_bytes, need);
+    ByteRange r[3 * LUCE_MAX_SEQ + 5];
+    int nr = 0;
+    const int64_t heads = (int64_t)b.n_row * Hq;
+    for (int s = 0; s < b.n_view; ++s) add_view_ranges(r, &nr, b.view[s], s, Hkv);
+    // (a row's q is read before its out is written)
+    r[nr++] = range_of(q, heads * LUCE_HEAD_DIM * 4, -1, "q", false, 1);
+    r[nr++] = range_of(out, heads * LUCE_HEAD_DIM * 4, -1, "out", true, 1);
+    if (scores) r[nr++] = range_of(scores, heads * lds * 4, -1, "scores", true);
+    if (stats) r[nr++] = range_of(stats, heads * 8, -1, "stats", true);
+    r[nr++] = range_of(ws, need, -1, "workspace", true);
+    const int rc = check_apart(r, nr, who);
+    if (rc) return rc;
     return cuda_status(launch_tree_attention(q, b, Hq, Hkv, scale, ws, out, scores, lds, stats, nullptr, nullptr,
                                              (cudaStream_t)stream),
                        who);
@@ -178,25 +225,7 @@ int luce_tree_attn_paged(const float* q, const luce_pagedtreeview* views, int n_
     return run_tree(b, covered, q, Hq, Hkv, scale, out, scores, lds, stats, ws, ws_bytes, stream, who);
 }
 
-// ------------------------------------------------------------ ranges
-
-int luce::check_apart(const ByteRange* r, int n, const char* who)
-{
-    for (int a = 0; a < n; ++a)
-        for (int c = 0; c < a; ++c) {
-            const bool apart = r[a].hi <= r[c].lo || r[c].hi <= r[a].lo;
-            const bool both_read = !r[a].written && !r[c].written;
-            const bool in_place = r[a].slot == r[c].slot && r[a].pair && r[a].pair == r[c].pair && r[a].lo == r[c].lo;
-            REQUIRE(apart || both_read || in_place, LUCE_EINVAL, "%s: the %s of slot %d overlaps the %s of slot %d", who,
-                    r[a].what, r[a].slot, r[c].what, r[c].slot);
-        }
-    return LUCE_OK;
-}
-
-static ByteRange range_of(const void* p, int64_t bytes, int slot, const char* what, bool written, int pair = 0)
-{
-    return ByteRange{(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes, slot, what, written, pair};
-}
+// ------------------------------------------------------------ pools
 
 static const char* const kPoolK = "K pool";
 static const char* const kPoolV = "V pool";
