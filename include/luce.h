@@ -80,7 +80,8 @@ uint64_t luce_launch_count(void);
  * after about one second and adds one to this device counter, so a stalled
  * copy engine or tensor core surfaces here instead of as a hung stream.  A
  * healthy run reads 0 (an attention CTA whose wait expired writes none of its
- * partial outputs).
+ * partial outputs; what the merge behind it makes of their place is as
+ * untrusted as the rest).
  *
  * A non-zero count means the device context is suspect, not that some
  * outputs were merely skipped: the CTA whose wait expired stops writing;
@@ -106,6 +107,7 @@ int luce_wait_timeouts(uint32_t* count, int reset);
  * LUCE_ECUDA.
  */
 int luce_test_wait_expiry(int64_t limit_ns, void* stream);
+int luce_test_tree_wait_expiry(int64_t limit_ns, void* stream); /* the same, counted by the attention of draft trees */
 
 /*
  * Activation quantization to q8_0 blocks [qfuse, item 2: the consumer's

@@ -138,6 +138,9 @@ cudaError_t launch_tree_attention(const float* q, const TreeBatch& b, int Hq, in
                                   float* out, float* scores, int64_t lds, float* stats, int8_t* out_q, float* out_d,
                                   cudaStream_t s);
 
+// One wait of limit_ns on a barrier that nothing completes, counted as the tree attention's.
+cudaError_t launch_tree_wait_expiry(uint64_t limit_ns, cudaStream_t s);
+
 // Bounded waits of the tree attention that expired on the current device.
 cudaError_t read_tree_wait_timeouts(uint32_t* count, bool reset);
 

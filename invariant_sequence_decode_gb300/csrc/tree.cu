@@ -516,11 +516,12 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
         float unit = 0.0f;                      // the row's power of two: q is held in units of it
         bool ok = true, left = false;
         // the tile whose O is still to come: its correction of the sum before
-        // it (none: the chunk's first), whether the warp has rows in it, where
-        // the sums go after it
-        float prev_alpha = 0.0f;
+        // it (none: the chunk's first), whether the warp has rows in it, the
+        // row of results that the sums go to after it (-1: it is not the
+        // chunk's last) with their maximum and weights' sum
+        float prev_alpha = 0.0f, prev_m = 0.0f, prev_l = 0.0f;
         bool prev_first = true, prev_live = false;
-        float* prev_out = nullptr;
+        int64_t prev_row = -1;
         auto take = [&](int j) {
             const bool done = __all_sync(0xffffffffu, mbar_wait(&bar.o_full, j & 1, late));
             tm_after();
@@ -538,12 +539,15 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
             } else {
                 warp_arrive(&bar.o_free);
             }
-            if (prev_out && done) {
+            if (prev_row >= 0 && done) {
+                float* to = part_o + prev_row * kHeadDim + 64 * half;
+                if (half == 0) part_ml[4 * prev_row] = prev_m;
+                part_ml[4 * prev_row + 1 + half] = prev_l;
 #pragma unroll
                 for (int e = 0; e < 32; e += 4) {
                     const float2 a = unpair(o[e]), c = unpair(o[e + 1]), d = unpair(o[e + 2]), f = unpair(o[e + 3]);
                     const float x[8] = {a.x, a.y, c.x, c.y, d.x, d.y, f.x, f.y};
-                    st_v8(prev_out + 2 * e, x);
+                    st_v8(to + 2 * e, x);
                 }
             }
             return done;
@@ -716,13 +720,13 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
                 prev_alpha = alpha;
                 prev_first = kc == 0;
                 prev_live = live;
-                prev_out = nullptr;
+                prev_row = -1;
                 if (++kc == ct || k + 1 == t.tiles) {  // the chunk's last tile
                     kc = 0;
                     if (row < R) {
-                        prev_out = part_o + pr * kHeadDim + 64 * half;
-                        if (half == 0) part_ml[4 * pr] = m;
-                        part_ml[4 * pr + 1 + half] = l;
+                        prev_row = pr;
+                        prev_m = m;
+                        prev_l = l;
                     }
                     pr += (int64_t)Hkv * R;
                 }
@@ -733,6 +737,22 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
     tm_before();
     __syncthreads();
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+}
+
+__global__ void tree_wait_expiry_kernel(uint64_t limit_ns)
+{
+    __shared__ uint64_t bar;
+    if (threadIdx.x != 0) return;
+    mbar_init(&bar, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    mbar_wait(&bar, 0, &g_tree_wait_timeouts, limit_ns);
+}
+
+cudaError_t launch_tree_wait_expiry(uint64_t limit_ns, cudaStream_t s)
+{
+    tree_wait_expiry_kernel<<<1, 32, 0, s>>>(limit_ns);
+    count_launches(1);
+    return cudaGetLastError();
 }
 
 cudaError_t read_tree_wait_timeouts(uint32_t* count, bool reset)

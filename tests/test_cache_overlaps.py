@@ -67,3 +67,8 @@ def test_arrays_that_touch_are_not_refused(lib):
     arr = (luce.PagedTreeSlotC * 1)(ptslot())
     end = P + 2 * 2 * 128 * 128 * 2 * 4
     assert lib.luce_decode_step_tree_paged(ctypes.byref(model()), arr, 1, Q, None, None, end, 12, ST, WS, 1024, None) == S
+
+
+def test_the_trees_expiry_hook_takes_a_limit(lib):
+    for bad in (0, 999, 1_000_000_001, -5):
+        assert lib.luce_test_tree_wait_expiry(bad, None) == E and b"limit_ns" in lib.luce_last_error()

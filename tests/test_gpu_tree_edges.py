@@ -47,3 +47,18 @@ def test_a_prepared_call_follows_the_trees_of_a_loop(paged):
             v.parent, v.row0 = tree_of("random", n, 10 * step + i), sum(sizes[:i])
         got = call().clone()
         assert np.array_equal(bits(got), bits(fn(q, views, 2, 0.09)))
+
+
+def test_an_expired_wait_is_counted_and_leaves_the_context_usable():
+    lib = luce.load_library()
+    stream = torch.cuda.current_stream().cuda_stream
+    luce.wait_timeouts(reset=True)
+    assert lib.luce_test_tree_wait_expiry(5_000_000, stream) == 0
+    torch.cuda.synchronize()
+    assert luce.wait_timeouts() == 1                        # (read, not reset)
+    assert lib.luce_test_tree_wait_expiry(1_000_000, stream) == lib.luce_test_wait_expiry(1_000_000, stream) == 0
+    torch.cuda.synchronize()
+    assert luce.wait_timeouts(reset=True) == 3              # the rings' and the trees' together
+    assert luce.wait_timeouts() == 0
+    s = Slot(np.random.default_rng(2), 8, 2, 700, tree_of("random", 5, 2))
+    check([s], *run([s], [s.flat(0)], 2, scores=True), 2)

@@ -35,3 +35,12 @@ def test_nothing_is_read_ahead_of_the_wait(name):
     body = kernel(name)
     ahead = body[:body.index("pdl_wait()")]
     assert not re.search(r"ld_\w+\(|tree_key\(|__ldg|__ldcg|\b(q|part_o|part_ml|qp|mlp|po)\[|\*\s*(q|qp|mlp|po)\s*;", ahead)
+
+
+def test_a_chunk_writes_none_of_its_results_before_its_last_product_is_awaited():
+    """Maximum and sum go out with O: after an expired wait none of the three does."""
+    body = kernel("tree_chunk_kernel")
+    take = body[body.index("auto take = "):]
+    take = take[:take.index("return done;")]
+    assert body.count("part_ml[") == take.count("part_ml[") == 2 and "prev_row >= 0 && done" in take
+    assert take.index("part_ml[") > take.index("mbar_wait(&bar.o_full")
