@@ -945,6 +945,9 @@ class _Prepared:
             _check(rc)
 
 
+_NOTHING = (None,) * 8  # what no view holds
+
+
 class TreeAttention(_Prepared):
     """luce_tree_attn (or luce_tree_attn_paged, for PagedTreeViews) with its
     arguments marshalled once, for repeated calls over the same buffers: q fp32
@@ -984,8 +987,7 @@ class TreeAttention(_Prepared):
         n = len(self.views)
         self._paged, self._q, self._shape = paged, q, (T, Hq, int(n_kv_heads), D)
         self._vc = ((PagedTreeViewC if paged else TreeViewC) * n)()
-        self._items, self._lens = [self._vc[i] for i in range(n)], [v.len for v in self.views]
-        self._caps, self._seen = [0] * n, [None] * n
+        self._items, self._caps, self._seen = [self._vc[i] for i in range(n)], [0] * n, [None] * n
         for i, v in enumerate(self.views):
             self._take(i, v)
         self._check_rows()
@@ -1000,10 +1002,10 @@ class TreeAttention(_Prepared):
         self._bind("luce_tree_attn_paged" if paged else "luce_tree_attn", args, q.device, stream, (q, scores, stats, ws))
 
     def _take(self, i, v):
-        """View i's tensors, tree and rows."""
+        """View i's tensors, then its tree."""
         import torch
         c, Hkv = self._items[i], self._shape[2]
-        nn, par = _tree(v.parent)
+        self._seen[i] = (i, v, *_NOTHING)  # (until all is checked)
         if self._paged:
             _kv_pair(v.k_pool, v.v_pool, 4, f"views[{i}]")
             _need(v.k_pool, torch.float16, f"views[{i}].k_pool")
@@ -1012,24 +1014,32 @@ class TreeAttention(_Prepared):
             if v.k_pool.shape[1:] != (Hkv, PAGE_KEYS, HEAD_DIM):
                 raise ValueError(f"views[{i}]: expected pools [n_pages][{Hkv}][128][128]")
             _same_device(self._q, v.k_pool, v.v_pool, v.table)
-            cap, tensors = v.table.numel() * PAGE_KEYS, (v.k_pool, v.v_pool, v.table)
-            c.k_pool, c.v_pool, c.table, c.n_pages = *(t.data_ptr() for t in tensors), v.k_pool.shape[0]
+            self._caps[i] = min(v.table.numel() * PAGE_KEYS, MAX_KEYS)
+            c.k_pool, c.v_pool, c.table, c.n_pages = v.k_pool.data_ptr(), v.v_pool.data_ptr(), v.table.data_ptr(), v.k_pool.shape[0]
+            self._take_tree(i, v, (v.k_pool, v.v_pool, v.table))
         else:
             _kv_pair(v.k, v.v, 3, f"views[{i}]")
             if v.k.shape[0] != Hkv:
                 raise ValueError(f"views[{i}]: {v.k.shape[0]} heads, expected {Hkv}")
             _same_device(self._q, v.k, v.v)
-            cap, tensors = v.k.shape[1], (v.k, v.v, None)
-            c.k, c.v, c.cap = v.k.data_ptr(), v.v.data_ptr(), cap
+            self._caps[i] = min(v.k.shape[1], MAX_KEYS)
+            c.k, c.v, c.cap = v.k.data_ptr(), v.v.data_ptr(), v.k.shape[1]
             c.head_stride, c.tok_stride = v.k.stride(0), v.k.stride(1)
-        self._caps[i] = min(cap, MAX_KEYS) - nn
-        self._fits(v.len, self._caps[i])
-        c.len, c.n_nodes, c.row0, c.parent = v.len, nn, v.row0, par
-        self._lens[i] = v.len
+            self._take_tree(i, v, (v.k, v.v, None))
+
+    def _take_tree(self, i, v, tensors):
+        """View i's tree, rows and length."""
+        c, seen = self._items[i], self._seen[i]
         # the tree as given, to tell whether it changed (one that has no == of its own is taken at every call)
-        kind = type(v.parent) if type(v.parent) in (int, list, tuple) else None
-        self._seen[i] = (*tensors, v.row0, kind, list(v.parent) if kind is list else v.parent, par)
-        self._rows = None
+        kind = v.parent.__class__ if v.parent.__class__ in (int, list, tuple) else None
+        same = kind is not None and kind is seen[7] and v.parent == seen[8]
+        nn, par, parent = (c.n_nodes, seen[9], seen[8]) if same else (*_tree(v.parent), list(v.parent) if kind is list else v.parent)
+        if v.len + nn > self._caps[i]:
+            raise ValueError(f"len {v.len} and the tree exceed the cache")
+        if not same or v.row0 != seen[5]:
+            self._rows = None
+        c.len, c.n_nodes, c.row0, c.parent = v.len, nn, v.row0, par
+        self._seen[i] = (i, v, *tensors, v.row0, v.len, kind, parent, par)
 
     def _check_rows(self):
         rows, T = max(c.row0 + c.n_nodes for c in self._items), self._shape[0]
@@ -1038,32 +1048,31 @@ class TreeAttention(_Prepared):
         self._rows = rows
 
     def _ws_bytes(self):
-        return max(256, luce_tree_attn_workspace_size(*self._shape, max(0, *self._caps)))
+        return max(256, luce_tree_attn_workspace_size(*self._shape, max(0, *(cap - c.n_nodes for cap, c in zip(self._caps, self._items)))))
 
     def _retake(self, i, v):
         """View i changed: more room is asked for where its cache grew."""
         import torch
+        seen, at = self._seen[i], self._ws_args
+        if (v.k_pool is seen[2] and v.v_pool is seen[3] and v.table is seen[4]) if self._paged else (v.k is seen[2] and v.v is seen[3]):
+            self._take_tree(i, v, seen[2:5])
+            return
         self._take(i, v)
-        at = self._ws_args
         if self._own_ws and self._ws_bytes() > self._args[at + 1].value:
             ws = self._allocate((self._ws_bytes(),), torch.uint8, self._q.device, self._keep[0])
             self._args = (*self._args[:at], ctypes.c_void_p(ws.data_ptr()), ctypes.c_size_t(ws.numel()))
 
-    @staticmethod
-    def _fits(length, cap):
-        if length > cap:
-            raise ValueError(f"len {length} and the tree exceed the cache")
-
     def __call__(self):
-        paged = self._paged
-        for i, v in enumerate(self.views):
-            k, vv, table, row0, kind, parent, _ = self._seen[i]
-            if not ((v.k_pool is k and v.v_pool is vv and v.table is table) if paged else (v.k is k and v.v is vv)) or \
-                    v.row0 != row0 or type(v.parent) is not kind or v.parent != parent:
-                self._retake(i, v)
-            if v.len != self._lens[i]:
-                self._fits(v.len, self._caps[i])
-                self._items[i].len = self._lens[i] = v.len
+        if self._paged:
+            for i, v, k, vv, table, row0, length, kind, parent, _ in self._seen:
+                if v.k_pool is not k or v.v_pool is not vv or v.table is not table or v.row0 != row0 or v.len != length or \
+                        v.parent.__class__ is not kind or v.parent != parent:
+                    self._retake(i, v)
+        else:
+            for i, v, k, vv, _, row0, length, kind, parent, _ in self._seen:
+                if v.k is not k or v.v is not vv or v.row0 != row0 or v.len != length or \
+                        v.parent.__class__ is not kind or v.parent != parent:
+                    self._retake(i, v)
         if self._rows is None:
             self._check_rows()
         self._call()
@@ -1195,7 +1204,7 @@ class TreeCommit(_Prepared):
         self._first, self._heads = first, (L, Hkv)
         _same_device(first, scores, stats)
         self._sc = ((PagedCommitSlotC if paged else CommitSlotC) * n)()
-        self._items, self._tensors = [self._sc[i] for i in range(n)], [None] * n
+        self._items, self._seen = [self._sc[i] for i in range(n)], [None] * n
         self._now, self._arrays, self._tables = [None] * n, [None] * n, [None] * n
         for i, s in enumerate(self.slots):
             self._take(i, s)
@@ -1222,7 +1231,14 @@ class TreeCommit(_Prepared):
         else:
             c.k, c.v = k.data_ptr(), v.data_ptr()
         c.cap, c.acc, c.pos = cap, _ptr(s.acc), _ptr(s.pos)
-        self._tensors[i] = (k, v, s.acc, s.pos)
+        self._seen[i] = (i, s, k, v, s.acc, s.pos)
+
+    def _take_path(self, i, s):
+        path, c = list(s.path), self._items[i]
+        self._arrays[i] = (ctypes.c_int32 * max(1, len(path)))(*path)
+        c.len, c.row0, c.path, c.n_path = s.len, s.row0, self._arrays[i], len(path)
+        c.pos0 = s.len if s.pos0 is None else s.pos0
+        self._now[i] = (s.len, s.row0, s.pos0, *path)
 
     def _take_table(self, i, s):
         import numpy as np
@@ -1232,21 +1248,20 @@ class TreeCommit(_Prepared):
         self._items[i].n_table = t.size
 
     def __call__(self):
-        paged = self._paged
-        for i, s in enumerate(self.slots):
-            t = self._tensors[i]
-            if not ((s.k_pool is t[0] and s.v_pool is t[1]) if paged else (s.k is t[0] and s.v is t[1])) or \
-                    s.acc is not t[2] or s.pos is not t[3]:
-                self._take(i, s)
-            if paged and s.table is not self._tables[i]:
-                self._take_table(i, s)
-            now = (s.len, s.row0, s.pos0, *s.path)
-            if now != self._now[i]:
-                path, c = now[3:], self._items[i]
-                self._arrays[i] = (ctypes.c_int32 * max(1, len(path)))(*path)
-                c.len, c.row0, c.path, c.n_path = s.len, s.row0, self._arrays[i], len(path)
-                c.pos0 = s.len if s.pos0 is None else s.pos0
-                self._now[i] = now
+        if self._paged:
+            for i, s, k, v, acc, pos in self._seen:
+                if s.k_pool is not k or s.v_pool is not v or s.acc is not acc or s.pos is not pos:
+                    self._take(i, s)
+                if s.table is not self._tables[i]:
+                    self._take_table(i, s)
+                if (s.len, s.row0, s.pos0, *s.path) != self._now[i]:
+                    self._take_path(i, s)
+        else:
+            for i, s, k, v, acc, pos in self._seen:
+                if s.k is not k or s.v is not v or s.acc is not acc or s.pos is not pos:
+                    self._take(i, s)
+                if (s.len, s.row0, s.pos0, *s.path) != self._now[i]:
+                    self._take_path(i, s)
         self._call()
 
 
@@ -1270,7 +1285,7 @@ class KvEvict(_Prepared):
         n = len(self.slots)
         self._first, self._heads = first, (L, Hkv)
         self._sc = ((PagedEvictSlotC if paged else EvictSlotC) * n)()
-        self._items, self._now, self._tensors, self._pages = [self._sc[i] for i in range(n)], [None] * n, [None] * n, [0] * n
+        self._items, self._seen, self._pages = [self._sc[i] for i in range(n)], [None] * n, [0] * n
         for i, s in enumerate(self.slots):
             self._take(i, s)
         args = (self._sc, n, L, Hkv, HEAD_DIM)
@@ -1302,26 +1317,26 @@ class KvEvict(_Prepared):
             c.k, c.v = k.data_ptr(), v.data_ptr()
         c.acc, c.pos, c.acc_out, c.pos_out = s.acc.data_ptr(), s.pos.data_ptr(), acc_out.data_ptr(), pos_out.data_ptr()
         c.cap = cap
-        self._tensors[i] = (k, v, s.acc, s.pos, s.acc_out, s.pos_out, table)
-        self._now[i] = None
+        self._seen[i] = (i, s, k, v, table, s.acc, s.pos, s.acc_out, s.pos_out, None)
+
+    def _take_sizes(self, i, s):
+        if self._paged and s.len > self._pages[i]:
+            raise ValueError(f"slots[{i}].table does not hold {s.len} keys")
+        if s.next_pos is None and s.recent:
+            raise ValueError(f"slots[{i}]: recent={s.recent} needs next_pos, the position of the next token")
+        c = self._items[i]
+        c.len, c.budget, c.sinks, c.recent = s.len, s.budget, s.sinks, s.recent
+        c.next_pos = LAST_POS if s.next_pos is None else s.next_pos
+        self._seen[i] = (*self._seen[i][:-1], (s.len, s.next_pos, s.budget, s.sinks, s.recent))
 
     def __call__(self):
         paged = self._paged
-        for i, s in enumerate(self.slots):
-            t = self._tensors[i]
-            if not ((s.k_pool is t[0] and s.v_pool is t[1] and s.table is t[6]) if paged else (s.k is t[0] and s.v is t[1])) or \
-                    not (s.acc is t[2] and s.pos is t[3] and s.acc_out is t[4] and s.pos_out is t[5]):
-                self._take(i, s)
-            now = (s.len, s.next_pos, s.budget, s.sinks, s.recent)
-            if now != self._now[i]:
-                if paged and s.len > self._pages[i]:
-                    raise ValueError(f"slots[{i}].table does not hold {s.len} keys")
-                if s.next_pos is None and s.recent:
-                    raise ValueError(f"slots[{i}]: recent={s.recent} needs next_pos, the position of the next token")
-                c = self._items[i]
-                c.len, c.budget, c.sinks, c.recent = s.len, s.budget, s.sinks, s.recent
-                c.next_pos = LAST_POS if s.next_pos is None else s.next_pos
-                self._now[i] = now
+        for i, s, k, v, table, acc, pos, acc_out, pos_out, now in self._seen:
+            if (s.k_pool is not k or s.v_pool is not v or s.table is not table if paged else s.k is not k or s.v is not v) or \
+                    s.acc is not acc or s.pos is not pos or s.acc_out is not acc_out or s.pos_out is not pos_out:
+                now = self._take(i, s)
+            if (s.len, s.next_pos, s.budget, s.sinks, s.recent) != now:
+                self._take_sizes(i, s)
         self._call()
 
 
