@@ -535,10 +535,12 @@ typedef struct luce_treeview {
  * The same over pages (luce_pagedview's pools and table, which holds
  * ceil((len + n_nodes) / LUCE_PAGE_KEYS) entries).  n_pages bounds the table's
  * entries: a page outside [0, n_pages) is never read, its keys and values
- * count as zero.
+ * count as zero.  Of a pool of several layers ([n_pages][n_layers][Hkv][128][128],
+ * as the step, the commit and eviction take it) layer l is k_pool at
+ * l * Hkv * 128 * 128 with a page_stride of n_layers * Hkv * 128 * 128.
  */
 typedef struct luce_pagedtreeview {
-    const uint16_t* k_pool; /* (device) [n_pages][Hkv][128][128], 16-byte aligned */
+    const uint16_t* k_pool; /* (device) [n_pages] x [Hkv][128][128], 16-byte aligned */
     const uint16_t* v_pool; /* (device) same layout */
     const int32_t* table;   /* (device) page of each 128-key span */
     int32_t n_pages;
@@ -546,6 +548,7 @@ typedef struct luce_pagedtreeview {
     int32_t n_nodes;        /* 1..LUCE_MAX_TREE */
     int32_t row0;
     const int32_t* parent;  /* (host) [n_nodes] or NULL */
+    int64_t page_stride;    /* elements from page to page, a multiple of 8, >= Hkv * 128 * 128; 0: that */
 } luce_pagedtreeview;
 
 /*

@@ -79,7 +79,7 @@ class TreeViewC(ctypes.Structure):
 class PagedTreeViewC(ctypes.Structure):
     _fields_ = [("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p), ("table", ctypes.c_void_p),
                 ("n_pages", ctypes.c_int32), ("len", ctypes.c_int32), ("n_nodes", ctypes.c_int32),
-                ("row0", ctypes.c_int32), ("parent", ctypes.POINTER(ctypes.c_int32))]
+                ("row0", ctypes.c_int32), ("parent", ctypes.POINTER(ctypes.c_int32)), ("page_stride", ctypes.c_int64)]
 
 
 class TreeSlotC(ctypes.Structure):
@@ -756,8 +756,9 @@ class TreeView:
 
 @dataclass
 class PagedTreeView:
-    """The same over pools fp16 [n_pages][Hkv][128][128] and a device int32
-    ``table`` of the pool page of each 128-key span."""
+    """The same over pools fp16 [n_pages][Hkv][128][128] (or a layer pool[:, l] of
+    pools [n_pages][n_layers][Hkv][128][128]) and a device int32 ``table`` of
+    the pool page of each 128-key span."""
     k_pool: object
     v_pool: object
     table: object
@@ -1008,11 +1009,11 @@ class TreeAttention(_Prepared):
         self._seen[i] = (i, v, *_NOTHING)  # (until all is checked)
         if self._paged:
             _kv_pair(v.k_pool, v.v_pool, 4, f"views[{i}]")
-            _need(v.k_pool, torch.float16, f"views[{i}].k_pool")
-            _need(v.v_pool, torch.float16, f"views[{i}].v_pool")
             _need(v.table, torch.int32, f"views[{i}].table")
-            if v.k_pool.shape[1:] != (Hkv, PAGE_KEYS, HEAD_DIM):
-                raise ValueError(f"views[{i}]: expected pools [n_pages][{Hkv}][128][128]")
+            page, stride = (Hkv, PAGE_KEYS, HEAD_DIM), v.k_pool.stride()
+            if v.k_pool.shape[1:] != page or stride[2] != HEAD_DIM or (Hkv > 1 and stride[1] != PAGE_KEYS * HEAD_DIM):
+                raise ValueError(f"views[{i}]: expected pools [n_pages][{Hkv}][128][128], each page contiguous")
+            c.page_stride = stride[0] if v.k_pool.shape[0] > 1 else 0
             _same_device(self._q, v.k_pool, v.v_pool, v.table)
             self._caps[i] = min(v.table.numel() * PAGE_KEYS, MAX_KEYS)
             c.k_pool, c.v_pool, c.table, c.n_pages = v.k_pool.data_ptr(), v.v_pool.data_ptr(), v.table.data_ptr(), v.k_pool.shape[0]

@@ -92,7 +92,7 @@ extern "C" {
 
 const char* luce_last_error(void) { return g_err.c_str(); }
 
-int luce_version(void) { return 10100; }
+int luce_version(void) { return 10200; }
 
 uint64_t luce_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }
 

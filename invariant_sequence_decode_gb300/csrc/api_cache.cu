@@ -132,7 +132,7 @@ static int add_tree_view(TreeBatch& b, int s, int len, int n_nodes, int row0, co
 static void add_view_ranges(ByteRange* r, int* nr, const TreeView& v, int s, int Hkv)
 {
     const int64_t keys = v.len + v.n_nodes;
-    const int64_t elems = v.pages ? v.page_stride * v.n_pages
+    const int64_t elems = v.pages ? v.page_stride * (v.n_pages - 1) + v.head_stride * Hkv
                                   : v.head_stride * (Hkv - 1) + v.tok_stride * (keys - 1) + LUCE_HEAD_DIM;
     r[(*nr)++] = range_of(v.k, elems * 2, s, "K", false);
     r[(*nr)++] = range_of(v.v, elems * 2, s, "V", false);
@@ -220,7 +220,10 @@ int luce_tree_attn_paged(const float* q, const luce_pagedtreeview* views, int n_
         t.cap = LUCE_PAGE_KEYS;
         t.tok_stride = D;
         t.head_stride = (int64_t)LUCE_PAGE_KEYS * D;
-        t.page_stride = t.head_stride * Hkv;
+        const int64_t page = t.head_stride * Hkv;
+        REQUIRE(v.page_stride == 0 || (v.page_stride >= page && v.page_stride % 8 == 0 && v.page_stride < ((int64_t)1 << 38)),
+                LUCE_EINVAL, "%s: view %d page_stride must be a multiple of 8 and keep the pages apart", who, s);
+        t.page_stride = v.page_stride ? v.page_stride : page;
     }
     return run_tree(b, covered, q, Hq, Hkv, scale, out, scores, lds, stats, ws, ws_bytes, stream, who);
 }

@@ -72,3 +72,20 @@ def test_arrays_that_touch_are_not_refused(lib):
 def test_the_trees_expiry_hook_takes_a_limit(lib):
     for bad in (0, 999, 1_000_000_001, -5):
         assert lib.luce_test_tree_wait_expiry(bad, None) == E and b"limit_ns" in lib.luce_last_error()
+
+
+@pytest.mark.parametrize("stride", [2 * 128 * 128 - 8, 2 * 128 * 128 + 4, -(1 << 20), 1 << 38, 8])
+def test_paged_tree_attention_refuses_pages_that_are_not_apart(lib, stride):
+    arr = (luce.PagedTreeViewC * 1)(luce.PagedTreeViewC(P, P + BIG, P + 9 * BIG, 4, 10, 2, 0, None, stride))
+    assert lib.luce_tree_attn_paged(Q, arr, 1, 8, 2, 128, 0.1, OUT, None, 0, None, WS, 1 << 20, None) == E
+    assert b"page_stride" in lib.luce_last_error()
+
+
+def test_a_layer_reaches_to_its_own_end_of_the_pool(lib):
+    """Layer 1 of 2: what lies behind the last page's layer 1 is not the view's."""
+    page = 2 * 128 * 128
+    end = P + 2 * (7 * page + page)                      # 4 pages x 2 layers
+    arr = (luce.PagedTreeViewC * 1)(luce.PagedTreeViewC(P + 2 * page, P + BIG, P + 9 * BIG, 4, 10, 2, 0, None, 2 * page))
+    call = lambda out: lib.luce_tree_attn_paged(Q, arr, 1, 8, 2, 128, 0.1, out, SC, 12, SC, WS, 1 << 20, None)  # noqa: E731
+    assert call(end - 16) == E and b"overlaps the K" in lib.luce_last_error()
+    assert call(end) == E and b"stats overlaps the scores" in lib.luce_last_error()

@@ -62,3 +62,28 @@ def test_an_expired_wait_is_counted_and_leaves_the_context_usable():
     assert luce.wait_timeouts() == 0
     s = Slot(np.random.default_rng(2), 8, 2, 700, tree_of("random", 5, 2))
     check([s], *run([s], [s.flat(0)], 2, scores=True), 2)
+
+
+@pytest.mark.parametrize("Hkv,lens", [(2, [300, 40]), (1, [129, 1000]), (8, [700])])
+def test_a_layer_of_a_pool_of_several(Hkv, lens):
+    """The pools that the step, the commit and eviction take: the same bits as a pool of the layer alone."""
+    rng = np.random.default_rng(sum(lens))
+    slots = [Slot(rng, 4 * Hkv, Hkv, L, tree_of("random", 3, L)) for L in lens]
+    views = [s.paged(3 * i, rng) for i, s in enumerate(slots)]
+    want = run(slots, views, Hkv, scores=True)
+    for layers, layer in ((3, 0), (3, 2), (2, 1)):
+        wide = []
+        for v in views:
+            pools = []
+            for x in (v.k_pool, v.v_pool):
+                pool = torch.full((x.shape[0], layers, *x.shape[1:]), float("nan"), dtype=torch.float16, device="cuda")
+                pool[:, layer] = x
+                pools.append(pool[:, layer])
+            wide.append(luce.PagedTreeView(*pools, v.table, v.len, v.parent, v.row0))
+        got = run(slots, wide, Hkv, scores=True)
+        assert all(np.array_equal(bits(a), bits(b)) for a, b in zip(got, want))
+    v = views[0]
+    with pytest.raises(ValueError):                             # pages whose heads lie apart
+        k = torch.zeros(4, 2 * Hkv, 128, 128, dtype=torch.float16, device="cuda")[:, ::2]
+        k = k if Hkv > 1 else torch.zeros(4, 1, 256, 128, dtype=torch.float16, device="cuda")[:, :, ::2]
+        luce.luce_tree_attn_paged(torch.zeros(3, 4 * Hkv, 128, device="cuda"), [luce.PagedTreeView(k, k, v.table, 100, 3)], Hkv, 0.1)
