@@ -69,7 +69,8 @@ tree_commit_kernel(const __grid_constant__ CommitBatch b, int n_layers, int Hq, 
     pdl_wait();
     for (int i = tid; i < n; i += kCommitThreads) {
         const float2 st = ld_placed_f2(stats + 2 * at[i]);
-        ml[i] = make_float2(st.x == -INFINITY ? 0.0f : st.x, st.y == 0.0f ? 0.0f : __fdiv_rn(1.0f, st.y));
+        // (l = 0: e^(s - inf) adds nothing, whatever s)
+        ml[i] = st.y == 0.0f ? make_float2(INFINITY, 0.0f) : make_float2(st.x == -INFINITY ? 0.0f : st.x, __fdiv_rn(1.0f, st.y));
     }
     float* acc = sl.acc + (int64_t)lh * sl.cap;
     const int j = tile * kCommitKeys + 4 * tid;

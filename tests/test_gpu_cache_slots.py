@@ -6,7 +6,7 @@ import cache_reference as ref
 
 torch = pytest.importorskip("torch")
 import invariant_sequence_decode_gb300 as luce  # noqa: E402
-from test_gpu_cache import cuda, same  # noqa: E402
+from test_gpu_cache import cuda, same, weight_tolerance  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +74,23 @@ def test_a_prepared_eviction_follows_a_replaced_table(length, budget):
         for pool, w in zip(pools, want[:2]):
             got = pool[torch.from_numpy(table).long()].cpu().numpy().transpose(1, 2, 0, 3, 4).reshape(L, Hkv, per * 128, 128)
             assert np.array_equal(got.view(np.uint16), w.view(np.uint16))
+
+
+@pytest.mark.parametrize("m", [float("-inf"), 0.0, -50.0, 3.0])
+@pytest.mark.parametrize("length", [1, 70, 1300])
+def test_a_row_without_weights_adds_nothing_whatever_its_scores(m, length):
+    rng = np.random.default_rng(length)
+    L, Hq, Hkv, n, path = 2, 4, 2, 3, [0, 2]
+    cap = length + n
+    k, v = (cuda(rng.standard_normal((L, Hkv, cap, 128)).astype(np.float16)) for _ in range(2))
+    acc = rng.random((L, Hkv, cap)).astype(np.float32)
+    scores = rng.standard_normal((L, n, Hq, -(-cap // 4) * 4)).astype(np.float32)
+    stats = np.stack([scores.max(-1), np.exp(scores - scores.max(-1, keepdims=True)).sum(-1)], -1).astype(np.float32)
+    scores[:, 2] = 100 * np.abs(scores[:, 2]) + 100             # e^s is past fp32
+    scores[:, 2, :, ::3] = -np.inf
+    stats[:, 2] = m, 0
+    _, _, want, _ = ref.commit(k.cpu().numpy(), v.cpu().numpy(), length, path, acc, scores=scores, stats=stats)
+    slot = luce.CommitSlot(k, v, length, path, acc=cuda(acc))
+    luce.luce_tree_commit([slot], Hq, cuda(scores), cuda(stats))
+    got = slot.acc.cpu().numpy()[:, :, :length + 2]
+    assert np.abs(got - want[:, :, :length + 2]).max() <= weight_tolerance(want, Hq // Hkv, len(path))
