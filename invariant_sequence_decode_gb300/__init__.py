@@ -1114,6 +1114,17 @@ def luce_decode_step_tree(model: "Model", slots: Sequence[TreeSlot], x, ws, logi
     trees = [_tree(s.parent) for s in slots]
     if sum(t[0] for t in trees) != T:
         raise ValueError(f"x has {T} rows, the trees {sum(t[0] for t in trees)}")
+    if x.shape != (T, model.hidden):
+        raise ValueError(f"x: expected [T][{model.hidden}]")
+    if logits is not None:
+        _need(logits, torch.float32, "logits")
+        if logits.numel() < T * model.vocab:
+            raise ValueError(f"logits: expected [{T}][{model.vocab}]")
+    if argmax is not None:
+        _need(argmax, torch.int32, "argmax")
+        if argmax.numel() < T:
+            raise ValueError(f"argmax: expected [{T}]")
+    _need(ws, torch.uint8, "ws")
     sc = ((PagedTreeSlotC if paged else TreeSlotC) * max(1, n))()
     tables = [s.mirror_table(stream) if paged else None for s in slots]
     for i, (s, (nn, par), t) in enumerate(zip(slots, trees, tables)):

@@ -33,7 +33,7 @@ def library(monkeypatch):
 
 
 class TinyModel:
-    layers, n_kv_heads, n_q_heads, vocab = [None], 2, 4, 0
+    layers, n_kv_heads, n_q_heads, vocab, hidden = [None], 2, 4, 0, 256
     c = luce.ModelC()
 
 
@@ -269,3 +269,23 @@ def test_two_threads_on_two_streams_keep_to_their_own(prepared, monkeypatch):
     assert launched == [22, 11]
     call()
     assert launched == [22, 11, 11]
+
+
+@pytest.mark.parametrize("bad", [dict(x=torch.zeros(1, 255)), dict(x=torch.zeros(1, 2, 128)), dict(x=torch.zeros(2, 256)),
+                                 dict(logits=torch.zeros(1, 9)), dict(argmax=torch.zeros(0, dtype=torch.int32))])
+def test_a_tree_step_refuses_buffers_that_are_too_small(library, bad):
+    """They would be read or written past their ends."""
+    class Model(TinyModel):
+        vocab = 10
+
+    calls = []
+    library.luce_decode_step_tree = lambda *a: calls.append(a) or 0
+    library.luce_decode_step_tree.argtypes = None
+    kv = lambda: torch.zeros(1, 2, 40, 128, dtype=torch.float16)  # noqa: E731
+    a = dict(x=torch.zeros(1, 256), logits=torch.zeros(1, 10), argmax=torch.zeros(1, dtype=torch.int32))
+    run = lambda **kw: luce.luce_decode_step_tree(Model, [luce.TreeSlot(kv(), kv(), 10, 1)], ws=torch.zeros(64, dtype=torch.uint8), **kw)  # noqa: E731
+    run(**a)
+    a.update(bad)
+    with pytest.raises(ValueError):
+        run(**a)
+    assert len(calls) == 1
