@@ -540,7 +540,10 @@ class _TableMirror:
         import torch
         table, device = np.ascontiguousarray(self.table, dtype=np.int32), self.k_pool.device
         now = None if device.type != "cuda" else stream or torch.cuda.current_stream(device)
-        capturing = now is not None and torch.cuda.is_current_stream_capturing()
+        capturing = False
+        if now is not None:
+            with torch.cuda.stream(now):
+                capturing = torch.cuda.is_current_stream_capturing()
         if self._mirrored is None or not np.array_equal(table, self._mirrored):
             if capturing:
                 raise RuntimeError("the slot's table changed: call mirror_table() before the capture")

@@ -144,8 +144,8 @@ cudaError_t launch_tree_wait_expiry(uint64_t limit_ns, cudaStream_t s);
 // Bounded waits of the tree attention that expired on the current device.
 cudaError_t read_tree_wait_timeouts(uint32_t* count, bool reset);
 
-// Offsets are in elements from k and v: path row i moves from from[i] to to[i]
-// in each (layer, KV head), head_step apart.
+// In each (layer, KV head) lh, row at(len + path[i]) moves to row at(len + i), in
+// elements from k + lh * head_step and v + lh * head_step.
 struct CommitSlot {
     __half* k;
     __half* v;

@@ -69,3 +69,31 @@ def test_a_captured_step_keeps_its_table(model):  # noqa: F811
     torch.cuda.synchronize()
     luce.luce_decode_step_tree(model, [slot], x, ws)
     torch.cuda.synchronize()
+
+
+def test_a_capture_on_a_stream_that_is_not_the_current_one(model):  # noqa: F811
+    d = wl.TINY_LAYER
+    k, v = (torch.randn(6, LAYERS, d.n_kv_heads, 128, 128, device="cuda").half() for _ in range(2))
+    slot = luce.PagedTreeSlot(k, v, np.array([1, 4]), 200)
+    xh = cuda(wl.acts(3, 1, d.hidden, sub=9))
+    x, ws, side, graph = xh.clone(), model.tree_workspace(1, 300), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    luce.luce_decode_step_tree(model, [slot], x, ws)
+    torch.cuda.synchronize()
+    want, first = bits(x), slot.table_dev
+    with torch.cuda.stream(side):
+        graph.capture_begin()
+    try:
+        luce.luce_decode_step_tree(model, [slot], x, ws, stream=side)
+        slot.table = np.array([5, 0, 2])
+        with pytest.raises(RuntimeError, match="before the capture"):
+            luce.luce_decode_step_tree(model, [slot], x, ws, stream=side)
+    finally:
+        with torch.cuda.stream(side):
+            graph.capture_end()
+    luce.luce_decode_step_tree(model, [slot], xh.clone(), ws)
+    assert slot.table_dev is not first and any(t is first for t in slot._captured)
+    x.copy_(xh)
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert np.array_equal(bits(x), want)
