@@ -30,8 +30,8 @@
 // the products, and 256 threads (two to a row, 64 keys each) turn S into P in
 // place in tensor memory and add each tile's O into registers with the running
 // maximum's correction; a tile takes 2,650 cycles.  16 nodes of 40 heads over
-// 130,800 keys of 8 heads: 98 us, 86 alone at 6.2 TB/s.  Short ones are bound by
-// one tile's chain (K, S, softmax, P V, O: 6 us) and the merge (3.5 us).
+// 130,800 keys of 8 heads: 102 us, the chunks alone 89 at 6.0 TB/s.  Short ones
+// are bound by one tile's chain (K, S, softmax, P V, O: 6 us) and the merge (4 us).
 #include <limits.h>
 
 #include <algorithm>
@@ -48,8 +48,8 @@ constexpr int kTreeTile = 128;  // keys of a tile, and rows of the products
 constexpr int kMaxTreeChunks = 160;
 // Longest prefix that tree_short_kernel takes.  It reads the prefix once per row
 // and head, the chunks once per KV head: at 64 keys it takes 3.2 us for one row
-// of 8 heads and 7.3 for 16 rows of 40, through chunks 6.1 and 9.4; at 128 keys
-// 4.5 and 13.2 against 5.7 and 8.8.
+// of 8 heads and 7.3 for 16 rows of 40, through chunks 6.8 and 9.9; at 128 keys
+// 4.6 and 13.0 against 6.5 and 9.3.
 constexpr int kTreeShort = 64;
 constexpr int kTreeCtas = 152;  // the CTAs that a cut aims at: one per multiprocessor
 
@@ -57,7 +57,7 @@ constexpr int kTreeCtas = 152;  // the CTAs that a cut aims at: one per multipro
 // one more (its q, its results); one view's chunks, Hkv heads, go to kTreeCtas
 // CTAs in rounds.  Of the cuts that fill 1, 2, 3 or 4 rounds the cheapest is
 // taken, the one with fewer chunks of equals: 130,800 keys of 8 heads make 19
-// chunks of 54 tiles (8-tile chunks, 128 a head: 117 against 97 us).
+// chunks of 54 tiles (8-tile chunks, 128 a head: 129 against 90 us, replayed).
 static int tree_chunk_tiles(int nt, int Hkv)
 {
     int best = nt, least = INT_MAX;
