@@ -661,7 +661,8 @@ tree_chunk_kernel(const __grid_constant__ TreeMaps maps, const float* q, const _
                     // below), an expired wait or not, and leave together
                     asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
                     if ((left = bail[quad])) break;
-                    // rounded up, and the weights' shift below down: none is above 2^kTreeUp
+                    // rounded up, and the weights' shift down: none is above 2^kTreeUp (the
+                    // shift is exact for top >= 15, else off by one unit of itself at most)
                     const float log2 = __fmul_rn(scale.log2, unit);
                     const float top = fmaxf(m, __fmul_ru(fmaxf(mx[i & 1][0][row], mx[i & 1][1][row]), log2));
                     const float at = top == -INFINITY ? 0.0f : top, up = __fsub_rd(kTreeUp, at);
