@@ -528,33 +528,50 @@ class _TableMirror:
     ``table_dev`` is its copy on the device."""
 
     def __post_init__(self):
-        import numpy as np
-        self.table, self._mirrored, self._captured = np.ascontiguousarray(self.table, dtype=np.int32), None, []
+        self._array = self._mirrored = None
+        self._captured = []
         self.mirror_table()
+        self.table = self._array
 
     def mirror_table(self, stream=None):
         """Bring table_dev up to date for a call on ``stream`` and return the host
         table.  A changed table gets a new device copy (calls under way and
         captured ones keep theirs), which cannot be made during a capture."""
+        return _mirror_tables([self], stream)[0]
+
+    def _mirror(self, stream, now, capturing):
         import numpy as np
         import torch
-        table, device = np.ascontiguousarray(self.table, dtype=np.int32), self.k_pool.device
-        now = None if device.type != "cuda" else stream or torch.cuda.current_stream(device)
-        capturing = False
-        if now is not None:
-            with torch.cuda.stream(now):
-                capturing = torch.cuda.is_current_stream_capturing()
-        if self._mirrored is None or not np.array_equal(table, self._mirrored):
+        table = self.table
+        if table is not self._array:  # (an int32 array stays itself, anything else is copied at every call)
+            table = self._array = np.ascontiguousarray(table, dtype=np.int32)
+            self._host = table.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))  # (1.5 us)
+        contents = table.tobytes()
+        if contents != self._mirrored:
             if capturing:
                 raise RuntimeError("the slot's table changed: call mirror_table() before the capture")
-            self._mirrored = table.copy()
-            self.table_dev = torch.from_numpy(table.copy()).to(device)
-            self._home = None if now is None else torch.cuda.current_stream(device).cuda_stream
+            self.table_dev, self._mirrored, self._home = torch.from_numpy(table.copy()).to(self.k_pool.device), contents, now
         if capturing:
             self._captured.append(self.table_dev)
-        elif now is not None and now.cuda_stream != self._home:
-            self.table_dev.record_stream(now)
+        elif stream != self._home:
+            self.table_dev.record_stream(torch.cuda.ExternalStream(stream, device=self.k_pool.device))
         return table
+
+
+def _mirror_tables(slots, stream):
+    """The slots' host tables, their device copies brought up to date for a call on ``stream``."""
+    import torch
+    device = slots[0].k_pool.device if slots else None
+    if device is None or device.type != "cuda":
+        return [s._mirror(None, None, False) for s in slots]
+    now = torch._C._cuda_getCurrentRawStream(device.index)
+    at = now if stream is None else stream.cuda_stream
+    if at == now:
+        capturing = torch.cuda.is_current_stream_capturing()
+    else:
+        with torch.cuda.stream(stream):
+            capturing = torch.cuda.is_current_stream_capturing()
+    return [s._mirror(at, now, capturing) for s in slots]
 
 
 @dataclass
@@ -575,10 +592,9 @@ def luce_decode_step_paged(model: "Model", slots: Sequence[PagedSlot], rows_per_
     _need(x, torch.float32, "x")
     n = len(slots)
     sc = (PagedSlotC * max(1, n))()
-    tables = [s.mirror_table(stream) for s in slots]
-    for i, (s, t) in enumerate(zip(slots, tables)):
+    for i, (s, t) in enumerate(zip(slots, _mirror_tables(slots, stream))):
         sc[i] = PagedSlotC(s.k_pool.data_ptr(), s.v_pool.data_ptr(), s.table_dev.data_ptr(),
-                           t.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)), t.size, s.k_pool.shape[0], s.len)
+                           s._host, t.size, s.k_pool.shape[0], s.len)
     rows = (ctypes.c_int32 * max(1, n))(*rows_per_slot)
     _check(load_library().luce_decode_step_paged(ctypes.byref(model.c), sc, rows, n, x.data_ptr(), _ptr(logits),
                                                  _ptr(argmax), ws.data_ptr(), ws.numel(), _stream(stream)))
@@ -1129,15 +1145,14 @@ def luce_decode_step_tree(model: "Model", slots: Sequence[TreeSlot], x, ws, logi
             raise ValueError(f"argmax: expected [{T}]")
     _need(ws, torch.uint8, "ws")
     sc = ((PagedTreeSlotC if paged else TreeSlotC) * max(1, n))()
-    tables = [s.mirror_table(stream) if paged else None for s in slots]
+    tables = _mirror_tables(slots, stream) if paged else [None] * n
     for i, (s, (nn, par), t) in enumerate(zip(slots, trees, tables)):
         pos0 = s.len if s.pos0 is None else s.pos0
         if paged:
             _pools(s.k_pool, s.v_pool, L, Hkv, f"slots[{i}]")
             _same_device(x, s.k_pool, s.v_pool, s.table_dev)
             sc[i] = PagedTreeSlotC(s.k_pool.data_ptr(), s.v_pool.data_ptr(), s.table_dev.data_ptr(),
-                                   t.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)), t.size, s.k_pool.shape[0], s.len,
-                                   pos0, nn, par)
+                                   s._host, t.size, s.k_pool.shape[0], s.len, pos0, nn, par)
         else:
             _caches(s.k, s.v, L, Hkv, f"slots[{i}]")
             _same_device(x, s.k, s.v)
