@@ -41,6 +41,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "ring.cuh"
+#include "tensor.cuh"
 
 namespace luce {
 
@@ -170,51 +171,6 @@ __device__ __forceinline__ TreeRun tree_run(const TreeBatch& b, int Hkv, int u, 
     return t;
 }
 
-__device__ __forceinline__ uint64_t tree_desc(uint32_t addr, uint32_t lbo, uint32_t sbo)
-{
-    // 128-byte swizzle; start address, leading and stride byte offsets in units of 16
-    return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) | (1ull << 46) |
-           (2ull << 61);
-}
-
-// D[128][128] (+)= A (tensor memory, f16) * B (shared memory), one 16-wide
-// step, by the lane whose `elected` is set.  The whole warp comes here: issued
-// from a branch of one thread, each product cost 152 cycles (its descriptor
-// goes through registers that only a converged warp has at hand) against 64.
-__device__ __forceinline__ void tree_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate,
-                                         uint32_t elected)
-{
-    asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-                 " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-                 "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(elected));
-}
-
-__device__ __forceinline__ void tree_commit_mma(uint64_t* bar, uint32_t elected)
-{
-    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
-                 " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_addr(bar)),
-                 "r"(elected)
-                 : "memory");
-}
-
-// One arrival for the warp, behind what all of its threads have done to tensor
-// memory (32 arrivals of their own would queue at the barrier's word).
-__device__ __forceinline__ void warp_arrive(uint64_t* bar)
-{
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-}
-
-__device__ __forceinline__ uint32_t elect_one()
-{
-    uint32_t e;
-    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(e));
-    return e;
-}
-__device__ __forceinline__ void tm_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tm_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
 // 64 columns of this warp's 32 lanes of tensor memory, waited for.
 __device__ __forceinline__ void tm_ld64(uint32_t addr, float* v)
 {
@@ -248,68 +204,11 @@ __device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t* r)
         "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
         : "memory");
 }
-__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ float tree_exp2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// Pairs of fp32 values: two sums or fused multiply-adds per instruction.
-__device__ __forceinline__ uint64_t pair(float a, float b)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t x)
-{
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
-// Two fp32 values as f16 pairs, x = hi + lo; the first in the low half.
-__device__ __forceinline__ void tree_split(float x0, float x1, uint32_t& hi, uint32_t& lo)
-{
-    float l0, l1;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(x1), "f"(x0));
-    asm("{\n .reg .f16 a, b, n;\n mov.b32 {a, b}, %2;\n mov.b16 n, 0xBC00;\n"  // x - hi, exactly
-        " fma.rn.f32.f16 %0, a, n, %3;\n fma.rn.f32.f16 %1, b, n, %4;\n}"
-        : "=f"(l0), "=f"(l1)
-        : "r"(hi), "f"(x0), "f"(x1));
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(l1), "f"(l0));
-}
-
 __device__ __forceinline__ void st_v8(float* p, const float* v)
 {
     asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
                  "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                  : "memory");
-}
-
-// A box of the (d, key, head, page) map.
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, int x, int y, int z, int w, uint64_t* bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-        "[%6];" ::"r"(smem_addr(dst)),
-        "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
-        : "memory");
 }
 
 // The producer: K and V tiles of the CTA's chunks, in order.  Returns the
@@ -766,7 +665,7 @@ cudaError_t read_tree_wait_timeouts(uint32_t* count, bool reset)
     return e;
 }
 
-static PFN_cuTensorMapEncodeTiled_v12000 tree_map_encoder()
+PFN_cuTensorMapEncodeTiled_v12000 tree_map_encoder()
 {
     static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
         void* p = nullptr;
@@ -812,21 +711,6 @@ static bool tree_maps(const TreeBatch& b, int Hkv, TreeMaps* maps)
 // wait only addresses are formed and lines of flat caches asked for in L2 (16
 // nodes with scores 12.3 us, 13.2 without that).
 constexpr int kMergeAhead = 8;  // chunk sums in flight per warp
-
-__device__ __forceinline__ float4 half4(uint2 x)
-{
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&x.x));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&x.y));
-    return make_float4(a.x, a.y, b.x, b.y);
-}
-
-__device__ __forceinline__ void axpy4(float4& o, float4 x, float a)
-{
-    o.x = __fmaf_rn(x.x, a, o.x);
-    o.y = __fmaf_rn(x.y, a, o.y);
-    o.z = __fmaf_rn(x.z, a, o.z);
-    o.w = __fmaf_rn(x.w, a, o.w);
-}
 
 // Asks for a line in L2; no value is read.
 __device__ __forceinline__ void fetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory"); }
