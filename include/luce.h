@@ -766,6 +766,130 @@ typedef struct luce_paged_evict_slot {
 } luce_paged_evict_slot;
 int luce_kv_evict_paged(const luce_paged_evict_slot* slots, int n_seq, int n_layers, int Hkv, int D, void* stream);
 
+/* ---------------------------------------------------------------- caches in 8 bits */
+
+/*
+ * A slot's cache in 8 bits.  Its first `sealed` keys, a multiple of
+ * LUCE_Q8KV_BLOCK, are int8 codes in pages of LUCE_PAGE_KEYS keys; a block of 32
+ * tokens of one layer and KV head shares one fp32 scale for K and one for V, and a
+ * code stands for code * scale.  The keys behind them are binary16 rows in
+ * a short tail (rows 0 ..; the step's and the commit's flat caches), where draft
+ * trees live too, until luce_q8kv_seal turns whole blocks of them into codes.
+ * A block is so quantised once, from its committed tokens alone.
+ *   codes of K   [n_pages][n_layers][Hkv][128 keys][128 dims]
+ *   codes of V   [n_pages][n_layers][Hkv][128 dims][128 keys] (transposed)
+ *   scales       [n_pages][n_layers][Hkv][2][4]: K's of the page's four blocks, V's
+ * Key j is in page table[j / 128] at key j % 128; without a table page i holds the
+ * keys 128 i ..
+ */
+#define LUCE_Q8KV_BLOCK 32
+#define LUCE_Q8KV_MAX_TAIL 112  /* f16 keys between the blocks and the tree that attention takes */
+
+typedef struct luce_q8kv_slot {
+    uint16_t* k;            /* (device) tail, binary16 [n_layers][Hkv][cap][128], 16-byte aligned */
+    uint16_t* v;            /* (device) same layout */
+    int32_t len;            /* rows of the tail */
+    int32_t cap;
+    int8_t* k_codes;        /* (device) as above, 16-byte aligned */
+    int8_t* v_codes;        /* (device) */
+    float* scales;          /* (device) 16-byte aligned */
+    const int32_t* table;   /* (device) or NULL; ceil((sealed + len / 32 * 32) / 128) entries */
+    int32_t n_pages;
+    int32_t sealed;         /* keys already in blocks */
+} luce_q8kv_slot;
+
+/*
+ * Seals the whole blocks of up to 4 slots' tails, in every layer and KV head:
+ * rows 32 i .. 32 i + 31 of the tail, i < len / 32, become the block at keys
+ * sealed + 32 i ..:  scale = amax / 127 (fp32, IEEE division; amax: the largest
+ * finite magnitude of the block), code = round(x / scale) with an IEEE fp32
+ * division and rounding half away from zero, clamped to [-127, 127]; a
+ * block with scale 0 gives zeros, a NaN gives 0.  The len % 32 rows behind
+ * them move to rows 0 ..; other rows, and everything of a slot with len < 32, are
+ * left as they were.  The caller continues with sealed + len / 32 * 32
+ * keys in blocks and a tail of len % 32.  An entry of table outside [0, n_pages):
+ * its blocks are not written.  Slots may share pools, no page is named twice
+ * at spans that the call writes; other arrays overlap nothing.
+ * sealed + len <= LUCE_MAX_KEYS, D == 128, 1 <= n_seq <= LUCE_MAX_SEQ.
+ */
+int luce_q8kv_seal(const luce_q8kv_slot* slots, int n_seq, int n_layers, int Hkv, int D, void* stream);
+
+/*
+ * A slot's cache in 8 bits for one layer, with its draft tree (parent and
+ * n_nodes as in luce_treeview; one node for plain decode).  Of pools of several
+ * layers, layer l's codes start at l * Hkv * 128 * 128, its scales at l * Hkv * 8, with a
+ * page_stride of n_layers * Hkv * 128 * 128.  With a window > 0 a row at position
+ * p = sealed + len + (its ancestors) sees, of the prefix and its own path, the
+ * keys at positions i < sinks or p - i < window; so always itself.
+ * Codes, scales and table may be NULL and n_pages 0 while nothing is sealed.
+ */
+typedef struct luce_q8kv_view {
+    const int8_t* k_codes;  /* (device) 16-byte aligned */
+    const int8_t* v_codes;  /* (device) */
+    const float* scales;    /* (device) 16-byte aligned */
+    const int32_t* table;   /* (device) or NULL; ceil(sealed / 128) entries, one outside [0, n_pages) holds zeros */
+    const uint16_t* k;      /* (device) tail: element (g, i, d) at g*head_stride + i*tok_stride + d, 16-byte aligned */
+    const uint16_t* v;      /* (device) */
+    int64_t page_stride;    /* codes from page to page, a multiple of 128 * 128; 0: Hkv * 128 * 128 */
+    int64_t head_stride;    /* of the tail, elements, multiple of 8 */
+    int64_t tok_stride;     /* elements, multiple of 8, >= D */
+    int32_t n_pages;
+    int32_t sealed;         /* keys in blocks, a multiple of 32 */
+    int32_t len;            /* keys of the tail ahead of the tree, 0..LUCE_Q8KV_MAX_TAIL */
+    int32_t cap;            /* rows of the tail (len + n_nodes <= cap) */
+    int32_t n_nodes;        /* 1..LUCE_MAX_TREE */
+    int32_t row0;
+    int32_t window;         /* 0: none */
+    int32_t sinks;          /* the first keys stay visible (with a window) */
+    const int32_t* parent;  /* (host) [n_nodes] or NULL */
+} luce_q8kv_view;
+
+/*
+ * Attention of every node of up to 4 slots' draft trees over caches in 8 bits:
+ * luce_tree_attn's rows, output and invariance (a node gives the same bits in any
+ * tree, in a chain of its own path, with any other slots, with or without a
+ * table), over the keys that the row sees.
+ *   q   (device) fp32 [T][Hq][D], 16-byte aligned, |q| < 65504;  out (device) fp32 [T][Hq][D]
+ *   ws  (device) luce_q8kv_attn_workspace_size(...) bytes, 256-byte aligned (no
+ *       initial contents); calls that can overlap on the GPU need scratches of
+ *       their own
+ * q, scales and the tail's rows that a node sees must be finite; what lies where no
+ * row sees it is not used, whatever it is.  Sizes as luce_tree_attn, sealed + len
+ * + n_nodes <= LUCE_MAX_KEYS.  out and ws overlap nothing that the call reads or
+ * writes (LUCE_EINVAL), but out may be q itself.
+ */
+int luce_q8kv_attn(const float* q, const luce_q8kv_view* views, int n_seq, int Hq, int Hkv, int D, float scale,
+                   float* out, void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of scratch luce_q8kv_attn needs for n_rows rows over at most max_sealed
+ * keys in blocks (0 for arguments it refuses). */
+size_t luce_q8kv_attn_workspace_size(int n_rows, int Hq, int Hkv, int D, int max_sealed);
+
+/*
+ * Norms of q and k per head, RoPE and the K/V append of a projection's rows in one
+ * pass, for models that norm their heads or whose positions have several axes
+ * (time, height, width), and for prompts of any length.  Row t of qkv holds Hq q
+ * heads, Hkv k heads and Hkv v heads.  A q or k head x becomes
+ *   y = x * (1 / sqrt(mean(x^2) + eps)) * gamma      (x itself where gamma is NULL)
+ * and its dims (i, i + D/2) rotate by pos[pair_axis[i]][t] * theta^(-2i/D), cosine and
+ * sine as in luce_rope_posvec.  q is written as fp32, k and v heads are rounded to
+ * binary16 (nearest even) at the rows' positions in their views' caches: row row0 + j
+ * of a view at position len - n_q + j, as in luce_kv_append, with any n_q >= 1.
+ * Without gammas and with one axis the bits are those of luce_rope_posvec and
+ * luce_kv_append; a row's bits do not depend on the other rows.
+ *   qkv (device) fp32 [T][ld], 16-byte aligned, ld a multiple of 4
+ *   q_gamma, k_gamma (device) fp32 [D], 16-byte aligned, or NULL
+ *   pos (device) int32 [n_axes][T];  pair_axis (host) [D/2], each < n_axes, or
+ *       NULL for one axis
+ *   q   (device) fp32 [T][Hq][D], 16-byte aligned
+ * The views name every row 0 .. T-1 once; nothing written overlaps anything else.
+ * D == 128, 1 <= n_axes <= LUCE_MAX_AXES, 1 <= n_seq <= LUCE_MAX_SEQ.
+ */
+#define LUCE_MAX_AXES 4
+int luce_qk_norm_rope(const float* qkv, int64_t ld, const luce_seqview* views, int n_seq, int Hq, int Hkv, int D,
+                      const float* q_gamma, const float* k_gamma, float eps, const int32_t* pos, int n_axes,
+                      const uint8_t* pair_axis, double theta, float* q, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

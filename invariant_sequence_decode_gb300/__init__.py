@@ -123,6 +123,21 @@ class PagedEvictSlotC(ctypes.Structure):
                 ("recent", ctypes.c_int32), ("next_pos", ctypes.c_int32)]
 
 
+class Q8SlotC(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("len", ctypes.c_int32), ("cap", ctypes.c_int32),
+                ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("n_pages", ctypes.c_int32), ("sealed", ctypes.c_int32)]
+
+
+class Q8ViewC(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("tok_stride", ctypes.c_int64),
+                ("n_pages", ctypes.c_int32), ("sealed", ctypes.c_int32), ("len", ctypes.c_int32), ("cap", ctypes.c_int32),
+                ("n_nodes", ctypes.c_int32), ("row0", ctypes.c_int32), ("window", ctypes.c_int32), ("sinks", ctypes.c_int32),
+                ("parent", ctypes.POINTER(ctypes.c_int32))]
+
+
 _LAYOUT_FIELDS = ("xn", "xn_q", "xn_d", "qkv", "q_rot", "part", "attn", "attn_q", "attn_d", "x1",
                   "xn2", "xn2_q", "xn2_d", "gu", "h", "h_q", "h_d", "xf", "xf_q", "xf_d", "total")
 
@@ -140,7 +155,8 @@ EXPORTS = ("luce_last_error", "luce_version", "luce_launch_count", "luce_q8_quan
            "luce_swiglu_q8", "luce_step_graph_create", "luce_step_graph_run", "luce_step_graph_stats",
            "luce_step_graph_destroy", "luce_tree_attn", "luce_tree_attn_paged", "luce_tree_attn_workspace_size",
            "luce_tree_commit", "luce_kv_evict", "luce_decode_step_tree", "luce_decode_step_tree_layout",
-           "luce_decode_step_tree_paged", "luce_tree_commit_paged", "luce_kv_evict_paged")
+           "luce_decode_step_tree_paged", "luce_tree_commit_paged", "luce_kv_evict_paged", "luce_q8kv_seal",
+           "luce_q8kv_attn", "luce_q8kv_attn_workspace_size", "luce_qk_norm_rope")
 
 _lib = None
 
@@ -207,9 +223,16 @@ def load_library(path: str = LIB_PATH):
     lib.luce_decode_step_tree_layout.argtypes = [ctypes.POINTER(ModelC), i32, i32, ctypes.POINTER(StepLayoutC)]
     lib.luce_tree_commit.argtypes = [ctypes.POINTER(CommitSlotC), i32, i32, i32, i32, i32, vp, i32, i64, vp, vp]
     lib.luce_kv_evict.argtypes = [ctypes.POINTER(EvictSlotC), i32, i32, i32, i32, vp]
+    lib.luce_q8kv_seal.argtypes = [ctypes.POINTER(Q8SlotC), i32, i32, i32, i32, vp]
+    lib.luce_q8kv_attn.argtypes = [vp, ctypes.POINTER(Q8ViewC), i32, i32, i32, i32, f32, vp, vp, sz, vp]
+    lib.luce_q8kv_attn_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+    lib.luce_q8kv_attn_workspace_size.restype = sz
+    lib.luce_qk_norm_rope.argtypes = [vp, i64, ctypes.POINTER(SeqViewC), i32, i32, i32, i32, vp, vp, f32, vp, i32, vp, f64, vp,
+                                      vp]
     for name in EXPORTS:
         if name not in ("luce_last_error", "luce_version", "luce_launch_count", "luce_decode_attn_workspace_size",
-                        "luce_decode_attn_noalloc_max_bytes", "luce_tree_attn_workspace_size"):
+                        "luce_decode_attn_noalloc_max_bytes", "luce_tree_attn_workspace_size",
+                        "luce_q8kv_attn_workspace_size"):
             getattr(lib, name).restype = i32
     _lib = lib
     return lib
@@ -1374,3 +1397,377 @@ def luce_kv_evict(slots: Sequence[EvictSlot], stream=None):
     """Cut the slots' caches to their budgets by accumulated attention weight,
     per layer and KV head.  The caller continues with min(len, budget) keys."""
     KvEvict(slots, stream)()
+
+
+# ------------------------------------------------------------ caches in 8 bits
+
+Q8_BLOCK = 32       # tokens that share a scale
+Q8_MAX_TAIL = 112   # f16 keys between the blocks and the tree
+
+
+def q8_cache(n_pages: int, n_layers: int, n_kv_heads: int, device="cuda"):
+    """Empty pools of a cache in 8 bits: k_codes, v_codes (int8 [n_pages][n_layers][Hkv][128][128],
+    V's transposed) and scales (fp32 [n_pages][n_layers][Hkv][2][4]) of pages of 128 tokens."""
+    import torch
+    shape = (n_pages, n_layers, n_kv_heads)
+    return (torch.zeros(*shape, PAGE_KEYS, HEAD_DIM, dtype=torch.int8, device=device),
+            torch.zeros(*shape, HEAD_DIM, PAGE_KEYS, dtype=torch.int8, device=device),
+            torch.zeros(*shape, 2, PAGE_KEYS // Q8_BLOCK, device=device))
+
+
+@dataclass
+class Q8Slot:
+    """A slot to be sealed: the tail's rows of every layer (fp16 [n_layers][Hkv][cap][128]),
+    ``len`` of them, behind ``sealed`` keys in the pools of ``q8_cache``; ``table`` (device int32)
+    names the pool page of each 128-key span (None: page i is span i's)."""
+    k: object
+    v: object
+    len: int
+    k_codes: object
+    v_codes: object
+    scales: object
+    sealed: int = 0
+    table: object = None
+
+
+@dataclass
+class Q8View:
+    """A slot's cache in 8 bits for one layer: ``sealed`` keys in codes (int8
+    [n_pages][Hkv][128][128], V's transposed) and scales (fp32 [n_pages][Hkv][2][4]), or the layer
+    pool[:, l] of ``q8_cache``'s pools; ``len`` keys of the tail (fp16 [Hkv][cap][128]), node j of
+    the tree ``parent`` (as in TreeView) at its row len + j.  ``window`` > 0: a row sees itself, the
+    window - 1 keys before it and the first ``sinks`` keys."""
+    k_codes: object
+    v_codes: object
+    scales: object
+    sealed: int
+    k: object
+    v: object
+    len: int = 0
+    parent: object = 1
+    row0: int = 0
+    table: object = None
+    window: int = 0
+    sinks: int = 0
+
+
+def _q8_pools(k_codes, v_codes, scales, lead, name):
+    """Checks a page's codes and scales behind the pools' leading dims (pages, or pages and layers)."""
+    import torch
+    for t, dt, page, w in ((k_codes, torch.int8, (PAGE_KEYS, HEAD_DIM), "k_codes"),
+                           (v_codes, torch.int8, (HEAD_DIM, PAGE_KEYS), "v_codes"),
+                           (scales, torch.float32, (2, PAGE_KEYS // Q8_BLOCK), "scales")):
+        if not isinstance(t, torch.Tensor) or t.dtype != dt or not t.is_cuda:
+            raise TypeError(f"{name}.{w}: expected a CUDA {dt} tensor")
+        if t.dim() != 3 + len(lead) or t.shape[1:] != (*lead, *page) or t.shape[0] != k_codes.shape[0]:
+            raise ValueError(f"{name}.{w}: expected [n_pages]{''.join(f'[{n}]' for n in (*lead, *page))}")
+
+
+def _page_stride(t, per_page, name):
+    """Elements from page to page of pools whose pages lie in a row each; 0 for a single page."""
+    want = []
+    n = 1
+    for size in reversed(t.shape[1:]):
+        want.insert(0, n)
+        n *= size
+    if any(size > 1 and s != w for size, s, w in zip(t.shape[1:], t.stride()[1:], want)):
+        raise ValueError(f"{name}: each page of a layer must be contiguous")
+    if t.shape[0] <= 1:
+        return 0
+    if t.stride(0) % per_page:
+        raise ValueError(f"{name}: pages must be apart by a multiple of {per_page} elements")
+    return t.stride(0)
+
+
+class Q8Attention(_Prepared):
+    """luce_q8kv_attn with its arguments marshalled once, for repeated calls over the same buffers: q
+    fp32 [T][Hq][128], ``out`` as q.  Each call takes what the views hold by then (lengths, blocks
+    sealed meanwhile, another tree, another window) and checks tensors that were replaced.  The
+    object owns its workspace (sized for the views' pages) unless one is given, so calls of
+    one object must not overlap on the GPU, and a graph that captured a call needs the object and
+    the call's caches alive."""
+
+    def __init__(self, q, views: Sequence[Q8View], n_kv_heads: int, scale: float, out=None, ws=None, stream=None):
+        import torch
+        _need(q, torch.float32, "q")
+        if q.dim() != 3:
+            raise ValueError("q: expected [T][Hq][128]")
+        T, Hq, D = q.shape
+        self.views = list(views)
+        if not self.views:
+            raise ValueError("views: expected at least one")
+        if not all(isinstance(v, Q8View) for v in self.views):
+            raise TypeError("views: expected Q8Views")
+        self.out = self._allocate(q.shape, torch.float32, q.device, stream) if out is None else out
+        _need(self.out, torch.float32, "out")
+        if self.out.shape != q.shape:
+            raise ValueError("out: expected q's shape")
+        n = len(self.views)
+        self._q, self._shape = q, (T, Hq, int(n_kv_heads), D)
+        self._vc = (Q8ViewC * n)()
+        self._items, self._caps, self._seen, self._trees = [self._vc[i] for i in range(n)], [0] * n, [None] * n, [None] * n
+        for i, v in enumerate(self.views):
+            self._take(i, v)
+        self._check_rows()
+        _same_device(q, self.out, ws)
+        self._own_ws = ws is None
+        if ws is None:
+            ws = self._allocate((self._ws_bytes(),), torch.uint8, q.device, stream)
+        _need(ws, torch.uint8, "ws")
+        args = (q.data_ptr(), self._vc, n, Hq, int(n_kv_heads), D, float(scale), self.out.data_ptr(), ws.data_ptr(), ws.numel())
+        self._ws_args = len(args) - 2
+        self._bind("luce_q8kv_attn", args, q.device, stream, (q, ws))
+
+    def _take(self, i, v):
+        """View i's tensors, then its sizes and tree."""
+        import torch
+        c, Hkv, name = self._items[i], self._shape[2], f"views[{i}]"
+        self._seen[i] = (i, v, *_NOTHING[:6], None)  # (until all is checked)
+        _kv_pair(v.k, v.v, 3, name)
+        if v.k.shape[0] != Hkv:
+            raise ValueError(f"{name}: {v.k.shape[0]} heads, expected {Hkv}")
+        if v.k_codes is None:
+            if v.v_codes is not None or v.scales is not None or v.table is not None:
+                raise ValueError(f"{name}: codes, scales and table come together")
+            c.k_codes = c.v_codes = c.scales = c.table = None
+            c.n_pages = c.page_stride = keys = 0
+        else:
+            _q8_pools(v.k_codes, v.v_codes, v.scales, (Hkv,), name)
+            per = PAGE_KEYS * HEAD_DIM
+            c.page_stride = _page_stride(v.k_codes, per, name + ".k_codes")
+            if _page_stride(v.v_codes, per, name + ".v_codes") != c.page_stride or \
+                    _page_stride(v.scales, 8, name + ".scales") * (per // 8) != c.page_stride:
+                raise ValueError(f"{name}: codes and scales must have their pages apart alike")
+            c.k_codes, c.v_codes, c.scales, c.n_pages = _ptr(v.k_codes), _ptr(v.v_codes), _ptr(v.scales), v.k_codes.shape[0]
+            if v.table is not None:
+                _need(v.table, torch.int32, name + ".table")
+            c.table = _ptr(v.table)
+            keys = (c.n_pages if v.table is None else v.table.numel()) * PAGE_KEYS
+        _same_device(self._q, v.k, v.v, v.k_codes, v.v_codes, v.scales, v.table)
+        self._caps[i] = min(keys, MAX_KEYS)
+        c.k, c.v, c.cap, c.head_stride, c.tok_stride = v.k.data_ptr(), v.v.data_ptr(), v.k.shape[1], v.k.stride(0), v.k.stride(1)
+        self._seen[i] = (i, v, v.k, v.v, v.k_codes, v.v_codes, v.scales, v.table, None)
+
+    def _take_sizes(self, i, v):
+        c, tree = self._items[i], self._trees[i]
+        kind = v.parent.__class__ if v.parent.__class__ in (int, list, tuple) else None
+        if tree is None or kind is None or kind is not tree[0] or v.parent != tree[1]:
+            nn, par = _tree(v.parent)
+            self._trees[i] = (kind, list(v.parent) if kind is list else v.parent, par)
+            c.n_nodes, c.parent = nn, par
+            self._rows = None
+        if v.sealed > self._caps[i]:
+            raise ValueError(f"views[{i}]: {v.sealed} sealed keys exceed the {self._caps[i]} that its pages hold")
+        if v.row0 != c.row0:
+            self._rows = None
+        c.sealed, c.len, c.row0, c.window, c.sinks = v.sealed, v.len, v.row0, v.window, v.sinks
+        self._seen[i] = (*self._seen[i][:-1], (v.sealed, v.len, v.row0, v.window, v.sinks, v.parent if kind is int else None))
+
+    def _check_rows(self):
+        for i, v in enumerate(self.views):
+            if self._seen[i][-1] is None:
+                self._take_sizes(i, v)
+        rows, T = max(c.row0 + c.n_nodes for c in self._items), self._shape[0]
+        if rows != T:
+            raise ValueError(f"q has {T} rows, the views name {rows}")
+        self._rows = rows
+
+    def _ws_bytes(self):
+        return max(256, luce_q8kv_attn_workspace_size(*self._shape, max(self._caps)))
+
+    def _retake(self, i, v):
+        """View i's tensors were replaced: more room is asked for where its cache grew."""
+        import torch
+        at = self._ws_args
+        self._take(i, v)
+        if self._own_ws and self._ws_bytes() > self._args[at + 1].value:
+            ws = self._allocate((self._ws_bytes(),), torch.uint8, self._q.device, self._keep[0])
+            self._args = (*self._args[:at], ctypes.c_void_p(ws.data_ptr()), ctypes.c_size_t(ws.numel()))
+
+    def __call__(self):
+        for i, v, k, vv, kc, vc, sc, table, now in self._seen:
+            if v.k is not k or v.v is not vv or v.k_codes is not kc or v.v_codes is not vc or v.scales is not sc or \
+                    v.table is not table:
+                now = self._retake(i, v)
+            # (a tree that is no int is compared where it is kept)
+            parent = v.parent
+            if parent.__class__ is not int:
+                tree = self._trees[i]
+                if tree[0] is None or parent.__class__ is not tree[0] or parent != tree[1]:
+                    now = None
+                parent = None
+            if now is None or now != (v.sealed, v.len, v.row0, v.window, v.sinks, parent):
+                self._take_sizes(i, v)
+        if self._rows is None:
+            self._check_rows()
+        self._call()
+        return self.out
+
+
+def luce_q8kv_attn_workspace_size(n_rows: int, Hq: int, Hkv: int, D: int, max_sealed: int) -> int:
+    return int(load_library().luce_q8kv_attn_workspace_size(n_rows, Hq, Hkv, D, max_sealed))
+
+
+def luce_q8kv_attn(q, views: Sequence[Q8View], n_kv_heads: int, scale: float, out=None, ws=None, stream=None):
+    """Attention of the views' draft trees over caches in 8 bits: fp32 q [T][Hq][128] against each
+    node's prefix (sealed blocks, tail), ancestors and itself, as far as its window reaches."""
+    return Q8Attention(q, views, n_kv_heads, scale, out, ws, stream)()
+
+
+class Q8Seal(_Prepared):
+    """luce_q8kv_seal with its arguments marshalled once: each call takes what the slots hold by
+    then, and checks tensors that were replaced.  The caller then continues with
+    ``slot.sealed + slot.len // 32 * 32`` keys in blocks and a tail of ``slot.len % 32``."""
+
+    def __init__(self, slots: Sequence[Q8Slot], stream=None):
+        self.slots = list(slots)
+        if not self.slots:
+            raise ValueError("slots: expected at least one")
+        if not all(isinstance(s, Q8Slot) for s in self.slots):
+            raise TypeError("slots: expected Q8Slots")
+        first = self.slots[0].k
+        L, Hkv = first.shape[:2]
+        n = len(self.slots)
+        self._first, self._heads = first, (L, Hkv)
+        self._sc = (Q8SlotC * n)()
+        self._items, self._caps, self._seen = [self._sc[i] for i in range(n)], [0] * n, [None] * n
+        for i, s in enumerate(self.slots):
+            self._take(i, s)
+        self._bind("luce_q8kv_seal", (self._sc, n, L, Hkv, HEAD_DIM), first.device, stream, None)
+
+    def _take(self, i, s):
+        """Slot i's tensors."""
+        import torch
+        (L, Hkv), c, name = self._heads, self._items[i], f"slots[{i}]"
+        self._seen[i] = (i, s, *_NOTHING[:6], None)  # (until all is checked)
+        _caches(s.k, s.v, L, Hkv, name)
+        _q8_pools(s.k_codes, s.v_codes, s.scales, (L, Hkv), name)
+        for t, w in ((s.k_codes, "k_codes"), (s.v_codes, "v_codes"), (s.scales, "scales")):
+            _need(t, t.dtype, f"{name}.{w}")
+        if s.table is not None:
+            _need(s.table, torch.int32, name + ".table")
+        _same_device(self._first, s.k, s.v, s.k_codes, s.v_codes, s.scales, s.table)
+        c.k, c.v, c.cap = s.k.data_ptr(), s.v.data_ptr(), s.k.shape[2]
+        c.k_codes, c.v_codes, c.scales, c.n_pages = _ptr(s.k_codes), _ptr(s.v_codes), _ptr(s.scales), s.k_codes.shape[0]
+        c.table = _ptr(s.table)
+        self._caps[i] = (c.n_pages if s.table is None else s.table.numel()) * PAGE_KEYS
+        self._seen[i] = (i, s, s.k, s.v, s.k_codes, s.v_codes, s.scales, s.table, None)
+
+    def _take_sizes(self, i, s):
+        if s.sealed + s.len // Q8_BLOCK * Q8_BLOCK > self._caps[i]:
+            raise ValueError(f"slots[{i}]: its pages hold {self._caps[i]} keys, {s.sealed} + {s.len // Q8_BLOCK * Q8_BLOCK} come")
+        c = self._items[i]
+        c.len, c.sealed = s.len, s.sealed
+        self._seen[i] = (*self._seen[i][:-1], (s.len, s.sealed))
+
+    def __call__(self):
+        for i, s, k, v, kc, vc, sc, table, now in self._seen:
+            if s.k is not k or s.v is not v or s.k_codes is not kc or s.v_codes is not vc or s.scales is not sc or \
+                    s.table is not table:
+                now = self._take(i, s)
+            if (s.len, s.sealed) != now:
+                self._take_sizes(i, s)
+        self._call()
+
+
+def luce_q8kv_seal(slots: Sequence[Q8Slot], stream=None):
+    """Turn the whole blocks of 32 tokens of the slots' tails into 8-bit codes behind their sealed
+    keys; the rows that are left move to the tails' front."""
+    Q8Seal(slots, stream)()
+
+
+def rope_sections(sections: Sequence[int], interleaved: bool = False) -> List[int]:
+    """The axis of each of the 64 pairs for ``sections`` pairs per axis (64 in all): the sections one
+    after the other, or in turn (0, 1, 2, 0, 1, 2, .. while an axis has pairs left)."""
+    if sum(sections) != HEAD_DIM // 2 or min(sections) < 0:
+        raise ValueError(f"sections: expected {HEAD_DIM // 2} pairs in all, got {list(sections)}")
+    if not interleaved:
+        return [a for a, n in enumerate(sections) for _ in range(n)]
+    left, out = list(sections), []
+    while len(out) < HEAD_DIM // 2:
+        for a in range(len(left)):
+            if left[a] > 0:
+                left[a] -= 1
+                out.append(a)
+    return out
+
+
+class QkNormRope(_Prepared):
+    """luce_qk_norm_rope with its arguments marshalled once: qkv fp32 [T][(Hq + 2 Hkv) 128] (rows may
+    be further apart), ``pos`` int32 [T] or [n_axes][T], ``pair_axis`` the axis of each of the 64 pairs
+    (``rope_sections``), gammas fp32 [128] or None; views as for luce_kv_append, with any
+    n_q.  q comes back in ``out`` (fp32 [T][Hq][128]), k and v are appended.  Each call takes what the views
+    hold by then and checks caches that were replaced."""
+
+    def __init__(self, qkv, views: Sequence[SeqView], n_q_heads: int, pos, theta: float, q_gamma=None, k_gamma=None,
+                 eps: float = 1e-6, pair_axis=None, out=None, stream=None):
+        import torch
+        if not isinstance(qkv, torch.Tensor) or qkv.dtype != torch.float32 or not qkv.is_cuda:
+            raise TypeError(f"qkv: expected a CUDA {torch.float32} tensor")
+        self.views = list(views)
+        if not self.views:
+            raise ValueError("views: expected at least one")
+        T, Hq, Hkv = qkv.shape[0], int(n_q_heads), self.views[0].k.shape[0]
+        if qkv.dim() != 2 or qkv.shape[1] != (Hq + 2 * Hkv) * HEAD_DIM or qkv.stride(1) != 1:
+            raise ValueError(f"qkv: expected [T][({Hq} + 2 * {Hkv}) * 128], the last dim contiguous")
+        _need(pos, torch.int32, "pos")
+        axes = 1 if pos.dim() == 1 else pos.shape[0]
+        if pos.dim() > 2 or pos.shape[-1] != T:
+            raise ValueError(f"pos: expected [{T}] or [n_axes][{T}]")
+        for g, w in ((q_gamma, "q_gamma"), (k_gamma, "k_gamma")):
+            if g is not None:
+                _need(g, torch.float32, w)
+                if g.shape != (HEAD_DIM,):
+                    raise ValueError(f"{w}: expected [128]")
+        if pair_axis is not None:
+            pair_axis = [int(a) for a in pair_axis]
+            if len(pair_axis) != HEAD_DIM // 2 or not all(0 <= a < axes for a in pair_axis):
+                raise ValueError(f"pair_axis: expected 64 numbers below {axes}")
+            pair_axis = (ctypes.c_uint8 * (HEAD_DIM // 2))(*pair_axis)
+        self.out = self._allocate((T, Hq, HEAD_DIM), torch.float32, qkv.device, stream) if out is None else out
+        _need(self.out, torch.float32, "out")
+        if self.out.shape != (T, Hq, HEAD_DIM):
+            raise ValueError(f"out: expected [{T}][{Hq}][128]")
+        _same_device(qkv, self.out, pos, q_gamma, k_gamma)
+        n = len(self.views)
+        self._T, self._Hkv, self._first = T, Hkv, qkv
+        self._vc = (SeqViewC * n)()
+        self._items, self._seen = [self._vc[i] for i in range(n)], [None] * n
+        for i, v in enumerate(self.views):
+            self._take(i, v)
+        ld = qkv.stride(0) if T > 1 else qkv.shape[1]
+        args = (qkv.data_ptr(), ld, self._vc, n, Hq, Hkv, HEAD_DIM, _ptr(q_gamma), _ptr(k_gamma), float(eps), pos.data_ptr(), axes,
+                None if pair_axis is None else ctypes.addressof(pair_axis), float(theta), self.out.data_ptr())
+        self._bind("luce_qk_norm_rope", args, qkv.device, stream, (qkv, pos, q_gamma, k_gamma, pair_axis))
+
+    def _take(self, i, v):
+        """View i's caches."""
+        c, name = self._items[i], f"views[{i}]"
+        self._seen[i] = (i, v, None, None, None)  # (until all is checked)
+        _kv_pair(v.k, v.v, 3, name)
+        if v.k.shape[0] != self._Hkv:
+            raise ValueError(f"{name}: {v.k.shape[0]} heads, expected {self._Hkv}")
+        _same_device(self._first, v.k, v.v)
+        c.k, c.v, c.cap, c.head_stride, c.tok_stride = v.k.data_ptr(), v.v.data_ptr(), v.k.shape[1], v.k.stride(0), v.k.stride(1)
+        self._seen[i] = (i, v, v.k, v.v, None)
+
+    def __call__(self):
+        for i, v, k, vv, now in self._seen:
+            if v.k is not k or v.v is not vv:
+                now = self._take(i, v)
+            if (v.len, v.n_q, v.row0) != now:
+                c = self._items[i]
+                c.len, c.n_q, c.row0 = v.len, v.n_q, v.row0
+                rows = max(x.row0 + x.n_q for x in self.views)
+                if rows != self._T:
+                    raise ValueError(f"qkv has {self._T} rows, the views name {rows}")
+                self._seen[i] = (i, v, v.k, v.v, (v.len, v.n_q, v.row0))
+        self._call()
+        return self.out
+
+
+def luce_qk_norm_rope(qkv, views: Sequence[SeqView], n_q_heads: int, pos, theta: float, q_gamma=None, k_gamma=None,
+                      eps: float = 1e-6, pair_axis=None, out=None, stream=None):
+    """Per-head norms of q and k, RoPE on one or several position axes and the K/V append of a
+    projection's rows in one pass; returns q (fp32 [T][Hq][128])."""
+    return QkNormRope(qkv, views, n_q_heads, pos, theta, q_gamma, k_gamma, eps, pair_axis, out, stream)()

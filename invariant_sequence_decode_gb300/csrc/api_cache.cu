@@ -33,11 +33,6 @@ int luce::check_apart(const ByteRange* r, int n, const char* who)
     return LUCE_OK;
 }
 
-static ByteRange range_of(const void* p, int64_t bytes, int slot, const char* what, bool written, int pair = 0)
-{
-    return ByteRange{(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes, slot, what, written, pair};
-}
-
 // ------------------------------------------------------------ trees
 
 int luce::tree_path(const int32_t* parent, int n_nodes, TreeRow* rows, int view, int row0, const char* who)
@@ -233,9 +228,7 @@ int luce_tree_attn_paged(const float* q, const luce_pagedtreeview* views, int n_
 static const char* const kPoolK = "K pool";
 static const char* const kPoolV = "V pool";
 
-// Slots may share a pool, each with its own rows; pools that are not one overlap
-// nothing.
-static void add_pool(ByteRange* r, int* nr, const void* p, int64_t bytes, int slot, const char* what)
+void luce::add_pool(ByteRange* r, int* nr, const void* p, int64_t bytes, int slot, const char* what)
 {
     const ByteRange n = range_of(p, bytes, slot, what, true);
     for (int i = 0; i < *nr; ++i)
@@ -246,7 +239,7 @@ static void add_pool(ByteRange* r, int* nr, const void* p, int64_t bytes, int sl
     r[(*nr)++] = n;
 }
 
-static int check_layers(int n_seq, int n_layers, int Hkv, int D, const void* slots, const char* who)
+int luce::check_layers(int n_seq, int n_layers, int Hkv, int D, const void* slots, const char* who)
 {
     REQUIRE(slots, LUCE_EINVAL, "%s: null slots", who);
     REQUIRE(n_seq >= 1 && n_seq <= LUCE_MAX_SEQ, LUCE_EINVAL, "%s: n_seq=%d outside 1..%d", who, n_seq, LUCE_MAX_SEQ);

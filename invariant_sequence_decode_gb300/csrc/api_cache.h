@@ -3,7 +3,9 @@
 
 #include <stdint.h>
 
+#include "../../include/luce.h"
 #include "cache.h"
+#include "q8kv.h"
 
 namespace luce {
 
@@ -26,5 +28,21 @@ struct ByteRange {
     int pair;
 };
 int check_apart(const ByteRange* r, int n, const char* who);
+
+static inline ByteRange range_of(const void* p, int64_t bytes, int slot, const char* what, bool written, int pair = 0)
+{
+    return ByteRange{(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes, slot, what, written, pair};
+}
+
+// Slots may share a pool, each with its own rows; pools that are not one overlap
+// nothing.
+void add_pool(ByteRange* r, int* nr, const void* p, int64_t bytes, int slot, const char* what);
+
+// Sizes of an entry point over the caches of every layer.
+int check_layers(int n_seq, int n_layers, int Hkv, int D, const void* slots, const char* who);
+
+// A view of a cache in 8 bits, checked and entered into the batch; covered: the
+// rows that earlier views claimed.
+int add_q8kv_view(Q8Batch& b, int s, const luce_q8kv_view& v, int Hkv, bool* covered, const char* who);
 
 }  // namespace luce

@@ -12,8 +12,12 @@
 // error.  The rotation is fp32 with explicit rounding.  One CTA of 64 threads
 // per (row, head): thread i owns pair i.  The decode step applies the same
 // rotation and append in the epilogue of its q|k|v projection (matvec.cu).
+#include <algorithm>
+
+#include "cache.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "q8kv.h"
 
 namespace luce {
 
@@ -100,6 +104,122 @@ cudaError_t launch_kv_append(const float* k, const float* v, int64_t ld, int Hkv
                              cudaStream_t s)
 {
     const cudaError_t e = launch_pdl(kv_append_kernel, dim3(rows.n_rows), dim3(256), s, k, v, ld, Hkv, rows);
+    count_launches(1);
+    return e;
+}
+
+// Norms of q and k per head, rotation, and append of a projection's rows in one
+// pass.  Head x of row t becomes y = x / sqrt(mean(x^2) + eps) * gamma (as it is
+// without a gamma), and the pair (y_i, y_(i+64)) rotates by the row's position on
+// the pair's axis times theta^(-i/64); v heads are only rounded.
+// Bound by memory (read once, written once), so what is shared is kept small:
+// a row's 64 cosines and sines are formed once per CTA into shared memory, and
+// 16 lanes take a head, four pairs each as two 16-byte loads.  All loads of a
+// lane's heads are under way before the angles are: kProjectAhead heads of 16
+// at a time.  Sums of squares: a lane's eight in order, then lanes by an xor
+// butterfly, so a row's bits do not depend on the other rows or the grid; without
+// gammas and with one axis they are those of rope_posvec_kernel and kv_append_kernel.
+constexpr int kProjectAhead = 4;
+
+__global__ void __launch_bounds__(256)
+qk_norm_rope_kernel(const float* qkv, int64_t ld, int Hq, int Hkv, const __grid_constant__ AppendViews views,
+                    const float* q_gamma, const float* k_gamma, float eps, const int32_t* pos, int T, PairAxes axes,
+                    const __grid_constant__ RopeFreq f, float* __restrict__ q)
+{
+    __shared__ __align__(16) float cs[2][kHeadDim / 2];
+    pdl_trigger();
+    const int t = blockIdx.x, tid = threadIdx.x, part = tid & 15, heads = Hq + 2 * Hkv;
+    const int step = 16 * gridDim.y;
+    int v = 0;
+    while (v + 1 < views.n_view && (t < views.view[v].row0 || t >= views.view[v].row0 + views.view[v].n)) ++v;
+    const AppendView& to = views.view[v];
+    const int64_t at = (int64_t)(to.at0 + t - to.row0) * to.tok_stride;
+    const float* row = qkv + (int64_t)t * ld + 4 * part;
+    pdl_wait();
+    bool turned = false;
+    for (int h0 = blockIdx.y * 16 + (tid >> 4); h0 - (tid >> 4) < heads; h0 += kProjectAhead * step) {
+        float4 a[kProjectAhead], b[kProjectAhead];
+#pragma unroll
+        for (int e = 0; e < kProjectAhead; ++e) {
+            const int h = h0 + e * step;
+            a[e] = b[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (h < heads) {
+                a[e] = ld_placed_cs_f4(row + (int64_t)h * kHeadDim);
+                b[e] = ld_placed_cs_f4(row + (int64_t)h * kHeadDim + kHeadDim / 2);
+            }
+        }
+        if (!turned) {
+            if (tid < kHeadDim / 2) {
+                const int axis = axes.bits[tid >> 4] >> (2 * (tid & 15)) & 3;
+                const float2 x = rope_cs(ld_placed_i(pos + (int64_t)axis * T + t), f.inv[tid]);
+                cs[0][tid] = x.x;
+                cs[1][tid] = x.y;
+            }
+            __syncthreads();
+            turned = true;
+        }
+        const float4 c = *reinterpret_cast<const float4*>(&cs[0][4 * part]);
+        const float4 s = *reinterpret_cast<const float4*>(&cs[1][4 * part]);
+#pragma unroll
+        for (int e = 0; e < kProjectAhead; ++e) {
+            const int h = h0 + e * step;
+            if (h - (tid >> 4) >= heads) break;  // (the same for all threads of the CTA)
+            float4 x = a[e], y = b[e];
+            const float* gamma = h < Hq ? q_gamma : h < Hq + Hkv ? k_gamma : nullptr;
+            // (all lanes of the warp come here: the butterfly needs them)
+            float sq = __fmul_rn(x.x, x.x);
+            sq = __fmaf_rn(x.y, x.y, sq);
+            sq = __fmaf_rn(x.z, x.z, sq);
+            sq = __fmaf_rn(x.w, x.w, sq);
+            sq = __fmaf_rn(y.x, y.x, sq);
+            sq = __fmaf_rn(y.y, y.y, sq);
+            sq = __fmaf_rn(y.z, y.z, sq);
+            sq = __fmaf_rn(y.w, y.w, sq);
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) sq = __fadd_rn(sq, __shfl_xor_sync(0xffffffffu, sq, o));
+            if (gamma) {
+                const float inv = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fmul_rn(sq, 1.0f / kHeadDim), eps)));
+                const float4 g0 = ld_placed_f4(gamma + 4 * part), g1 = ld_placed_f4(gamma + kHeadDim / 2 + 4 * part);
+                x.x = __fmul_rn(__fmul_rn(x.x, inv), g0.x);
+                x.y = __fmul_rn(__fmul_rn(x.y, inv), g0.y);
+                x.z = __fmul_rn(__fmul_rn(x.z, inv), g0.z);
+                x.w = __fmul_rn(__fmul_rn(x.w, inv), g0.w);
+                y.x = __fmul_rn(__fmul_rn(y.x, inv), g1.x);
+                y.y = __fmul_rn(__fmul_rn(y.y, inv), g1.y);
+                y.z = __fmul_rn(__fmul_rn(y.z, inv), g1.z);
+                y.w = __fmul_rn(__fmul_rn(y.w, inv), g1.w);
+            }
+            if (h < Hq + Hkv) {
+                rope_rotate(x.x, y.x, c.x, s.x);
+                rope_rotate(x.y, y.y, c.y, s.y);
+                rope_rotate(x.z, y.z, c.z, s.z);
+                rope_rotate(x.w, y.w, c.w, s.w);
+            }
+            if (h >= heads) continue;
+            if (h < Hq) {
+                float* o = q + ((int64_t)t * Hq + h) * kHeadDim + 4 * part;
+                *reinterpret_cast<float4*>(o) = x;
+                *reinterpret_cast<float4*>(o + kHeadDim / 2) = y;
+            } else {
+                __half* o = h < Hq + Hkv ? to.k + (h - Hq) * to.head_stride : to.v + (h - Hq - Hkv) * to.head_stride;
+                o += at + 4 * part;
+                __half2 w[4] = {__floats2half2_rn(x.x, x.y), __floats2half2_rn(x.z, x.w), __floats2half2_rn(y.x, y.y),
+                                __floats2half2_rn(y.z, y.w)};
+                *reinterpret_cast<uint2*>(o) = *reinterpret_cast<uint2*>(&w[0]);
+                *reinterpret_cast<uint2*>(o + kHeadDim / 2) = *reinterpret_cast<uint2*>(&w[2]);
+            }
+        }
+    }
+}
+
+cudaError_t launch_qk_norm_rope(const float* qkv, int64_t ld, int T, int Hq, int Hkv, const AppendViews& views,
+                                const float* q_gamma, const float* k_gamma, float eps, const int32_t* pos,
+                                const PairAxes& axes, const RopeFreq& f, float* q, cudaStream_t s)
+{
+    // few rows: 16 heads a CTA, so that a row's heads go at once; many: a row a CTA, its angles formed once
+    const int groups = T < 152 ? std::min((Hq + 2 * Hkv + 15) / 16, 65535) : 1;
+    const cudaError_t e = launch_pdl(qk_norm_rope_kernel, dim3(T, groups), dim3(256), s, qkv, ld, Hq, Hkv, views, q_gamma,
+                                     k_gamma, eps, pos, T, axes, f, q);
     count_launches(1);
     return e;
 }
