@@ -19,6 +19,7 @@
 #include "cache.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "q8kv.h"
 
 using namespace luce;
 
@@ -99,10 +100,11 @@ uint64_t luce_launch_count(void) { return g_launches.load(std::memory_order_rela
 int luce_wait_timeouts(uint32_t* count, int reset)
 {
     REQUIRE(count, LUCE_EINVAL, "wait_timeouts: null count");
-    uint32_t rings = 0, trees = 0;
+    uint32_t rings = 0, trees = 0, codes = 0;
     cudaError_t e = read_wait_timeouts(&rings, reset != 0);
     if (e == cudaSuccess) e = read_tree_wait_timeouts(&trees, reset != 0);
-    if (e == cudaSuccess) *count = rings + trees;
+    if (e == cudaSuccess) e = read_q8kv_wait_timeouts(&codes, reset != 0);
+    if (e == cudaSuccess) *count = rings + trees + codes;
     return cuda_status(e, "wait_timeouts");
 }
 

@@ -18,6 +18,7 @@
 #include "kernels.h"
 #include "q8kv.h"
 #include "ring.cuh"
+#include "tensor.cuh"
 
 namespace luce {
 
@@ -35,7 +36,9 @@ struct Q8Scale {
 
 int q8kv_max_chunks(int max_sealed, int Hkv) { return max_sealed > 0 ? tree_max_chunks(std::max(max_sealed, kQ8Page), Hkv) : 0; }
 
-size_t q8kv_part_bytes(int64_t n_part) { return (size_t)n_part * (kHeadDim + 2) * sizeof(float); }
+// A chunk's row of results: part_o [row][128] and part_ml [row][8] = (m, three unused,
+// l of the tiles' first to fourth block), the sums times 2^15.
+size_t q8kv_part_bytes(int64_t n_part) { return (size_t)n_part * (kHeadDim + 8) * sizeof(float); }
 
 int64_t q8kv_chunks(Q8Batch& b, int Hq, int Hkv)
 {
@@ -64,134 +67,668 @@ int64_t q8kv_chunks(Q8Batch& b, int Hq, int Hkv)
 // The key that tile t of a view's starts with.
 __device__ __forceinline__ int q8_tile_key(const Q8View& v, int t) { return (t < v.front ? t : t - v.front + v.back) * kQ8Page; }
 
-__device__ __forceinline__ float q8_exp2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // ---------------------------------------------------------------- chunks
 
-// One CTA of 128 threads a chunk and KV head; rows in groups of 32.  Scores: a key
-// a thread.  Sums: a dim a thread.
-constexpr int kQ8Rows = 32;
+// 16 warps: 8 on scores, weights and sums, 4 that turn codes into f16, one that
+// feeds the tiles, one that issues the products, one that holds tensor memory.
+// 512 threads are launched with 128 registers each; the warps on scores get 208,
+// the turning ones 56, the last four 40: 256 * 208 + 128 * 56 + 128 * 40 = 65,536.
+constexpr int kQ8Threads = 512;
+constexpr int kQ8ScaleSlots = 16;  // tiles whose scales are held: more than lie between the producer and the weights
 
-__global__ void __launch_bounds__(128)
-q8kv_chunk_kernel(const float* q, const __grid_constant__ Q8Batch b, int Hq, int Hkv, Q8Scale scale,
-                  float* __restrict__ part_o, float* __restrict__ part_ml)
+__device__ unsigned int g_q8kv_wait_timeouts;
+
+// Sizes of a kernel for up to 16 NG rows of a KV head.
+template <int NG>
+struct Q8Shape {
+    static constexpr int kRows = 16 * NG;                      // columns of the products
+    static constexpr int kStages = NG == 1 ? 6 : NG == 2 ? 5 : NG == 3 ? 4 : NG == 5 ? 3 : 2;  // tiles of K, and of V, in flight
+    static constexpr int kTurned = NG <= 5 ? 2 : 1;            // tiles of K, and of V, in tensor memory
+    static constexpr int kWeights = NG <= 5 ? 2 : 1;           // tiles of weights in shared memory
+    static constexpr bool kTwice = NG > 3;                     // scores are read twice, not held while O is added
+    static constexpr int kPart = kRows * kHeadDim * 2;         // bytes of one part of q, or of the weights
+    static constexpr uint32_t kColK = 0, kColV = 64 * kTurned, kColS = 128 * kTurned, kColO = kColS + 2 * kRows;
+    static constexpr int kBytes = kStages * 2 * kQ8PageBytes + (2 + 2 * kWeights) * kPart + 1024;
+    static_assert(kColO + kRows <= 512, "tensor memory");
+};
+
+struct Q8Maps {
+    CUtensorMap k[4], v[4];
+};
+
+template <int NG>
+struct Q8Bars {
+    using S = Q8Shape<NG>;
+    uint64_t k_full[S::kStages], k_empty[S::kStages], v_full[S::kStages], v_empty[S::kStages];
+    uint64_t ka_full[S::kTurned], ka_free[S::kTurned];   // K of a tile is f16 in tensor memory; has been multiplied
+    uint64_t va_full[S::kTurned], va_free[S::kTurned];
+    uint64_t s_full[2], s_free[2];                       // S of a tile is complete; has been read
+    uint64_t p_full[S::kWeights], p_free[S::kWeights];   // its weights are in place; have been multiplied
+    uint64_t o_full, o_free;                             // O of a tile is complete; has been read
+    uint64_t q_full;                                     // q's parts are in place
+    uint64_t sc_full[kQ8ScaleSlots];                     // a tile's scales are there
+    uint64_t done;                                       // every product that was issued is complete
+};
+
+// Chunks of one (view, KV head) that a CTA takes one after the other: `chunks` of
+// them from number c on, tiles t0 .. t0 + tiles - 1, in the order view, head, chunk.
+struct Q8Run {
+    int view, g, c, chunks, tiles, t0;
+};
+
+__device__ __forceinline__ Q8Run q8_run(const Q8Batch& b, int Hkv, int u, int end)
 {
-    __shared__ __align__(16) float qs[kQ8Rows][kHeadDim];
-    __shared__ float ps[kQ8Rows][kQ8Page];
-    __shared__ float ms[kQ8Rows], ls[kQ8Rows], al[kQ8Rows];
-    pdl_trigger();
-    int u = blockIdx.x, vi = 0;
-    while (vi + 1 < b.n_view && u >= Hkv * b.view[vi].n_chunk) u -= Hkv * b.view[vi++].n_chunk;
-    const Q8View& v = b.view[vi];
-    const int c = u / Hkv, g = u % Hkv, GQ = Hq / Hkv, R = v.n_nodes * GQ, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int t0 = c * v.chunk, t1 = min(t0 + v.chunk, v.n_tile), total = v.sealed + v.tail;
-    const int64_t pr = v.part0 + ((int64_t)c * Hkv + g) * R;
-    pdl_wait();
-    for (int r0 = 0; r0 < R; r0 += kQ8Rows) {
-        const int n = min(kQ8Rows, R - r0);
-        __syncthreads();
-        for (int r = 0; r < n; ++r) {
-            const int i = r0 + r;
-            qs[r][tid] = __fmul_rn(ld_placed_f(q + ((int64_t)(v.row0 + i / GQ) * Hq + g * GQ + i % GQ) * kHeadDim + tid), scale.sign);
-        }
-        if (tid < kQ8Rows) {
-            ms[tid] = -INFINITY;
-            ls[tid] = 0.0f;
-        }
-        float o[kQ8Rows];
-#pragma unroll
-        for (int r = 0; r < kQ8Rows; ++r) o[r] = 0.0f;
-        for (int t = t0; t < t1; ++t) {
-            const int key0 = q8_tile_key(v, t), page = v.table ? ld_placed_i(v.table + key0 / kQ8Page) : key0 / kQ8Page;
-            const bool in = page >= 0 && page < v.n_pages;
-            const int64_t at = (int64_t)page * v.page_stride + (int64_t)g * kQ8PageBytes + tid * 128;
-            const float* sc = v.scales + (int64_t)page * v.scale_stride + g * kQ8PageScales;
-            __syncthreads();
-            {
-                uint4 x[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = in ? ld_placed_u4(v.k_codes + at + 16 * e) : make_uint4(0, 0, 0, 0);
-                const int key = key0 + tid;
-                const float ks = in && key < v.sealed ? __fmul_rn(ld_placed_f(sc + warp), scale.log2) : 0.0f;
-                for (int r = 0; r < n; ++r) {
-                    float dot = 0.0f;
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const uint32_t w = reinterpret_cast<const uint32_t*>(x)[e];
-                        const float4 y = *reinterpret_cast<const float4*>(&qs[r][4 * e]);
-                        dot = __fmaf_rn(y.x, (float)(int8_t)w, dot);
-                        dot = __fmaf_rn(y.y, (float)(int8_t)(w >> 8), dot);
-                        dot = __fmaf_rn(y.z, (float)(int8_t)(w >> 16), dot);
-                        dot = __fmaf_rn(y.w, (float)(int8_t)(w >> 24), dot);
-                    }
-                    const int p = total + b.row[v.row0 + (r0 + r) / GQ].n_path - 1;
-                    const bool seen = key < v.sealed && (v.window == 0 || key < v.sinks || p - key < v.window);
-                    ps[r][tid] = seen ? __fmul_rn(dot, ks) : -INFINITY;
-                }
-            }
-            __syncthreads();
-            for (int r = warp; r < n; r += 4) {
-                float x[4], top = ms[r];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[e] = ps[r][lane + 32 * e];
-                    top = fmaxf(top, x[e]);
-                }
-                top = warp_max(top);
-                const float ref = top == -INFINITY ? 0.0f : top;
-                float sum = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[e] = q8_exp2(__fadd_rn(__fsub_rn(x[e], ref), kQ8Up));
-                    ps[r][lane + 32 * e] = x[e];
-                    sum = __fadd_rn(sum, x[e]);
-                }
-                sum = warp_sum_butterfly(sum);
-                __syncwarp();
-                if (lane == 0) {
-                    al[r] = q8_exp2(__fsub_rn(ms[r], ref));
-                    ls[r] = __fmaf_rn(ls[r], al[r], sum);
-                    ms[r] = top;
-                }
-            }
-            __syncthreads();
-            uint4 x[8];
-            float vs[4];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = in ? ld_placed_u4(v.v_codes + at + 16 * e) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) vs[e] = in && key0 + 32 * e < v.sealed ? ld_placed_f(sc + 4 + e) : 0.0f;
-#pragma unroll
-            for (int r = 0; r < kQ8Rows; ++r) {
-                if (r >= n) break;
-                o[r] = __fmul_rn(o[r], al[r]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float sum = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t w = reinterpret_cast<const uint32_t*>(x)[8 * e + i];
-                        const float* p = &ps[r][32 * e + 4 * i];
-                        sum = __fmaf_rn(p[0], (float)(int8_t)w, sum);
-                        sum = __fmaf_rn(p[1], (float)(int8_t)(w >> 8), sum);
-                        sum = __fmaf_rn(p[2], (float)(int8_t)(w >> 16), sum);
-                        sum = __fmaf_rn(p[3], (float)(int8_t)(w >> 24), sum);
-                    }
-                    o[r] = __fmaf_rn(sum, vs[e], o[r]);
-                }
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int r = 0; r < kQ8Rows; ++r)
-            if (r < n) part_o[(pr + r0 + r) * kHeadDim + tid] = o[r];
-        if (tid < n) *reinterpret_cast<float2*>(part_ml + 2 * (pr + r0 + tid)) = make_float2(ms[tid], ls[tid]);
+    Q8Run t;
+    const int u0 = u;
+    t.view = 0;
+    while (t.view + 1 < b.n_view && u >= Hkv * b.view[t.view].n_chunk) u -= Hkv * b.view[t.view++].n_chunk;
+    const Q8View& v = b.view[t.view];
+    t.g = u / v.n_chunk;
+    t.c = u - t.g * v.n_chunk;
+    t.chunks = min(v.n_chunk - t.c, end - u0);
+    t.t0 = t.c * v.chunk;
+    t.tiles = min(t.chunks * v.chunk, v.n_tile - t.t0);
+    return t;
+}
+
+// The CTA's runs: chunks u0, u0 + step, .. below u1, or one run of neighbours (step 0).
+struct Q8Share {
+    int u0, u1, step;
+};
+
+template <typename F>
+__device__ __forceinline__ void q8_each_run(const Q8Batch& b, int Hkv, const Q8Share& w, F f)
+{
+    for (int u = w.u0, next; u < w.u1; u = next) {
+        const Q8Run t = q8_run(b, Hkv, u, w.step ? u + 1 : w.u1);
+        next = w.step ? u + w.step : u + t.chunks;
+        if (!f(t)) return;
     }
+}
+
+// 16 lanes by 8 columns of tensor memory: v[0], v[1] are lane t / 4's columns 2 (t % 4)
+// and the next, v[2], v[3] lane t / 4 + 8's.  Not there before tm_loaded.
+__device__ __forceinline__ void tm_ld_frag(uint32_t addr, float* v)
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                 : "r"(addr));
+}
+template <int N>
+__device__ __forceinline__ void tm_loaded(float* v)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));  // (no use of them moves ahead of the wait)
+}
+
+// Four 8 x 8 matrices of f16 pairs, stored turned: a lane's address is a row of what is
+// stored, a column of what the registers hold.
+__device__ __forceinline__ void st_matrix_turned(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
+// Four codes as f16 pairs, exactly: 1152 + code by its bits, less 1152.
+__device__ __forceinline__ void q8_half_codes(uint32_t w, uint32_t& lo, uint32_t& hi)
+{
+    w ^= 0x80808080u;
+    const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+    asm("{ .reg .b32 n; mov.b32 n, 0x64806480; sub.rn.f16x2 %0, %1, n; }" : "=r"(lo) : "r"(a));
+    asm("{ .reg .b32 n; mov.b32 n, 0x64806480; sub.rn.f16x2 %0, %1, n; }" : "=r"(hi) : "r"(b));
+}
+
+// The producer: tiles and scales of the CTA's runs, in order.  Returns the tiles
+// issued.
+template <int NG>
+__device__ int q8_produce(const Q8Maps& maps, const Q8Batch& b, int Hkv, const Q8Share& w, uint8_t* tiles, float (*scales)[8],
+                          Q8Bars<NG>& bar)
+{
+    constexpr int kStages = Q8Shape<NG>::kStages;
+    unsigned int* late = &g_q8kv_wait_timeouts;
+    int i = 0;
+    pdl_wait();
+    pdl_trigger();
+    q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
+        const Q8View& v = b.view[t.view];
+        auto page_of = [&](int k) {
+            const int span = q8_tile_key(v, t.t0 + k) / kQ8Page;
+            return v.table ? ld_placed_i(v.table + span) : span;
+        };
+        int next = page_of(0);
+        for (int k = 0; k < t.tiles; ++k, ++i) {
+            const int st = i % kStages, sl = i % kQ8ScaleSlots;
+            const uint32_t free = ((i / kStages) & 1) ^ 1;
+            int page = next;
+            if (k + 1 < t.tiles) next = page_of(k + 1);  // (on its way while this tile's place becomes free)
+            const bool in = page >= 0 && page < v.n_pages;
+            if (!in) page = v.n_pages;                   // outside the map: zeros
+            uint8_t* kt = tiles + st * 2 * kQ8PageBytes;
+            if (!mbar_wait(&bar.k_empty[st], free, late)) return false;
+            if (in) {
+                mbar_expect_tx(&bar.sc_full[sl], 32);
+                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], 32, [%2];" ::"r"(
+                                 smem_addr(scales[sl])),
+                             "l"(v.scales + page * v.scale_stride + t.g * kQ8PageScales), "r"(smem_addr(&bar.sc_full[sl]))
+                             : "memory");
+            } else {
+                for (int e = 0; e < 8; ++e) scales[sl][e] = 0.0f;
+                mbar_arrive(&bar.sc_full[sl]);
+            }
+            mbar_expect_tx(&bar.k_full[st], kQ8PageBytes);
+            tma_load_4d(kt, &maps.k[t.view], 0, 0, t.g, page, &bar.k_full[st]);
+            if (!mbar_wait(&bar.v_empty[st], free, late)) {
+                ring_drain<kStages>(bar.k_full, i + 1, late);
+                ring_drain<kQ8ScaleSlots>(bar.sc_full, i + 1, late);
+                return false;
+            }
+            mbar_expect_tx(&bar.v_full[st], kQ8PageBytes);
+            tma_load_4d(kt + kQ8PageBytes, &maps.v[t.view], 0, 0, t.g, page, &bar.v_full[st]);
+        }
+        return true;
+    });
+    return i;
+}
+
+// One operand's codes, [lane's row][128], into tensor memory as f16.
+__device__ __forceinline__ void q8_turn(const uint8_t* tile, int row, uint32_t to)
+{
+    const uint8_t* p = tile + row * 128;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        uint32_t o[32];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint4 x = lds128(p + (((4 * half + e) ^ (row & 7)) << 4));
+            q8_half_codes(x.x, o[8 * e], o[8 * e + 1]);
+            q8_half_codes(x.y, o[8 * e + 2], o[8 * e + 3]);
+            q8_half_codes(x.z, o[8 * e + 4], o[8 * e + 5]);
+            q8_half_codes(x.w, o[8 * e + 6], o[8 * e + 7]);
+        }
+        tm_st32(to + 32 * half, o);
+    }
+    tm_wait_st();
+}
+
+// The turning warps: K and V of every tile, a row of 128 codes per thread.
+template <int NG>
+__device__ void q8_turn_tiles(int n, const uint8_t* tiles, uint32_t tmem, int quad, int lane, Q8Bars<NG>& bar)
+{
+    using S = Q8Shape<NG>;
+    unsigned int* late = &g_q8kv_wait_timeouts;
+    const int row = 32 * quad + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+    for (int i = 0; i < n; ++i) {
+        const int st = i % S::kStages, to = i % S::kTurned;
+        const uint32_t full = (i / S::kStages) & 1, free = ((i / S::kTurned) & 1) ^ 1;
+        const uint8_t* kt = tiles + st * 2 * kQ8PageBytes;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bar.k_full[st], full, late) && mbar_wait(&bar.ka_free[to], free, late))) return;
+        tm_after();
+        q8_turn(kt, row, lanes + S::kColK + 64 * to);
+        warp_arrive(&bar.ka_full[to]);
+        if (lane == 0) mbar_arrive(&bar.k_empty[st]);
+        if (!__all_sync(0xffffffffu, mbar_wait(&bar.v_full[st], full, late) && mbar_wait(&bar.va_free[to], free, late))) return;
+        tm_after();
+        q8_turn(kt + kQ8PageBytes, row, lanes + S::kColV + 64 * to);
+        warp_arrive(&bar.va_full[to]);
+        if (lane == 0) mbar_arrive(&bar.v_empty[st]);
+    }
+}
+
+// The products, issued by one warp: S of tile i, then O of tile i - 1, so that
+// the tensor cores have the one while the other's weights are formed.  The low
+// parts go first: an accumulation loses digits by the sum's size, and theirs is small.
+template <int NG>
+__device__ void q8_products(const Q8Batch& b, int Hq, int Hkv, const Q8Share& w, uint32_t q, uint32_t weights, uint32_t tmem,
+                            Q8Bars<NG>& bar)
+{
+    using S = Q8Shape<NG>;
+    unsigned int* late = &g_q8kv_wait_timeouts;
+    const uint32_t elected = elect_one();
+    int i = 0, heads = 0, last = -1;
+    uint32_t idesc = 0, before = 0;  // of the tile's products, and of the tile's before it
+    // 128 x 16 steps of A (tensor memory, from column a) and B (rows of 256 bytes in two halves)
+    auto multiply = [&](uint32_t d, uint32_t a, uint32_t bytes, uint32_t id) {
+#pragma unroll 4
+        for (int ks = 0; ks < 16; ++ks) {
+            const uint32_t part = ks < 8 ? S::kPart : 0;
+            const uint64_t desc = tree_desc(bytes + part + (ks >> 2 & 1) * (S::kPart / 2), 16, 1024) + 2 * (ks & 3);
+            tree_mma(d, a + 8 * (ks & 7), desc, id, ks > 0, elected);
+        }
+    };
+    auto sums = [&](int j) {
+        const int to = j % S::kTurned, p = j % S::kWeights;
+        const bool there = mbar_wait(&bar.va_full[to], (j / S::kTurned) & 1, late) &&
+                           mbar_wait(&bar.p_full[p], (j / S::kWeights) & 1, late) &&
+                           (j == 0 || mbar_wait(&bar.o_free, (j - 1) & 1, late));
+        if (!__all_sync(0xffffffffu, there)) return false;  // (the warp leaves as one)
+        tm_after();
+        multiply(tmem + S::kColO, tmem + S::kColV + 64 * to, weights + p * 2 * S::kPart, before);
+        tree_commit_mma(&bar.o_full, elected);
+        tree_commit_mma(&bar.p_free[p], elected);
+        tree_commit_mma(&bar.va_free[to], elected);
+        return true;
+    };
+    bool ok = true, open = false;    // open: the last tile's sums have not been issued
+    q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
+        const int R = b.view[t.view].n_nodes * (Hq / Hkv);
+        idesc = (1u << 4) | ((uint32_t)((R + 15) / 16 * 2) << 17) | (8u << 24);  // D f32, A and B f16, 128 rows, R columns
+        if (t.view * Hkv + t.g != last) {
+            last = t.view * Hkv + t.g;
+            // (the next head's q comes when the last one's sums have been taken)
+            ok = (!open || sums(i - 1)) && __all_sync(0xffffffffu, mbar_wait(&bar.q_full, heads++ & 1, late));
+            open = false;
+        }
+        for (int k = 0; ok && k < t.tiles; ++k, ++i) {
+            const int to = i % S::kTurned;
+            const bool there = mbar_wait(&bar.ka_full[to], (i / S::kTurned) & 1, late) &&
+                               mbar_wait(&bar.s_free[i & 1], ((i >> 1) & 1) ^ 1, late);
+            if (!(ok = __all_sync(0xffffffffu, there))) break;
+            tm_after();
+            multiply(tmem + S::kColS + S::kRows * (i & 1), tmem + S::kColK + 64 * to, q, idesc);
+            tree_commit_mma(&bar.s_full[i & 1], elected);
+            tree_commit_mma(&bar.ka_free[to], elected);
+            if (open) ok = sums(i - 1);
+            open = true;
+            before = idesc;
+        }
+        return ok;
+    });
+    if (ok && open) sums(i - 1);
+    // also after an expired wait, tensor memory is not freed under a product
+    tree_commit_mma(&bar.done, elected);
+    mbar_wait(&bar.done, 0, late);
+}
+
+// Maxima over the eight lanes that share lane % 4: each value's ends in one lane of
+// them or in several; value k of what is left is value k + `first` of all.
+template <int N, int OFF>
+__device__ __forceinline__ void q8_maxima(float* v, int lane, int& first)
+{
+    if constexpr (OFF >= 4) {
+        if constexpr (N % 2 == 0) {
+            constexpr int H = N / 2;
+            const bool upper = lane & OFF;
+#pragma unroll
+            for (int e = 0; e < H; ++e) {
+                const float give = upper ? v[e] : v[e + H], keep = upper ? v[e + H] : v[e];
+                v[e] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, OFF));
+            }
+            if (upper) first += H;
+            q8_maxima<H, OFF / 2>(v, lane, first);
+        } else {
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[e] = fmaxf(v[e], __shfl_xor_sync(0xffffffffu, v[e], OFF));
+            q8_maxima<N, OFF / 2>(v, lane, first);
+        }
+    }
+}
+constexpr int q8_left(int n, int off = 16) { return off < 4 ? n : q8_left(n % 2 == 0 ? n / 2 : n, off / 2); }
+
+// One CTA an SM, each with its share of all chunks.
+template <int NG>
+__global__ void __launch_bounds__(kQ8Threads, 1)
+q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __grid_constant__ Q8Batch b, int Hq, int Hkv, int units,
+                  bool runs, Q8Scale scale, float* __restrict__ part_o, float* __restrict__ part_ml)
+{
+    using S = Q8Shape<NG>;
+    extern __shared__ uint8_t q8_smem[];
+    uint8_t* tiles = q8_smem + ((1024u - (smem_addr(q8_smem) & 1023u)) & 1023u);
+    uint8_t* qs = tiles + S::kStages * 2 * kQ8PageBytes;  // q: low and high part, two halves of the dims each
+    uint8_t* ps = qs + 2 * S::kPart;                      // weights, the same way
+    __shared__ Q8Bars<NG> bar;
+    __shared__ uint32_t tmem_at;
+    __shared__ __align__(16) float scales[kQ8ScaleSlots][8];
+    __shared__ __align__(16) float mx[2][4][S::kRows];  // the columns' maxima of a tile's blocks, by tile parity
+    __shared__ __align__(16) float unit_s[S::kRows];    // a score's power of two per unit of its product
+    __shared__ __align__(16) int from_s[S::kRows];      // the first key in the row's window
+    __shared__ volatile int bail[2][2];                 // a wait of the half's warps expired, by tile parity
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (warp == 14) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_at)), "r"(512u));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    if (tid == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(&bar.k_full[i], 1);
+            mbar_init(&bar.v_full[i], 1);
+            mbar_init(&bar.k_empty[i], 4);
+            mbar_init(&bar.v_empty[i], 4);
+        }
+        for (int i = 0; i < S::kTurned; ++i) {
+            mbar_init(&bar.ka_full[i], 4);
+            mbar_init(&bar.va_full[i], 4);
+            mbar_init(&bar.ka_free[i], 1);
+            mbar_init(&bar.va_free[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.s_full[i], 1);
+            mbar_init(&bar.s_free[i], 8);
+            bail[i][0] = bail[i][1] = 0;
+        }
+        for (int i = 0; i < S::kWeights; ++i) {
+            mbar_init(&bar.p_full[i], 8);
+            mbar_init(&bar.p_free[i], 1);
+        }
+        for (int i = 0; i < kQ8ScaleSlots; ++i) mbar_init(&bar.sc_full[i], 1);
+        mbar_init(&bar.o_full, 1);
+        mbar_init(&bar.o_free, 8);
+        mbar_init(&bar.q_full, 8);
+        mbar_init(&bar.done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    tm_before();
+    __syncthreads();
+    tm_after();
+    const uint32_t tmem = tmem_at;
+    if (tid < 2 * b.n_view) {
+        const int view = tid % b.n_view;
+        const CUtensorMap* m = tid < b.n_view ? &maps.k[view] : &maps.v[view];
+        if (b.view[view].n_chunk > 0)  // (a view without blocks has no map)
+            asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+    }
+    // one-tile chunks: a run of them each (a run's heads change least); longer
+    // ones: every gridDim.x-th, as chunks of unlike views then spread evenly
+    Q8Share w = {(int)blockIdx.x, units, (int)gridDim.x};
+    if (runs)
+        w = Q8Share{(int)((int64_t)units * blockIdx.x / gridDim.x), (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x), 0};
+    unsigned int* late = &g_q8kv_wait_timeouts;
+
+    if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == 12 && lane == 0) {
+            const int n = q8_produce<NG>(maps, b, Hkv, w, tiles, scales, bar);
+            ring_drain<S::kStages>(bar.k_full, n, late);
+            ring_drain<S::kStages>(bar.v_full, n, late);
+            ring_drain<kQ8ScaleSlots>(bar.sc_full, n, late);
+        }
+        if (warp == 13) q8_products<NG>(b, Hq, Hkv, w, smem_addr(qs), smem_addr(ps), tmem, bar);
+        __syncwarp();
+    } else if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        int n = 0;
+        q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
+            n += t.tiles;
+            return true;
+        });
+        q8_turn_tiles<NG>(n, tiles, tmem, warp & 3, lane, bar);
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        // The warp's keys are its block of the tile, 32 quad ..; its columns the groups of
+        // eight 2 j + half, j < groups.  Of them a thread has keys lane / 4 + 8 i and columns 2 (lane
+        // % 4) and the next: of O the same columns, dims 32 quad + lane / 4 + 8 i.
+        const int half = warp >> 2, quad = warp & 3, GQ = Hq / Hkv, col0 = 8 * half + 2 * (lane & 3);
+        const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16) + 8 * half;
+        const uint32_t row_at = (quad >> 1) * (S::kPart / 2) + half * 1024 + (lane & 7) * 128 +
+                                (((4 * (quad & 1) + (lane >> 3)) ^ (lane & 7)) << 4);  // where its keys' weights go
+        float o[NG][8], m[2 * NG], l[2 * NG], alpha[2 * NG];
+        int i = 0, last = -1, R = 0, groups = 0;
+        bool ok = true;
+        auto half_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); };
+        // adds O of tile j, `fresh`: the chunk's first
+        auto take = [&](int j, bool fresh) {
+            ok = __all_sync(0xffffffffu, ok && mbar_wait(&bar.o_full, j & 1, late));
+            tm_after();
+            constexpr int B = NG <= 3 ? NG : 2;  // groups at a time
+#pragma unroll
+            for (int e0 = 0; e0 < NG; e0 += B) {
+                float x[B][8];
+#pragma unroll
+                for (int e = e0; e < e0 + B && e < NG; ++e)
+                    if (e < groups) {
+                        tm_ld_frag(lanes + S::kColO + 16 * e, x[e - e0]);
+                        tm_ld_frag(lanes + (16u << 16) + S::kColO + 16 * e, x[e - e0] + 4);
+                    }
+                tm_loaded<8 * B>(&x[0][0]);
+                if (e0 + B >= NG) warp_arrive(&bar.o_free);
+#pragma unroll
+                for (int e = e0; e < e0 + B && e < NG; ++e)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) o[e][c] = fresh ? x[e - e0][c] : __fmaf_rn(o[e][c], alpha[2 * e + (c & 1)], x[e - e0][c]);
+            }
+        };
+        q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
+            const Q8View& v = b.view[t.view];
+            if (t.view * Hkv + t.g != last) {  // (S of every tile of the last head is complete: its q is free)
+                if (last < 0) pdl_wait();
+                last = t.view * Hkv + t.g;
+                R = v.n_nodes * GQ;
+                groups = (R + 15) / 16;
+                half_sync();                   // (the last head's units have been read)
+                const int part = tid & 15;
+                for (int j = 0; j < groups; ++j) {
+                    const int c = 16 * j + 8 * half + ((tid & 127) >> 4);
+                    float4 x = make_float4(0, 0, 0, 0), y = x;
+                    if (c < R) {
+                        const float* p = q + ((int64_t)(v.row0 + c / GQ) * Hq + t.g * GQ + c % GQ) * kHeadDim + 8 * part;
+                        x = ld_placed_f4(p);
+                        y = ld_placed_f4(p + 4);
+                    }
+                    float big = fmaxf(fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))),
+                                      fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w))));
+#pragma unroll
+                    for (int e = 1; e < 16; e <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, e));
+                    // the row's unit puts its largest element into [2^14, 2^15)
+                    const int exp = max((__float_as_int(big) >> 23) - 127 - 14, -112);
+                    const float into = __fmul_rn(scale.sign, __int_as_float((127 - exp) << 23));
+                    uint4 hi, lo;
+                    tree_split(__fmul_rn(x.x, into), __fmul_rn(x.y, into), hi.x, lo.x);
+                    tree_split(__fmul_rn(x.z, into), __fmul_rn(x.w, into), hi.y, lo.y);
+                    tree_split(__fmul_rn(y.x, into), __fmul_rn(y.y, into), hi.z, lo.z);
+                    tree_split(__fmul_rn(y.z, into), __fmul_rn(y.w, into), hi.w, lo.w);
+                    uint8_t* to = qs + (part >> 3) * (S::kPart / 2) + (c >> 3) * 1024 + (c & 7) * 128 + (((part & 7) ^ (c & 7)) << 4);
+                    *reinterpret_cast<uint4*>(to) = hi;
+                    *reinterpret_cast<uint4*>(to + S::kPart) = lo;
+                    if (part == 0) {
+                        unit_s[c] = __fmul_rn(scale.log2, __int_as_float((127 + exp) << 23));
+                        const int node = min(c / GQ, v.n_nodes - 1);
+                        from_s[c] = v.sealed + v.tail + b.row[v.row0 + node].n_path - v.window;
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                half_sync();
+                if (lane == 0) mbar_arrive(&bar.q_full);
+            }
+            int64_t pr = v.part0 + ((int64_t)t.c * Hkv + t.g) * R;  // the chunk's rows of results
+            int kc = 0;                                              // the chunk's tiles so far
+            for (int k = 0; k < t.tiles; ++k, ++i) {
+                const int key0 = q8_tile_key(v, t.t0 + k), buf = i & 1;
+                const float* sc = scales[i % kQ8ScaleSlots];
+                if (kc == 0) {
+#pragma unroll
+                    for (int e = 0; e < 2 * NG; ++e) {
+                        m[e] = -INFINITY;
+                        l[e] = 0.0f;
+                    }
+                }
+                ok = ok && mbar_wait(&bar.sc_full[i % kQ8ScaleSlots], (i / kQ8ScaleSlots) & 1, late) &&
+                     mbar_wait(&bar.s_full[buf], (i >> 1) & 1, late);
+                tm_after();
+                const bool valid = key0 + kQ8Block * quad < v.sealed;
+                const float ks = valid ? sc[quad] : 0.0f;
+                // V's scale goes into the weights as a power of two: 2^(s + log2 vs - m) is
+                // what multiplies a code, and over vs the weight itself.  (A block of zeros
+                // weighs as one of the smallest scale, 2^-31.)
+                const float vs = fmaxf(valid ? sc[4 + quad] : 0.0f, 4.656612873e-10f);
+                float lv;
+                asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lv) : "f"(vs));
+                const float iv = __frcp_rn(vs);
+                const bool masked = v.window > 0 && key0 < v.sealed + v.tail + v.n_nodes - v.window && key0 + kQ8Page > v.sinks;
+                // scores, `B` groups at a time: held from the maxima on where there are few, else read twice
+                constexpr int B = NG <= 5 ? NG : 4;
+                float s[B][8];
+                auto load_s = [&](int e0) {
+#pragma unroll
+                    for (int e = 0; e < B; ++e)
+                        if (e0 + e < groups) {
+                            tm_ld_frag(lanes + S::kColS + S::kRows * buf + 16 * (e0 + e), s[e]);
+                            tm_ld_frag(lanes + (16u << 16) + S::kColS + S::kRows * buf + 16 * (e0 + e), s[e] + 4);
+                        }
+                    tm_loaded<8 * B>(&s[0][0]);
+                    if (!valid) {
+#pragma unroll
+                        for (int e = 0; e < B; ++e)
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) s[e][c] = -INFINITY;
+                    } else if (masked) {
+#pragma unroll
+                        for (int e = 0; e < B; ++e)
+                            if (e0 + e < groups) {
+                                const int2 from = *reinterpret_cast<const int2*>(&from_s[16 * (e0 + e) + col0]);
+#pragma unroll
+                                for (int c = 0; c < 8; ++c) {
+                                    const int key = key0 + kQ8Block * quad + (lane >> 2) + 8 * (c >> 1);
+                                    if (key >= v.sinks && key < (c & 1 ? from.y : from.x)) s[e][c] = -INFINITY;
+                                }
+                            }
+                    }
+                };
+                float top[2 * NG];
+#pragma unroll
+                for (int e0 = 0; e0 < NG; e0 += B) {
+                    load_s(e0);
+#pragma unroll
+                    for (int e = 0; e < B; ++e) {
+                        top[2 * (e0 + e)] = top[2 * (e0 + e) + 1] = -INFINITY;
+                        if (e0 + e < groups) {
+                            top[2 * (e0 + e)] = fmaxf(fmaxf(s[e][0], s[e][2]), fmaxf(s[e][4], s[e][6]));
+                            top[2 * (e0 + e) + 1] = fmaxf(fmaxf(s[e][1], s[e][3]), fmaxf(s[e][5], s[e][7]));
+                        }
+                    }
+                }
+                if (!S::kTwice) warp_arrive(&bar.s_free[buf]);
+                int first = 0;
+                q8_maxima<2 * NG, 16>(top, lane, first);
+#pragma unroll
+                for (int e = 0; e < q8_left(2 * NG); ++e) {
+                    const int at = first + e, c = 16 * (at >> 1) + col0 + (at & 1);
+                    if ((at >> 1) < groups)  // (rounded up: no weight is above 2^15 by more than its exponent's own rounding)
+                        mx[buf][quad][c] = __fadd_ru(__fmul_ru(top[e], fmaxf(__fmul_rn(unit_s[c], ks), 1e-37f)), lv);
+                }
+                // all four warps of a half meet here, an expired wait or not, and leave together
+                if (!ok) bail[half][buf] = 1;
+                half_sync();
+                if (bail[half][buf]) return false;
+                if (kc > 0) take(i - 1, kc == 1);
+                ok = ok && mbar_wait(&bar.p_free[i % S::kWeights], ((i / S::kWeights) & 1) ^ 1, late);
+                const uint32_t to = smem_addr(ps) + (i % S::kWeights) * 2 * S::kPart + row_at;
+#pragma unroll
+                for (int e = 0; e < NG; ++e) {
+                    if (S::kTwice && e % B == 0) {
+                        load_s(e);
+                        if (e + B >= NG) warp_arrive(&bar.s_free[buf]);
+                    }
+                    if (e < groups) {
+                        const int c = 16 * e + col0;
+                        float2 big = *reinterpret_cast<const float2*>(&mx[buf][0][c]);
+#pragma unroll
+                        for (int d = 1; d < 4; ++d) {
+                            const float2 x = *reinterpret_cast<const float2*>(&mx[buf][d][c]);
+                            big = make_float2(fmaxf(big.x, x.x), fmaxf(big.y, x.y));
+                        }
+                        const float2 unit = *reinterpret_cast<const float2*>(&unit_s[c]);
+                        float p[2][4];
+#pragma unroll
+                        for (int d = 0; d < 2; ++d) {
+                            const float now = fmaxf(m[2 * e + d], d ? big.y : big.x), at = now == -INFINITY ? 0.0f : now;
+                            const float f = fmaxf(__fmul_rn(d ? unit.y : unit.x, ks), 1e-37f), up = __fadd_rn(__fsub_rn(kQ8Up, at), lv);
+                            alpha[2 * e + d] = tree_exp2(__fsub_rn(m[2 * e + d], at));  // 0 for m = -inf
+                            m[2 * e + d] = now;
+#pragma unroll
+                            for (int c2 = 0; c2 < 4; ++c2) p[d][c2] = tree_exp2(__fmaf_rn(s[e % B][2 * c2 + d], f, up));
+                            const float sum = __fadd_rn(__fadd_rn(p[d][0], p[d][1]), __fadd_rn(p[d][2], p[d][3]));
+                            l[2 * e + d] = __fmaf_rn(l[2 * e + d], alpha[2 * e + d], __fmul_rn(sum, iv));
+                        }
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int c2 = 0; c2 < 4; ++c2) tree_split(p[0][c2], p[1][c2], hi[c2], lo[c2]);
+                        st_matrix_turned(to + 2048 * e, hi[0], hi[1], hi[2], hi[3]);
+                        st_matrix_turned(to + 2048 * e + S::kPart, lo[0], lo[1], lo[2], lo[3]);
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.p_full[i % S::kWeights]);
+                ++kc;
+                if (kc == v.chunk || k + 1 == t.tiles) {  // the chunk's last tile
+                    take(i, kc == 1);
+#pragma unroll
+                    for (int e = 0; e < 2 * NG; ++e)
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) l[e] = __fadd_rn(l[e], __shfl_xor_sync(0xffffffffu, l[e], d));
+                    float* ml = part_ml + 8 * (pr + col0);
+                    float* po = part_o + (pr + col0) * kHeadDim + 32 * quad + (lane >> 2);
+                    asm volatile("" : "+l"(ml), "+l"(po));  // (one address each, not one for every store)
+                    const int left = ok ? R - col0 : 0;
+#pragma unroll
+                    for (int e = 0; e < 2 * NG; ++e) {
+                        const int c = 16 * (e >> 1) + (e & 1);
+                        if (c < left) {
+                            if ((lane >> 2) == 0) {
+                                ml[8 * c + 4 + quad] = l[e];
+                                if (quad == 0) ml[8 * c] = m[e];
+                            }
+#pragma unroll
+                            for (int d = 0; d < 4; ++d) po[c * kHeadDim + 8 * d] = o[e >> 1][2 * d + (e & 1)];
+                        }
+                    }
+                    kc = 0;
+                    pr += (int64_t)Hkv * R;
+                }
+            }
+            return true;
+        });
+    }
+    tm_before();
+    __syncthreads();
+    if (warp == 14) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+}
+
+cudaError_t read_q8kv_wait_timeouts(uint32_t* count, bool reset)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(count, g_q8kv_wait_timeouts, sizeof(uint32_t));
+    if (e == cudaSuccess && reset) {
+        const uint32_t zero = 0;
+        e = cudaMemcpyToSymbol(g_q8kv_wait_timeouts, &zero, sizeof(uint32_t));
+    }
+    return e;
+}
+
+// The maps of the views' codes: dims (byte, row, head, page), a box a page of one
+// head, zeros outside.  Made anew by each call: two of them take 0.1 us.
+static bool q8_maps(const Q8Batch& b, int Hkv, Q8Maps* maps)
+{
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = tree_map_encoder();
+    if (!enc) return false;
+    for (int i = 0; i < b.n_view; ++i) {
+        const Q8View& v = b.view[i];
+        if (v.n_chunk == 0) continue;
+        const cuuint64_t dims[4] = {128, 128, (cuuint64_t)Hkv, (cuuint64_t)v.n_pages};
+        const cuuint64_t strides[3] = {128, kQ8PageBytes, (cuuint64_t)v.page_stride};
+        const cuuint32_t box[4] = {128, 128, 1, 1}, step[4] = {1, 1, 1, 1};
+        for (int kv = 0; kv < 2; ++kv)
+            if (enc(kv ? &maps->v[i] : &maps->k[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<int8_t*>(kv ? v.v_codes : v.k_codes), dims,
+                    strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+                return false;
+    }
+    return true;
+}
+
+template <int NG>
+static cudaError_t launch_chunks(const Q8Maps& maps, const float* q, const Q8Batch& b, int Hq, int Hkv, int64_t units, bool runs,
+                                 const Q8Scale& scale, float* part_o, float* part_ml, cudaStream_t s)
+{
+    const int sms = sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    static std::atomic<bool> done[kMaxDevices];
+    cudaError_t e = set_smem_once(q8kv_chunk_kernel<NG>, Q8Shape<NG>::kBytes, done);
+    if (e == cudaSuccess)
+        e = launch_pdl_smem(q8kv_chunk_kernel<NG>, dim3((unsigned)std::min<int64_t>(sms, units)), dim3(kQ8Threads), Q8Shape<NG>::kBytes, s,
+                            maps, q, b, Hq, Hkv, (int)units, runs, scale, part_o, part_ml);
+    if (e == cudaSuccess) count_launches(1);
+    return e;
 }
 
 // ---------------------------------------------------------------- merge
@@ -206,21 +743,6 @@ q8kv_chunk_kernel(const float* q, const __grid_constant__ Q8Batch b, int Hq, int
 constexpr int kQ8Ahead = 8;       // chunk sums in flight per warp
 constexpr int kQ8Keys = 48;       // f16 keys in flight
 constexpr int kQ8MaxKeys = kQ8MaxTail + kMaxTree;
-
-__device__ __forceinline__ float4 q8_half4(uint2 x)
-{
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&x.x));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&x.y));
-    return make_float4(a.x, a.y, b.x, b.y);
-}
-
-__device__ __forceinline__ void q8_axpy(float4& o, float4 x, float a)
-{
-    o.x = __fmaf_rn(x.x, a, o.x);
-    o.y = __fmaf_rn(x.y, a, o.y);
-    o.z = __fmaf_rn(x.z, a, o.z);
-    o.w = __fmaf_rn(x.w, a, o.w);
-}
 
 __global__ void __launch_bounds__(kHeadDim)
 q8kv_merge_kernel(const float* q, const __grid_constant__ Q8Batch b, int Hq, int Hkv, Q8Scale scale, const float* part_o,
@@ -276,9 +798,10 @@ q8kv_merge_kernel(const float* q, const __grid_constant__ Q8Batch b, int Hq, int
         w[j] = -INFINITY;
         ls[j] = 0.0f;
         if (c < nch) {
-            const float2 ml = ld_placed_f2(part_ml + 2 * (pr0 + c * pstep));
-            w[j] = ml.x;
-            ls[j] = ml.y;
+            const float* ml = part_ml + 8 * (pr0 + c * pstep);
+            const float4 x = ld_placed_cg_f4(ml + 4);
+            w[j] = ld_placed_f(ml);
+            ls[j] = __fadd_rn(__fadd_rn(x.x, x.y), __fadd_rn(x.z, x.w));
         }
     }
     float4 ov[kQ8Ahead];
@@ -299,7 +822,7 @@ q8kv_merge_kernel(const float* q, const __grid_constant__ Q8Batch b, int Hq, int
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const uint4 x = kx[i][e >> 1];
-                const float4 k = q8_half4(e & 1 ? make_uint2(x.z, x.w) : make_uint2(x.x, x.y));
+                const float4 k = half4(e & 1 ? make_uint2(x.z, x.w) : make_uint2(x.x, x.y));
                 dot = __fmaf_rn(qv[e].w, k.w, __fmaf_rn(qv[e].z, k.z, __fmaf_rn(qv[e].y, k.y, __fmaf_rn(qv[e].x, k.x, dot))));
             }
 #pragma unroll
@@ -320,12 +843,12 @@ q8kv_merge_kernel(const float* q, const __grid_constant__ Q8Batch b, int Hq, int
     M = warp_max(M);  // (a row sees itself: there is one)
 #pragma unroll
     for (int j = 0; j < kStats; ++j) {
-        w[j] = __fmul_rn(q8_exp2(__fsub_rn(w[j], M)), kQ8Down);
+        w[j] = __fmul_rn(tree_exp2(__fsub_rn(w[j], M)), kQ8Down);
         L = __fmaf_rn(ls[j], w[j], L);
     }
 #pragma unroll
     for (int j = 0; j < kKeyStats; ++j) {
-        p[j] = q8_exp2(__fsub_rn(p[j], M));
+        p[j] = tree_exp2(__fsub_rn(p[j], M));
         L = __fadd_rn(L, p[j]);
     }
     L = warp_sum_butterfly(L);
@@ -338,14 +861,14 @@ q8kv_merge_kernel(const float* q, const __grid_constant__ Q8Batch b, int Hq, int
             load_o(j);
         }
         const float f = __shfl_sync(0xffffffffu, w[j >> 3], c & 31);
-        if (c < nch) q8_axpy(o, ov[j & (kQ8Ahead - 1)], f);
+        if (c < nch) axpy4(o, ov[j & (kQ8Ahead - 1)], f);
     }
     for (int base = 0; base < n; base += kQ8Keys) {
         if (base > 0) load_v(base);
 #pragma unroll
         for (int i = 0; i < kQ8Keys / 4; ++i) {
             const int a = base + 4 * i + warp;  // (its weight: recomputed from ps, the same in every lane)
-            if (a < n) q8_axpy(o, q8_half4(vx[i]), q8_exp2(__fsub_rn(ps[a], M)));
+            if (a < n) axpy4(o, half4(vx[i]), tree_exp2(__fsub_rn(ps[a], M)));
         }
     }
     os[warp][lane] = o;
@@ -366,17 +889,26 @@ cudaError_t launch_q8kv_attention(const float* q, const Q8Batch& b, int Hq, int 
                                   int8_t* out_q, float* out_d, cudaStream_t s)
 {
     int64_t units = 0, n_part = 0;
+    bool runs = true;
+    int rows = 0;  // the most of a KV head
     for (int i = 0; i < b.n_view; ++i) {
-        units += (int64_t)b.view[i].n_chunk * Hkv;
-        n_part += (int64_t)b.view[i].n_chunk * b.view[i].n_nodes * Hq;
+        const Q8View& v = b.view[i];
+        units += (int64_t)v.n_chunk * Hkv;
+        n_part += (int64_t)v.n_chunk * v.n_nodes * Hq;
+        if (v.n_chunk == 0) continue;
+        runs = runs && v.chunk == 1;
+        rows = std::max(rows, v.n_nodes * (Hq / Hkv));
     }
     float* part_o = (float*)part;
     float* part_ml = part_o + n_part * kHeadDim;
     const Q8Scale sc = {scale < 0 ? -1.0f : 1.0f, (float)(std::fabs((double)scale) * 1.4426950408889634)};
     if (units > 0) {
-        const cudaError_t e = launch_pdl(q8kv_chunk_kernel, dim3((unsigned)units), dim3(128), s, q, b, Hq, Hkv, sc, part_o, part_ml);
+        Q8Maps maps{};
+        if (!q8_maps(b, Hkv, &maps)) return cudaErrorInvalidValue;
+        const auto launch = rows <= 16 ? launch_chunks<1> : rows <= 32 ? launch_chunks<2> : rows <= 48 ? launch_chunks<3>
+                            : rows <= 80 ? launch_chunks<5> : launch_chunks<8>;
+        const cudaError_t e = launch(maps, q, b, Hq, Hkv, units, runs, sc, part_o, part_ml, s);
         if (e != cudaSuccess) return e;
-        count_launches(1);
     }
     const cudaError_t e = launch_pdl(q8kv_merge_kernel, dim3(Hq, b.n_row), dim3(kHeadDim), s, q, b, Hq, Hkv, sc,
                                      (const float*)part_o, (const float*)part_ml, out, out_q, out_d);
