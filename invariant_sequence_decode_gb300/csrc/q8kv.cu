@@ -82,10 +82,10 @@ __device__ unsigned int g_q8kv_wait_timeouts;
 template <int NG>
 struct Q8Shape {
     static constexpr int kRows = 16 * NG;                      // columns of the products
-    static constexpr int kStages = NG == 1 ? 6 : NG == 2 ? 5 : NG == 3 ? 4 : NG == 5 ? 3 : 2;  // tiles of K, and of V, in flight
+    static constexpr int kStages = NG == 1 ? 6 : NG == 2 ? 5 : NG == 3 ? 4 : NG <= 6 ? 3 : 2;  // tiles of K, and of V, in flight
     static constexpr int kTurned = NG <= 5 ? 2 : 1;            // tiles of K, and of V, in tensor memory
     static constexpr int kWeights = NG <= 5 ? 2 : 1;           // tiles of weights in shared memory
-    static constexpr bool kTwice = NG > 3;                     // scores are read twice, not held while O is added
+    static constexpr bool kTwice = NG > 6;                     // scores are read twice, not held while O is added
     static constexpr int kPart = kRows * kHeadDim * 2;         // bytes of one part of q, or of the weights
     static constexpr uint32_t kColK = 0, kColV = 64 * kTurned, kColS = 128 * kTurned, kColO = kColS + 2 * kRows;
     static constexpr int kBytes = kStages * 2 * kQ8PageBytes + (2 + 2 * kWeights) * kPart + 1024;
@@ -280,22 +280,25 @@ __device__ void q8_turn_tiles(int n, const uint8_t* tiles, uint32_t tmem, int qu
 // the tensor cores have the one while the other's weights are formed.  The low
 // parts go first: an accumulation loses digits by the sum's size, and theirs is small.
 template <int NG>
-__device__ void q8_products(const Q8Batch& b, int Hq, int Hkv, const Q8Share& w, uint32_t q, uint32_t weights, uint32_t tmem,
+__device__ void q8_products(const Q8Batch& b, int Hkv, const Q8Share& w, uint32_t q, uint32_t weights, uint32_t tmem,
                             Q8Bars<NG>& bar)
 {
     using S = Q8Shape<NG>;
     unsigned int* late = &g_q8kv_wait_timeouts;
     const uint32_t elected = elect_one();
     int i = 0, heads = 0, last = -1;
-    uint32_t idesc = 0, before = 0;  // of the tile's products, and of the tile's before it
-    // 128 x 16 steps of A (tensor memory, from column a) and B (rows of 256 bytes in two halves)
-    auto multiply = [&](uint32_t d, uint32_t a, uint32_t bytes, uint32_t id) {
-#pragma unroll 4
-        for (int ks = 0; ks < 16; ++ks) {
-            const uint32_t part = ks < 8 ? S::kPart : 0;
-            const uint64_t desc = tree_desc(bytes + part + (ks >> 2 & 1) * (S::kPart / 2), 16, 1024) + 2 * (ks & 3);
-            tree_mma(d, a + 8 * (ks & 7), desc, id, ks > 0, elected);
-        }
+    constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(2 * NG) << 17) | (8u << 24);  // D f32, A and B f16, 128 by 16 NG
+    // all steps of a product: A in tensor memory from column a, B rows of 256 bytes in two halves
+    const uint64_t step = tree_desc(0, 16, 1024);
+    auto multiply = [&](uint32_t d, uint32_t a, uint32_t bytes) {
+        // (told to be the warp's, as they are: else every product moves its own copies)
+        d = __shfl_sync(0xffffffffu, d, 0);
+        a = __shfl_sync(0xffffffffu, a, 0);
+        const uint64_t desc = step | ((__shfl_sync(0xffffffffu, bytes, 0) >> 4) & 0x3FFF);
+#pragma unroll
+        for (int ks = 0; ks < 16; ++ks)
+            tree_mma(d, a + 8 * (ks & 7), desc + ((ks < 8 ? S::kPart : 0) + (ks >> 2 & 1) * (S::kPart / 2)) / 16 + 2 * (ks & 3), idesc, ks > 0,
+                     elected);
     };
     auto sums = [&](int j) {
         const int to = j % S::kTurned, p = j % S::kWeights;
@@ -304,7 +307,7 @@ __device__ void q8_products(const Q8Batch& b, int Hq, int Hkv, const Q8Share& w,
                            (j == 0 || mbar_wait(&bar.o_free, (j - 1) & 1, late));
         if (!__all_sync(0xffffffffu, there)) return false;  // (the warp leaves as one)
         tm_after();
-        multiply(tmem + S::kColO, tmem + S::kColV + 64 * to, weights + p * 2 * S::kPart, before);
+        multiply(tmem + S::kColO, tmem + S::kColV + 64 * to, weights + p * 2 * S::kPart);
         tree_commit_mma(&bar.o_full, elected);
         tree_commit_mma(&bar.p_free[p], elected);
         tree_commit_mma(&bar.va_free[to], elected);
@@ -312,8 +315,6 @@ __device__ void q8_products(const Q8Batch& b, int Hq, int Hkv, const Q8Share& w,
     };
     bool ok = true, open = false;    // open: the last tile's sums have not been issued
     q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
-        const int R = b.view[t.view].n_nodes * (Hq / Hkv);
-        idesc = (1u << 4) | ((uint32_t)((R + 15) / 16 * 2) << 17) | (8u << 24);  // D f32, A and B f16, 128 rows, R columns
         if (t.view * Hkv + t.g != last) {
             last = t.view * Hkv + t.g;
             // (the next head's q comes when the last one's sums have been taken)
@@ -326,12 +327,11 @@ __device__ void q8_products(const Q8Batch& b, int Hq, int Hkv, const Q8Share& w,
                                mbar_wait(&bar.s_free[i & 1], ((i >> 1) & 1) ^ 1, late);
             if (!(ok = __all_sync(0xffffffffu, there))) break;
             tm_after();
-            multiply(tmem + S::kColS + S::kRows * (i & 1), tmem + S::kColK + 64 * to, q, idesc);
+            multiply(tmem + S::kColS + S::kRows * (i & 1), tmem + S::kColK + 64 * to, q);
             tree_commit_mma(&bar.s_full[i & 1], elected);
             tree_commit_mma(&bar.ka_free[to], elected);
             if (open) ok = sums(i - 1);
             open = true;
-            before = idesc;
         }
         return ok;
     });
@@ -339,6 +339,13 @@ __device__ void q8_products(const Q8Batch& b, int Hq, int Hkv, const Q8Share& w,
     // also after an expired wait, tensor memory is not freed under a product
     tree_commit_mma(&bar.done, elected);
     mbar_wait(&bar.done, 0, late);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 // Maxima over the eight lanes that share lane % 4: each value's ends in one lane of
@@ -380,9 +387,14 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
     __shared__ Q8Bars<NG> bar;
     __shared__ uint32_t tmem_at;
     __shared__ __align__(16) float scales[kQ8ScaleSlots][8];
-    __shared__ __align__(16) float mx[2][4][S::kRows];  // the columns' maxima of a tile's blocks, by tile parity
-    __shared__ __align__(16) float unit_s[S::kRows];    // a score's power of two per unit of its product
-    __shared__ __align__(16) int from_s[S::kRows];      // the first key in the row's window
+    // by half: its columns are the groups of eight 2 e + half, numbered through
+    __shared__ float mx[2][2][4][S::kRows / 2];           // the columns' maxima of a tile's blocks, by tile parity
+    __shared__ float unit_s[2][S::kRows / 2];             // a score's power of two per unit of its product
+    __shared__ __align__(8) int from_s[2][S::kRows / 2];  // the first key in the row's window
+    // by warp: what turns a column's products into exponents (a factor, an offset),
+    // and what O so far is multiplied by, by tile parity
+    __shared__ __align__(16) float2 turn_s[8][S::kRows / 2];
+    __shared__ __align__(8) float alpha_s[2][8][S::kRows / 2];
     __shared__ volatile int bail[2][2];                 // a wait of the half's warps expired, by tile parity
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (warp == 14) {
@@ -443,7 +455,7 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
             ring_drain<S::kStages>(bar.v_full, n, late);
             ring_drain<kQ8ScaleSlots>(bar.sc_full, n, late);
         }
-        if (warp == 13) q8_products<NG>(b, Hq, Hkv, w, smem_addr(qs), smem_addr(ps), tmem, bar);
+        if (warp == 13) q8_products<NG>(b, Hkv, w, smem_addr(qs), smem_addr(ps), tmem, bar);
         __syncwarp();
     } else if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -456,18 +468,23 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // The warp's keys are its block of the tile, 32 quad ..; its columns the groups of
-        // eight 2 j + half, j < groups.  Of them a thread has keys lane / 4 + 8 i and columns 2 (lane
-        // % 4) and the next: of O the same columns, dims 32 quad + lane / 4 + 8 i.
-        const int half = warp >> 2, quad = warp & 3, GQ = Hq / Hkv, col0 = 8 * half + 2 * (lane & 3);
+        // eight 2 e + half, e < NG.  Of them a thread has keys lane / 4 + 8 i and columns 2 (lane
+        // % 4) and the next: of O the same columns, dims 32 quad + lane / 4 + 8 i.  What is
+        // the same for a column's keys (maximum, factor, correction) a lane forms per
+        // column, and the threads pick it up from shared memory: formed by each
+        // thread for its own columns it took twice the instructions of the weights.
+        constexpr int kCols = S::kRows / 2, kMine = (kCols + 31) / 32;  // columns of a half, and of a lane
+        const int half = warp >> 2, quad = warp & 3, GQ = Hq / Hkv, pair2 = 2 * (lane & 3);
         const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16) + 8 * half;
         const uint32_t row_at = (quad >> 1) * (S::kPart / 2) + half * 1024 + (lane & 7) * 128 +
                                 (((4 * (quad & 1) + (lane >> 3)) ^ (lane & 7)) << 4);  // where its keys' weights go
-        float o[NG][8], m[2 * NG], l[2 * NG], alpha[2 * NG];
-        int i = 0, last = -1, R = 0, groups = 0;
+        uint64_t o[NG][4], l[NG];      // pairs of columns
+        float m[kMine];                // of columns lane + 32 e
+        int i = 0, last = -1, R = 0;
         bool ok = true;
         auto half_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); };
-        // adds O of tile j, `fresh`: the chunk's first
-        auto take = [&](int j, bool fresh) {
+        // adds O of tile j
+        auto take = [&](int j) {
             ok = __all_sync(0xffffffffu, ok && mbar_wait(&bar.o_full, j & 1, late));
             tm_after();
             constexpr int B = NG <= 3 ? NG : 2;  // groups at a time
@@ -475,17 +492,18 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
             for (int e0 = 0; e0 < NG; e0 += B) {
                 float x[B][8];
 #pragma unroll
-                for (int e = e0; e < e0 + B && e < NG; ++e)
-                    if (e < groups) {
-                        tm_ld_frag(lanes + S::kColO + 16 * e, x[e - e0]);
-                        tm_ld_frag(lanes + (16u << 16) + S::kColO + 16 * e, x[e - e0] + 4);
-                    }
+                for (int e = e0; e < e0 + B && e < NG; ++e) {
+                    tm_ld_frag(lanes + S::kColO + 16 * e, x[e - e0]);
+                    tm_ld_frag(lanes + (16u << 16) + S::kColO + 16 * e, x[e - e0] + 4);
+                }
                 tm_loaded<8 * B>(&x[0][0]);
                 if (e0 + B >= NG) warp_arrive(&bar.o_free);
 #pragma unroll
-                for (int e = e0; e < e0 + B && e < NG; ++e)
+                for (int e = e0; e < e0 + B && e < NG; ++e) {
+                    const float2 a = *reinterpret_cast<const float2*>(&alpha_s[j & 1][warp][8 * e + pair2]);
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) o[e][c] = fresh ? x[e - e0][c] : __fmaf_rn(o[e][c], alpha[2 * e + (c & 1)], x[e - e0][c]);
+                    for (int c = 0; c < 4; ++c) o[e][c] = fma2(o[e][c], pair(a.x, a.y), pair(x[e - e0][2 * c], x[e - e0][2 * c + 1]));
+                }
             }
         };
         q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
@@ -494,11 +512,10 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                 if (last < 0) pdl_wait();
                 last = t.view * Hkv + t.g;
                 R = v.n_nodes * GQ;
-                groups = (R + 15) / 16;
                 half_sync();                   // (the last head's units have been read)
                 const int part = tid & 15;
-                for (int j = 0; j < groups; ++j) {
-                    const int c = 16 * j + 8 * half + ((tid & 127) >> 4);
+                for (int j = 0; j < NG; ++j) {
+                    const int in8 = (tid & 127) >> 4, c = 16 * j + 8 * half + in8;
                     float4 x = make_float4(0, 0, 0, 0), y = x;
                     if (c < R) {
                         const float* p = q + ((int64_t)(v.row0 + c / GQ) * Hq + t.g * GQ + c % GQ) * kHeadDim + 8 * part;
@@ -521,9 +538,9 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                     *reinterpret_cast<uint4*>(to) = hi;
                     *reinterpret_cast<uint4*>(to + S::kPart) = lo;
                     if (part == 0) {
-                        unit_s[c] = __fmul_rn(scale.log2, __int_as_float((127 + exp) << 23));
+                        unit_s[half][8 * j + in8] = __fmul_rn(scale.log2, __int_as_float((127 + exp) << 23));
                         const int node = min(c / GQ, v.n_nodes - 1);
-                        from_s[c] = v.sealed + v.tail + b.row[v.row0 + node].n_path - v.window;
+                        from_s[half][8 * j + in8] = v.sealed + v.tail + b.row[v.row0 + node].n_path - v.window;
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -535,12 +552,15 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
             for (int k = 0; k < t.tiles; ++k, ++i) {
                 const int key0 = q8_tile_key(v, t.t0 + k), buf = i & 1;
                 const float* sc = scales[i % kQ8ScaleSlots];
-                if (kc == 0) {
+                if (kc == 0) {  // (what the last chunk left may be anything: it is not multiplied by 0)
 #pragma unroll
-                    for (int e = 0; e < 2 * NG; ++e) {
-                        m[e] = -INFINITY;
-                        l[e] = 0.0f;
+                    for (int e = 0; e < NG; ++e) {
+                        l[e] = 0;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) o[e][c] = 0;
                     }
+#pragma unroll
+                    for (int e = 0; e < kMine; ++e) m[e] = -INFINITY;
                 }
                 ok = ok && mbar_wait(&bar.sc_full[i % kQ8ScaleSlots], (i / kQ8ScaleSlots) & 1, late) &&
                      mbar_wait(&bar.s_full[buf], (i >> 1) & 1, late);
@@ -556,15 +576,14 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                 const float iv = __frcp_rn(vs);
                 const bool masked = v.window > 0 && key0 < v.sealed + v.tail + v.n_nodes - v.window && key0 + kQ8Page > v.sinks;
                 // scores, `B` groups at a time: held from the maxima on where there are few, else read twice
-                constexpr int B = NG <= 5 ? NG : 4;
+                constexpr int B = S::kTwice ? 4 : NG;
                 float s[B][8];
                 auto load_s = [&](int e0) {
 #pragma unroll
-                    for (int e = 0; e < B; ++e)
-                        if (e0 + e < groups) {
-                            tm_ld_frag(lanes + S::kColS + S::kRows * buf + 16 * (e0 + e), s[e]);
-                            tm_ld_frag(lanes + (16u << 16) + S::kColS + S::kRows * buf + 16 * (e0 + e), s[e] + 4);
-                        }
+                    for (int e = 0; e < B; ++e) {
+                        tm_ld_frag(lanes + S::kColS + S::kRows * buf + 16 * (e0 + e), s[e]);
+                        tm_ld_frag(lanes + (16u << 16) + S::kColS + S::kRows * buf + 16 * (e0 + e), s[e] + 4);
+                    }
                     tm_loaded<8 * B>(&s[0][0]);
                     if (!valid) {
 #pragma unroll
@@ -573,15 +592,14 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                             for (int c = 0; c < 8; ++c) s[e][c] = -INFINITY;
                     } else if (masked) {
 #pragma unroll
-                        for (int e = 0; e < B; ++e)
-                            if (e0 + e < groups) {
-                                const int2 from = *reinterpret_cast<const int2*>(&from_s[16 * (e0 + e) + col0]);
+                        for (int e = 0; e < B; ++e) {
+                            const int2 from = *reinterpret_cast<const int2*>(&from_s[half][8 * (e0 + e) + pair2]);
 #pragma unroll
-                                for (int c = 0; c < 8; ++c) {
-                                    const int key = key0 + kQ8Block * quad + (lane >> 2) + 8 * (c >> 1);
-                                    if (key >= v.sinks && key < (c & 1 ? from.y : from.x)) s[e][c] = -INFINITY;
-                                }
+                            for (int c = 0; c < 8; ++c) {
+                                const int key = key0 + kQ8Block * quad + (lane >> 2) + 8 * (c >> 1);
+                                if (key >= v.sinks && key < (c & 1 ? from.y : from.x)) s[e][c] = -INFINITY;
                             }
+                        }
                     }
                 };
                 float top[2 * NG];
@@ -590,11 +608,8 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                     load_s(e0);
 #pragma unroll
                     for (int e = 0; e < B; ++e) {
-                        top[2 * (e0 + e)] = top[2 * (e0 + e) + 1] = -INFINITY;
-                        if (e0 + e < groups) {
-                            top[2 * (e0 + e)] = fmaxf(fmaxf(s[e][0], s[e][2]), fmaxf(s[e][4], s[e][6]));
-                            top[2 * (e0 + e) + 1] = fmaxf(fmaxf(s[e][1], s[e][3]), fmaxf(s[e][5], s[e][7]));
-                        }
+                        top[2 * (e0 + e)] = fmaxf(max3(s[e][0], s[e][2], s[e][4]), s[e][6]);
+                        top[2 * (e0 + e) + 1] = fmaxf(max3(s[e][1], s[e][3], s[e][5]), s[e][7]);
                     }
                 }
                 if (!S::kTwice) warp_arrive(&bar.s_free[buf]);
@@ -602,76 +617,92 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                 q8_maxima<2 * NG, 16>(top, lane, first);
 #pragma unroll
                 for (int e = 0; e < q8_left(2 * NG); ++e) {
-                    const int at = first + e, c = 16 * (at >> 1) + col0 + (at & 1);
-                    if ((at >> 1) < groups)  // (rounded up: no weight is above 2^15 by more than its exponent's own rounding)
-                        mx[buf][quad][c] = __fadd_ru(__fmul_ru(top[e], fmaxf(__fmul_rn(unit_s[c], ks), 1e-37f)), lv);
+                    const int at = first + e;
+                    mx[buf][half][quad][8 * (at >> 1) + pair2 + (at & 1)] = top[e];
                 }
+                __syncwarp();
+                float factor[kMine];
+#pragma unroll
+                for (int e = 0; e < kMine; ++e)
+                    if (lane + 32 * e < kCols) {
+                        // (rounded up: no weight is above 2^15 by more than its exponent's own rounding)
+                        float* x = &mx[buf][half][quad][lane + 32 * e];
+                        factor[e] = fmaxf(__fmul_rn(unit_s[half][lane + 32 * e], ks), 1e-37f);
+                        *x = __fadd_ru(__fmul_ru(*x, factor[e]), lv);
+                    }
                 // all four warps of a half meet here, an expired wait or not, and leave together
                 if (!ok) bail[half][buf] = 1;
                 half_sync();
                 if (bail[half][buf]) return false;
-                if (kc > 0) take(i - 1, kc == 1);
+#pragma unroll
+                for (int e = 0; e < kMine; ++e)
+                    if (lane + 32 * e < kCols) {
+                        const float* x = &mx[buf][half][0][lane + 32 * e];
+                        const float now = fmaxf(m[e], max3(fmaxf(x[0], x[kCols]), x[2 * kCols], x[3 * kCols]));
+                        const float at = now == -INFINITY ? 0.0f : now;
+                        turn_s[warp][lane + 32 * e] = make_float2(factor[e], __fadd_rn(__fsub_rn(kQ8Up, at), lv));
+                        alpha_s[buf][warp][lane + 32 * e] = tree_exp2(__fsub_rn(m[e], at));  // 0 for m = -inf
+                        m[e] = now;
+                    }
+                __syncwarp();
                 ok = ok && mbar_wait(&bar.p_free[i % S::kWeights], ((i / S::kWeights) & 1) ^ 1, late);
                 const uint32_t to = smem_addr(ps) + (i % S::kWeights) * 2 * S::kPart + row_at;
+                const uint64_t iv2 = pair(iv, iv);
 #pragma unroll
                 for (int e = 0; e < NG; ++e) {
                     if (S::kTwice && e % B == 0) {
                         load_s(e);
                         if (e + B >= NG) warp_arrive(&bar.s_free[buf]);
                     }
-                    if (e < groups) {
-                        const int c = 16 * e + col0;
-                        float2 big = *reinterpret_cast<const float2*>(&mx[buf][0][c]);
+                    const float4 f = *reinterpret_cast<const float4*>(&turn_s[warp][8 * e + pair2]);
+                    const float2 a = *reinterpret_cast<const float2*>(&alpha_s[buf][warp][8 * e + pair2]);
+                    uint64_t p[4];
+                    uint32_t hi[4], lo[4];
 #pragma unroll
-                        for (int d = 1; d < 4; ++d) {
-                            const float2 x = *reinterpret_cast<const float2*>(&mx[buf][d][c]);
-                            big = make_float2(fmaxf(big.x, x.x), fmaxf(big.y, x.y));
-                        }
-                        const float2 unit = *reinterpret_cast<const float2*>(&unit_s[c]);
-                        float p[2][4];
-#pragma unroll
-                        for (int d = 0; d < 2; ++d) {
-                            const float now = fmaxf(m[2 * e + d], d ? big.y : big.x), at = now == -INFINITY ? 0.0f : now;
-                            const float f = fmaxf(__fmul_rn(d ? unit.y : unit.x, ks), 1e-37f), up = __fadd_rn(__fsub_rn(kQ8Up, at), lv);
-                            alpha[2 * e + d] = tree_exp2(__fsub_rn(m[2 * e + d], at));  // 0 for m = -inf
-                            m[2 * e + d] = now;
-#pragma unroll
-                            for (int c2 = 0; c2 < 4; ++c2) p[d][c2] = tree_exp2(__fmaf_rn(s[e % B][2 * c2 + d], f, up));
-                            const float sum = __fadd_rn(__fadd_rn(p[d][0], p[d][1]), __fadd_rn(p[d][2], p[d][3]));
-                            l[2 * e + d] = __fmaf_rn(l[2 * e + d], alpha[2 * e + d], __fmul_rn(sum, iv));
-                        }
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int c2 = 0; c2 < 4; ++c2) tree_split(p[0][c2], p[1][c2], hi[c2], lo[c2]);
-                        st_matrix_turned(to + 2048 * e, hi[0], hi[1], hi[2], hi[3]);
-                        st_matrix_turned(to + 2048 * e + S::kPart, lo[0], lo[1], lo[2], lo[3]);
+                    for (int c = 0; c < 4; ++c) {
+                        const float2 x = unpair(fma2(pair(s[e % B][2 * c], s[e % B][2 * c + 1]), pair(f.x, f.z), pair(f.y, f.w)));
+                        const float p0 = tree_exp2(x.x), p1 = tree_exp2(x.y);
+                        p[c] = pair(p0, p1);
+                        tree_split(p0, p1, hi[c], lo[c]);
                     }
+                    const uint64_t sum = add2(add2(p[0], p[1]), add2(p[2], p[3]));
+                    l[e] = fma2(sum, iv2, fma2(l[e], pair(a.x, a.y), 0));
+                    st_matrix_turned(to + 2048 * e, hi[0], hi[1], hi[2], hi[3]);
+                    st_matrix_turned(to + 2048 * e + S::kPart, lo[0], lo[1], lo[2], lo[3]);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.p_full[i % S::kWeights]);
-                ++kc;
-                if (kc == v.chunk || k + 1 == t.tiles) {  // the chunk's last tile
-                    take(i, kc == 1);
-#pragma unroll
-                    for (int e = 0; e < 2 * NG; ++e)
-#pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) l[e] = __fadd_rn(l[e], __shfl_xor_sync(0xffffffffu, l[e], d));
-                    float* ml = part_ml + 8 * (pr + col0);
-                    float* po = part_o + (pr + col0) * kHeadDim + 32 * quad + (lane >> 2);
+                if (kc > 0) take(i - 1);
+                if (++kc == v.chunk || k + 1 == t.tiles) {  // the chunk's last tile
+                    take(i);
+                    float* ml = part_ml + 8 * (pr + 8 * half);
+                    float* po = part_o + (pr + 8 * half + pair2) * kHeadDim + 32 * quad + (lane >> 2);
                     asm volatile("" : "+l"(ml), "+l"(po));  // (one address each, not one for every store)
-                    const int left = ok ? R - col0 : 0;
+                    const int left = ok ? R - 8 * half : 0;
 #pragma unroll
-                    for (int e = 0; e < 2 * NG; ++e) {
-                        const int c = 16 * (e >> 1) + (e & 1);
-                        if (c < left) {
-                            if ((lane >> 2) == 0) {
-                                ml[8 * c + 4 + quad] = l[e];
-                                if (quad == 0) ml[8 * c] = m[e];
+                    for (int e = 0; e < NG; ++e) {
+                        const float2 mine = unpair(l[e]);
+                        float x[2] = {mine.x, mine.y};
+#pragma unroll
+                        for (int d = 0; d < 2; ++d) {
+#pragma unroll
+                            for (int f = 4; f < 32; f <<= 1) x[d] = __fadd_rn(x[d], __shfl_xor_sync(0xffffffffu, x[d], f));
+                            const int c = 16 * e + d;
+                            if (c + pair2 < left) {
+                                if ((lane >> 2) == 0) ml[8 * (c + pair2) + 4 + quad] = x[d];
+#pragma unroll
+                                for (int f = 0; f < 4; ++f) {
+                                    const float2 y = unpair(o[e][f]);
+                                    po[c * kHeadDim + 8 * f] = d ? y.y : y.x;
+                                }
                             }
-#pragma unroll
-                            for (int d = 0; d < 4; ++d) po[c * kHeadDim + 8 * d] = o[e >> 1][2 * d + (e & 1)];
                         }
+                    }
+#pragma unroll
+                    for (int e = 0; e < kMine; ++e) {
+                        const int at = lane + 32 * e, c = 16 * (at >> 3) + (at & 7);
+                        if (quad == 0 && at < kCols && c < left) ml[8 * c] = m[e];
                     }
                     kc = 0;
                     pr += (int64_t)Hkv * R;
@@ -906,7 +937,7 @@ cudaError_t launch_q8kv_attention(const float* q, const Q8Batch& b, int Hq, int 
         Q8Maps maps{};
         if (!q8_maps(b, Hkv, &maps)) return cudaErrorInvalidValue;
         const auto launch = rows <= 16 ? launch_chunks<1> : rows <= 32 ? launch_chunks<2> : rows <= 48 ? launch_chunks<3>
-                            : rows <= 80 ? launch_chunks<5> : launch_chunks<8>;
+                            : rows <= 64 ? launch_chunks<4> : rows <= 80 ? launch_chunks<5> : rows <= 96 ? launch_chunks<6> : launch_chunks<8>;
         const cudaError_t e = launch(maps, q, b, Hq, Hkv, units, runs, sc, part_o, part_ml, s);
         if (e != cudaSuccess) return e;
     }
