@@ -10,6 +10,8 @@
 // into chunks of 128-key tiles; each chunk yields (m, l, sum e^(s - m) v) per row, and
 // the merge adds the chunks in order, then the tail's keys and the path's.  A
 // node's bits follow from its prefix and its path alone.
+#include <limits.h>
+
 #include <algorithm>
 #include <cmath>
 
@@ -23,6 +25,7 @@
 namespace luce {
 
 constexpr int kQ8MaxChunks = 160;
+constexpr int kQ8Ctas = 304;  // the CTAs that a cut aims at
 
 // A chunk's weights, and so its sums, are 2^15 e^(s - m): the tree attention's
 // reason, f16 has no digits below 2^-24.
@@ -34,7 +37,31 @@ struct Q8Scale {
     float sign, log2;
 };
 
-int q8kv_max_chunks(int max_sealed, int Hkv) { return max_sealed > 0 ? tree_max_chunks(std::max(max_sealed, kQ8Page), Hkv) : 0; }
+// Tiles of a chunk for a view of nt tiles: of the cuts that fill the kernel's CTAs
+// (kQ8Ctas of them where rows are few, half as many with twice the warps where they
+// are many) 1, 2, 3 or 4 times the cheapest is taken, a chunk costing its tiles and about one more
+// (its q, its results).  A function of the tiles and the KV heads alone, so that a
+// row's sums are cut the same way whatever else is in the call.
+static int q8_chunk_tiles(int nt, int Hkv)
+{
+    int best = nt, least = INT_MAX;
+    for (int rounds = 1; rounds <= 4; ++rounds) {
+        const int n = std::min({kQ8Ctas * rounds / Hkv, nt, kQ8MaxChunks});
+        if (n < 1) continue;
+        const int tiles = (nt + n - 1) / n;
+        const int cost = (Hkv * n + kQ8Ctas - 1) / kQ8Ctas * (tiles + 1);
+        if (cost < least) {
+            least = cost;
+            best = tiles;
+        }
+    }
+    return std::max(best, 1);
+}
+
+int q8kv_max_chunks(int max_sealed, int Hkv)
+{
+    return std::min({(max_sealed + kQ8Page - 1) / kQ8Page, kQ8MaxChunks, std::max(1, 4 * kQ8Ctas / Hkv)});
+}
 
 // A chunk's row of results: part_o [row][128] and part_ml [row][8] = (m, three unused,
 // l of the tiles' first to fourth block), the sums times 2^15.
@@ -56,7 +83,7 @@ int64_t q8kv_chunks(Q8Batch& b, int Hq, int Hkv)
             if (v.front >= v.back) v.front = v.back = all;
         }
         v.n_tile = v.front + all - v.back;
-        v.chunk = v.n_tile ? tree_chunk_keys(v.n_tile * kQ8Page, Hkv) / kQ8Page : 1;
+        v.chunk = v.n_tile ? q8_chunk_tiles(v.n_tile, Hkv) : 1;
         v.n_chunk = (v.n_tile + v.chunk - 1) / v.chunk;
         v.part0 = part;
         part += (int64_t)v.n_chunk * v.n_nodes * Hq;
@@ -69,39 +96,46 @@ __device__ __forceinline__ int q8_tile_key(const Q8View& v, int t) { return (t <
 
 // ---------------------------------------------------------------- chunks
 
-// 16 warps: 8 on scores, weights and sums, 4 that turn codes into f16, one that
-// feeds the tiles, one that issues the products, one that holds tensor memory.
-// 512 threads are launched with 128 registers each; the warps on scores get 208,
-// the turning ones 56, the last four 40: 256 * 208 + 128 * 56 + 128 * 40 = 65,536.
-constexpr int kQ8Threads = 512;
 constexpr int kQ8ScaleSlots = 16;  // tiles whose scales are held: more than lie between the producer and the weights
 
 __device__ unsigned int g_q8kv_wait_timeouts;
 
-// Sizes of a kernel for up to 16 NG rows of a KV head.
-template <int NG>
+// Sizes of a kernel for up to 16 NG rows of a KV head.  4 PARTS warps form scores into
+// weights and add up sums, each with 32 keys and a PARTS-th of the rows; four turn
+// codes into f16, and of the last four one feeds the tiles, one issues the products
+// and one holds tensor memory.
+template <int NG, int PARTS>
 struct Q8Shape {
     static constexpr int kRows = 16 * NG;                      // columns of the products
-    static constexpr int kStages = NG == 1 ? 6 : NG == 2 ? 5 : NG == 3 ? 4 : NG <= 6 ? 3 : 2;  // tiles of K, and of V, in flight
-    static constexpr int kTurned = NG <= 5 ? 2 : 1;            // tiles of K, and of V, in tensor memory
-    static constexpr int kWeights = NG <= 5 ? 2 : 1;           // tiles of weights in shared memory
-    static constexpr bool kTwice = NG > 6;                     // scores are read twice, not held while O is added
+    static constexpr int kParts = PARTS;
+    static constexpr int kGroups = 2 * NG / PARTS;             // of eight columns, of a part
+    static constexpr int kCols = 8 * kGroups;
+    static constexpr int kWarps = 4 * PARTS;
+    static constexpr int kThreads = 32 * (kWarps + 8);
+    static constexpr int kCtas = PARTS == 1 ? 2 : 1;           // of a multiprocessor
+    // registers of a thread on weights; 56 of a turning one and 40 of the others: 30,720
+    // of a CTA launched with 80 each (twice), 65,536 with 128, 61,440 with 80
+    static constexpr int kRegs = PARTS == 1 ? 144 : PARTS == 2 ? 208 : 96;
+    static constexpr int kSlots = NG == 1 ? 5 : NG == 2 ? 4 : NG == 3 ? 8 : NG == 4 ? 7 : NG == 6 ? 4 : 5;  // tiles of K or V in flight
+    static constexpr int kTurnedK = NG == 2 || NG == 8 ? 1 : 2, kTurnedV = NG == 3 || NG == 4 ? 2 : 1;       // in tensor memory
+    static constexpr int kWeights = NG == 3 || NG == 4 || NG == 6 ? 2 : 1;  // tiles of weights in shared memory
+    static constexpr bool kTwice = NG == 8;                    // scores are read twice, not held while maxima are found
     static constexpr int kPart = kRows * kHeadDim * 2;         // bytes of one part of q, or of the weights
-    static constexpr uint32_t kColK = 0, kColV = 64 * kTurned, kColS = 128 * kTurned, kColO = kColS + 2 * kRows;
-    static constexpr int kBytes = kStages * 2 * kQ8PageBytes + (2 + 2 * kWeights) * kPart + 1024;
-    static_assert(kColO + kRows <= 512, "tensor memory");
+    static constexpr uint32_t kColK = 0, kColV = 64 * kTurnedK, kColS = kColV + 64 * kTurnedV, kColO = kColS + 2 * kRows;
+    static constexpr uint32_t kTmem = 512 / kCtas;
+    static constexpr int kBytes = kSlots * kQ8PageBytes + (2 + 2 * kWeights) * kPart + 1024;
+    static_assert(kColO + kRows <= kTmem && 2 * NG % PARTS == 0, "tensor memory");
 };
 
 struct Q8Maps {
     CUtensorMap k[4], v[4];
 };
 
-template <int NG>
+template <typename S>
 struct Q8Bars {
-    using S = Q8Shape<NG>;
-    uint64_t k_full[S::kStages], k_empty[S::kStages], v_full[S::kStages], v_empty[S::kStages];
-    uint64_t ka_full[S::kTurned], ka_free[S::kTurned];   // K of a tile is f16 in tensor memory; has been multiplied
-    uint64_t va_full[S::kTurned], va_free[S::kTurned];
+    uint64_t full[S::kSlots], empty[S::kSlots];          // a tile of K or V is there; has been turned
+    uint64_t ka_full[S::kTurnedK], ka_free[S::kTurnedK];  // K of a tile is f16 in tensor memory; has been multiplied
+    uint64_t va_full[S::kTurnedV], va_free[S::kTurnedV];
     uint64_t s_full[2], s_free[2];                       // S of a tile is complete; has been read
     uint64_t p_full[S::kWeights], p_free[S::kWeights];   // its weights are in place; have been multiplied
     uint64_t o_full, o_free;                             // O of a tile is complete; has been read
@@ -179,15 +213,14 @@ __device__ __forceinline__ void q8_half_codes(uint32_t w, uint32_t& lo, uint32_t
     asm("{ .reg .b32 n; mov.b32 n, 0x64806480; sub.rn.f16x2 %0, %1, n; }" : "=r"(hi) : "r"(b));
 }
 
-// The producer: tiles and scales of the CTA's runs, in order.  Returns the tiles
-// issued.
-template <int NG>
+// The producer: tiles (K and V in turn) and scales of the CTA's runs, in order.
+// Returns the tiles of K and V issued.
+template <typename S>
 __device__ int q8_produce(const Q8Maps& maps, const Q8Batch& b, int Hkv, const Q8Share& w, uint8_t* tiles, float (*scales)[8],
-                          Q8Bars<NG>& bar)
+                          Q8Bars<S>& bar)
 {
-    constexpr int kStages = Q8Shape<NG>::kStages;
     unsigned int* late = &g_q8kv_wait_timeouts;
-    int i = 0;
+    int i = 0;  // tiles of K and V
     pdl_wait();
     pdl_trigger();
     q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
@@ -197,34 +230,27 @@ __device__ int q8_produce(const Q8Maps& maps, const Q8Batch& b, int Hkv, const Q
             return v.table ? ld_placed_i(v.table + span) : span;
         };
         int next = page_of(0);
-        for (int k = 0; k < t.tiles; ++k, ++i) {
-            const int st = i % kStages, sl = i % kQ8ScaleSlots;
-            const uint32_t free = ((i / kStages) & 1) ^ 1;
+        for (int k = 0; k < t.tiles; ++k) {
             int page = next;
             if (k + 1 < t.tiles) next = page_of(k + 1);  // (on its way while this tile's place becomes free)
             const bool in = page >= 0 && page < v.n_pages;
             if (!in) page = v.n_pages;                   // outside the map: zeros
-            uint8_t* kt = tiles + st * 2 * kQ8PageBytes;
-            if (!mbar_wait(&bar.k_empty[st], free, late)) return false;
-            if (in) {
-                mbar_expect_tx(&bar.sc_full[sl], 32);
-                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], 32, [%2];" ::"r"(
-                                 smem_addr(scales[sl])),
-                             "l"(v.scales + page * v.scale_stride + t.g * kQ8PageScales), "r"(smem_addr(&bar.sc_full[sl]))
-                             : "memory");
-            } else {
-                for (int e = 0; e < 8; ++e) scales[sl][e] = 0.0f;
-                mbar_arrive(&bar.sc_full[sl]);
+            for (int kv = 0; kv < 2; ++kv, ++i) {
+                const int st = i % S::kSlots, sl = (i >> 1) % kQ8ScaleSlots;
+                if (!mbar_wait(&bar.empty[st], ((i / S::kSlots) & 1) ^ 1, late)) return false;
+                if (kv == 0 && in) {
+                    mbar_expect_tx(&bar.sc_full[sl], 32);
+                    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], 32, [%2];" ::"r"(
+                                     smem_addr(scales[sl])),
+                                 "l"(v.scales + page * v.scale_stride + t.g * kQ8PageScales), "r"(smem_addr(&bar.sc_full[sl]))
+                                 : "memory");
+                } else if (kv == 0) {
+                    for (int e = 0; e < 8; ++e) scales[sl][e] = 0.0f;
+                    mbar_arrive(&bar.sc_full[sl]);
+                }
+                mbar_expect_tx(&bar.full[st], kQ8PageBytes);
+                tma_load_4d(tiles + st * kQ8PageBytes, kv ? &maps.v[t.view] : &maps.k[t.view], 0, 0, t.g, page, &bar.full[st]);
             }
-            mbar_expect_tx(&bar.k_full[st], kQ8PageBytes);
-            tma_load_4d(kt, &maps.k[t.view], 0, 0, t.g, page, &bar.k_full[st]);
-            if (!mbar_wait(&bar.v_empty[st], free, late)) {
-                ring_drain<kStages>(bar.k_full, i + 1, late);
-                ring_drain<kQ8ScaleSlots>(bar.sc_full, i + 1, late);
-                return false;
-            }
-            mbar_expect_tx(&bar.v_full[st], kQ8PageBytes);
-            tma_load_4d(kt + kQ8PageBytes, &maps.v[t.view], 0, 0, t.g, page, &bar.v_full[st]);
         }
         return true;
     });
@@ -252,42 +278,35 @@ __device__ __forceinline__ void q8_turn(const uint8_t* tile, int row, uint32_t t
 }
 
 // The turning warps: K and V of every tile, a row of 128 codes per thread.
-template <int NG>
-__device__ void q8_turn_tiles(int n, const uint8_t* tiles, uint32_t tmem, int quad, int lane, Q8Bars<NG>& bar)
+template <typename S>
+__device__ void q8_turn_tiles(int n, const uint8_t* tiles, uint32_t tmem, int quad, int lane, Q8Bars<S>& bar)
 {
-    using S = Q8Shape<NG>;
     unsigned int* late = &g_q8kv_wait_timeouts;
     const int row = 32 * quad + lane;
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
-    for (int i = 0; i < n; ++i) {
-        const int st = i % S::kStages, to = i % S::kTurned;
-        const uint32_t full = (i / S::kStages) & 1, free = ((i / S::kTurned) & 1) ^ 1;
-        const uint8_t* kt = tiles + st * 2 * kQ8PageBytes;
-        if (!__all_sync(0xffffffffu, mbar_wait(&bar.k_full[st], full, late) && mbar_wait(&bar.ka_free[to], free, late))) return;
+    for (int i = 0; i < 2 * n; ++i) {
+        const int st = i % S::kSlots, j = i >> 1, to = i & 1 ? j % S::kTurnedV : j % S::kTurnedK;
+        const uint32_t free = ((i & 1 ? j / S::kTurnedV : j / S::kTurnedK) & 1) ^ 1;
+        const bool there = mbar_wait(&bar.full[st], (i / S::kSlots) & 1, late) &&
+                           mbar_wait(i & 1 ? &bar.va_free[to] : &bar.ka_free[to], free, late);
+        if (!__all_sync(0xffffffffu, there)) return;
         tm_after();
-        q8_turn(kt, row, lanes + S::kColK + 64 * to);
-        warp_arrive(&bar.ka_full[to]);
-        if (lane == 0) mbar_arrive(&bar.k_empty[st]);
-        if (!__all_sync(0xffffffffu, mbar_wait(&bar.v_full[st], full, late) && mbar_wait(&bar.va_free[to], free, late))) return;
-        tm_after();
-        q8_turn(kt + kQ8PageBytes, row, lanes + S::kColV + 64 * to);
-        warp_arrive(&bar.va_full[to]);
-        if (lane == 0) mbar_arrive(&bar.v_empty[st]);
+        q8_turn(tiles + st * kQ8PageBytes, row, lanes + (i & 1 ? S::kColV : S::kColK) + 64 * to);
+        warp_arrive(i & 1 ? &bar.va_full[to] : &bar.ka_full[to]);
+        if (lane == 0) mbar_arrive(&bar.empty[st]);
     }
 }
 
 // The products, issued by one warp: S of tile i, then O of tile i - 1, so that
 // the tensor cores have the one while the other's weights are formed.  The low
 // parts go first: an accumulation loses digits by the sum's size, and theirs is small.
-template <int NG>
-__device__ void q8_products(const Q8Batch& b, int Hkv, const Q8Share& w, uint32_t q, uint32_t weights, uint32_t tmem,
-                            Q8Bars<NG>& bar)
+template <typename S>
+__device__ void q8_products(const Q8Batch& b, int Hkv, const Q8Share& w, uint32_t q, uint32_t weights, uint32_t tmem, Q8Bars<S>& bar)
 {
-    using S = Q8Shape<NG>;
     unsigned int* late = &g_q8kv_wait_timeouts;
     const uint32_t elected = elect_one();
     int i = 0, heads = 0, last = -1;
-    constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(2 * NG) << 17) | (8u << 24);  // D f32, A and B f16, 128 by 16 NG
+    constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(S::kRows / 8) << 17) | (8u << 24);  // D f32, A and B f16, 128 rows, kRows columns
     // all steps of a product: A in tensor memory from column a, B rows of 256 bytes in two halves
     const uint64_t step = tree_desc(0, 16, 1024);
     auto multiply = [&](uint32_t d, uint32_t a, uint32_t bytes) {
@@ -301,8 +320,8 @@ __device__ void q8_products(const Q8Batch& b, int Hkv, const Q8Share& w, uint32_
                      elected);
     };
     auto sums = [&](int j) {
-        const int to = j % S::kTurned, p = j % S::kWeights;
-        const bool there = mbar_wait(&bar.va_full[to], (j / S::kTurned) & 1, late) &&
+        const int to = j % S::kTurnedV, p = j % S::kWeights;
+        const bool there = mbar_wait(&bar.va_full[to], (j / S::kTurnedV) & 1, late) &&
                            mbar_wait(&bar.p_full[p], (j / S::kWeights) & 1, late) &&
                            (j == 0 || mbar_wait(&bar.o_free, (j - 1) & 1, late));
         if (!__all_sync(0xffffffffu, there)) return false;  // (the warp leaves as one)
@@ -322,8 +341,8 @@ __device__ void q8_products(const Q8Batch& b, int Hkv, const Q8Share& w, uint32_
             open = false;
         }
         for (int k = 0; ok && k < t.tiles; ++k, ++i) {
-            const int to = i % S::kTurned;
-            const bool there = mbar_wait(&bar.ka_full[to], (i / S::kTurned) & 1, late) &&
+            const int to = i % S::kTurnedK;
+            const bool there = mbar_wait(&bar.ka_full[to], (i / S::kTurnedK) & 1, late) &&
                                mbar_wait(&bar.s_free[i & 1], ((i >> 1) & 1) ^ 1, late);
             if (!(ok = __all_sync(0xffffffffu, there))) break;
             tm_after();
@@ -373,60 +392,60 @@ __device__ __forceinline__ void q8_maxima(float* v, int lane, int& first)
 }
 constexpr int q8_left(int n, int off = 16) { return off < 4 ? n : q8_left(n % 2 == 0 ? n / 2 : n, off / 2); }
 
-// One CTA an SM, each with its share of all chunks.
-template <int NG>
-__global__ void __launch_bounds__(kQ8Threads, 1)
+// kCtas CTAs an SM, each with its share of all chunks.
+template <int NG, int PARTS>
+__global__ void __launch_bounds__(Q8Shape<NG, PARTS>::kThreads, Q8Shape<NG, PARTS>::kCtas)
 q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __grid_constant__ Q8Batch b, int Hq, int Hkv, int units,
                   bool runs, Q8Scale scale, float* __restrict__ part_o, float* __restrict__ part_ml)
 {
-    using S = Q8Shape<NG>;
+    using S = Q8Shape<NG, PARTS>;
     extern __shared__ uint8_t q8_smem[];
     uint8_t* tiles = q8_smem + ((1024u - (smem_addr(q8_smem) & 1023u)) & 1023u);
-    uint8_t* qs = tiles + S::kStages * 2 * kQ8PageBytes;  // q: low and high part, two halves of the dims each
+    uint8_t* qs = tiles + S::kSlots * kQ8PageBytes;       // q: high and low part, two halves of the dims each
     uint8_t* ps = qs + 2 * S::kPart;                      // weights, the same way
-    __shared__ Q8Bars<NG> bar;
+    __shared__ Q8Bars<S> bar;
     __shared__ uint32_t tmem_at;
     __shared__ __align__(16) float scales[kQ8ScaleSlots][8];
-    // by half: its columns are the groups of eight 2 e + half, numbered through
-    __shared__ float mx[2][2][4][S::kRows / 2];           // the columns' maxima of a tile's blocks, by tile parity
-    __shared__ float unit_s[2][S::kRows / 2];             // a score's power of two per unit of its product
-    __shared__ __align__(8) int from_s[2][S::kRows / 2];  // the first key in the row's window
+    // by part: its columns are the groups of eight PARTS e + part, numbered through
+    __shared__ float mx[2][PARTS][4][S::kCols];           // the columns' maxima of a tile's blocks, by tile parity
+    __shared__ float unit_s[PARTS][S::kCols];             // a score's power of two per unit of its product
+    __shared__ __align__(8) int from_s[PARTS][S::kCols];  // the first key in the row's window
     // by warp: what turns a column's products into exponents (a factor, an offset),
     // and what O so far is multiplied by, by tile parity
-    __shared__ __align__(16) float2 turn_s[8][S::kRows / 2];
-    __shared__ __align__(8) float alpha_s[2][8][S::kRows / 2];
-    __shared__ volatile int bail[2][2];                 // a wait of the half's warps expired, by tile parity
+    __shared__ __align__(16) float2 turn_s[S::kWarps][S::kCols];
+    __shared__ __align__(8) float alpha_s[2][S::kWarps][S::kCols];
+    __shared__ volatile int bail[PARTS][2];               // a wait of the part's warps expired, by tile parity
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (warp == 14) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_at)), "r"(512u));
+    if (warp == S::kWarps + 6) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_at)), "r"(S::kTmem));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     if (tid == 0) {
-        for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(&bar.k_full[i], 1);
-            mbar_init(&bar.v_full[i], 1);
-            mbar_init(&bar.k_empty[i], 4);
-            mbar_init(&bar.v_empty[i], 4);
+        for (int i = 0; i < S::kSlots; ++i) {
+            mbar_init(&bar.full[i], 1);
+            mbar_init(&bar.empty[i], 4);
         }
-        for (int i = 0; i < S::kTurned; ++i) {
+        for (int i = 0; i < S::kTurnedK; ++i) {
             mbar_init(&bar.ka_full[i], 4);
-            mbar_init(&bar.va_full[i], 4);
             mbar_init(&bar.ka_free[i], 1);
+        }
+        for (int i = 0; i < S::kTurnedV; ++i) {
+            mbar_init(&bar.va_full[i], 4);
             mbar_init(&bar.va_free[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.s_full[i], 1);
-            mbar_init(&bar.s_free[i], 8);
-            bail[i][0] = bail[i][1] = 0;
+            mbar_init(&bar.s_free[i], S::kWarps);
         }
+        for (int i = 0; i < PARTS; ++i) bail[i][0] = bail[i][1] = 0;
         for (int i = 0; i < S::kWeights; ++i) {
-            mbar_init(&bar.p_full[i], 8);
+            mbar_init(&bar.p_full[i], S::kWarps);
             mbar_init(&bar.p_free[i], 1);
         }
         for (int i = 0; i < kQ8ScaleSlots; ++i) mbar_init(&bar.sc_full[i], 1);
         mbar_init(&bar.o_full, 1);
-        mbar_init(&bar.o_free, 8);
-        mbar_init(&bar.q_full, 8);
+        mbar_init(&bar.o_free, S::kWarps);
+        mbar_init(&bar.q_full, S::kWarps);
         mbar_init(&bar.done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -447,59 +466,58 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
         w = Q8Share{(int)((int64_t)units * blockIdx.x / gridDim.x), (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x), 0};
     unsigned int* late = &g_q8kv_wait_timeouts;
 
-    if (warp >= 12) {
+    if (warp >= S::kWarps + 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        if (warp == 12 && lane == 0) {
-            const int n = q8_produce<NG>(maps, b, Hkv, w, tiles, scales, bar);
-            ring_drain<S::kStages>(bar.k_full, n, late);
-            ring_drain<S::kStages>(bar.v_full, n, late);
-            ring_drain<kQ8ScaleSlots>(bar.sc_full, n, late);
+        if (warp == S::kWarps + 4 && lane == 0) {
+            const int n = q8_produce(maps, b, Hkv, w, tiles, scales, bar);
+            ring_drain<S::kSlots>(bar.full, n, late);
+            ring_drain<kQ8ScaleSlots>(bar.sc_full, (n + 1) / 2, late);
         }
-        if (warp == 13) q8_products<NG>(b, Hkv, w, smem_addr(qs), smem_addr(ps), tmem, bar);
+        if (warp == S::kWarps + 5) q8_products(b, Hkv, w, smem_addr(qs), smem_addr(ps), tmem, bar);
         __syncwarp();
-    } else if (warp >= 8) {
+    } else if (warp >= S::kWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         int n = 0;
         q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
             n += t.tiles;
             return true;
         });
-        q8_turn_tiles<NG>(n, tiles, tmem, warp & 3, lane, bar);
+        q8_turn_tiles(n, tiles, tmem, warp & 3, lane, bar);
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegs));
         // The warp's keys are its block of the tile, 32 quad ..; its columns the groups of
-        // eight 2 e + half, e < NG.  Of them a thread has keys lane / 4 + 8 i and columns 2 (lane
+        // eight PARTS e + part, e < G.  Of them a thread has keys lane / 4 + 8 i and columns 2 (lane
         // % 4) and the next: of O the same columns, dims 32 quad + lane / 4 + 8 i.  What is
         // the same for a column's keys (maximum, factor, correction) a lane forms per
         // column, and the threads pick it up from shared memory: formed by each
         // thread for its own columns it took twice the instructions of the weights.
-        constexpr int kCols = S::kRows / 2, kMine = (kCols + 31) / 32;  // columns of a half, and of a lane
-        const int half = warp >> 2, quad = warp & 3, GQ = Hq / Hkv, pair2 = 2 * (lane & 3);
-        const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16) + 8 * half;
-        const uint32_t row_at = (quad >> 1) * (S::kPart / 2) + half * 1024 + (lane & 7) * 128 +
+        constexpr int G = S::kGroups, kCols = S::kCols, kMine = (kCols + 31) / 32;  // (columns of a lane)
+        const int part = warp >> 2, quad = warp & 3, GQ = Hq / Hkv, pair2 = 2 * (lane & 3);
+        const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16) + 8 * part;
+        const uint32_t row_at = (quad >> 1) * (S::kPart / 2) + part * 1024 + (lane & 7) * 128 +
                                 (((4 * (quad & 1) + (lane >> 3)) ^ (lane & 7)) << 4);  // where its keys' weights go
-        uint64_t o[NG][4], l[NG];      // pairs of columns
+        uint64_t o[G][4], l[G];      // pairs of columns
         float m[kMine];                // of columns lane + 32 e
         int i = 0, last = -1, R = 0;
         bool ok = true;
-        auto half_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); };
+        auto part_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory"); };
         // adds O of tile j
         auto take = [&](int j) {
             ok = __all_sync(0xffffffffu, ok && mbar_wait(&bar.o_full, j & 1, late));
             tm_after();
-            constexpr int B = NG <= 3 ? NG : 2;  // groups at a time
+            constexpr int B = G <= 3 ? G : 2;  // groups at a time
 #pragma unroll
-            for (int e0 = 0; e0 < NG; e0 += B) {
+            for (int e0 = 0; e0 < G; e0 += B) {
                 float x[B][8];
 #pragma unroll
-                for (int e = e0; e < e0 + B && e < NG; ++e) {
-                    tm_ld_frag(lanes + S::kColO + 16 * e, x[e - e0]);
-                    tm_ld_frag(lanes + (16u << 16) + S::kColO + 16 * e, x[e - e0] + 4);
+                for (int e = e0; e < e0 + B && e < G; ++e) {
+                    tm_ld_frag(lanes + S::kColO + 8 * PARTS * e, x[e - e0]);
+                    tm_ld_frag(lanes + (16u << 16) + S::kColO + 8 * PARTS * e, x[e - e0] + 4);
                 }
                 tm_loaded<8 * B>(&x[0][0]);
-                if (e0 + B >= NG) warp_arrive(&bar.o_free);
+                if (e0 + B >= G) warp_arrive(&bar.o_free);
 #pragma unroll
-                for (int e = e0; e < e0 + B && e < NG; ++e) {
+                for (int e = e0; e < e0 + B && e < G; ++e) {
                     const float2 a = *reinterpret_cast<const float2*>(&alpha_s[j & 1][warp][8 * e + pair2]);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) o[e][c] = fma2(o[e][c], pair(a.x, a.y), pair(x[e - e0][2 * c], x[e - e0][2 * c + 1]));
@@ -512,13 +530,13 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                 if (last < 0) pdl_wait();
                 last = t.view * Hkv + t.g;
                 R = v.n_nodes * GQ;
-                half_sync();                   // (the last head's units have been read)
-                const int part = tid & 15;
-                for (int j = 0; j < NG; ++j) {
-                    const int in8 = (tid & 127) >> 4, c = 16 * j + 8 * half + in8;
+                part_sync();                   // (the last head's units have been read)
+                const int piece = tid & 15;
+                for (int j = 0; j < G; ++j) {
+                    const int in8 = (tid & 127) >> 4, c = 8 * (PARTS * j + part) + in8;
                     float4 x = make_float4(0, 0, 0, 0), y = x;
                     if (c < R) {
-                        const float* p = q + ((int64_t)(v.row0 + c / GQ) * Hq + t.g * GQ + c % GQ) * kHeadDim + 8 * part;
+                        const float* p = q + ((int64_t)(v.row0 + c / GQ) * Hq + t.g * GQ + c % GQ) * kHeadDim + 8 * piece;
                         x = ld_placed_f4(p);
                         y = ld_placed_f4(p + 4);
                     }
@@ -534,17 +552,17 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                     tree_split(__fmul_rn(x.z, into), __fmul_rn(x.w, into), hi.y, lo.y);
                     tree_split(__fmul_rn(y.x, into), __fmul_rn(y.y, into), hi.z, lo.z);
                     tree_split(__fmul_rn(y.z, into), __fmul_rn(y.w, into), hi.w, lo.w);
-                    uint8_t* to = qs + (part >> 3) * (S::kPart / 2) + (c >> 3) * 1024 + (c & 7) * 128 + (((part & 7) ^ (c & 7)) << 4);
+                    uint8_t* to = qs + (piece >> 3) * (S::kPart / 2) + (c >> 3) * 1024 + (c & 7) * 128 + (((piece & 7) ^ (c & 7)) << 4);
                     *reinterpret_cast<uint4*>(to) = hi;
                     *reinterpret_cast<uint4*>(to + S::kPart) = lo;
-                    if (part == 0) {
-                        unit_s[half][8 * j + in8] = __fmul_rn(scale.log2, __int_as_float((127 + exp) << 23));
+                    if (piece == 0) {
+                        unit_s[part][8 * j + in8] = __fmul_rn(scale.log2, __int_as_float((127 + exp) << 23));
                         const int node = min(c / GQ, v.n_nodes - 1);
-                        from_s[half][8 * j + in8] = v.sealed + v.tail + b.row[v.row0 + node].n_path - v.window;
+                        from_s[part][8 * j + in8] = v.sealed + v.tail + b.row[v.row0 + node].n_path - v.window;
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                half_sync();
+                part_sync();
                 if (lane == 0) mbar_arrive(&bar.q_full);
             }
             int64_t pr = v.part0 + ((int64_t)t.c * Hkv + t.g) * R;  // the chunk's rows of results
@@ -554,7 +572,7 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                 const float* sc = scales[i % kQ8ScaleSlots];
                 if (kc == 0) {  // (what the last chunk left may be anything: it is not multiplied by 0)
 #pragma unroll
-                    for (int e = 0; e < NG; ++e) {
+                    for (int e = 0; e < G; ++e) {
                         l[e] = 0;
 #pragma unroll
                         for (int c = 0; c < 4; ++c) o[e][c] = 0;
@@ -576,13 +594,13 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                 const float iv = __frcp_rn(vs);
                 const bool masked = v.window > 0 && key0 < v.sealed + v.tail + v.n_nodes - v.window && key0 + kQ8Page > v.sinks;
                 // scores, `B` groups at a time: held from the maxima on where there are few, else read twice
-                constexpr int B = S::kTwice ? 4 : NG;
+                constexpr int B = S::kTwice ? 2 : G;
                 float s[B][8];
                 auto load_s = [&](int e0) {
 #pragma unroll
                     for (int e = 0; e < B; ++e) {
-                        tm_ld_frag(lanes + S::kColS + S::kRows * buf + 16 * (e0 + e), s[e]);
-                        tm_ld_frag(lanes + (16u << 16) + S::kColS + S::kRows * buf + 16 * (e0 + e), s[e] + 4);
+                        tm_ld_frag(lanes + S::kColS + S::kRows * buf + 8 * PARTS * (e0 + e), s[e]);
+                        tm_ld_frag(lanes + (16u << 16) + S::kColS + S::kRows * buf + 8 * PARTS * (e0 + e), s[e] + 4);
                     }
                     tm_loaded<8 * B>(&s[0][0]);
                     if (!valid) {
@@ -593,7 +611,7 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                     } else if (masked) {
 #pragma unroll
                         for (int e = 0; e < B; ++e) {
-                            const int2 from = *reinterpret_cast<const int2*>(&from_s[half][8 * (e0 + e) + pair2]);
+                            const int2 from = *reinterpret_cast<const int2*>(&from_s[part][8 * (e0 + e) + pair2]);
 #pragma unroll
                             for (int c = 0; c < 8; ++c) {
                                 const int key = key0 + kQ8Block * quad + (lane >> 2) + 8 * (c >> 1);
@@ -602,9 +620,9 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                         }
                     }
                 };
-                float top[2 * NG];
+                float top[2 * G];
 #pragma unroll
-                for (int e0 = 0; e0 < NG; e0 += B) {
+                for (int e0 = 0; e0 < G; e0 += B) {
                     load_s(e0);
 #pragma unroll
                     for (int e = 0; e < B; ++e) {
@@ -614,11 +632,11 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                 }
                 if (!S::kTwice) warp_arrive(&bar.s_free[buf]);
                 int first = 0;
-                q8_maxima<2 * NG, 16>(top, lane, first);
+                q8_maxima<2 * G, 16>(top, lane, first);
 #pragma unroll
-                for (int e = 0; e < q8_left(2 * NG); ++e) {
+                for (int e = 0; e < q8_left(2 * G); ++e) {
                     const int at = first + e;
-                    mx[buf][half][quad][8 * (at >> 1) + pair2 + (at & 1)] = top[e];
+                    mx[buf][part][quad][8 * (at >> 1) + pair2 + (at & 1)] = top[e];
                 }
                 __syncwarp();
                 float factor[kMine];
@@ -626,18 +644,18 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                 for (int e = 0; e < kMine; ++e)
                     if (lane + 32 * e < kCols) {
                         // (rounded up: no weight is above 2^15 by more than its exponent's own rounding)
-                        float* x = &mx[buf][half][quad][lane + 32 * e];
-                        factor[e] = fmaxf(__fmul_rn(unit_s[half][lane + 32 * e], ks), 1e-37f);
+                        float* x = &mx[buf][part][quad][lane + 32 * e];
+                        factor[e] = fmaxf(__fmul_rn(unit_s[part][lane + 32 * e], ks), 1e-37f);
                         *x = __fadd_ru(__fmul_ru(*x, factor[e]), lv);
                     }
-                // all four warps of a half meet here, an expired wait or not, and leave together
-                if (!ok) bail[half][buf] = 1;
-                half_sync();
-                if (bail[half][buf]) return false;
+                // all four warps of a part meet here, an expired wait or not, and leave together
+                if (!ok) bail[part][buf] = 1;
+                part_sync();
+                if (bail[part][buf]) return false;
 #pragma unroll
                 for (int e = 0; e < kMine; ++e)
                     if (lane + 32 * e < kCols) {
-                        const float* x = &mx[buf][half][0][lane + 32 * e];
+                        const float* x = &mx[buf][part][0][lane + 32 * e];
                         const float now = fmaxf(m[e], max3(fmaxf(x[0], x[kCols]), x[2 * kCols], x[3 * kCols]));
                         const float at = now == -INFINITY ? 0.0f : now;
                         turn_s[warp][lane + 32 * e] = make_float2(factor[e], __fadd_rn(__fsub_rn(kQ8Up, at), lv));
@@ -649,10 +667,10 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                 const uint32_t to = smem_addr(ps) + (i % S::kWeights) * 2 * S::kPart + row_at;
                 const uint64_t iv2 = pair(iv, iv);
 #pragma unroll
-                for (int e = 0; e < NG; ++e) {
+                for (int e = 0; e < G; ++e) {
                     if (S::kTwice && e % B == 0) {
                         load_s(e);
-                        if (e + B >= NG) warp_arrive(&bar.s_free[buf]);
+                        if (e + B >= G) warp_arrive(&bar.s_free[buf]);
                     }
                     const float4 f = *reinterpret_cast<const float4*>(&turn_s[warp][8 * e + pair2]);
                     const float2 a = *reinterpret_cast<const float2*>(&alpha_s[buf][warp][8 * e + pair2]);
@@ -667,8 +685,8 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                     }
                     const uint64_t sum = add2(add2(p[0], p[1]), add2(p[2], p[3]));
                     l[e] = fma2(sum, iv2, fma2(l[e], pair(a.x, a.y), 0));
-                    st_matrix_turned(to + 2048 * e, hi[0], hi[1], hi[2], hi[3]);
-                    st_matrix_turned(to + 2048 * e + S::kPart, lo[0], lo[1], lo[2], lo[3]);
+                    st_matrix_turned(to + 1024 * PARTS * e, hi[0], hi[1], hi[2], hi[3]);
+                    st_matrix_turned(to + 1024 * PARTS * e + S::kPart, lo[0], lo[1], lo[2], lo[3]);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
@@ -676,19 +694,19 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                 if (kc > 0) take(i - 1);
                 if (++kc == v.chunk || k + 1 == t.tiles) {  // the chunk's last tile
                     take(i);
-                    float* ml = part_ml + 8 * (pr + 8 * half);
-                    float* po = part_o + (pr + 8 * half + pair2) * kHeadDim + 32 * quad + (lane >> 2);
+                    float* ml = part_ml + 8 * (pr + 8 * part);
+                    float* po = part_o + (pr + 8 * part + pair2) * kHeadDim + 32 * quad + (lane >> 2);
                     asm volatile("" : "+l"(ml), "+l"(po));  // (one address each, not one for every store)
-                    const int left = ok ? R - 8 * half : 0;
+                    const int left = ok ? R - 8 * part : 0;
 #pragma unroll
-                    for (int e = 0; e < NG; ++e) {
+                    for (int e = 0; e < G; ++e) {
                         const float2 mine = unpair(l[e]);
                         float x[2] = {mine.x, mine.y};
 #pragma unroll
                         for (int d = 0; d < 2; ++d) {
 #pragma unroll
                             for (int f = 4; f < 32; f <<= 1) x[d] = __fadd_rn(x[d], __shfl_xor_sync(0xffffffffu, x[d], f));
-                            const int c = 16 * e + d;
+                            const int c = 8 * PARTS * e + d;
                             if (c + pair2 < left) {
                                 if ((lane >> 2) == 0) ml[8 * (c + pair2) + 4 + quad] = x[d];
 #pragma unroll
@@ -701,7 +719,7 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                     }
 #pragma unroll
                     for (int e = 0; e < kMine; ++e) {
-                        const int at = lane + 32 * e, c = 16 * (at >> 3) + (at & 7);
+                        const int at = lane + 32 * e, c = 8 * PARTS * (at >> 3) + (at & 7);
                         if (quad == 0 && at < kCols && c < left) ml[8 * c] = m[e];
                     }
                     kc = 0;
@@ -713,7 +731,7 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
     }
     tm_before();
     __syncthreads();
-    if (warp == 14) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+    if (warp == S::kWarps + 6) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kTmem));
 }
 
 cudaError_t read_q8kv_wait_timeouts(uint32_t* count, bool reset)
@@ -747,17 +765,18 @@ static bool q8_maps(const Q8Batch& b, int Hkv, Q8Maps* maps)
     return true;
 }
 
-template <int NG>
+template <int NG, int PARTS>
 static cudaError_t launch_chunks(const Q8Maps& maps, const float* q, const Q8Batch& b, int Hq, int Hkv, int64_t units, bool runs,
                                  const Q8Scale& scale, float* part_o, float* part_ml, cudaStream_t s)
 {
+    using S = Q8Shape<NG, PARTS>;
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     static std::atomic<bool> done[kMaxDevices];
-    cudaError_t e = set_smem_once(q8kv_chunk_kernel<NG>, Q8Shape<NG>::kBytes, done);
+    cudaError_t e = set_smem_once(q8kv_chunk_kernel<NG, PARTS>, S::kBytes, done);
     if (e == cudaSuccess)
-        e = launch_pdl_smem(q8kv_chunk_kernel<NG>, dim3((unsigned)std::min<int64_t>(sms, units)), dim3(kQ8Threads), Q8Shape<NG>::kBytes, s,
-                            maps, q, b, Hq, Hkv, (int)units, runs, scale, part_o, part_ml);
+        e = launch_pdl_smem(q8kv_chunk_kernel<NG, PARTS>, dim3((unsigned)std::min<int64_t>(sms * S::kCtas, units)), dim3(S::kThreads),
+                            S::kBytes, s, maps, q, b, Hq, Hkv, (int)units, runs, scale, part_o, part_ml);
     if (e == cudaSuccess) count_launches(1);
     return e;
 }
@@ -936,8 +955,8 @@ cudaError_t launch_q8kv_attention(const float* q, const Q8Batch& b, int Hq, int 
     if (units > 0) {
         Q8Maps maps{};
         if (!q8_maps(b, Hkv, &maps)) return cudaErrorInvalidValue;
-        const auto launch = rows <= 16 ? launch_chunks<1> : rows <= 32 ? launch_chunks<2> : rows <= 48 ? launch_chunks<3>
-                            : rows <= 64 ? launch_chunks<4> : rows <= 80 ? launch_chunks<5> : rows <= 96 ? launch_chunks<6> : launch_chunks<8>;
+        const auto launch = rows <= 16 ? launch_chunks<1, 1> : rows <= 32 ? launch_chunks<2, 1> : rows <= 48 ? launch_chunks<3, 2>
+                            : rows <= 64 ? launch_chunks<4, 4> : rows <= 96 ? launch_chunks<6, 4> : launch_chunks<8, 4>;
         const cudaError_t e = launch(maps, q, b, Hq, Hkv, units, runs, sc, part_o, part_ml, s);
         if (e != cudaSuccess) return e;
     }

@@ -122,6 +122,14 @@ def test_one_slot(Hq, Hkv, sealed, tail, kind, n, paged):
     check([s], run([s], [s.paged(rng, layers=2, layer=1) if paged else s.flat()], Hkv))
 
 
+@pytest.mark.parametrize("G,n", [(1, 1), (8, 2), (8, 3), (5, 6), (7, 7), (8, 8), (6, 13), (8, 11), (8, 16)])
+def test_chunks_of_several_tiles(G, n):
+    """Every width of the products, over chunks of more tiles than lie in flight."""
+    rng = np.random.default_rng(G * n)
+    s = Cache(rng, G, 1, 130784 - 4096 * (n % 3), 5, tree_of("random", n, n), window=0 if n % 2 else 100000, sinks=300)
+    check([s], run([s], [s.paged(rng)], 1))
+
+
 def test_longest():
     rng = np.random.default_rng(5)
     s = Cache(rng, 8, 1, 130784, 16, tree_of("random", 16, 3), slack=0)
