@@ -102,8 +102,8 @@ __device__ unsigned int g_q8kv_wait_timeouts;
 
 // Sizes of a kernel for up to 16 NG rows of a KV head.  4 PARTS warps form scores into
 // weights and add up sums, each with 32 keys and a PARTS-th of the rows; four turn
-// codes into f16, and of the last four one feeds the tiles, one issues the products
-// and one holds tensor memory.
+// codes into f16, and of the last four one feeds the tiles, two issue the products and
+// one prepares the next head's q.
 template <int NG, int PARTS>
 struct Q8Shape {
     static constexpr int kRows = 16 * NG;                      // columns of the products
@@ -113,17 +113,20 @@ struct Q8Shape {
     static constexpr int kWarps = 4 * PARTS;
     static constexpr int kThreads = 32 * (kWarps + 8);
     static constexpr int kCtas = PARTS == 1 ? 2 : 1;           // of a multiprocessor
-    // registers of a thread on weights; 56 of a turning one and 40 of the others: 30,720
-    // of a CTA launched with 80 each (twice), 65,536 with 128, 61,440 with 80
-    static constexpr int kRegs = PARTS == 1 ? 144 : PARTS == 2 ? 208 : 96;
-    static constexpr int kSlots = NG == 1 ? 5 : NG == 2 ? 4 : NG == 3 ? 8 : NG == 4 ? 7 : NG == 6 ? 4 : 5;  // tiles of K or V in flight
-    static constexpr int kTurnedK = NG == 2 || NG == 8 ? 1 : 2, kTurnedV = NG == 3 || NG == 4 ? 2 : 1;       // in tensor memory
-    static constexpr int kWeights = NG == 3 || NG == 4 || NG == 6 ? 2 : 1;  // tiles of weights in shared memory
+    // registers of a thread on weights, and of the others: 30,720 of a CTA launched with
+    // 80 each, 65,536 with 128
+    static constexpr int kRegs = PARTS == 1 ? 144 : 200, kOther = PARTS == 1 ? 48 : 56;
+    static constexpr int kSlots = NG == 1 ? 5 : NG == 2 ? 3 : NG == 3 ? 7 : NG == 6 ? 4 : 5;  // tiles of K or V in flight
+    // In tensor memory: one tile of K, which is multiplied as soon as it is there, two
+    // of V, which wait for their weights, and two of scores where there is room
+    static constexpr int kTurnedV = 2, kScores = NG == 2 || NG == 8 ? 1 : 2;
+    static constexpr int kWeights = NG == 3 || NG == 4 ? 2 : 1;  // tiles of weights in shared memory
+    static constexpr int kHeads = NG <= 6 ? 2 : 1;             // heads of q in shared memory
     static constexpr bool kTwice = NG == 8;                    // scores are read twice, not held while maxima are found
     static constexpr int kPart = kRows * kHeadDim * 2;         // bytes of one part of q, or of the weights
-    static constexpr uint32_t kColK = 0, kColV = 64 * kTurnedK, kColS = kColV + 64 * kTurnedV, kColO = kColS + 2 * kRows;
+    static constexpr uint32_t kColK = 0, kColV = 64, kColS = kColV + 64 * kTurnedV, kColO = kColS + kScores * kRows;
     static constexpr uint32_t kTmem = 512 / kCtas;
-    static constexpr int kBytes = kSlots * kQ8PageBytes + (2 + 2 * kWeights) * kPart + 1024;
+    static constexpr int kBytes = kSlots * kQ8PageBytes + 2 * (kHeads + kWeights) * kPart + 1024;
     static_assert(kColO + kRows <= kTmem && 2 * NG % PARTS == 0, "tensor memory");
 };
 
@@ -134,14 +137,14 @@ struct Q8Maps {
 template <typename S>
 struct Q8Bars {
     uint64_t full[S::kSlots], empty[S::kSlots];          // a tile of K or V is there; has been turned
-    uint64_t ka_full[S::kTurnedK], ka_free[S::kTurnedK];  // K of a tile is f16 in tensor memory; has been multiplied
+    uint64_t ka_full, ka_free;                           // K of a tile is f16 in tensor memory; has been multiplied
     uint64_t va_full[S::kTurnedV], va_free[S::kTurnedV];
-    uint64_t s_full[2], s_free[2];                       // S of a tile is complete; has been read
+    uint64_t s_full[S::kScores], s_free[S::kScores];     // S of a tile is complete; has been read
     uint64_t p_full[S::kWeights], p_free[S::kWeights];   // its weights are in place; have been multiplied
     uint64_t o_full, o_free;                             // O of a tile is complete; has been read
-    uint64_t q_full;                                     // q's parts are in place
+    uint64_t q_full[S::kHeads], q_free[S::kHeads];       // a head's q is in place; has been multiplied, its units read
     uint64_t sc_full[kQ8ScaleSlots];                     // a tile's scales are there
-    uint64_t done;                                       // every product that was issued is complete
+    uint64_t done[2];                                    // every S, every O that was issued is complete
 };
 
 // Chunks of one (view, KV head) that a CTA takes one after the other: `chunks` of
@@ -213,16 +216,26 @@ __device__ __forceinline__ void q8_half_codes(uint32_t w, uint32_t& lo, uint32_t
     asm("{ .reg .b32 n; mov.b32 n, 0x64806480; sub.rn.f16x2 %0, %1, n; }" : "=r"(hi) : "r"(b));
 }
 
-// The producer: tiles (K and V in turn) and scales of the CTA's runs, in order.
-// Returns the tiles of K and V issued.
+// The producer: tiles and scales of the CTA's runs, in order, a tile's V behind the
+// next tile's K (which is needed first).  Returns the tiles of K and V issued.
 template <typename S>
 __device__ int q8_produce(const Q8Maps& maps, const Q8Batch& b, int Hkv, const Q8Share& w, uint8_t* tiles, float (*scales)[8],
                           Q8Bars<S>& bar)
 {
     unsigned int* late = &g_q8kv_wait_timeouts;
-    int i = 0;  // tiles of K and V
+    int i = 0, n = 0;  // tiles of K and V, tiles
+    int view = -1, g = 0, page = 0;  // the last tile's
+    auto load = [&](const CUtensorMap* m, int head, int p) {
+        const int st = i % S::kSlots;
+        if (!mbar_wait(&bar.empty[st], ((i / S::kSlots) & 1) ^ 1, late)) return false;
+        mbar_expect_tx(&bar.full[st], kQ8PageBytes);
+        tma_load_4d(tiles + st * kQ8PageBytes, m, 0, 0, head, p, &bar.full[st]);
+        ++i;
+        return true;
+    };
     pdl_wait();
     pdl_trigger();
+    bool ok = true;
     q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
         const Q8View& v = b.view[t.view];
         auto page_of = [&](int k) {
@@ -230,30 +243,35 @@ __device__ int q8_produce(const Q8Maps& maps, const Q8Batch& b, int Hkv, const Q
             return v.table ? ld_placed_i(v.table + span) : span;
         };
         int next = page_of(0);
-        for (int k = 0; k < t.tiles; ++k) {
-            int page = next;
+        for (int k = 0; k < t.tiles; ++k, ++n) {
+            int now = next;
             if (k + 1 < t.tiles) next = page_of(k + 1);  // (on its way while this tile's place becomes free)
-            const bool in = page >= 0 && page < v.n_pages;
-            if (!in) page = v.n_pages;                   // outside the map: zeros
-            for (int kv = 0; kv < 2; ++kv, ++i) {
-                const int st = i % S::kSlots, sl = (i >> 1) % kQ8ScaleSlots;
-                if (!mbar_wait(&bar.empty[st], ((i / S::kSlots) & 1) ^ 1, late)) return false;
-                if (kv == 0 && in) {
-                    mbar_expect_tx(&bar.sc_full[sl], 32);
-                    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], 32, [%2];" ::"r"(
-                                     smem_addr(scales[sl])),
-                                 "l"(v.scales + page * v.scale_stride + t.g * kQ8PageScales), "r"(smem_addr(&bar.sc_full[sl]))
-                                 : "memory");
-                } else if (kv == 0) {
-                    for (int e = 0; e < 8; ++e) scales[sl][e] = 0.0f;
-                    mbar_arrive(&bar.sc_full[sl]);
-                }
-                mbar_expect_tx(&bar.full[st], kQ8PageBytes);
-                tma_load_4d(tiles + st * kQ8PageBytes, kv ? &maps.v[t.view] : &maps.k[t.view], 0, 0, t.g, page, &bar.full[st]);
+            const bool in = now >= 0 && now < v.n_pages;
+            if (!in) now = v.n_pages;                    // outside the map: zeros
+            if (!(ok = load(&maps.k[t.view], t.g, now))) return false;
+            const int sl = n % kQ8ScaleSlots;
+            if (in) {
+                mbar_expect_tx(&bar.sc_full[sl], 32);
+                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], 32, [%2];" ::"r"(
+                                 smem_addr(scales[sl])),
+                             "l"(v.scales + now * v.scale_stride + t.g * kQ8PageScales), "r"(smem_addr(&bar.sc_full[sl]))
+                             : "memory");
+            } else {
+                for (int e = 0; e < 8; ++e) scales[sl][e] = 0.0f;
+                mbar_arrive(&bar.sc_full[sl]);
             }
+            if (view >= 0 && !(ok = load(&maps.v[view], g, page))) {
+                ++n;
+                return false;
+            }
+            view = t.view;
+            g = t.g;
+            page = now;
         }
         return true;
     });
+    if (ok && view >= 0) load(&maps.v[view], g, page);
+    ring_drain<kQ8ScaleSlots>(bar.sc_full, n, late);
     return i;
 }
 
@@ -284,80 +302,146 @@ __device__ void q8_turn_tiles(int n, const uint8_t* tiles, uint32_t tmem, int qu
     unsigned int* late = &g_q8kv_wait_timeouts;
     const int row = 32 * quad + lane;
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
-    for (int i = 0; i < 2 * n; ++i) {
-        const int st = i % S::kSlots, j = i >> 1, to = i & 1 ? j % S::kTurnedV : j % S::kTurnedK;
-        const uint32_t free = ((i & 1 ? j / S::kTurnedV : j / S::kTurnedK) & 1) ^ 1;
-        const bool there = mbar_wait(&bar.full[st], (i / S::kSlots) & 1, late) &&
-                           mbar_wait(i & 1 ? &bar.va_free[to] : &bar.ka_free[to], free, late);
-        if (!__all_sync(0xffffffffu, there)) return;
+    int i = 0;
+    // one of the ring's tiles, as soon as its place is free
+    auto turn = [&](uint64_t* free, uint32_t parity, uint64_t* full, uint32_t to) {
+        const int st = i % S::kSlots;
+        const bool there = mbar_wait(&bar.full[st], (i / S::kSlots) & 1, late) && mbar_wait(free, parity, late);
+        if (!__all_sync(0xffffffffu, there)) return false;
         tm_after();
-        q8_turn(tiles + st * kQ8PageBytes, row, lanes + (i & 1 ? S::kColV : S::kColK) + 64 * to);
-        warp_arrive(i & 1 ? &bar.va_full[to] : &bar.ka_full[to]);
+        q8_turn(tiles + st * kQ8PageBytes, row, lanes + to);
+        warp_arrive(full);
         if (lane == 0) mbar_arrive(&bar.empty[st]);
+        ++i;
+        return true;
+    };
+    for (int k = 0; k <= n; ++k) {  // K of tile k, V of the one before it
+        const int j = k - 1, to = j & 1;
+        if (k < n && !turn(&bar.ka_free, (k & 1) ^ 1, &bar.ka_full, S::kColK)) return;
+        if (k > 0 && !turn(&bar.va_free[to], ((j >> 1) & 1) ^ 1, &bar.va_full[to], S::kColV + 64 * to)) return;
     }
 }
 
-// The products, issued by one warp: S of tile i, then O of tile i - 1, so that
-// the tensor cores have the one while the other's weights are formed.  The low
-// parts go first: an accumulation loses digits by the sum's size, and theirs is small.
+// A product's steps, 128 x kRows x 16 each: A in tensor memory from column a, B rows of
+// 256 bytes in two halves.  The low parts go first: an accumulation loses digits by
+// the sum's size, and theirs is small.
 template <typename S>
-__device__ void q8_products(const Q8Batch& b, int Hkv, const Q8Share& w, uint32_t q, uint32_t weights, uint32_t tmem, Q8Bars<S>& bar)
+__device__ __forceinline__ void q8_multiply(uint32_t d, uint32_t a, uint32_t bytes, uint32_t elected)
+{
+    constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(S::kRows / 8) << 17) | (8u << 24);  // D f32, A and B f16
+    // (told to be the warp's, as they are: else every product moves its own copies)
+    d = __shfl_sync(0xffffffffu, d, 0);
+    a = __shfl_sync(0xffffffffu, a, 0);
+    const uint64_t desc = tree_desc(__shfl_sync(0xffffffffu, bytes, 0), 16, 1024);
+#pragma unroll
+    for (int ks = 0; ks < 16; ++ks)
+        tree_mma(d, a + 8 * (ks & 7), desc + ((ks < 8 ? S::kPart : 0) + (ks >> 2 & 1) * (S::kPart / 2)) / 16 + 2 * (ks & 3), idesc, ks > 0,
+                 elected);
+}
+
+// The products are issued by a warp each: S of a tile as soon as its K is there, and
+// its O behind its weights.  A step of 16 columns takes the tensor cores 9 cycles
+// and its issue about as many slots of a scheduler that five other warps use: by one
+// warp, the 32 steps of a tile took 2,100 cycles.
+template <typename S>
+__device__ void q8_scores(const Q8Batch& b, int Hkv, const Q8Share& w, uint32_t q, uint32_t tmem, Q8Bars<S>& bar)
 {
     unsigned int* late = &g_q8kv_wait_timeouts;
     const uint32_t elected = elect_one();
-    int i = 0, heads = 0, last = -1;
-    constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(S::kRows / 8) << 17) | (8u << 24);  // D f32, A and B f16, 128 rows, kRows columns
-    // all steps of a product: A in tensor memory from column a, B rows of 256 bytes in two halves
-    const uint64_t step = tree_desc(0, 16, 1024);
-    auto multiply = [&](uint32_t d, uint32_t a, uint32_t bytes) {
-        // (told to be the warp's, as they are: else every product moves its own copies)
-        d = __shfl_sync(0xffffffffu, d, 0);
-        a = __shfl_sync(0xffffffffu, a, 0);
-        const uint64_t desc = step | ((__shfl_sync(0xffffffffu, bytes, 0) >> 4) & 0x3FFF);
-#pragma unroll
-        for (int ks = 0; ks < 16; ++ks)
-            tree_mma(d, a + 8 * (ks & 7), desc + ((ks < 8 ? S::kPart : 0) + (ks >> 2 & 1) * (S::kPart / 2)) / 16 + 2 * (ks & 3), idesc, ks > 0,
-                     elected);
-    };
-    auto sums = [&](int j) {
+    int i = 0, head = -1, last = -1;
+    q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
+        bool ok = true;
+        if (t.view * Hkv + t.g != last) {
+            if (last >= 0) tree_commit_mma(&bar.q_free[head % S::kHeads], elected);
+            last = t.view * Hkv + t.g;
+            ++head;
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar.q_full[head % S::kHeads], (head / S::kHeads) & 1, late));
+        }
+        for (int k = 0; ok && k < t.tiles; ++k, ++i) {
+            const int to = i % S::kScores;
+            const bool there = mbar_wait(&bar.ka_full, i & 1, late) && mbar_wait(&bar.s_free[to], ((i / S::kScores) & 1) ^ 1, late);
+            if (!(ok = __all_sync(0xffffffffu, there))) break;  // (the warp leaves as one)
+            tm_after();
+            q8_multiply<S>(tmem + S::kColS + S::kRows * to, tmem + S::kColK, q + head % S::kHeads * 2 * S::kPart, elected);
+            tree_commit_mma(&bar.s_full[to], elected);
+            tree_commit_mma(&bar.ka_free, elected);
+        }
+        return ok;
+    });
+    // also after an expired wait, tensor memory is not freed under a product
+    tree_commit_mma(&bar.done[0], elected);
+    mbar_wait(&bar.done[0], 0, late);
+}
+
+template <typename S>
+__device__ void q8_sums(int n, uint32_t weights, uint32_t tmem, Q8Bars<S>& bar)
+{
+    unsigned int* late = &g_q8kv_wait_timeouts;
+    const uint32_t elected = elect_one();
+    for (int j = 0; j < n; ++j) {
         const int to = j % S::kTurnedV, p = j % S::kWeights;
         const bool there = mbar_wait(&bar.va_full[to], (j / S::kTurnedV) & 1, late) &&
                            mbar_wait(&bar.p_full[p], (j / S::kWeights) & 1, late) &&
                            (j == 0 || mbar_wait(&bar.o_free, (j - 1) & 1, late));
-        if (!__all_sync(0xffffffffu, there)) return false;  // (the warp leaves as one)
+        if (!__all_sync(0xffffffffu, there)) break;
         tm_after();
-        multiply(tmem + S::kColO, tmem + S::kColV + 64 * to, weights + p * 2 * S::kPart);
+        q8_multiply<S>(tmem + S::kColO, tmem + S::kColV + 64 * to, weights + p * 2 * S::kPart, elected);
         tree_commit_mma(&bar.o_full, elected);
         tree_commit_mma(&bar.p_free[p], elected);
         tree_commit_mma(&bar.va_free[to], elected);
-        return true;
-    };
-    bool ok = true, open = false;    // open: the last tile's sums have not been issued
-    q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
-        if (t.view * Hkv + t.g != last) {
-            last = t.view * Hkv + t.g;
-            // (the next head's q comes when the last one's sums have been taken)
-            ok = (!open || sums(i - 1)) && __all_sync(0xffffffffu, mbar_wait(&bar.q_full, heads++ & 1, late));
-            open = false;
+    }
+    tree_commit_mma(&bar.done[1], elected);
+    mbar_wait(&bar.done[1], 0, late);
+}
+
+// A head's rows of q, in units of a power of two each, as two f16 parts in the products'
+// layout: 16 lanes a row, rows first, first + step, ..
+template <typename S>
+__device__ void q8_prepare(const float* q, const Q8Batch& b, int Hq, int Hkv, const Q8Run& t, const Q8Scale& scale, uint8_t* parts,
+                           float (*unit_s)[S::kCols], int (*from_s)[S::kCols], int first, int step)
+{
+    constexpr int kAhead = S::kRows <= 32 ? 2 : 4;
+    const Q8View& v = b.view[t.view];
+    const int GQ = Hq / Hkv, R = v.n_nodes * GQ, piece = threadIdx.x & 15;
+    for (int c0 = first; c0 < S::kRows; c0 += step * kAhead) {
+        float4 x[kAhead], y[kAhead];
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) {
+            const int c = c0 + step * e;
+            x[e] = y[e] = make_float4(0, 0, 0, 0);
+            if (c < R) {
+                const float* p = q + ((int64_t)(v.row0 + c / GQ) * Hq + t.g * GQ + c % GQ) * kHeadDim + 8 * piece;
+                x[e] = ld_placed_f4(p);
+                y[e] = ld_placed_f4(p + 4);
+            }
         }
-        for (int k = 0; ok && k < t.tiles; ++k, ++i) {
-            const int to = i % S::kTurnedK;
-            const bool there = mbar_wait(&bar.ka_full[to], (i / S::kTurnedK) & 1, late) &&
-                               mbar_wait(&bar.s_free[i & 1], ((i >> 1) & 1) ^ 1, late);
-            if (!(ok = __all_sync(0xffffffffu, there))) break;
-            tm_after();
-            multiply(tmem + S::kColS + S::kRows * (i & 1), tmem + S::kColK + 64 * to, q);
-            tree_commit_mma(&bar.s_full[i & 1], elected);
-            tree_commit_mma(&bar.ka_free[to], elected);
-            if (open) ok = sums(i - 1);
-            open = true;
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) {
+            const int c = c0 + step * e;
+            float big = fmaxf(fmaxf(fmaxf(fabsf(x[e].x), fabsf(x[e].y)), fmaxf(fabsf(x[e].z), fabsf(x[e].w))),
+                              fmaxf(fmaxf(fabsf(y[e].x), fabsf(y[e].y)), fmaxf(fabsf(y[e].z), fabsf(y[e].w))));
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+            if (c >= S::kRows) continue;
+            // the row's unit puts its largest element into [2^14, 2^15)
+            const int exp = max((__float_as_int(big) >> 23) - 127 - 14, -112);
+            const float into = __fmul_rn(scale.sign, __int_as_float((127 - exp) << 23));
+            uint4 hi, lo;
+            tree_split(__fmul_rn(x[e].x, into), __fmul_rn(x[e].y, into), hi.x, lo.x);
+            tree_split(__fmul_rn(x[e].z, into), __fmul_rn(x[e].w, into), hi.y, lo.y);
+            tree_split(__fmul_rn(y[e].x, into), __fmul_rn(y[e].y, into), hi.z, lo.z);
+            tree_split(__fmul_rn(y[e].z, into), __fmul_rn(y[e].w, into), hi.w, lo.w);
+            uint8_t* at = parts + (piece >> 3) * (S::kPart / 2) + (c >> 3) * 1024 + (c & 7) * 128 + (((piece & 7) ^ (c & 7)) << 4);
+            *reinterpret_cast<uint4*>(at) = hi;
+            *reinterpret_cast<uint4*>(at + S::kPart) = lo;
+            if (piece == 0) {
+                const int part = (c >> 3) % S::kParts, col = (c >> 3) / S::kParts * 8 + (c & 7);
+                unit_s[part][col] = __fmul_rn(scale.log2, __int_as_float((127 + exp) << 23));
+                from_s[part][col] = v.sealed + v.tail + b.row[v.row0 + min(c / GQ, v.n_nodes - 1)].n_path - v.window;
+            }
         }
-        return ok;
-    });
-    if (ok && open) sums(i - 1);
-    // also after an expired wait, tensor memory is not freed under a product
-    tree_commit_mma(&bar.done, elected);
-    mbar_wait(&bar.done, 0, late);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c)
@@ -402,17 +486,17 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
     extern __shared__ uint8_t q8_smem[];
     uint8_t* tiles = q8_smem + ((1024u - (smem_addr(q8_smem) & 1023u)) & 1023u);
     uint8_t* qs = tiles + S::kSlots * kQ8PageBytes;       // q: high and low part, two halves of the dims each
-    uint8_t* ps = qs + 2 * S::kPart;                      // weights, the same way
+    uint8_t* ps = qs + 2 * S::kHeads * S::kPart;          // weights, the same way
     __shared__ Q8Bars<S> bar;
     __shared__ uint32_t tmem_at;
     __shared__ __align__(16) float scales[kQ8ScaleSlots][8];
     // by part: its columns are the groups of eight PARTS e + part, numbered through
     __shared__ float mx[2][PARTS][4][S::kCols];           // the columns' maxima of a tile's blocks, by tile parity
-    __shared__ float unit_s[PARTS][S::kCols];             // a score's power of two per unit of its product
-    __shared__ __align__(8) int from_s[PARTS][S::kCols];  // the first key in the row's window
+    __shared__ float unit_s[S::kHeads][PARTS][S::kCols];             // a score's power of two per unit of its product
+    __shared__ __align__(8) int from_s[S::kHeads][PARTS][S::kCols];  // the first key in the row's window
     // by warp: what turns a column's products into exponents (a factor, an offset),
     // and what O so far is multiplied by, by tile parity
-    __shared__ __align__(16) float2 turn_s[S::kWarps][S::kCols];
+    __shared__ __align__(8) float factor_s[S::kWarps][S::kCols], offset_s[S::kWarps][S::kCols];
     __shared__ __align__(8) float alpha_s[2][S::kWarps][S::kCols];
     __shared__ volatile int bail[PARTS][2];               // a wait of the part's warps expired, by tile parity
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -425,15 +509,13 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
             mbar_init(&bar.full[i], 1);
             mbar_init(&bar.empty[i], 4);
         }
-        for (int i = 0; i < S::kTurnedK; ++i) {
-            mbar_init(&bar.ka_full[i], 4);
-            mbar_init(&bar.ka_free[i], 1);
-        }
+        mbar_init(&bar.ka_full, 4);
+        mbar_init(&bar.ka_free, 1);
         for (int i = 0; i < S::kTurnedV; ++i) {
             mbar_init(&bar.va_full[i], 4);
             mbar_init(&bar.va_free[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < S::kScores; ++i) {
             mbar_init(&bar.s_full[i], 1);
             mbar_init(&bar.s_free[i], S::kWarps);
         }
@@ -445,8 +527,12 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
         for (int i = 0; i < kQ8ScaleSlots; ++i) mbar_init(&bar.sc_full[i], 1);
         mbar_init(&bar.o_full, 1);
         mbar_init(&bar.o_free, S::kWarps);
-        mbar_init(&bar.q_full, S::kWarps);
-        mbar_init(&bar.done, 1);
+        for (int i = 0; i < S::kHeads; ++i) {
+            mbar_init(&bar.q_full[i], 1);
+            mbar_init(&bar.q_free[i], 1 + S::kWarps);
+        }
+        mbar_init(&bar.done[0], 1);
+        mbar_init(&bar.done[1], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     tm_before();
@@ -466,23 +552,49 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
         w = Q8Share{(int)((int64_t)units * blockIdx.x / gridDim.x), (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x), 0};
     unsigned int* late = &g_q8kv_wait_timeouts;
 
-    if (warp >= S::kWarps + 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        if (warp == S::kWarps + 4 && lane == 0) {
-            const int n = q8_produce(maps, b, Hkv, w, tiles, scales, bar);
-            ring_drain<S::kSlots>(bar.full, n, late);
-            ring_drain<kQ8ScaleSlots>(bar.sc_full, (n + 1) / 2, late);
-        }
-        if (warp == S::kWarps + 5) q8_products(b, Hkv, w, smem_addr(qs), smem_addr(ps), tmem, bar);
-        __syncwarp();
-    } else if (warp >= S::kWarps) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    auto tiles_of_all = [&] {
         int n = 0;
         q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
             n += t.tiles;
             return true;
         });
-        q8_turn_tiles(n, tiles, tmem, warp & 3, lane, bar);
+        return n;
+    };
+    if (warp >= S::kWarps + 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kOther));
+        if (warp == S::kWarps + 4 && lane == 0) {
+            const int n = q8_produce(maps, b, Hkv, w, tiles, scales, bar);
+            ring_drain<S::kSlots>(bar.full, n, late);
+        }
+        if (warp > S::kWarps + 4) {
+            // the first head's q by all three of these warps, which have nothing else to do
+            // before; the others' ahead of time by the last one
+            const int first = (tid - 32 * (S::kWarps + 5)) >> 4;
+            pdl_wait();
+            q8_prepare<S>(q, b, Hq, Hkv, q8_run(b, Hkv, w.u0, w.u0 + 1), scale, qs, unit_s[0], from_s[0], first, 6);
+            asm volatile("bar.sync 15, 96;" ::: "memory");
+            if (warp == S::kWarps + 5) q8_scores(b, Hkv, w, smem_addr(qs), tmem, bar);
+            if (warp == S::kWarps + 6) q8_sums(tiles_of_all(), smem_addr(ps), tmem, bar);
+            if (warp == S::kWarps + 7) {
+                int head = -1, last = -1;
+                q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
+                    if (t.view * Hkv + t.g == last) return true;
+                    last = t.view * Hkv + t.g;
+                    const int to = ++head % S::kHeads;
+                    if (head > 0) {
+                        if (!__all_sync(0xffffffffu, mbar_wait(&bar.q_free[to], ((head / S::kHeads) & 1) ^ 1, late))) return false;
+                        q8_prepare<S>(q, b, Hq, Hkv, t, scale, qs + to * 2 * S::kPart, unit_s[to], from_s[to], lane >> 4, 2);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.q_full[to]);
+                    return true;
+                });
+            }
+        }
+        __syncwarp();
+    } else if (warp >= S::kWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kOther));
+        q8_turn_tiles(tiles_of_all(), tiles, tmem, warp & 3, lane, bar);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegs));
         // The warp's keys are its block of the tile, 32 quad ..; its columns the groups of
@@ -496,10 +608,16 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
         const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16) + 8 * part;
         const uint32_t row_at = (quad >> 1) * (S::kPart / 2) + part * 1024 + (lane & 7) * 128 +
                                 (((4 * (quad & 1) + (lane >> 3)) ^ (lane & 7)) << 4);  // where its keys' weights go
-        uint64_t o[G][4], l[G];      // pairs of columns
+        uint64_t o[G][4], l[G];        // pairs of columns
         float m[kMine];                // of columns lane + 32 e
-        int i = 0, last = -1, R = 0;
-        bool ok = true;
+        int i = 0, head = -1, last = -1;
+        bool ok = true, gone = false;
+        // the chunk whose last tile's O is still to come: its rows of results (-1: it is not a
+        // chunk's last tile), how many they are, their weights' sums and maxima
+        int64_t end_row = -1;
+        int end_left = 0;
+        uint64_t end_l[G];
+        float end_m[kMine];
         auto part_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory"); };
         // adds O of tile j
         auto take = [&](int j) {
@@ -518,70 +636,73 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                 if (e0 + B >= G) warp_arrive(&bar.o_free);
 #pragma unroll
                 for (int e = e0; e < e0 + B && e < G; ++e) {
-                    const float2 a = *reinterpret_cast<const float2*>(&alpha_s[j & 1][warp][8 * e + pair2]);
+                    const uint64_t a = *reinterpret_cast<const uint64_t*>(&alpha_s[j & 1][warp][8 * e + pair2]);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) o[e][c] = fma2(o[e][c], pair(a.x, a.y), pair(x[e - e0][2 * c], x[e - e0][2 * c + 1]));
+                    for (int c = 0; c < 4; ++c) o[e][c] = fma2(o[e][c], a, pair(x[e - e0][2 * c], x[e - e0][2 * c + 1]));
                 }
+            }
+            if (end_row < 0) return;
+            float* ml = part_ml + 8 * (end_row + 8 * part);
+            float* po = part_o + (end_row + 8 * part + pair2) * kHeadDim + 32 * quad + (lane >> 2);
+            asm volatile("" : "+l"(ml), "+l"(po));  // (one address each, not one for every store)
+            const int left = ok ? end_left - 8 * part : 0;
+#pragma unroll
+            for (int e = 0; e < G; ++e) {
+                const float2 mine = unpair(end_l[e]);
+                float x[2] = {mine.x, mine.y};
+#pragma unroll
+                for (int d = 0; d < 2; ++d) {
+#pragma unroll
+                    for (int f = 4; f < 32; f <<= 1) x[d] = __fadd_rn(x[d], __shfl_xor_sync(0xffffffffu, x[d], f));
+                    const int c = 8 * PARTS * e + d;
+                    if (c + pair2 < left) {
+                        if ((lane >> 2) == 0) ml[8 * (c + pair2) + 4 + quad] = x[d];
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) {
+                            const float2 y = unpair(o[e][f]);
+                            po[c * kHeadDim + 8 * f] = d ? y.y : y.x;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[e][c] = 0;  // (what the next chunk's first correction, 0, meets is finite)
+            }
+#pragma unroll
+            for (int e = 0; e < kMine; ++e) {
+                const int at = lane + 32 * e, c = 8 * PARTS * (at >> 3) + (at & 7);
+                if (quad == 0 && at < kCols && c < left) ml[8 * c] = end_m[e];
             }
         };
+#pragma unroll
+        for (int e = 0; e < G; ++e)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[e][c] = 0;
         q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
             const Q8View& v = b.view[t.view];
-            if (t.view * Hkv + t.g != last) {  // (S of every tile of the last head is complete: its q is free)
-                if (last < 0) pdl_wait();
+            const int R = v.n_nodes * GQ;
+            if (t.view * Hkv + t.g != last) {
+                __syncwarp();
+                if (last >= 0 && lane == 0) mbar_arrive(&bar.q_free[head % S::kHeads]);  // (its units have been read)
                 last = t.view * Hkv + t.g;
-                R = v.n_nodes * GQ;
-                part_sync();                   // (the last head's units have been read)
-                const int piece = tid & 15;
-                for (int j = 0; j < G; ++j) {
-                    const int in8 = (tid & 127) >> 4, c = 8 * (PARTS * j + part) + in8;
-                    float4 x = make_float4(0, 0, 0, 0), y = x;
-                    if (c < R) {
-                        const float* p = q + ((int64_t)(v.row0 + c / GQ) * Hq + t.g * GQ + c % GQ) * kHeadDim + 8 * piece;
-                        x = ld_placed_f4(p);
-                        y = ld_placed_f4(p + 4);
-                    }
-                    float big = fmaxf(fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))),
-                                      fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w))));
-#pragma unroll
-                    for (int e = 1; e < 16; e <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, e));
-                    // the row's unit puts its largest element into [2^14, 2^15)
-                    const int exp = max((__float_as_int(big) >> 23) - 127 - 14, -112);
-                    const float into = __fmul_rn(scale.sign, __int_as_float((127 - exp) << 23));
-                    uint4 hi, lo;
-                    tree_split(__fmul_rn(x.x, into), __fmul_rn(x.y, into), hi.x, lo.x);
-                    tree_split(__fmul_rn(x.z, into), __fmul_rn(x.w, into), hi.y, lo.y);
-                    tree_split(__fmul_rn(y.x, into), __fmul_rn(y.y, into), hi.z, lo.z);
-                    tree_split(__fmul_rn(y.z, into), __fmul_rn(y.w, into), hi.w, lo.w);
-                    uint8_t* to = qs + (piece >> 3) * (S::kPart / 2) + (c >> 3) * 1024 + (c & 7) * 128 + (((piece & 7) ^ (c & 7)) << 4);
-                    *reinterpret_cast<uint4*>(to) = hi;
-                    *reinterpret_cast<uint4*>(to + S::kPart) = lo;
-                    if (piece == 0) {
-                        unit_s[part][8 * j + in8] = __fmul_rn(scale.log2, __int_as_float((127 + exp) << 23));
-                        const int node = min(c / GQ, v.n_nodes - 1);
-                        from_s[part][8 * j + in8] = v.sealed + v.tail + b.row[v.row0 + node].n_path - v.window;
-                    }
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                part_sync();
-                if (lane == 0) mbar_arrive(&bar.q_full);
+                ++head;
+                ok = ok && mbar_wait(&bar.q_full[head % S::kHeads], (head / S::kHeads) & 1, late);
+                if (head == 0) pdl_wait();  // (the results' place is free)
             }
+            const float* units = unit_s[head % S::kHeads][part];
+            const int* froms = from_s[head % S::kHeads][part];
             int64_t pr = v.part0 + ((int64_t)t.c * Hkv + t.g) * R;  // the chunk's rows of results
             int kc = 0;                                              // the chunk's tiles so far
             for (int k = 0; k < t.tiles; ++k, ++i) {
-                const int key0 = q8_tile_key(v, t.t0 + k), buf = i & 1;
+                const int key0 = q8_tile_key(v, t.t0 + k), buf = i & 1, from = i % S::kScores;
                 const float* sc = scales[i % kQ8ScaleSlots];
-                if (kc == 0) {  // (what the last chunk left may be anything: it is not multiplied by 0)
+                if (kc == 0) {
 #pragma unroll
-                    for (int e = 0; e < G; ++e) {
-                        l[e] = 0;
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) o[e][c] = 0;
-                    }
+                    for (int e = 0; e < G; ++e) l[e] = 0;
 #pragma unroll
                     for (int e = 0; e < kMine; ++e) m[e] = -INFINITY;
                 }
                 ok = ok && mbar_wait(&bar.sc_full[i % kQ8ScaleSlots], (i / kQ8ScaleSlots) & 1, late) &&
-                     mbar_wait(&bar.s_full[buf], (i >> 1) & 1, late);
+                     mbar_wait(&bar.s_full[from], (i / S::kScores) & 1, late);
                 tm_after();
                 const bool valid = key0 + kQ8Block * quad < v.sealed;
                 const float ks = valid ? sc[quad] : 0.0f;
@@ -599,8 +720,8 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                 auto load_s = [&](int e0) {
 #pragma unroll
                     for (int e = 0; e < B; ++e) {
-                        tm_ld_frag(lanes + S::kColS + S::kRows * buf + 8 * PARTS * (e0 + e), s[e]);
-                        tm_ld_frag(lanes + (16u << 16) + S::kColS + S::kRows * buf + 8 * PARTS * (e0 + e), s[e] + 4);
+                        tm_ld_frag(lanes + S::kColS + S::kRows * from + 8 * PARTS * (e0 + e), s[e]);
+                        tm_ld_frag(lanes + (16u << 16) + S::kColS + S::kRows * from + 8 * PARTS * (e0 + e), s[e] + 4);
                     }
                     tm_loaded<8 * B>(&s[0][0]);
                     if (!valid) {
@@ -611,11 +732,11 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                     } else if (masked) {
 #pragma unroll
                         for (int e = 0; e < B; ++e) {
-                            const int2 from = *reinterpret_cast<const int2*>(&from_s[part][8 * (e0 + e) + pair2]);
+                            const int2 key1 = *reinterpret_cast<const int2*>(&froms[8 * (e0 + e) + pair2]);
 #pragma unroll
                             for (int c = 0; c < 8; ++c) {
                                 const int key = key0 + kQ8Block * quad + (lane >> 2) + 8 * (c >> 1);
-                                if (key >= v.sinks && key < (c & 1 ? from.y : from.x)) s[e][c] = -INFINITY;
+                                if (key >= v.sinks && key < (c & 1 ? key1.y : key1.x)) s[e][c] = -INFINITY;
                             }
                         }
                     }
@@ -630,7 +751,7 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                         top[2 * (e0 + e) + 1] = fmaxf(max3(s[e][1], s[e][3], s[e][5]), s[e][7]);
                     }
                 }
-                if (!S::kTwice) warp_arrive(&bar.s_free[buf]);
+                if (!S::kTwice) warp_arrive(&bar.s_free[from]);
                 int first = 0;
                 q8_maxima<2 * G, 16>(top, lane, first);
 #pragma unroll
@@ -645,20 +766,24 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                     if (lane + 32 * e < kCols) {
                         // (rounded up: no weight is above 2^15 by more than its exponent's own rounding)
                         float* x = &mx[buf][part][quad][lane + 32 * e];
-                        factor[e] = fmaxf(__fmul_rn(unit_s[part][lane + 32 * e], ks), 1e-37f);
+                        factor[e] = fmaxf(__fmul_rn(units[lane + 32 * e], ks), 1e-37f);
                         *x = __fadd_ru(__fmul_ru(*x, factor[e]), lv);
                     }
                 // all four warps of a part meet here, an expired wait or not, and leave together
                 if (!ok) bail[part][buf] = 1;
                 part_sync();
-                if (bail[part][buf]) return false;
+                if (bail[part][buf]) {
+                    gone = true;
+                    return false;
+                }
 #pragma unroll
                 for (int e = 0; e < kMine; ++e)
                     if (lane + 32 * e < kCols) {
                         const float* x = &mx[buf][part][0][lane + 32 * e];
                         const float now = fmaxf(m[e], max3(fmaxf(x[0], x[kCols]), x[2 * kCols], x[3 * kCols]));
                         const float at = now == -INFINITY ? 0.0f : now;
-                        turn_s[warp][lane + 32 * e] = make_float2(factor[e], __fadd_rn(__fsub_rn(kQ8Up, at), lv));
+                        factor_s[warp][lane + 32 * e] = factor[e];
+                        offset_s[warp][lane + 32 * e] = __fadd_rn(__fsub_rn(kQ8Up, at), lv);
                         alpha_s[buf][warp][lane + 32 * e] = tree_exp2(__fsub_rn(m[e], at));  // 0 for m = -inf
                         m[e] = now;
                     }
@@ -670,64 +795,45 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                 for (int e = 0; e < G; ++e) {
                     if (S::kTwice && e % B == 0) {
                         load_s(e);
-                        if (e + B >= G) warp_arrive(&bar.s_free[buf]);
+                        if (e + B >= G) warp_arrive(&bar.s_free[from]);
                     }
-                    const float4 f = *reinterpret_cast<const float4*>(&turn_s[warp][8 * e + pair2]);
-                    const float2 a = *reinterpret_cast<const float2*>(&alpha_s[buf][warp][8 * e + pair2]);
+                    // (pairs as they lie: put together from single values they cost moves)
+                    const uint64_t f = *reinterpret_cast<const uint64_t*>(&factor_s[warp][8 * e + pair2]);
+                    const uint64_t up = *reinterpret_cast<const uint64_t*>(&offset_s[warp][8 * e + pair2]);
+                    const uint64_t a = *reinterpret_cast<const uint64_t*>(&alpha_s[buf][warp][8 * e + pair2]);
                     uint64_t p[4];
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const float2 x = unpair(fma2(pair(s[e % B][2 * c], s[e % B][2 * c + 1]), pair(f.x, f.z), pair(f.y, f.w)));
+                        const float2 x = unpair(fma2(pair(s[e % B][2 * c], s[e % B][2 * c + 1]), f, up));
                         const float p0 = tree_exp2(x.x), p1 = tree_exp2(x.y);
                         p[c] = pair(p0, p1);
                         tree_split(p0, p1, hi[c], lo[c]);
                     }
                     const uint64_t sum = add2(add2(p[0], p[1]), add2(p[2], p[3]));
-                    l[e] = fma2(sum, iv2, fma2(l[e], pair(a.x, a.y), 0));
+                    l[e] = fma2(sum, iv2, fma2(l[e], a, 0));
                     st_matrix_turned(to + 1024 * PARTS * e, hi[0], hi[1], hi[2], hi[3]);
                     st_matrix_turned(to + 1024 * PARTS * e + S::kPart, lo[0], lo[1], lo[2], lo[3]);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.p_full[i % S::kWeights]);
-                if (kc > 0) take(i - 1);
+                if (i > 0) take(i - 1);
+                end_row = -1;
                 if (++kc == v.chunk || k + 1 == t.tiles) {  // the chunk's last tile
-                    take(i);
-                    float* ml = part_ml + 8 * (pr + 8 * part);
-                    float* po = part_o + (pr + 8 * part + pair2) * kHeadDim + 32 * quad + (lane >> 2);
-                    asm volatile("" : "+l"(ml), "+l"(po));  // (one address each, not one for every store)
-                    const int left = ok ? R - 8 * part : 0;
+                    end_row = pr;
+                    end_left = R;
 #pragma unroll
-                    for (int e = 0; e < G; ++e) {
-                        const float2 mine = unpair(l[e]);
-                        float x[2] = {mine.x, mine.y};
+                    for (int e = 0; e < G; ++e) end_l[e] = l[e];
 #pragma unroll
-                        for (int d = 0; d < 2; ++d) {
-#pragma unroll
-                            for (int f = 4; f < 32; f <<= 1) x[d] = __fadd_rn(x[d], __shfl_xor_sync(0xffffffffu, x[d], f));
-                            const int c = 8 * PARTS * e + d;
-                            if (c + pair2 < left) {
-                                if ((lane >> 2) == 0) ml[8 * (c + pair2) + 4 + quad] = x[d];
-#pragma unroll
-                                for (int f = 0; f < 4; ++f) {
-                                    const float2 y = unpair(o[e][f]);
-                                    po[c * kHeadDim + 8 * f] = d ? y.y : y.x;
-                                }
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int e = 0; e < kMine; ++e) {
-                        const int at = lane + 32 * e, c = 8 * PARTS * (at >> 3) + (at & 7);
-                        if (quad == 0 && at < kCols && c < left) ml[8 * c] = m[e];
-                    }
+                    for (int e = 0; e < kMine; ++e) end_m[e] = m[e];
                     kc = 0;
                     pr += (int64_t)Hkv * R;
                 }
             }
             return true;
         });
+        if (!gone && i > 0) take(i - 1);
     }
     tm_before();
     __syncthreads();
@@ -956,7 +1062,8 @@ cudaError_t launch_q8kv_attention(const float* q, const Q8Batch& b, int Hq, int 
         Q8Maps maps{};
         if (!q8_maps(b, Hkv, &maps)) return cudaErrorInvalidValue;
         const auto launch = rows <= 16 ? launch_chunks<1, 1> : rows <= 32 ? launch_chunks<2, 1> : rows <= 48 ? launch_chunks<3, 2>
-                            : rows <= 64 ? launch_chunks<4, 4> : rows <= 96 ? launch_chunks<6, 4> : launch_chunks<8, 4>;
+                            : rows <= 64 ? launch_chunks<4, 2> : rows <= 80 ? launch_chunks<5, 2> : rows <= 96 ? launch_chunks<6, 2>
+                                         : launch_chunks<8, 2>;
         const cudaError_t e = launch(maps, q, b, Hq, Hkv, units, runs, sc, part_o, part_ml, s);
         if (e != cudaSuccess) return e;
     }
