@@ -116,12 +116,12 @@ struct Q8Shape {
     // registers of a thread on weights, and of the others: 30,720 of a CTA launched with
     // 80 each, 65,536 with 128
     static constexpr int kRegs = PARTS == 1 ? 144 : 200, kOther = PARTS == 1 ? 48 : 56;
-    static constexpr int kSlots = NG == 1 ? 5 : NG == 2 ? 3 : NG == 3 ? 7 : NG == 6 ? 4 : 5;  // tiles of K or V in flight
+    static constexpr int kSlots = NG == 1 ? 4 : NG == 2 ? 3 : NG == 3 ? 7 : NG == 6 ? 4 : 5;  // tiles of K or V in flight
     // In tensor memory: one tile of K, which is multiplied as soon as it is there, two
     // of V, which wait for their weights, and two of scores where there is room
     static constexpr int kTurnedV = 2, kScores = NG == 2 || NG == 8 ? 1 : 2;
-    static constexpr int kWeights = NG == 3 || NG == 4 ? 2 : 1;  // tiles of weights in shared memory
-    static constexpr int kHeads = NG <= 6 ? 2 : 1;             // heads of q in shared memory
+    static constexpr int kWeights = NG == 8 ? 1 : 2;           // tiles of weights in shared memory
+    static constexpr int kHeads = NG == 1 || NG == 3 || NG == 4 ? 2 : 1;  // heads of q in shared memory
     static constexpr bool kTwice = NG == 8;                    // scores are read twice, not held while maxima are found
     static constexpr int kPart = kRows * kHeadDim * 2;         // bytes of one part of q, or of the weights
     static constexpr uint32_t kColK = 0, kColV = 64, kColS = kColV + 64 * kTurnedV, kColO = kColS + kScores * kRows;
@@ -140,10 +140,9 @@ struct Q8Bars {
     uint64_t ka_full, ka_free;                           // K of a tile is f16 in tensor memory; has been multiplied
     uint64_t va_full[S::kTurnedV], va_free[S::kTurnedV];
     uint64_t s_full[S::kScores], s_free[S::kScores];     // S of a tile is complete; has been read
-    uint64_t p_full[S::kWeights], p_free[S::kWeights];   // its weights are in place; have been multiplied
+    uint64_t p_full[S::kWeights];                        // its weights are in place
     uint64_t o_full, o_free;                             // O of a tile is complete; has been read
     uint64_t q_full[S::kHeads], q_free[S::kHeads];       // a head's q is in place; has been multiplied, its units read
-    uint64_t sc_full[kQ8ScaleSlots];                     // a tile's scales are there
     uint64_t done[2];                                    // every S, every O that was issued is complete
 };
 
@@ -225,10 +224,16 @@ __device__ int q8_produce(const Q8Maps& maps, const Q8Batch& b, int Hkv, const Q
     unsigned int* late = &g_q8kv_wait_timeouts;
     int i = 0, n = 0;  // tiles of K and V, tiles
     int view = -1, g = 0, page = 0;  // the last tile's
-    auto load = [&](const CUtensorMap* m, int head, int p) {
+    // scales (nullable): come with the tile; the weights' warps read them behind S, which
+    // the turning warps' wait for this tile has come before
+    auto load = [&](const CUtensorMap* m, int head, int p, const float* sc, float* to) {
         const int st = i % S::kSlots;
         if (!mbar_wait(&bar.empty[st], ((i / S::kSlots) & 1) ^ 1, late)) return false;
-        mbar_expect_tx(&bar.full[st], kQ8PageBytes);
+        mbar_expect_tx(&bar.full[st], kQ8PageBytes + (sc ? 32 : 0));
+        if (sc)
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], 32, [%2];" ::"r"(smem_addr(to)),
+                         "l"(sc), "r"(smem_addr(&bar.full[st]))
+                         : "memory");
         tma_load_4d(tiles + st * kQ8PageBytes, m, 0, 0, head, p, &bar.full[st]);
         ++i;
         return true;
@@ -248,30 +253,19 @@ __device__ int q8_produce(const Q8Maps& maps, const Q8Batch& b, int Hkv, const Q
             if (k + 1 < t.tiles) next = page_of(k + 1);  // (on its way while this tile's place becomes free)
             const bool in = now >= 0 && now < v.n_pages;
             if (!in) now = v.n_pages;                    // outside the map: zeros
-            if (!(ok = load(&maps.k[t.view], t.g, now))) return false;
-            const int sl = n % kQ8ScaleSlots;
-            if (in) {
-                mbar_expect_tx(&bar.sc_full[sl], 32);
-                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], 32, [%2];" ::"r"(
-                                 smem_addr(scales[sl])),
-                             "l"(v.scales + now * v.scale_stride + t.g * kQ8PageScales), "r"(smem_addr(&bar.sc_full[sl]))
-                             : "memory");
-            } else {
-                for (int e = 0; e < 8; ++e) scales[sl][e] = 0.0f;
-                mbar_arrive(&bar.sc_full[sl]);
-            }
-            if (view >= 0 && !(ok = load(&maps.v[view], g, page))) {
-                ++n;
-                return false;
-            }
+            float* to = scales[n % kQ8ScaleSlots];
+            if (!in)
+                for (int e = 0; e < 8; ++e) to[e] = 0.0f;
+            const float* sc = in ? v.scales + now * v.scale_stride + t.g * kQ8PageScales : nullptr;
+            if (!(ok = load(&maps.k[t.view], t.g, now, sc, to))) return false;
+            if (view >= 0 && !(ok = load(&maps.v[view], g, page, nullptr, nullptr))) return false;
             view = t.view;
             g = t.g;
             page = now;
         }
         return true;
     });
-    if (ok && view >= 0) load(&maps.v[view], g, page);
-    ring_drain<kQ8ScaleSlots>(bar.sc_full, n, late);
+    if (ok && view >= 0) load(&maps.v[view], g, page, nullptr, nullptr);
     return i;
 }
 
@@ -387,7 +381,6 @@ __device__ void q8_sums(int n, uint32_t weights, uint32_t tmem, Q8Bars<S>& bar)
         tm_after();
         q8_multiply<S>(tmem + S::kColO, tmem + S::kColV + 64 * to, weights + p * 2 * S::kPart, elected);
         tree_commit_mma(&bar.o_full, elected);
-        tree_commit_mma(&bar.p_free[p], elected);
         tree_commit_mma(&bar.va_free[to], elected);
     }
     tree_commit_mma(&bar.done[1], elected);
@@ -520,11 +513,7 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
             mbar_init(&bar.s_free[i], S::kWarps);
         }
         for (int i = 0; i < PARTS; ++i) bail[i][0] = bail[i][1] = 0;
-        for (int i = 0; i < S::kWeights; ++i) {
-            mbar_init(&bar.p_full[i], S::kWarps);
-            mbar_init(&bar.p_free[i], 1);
-        }
-        for (int i = 0; i < kQ8ScaleSlots; ++i) mbar_init(&bar.sc_full[i], 1);
+        for (int i = 0; i < S::kWeights; ++i) mbar_init(&bar.p_full[i], S::kWarps);
         mbar_init(&bar.o_full, 1);
         mbar_init(&bar.o_free, S::kWarps);
         for (int i = 0; i < S::kHeads; ++i) {
@@ -603,13 +592,18 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
         // the same for a column's keys (maximum, factor, correction) a lane forms per
         // column, and the threads pick it up from shared memory: formed by each
         // thread for its own columns it took twice the instructions of the weights.
-        constexpr int G = S::kGroups, kCols = S::kCols, kMine = (kCols + 31) / 32;  // (columns of a lane)
-        const int part = warp >> 2, quad = warp & 3, GQ = Hq / Hkv, pair2 = 2 * (lane & 3);
+        // (a lane's columns: where the groups are a power of two, those whose maxima it ends
+        // with; else lane, lane + 32, ..)
+        constexpr int G = S::kGroups, kCols = S::kCols;
+        constexpr bool kDirect = (G & (G - 1)) == 0;
+        constexpr int kMine = kDirect ? q8_left(2 * G) : (kCols + 31) / 32;
+        int col[kMine];
+        const int part = warp >> 2, quad = warp & 3, pair2 = 2 * (lane & 3);
         const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16) + 8 * part;
         const uint32_t row_at = (quad >> 1) * (S::kPart / 2) + part * 1024 + (lane & 7) * 128 +
                                 (((4 * (quad & 1) + (lane >> 3)) ^ (lane & 7)) << 4);  // where its keys' weights go
         uint64_t o[G][4], l[G];        // pairs of columns
-        float m[kMine];                // of columns lane + 32 e
+        float m[kMine];                // of the lane's columns
         int i = 0, head = -1, last = -1;
         bool ok = true, gone = false;
         // the chunk whose last tile's O is still to come: its rows of results (-1: it is not a
@@ -618,6 +612,16 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
         int end_left = 0;
         uint64_t end_l[G];
         float end_m[kMine];
+        if (kDirect) {
+            float none[2 * G] = {};
+            int first = 0;
+            q8_maxima<2 * G, 16>(none, lane, first);
+#pragma unroll
+            for (int e = 0; e < kMine; ++e) col[e] = 8 * ((first + e) >> 1) + pair2 + ((first + e) & 1);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kMine; ++e) col[e] = lane + 32 * e;
+        }
         auto part_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory"); };
         // adds O of tile j
         auto take = [&](int j) {
@@ -669,8 +673,8 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
             }
 #pragma unroll
             for (int e = 0; e < kMine; ++e) {
-                const int at = lane + 32 * e, c = 8 * PARTS * (at >> 3) + (at & 7);
-                if (quad == 0 && at < kCols && c < left) ml[8 * c] = end_m[e];
+                const int c = 8 * PARTS * (col[e] >> 3) + (col[e] & 7);
+                if (quad == 0 && col[e] < kCols && c < left) ml[8 * c] = end_m[e];
             }
         };
 #pragma unroll
@@ -679,7 +683,7 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
             for (int c = 0; c < 4; ++c) o[e][c] = 0;
         q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
             const Q8View& v = b.view[t.view];
-            const int R = v.n_nodes * GQ;
+            const int R = v.n_nodes * (Hq / Hkv);
             if (t.view * Hkv + t.g != last) {
                 __syncwarp();
                 if (last >= 0 && lane == 0) mbar_arrive(&bar.q_free[head % S::kHeads]);  // (its units have been read)
@@ -688,12 +692,15 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                 ok = ok && mbar_wait(&bar.q_full[head % S::kHeads], (head / S::kHeads) & 1, late);
                 if (head == 0) pdl_wait();  // (the results' place is free)
             }
+            // (out of the views' table, once)
+            const int sealed = v.sealed, front = v.front, skip = v.back - v.front, sinks = v.sinks, chunk = v.chunk, tile0 = t.t0;
+            const int edge = v.window > 0 ? v.sealed + v.tail + v.n_nodes - v.window : INT_MIN;  // keys from here on are in every row's window
             const float* units = unit_s[head % S::kHeads][part];
             const int* froms = from_s[head % S::kHeads][part];
             int64_t pr = v.part0 + ((int64_t)t.c * Hkv + t.g) * R;  // the chunk's rows of results
             int kc = 0;                                              // the chunk's tiles so far
             for (int k = 0; k < t.tiles; ++k, ++i) {
-                const int key0 = q8_tile_key(v, t.t0 + k), buf = i & 1, from = i % S::kScores;
+                const int key0 = (tile0 + k + (tile0 + k < front ? 0 : skip)) * kQ8Page, buf = i & 1, from = i % S::kScores;
                 const float* sc = scales[i % kQ8ScaleSlots];
                 if (kc == 0) {
 #pragma unroll
@@ -701,10 +708,9 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
 #pragma unroll
                     for (int e = 0; e < kMine; ++e) m[e] = -INFINITY;
                 }
-                ok = ok && mbar_wait(&bar.sc_full[i % kQ8ScaleSlots], (i / kQ8ScaleSlots) & 1, late) &&
-                     mbar_wait(&bar.s_full[from], (i / S::kScores) & 1, late);
+                ok = ok && mbar_wait(&bar.s_full[from], (i / S::kScores) & 1, late);
                 tm_after();
-                const bool valid = key0 + kQ8Block * quad < v.sealed;
+                const bool valid = key0 + kQ8Block * quad < sealed;
                 const float ks = valid ? sc[quad] : 0.0f;
                 // V's scale goes into the weights as a power of two: 2^(s + log2 vs - m) is
                 // what multiplies a code, and over vs the weight itself.  (A block of zeros
@@ -713,7 +719,7 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                 float lv;
                 asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lv) : "f"(vs));
                 const float iv = __frcp_rn(vs);
-                const bool masked = v.window > 0 && key0 < v.sealed + v.tail + v.n_nodes - v.window && key0 + kQ8Page > v.sinks;
+                const bool masked = key0 < edge && key0 + kQ8Page > sinks;
                 // scores, `B` groups at a time: held from the maxima on where there are few, else read twice
                 constexpr int B = S::kTwice ? 2 : G;
                 float s[B][8];
@@ -736,7 +742,7 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
 #pragma unroll
                             for (int c = 0; c < 8; ++c) {
                                 const int key = key0 + kQ8Block * quad + (lane >> 2) + 8 * (c >> 1);
-                                if (key >= v.sinks && key < (c & 1 ? key1.y : key1.x)) s[e][c] = -INFINITY;
+                                if (key >= sinks && key < (c & 1 ? key1.y : key1.x)) s[e][c] = -INFINITY;
                             }
                         }
                     }
@@ -754,20 +760,22 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                 if (!S::kTwice) warp_arrive(&bar.s_free[from]);
                 int first = 0;
                 q8_maxima<2 * G, 16>(top, lane, first);
-#pragma unroll
-                for (int e = 0; e < q8_left(2 * G); ++e) {
-                    const int at = first + e;
-                    mx[buf][part][quad][8 * (at >> 1) + pair2 + (at & 1)] = top[e];
-                }
-                __syncwarp();
                 float factor[kMine];
+                if (!kDirect) {
+#pragma unroll
+                    for (int e = 0; e < q8_left(2 * G); ++e) {
+                        const int at = first + e;
+                        mx[buf][part][quad][8 * (at >> 1) + pair2 + (at & 1)] = top[e];
+                    }
+                    __syncwarp();
+                }
 #pragma unroll
                 for (int e = 0; e < kMine; ++e)
-                    if (lane + 32 * e < kCols) {
+                    if (kDirect || col[e] < kCols) {
                         // (rounded up: no weight is above 2^15 by more than its exponent's own rounding)
-                        float* x = &mx[buf][part][quad][lane + 32 * e];
-                        factor[e] = fmaxf(__fmul_rn(units[lane + 32 * e], ks), 1e-37f);
-                        *x = __fadd_ru(__fmul_ru(*x, factor[e]), lv);
+                        float* x = &mx[buf][part][quad][col[e]];
+                        factor[e] = fmaxf(__fmul_rn(units[col[e]], ks), 1e-37f);
+                        *x = __fadd_ru(__fmul_ru(kDirect ? top[e] : *x, factor[e]), lv);
                     }
                 // all four warps of a part meet here, an expired wait or not, and leave together
                 if (!ok) bail[part][buf] = 1;
@@ -778,17 +786,19 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                 }
 #pragma unroll
                 for (int e = 0; e < kMine; ++e)
-                    if (lane + 32 * e < kCols) {
-                        const float* x = &mx[buf][part][0][lane + 32 * e];
+                    if (kDirect || col[e] < kCols) {
+                        const float* x = &mx[buf][part][0][col[e]];
                         const float now = fmaxf(m[e], max3(fmaxf(x[0], x[kCols]), x[2 * kCols], x[3 * kCols]));
                         const float at = now == -INFINITY ? 0.0f : now;
-                        factor_s[warp][lane + 32 * e] = factor[e];
-                        offset_s[warp][lane + 32 * e] = __fadd_rn(__fsub_rn(kQ8Up, at), lv);
-                        alpha_s[buf][warp][lane + 32 * e] = tree_exp2(__fsub_rn(m[e], at));  // 0 for m = -inf
+                        factor_s[warp][col[e]] = factor[e];
+                        offset_s[warp][col[e]] = __fadd_rn(__fsub_rn(kQ8Up, at), lv);
+                        alpha_s[buf][warp][col[e]] = tree_exp2(__fsub_rn(m[e], at));  // 0 for m = -inf
                         m[e] = now;
                     }
                 __syncwarp();
-                ok = ok && mbar_wait(&bar.p_free[i % S::kWeights], ((i / S::kWeights) & 1) ^ 1, late);
+                // (the place of the weights: with two of them the O that was last taken says that
+                // it is free, with one the last tile's is needed first)
+                if (S::kWeights == 1 && i > 0) take(i - 1);
                 const uint32_t to = smem_addr(ps) + (i % S::kWeights) * 2 * S::kPart + row_at;
                 const uint64_t iv2 = pair(iv, iv);
 #pragma unroll
@@ -818,9 +828,9 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.p_full[i % S::kWeights]);
-                if (i > 0) take(i - 1);
+                if (S::kWeights == 2 && i > 0) take(i - 1);
                 end_row = -1;
-                if (++kc == v.chunk || k + 1 == t.tiles) {  // the chunk's last tile
+                if (++kc == chunk || k + 1 == t.tiles) {  // the chunk's last tile
                     end_row = pr;
                     end_left = R;
 #pragma unroll
