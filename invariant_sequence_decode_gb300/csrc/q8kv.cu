@@ -273,8 +273,8 @@ __device__ int q8_produce(const Q8Maps& maps, const Q8Batch& b, int Hkv, const Q
 __device__ __forceinline__ void q8_turn(const uint8_t* tile, int row, uint32_t to)
 {
     const uint8_t* p = tile + row * 128;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {  // (code that fits the schedulers' first instruction cache, here and below)
         uint32_t o[32];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -296,23 +296,20 @@ __device__ void q8_turn_tiles(int n, const uint8_t* tiles, uint32_t tmem, int qu
     unsigned int* late = &g_q8kv_wait_timeouts;
     const int row = 32 * quad + lane;
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
-    int i = 0;
-    // one of the ring's tiles, as soon as its place is free
-    auto turn = [&](uint64_t* free, uint32_t parity, uint64_t* full, uint32_t to) {
-        const int st = i % S::kSlots;
-        const bool there = mbar_wait(&bar.full[st], (i / S::kSlots) & 1, late) && mbar_wait(free, parity, late);
-        if (!__all_sync(0xffffffffu, there)) return false;
+    // K of tile 0, then K of tile k and V of tile k - 1 in turn, V of the last
+#pragma unroll 1
+    for (int i = 0; i < 2 * n; ++i) {
+        const bool is_v = i > 0 && ((i & 1) == 0 || i == 2 * n - 1);
+        const int st = i % S::kSlots, tile = is_v ? (i - 1) >> 1 : (i + 1) >> 1, to = is_v ? tile & 1 : 0;
+        uint64_t* free = is_v ? &bar.va_free[to] : &bar.ka_free;
+        uint64_t* done = is_v ? &bar.va_full[to] : &bar.ka_full;
+        const bool there = mbar_wait(&bar.full[st], (i / S::kSlots) & 1, late) &&
+                           mbar_wait(free, ((is_v ? tile >> 1 : tile) & 1) ^ 1, late);
+        if (!__all_sync(0xffffffffu, there)) return;
         tm_after();
-        q8_turn(tiles + st * kQ8PageBytes, row, lanes + to);
-        warp_arrive(full);
+        q8_turn(tiles + st * kQ8PageBytes, row, lanes + (is_v ? S::kColV + 64 * to : S::kColK));
+        warp_arrive(done);
         if (lane == 0) mbar_arrive(&bar.empty[st]);
-        ++i;
-        return true;
-    };
-    for (int k = 0; k <= n; ++k) {  // K of tile k, V of the one before it
-        const int j = k - 1, to = j & 1;
-        if (k < n && !turn(&bar.ka_free, (k & 1) ^ 1, &bar.ka_full, S::kColK)) return;
-        if (k > 0 && !turn(&bar.va_free[to], ((j >> 1) & 1) ^ 1, &bar.va_full[to], S::kColV + 64 * to)) return;
     }
 }
 
@@ -327,7 +324,7 @@ __device__ __forceinline__ void q8_multiply(uint32_t d, uint32_t a, uint32_t byt
     d = __shfl_sync(0xffffffffu, d, 0);
     a = __shfl_sync(0xffffffffu, a, 0);
     const uint64_t desc = tree_desc(__shfl_sync(0xffffffffu, bytes, 0), 16, 1024);
-#pragma unroll
+#pragma unroll 4
     for (int ks = 0; ks < 16; ++ks)
         tree_mma(d, a + 8 * (ks & 7), desc + ((ks < 8 ? S::kPart : 0) + (ks >> 2 & 1) * (S::kPart / 2)) / 16 + 2 * (ks & 3), idesc, ks > 0,
                  elected);
@@ -645,7 +642,7 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                     for (int c = 0; c < 4; ++c) o[e][c] = fma2(o[e][c], a, pair(x[e - e0][2 * c], x[e - e0][2 * c + 1]));
                 }
             }
-            if (end_row < 0) return;
+            if (__builtin_expect(end_row < 0, 1)) return;
             float* ml = part_ml + 8 * (end_row + 8 * part);
             float* po = part_o + (end_row + 8 * part + pair2) * kHeadDim + 32 * quad + (lane >> 2);
             asm volatile("" : "+l"(ml), "+l"(po));  // (one address each, not one for every store)
@@ -730,12 +727,12 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                         tm_ld_frag(lanes + (16u << 16) + S::kColS + S::kRows * from + 8 * PARTS * (e0 + e), s[e] + 4);
                     }
                     tm_loaded<8 * B>(&s[0][0]);
-                    if (!valid) {
+                    if (__builtin_expect(!valid, 0)) {
 #pragma unroll
                         for (int e = 0; e < B; ++e)
 #pragma unroll
                             for (int c = 0; c < 8; ++c) s[e][c] = -INFINITY;
-                    } else if (masked) {
+                    } else if (__builtin_expect(masked, 0)) {
 #pragma unroll
                         for (int e = 0; e < B; ++e) {
                             const int2 key1 = *reinterpret_cast<const int2*>(&froms[8 * (e0 + e) + pair2]);
