@@ -37,30 +37,33 @@ struct Q8Scale {
     float sign, log2;
 };
 
-// Tiles of a chunk for a view of nt tiles: of the cuts that fill the kernel's CTAs
-// (kQ8Ctas of them where rows are few, half as many with twice the warps where they
-// are many) 1, 2, 3 or 4 times the cheapest is taken, a chunk costing its tiles and about one more
-// (its q, its results).  A function of the tiles and the KV heads alone, so that a
-// row's sums are cut the same way whatever else is in the call.
+// Tiles of a chunk for a view of nt tiles, an even number: a step of the kernel takes
+// two.  Of the cuts that fill the kernel's CTAs (kQ8Ctas of them where rows are few, half
+// as many with twice the warps where they are many) 1, 2, 3 or 4 times the cheapest
+// is taken, a chunk costing its steps and about one more (its q, its results).  A
+// function of the tiles and the KV heads alone, so that a row's sums are cut the same
+// way whatever else is in the call.
 static int q8_chunk_tiles(int nt, int Hkv)
 {
-    int best = nt, least = INT_MAX;
+    const int all = (nt + 1) / 2;
+    int best = all, least = INT_MAX;
     for (int rounds = 1; rounds <= 4; ++rounds) {
-        const int n = std::min({kQ8Ctas * rounds / Hkv, nt, kQ8MaxChunks});
+        const int n = std::min({kQ8Ctas * rounds / Hkv, all, kQ8MaxChunks});
         if (n < 1) continue;
-        const int tiles = (nt + n - 1) / n;
-        const int cost = (Hkv * n + kQ8Ctas - 1) / kQ8Ctas * (tiles + 1);
+        const int steps = (all + n - 1) / n;
+        const int cost = (Hkv * n + kQ8Ctas - 1) / kQ8Ctas * (steps + 1);
         if (cost < least) {
             least = cost;
-            best = tiles;
+            best = steps;
         }
     }
-    return std::max(best, 1);
+    return 2 * std::max(best, 1);
 }
 
 int q8kv_max_chunks(int max_sealed, int Hkv)
 {
-    return std::min({(max_sealed + kQ8Page - 1) / kQ8Page, kQ8MaxChunks, std::max(1, 4 * kQ8Ctas / Hkv)});
+    const int tiles = (max_sealed + kQ8Page - 1) / kQ8Page;
+    return std::min({(tiles + 1) / 2, kQ8MaxChunks, std::max(1, 4 * kQ8Ctas / Hkv)});
 }
 
 // A chunk's row of results: part_o [row][128] and part_ml [row][8] = (m, three unused,
@@ -83,11 +86,13 @@ int64_t q8kv_chunks(Q8Batch& b, int Hq, int Hkv)
             if (v.front >= v.back) v.front = v.back = all;
         }
         v.n_tile = v.front + all - v.back;
-        v.chunk = v.n_tile ? q8_chunk_tiles(v.n_tile, Hkv) : 1;
+        v.chunk = v.n_tile ? q8_chunk_tiles(v.n_tile, Hkv) : 2;
         v.n_chunk = (v.n_tile + v.chunk - 1) / v.chunk;
         v.part0 = part;
         part += (int64_t)v.n_chunk * v.n_nodes * Hq;
+        b.order[i] = (uint8_t)i;
     }
+    std::stable_sort(b.order, b.order + b.n_view, [&](int x, int y) { return b.view[x].chunk > b.view[y].chunk; });
     return part;
 }
 
@@ -117,14 +122,18 @@ struct Q8Shape {
     // 80 each, 65,536 with 128
     static constexpr int kRegs = PARTS == 1 ? 144 : 200, kOther = PARTS == 1 ? 48 : 56;
     static constexpr int kSlots = NG == 1 ? 4 : NG == 2 ? 3 : NG == 3 ? 7 : NG == 6 ? 4 : 5;  // tiles of K or V in flight
-    // In tensor memory: one tile of K, which is multiplied as soon as it is there, two
-    // of V, which wait for their weights, and two of scores where there is room
-    static constexpr int kTurnedV = 2, kScores = NG == 2 || NG == 8 ? 1 : 2;
+    // In tensor memory: one tile of K, which is multiplied as soon as it is there, the
+    // scores of a step's two, and its V, which waits for their weights
+    static constexpr int kTurnedV = NG == 2 || NG == 8 ? 1 : 2;
     static constexpr int kWeights = NG == 8 ? 1 : 2;           // tiles of weights in shared memory
     static constexpr int kHeads = NG == 1 || NG == 3 || NG == 4 ? 2 : 1;  // heads of q in shared memory
-    static constexpr bool kTwice = NG == 8;                    // scores are read twice, not held while maxima are found
+    static constexpr bool kTwice = NG == 2 || NG >= 5;                    // scores are read twice, not held while maxima are found
+    // The next step's K is turned ahead of a step's V, so that its scores come early.
+    // (Not where the second tile's weights wait for the first's product: scores would wait
+    // for V, V behind K for scores.)
+    static constexpr bool kKeysFirst = kWeights == 2;
     static constexpr int kPart = kRows * kHeadDim * 2;         // bytes of one part of q, or of the weights
-    static constexpr uint32_t kColK = 0, kColV = 64, kColS = kColV + 64 * kTurnedV, kColO = kColS + kScores * kRows;
+    static constexpr uint32_t kColK = 0, kColV = 64, kColS = kColV + 64 * kTurnedV, kColO = kColS + 2 * kRows;
     static constexpr uint32_t kTmem = 512 / kCtas;
     static constexpr int kBytes = kSlots * kQ8PageBytes + 2 * (kHeads + kWeights) * kPart + 1024;
     static_assert(kColO + kRows <= kTmem && 2 * NG % PARTS == 0, "tensor memory");
@@ -139,15 +148,15 @@ struct Q8Bars {
     uint64_t full[S::kSlots], empty[S::kSlots];          // a tile of K or V is there; has been turned
     uint64_t ka_full, ka_free;                           // K of a tile is f16 in tensor memory; has been multiplied
     uint64_t va_full[S::kTurnedV], va_free[S::kTurnedV];
-    uint64_t s_full[S::kScores], s_free[S::kScores];     // S of a tile is complete; has been read
-    uint64_t p_full[S::kWeights];                        // its weights are in place
-    uint64_t o_full, o_free;                             // O of a tile is complete; has been read
+    uint64_t s_full, s_free;                             // S of a step is complete; has been read
+    uint64_t p_full[S::kWeights], p_free;                // a tile's weights are in place; have been multiplied (where there is one place)
+    uint64_t o_full, o_free;                             // O of a step is complete; has been read
     uint64_t q_full[S::kHeads], q_free[S::kHeads];       // a head's q is in place; has been multiplied, its units read
     uint64_t done[2];                                    // every S, every O that was issued is complete
 };
 
 // Chunks of one (view, KV head) that a CTA takes one after the other: `chunks` of
-// them from number c on, tiles t0 .. t0 + tiles - 1, in the order view, head, chunk.
+// them from number c on, tiles t0 .. t0 + tiles - 1; views in b.order, head, chunk.
 struct Q8Run {
     int view, g, c, chunks, tiles, t0;
 };
@@ -156,8 +165,9 @@ __device__ __forceinline__ Q8Run q8_run(const Q8Batch& b, int Hkv, int u, int en
 {
     Q8Run t;
     const int u0 = u;
-    t.view = 0;
-    while (t.view + 1 < b.n_view && u >= Hkv * b.view[t.view].n_chunk) u -= Hkv * b.view[t.view++].n_chunk;
+    int at = 0;
+    while (at + 1 < b.n_view && u >= Hkv * b.view[b.order[at]].n_chunk) u -= Hkv * b.view[b.order[at++]].n_chunk;
+    t.view = b.order[at];
     const Q8View& v = b.view[t.view];
     t.g = u / v.n_chunk;
     t.c = u - t.g * v.n_chunk;
@@ -167,7 +177,9 @@ __device__ __forceinline__ Q8Run q8_run(const Q8Batch& b, int Hkv, int u, int en
     return t;
 }
 
-// The CTA's runs: chunks u0, u0 + step, .. below u1, or one run of neighbours (step 0).
+// The CTA's runs.  Chunks of one step: neighbours u0 .. u1 - 1 (heads change least).
+// Longer ones: of every `step` of them one, from the longest on, back and forth, so
+// that the CTAs' shares are alike.
 struct Q8Share {
     int u0, u1, step;
 };
@@ -175,9 +187,10 @@ struct Q8Share {
 template <typename F>
 __device__ __forceinline__ void q8_each_run(const Q8Batch& b, int Hkv, const Q8Share& w, F f)
 {
-    for (int u = w.u0, next; u < w.u1; u = next) {
+    int u = w.u0;
+    for (int round = 1; u < w.u1; ++round) {
         const Q8Run t = q8_run(b, Hkv, u, w.step ? u + 1 : w.u1);
-        next = w.step ? u + w.step : u + t.chunks;
+        u = !w.step ? u + t.chunks : round & 1 ? (round + 1) * w.step - 1 - w.u0 : round * w.step + w.u0;
         if (!f(t)) return;
     }
 }
@@ -215,15 +228,18 @@ __device__ __forceinline__ void q8_half_codes(uint32_t w, uint32_t& lo, uint32_t
     asm("{ .reg .b32 n; mov.b32 n, 0x64806480; sub.rn.f16x2 %0, %1, n; }" : "=r"(hi) : "r"(b));
 }
 
-// The producer: tiles and scales of the CTA's runs, in order, a tile's V behind the
-// next tile's K (which is needed first).  Returns the tiles of K and V issued.
+// A step's tiles: two, or one at a run's end.
+__device__ __forceinline__ int q8_step_tiles(const Q8Run& t, int k) { return min(2, t.tiles - k); }
+
+// The producer: tiles and scales of the CTA's runs, in the order in which they are
+// turned.  Returns the tiles of K and V issued.
 template <typename S>
 __device__ int q8_produce(const Q8Maps& maps, const Q8Batch& b, int Hkv, const Q8Share& w, uint8_t* tiles, float (*scales)[8],
                           Q8Bars<S>& bar)
 {
     unsigned int* late = &g_q8kv_wait_timeouts;
     int i = 0, n = 0;  // tiles of K and V, tiles
-    int view = -1, g = 0, page = 0;  // the last tile's
+    int view = -1, g = 0, page[2] = {}, values = 0;  // the last step's, whose V is still to come
     // scales (nullable): come with the tile; the weights' warps read them behind S, which
     // the turning warps' wait for this tile has come before
     auto load = [&](const CUtensorMap* m, int head, int p, const float* sc, float* to) {
@@ -238,6 +254,12 @@ __device__ int q8_produce(const Q8Maps& maps, const Q8Batch& b, int Hkv, const Q
         ++i;
         return true;
     };
+    auto load_values = [&] {
+        for (int x = 0; x < values; ++x)
+            if (!load(&maps.v[view], g, page[x], nullptr, nullptr)) return false;
+        values = 0;
+        return true;
+    };
     pdl_wait();
     pdl_trigger();
     bool ok = true;
@@ -247,25 +269,32 @@ __device__ int q8_produce(const Q8Maps& maps, const Q8Batch& b, int Hkv, const Q
             const int span = q8_tile_key(v, t.t0 + k) / kQ8Page;
             return v.table ? ld_placed_i(v.table + span) : span;
         };
-        int next = page_of(0);
-        for (int k = 0; k < t.tiles; ++k, ++n) {
-            int now = next;
-            if (k + 1 < t.tiles) next = page_of(k + 1);  // (on its way while this tile's place becomes free)
-            const bool in = now >= 0 && now < v.n_pages;
-            if (!in) now = v.n_pages;                    // outside the map: zeros
-            float* to = scales[n % kQ8ScaleSlots];
-            if (!in)
-                for (int e = 0; e < 8; ++e) to[e] = 0.0f;
-            const float* sc = in ? v.scales + now * v.scale_stride + t.g * kQ8PageScales : nullptr;
-            if (!(ok = load(&maps.k[t.view], t.g, now, sc, to))) return false;
-            if (view >= 0 && !(ok = load(&maps.v[view], g, page, nullptr, nullptr))) return false;
+        int next[2] = {page_of(0), t.tiles > 1 ? page_of(1) : 0};
+        for (int k = 0; k < t.tiles; k += 2) {
+            int now[2] = {next[0], next[1]};
+            for (int x = 0; x < 2; ++x)
+                if (k + 2 + x < t.tiles) next[x] = page_of(k + 2 + x);  // (on their way while this step's places become free)
+            const int two = q8_step_tiles(t, k);
+            for (int x = 0; x < two; ++x, ++n) {
+                const bool in = now[x] >= 0 && now[x] < v.n_pages;
+                if (!in) now[x] = v.n_pages;             // outside the map: zeros
+                float* to = scales[n % kQ8ScaleSlots];
+                if (!in)
+                    for (int e = 0; e < 8; ++e) to[e] = 0.0f;
+                const float* sc = in ? v.scales + now[x] * v.scale_stride + t.g * kQ8PageScales : nullptr;
+                if (!(ok = load(&maps.k[t.view], t.g, now[x], sc, to))) return false;
+            }
+            if (S::kKeysFirst && !(ok = load_values())) return false;
             view = t.view;
             g = t.g;
-            page = now;
+            page[0] = now[0];
+            page[1] = now[1];
+            values = two;
+            if (!S::kKeysFirst && !(ok = load_values())) return false;
         }
         return true;
     });
-    if (ok && view >= 0) load(&maps.v[view], g, page, nullptr, nullptr);
+    if (ok) load_values();
     return i;
 }
 
@@ -291,33 +320,49 @@ __device__ __forceinline__ void q8_turn(const uint8_t* tile, int row, uint32_t t
 
 // The turning warps: K and V of every tile, a row of 128 codes per thread.
 template <typename S>
-__device__ void q8_turn_tiles(int n, const uint8_t* tiles, uint32_t tmem, int quad, int lane, Q8Bars<S>& bar)
+__device__ void q8_turn_tiles(const Q8Batch& b, int Hkv, const Q8Share& w, const uint8_t* tiles, uint32_t tmem, int quad, int lane,
+                              Q8Bars<S>& bar)
 {
     unsigned int* late = &g_q8kv_wait_timeouts;
     const int row = 32 * quad + lane;
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
-    // K of tile 0, then K of tile k and V of tile k - 1 in turn, V of the last
+    int i = 0, nk = 0, nv = 0;  // tiles turned, of K, of V
+    // the next `keys` tiles of K, the next `values` of V, in the order of S::kKeysFirst
+    auto turn = [&](int keys, int values) {
 #pragma unroll 1
-    for (int i = 0; i < 2 * n; ++i) {
-        const bool is_v = i > 0 && ((i & 1) == 0 || i == 2 * n - 1);
-        const int st = i % S::kSlots, tile = is_v ? (i - 1) >> 1 : (i + 1) >> 1, to = is_v ? tile & 1 : 0;
-        uint64_t* free = is_v ? &bar.va_free[to] : &bar.ka_free;
-        uint64_t* done = is_v ? &bar.va_full[to] : &bar.ka_full;
-        const bool there = mbar_wait(&bar.full[st], (i / S::kSlots) & 1, late) &&
-                           mbar_wait(free, ((is_v ? tile >> 1 : tile) & 1) ^ 1, late);
-        if (!__all_sync(0xffffffffu, there)) return;
-        tm_after();
-        q8_turn(tiles + st * kQ8PageBytes, row, lanes + (is_v ? S::kColV + 64 * to : S::kColK));
-        warp_arrive(done);
-        if (lane == 0) mbar_arrive(&bar.empty[st]);
-    }
+        for (int x = 0; x < keys + values; ++x, ++i) {
+            const bool is_v = x >= keys;
+            const int st = i % S::kSlots, to = is_v ? nv % S::kTurnedV : 0;
+            const uint32_t parity = ((is_v ? nv / S::kTurnedV : nk) & 1) ^ 1;
+            const bool there = mbar_wait(&bar.full[st], (i / S::kSlots) & 1, late) &&
+                               mbar_wait(is_v ? &bar.va_free[to] : &bar.ka_free, parity, late);
+            if (!__all_sync(0xffffffffu, there)) return false;
+            tm_after();
+            q8_turn(tiles + st * kQ8PageBytes, row, lanes + (is_v ? S::kColV + 64 * to : S::kColK));
+            warp_arrive(is_v ? &bar.va_full[to] : &bar.ka_full);
+            if (lane == 0) mbar_arrive(&bar.empty[st]);
+            (is_v ? nv : nk) += 1;
+        }
+        return true;
+    };
+    int values = 0;
+    bool ok = true;
+    q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
+        for (int k = 0; ok && k < t.tiles; k += 2) {
+            const int two = q8_step_tiles(t, k);
+            ok = turn(two, S::kKeysFirst ? values : two);
+            values = two;
+        }
+        return ok;
+    });
+    if (ok && S::kKeysFirst) turn(0, values);
 }
 
 // A product's steps, 128 x kRows x 16 each: A in tensor memory from column a, B rows of
 // 256 bytes in two halves.  The low parts go first: an accumulation loses digits by
 // the sum's size, and theirs is small.
 template <typename S>
-__device__ __forceinline__ void q8_multiply(uint32_t d, uint32_t a, uint32_t bytes, uint32_t elected)
+__device__ __forceinline__ void q8_multiply(uint32_t d, uint32_t a, uint32_t bytes, bool adds, uint32_t elected)
 {
     constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(S::kRows / 8) << 17) | (8u << 24);  // D f32, A and B f16
     // (told to be the warp's, as they are: else every product moves its own copies)
@@ -326,8 +371,8 @@ __device__ __forceinline__ void q8_multiply(uint32_t d, uint32_t a, uint32_t byt
     const uint64_t desc = tree_desc(__shfl_sync(0xffffffffu, bytes, 0), 16, 1024);
 #pragma unroll 4
     for (int ks = 0; ks < 16; ++ks)
-        tree_mma(d, a + 8 * (ks & 7), desc + ((ks < 8 ? S::kPart : 0) + (ks >> 2 & 1) * (S::kPart / 2)) / 16 + 2 * (ks & 3), idesc, ks > 0,
-                 elected);
+        tree_mma(d, a + 8 * (ks & 7), desc + ((ks < 8 ? S::kPart : 0) + (ks >> 2 & 1) * (S::kPart / 2)) / 16 + 2 * (ks & 3), idesc,
+                 adds || ks > 0, elected);
 }
 
 // The products are issued by a warp each: S of a tile as soon as its K is there, and
@@ -339,7 +384,7 @@ __device__ void q8_scores(const Q8Batch& b, int Hkv, const Q8Share& w, uint32_t 
 {
     unsigned int* late = &g_q8kv_wait_timeouts;
     const uint32_t elected = elect_one();
-    int i = 0, head = -1, last = -1;
+    int i = 0, n = 0, head = -1, last = -1;  // steps, tiles, heads
     q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
         bool ok = true;
         if (t.view * Hkv + t.g != last) {
@@ -348,14 +393,16 @@ __device__ void q8_scores(const Q8Batch& b, int Hkv, const Q8Share& w, uint32_t 
             ++head;
             ok = __all_sync(0xffffffffu, mbar_wait(&bar.q_full[head % S::kHeads], (head / S::kHeads) & 1, late));
         }
-        for (int k = 0; ok && k < t.tiles; ++k, ++i) {
-            const int to = i % S::kScores;
-            const bool there = mbar_wait(&bar.ka_full, i & 1, late) && mbar_wait(&bar.s_free[to], ((i / S::kScores) & 1) ^ 1, late);
+        for (int k = 0; ok && k < t.tiles; ++k, ++n) {
+            const bool there = mbar_wait(&bar.ka_full, n & 1, late) && ((k & 1) || mbar_wait(&bar.s_free, (i & 1) ^ 1, late));
             if (!(ok = __all_sync(0xffffffffu, there))) break;  // (the warp leaves as one)
             tm_after();
-            q8_multiply<S>(tmem + S::kColS + S::kRows * to, tmem + S::kColK, q + head % S::kHeads * 2 * S::kPart, elected);
-            tree_commit_mma(&bar.s_full[to], elected);
+            q8_multiply<S>(tmem + S::kColS + S::kRows * (k & 1), tmem + S::kColK, q + head % S::kHeads * 2 * S::kPart, false, elected);
             tree_commit_mma(&bar.ka_free, elected);
+            if ((k & 1) || k + 1 == t.tiles) {
+                tree_commit_mma(&bar.s_full, elected);
+                ++i;
+            }
         }
         return ok;
     });
@@ -365,21 +412,30 @@ __device__ void q8_scores(const Q8Batch& b, int Hkv, const Q8Share& w, uint32_t 
 }
 
 template <typename S>
-__device__ void q8_sums(int n, uint32_t weights, uint32_t tmem, Q8Bars<S>& bar)
+__device__ void q8_sums(const Q8Batch& b, int Hkv, const Q8Share& w, uint32_t weights, uint32_t tmem, Q8Bars<S>& bar)
 {
     unsigned int* late = &g_q8kv_wait_timeouts;
     const uint32_t elected = elect_one();
-    for (int j = 0; j < n; ++j) {
-        const int to = j % S::kTurnedV, p = j % S::kWeights;
-        const bool there = mbar_wait(&bar.va_full[to], (j / S::kTurnedV) & 1, late) &&
-                           mbar_wait(&bar.p_full[p], (j / S::kWeights) & 1, late) &&
-                           (j == 0 || mbar_wait(&bar.o_free, (j - 1) & 1, late));
-        if (!__all_sync(0xffffffffu, there)) break;
-        tm_after();
-        q8_multiply<S>(tmem + S::kColO, tmem + S::kColV + 64 * to, weights + p * 2 * S::kPart, elected);
-        tree_commit_mma(&bar.o_full, elected);
-        tree_commit_mma(&bar.va_free[to], elected);
-    }
+    int i = 0, n = 0, used[2] = {0, 0};  // steps, tiles, of the places of weights
+    q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
+        for (int k = 0; k < t.tiles; ++k, ++n) {
+            const int to = n % S::kTurnedV, p = (k & 1) % S::kWeights;
+            const bool there = mbar_wait(&bar.va_full[to], (n / S::kTurnedV) & 1, late) &&
+                               mbar_wait(&bar.p_full[p], (p ? used[1] : used[0]) & 1, late) &&
+                               ((k & 1) || i == 0 || mbar_wait(&bar.o_free, (i - 1) & 1, late));
+            if (!__all_sync(0xffffffffu, there)) return false;
+            (p ? used[1] : used[0]) += 1;
+            tm_after();
+            q8_multiply<S>(tmem + S::kColO, tmem + S::kColV + 64 * to, weights + p * 2 * S::kPart, k & 1, elected);
+            tree_commit_mma(&bar.va_free[to], elected);
+            if (S::kWeights == 1) tree_commit_mma(&bar.p_free, elected);
+            if ((k & 1) || k + 1 == t.tiles) {
+                tree_commit_mma(&bar.o_full, elected);
+                ++i;
+            }
+        }
+        return true;
+    });
     tree_commit_mma(&bar.done[1], elected);
     mbar_wait(&bar.done[1], 0, late);
 }
@@ -480,15 +536,15 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
     __shared__ Q8Bars<S> bar;
     __shared__ uint32_t tmem_at;
     __shared__ __align__(16) float scales[kQ8ScaleSlots][8];
-    // by part: its columns are the groups of eight PARTS e + part, numbered through
-    __shared__ float mx[2][PARTS][4][S::kCols];           // the columns' maxima of a tile's blocks, by tile parity
+    // by part, and by the step's parity: its columns are the groups of eight PARTS e + part, numbered through
+    __shared__ float mx[2][PARTS][4][S::kCols];           // the columns' maxima of a warp's keys, by step parity
     __shared__ float unit_s[S::kHeads][PARTS][S::kCols];             // a score's power of two per unit of its product
     __shared__ __align__(8) int from_s[S::kHeads][PARTS][S::kCols];  // the first key in the row's window
     // by warp: what turns a column's products into exponents (a factor, an offset),
-    // and what O so far is multiplied by, by tile parity
-    __shared__ __align__(8) float factor_s[S::kWarps][S::kCols], offset_s[S::kWarps][S::kCols];
+    // for each of a step's tiles, and what O so far is multiplied by, by step parity
+    __shared__ __align__(8) float factor_s[S::kWarps][2][S::kCols], offset_s[S::kWarps][2][S::kCols];
     __shared__ __align__(8) float alpha_s[2][S::kWarps][S::kCols];
-    __shared__ volatile int bail[PARTS][2];               // a wait of the part's warps expired, by tile parity
+    __shared__ volatile int bail[PARTS][2];               // a wait of the part's warps expired, by step parity
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (warp == S::kWarps + 6) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_at)), "r"(S::kTmem));
@@ -505,10 +561,9 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
             mbar_init(&bar.va_full[i], 4);
             mbar_init(&bar.va_free[i], 1);
         }
-        for (int i = 0; i < S::kScores; ++i) {
-            mbar_init(&bar.s_full[i], 1);
-            mbar_init(&bar.s_free[i], S::kWarps);
-        }
+        mbar_init(&bar.s_full, 1);
+        mbar_init(&bar.s_free, S::kWarps);
+        mbar_init(&bar.p_free, 1);
         for (int i = 0; i < PARTS; ++i) bail[i][0] = bail[i][1] = 0;
         for (int i = 0; i < S::kWeights; ++i) mbar_init(&bar.p_full[i], S::kWarps);
         mbar_init(&bar.o_full, 1);
@@ -531,21 +586,11 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
         if (b.view[view].n_chunk > 0)  // (a view without blocks has no map)
             asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
     }
-    // one-tile chunks: a run of them each (a run's heads change least); longer
-    // ones: every gridDim.x-th, as chunks of unlike views then spread evenly
     Q8Share w = {(int)blockIdx.x, units, (int)gridDim.x};
     if (runs)
         w = Q8Share{(int)((int64_t)units * blockIdx.x / gridDim.x), (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x), 0};
     unsigned int* late = &g_q8kv_wait_timeouts;
 
-    auto tiles_of_all = [&] {
-        int n = 0;
-        q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
-            n += t.tiles;
-            return true;
-        });
-        return n;
-    };
     if (warp >= S::kWarps + 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kOther));
         if (warp == S::kWarps + 4 && lane == 0) {
@@ -560,7 +605,7 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
             q8_prepare<S>(q, b, Hq, Hkv, q8_run(b, Hkv, w.u0, w.u0 + 1), scale, qs, unit_s[0], from_s[0], first, 6);
             asm volatile("bar.sync 15, 96;" ::: "memory");
             if (warp == S::kWarps + 5) q8_scores(b, Hkv, w, smem_addr(qs), tmem, bar);
-            if (warp == S::kWarps + 6) q8_sums(tiles_of_all(), smem_addr(ps), tmem, bar);
+            if (warp == S::kWarps + 6) q8_sums(b, Hkv, w, smem_addr(ps), tmem, bar);
             if (warp == S::kWarps + 7) {
                 int head = -1, last = -1;
                 q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
@@ -580,7 +625,7 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
         __syncwarp();
     } else if (warp >= S::kWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kOther));
-        q8_turn_tiles(tiles_of_all(), tiles, tmem, warp & 3, lane, bar);
+        q8_turn_tiles(b, Hkv, w, tiles, tmem, warp & 3, lane, bar);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegs));
         // The warp's keys are its block of the tile, 32 quad ..; its columns the groups of
@@ -589,11 +634,8 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
         // the same for a column's keys (maximum, factor, correction) a lane forms per
         // column, and the threads pick it up from shared memory: formed by each
         // thread for its own columns it took twice the instructions of the weights.
-        // (a lane's columns: where the groups are a power of two, those whose maxima it ends
-        // with; else lane, lane + 32, ..)
-        constexpr int G = S::kGroups, kCols = S::kCols;
-        constexpr bool kDirect = (G & (G - 1)) == 0;
-        constexpr int kMine = kDirect ? q8_left(2 * G) : (kCols + 31) / 32;
+        // (a lane's columns are those whose maxima it ends with)
+        constexpr int G = S::kGroups, kCols = S::kCols, kMine = q8_left(2 * G);
         int col[kMine];
         const int part = warp >> 2, quad = warp & 3, pair2 = 2 * (lane & 3);
         const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16) + 8 * part;
@@ -601,26 +643,24 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                                 (((4 * (quad & 1) + (lane >> 3)) ^ (lane & 7)) << 4);  // where its keys' weights go
         uint64_t o[G][4], l[G];        // pairs of columns
         float m[kMine];                // of the lane's columns
-        int i = 0, head = -1, last = -1;
+        int i = 0, n = 0, head = -1, last = -1;  // steps, tiles, heads
         bool ok = true, gone = false;
-        // the chunk whose last tile's O is still to come: its rows of results (-1: it is not a
-        // chunk's last tile), how many they are, their weights' sums and maxima
+        int freed = 0;                 // tiles whose weights have been given to be multiplied
+        // the chunk whose last step's O is still to come: its rows of results (-1: it is not a
+        // chunk's last step), how many they are, their weights' sums and maxima
         int64_t end_row = -1;
         int end_left = 0;
         uint64_t end_l[G];
         float end_m[kMine];
-        if (kDirect) {
+        {
             float none[2 * G] = {};
             int first = 0;
             q8_maxima<2 * G, 16>(none, lane, first);
 #pragma unroll
             for (int e = 0; e < kMine; ++e) col[e] = 8 * ((first + e) >> 1) + pair2 + ((first + e) & 1);
-        } else {
-#pragma unroll
-            for (int e = 0; e < kMine; ++e) col[e] = lane + 32 * e;
         }
         auto part_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory"); };
-        // adds O of tile j
+        // adds O of step j
         auto take = [&](int j) {
             ok = __all_sync(0xffffffffu, ok && mbar_wait(&bar.o_full, j & 1, late));
             tm_after();
@@ -696,84 +736,82 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
             const int* froms = from_s[head % S::kHeads][part];
             int64_t pr = v.part0 + ((int64_t)t.c * Hkv + t.g) * R;  // the chunk's rows of results
             int kc = 0;                                              // the chunk's tiles so far
-            for (int k = 0; k < t.tiles; ++k, ++i) {
-                const int key0 = (tile0 + k + (tile0 + k < front ? 0 : skip)) * kQ8Page, buf = i & 1, from = i % S::kScores;
-                const float* sc = scales[i % kQ8ScaleSlots];
+            for (int k = 0; k < t.tiles; k += 2, ++i) {
+                const int two = q8_step_tiles(t, k), buf = i & 1;
                 if (kc == 0) {
 #pragma unroll
                     for (int e = 0; e < G; ++e) l[e] = 0;
 #pragma unroll
                     for (int e = 0; e < kMine; ++e) m[e] = -INFINITY;
                 }
-                ok = ok && mbar_wait(&bar.s_full[from], (i / S::kScores) & 1, late);
+                ok = ok && mbar_wait(&bar.s_full, i & 1, late);
                 tm_after();
-                const bool valid = key0 + kQ8Block * quad < sealed;
-                const float ks = valid ? sc[quad] : 0.0f;
-                // V's scale goes into the weights as a power of two: 2^(s + log2 vs - m) is
-                // what multiplies a code, and over vs the weight itself.  (A block of zeros
-                // weighs as one of the smallest scale, 2^-31.)
-                const float vs = fmaxf(valid ? sc[4 + quad] : 0.0f, 4.656612873e-10f);
-                float lv;
-                asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lv) : "f"(vs));
-                const float iv = __frcp_rn(vs);
-                const bool masked = key0 < edge && key0 + kQ8Page > sinks;
-                // scores, `B` groups at a time: held from the maxima on where there are few, else read twice
-                constexpr int B = S::kTwice ? 2 : G;
-                float s[B][8];
-                auto load_s = [&](int e0) {
+                // scores: both tiles', held from the maxima on where there are few, else read
+                // twice, `B` groups at a time
+                constexpr int B = G <= 5 ? G : G / 2;
+                float s[S::kTwice ? 1 : 2][B][8], factor[2][kMine], lv[2], iv[2], best[kMine];
+                auto load_s = [&](int x, int e0) {
+                    float(*to)[8] = s[S::kTwice ? 0 : x];
+                    const int key0 = (tile0 + k + x + (tile0 + k + x < front ? 0 : skip)) * kQ8Page;
 #pragma unroll
                     for (int e = 0; e < B; ++e) {
-                        tm_ld_frag(lanes + S::kColS + S::kRows * from + 8 * PARTS * (e0 + e), s[e]);
-                        tm_ld_frag(lanes + (16u << 16) + S::kColS + S::kRows * from + 8 * PARTS * (e0 + e), s[e] + 4);
+                        tm_ld_frag(lanes + S::kColS + S::kRows * x + 8 * PARTS * (e0 + e), to[e]);
+                        tm_ld_frag(lanes + (16u << 16) + S::kColS + S::kRows * x + 8 * PARTS * (e0 + e), to[e] + 4);
                     }
-                    tm_loaded<8 * B>(&s[0][0]);
-                    if (__builtin_expect(!valid, 0)) {
+                    tm_loaded<8 * B>(&to[0][0]);
+                    if (__builtin_expect(x >= two || key0 + kQ8Block * quad >= sealed, 0)) {
 #pragma unroll
                         for (int e = 0; e < B; ++e)
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) s[e][c] = -INFINITY;
-                    } else if (__builtin_expect(masked, 0)) {
+                            for (int c = 0; c < 8; ++c) to[e][c] = -INFINITY;
+                    } else if (__builtin_expect(key0 < edge && key0 + kQ8Page > sinks, 0)) {
 #pragma unroll
                         for (int e = 0; e < B; ++e) {
                             const int2 key1 = *reinterpret_cast<const int2*>(&froms[8 * (e0 + e) + pair2]);
 #pragma unroll
                             for (int c = 0; c < 8; ++c) {
                                 const int key = key0 + kQ8Block * quad + (lane >> 2) + 8 * (c >> 1);
-                                if (key >= sinks && key < (c & 1 ? key1.y : key1.x)) s[e][c] = -INFINITY;
+                                if (key >= sinks && key < (c & 1 ? key1.y : key1.x)) to[e][c] = -INFINITY;
                             }
                         }
                     }
                 };
-                float top[2 * G];
 #pragma unroll
-                for (int e0 = 0; e0 < G; e0 += B) {
-                    load_s(e0);
+                for (int x = 0; x < 2; ++x) {
+                    const float* sc = scales[(n + x) % kQ8ScaleSlots];
+                    const int key0 = (tile0 + k + x + (tile0 + k + x < front ? 0 : skip)) * kQ8Page;
+                    const bool valid = x < two && key0 + kQ8Block * quad < sealed;
+                    const float ks = valid ? sc[quad] : 0.0f;
+                    // V's scale goes into the weights as a power of two: 2^(s + log2 vs - m) is
+                    // what multiplies a code, and over vs the weight itself.  (A block of zeros
+                    // weighs as one of the smallest scale, 2^-31.)
+                    const float vs = fmaxf(valid ? sc[4 + quad] : 0.0f, 4.656612873e-10f);
+                    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lv[x]) : "f"(vs));
+                    iv[x] = __frcp_rn(vs);
+                    float top[2 * G];
 #pragma unroll
-                    for (int e = 0; e < B; ++e) {
-                        top[2 * (e0 + e)] = fmaxf(max3(s[e][0], s[e][2], s[e][4]), s[e][6]);
-                        top[2 * (e0 + e) + 1] = fmaxf(max3(s[e][1], s[e][3], s[e][5]), s[e][7]);
+                    for (int e0 = 0; e0 < G; e0 += B) {
+                        load_s(x, e0);
+#pragma unroll
+                        for (int e = 0; e < B; ++e) {
+                            const float* y = s[S::kTwice ? 0 : x][e];
+                            top[2 * (e0 + e)] = fmaxf(max3(y[0], y[2], y[4]), y[6]);
+                            top[2 * (e0 + e) + 1] = fmaxf(max3(y[1], y[3], y[5]), y[7]);
+                        }
                     }
-                }
-                if (!S::kTwice) warp_arrive(&bar.s_free[from]);
-                int first = 0;
-                q8_maxima<2 * G, 16>(top, lane, first);
-                float factor[kMine];
-                if (!kDirect) {
+                    int first = 0;
+                    q8_maxima<2 * G, 16>(top, lane, first);
 #pragma unroll
-                    for (int e = 0; e < q8_left(2 * G); ++e) {
-                        const int at = first + e;
-                        mx[buf][part][quad][8 * (at >> 1) + pair2 + (at & 1)] = top[e];
-                    }
-                    __syncwarp();
-                }
-#pragma unroll
-                for (int e = 0; e < kMine; ++e)
-                    if (kDirect || col[e] < kCols) {
+                    for (int e = 0; e < kMine; ++e) {
                         // (rounded up: no weight is above 2^15 by more than its exponent's own rounding)
-                        float* x = &mx[buf][part][quad][col[e]];
-                        factor[e] = fmaxf(__fmul_rn(units[col[e]], ks), 1e-37f);
-                        *x = __fadd_ru(__fmul_ru(kDirect ? top[e] : *x, factor[e]), lv);
+                        factor[x][e] = fmaxf(__fmul_rn(units[col[e]], ks), 1e-37f);
+                        const float y = __fadd_ru(__fmul_ru(top[e], factor[x][e]), lv[x]);
+                        best[e] = x ? fmaxf(best[e], y) : y;
                     }
+                }
+                if (!S::kTwice) warp_arrive(&bar.s_free);
+#pragma unroll
+                for (int e = 0; e < kMine; ++e) mx[buf][part][quad][col[e]] = best[e];
                 // all four warps of a part meet here, an expired wait or not, and leave together
                 if (!ok) bail[part][buf] = 1;
                 part_sync();
@@ -782,52 +820,60 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                     return false;
                 }
 #pragma unroll
-                for (int e = 0; e < kMine; ++e)
-                    if (kDirect || col[e] < kCols) {
-                        const float* x = &mx[buf][part][0][col[e]];
-                        const float now = fmaxf(m[e], max3(fmaxf(x[0], x[kCols]), x[2 * kCols], x[3 * kCols]));
-                        const float at = now == -INFINITY ? 0.0f : now;
-                        factor_s[warp][col[e]] = factor[e];
-                        offset_s[warp][col[e]] = __fadd_rn(__fsub_rn(kQ8Up, at), lv);
-                        alpha_s[buf][warp][col[e]] = tree_exp2(__fsub_rn(m[e], at));  // 0 for m = -inf
-                        m[e] = now;
-                    }
-                __syncwarp();
-                // (the place of the weights: with two of them the O that was last taken says that
-                // it is free, with one the last tile's is needed first)
-                if (S::kWeights == 1 && i > 0) take(i - 1);
-                const uint32_t to = smem_addr(ps) + (i % S::kWeights) * 2 * S::kPart + row_at;
-                const uint64_t iv2 = pair(iv, iv);
+                for (int e = 0; e < kMine; ++e) {
+                    const float* x = &mx[buf][part][0][col[e]];
+                    const float now = fmaxf(m[e], max3(fmaxf(x[0], x[kCols]), x[2 * kCols], x[3 * kCols]));
+                    const float at = now == -INFINITY ? 0.0f : now;
 #pragma unroll
-                for (int e = 0; e < G; ++e) {
-                    if (S::kTwice && e % B == 0) {
-                        load_s(e);
-                        if (e + B >= G) warp_arrive(&bar.s_free[from]);
+                    for (int d = 0; d < 2; ++d) {
+                        factor_s[warp][d][col[e]] = factor[d][e];
+                        offset_s[warp][d][col[e]] = __fadd_rn(__fsub_rn(kQ8Up, at), lv[d]);
                     }
-                    // (pairs as they lie: put together from single values they cost moves)
-                    const uint64_t f = *reinterpret_cast<const uint64_t*>(&factor_s[warp][8 * e + pair2]);
-                    const uint64_t up = *reinterpret_cast<const uint64_t*>(&offset_s[warp][8 * e + pair2]);
-                    const uint64_t a = *reinterpret_cast<const uint64_t*>(&alpha_s[buf][warp][8 * e + pair2]);
-                    uint64_t p[4];
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const float2 x = unpair(fma2(pair(s[e % B][2 * c], s[e % B][2 * c + 1]), f, up));
-                        const float p0 = tree_exp2(x.x), p1 = tree_exp2(x.y);
-                        p[c] = pair(p0, p1);
-                        tree_split(p0, p1, hi[c], lo[c]);
-                    }
-                    const uint64_t sum = add2(add2(p[0], p[1]), add2(p[2], p[3]));
-                    l[e] = fma2(sum, iv2, fma2(l[e], a, 0));
-                    st_matrix_turned(to + 1024 * PARTS * e, hi[0], hi[1], hi[2], hi[3]);
-                    st_matrix_turned(to + 1024 * PARTS * e + S::kPart, lo[0], lo[1], lo[2], lo[3]);
+                    alpha_s[buf][warp][col[e]] = tree_exp2(__fsub_rn(m[e], at));  // 0 for m = -inf
+                    m[e] = now;
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.p_full[i % S::kWeights]);
-                if (S::kWeights == 2 && i > 0) take(i - 1);
+                if (i > 0) take(i - 1);  // (behind its products the weights' places are free)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (x == 1 && two == 1) break;
+                    const uint32_t to = smem_addr(ps) + (x % S::kWeights) * 2 * S::kPart + row_at;
+                    const uint64_t iv2 = pair(iv[x], iv[x]);
+                    if (x == 1 && S::kWeights == 1) ok = ok && mbar_wait(&bar.p_free, freed & 1, late);
+#pragma unroll
+                    for (int e = 0; e < G; ++e) {
+                        if (S::kTwice && e % B == 0) {
+                            load_s(x, e);
+                            if (x + 1 == two && e + B >= G) warp_arrive(&bar.s_free);
+                        }
+                        // (pairs as they lie: put together from single values they cost moves)
+                        const uint64_t f = *reinterpret_cast<const uint64_t*>(&factor_s[warp][x][8 * e + pair2]);
+                        const uint64_t up = *reinterpret_cast<const uint64_t*>(&offset_s[warp][x][8 * e + pair2]);
+                        uint64_t p[4];
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const float* y = &s[S::kTwice ? 0 : x][e % B][2 * c];
+                            const float2 z = unpair(fma2(pair(y[0], y[1]), f, up));
+                            const float p0 = tree_exp2(z.x), p1 = tree_exp2(z.y);
+                            p[c] = pair(p0, p1);
+                            tree_split(p0, p1, hi[c], lo[c]);
+                        }
+                        const uint64_t sum = add2(add2(p[0], p[1]), add2(p[2], p[3]));
+                        if (x == 0) l[e] = fma2(l[e], *reinterpret_cast<const uint64_t*>(&alpha_s[buf][warp][8 * e + pair2]), 0);
+                        l[e] = fma2(sum, iv2, l[e]);
+                        st_matrix_turned(to + 1024 * PARTS * e, hi[0], hi[1], hi[2], hi[3]);
+                        st_matrix_turned(to + 1024 * PARTS * e + S::kPart, lo[0], lo[1], lo[2], lo[3]);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.p_full[x % S::kWeights]);
+                }
+                freed += two;
+                n += two;
                 end_row = -1;
-                if (++kc == chunk || k + 1 == t.tiles) {  // the chunk's last tile
+                kc += two;
+                if (kc == chunk || k + 2 >= t.tiles) {  // the chunk's last step
                     end_row = pr;
                     end_left = R;
 #pragma unroll
@@ -1059,7 +1105,7 @@ cudaError_t launch_q8kv_attention(const float* q, const Q8Batch& b, int Hq, int 
         units += (int64_t)v.n_chunk * Hkv;
         n_part += (int64_t)v.n_chunk * v.n_nodes * Hq;
         if (v.n_chunk == 0) continue;
-        runs = runs && v.chunk == 1;
+        runs = runs && v.chunk == 2;
         rows = std::max(rows, v.n_nodes * (Hq / Hkv));
     }
     float* part_o = (float*)part;

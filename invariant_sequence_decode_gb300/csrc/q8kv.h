@@ -51,6 +51,7 @@ struct Q8Batch {
     TreeRow row[kMaxTree];
     int32_t n_view;
     int32_t n_row;
+    uint8_t order[4];  // the views, those with the longest chunks first
 };
 
 // Cuts the views' tiles into chunks; returns the rows of partial results.
