@@ -106,9 +106,9 @@ constexpr int kQ8ScaleSlots = 16;  // tiles whose scales are held: more than lie
 __device__ unsigned int g_q8kv_wait_timeouts;
 
 // Sizes of a kernel for up to 16 NG rows of a KV head.  4 PARTS warps form scores into
-// weights and add up sums, each with 32 keys and a PARTS-th of the rows; four turn
-// codes into f16, and of the last four one feeds the tiles, two issue the products and
-// one prepares the next head's q.
+// weights and add up sums, each with 32 keys and a PARTS-th of the rows; four turn K's
+// codes into f16 and four V's, and of the last four one feeds the tiles, two issue the
+// products and one prepares the next head's q.
 template <int NG, int PARTS>
 struct Q8Shape {
     static constexpr int kRows = 16 * NG;                      // columns of the products
@@ -116,22 +116,20 @@ struct Q8Shape {
     static constexpr int kGroups = 2 * NG / PARTS;             // of eight columns, of a part
     static constexpr int kCols = 8 * kGroups;
     static constexpr int kWarps = 4 * PARTS;
-    static constexpr int kThreads = 32 * (kWarps + 8);
+    static constexpr int kThreads = 32 * (kWarps + 12);
     static constexpr int kCtas = PARTS == 1 ? 2 : 1;           // of a multiprocessor
-    // registers of a thread on weights, and of the others: 30,720 of a CTA launched with
-    // 80 each, 65,536 with 128
-    static constexpr int kRegs = PARTS == 1 ? 144 : 200, kOther = PARTS == 1 ? 48 : 56;
-    static constexpr int kSlots = NG == 1 ? 4 : NG == 2 ? 3 : NG == 3 ? 7 : NG == 6 ? 4 : 5;  // tiles of K or V in flight
+    // registers of a thread on weights; 32 of a turning one, 48 of the last four warps':
+    // 32,768 of a CTA launched with 64 each, 61,440 with 96
+    static constexpr int kRegs = PARTS == 1 ? 144 : 184;
+    static constexpr int kSlotsK = NG == 3 ? 4 : NG == 4 || NG == 5 || NG == 8 ? 3 : 2;  // tiles in flight
+    static constexpr int kSlotsV = NG == 3 ? 3 : NG == 2 ? 1 : 2;
+    static constexpr int kSlots = kSlotsK + kSlotsV;
     // In tensor memory: one tile of K, which is multiplied as soon as it is there, the
     // scores of a step's two, and its V, which waits for their weights
     static constexpr int kTurnedV = NG == 2 || NG == 8 ? 1 : 2;
     static constexpr int kWeights = NG == 8 ? 1 : 2;           // tiles of weights in shared memory
     static constexpr int kHeads = NG == 1 || NG == 3 || NG == 4 ? 2 : 1;  // heads of q in shared memory
     static constexpr bool kTwice = NG == 2 || NG >= 5;                    // scores are read twice, not held while maxima are found
-    // The next step's K is turned ahead of a step's V, so that its scores come early.
-    // (Not where the second tile's weights wait for the first's product: scores would wait
-    // for V, V behind K for scores.)
-    static constexpr bool kKeysFirst = kWeights == 2;
     static constexpr int kPart = kRows * kHeadDim * 2;         // bytes of one part of q, or of the weights
     static constexpr uint32_t kColK = 0, kColV = 64, kColS = kColV + 64 * kTurnedV, kColO = kColS + 2 * kRows;
     static constexpr uint32_t kTmem = 512 / kCtas;
@@ -145,7 +143,8 @@ struct Q8Maps {
 
 template <typename S>
 struct Q8Bars {
-    uint64_t full[S::kSlots], empty[S::kSlots];          // a tile of K or V is there; has been turned
+    uint64_t k_full[S::kSlotsK], k_empty[S::kSlotsK];    // a tile of K is there; has been turned
+    uint64_t v_full[S::kSlotsV], v_empty[S::kSlotsV];
     uint64_t ka_full, ka_free;                           // K of a tile is f16 in tensor memory; has been multiplied
     uint64_t va_full[S::kTurnedV], va_free[S::kTurnedV];
     uint64_t s_full, s_free;                             // S of a step is complete; has been read
@@ -231,131 +230,153 @@ __device__ __forceinline__ void q8_half_codes(uint32_t w, uint32_t& lo, uint32_t
 // A step's tiles: two, or one at a run's end.
 __device__ __forceinline__ int q8_step_tiles(const Q8Run& t, int k) { return min(2, t.tiles - k); }
 
-// The producer: tiles and scales of the CTA's runs, in the order in which they are
-// turned.  Returns the tiles of K and V issued.
-template <typename S>
-__device__ int q8_produce(const Q8Maps& maps, const Q8Batch& b, int Hkv, const Q8Share& w, uint8_t* tiles, float (*scales)[8],
-                          Q8Bars<S>& bar)
-{
-    unsigned int* late = &g_q8kv_wait_timeouts;
-    int i = 0, n = 0;  // tiles of K and V, tiles
-    int view = -1, g = 0, page[2] = {}, values = 0;  // the last step's, whose V is still to come
-    // scales (nullable): come with the tile; the weights' warps read them behind S, which
-    // the turning warps' wait for this tile has come before
-    auto load = [&](const CUtensorMap* m, int head, int p, const float* sc, float* to) {
-        const int st = i % S::kSlots;
-        if (!mbar_wait(&bar.empty[st], ((i / S::kSlots) & 1) ^ 1, late)) return false;
-        mbar_expect_tx(&bar.full[st], kQ8PageBytes + (sc ? 32 : 0));
-        if (sc)
-            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], 32, [%2];" ::"r"(smem_addr(to)),
-                         "l"(sc), "r"(smem_addr(&bar.full[st]))
-                         : "memory");
-        tma_load_4d(tiles + st * kQ8PageBytes, m, 0, 0, head, p, &bar.full[st]);
-        ++i;
+// A place in the CTA's tiles; the tile's page is on its way when its turn comes.
+struct Q8Cursor {
+    int u, round, tile, tiles, view, g, page;
+
+    __device__ __forceinline__ void enter(const Q8Batch& b, int Hkv, const Q8Share& w)
+    {
+        const Q8Run t = q8_run(b, Hkv, u, w.step ? u + 1 : w.u1);
+        u = !w.step ? u + t.chunks : round & 1 ? (round + 1) * w.step - 1 - w.u0 : round * w.step + w.u0;
+        ++round;
+        tile = t.t0;
+        tiles = t.tiles;
+        view = t.view;
+        g = t.g;
+    }
+    __device__ __forceinline__ void fetch(const Q8Batch& b)
+    {
+        const Q8View& v = b.view[view];
+        const int span = q8_tile_key(v, tile) / kQ8Page;
+        page = v.table ? ld_placed_i(v.table + span) : span;
+    }
+    __device__ __forceinline__ bool start(const Q8Batch& b, int Hkv, const Q8Share& w)
+    {
+        u = w.u0;
+        round = 1;
+        tiles = 0;
+        if (u >= w.u1) return false;
+        enter(b, Hkv, w);
+        fetch(b);
         return true;
-    };
-    auto load_values = [&] {
-        for (int x = 0; x < values; ++x)
-            if (!load(&maps.v[view], g, page[x], nullptr, nullptr)) return false;
-        values = 0;
-        return true;
-    };
-    pdl_wait();
-    pdl_trigger();
-    bool ok = true;
-    q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
-        const Q8View& v = b.view[t.view];
-        auto page_of = [&](int k) {
-            const int span = q8_tile_key(v, t.t0 + k) / kQ8Page;
-            return v.table ? ld_placed_i(v.table + span) : span;
-        };
-        int next[2] = {page_of(0), t.tiles > 1 ? page_of(1) : 0};
-        for (int k = 0; k < t.tiles; k += 2) {
-            int now[2] = {next[0], next[1]};
-            for (int x = 0; x < 2; ++x)
-                if (k + 2 + x < t.tiles) next[x] = page_of(k + 2 + x);  // (on their way while this step's places become free)
-            const int two = q8_step_tiles(t, k);
-            for (int x = 0; x < two; ++x, ++n) {
-                const bool in = now[x] >= 0 && now[x] < v.n_pages;
-                if (!in) now[x] = v.n_pages;             // outside the map: zeros
-                float* to = scales[n % kQ8ScaleSlots];
-                if (!in)
-                    for (int e = 0; e < 8; ++e) to[e] = 0.0f;
-                const float* sc = in ? v.scales + now[x] * v.scale_stride + t.g * kQ8PageScales : nullptr;
-                if (!(ok = load(&maps.k[t.view], t.g, now[x], sc, to))) return false;
-            }
-            if (S::kKeysFirst && !(ok = load_values())) return false;
-            view = t.view;
-            g = t.g;
-            page[0] = now[0];
-            page[1] = now[1];
-            values = two;
-            if (!S::kKeysFirst && !(ok = load_values())) return false;
+    }
+    __device__ __forceinline__ bool next(const Q8Batch& b, int Hkv, const Q8Share& w)
+    {
+        if (--tiles > 0) {
+            ++tile;
+        } else {
+            if (u >= w.u1) return false;
+            enter(b, Hkv, w);
         }
+        fetch(b);
         return true;
-    });
-    if (ok) load_values();
-    return i;
+    }
+};
+
+__device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(done)
+                 : "r"(smem_addr(b)), "r"(parity)
+                 : "memory");
+    return done != 0;
 }
 
-// One operand's codes, [lane's row][128], into tensor memory as f16.
+// The producer: tiles of K (with their scales) and of V, each into the next place of
+// its own ring that is free.  Gives up where no place becomes free for kWaitLimitNs.
+template <typename S>
+__device__ void q8_produce(const Q8Maps& maps, const Q8Batch& b, int Hkv, const Q8Share& w, uint8_t* tiles, float (*scales)[8],
+                           Q8Bars<S>& bar)
+{
+    unsigned int* late = &g_q8kv_wait_timeouts;
+    int nk = 0, nv = 0;
+    pdl_wait();
+    pdl_trigger();
+    Q8Cursor k, v;
+    bool more_k = k.start(b, Hkv, w), more_v = v.start(b, Hkv, w);
+    uint64_t since = global_ns();
+    while (more_k || more_v) {
+        bool moved = false;
+        if (more_k && mbar_test(&bar.k_empty[nk % S::kSlotsK], ((nk / S::kSlotsK) & 1) ^ 1)) {
+            const Q8View& o = b.view[k.view];
+            uint64_t* full = &bar.k_full[nk % S::kSlotsK];
+            float* to = scales[nk % kQ8ScaleSlots];
+            const bool in = k.page >= 0 && k.page < o.n_pages;  // (else outside the map: zeros)
+            // the scales come with the tile; the weights' warps read them behind S, which
+            // the turning warps' wait for this tile has come before
+            if (!in)
+                for (int e = 0; e < 8; ++e) to[e] = 0.0f;
+            mbar_expect_tx(full, kQ8PageBytes + (in ? 32 : 0));
+            if (in)
+                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], 32, [%2];" ::"r"(smem_addr(to)),
+                             "l"(o.scales + k.page * o.scale_stride + k.g * kQ8PageScales), "r"(smem_addr(full))
+                             : "memory");
+            tma_load_4d(tiles + nk % S::kSlotsK * kQ8PageBytes, &maps.k[k.view], 0, 0, k.g, in ? k.page : o.n_pages, full);
+            ++nk;
+            more_k = k.next(b, Hkv, w);
+            moved = true;
+        }
+        if (more_v && mbar_test(&bar.v_empty[nv % S::kSlotsV], ((nv / S::kSlotsV) & 1) ^ 1)) {
+            const Q8View& o = b.view[v.view];
+            uint64_t* full = &bar.v_full[nv % S::kSlotsV];
+            mbar_expect_tx(full, kQ8PageBytes);
+            tma_load_4d(tiles + (S::kSlotsK + nv % S::kSlotsV) * kQ8PageBytes, &maps.v[v.view], 0, 0, v.g,
+                        v.page >= 0 && v.page < o.n_pages ? v.page : o.n_pages, full);
+            ++nv;
+            more_v = v.next(b, Hkv, w);
+            moved = true;
+        }
+        if (moved) {
+            since = global_ns();
+        } else if (global_ns() - since > kWaitLimitNs) {
+            atomicAdd(late, 1u);
+            break;
+        } else {
+            __nanosleep(32);
+        }
+    }
+    ring_drain<S::kSlotsK>(bar.k_full, nk, late);
+    ring_drain<S::kSlotsV>(bar.v_full, nv, late);
+}
+
+// One operand's codes, [lane's row][128], into tensor memory as f16.  (Small pieces:
+// few registers, and code that fits the schedulers' first instruction cache.)
 __device__ __forceinline__ void q8_turn(const uint8_t* tile, int row, uint32_t to)
 {
     const uint8_t* p = tile + row * 128;
 #pragma unroll 1
-    for (int half = 0; half < 2; ++half) {  // (code that fits the schedulers' first instruction cache, here and below)
-        uint32_t o[32];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint4 x = lds128(p + (((4 * half + e) ^ (row & 7)) << 4));
-            q8_half_codes(x.x, o[8 * e], o[8 * e + 1]);
-            q8_half_codes(x.y, o[8 * e + 2], o[8 * e + 3]);
-            q8_half_codes(x.z, o[8 * e + 4], o[8 * e + 5]);
-            q8_half_codes(x.w, o[8 * e + 6], o[8 * e + 7]);
-        }
-        tm_st32(to + 32 * half, o);
+    for (int e = 0; e < 8; e += 2) {
+        const uint4 x = lds128(p + ((e ^ (row & 7)) << 4)), y = lds128(p + (((e + 1) ^ (row & 7)) << 4));
+        uint32_t o[16];
+        q8_half_codes(x.x, o[0], o[1]);
+        q8_half_codes(x.y, o[2], o[3]);
+        q8_half_codes(x.z, o[4], o[5]);
+        q8_half_codes(x.w, o[6], o[7]);
+        q8_half_codes(y.x, o[8], o[9]);
+        q8_half_codes(y.y, o[10], o[11]);
+        q8_half_codes(y.z, o[12], o[13]);
+        q8_half_codes(y.w, o[14], o[15]);
+        tm_st16(to + 8 * e, o);
     }
     tm_wait_st();
 }
 
-// The turning warps: K and V of every tile, a row of 128 codes per thread.
-template <typename S>
-__device__ void q8_turn_tiles(const Q8Batch& b, int Hkv, const Q8Share& w, const uint8_t* tiles, uint32_t tmem, int quad, int lane,
-                              Q8Bars<S>& bar)
+// The turning warps of K, or of V: a row of 128 codes per thread.
+template <int SLOTS, int TURNED>
+__device__ void q8_turn_tiles(int n, const uint8_t* tiles, uint32_t to, int row, uint64_t* full, uint64_t* empty, uint64_t* free, uint64_t* done)
 {
     unsigned int* late = &g_q8kv_wait_timeouts;
-    const int row = 32 * quad + lane;
-    const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
-    int i = 0, nk = 0, nv = 0;  // tiles turned, of K, of V
-    // the next `keys` tiles of K, the next `values` of V, in the order of S::kKeysFirst
-    auto turn = [&](int keys, int values) {
 #pragma unroll 1
-        for (int x = 0; x < keys + values; ++x, ++i) {
-            const bool is_v = x >= keys;
-            const int st = i % S::kSlots, to = is_v ? nv % S::kTurnedV : 0;
-            const uint32_t parity = ((is_v ? nv / S::kTurnedV : nk) & 1) ^ 1;
-            const bool there = mbar_wait(&bar.full[st], (i / S::kSlots) & 1, late) &&
-                               mbar_wait(is_v ? &bar.va_free[to] : &bar.ka_free, parity, late);
-            if (!__all_sync(0xffffffffu, there)) return false;
-            tm_after();
-            q8_turn(tiles + st * kQ8PageBytes, row, lanes + (is_v ? S::kColV + 64 * to : S::kColK));
-            warp_arrive(is_v ? &bar.va_full[to] : &bar.ka_full);
-            if (lane == 0) mbar_arrive(&bar.empty[st]);
-            (is_v ? nv : nk) += 1;
-        }
-        return true;
-    };
-    int values = 0;
-    bool ok = true;
-    q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
-        for (int k = 0; ok && k < t.tiles; k += 2) {
-            const int two = q8_step_tiles(t, k);
-            ok = turn(two, S::kKeysFirst ? values : two);
-            values = two;
-        }
-        return ok;
-    });
-    if (ok && S::kKeysFirst) turn(0, values);
+    for (int i = 0; i < n; ++i) {
+        const int st = i % SLOTS, x = i % TURNED;
+        const bool there = mbar_wait(&full[st], (i / SLOTS) & 1, late) && mbar_wait(&free[x], ((i / TURNED) & 1) ^ 1, late);
+        if (!__all_sync(0xffffffffu, there)) return;
+        tm_after();
+        q8_turn(tiles + st * kQ8PageBytes, row, to + 64 * x);
+        warp_arrive(&done[x]);
+        if ((row & 31) == 0) mbar_arrive(&empty[st]);
+    }
 }
 
 // A product's steps, 128 x kRows x 16 each: A in tensor memory from column a, B rows of
@@ -369,7 +390,7 @@ __device__ __forceinline__ void q8_multiply(uint32_t d, uint32_t a, uint32_t byt
     d = __shfl_sync(0xffffffffu, d, 0);
     a = __shfl_sync(0xffffffffu, a, 0);
     const uint64_t desc = tree_desc(__shfl_sync(0xffffffffu, bytes, 0), 16, 1024);
-#pragma unroll 4
+#pragma unroll
     for (int ks = 0; ks < 16; ++ks)
         tree_mma(d, a + 8 * (ks & 7), desc + ((ks < 8 ? S::kPart : 0) + (ks >> 2 & 1) * (S::kPart / 2)) / 16 + 2 * (ks & 3), idesc,
                  adds || ks > 0, elected);
@@ -546,14 +567,18 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
     __shared__ __align__(8) float alpha_s[2][S::kWarps][S::kCols];
     __shared__ volatile int bail[PARTS][2];               // a wait of the part's warps expired, by step parity
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (warp == S::kWarps + 6) {
+    if (warp == S::kWarps + 10) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_at)), "r"(S::kTmem));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     if (tid == 0) {
-        for (int i = 0; i < S::kSlots; ++i) {
-            mbar_init(&bar.full[i], 1);
-            mbar_init(&bar.empty[i], 4);
+        for (int i = 0; i < S::kSlotsK; ++i) {
+            mbar_init(&bar.k_full[i], 1);
+            mbar_init(&bar.k_empty[i], 4);
+        }
+        for (int i = 0; i < S::kSlotsV; ++i) {
+            mbar_init(&bar.v_full[i], 1);
+            mbar_init(&bar.v_empty[i], 4);
         }
         mbar_init(&bar.ka_full, 4);
         mbar_init(&bar.ka_free, 1);
@@ -591,22 +616,19 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
         w = Q8Share{(int)((int64_t)units * blockIdx.x / gridDim.x), (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x), 0};
     unsigned int* late = &g_q8kv_wait_timeouts;
 
-    if (warp >= S::kWarps + 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kOther));
-        if (warp == S::kWarps + 4 && lane == 0) {
-            const int n = q8_produce(maps, b, Hkv, w, tiles, scales, bar);
-            ring_drain<S::kSlots>(bar.full, n, late);
-        }
-        if (warp > S::kWarps + 4) {
+    if (warp >= S::kWarps + 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if (warp == S::kWarps + 8 && lane == 0) q8_produce(maps, b, Hkv, w, tiles, scales, bar);
+        if (warp > S::kWarps + 8) {
             // the first head's q by all three of these warps, which have nothing else to do
             // before; the others' ahead of time by the last one
-            const int first = (tid - 32 * (S::kWarps + 5)) >> 4;
+            const int first = (tid - 32 * (S::kWarps + 9)) >> 4;
             pdl_wait();
             q8_prepare<S>(q, b, Hq, Hkv, q8_run(b, Hkv, w.u0, w.u0 + 1), scale, qs, unit_s[0], from_s[0], first, 6);
             asm volatile("bar.sync 15, 96;" ::: "memory");
-            if (warp == S::kWarps + 5) q8_scores(b, Hkv, w, smem_addr(qs), tmem, bar);
-            if (warp == S::kWarps + 6) q8_sums(b, Hkv, w, smem_addr(ps), tmem, bar);
-            if (warp == S::kWarps + 7) {
+            if (warp == S::kWarps + 9) q8_scores(b, Hkv, w, smem_addr(qs), tmem, bar);
+            if (warp == S::kWarps + 10) q8_sums(b, Hkv, w, smem_addr(ps), tmem, bar);
+            if (warp == S::kWarps + 11) {
                 int head = -1, last = -1;
                 q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
                     if (t.view * Hkv + t.g == last) return true;
@@ -624,8 +646,19 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
         }
         __syncwarp();
     } else if (warp >= S::kWarps) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kOther));
-        q8_turn_tiles(b, Hkv, w, tiles, tmem, warp & 3, lane, bar);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
+        int n = 0;
+        q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
+            n += t.tiles;
+            return true;
+        });
+        const int row = 32 * (warp & 3) + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        if (warp < S::kWarps + 4)
+            q8_turn_tiles<S::kSlotsK, 1>(n, tiles, lanes + S::kColK, row, bar.k_full, bar.k_empty, &bar.ka_free, &bar.ka_full);
+        else
+            q8_turn_tiles<S::kSlotsV, S::kTurnedV>(n, tiles + S::kSlotsK * kQ8PageBytes, lanes + S::kColV, row, bar.v_full, bar.v_empty,
+                                                   bar.va_free, bar.va_full);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegs));
         // The warp's keys are its block of the tile, 32 quad ..; its columns the groups of
@@ -890,7 +923,7 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
     }
     tm_before();
     __syncthreads();
-    if (warp == S::kWarps + 6) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kTmem));
+    if (warp == S::kWarps + 10) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kTmem));
 }
 
 cudaError_t read_q8kv_wait_timeouts(uint32_t* count, bool reset)
