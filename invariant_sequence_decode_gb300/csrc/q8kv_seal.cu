@@ -9,10 +9,10 @@
 //
 // Bound by memory: 16 KB read and 8 KB written a block.  One CTA of 256 threads
 // a block, all its loads under way at once.  The division would take longer
-// than the bytes (25 instructions a value with it, 9 without): x * (1 / d) is
-// within 2^-22 of the quotient's 32-bit value relatively, 3e-5 in all, so its
-// rounding is the quotient's wherever it lies further than 1e-4 from a half;
-// eight values with one nearer go through the division.
+// than the bytes (25 instructions a value with it, 8 without): x * (1 / d), with a
+// reciprocal within 2^-23 of 1 / d, is within 2^-21 of the quotient's 32-bit value
+// relatively, 7e-5 in all, so its rounding is the quotient's wherever it lies further
+// than 1e-4 from a half; four values with one nearer go through the division.
 #include <algorithm>
 
 #include "cache.h"
@@ -25,49 +25,50 @@ namespace luce {
 constexpr int kSealThreads = 256;
 constexpr int kSealPitch = 33;  // words from key to key of V's codes on their way: the reads of a warp in 32 banks
 
-// The largest finite |x| of eight values.
-__device__ __forceinline__ float seal_top(const uint4& x)
+// 32 bytes, read once.
+__device__ __forceinline__ void seal_load(const __half* p, uint32_t (&v)[8])
 {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "l"(p)
+                 : "memory");
+}
+
+// The largest finite |x| of sixteen values.
+__device__ __forceinline__ float seal_top(const uint32_t (&w)[8])
+{
     uint32_t top = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 8; ++e) {
         const uint32_t lo = w[e] & 0x7fffu, hi = w[e] >> 16 & 0x7fffu;  // (magnitudes order as integers)
-        if (lo < 0x7c00u) top = max(top, lo);
-        if (hi < 0x7c00u) top = max(top, hi);
+        top = max(top, lo < 0x7c00u ? lo : 0u);
+        top = max(top, hi < 0x7c00u ? hi : 0u);
     }
     return __half2float(__ushort_as_half((unsigned short)top));
 }
 
-// Eight values' codes, in order.
-__device__ __forceinline__ uint2 seal_codes(const uint4& x, float d, float inv)
+// Four values' codes, in order.
+__device__ __forceinline__ uint32_t seal_codes(uint32_t a, uint32_t b, float d, float inv)
 {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    float v[8];
-    uint32_t n[8];
-    bool sure = true;
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a)), y = __half22float2(*reinterpret_cast<const __half2*>(&b));
+    const float v[4] = {x.x, x.y, y.x, y.y};
+    uint32_t n[4];
+    float far = 0.0f;  // the furthest from its nearest integer
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
-        v[2 * e] = f.x;
-        v[2 * e + 1] = f.y;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
         const float t = __fmul_rn(v[e], inv), m = __fadd_rn(t, 12582912.0f);  // 1.5 * 2^23: the nearest integer in the low bits
         n[e] = __float_as_uint(m);
-        sure = sure && fabsf(__fsub_rn(t, __fsub_rn(m, 12582912.0f))) < 0.4999f;  // (false for a NaN)
+        const float off = fabsf(__fsub_rn(t, __fsub_rn(m, 12582912.0f)));
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(far) : "f"(off));
     }
-    if (!sure) {
+    if (!(far < 0.4999f)) {  // (or a NaN, which the maximum keeps)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) n[e] = (uint32_t)q8_code(v[e], d);
+        for (int e = 0; e < 4; ++e) n[e] = (uint32_t)q8_code(v[e], d);
     }
-    const uint32_t a = __byte_perm(n[0], n[1], 0x0040), b = __byte_perm(n[2], n[3], 0x0040);
-    const uint32_t c = __byte_perm(n[4], n[5], 0x0040), e = __byte_perm(n[6], n[7], 0x0040);
-    return make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(c, e, 0x5410));
+    return __byte_perm(__byte_perm(n[0], n[1], 0x0040), __byte_perm(n[2], n[3], 0x0040), 0x5410);
 }
 
-__global__ void __launch_bounds__(kSealThreads)
+__global__ void __launch_bounds__(kSealThreads, 8)
 q8kv_seal_kernel(const __grid_constant__ Q8SealBatch b, int64_t heads)
 {
     __shared__ float tops[2][kSealThreads / 32];
@@ -83,27 +84,15 @@ q8kv_seal_kernel(const __grid_constant__ Q8SealBatch b, int64_t heads)
     const int block = s.sealed / kQ8Block + unit, quarter = block & 3;
     pdl_wait();
     const int page = s.table ? ld_placed_i(s.table + (block >> 2)) : block >> 2;
-    // 16 threads a row, 16 bytes each: rows tid / 16 and tid / 16 + 16
-    const int64_t at = ((int64_t)unit * kQ8Block + (tid >> 4)) * kHeadDim + 8 * (tid & 15);
-    uint4 x[2][2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        x[0][e] = ld_placed_cs_u4(k + at + 16 * e * kHeadDim);
-        x[1][e] = ld_placed_cs_u4(v + at + 16 * e * kHeadDim);
-    }
-    // the rows behind the last whole block move to the front, by the first block's CTA
-    const int whole = s.n / kQ8Block * kQ8Block, rest = unit == 0 ? (s.n - whole) * 16 : 0;
-    uint4 y[2][2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-        if (tid + e * kSealThreads < rest) {
-            const int64_t from = (int64_t)whole * kHeadDim + 8 * (tid + e * kSealThreads);
-            y[0][e] = ld_placed_cs_u4(k + from);
-            y[1][e] = ld_placed_cs_u4(v + from);
-        }
+    // eight threads a row, 32 bytes each
+    const int key = tid >> 3, piece = tid & 7;
+    const int64_t at = ((int64_t)unit * kQ8Block + key) * kHeadDim + 16 * piece;
+    uint32_t x[2][8];
+    seal_load(k + at, x[0]);
+    seal_load(v + at, x[1]);
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-        const float top = warp_max(fmaxf(seal_top(x[w][0]), seal_top(x[w][1])));
+        const float top = warp_max(seal_top(x[w]));
         if (lane == 0) tops[w][warp] = top;
     }
     __syncthreads();  // (every row of the block has been read, too)
@@ -114,26 +103,19 @@ q8kv_seal_kernel(const __grid_constant__ Q8SealBatch b, int64_t heads)
 #pragma unroll
         for (int e = 1; e < kSealThreads / 32; ++e) top = fmaxf(top, tops[w][e]);
         d[w] = __fdiv_rn(top, 127.0f);
-        inv[w] = __fdiv_rn(1.0f, d[w]);
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv[w]) : "f"(d[w]));
     }
     const bool in = page >= 0 && page < s.n_pages;
     const int64_t place = (int64_t)page * heads + lh;
     if (in && tid < 2) s.scales[place * kQ8PageScales + 4 * tid + quarter] = d[tid];
+    uint4 kc;
+    kc.x = seal_codes(x[0][0], x[0][1], d[0], inv[0]);
+    kc.y = seal_codes(x[0][2], x[0][3], d[0], inv[0]);
+    kc.z = seal_codes(x[0][4], x[0][5], d[0], inv[0]);
+    kc.w = seal_codes(x[0][6], x[0][7], d[0], inv[0]);
+    if (in) *reinterpret_cast<uint4*>(s.k_codes + place * kQ8PageBytes + (quarter * kQ8Block + key) * kHeadDim + 16 * piece) = kc;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int key = (tid >> 4) + 16 * e;
-        const uint2 kc = seal_codes(x[0][e], d[0], inv[0]), vc = seal_codes(x[1][e], d[1], inv[1]);
-        if (in)
-            *reinterpret_cast<uint2*>(s.k_codes + place * kQ8PageBytes + (quarter * kQ8Block + key) * kHeadDim + 8 * (tid & 15)) = kc;
-        vt[key * kSealPitch + 2 * (tid & 15)] = vc.x;
-        vt[key * kSealPitch + 2 * (tid & 15) + 1] = vc.y;
-    }
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-        if (tid + e * kSealThreads < rest) {
-            *reinterpret_cast<uint4*>(k + 8 * (tid + e * kSealThreads)) = y[0][e];
-            *reinterpret_cast<uint4*>(v + 8 * (tid + e * kSealThreads)) = y[1][e];
-        }
+    for (int e = 0; e < 4; ++e) vt[key * kSealPitch + 4 * piece + e] = seal_codes(x[1][2 * e], x[1][2 * e + 1], d[1], inv[1]);
     __syncthreads();
     // four keys by four dims a thread, turned
     const int kg = tid & 7, dg = tid >> 3;
@@ -148,6 +130,14 @@ q8kv_seal_kernel(const __grid_constant__ Q8SealBatch b, int64_t heads)
         int8_t* to = s.v_codes + place * kQ8PageBytes + 4 * dg * kQ8Page + quarter * kQ8Block + 4 * kg;
 #pragma unroll
         for (int e = 0; e < 4; ++e) *reinterpret_cast<uint32_t*>(to + e * kQ8Page) = o[e];
+    }
+    // the rows behind the last whole block move to the front, by the first block's CTA
+    // (which has read what lay there)
+    const int whole = s.n / kQ8Block * kQ8Block, rest = unit == 0 ? (s.n - whole) * 16 : 0;
+    for (int e = tid; e < rest; e += kSealThreads) {
+        const uint4 a = ld_placed_cs_u4(k + (int64_t)whole * kHeadDim + 8 * e), c = ld_placed_cs_u4(v + (int64_t)whole * kHeadDim + 8 * e);
+        *reinterpret_cast<uint4*>(k + 8 * e) = a;
+        *reinterpret_cast<uint4*>(v + 8 * e) = c;
     }
 }
 
