@@ -147,7 +147,7 @@ struct Q8Bars {
     uint64_t v_full[S::kSlotsV], v_empty[S::kSlotsV];
     uint64_t ka_full, ka_free;                           // K of a tile is f16 in tensor memory; has been multiplied
     uint64_t va_full[S::kTurnedV], va_free[S::kTurnedV];
-    uint64_t s_full, s_free;                             // S of a step is complete; has been read
+    uint64_t s_full, s_free[2];                          // S of a step is complete; its tiles' have been read
     uint64_t p_full[S::kWeights], p_free;                // a tile's weights are in place; have been multiplied (where there is one place)
     uint64_t o_full, o_free;                             // O of a step is complete; has been read
     uint64_t q_full[S::kHeads], q_free[S::kHeads];       // a head's q is in place; has been multiplied, its units read
@@ -405,7 +405,7 @@ __device__ void q8_scores(const Q8Batch& b, int Hkv, const Q8Share& w, uint32_t 
 {
     unsigned int* late = &g_q8kv_wait_timeouts;
     const uint32_t elected = elect_one();
-    int i = 0, n = 0, head = -1, last = -1;  // steps, tiles, heads
+    int n = 0, head = -1, last = -1, used[2] = {0, 0};  // tiles, heads, of the places of scores
     q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
         bool ok = true;
         if (t.view * Hkv + t.g != last) {
@@ -415,15 +415,14 @@ __device__ void q8_scores(const Q8Batch& b, int Hkv, const Q8Share& w, uint32_t 
             ok = __all_sync(0xffffffffu, mbar_wait(&bar.q_full[head % S::kHeads], (head / S::kHeads) & 1, late));
         }
         for (int k = 0; ok && k < t.tiles; ++k, ++n) {
-            const bool there = mbar_wait(&bar.ka_full, n & 1, late) && ((k & 1) || mbar_wait(&bar.s_free, (i & 1) ^ 1, late));
+            // (of a tile's two places of scores each has its own uses: a run's last step may have one tile)
+            const bool there = mbar_wait(&bar.ka_full, n & 1, late) && mbar_wait(&bar.s_free[k & 1], ((k & 1 ? used[1] : used[0]) & 1) ^ 1, late);
             if (!(ok = __all_sync(0xffffffffu, there))) break;  // (the warp leaves as one)
+            (k & 1 ? used[1] : used[0]) += 1;
             tm_after();
             q8_multiply<S>(tmem + S::kColS + S::kRows * (k & 1), tmem + S::kColK, q + head % S::kHeads * 2 * S::kPart, false, elected);
             tree_commit_mma(&bar.ka_free, elected);
-            if ((k & 1) || k + 1 == t.tiles) {
-                tree_commit_mma(&bar.s_full, elected);
-                ++i;
-            }
+            if ((k & 1) || k + 1 == t.tiles) tree_commit_mma(&bar.s_full, elected);
         }
         return ok;
     });
@@ -587,7 +586,8 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
             mbar_init(&bar.va_free[i], 1);
         }
         mbar_init(&bar.s_full, 1);
-        mbar_init(&bar.s_free, S::kWarps);
+        mbar_init(&bar.s_free[0], S::kWarps);
+        mbar_init(&bar.s_free[1], S::kWarps);
         mbar_init(&bar.p_free, 1);
         for (int i = 0; i < PARTS; ++i) bail[i][0] = bail[i][1] = 0;
         for (int i = 0; i < S::kWeights; ++i) mbar_init(&bar.p_full[i], S::kWarps);
@@ -842,7 +842,10 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                         best[e] = x ? fmaxf(best[e], y) : y;
                     }
                 }
-                if (!S::kTwice) warp_arrive(&bar.s_free);
+                if (!S::kTwice) {
+                    warp_arrive(&bar.s_free[0]);
+                    if (two == 2 && lane == 0) mbar_arrive(&bar.s_free[1]);
+                }
 #pragma unroll
                 for (int e = 0; e < kMine; ++e) mx[buf][part][quad][col[e]] = best[e];
                 // all four warps of a part meet here, an expired wait or not, and leave together
@@ -877,7 +880,7 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                     for (int e = 0; e < G; ++e) {
                         if (S::kTwice && e % B == 0) {
                             load_s(x, e);
-                            if (x + 1 == two && e + B >= G) warp_arrive(&bar.s_free);
+                            if (e + B >= G) warp_arrive(&bar.s_free[x]);
                         }
                         // (pairs as they lie: put together from single values they cost moves)
                         const uint64_t f = *reinterpret_cast<const uint64_t*>(&factor_s[warp][x][8 * e + pair2]);
@@ -976,81 +979,74 @@ static cudaError_t launch_chunks(const Q8Maps& maps, const float* q, const Q8Bat
 // ---------------------------------------------------------------- merge
 
 // Merge of one (row, query head): the chunks' results, the tail's keys and the
-// path's.  One CTA of 4 warps.  Scores of the f16 keys: eight lanes a key, 16 dims
-// each, key 16 i + 4 warp + lane / 8 in step i.  Sums: four dims a lane, warp w takes
+// path's.  One CTA of 4 warps.  Scores of the f16 keys: 16 lanes a key, eight dims
+// each, key 8 i + 2 warp + lane / 16 in step i.  Sums: four dims a lane, warp w takes
 // chunks w, w + 4, .. in order, then f16 keys w, w + 4, .. in order; the four are added
 // in order.  Bound by latency: K and V of the first 48 f16 keys (a tail that is
-// sealed at every step and the longest path), statistics and chunk sums are all
-// asked for before anything is used.
-constexpr int kQ8Ahead = 8;       // chunk sums in flight per warp
-constexpr int kQ8Keys = 48;       // f16 keys in flight
+// sealed at every step and the longest path), statistics and the first 20 chunks' sums
+// are all asked for before anything is used.  (Of 640 CTAs, 16 nodes of 40 heads, five
+// fit a multiprocessor.  With 8 warps 160 of them take 1 us less and 640 1 us more;
+// one order of summation serves both, as a row's bits do not depend on the others.)
+constexpr int kQ8MergeWarps = 4, kQ8MergeThreads = 32 * kQ8MergeWarps;
+constexpr int kQ8Ahead = 5;  // chunk sums in flight per warp
+constexpr int kQ8Keys = 48;  // f16 keys in flight
 constexpr int kQ8MaxKeys = kQ8MaxTail + kMaxTree;
 
-__global__ void __launch_bounds__(kHeadDim)
+__global__ void __launch_bounds__(kQ8MergeThreads, 5)
 q8kv_merge_kernel(const float* q, const __grid_constant__ Q8Batch b, int Hq, int Hkv, Q8Scale scale, const float* part_o,
                   const float* part_ml, float* __restrict__ out, int8_t* __restrict__ out_q, float* __restrict__ out_d)
 {
-    __shared__ float ps[kQ8MaxKeys];          // the f16 keys' products
-    __shared__ float4 os[4][kHeadDim / 4];    // the warps' sums
+    __shared__ float ps[kQ8MaxKeys];                    // the f16 keys' products
+    __shared__ float ms[kQ8MaxChunks], ls[kQ8MaxChunks];  // the chunks' maxima and sums
+    __shared__ float4 os[kQ8MergeWarps][kHeadDim / 4];  // the warps' sums
     pdl_trigger();
     const int h = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const TreeRow& row = b.row[r];
     const Q8View& v = b.view[row.view];
-    const int GQ = Hq / Hkv, g = h / GQ, R = v.n_nodes * GQ, nch = v.n_chunk, n = v.tail + row.n_path, total = v.sealed + v.tail;
+    const int GQ = Hq / Hkv, g = h / GQ, R = v.n_nodes * GQ, nch = v.n_chunk, tail = v.tail, n = tail + row.n_path;
     const int64_t pr0 = v.part0 + (int64_t)g * R + row.node * GQ + h % GQ, pstep = (int64_t)Hkv * R;
     const size_t rh = (size_t)r * Hq + h;
-    const int pos = total + row.n_path - 1;
-    // f16 key a: the tail's, then the path's; its row in the tail
-    auto place = [&](int a) { return a < v.tail ? a : v.tail + row.path[a - v.tail]; };
-    auto seen = [&](int a) { return a < n && (v.window == 0 || v.sealed + a < v.sinks || pos - (v.sealed + a) < v.window); };
+    // f16 key a: the tail's, then the path's.  It is seen at a position below `sinks` or from `from` on
+    const int sinks = v.window ? max(0, v.sinks - v.sealed) : n, from = v.window ? n - v.window : 0;
+    const __half *kb = v.k + g * v.head_stride, *vb = v.v + g * v.head_stride;
+    const int64_t tok = v.tok_stride;
+    auto place = [&](int a) { return (int64_t)(a < tail ? a : tail + row.path[a - tail]) * tok; };
+    auto seen = [&](int a) { return a < n && (a < sinks || a >= from); };
     pdl_wait();
-    const int part = lane & 7;
-    float4 qv[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) qv[e] = ld_placed_f4(q + rh * kHeadDim + 16 * part + 4 * e);
-    uint4 kx[kQ8Keys / 16][2];
-    uint2 vx[kQ8Keys / 4];
+    const int part = lane & 15;
+    const float4 q0 = ld_placed_f4(q + rh * kHeadDim + 8 * part), q1 = ld_placed_f4(q + rh * kHeadDim + 8 * part + 4);
+    constexpr int kK = kQ8Keys / (2 * kQ8MergeWarps), kV = kQ8Keys / kQ8MergeWarps;
+    uint4 kx[kK];
+    uint2 vx[kV];
     auto load_k = [&](int base) {
 #pragma unroll
-        for (int i = 0; i < kQ8Keys / 16; ++i) {
-            const int a = base + 16 * i + 4 * warp + (lane >> 3);
-            kx[i][0] = kx[i][1] = make_uint4(0, 0, 0, 0);
-            if (seen(a)) {
-                const __half* p = v.k + g * v.head_stride + place(a) * v.tok_stride + 16 * part;
-                kx[i][0] = ld_placed_u4(p);
-                kx[i][1] = ld_placed_u4(p + 8);
-            }
+        for (int i = 0; i < kK; ++i) {
+            const int a = base + 2 * kQ8MergeWarps * i + 2 * warp + (lane >> 4);
+            kx[i] = make_uint4(0, 0, 0, 0);
+            if (seen(a)) kx[i] = ld_placed_u4(kb + place(a) + 8 * part);
         }
     };
     auto load_v = [&](int base) {
 #pragma unroll
-        for (int i = 0; i < kQ8Keys / 4; ++i) {
-            const int a = base + 4 * i + warp;
+        for (int i = 0; i < kV; ++i) {
+            const int a = base + kQ8MergeWarps * i + warp;
             vx[i] = make_uint2(0, 0);
-            if (seen(a)) vx[i] = ld_placed_u2(v.v + g * v.head_stride + place(a) * v.tok_stride + 4 * lane);
+            if (seen(a)) vx[i] = ld_placed_u2(vb + place(a) + 4 * lane);
         }
     };
     load_k(0);
     load_v(0);
-    constexpr int kStats = kQ8MaxChunks / 32;
-    float w[kStats], ls[kStats], L = 0.0f, M = -INFINITY;  // every warp has all chunks': chunk lane + 32 j in its lane
-#pragma unroll
-    for (int j = 0; j < kStats; ++j) {
-        const int c = lane + 32 * j;
-        w[j] = -INFINITY;
-        ls[j] = 0.0f;
-        if (c < nch) {
-            const float* ml = part_ml + 8 * (pr0 + c * pstep);
-            const float4 x = ld_placed_cg_f4(ml + 4);
-            w[j] = ld_placed_f(ml);
-            ls[j] = __fadd_rn(__fadd_rn(x.x, x.y), __fadd_rn(x.z, x.w));
-        }
+    for (int c = tid; c < nch; c += kQ8MergeThreads) {
+        const float* ml = part_ml + 8 * (pr0 + c * pstep);
+        const float4 x = ld_placed_cg_f4(ml + 4);
+        ms[c] = ld_placed_f(ml);
+        ls[c] = __fadd_rn(__fadd_rn(x.x, x.y), __fadd_rn(x.z, x.w));
     }
     float4 ov[kQ8Ahead];
     auto load_o = [&](int j) {
 #pragma unroll
         for (int e = 0; e < kQ8Ahead; ++e) {
-            const int c = 4 * (j + e) + warp;
+            const int c = kQ8MergeWarps * (j + e) + warp;
             if (c < nch) ov[e] = ld_placed_cg_f4(part_o + (pr0 + c * pstep) * kHeadDim + 4 * lane);
         }
     };
@@ -1058,65 +1054,46 @@ q8kv_merge_kernel(const float* q, const __grid_constant__ Q8Batch b, int Hq, int
     for (int base = 0; base < n; base += kQ8Keys) {
         if (base > 0) load_k(base);
 #pragma unroll
-        for (int i = 0; i < kQ8Keys / 16; ++i) {
-            const int a = base + 16 * i + 4 * warp + (lane >> 3);
-            float dot = 0.0f;
+        for (int i = 0; i < kK; ++i) {
+            const int a = base + 2 * kQ8MergeWarps * i + 2 * warp + (lane >> 4);
+            const float4 k0 = half4(make_uint2(kx[i].x, kx[i].y)), k1 = half4(make_uint2(kx[i].z, kx[i].w));
+            float dot = __fmaf_rn(q0.w, k0.w, __fmaf_rn(q0.z, k0.z, __fmaf_rn(q0.y, k0.y, __fmul_rn(q0.x, k0.x))));
+            dot = __fmaf_rn(q1.w, k1.w, __fmaf_rn(q1.z, k1.z, __fmaf_rn(q1.y, k1.y, __fmaf_rn(q1.x, k1.x, dot))));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint4 x = kx[i][e >> 1];
-                const float4 k = half4(e & 1 ? make_uint2(x.z, x.w) : make_uint2(x.x, x.y));
-                dot = __fmaf_rn(qv[e].w, k.w, __fmaf_rn(qv[e].z, k.z, __fmaf_rn(qv[e].y, k.y, __fmaf_rn(qv[e].x, k.x, dot))));
-            }
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) dot = __fadd_rn(dot, __shfl_xor_sync(0xffffffffu, dot, o));
+            for (int o = 1; o < 16; o <<= 1) dot = __fadd_rn(dot, __shfl_xor_sync(0xffffffffu, dot, o));
             if (part == 0 && a < n) ps[a] = seen(a) ? __fmul_rn(__fmul_rn(dot, scale.sign), scale.log2) : -INFINITY;
         }
     }
     __syncthreads();
-    constexpr int kKeyStats = kQ8MaxKeys / 32;
-    float p[kKeyStats];  // key lane + 32 j
-#pragma unroll
-    for (int j = 0; j < kKeyStats; ++j) {
-        p[j] = lane + 32 * j < n ? ps[lane + 32 * j] : -INFINITY;
-        M = fmaxf(M, p[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < kStats; ++j) M = fmaxf(M, w[j]);
+    // every warp for itself: the largest of all, and the weights' sum
+    float M = -INFINITY, L = 0.0f;
+    for (int c = lane; c < nch; c += 32) M = fmaxf(M, ms[c]);
+    for (int a = lane; a < n; a += 32) M = fmaxf(M, ps[a]);
     M = warp_max(M);  // (a row sees itself: there is one)
-#pragma unroll
-    for (int j = 0; j < kStats; ++j) {
-        w[j] = __fmul_rn(tree_exp2(__fsub_rn(w[j], M)), kQ8Down);
-        L = __fmaf_rn(ls[j], w[j], L);
-    }
-#pragma unroll
-    for (int j = 0; j < kKeyStats; ++j) {
-        p[j] = tree_exp2(__fsub_rn(p[j], M));
-        L = __fadd_rn(L, p[j]);
-    }
+    for (int c = lane; c < nch; c += 32) L = __fmaf_rn(ls[c], __fmul_rn(tree_exp2(__fsub_rn(ms[c], M)), kQ8Down), L);
+    for (int a = lane; a < n; a += 32) L = __fadd_rn(L, tree_exp2(__fsub_rn(ps[a], M)));
     L = warp_sum_butterfly(L);
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int j = 0; kQ8MergeWarps * j < nch; j += kQ8Ahead) {
+        if (j > 0) load_o(j);
 #pragma unroll
-    for (int j = 0; j < kQ8MaxChunks / 4; ++j) {  // chunk 4 j + warp: its weight is in lane (4 j + warp) & 31's w[j >> 3]
-        const int c = 4 * j + warp;
-        if ((j & (kQ8Ahead - 1)) == 0 && j > 0) {
-            if (4 * j >= nch) break;
-            load_o(j);
+        for (int e = 0; e < kQ8Ahead; ++e) {
+            const int c = kQ8MergeWarps * (j + e) + warp;
+            if (c < nch) axpy4(o, ov[e], __fmul_rn(tree_exp2(__fsub_rn(ms[c], M)), kQ8Down));
         }
-        const float f = __shfl_sync(0xffffffffu, w[j >> 3], c & 31);
-        if (c < nch) axpy4(o, ov[j & (kQ8Ahead - 1)], f);
     }
     for (int base = 0; base < n; base += kQ8Keys) {
         if (base > 0) load_v(base);
 #pragma unroll
-        for (int i = 0; i < kQ8Keys / 4; ++i) {
-            const int a = base + 4 * i + warp;  // (its weight: recomputed from ps, the same in every lane)
+        for (int i = 0; i < kV; ++i) {
+            const int a = base + kQ8MergeWarps * i + warp;
             if (a < n) axpy4(o, half4(vx[i]), tree_exp2(__fsub_rn(ps[a], M)));
         }
     }
     os[warp][lane] = o;
     __syncthreads();
-    const float* of = &os[0][0].x;
-    const float O = __fadd_rn(__fadd_rn(of[tid], of[kHeadDim + tid]), __fadd_rn(of[2 * kHeadDim + tid], of[3 * kHeadDim + tid]));
+    const float* of = &os[0][0].x + tid;
+    const float O = __fadd_rn(__fadd_rn(of[0], of[kHeadDim]), __fadd_rn(of[2 * kHeadDim], of[3 * kHeadDim]));
     const float val = __fdiv_rn(O, L);
     out[rh * kHeadDim + tid] = val;
     if (out_q) {
@@ -1153,7 +1130,7 @@ cudaError_t launch_q8kv_attention(const float* q, const Q8Batch& b, int Hq, int 
         const cudaError_t e = launch(maps, q, b, Hq, Hkv, units, runs, sc, part_o, part_ml, s);
         if (e != cudaSuccess) return e;
     }
-    const cudaError_t e = launch_pdl(q8kv_merge_kernel, dim3(Hq, b.n_row), dim3(kHeadDim), s, q, b, Hq, Hkv, sc,
+    const cudaError_t e = launch_pdl(q8kv_merge_kernel, dim3(Hq, b.n_row), dim3(kQ8MergeThreads), s, q, b, Hq, Hkv, sc,
                                      (const float*)part_o, (const float*)part_ml, out, out_q, out_d);
     if (e != cudaSuccess) return e;
     count_launches(1);
