@@ -14,6 +14,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "cache.h"
 #include "common.cuh"
@@ -769,8 +770,12 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
             const int* froms = from_s[head % S::kHeads][part];
             int64_t pr = v.part0 + ((int64_t)t.c * Hkv + t.g) * R;  // the chunk's rows of results
             int kc = 0;                                              // the chunk's tiles so far
-            for (int k = 0; k < t.tiles; k += 2, ++i) {
-                const int two = q8_step_tiles(t, k), buf = i & 1;
+            auto key_of = [&](int k) { return (tile0 + k + (tile0 + k < front ? 0 : skip)) * kQ8Page; };
+            // A step from tile k on.  `masked`: some row's window begins in it or behind it
+            // (code of its own: the scores it overwrites cost the others moves).
+            auto step = [&](auto with_mask, int k, int two) {
+                constexpr bool masked = decltype(with_mask)::value;
+                const int buf = i & 1;
                 if (kc == 0) {
 #pragma unroll
                     for (int e = 0; e < G; ++e) l[e] = 0;
@@ -785,19 +790,14 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                 float s[S::kTwice ? 1 : 2][B][8], factor[2][kMine], lv[2], iv[2], best[kMine];
                 auto load_s = [&](int x, int e0) {
                     float(*to)[8] = s[S::kTwice ? 0 : x];
-                    const int key0 = (tile0 + k + x + (tile0 + k + x < front ? 0 : skip)) * kQ8Page;
+                    [[maybe_unused]] const int key0 = key_of(k + x);
 #pragma unroll
                     for (int e = 0; e < B; ++e) {
                         tm_ld_frag(lanes + S::kColS + S::kRows * x + 8 * PARTS * (e0 + e), to[e]);
                         tm_ld_frag(lanes + (16u << 16) + S::kColS + S::kRows * x + 8 * PARTS * (e0 + e), to[e] + 4);
                     }
                     tm_loaded<8 * B>(&to[0][0]);
-                    if (__builtin_expect(x >= two || key0 + kQ8Block * quad >= sealed, 0)) {
-#pragma unroll
-                        for (int e = 0; e < B; ++e)
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) to[e][c] = -INFINITY;
-                    } else if (__builtin_expect(key0 < edge && key0 + kQ8Page > sinks, 0)) {
+                    if (masked) {
 #pragma unroll
                         for (int e = 0; e < B; ++e) {
                             const int2 key1 = *reinterpret_cast<const int2*>(&froms[8 * (e0 + e) + pair2]);
@@ -812,14 +812,14 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const float* sc = scales[(n + x) % kQ8ScaleSlots];
-                    const int key0 = (tile0 + k + x + (tile0 + k + x < front ? 0 : skip)) * kQ8Page;
-                    const bool valid = x < two && key0 + kQ8Block * quad < sealed;
+                    const bool valid = x < two && key_of(k + x) + kQ8Block * quad < sealed;
                     const float ks = valid ? sc[quad] : 0.0f;
                     // V's scale goes into the weights as a power of two: 2^(s + log2 vs - m) is
                     // what multiplies a code, and over vs the weight itself.  (A block of zeros
                     // weighs as one of the smallest scale, 2^-31.)
                     const float vs = fmaxf(valid ? sc[4 + quad] : 0.0f, 4.656612873e-10f);
                     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lv[x]) : "f"(vs));
+                    if (!valid) lv[x] = -INFINITY;  // (whatever its scores are)
                     iv[x] = __frcp_rn(vs);
                     float top[2 * G];
 #pragma unroll
@@ -853,7 +853,7 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                 part_sync();
                 if (bail[part][buf]) {
                     gone = true;
-                    return false;
+                    return;
                 }
 #pragma unroll
                 for (int e = 0; e < kMine; ++e) {
@@ -919,7 +919,17 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                     kc = 0;
                     pr += (int64_t)Hkv * R;
                 }
+            };
+            for (int k = 0; k < t.tiles && !gone; k += 2, ++i) {
+                const int two = q8_step_tiles(t, k);
+                bool masked = false;
+                for (int x = 0; x < two; ++x) masked = masked || (key_of(k + x) < edge && key_of(k + x) + kQ8Page > sinks);
+                if (masked)
+                    step(std::true_type{}, k, two);
+                else
+                    step(std::false_type{}, k, two);
             }
+            if (gone) return false;
             return true;
         });
         if (!gone && i > 0) take(i - 1);
