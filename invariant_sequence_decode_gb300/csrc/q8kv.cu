@@ -341,14 +341,21 @@ __device__ void q8_produce(const Q8Maps& maps, const Q8Batch& b, int Hkv, const 
     ring_drain<S::kSlotsV>(bar.v_full, nv, late);
 }
 
-// One operand's codes, [lane's row][128], into tensor memory as f16.  (Small pieces:
-// few registers, and code that fits the schedulers' first instruction cache.)
-__device__ __forceinline__ void q8_turn(const uint8_t* tile, int row, uint32_t to)
+__device__ __forceinline__ uint4 lds128_at(uint32_t addr)
 {
-    const uint8_t* p = tile + row * 128;
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+
+// One operand's codes, [lane's row][128], into tensor memory as f16, from the row's
+// first piece of 16 in the tile's swizzle.  (Small pieces: few registers, and code
+// that fits the schedulers' first instruction cache.)
+__device__ __forceinline__ void q8_turn(uint32_t from, uint32_t to)
+{
 #pragma unroll 1
     for (int e = 0; e < 8; e += 2) {
-        const uint4 x = lds128(p + ((e ^ (row & 7)) << 4)), y = lds128(p + (((e + 1) ^ (row & 7)) << 4));
+        const uint4 x = lds128_at(from ^ (e << 4)), y = lds128_at(from ^ ((e + 1) << 4));
         uint32_t o[16];
         q8_half_codes(x.x, o[0], o[1]);
         q8_half_codes(x.y, o[2], o[3]);
@@ -368,15 +375,25 @@ template <int SLOTS, int TURNED>
 __device__ void q8_turn_tiles(int n, const uint8_t* tiles, uint32_t to, int row, uint64_t* full, uint64_t* empty, uint64_t* free, uint64_t* done)
 {
     unsigned int* late = &g_q8kv_wait_timeouts;
+    const uint32_t from = smem_addr(tiles) + row * 128 + ((row & 7) << 4);
+    int st = 0, x = 0;
+    uint32_t filled = 0, freed = 1;  // the parities of the places' next uses
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
-        const int st = i % SLOTS, x = i % TURNED;
-        const bool there = mbar_wait(&full[st], (i / SLOTS) & 1, late) && mbar_wait(&free[x], ((i / TURNED) & 1) ^ 1, late);
+        const bool there = mbar_wait(&full[st], filled, late) && mbar_wait(&free[x], freed, late);
         if (!__all_sync(0xffffffffu, there)) return;
         tm_after();
-        q8_turn(tiles + st * kQ8PageBytes, row, to + 64 * x);
+        q8_turn(from + st * kQ8PageBytes, to + 64 * x);
         warp_arrive(&done[x]);
         if ((row & 31) == 0) mbar_arrive(&empty[st]);
+        if (++st == SLOTS) {
+            st = 0;
+            filled ^= 1;
+        }
+        if (++x == TURNED) {
+            x = 0;
+            freed ^= 1;
+        }
     }
 }
 
