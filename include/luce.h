@@ -786,7 +786,7 @@ int luce_kv_evict_paged(const luce_paged_evict_slot* slots, int n_seq, int n_lay
 #define LUCE_Q8KV_MAX_TAIL 112  /* f16 keys between the blocks and the tree that attention takes */
 
 typedef struct luce_q8kv_slot {
-    uint16_t* k;            /* (device) tail, binary16 [n_layers][Hkv][cap][128], 16-byte aligned */
+    uint16_t* k;            /* (device) tail, binary16 [n_layers][Hkv][cap][128], 32-byte aligned */
     uint16_t* v;            /* (device) same layout */
     int32_t len;            /* rows of the tail */
     int32_t cap;
@@ -853,8 +853,8 @@ typedef struct luce_q8kv_view {
  *   ws  (device) luce_q8kv_attn_workspace_size(...) bytes, 256-byte aligned (no
  *       initial contents); calls that can overlap on the GPU need scratches of
  *       their own
- * q, scales and the tail's rows that a node sees must be finite; what lies where no
- * row sees it is not used, whatever it is.  Sizes as luce_tree_attn, sealed + len
+ * q, scales and the tail's rows that a node sees must be finite, scales not negative;
+ * what lies where no row sees it is not used, whatever it is.  Sizes as luce_tree_attn, sealed + len
  * + n_nodes <= LUCE_MAX_KEYS.  out and ws overlap nothing that the call reads or
  * writes (LUCE_EINVAL), but out may be q itself.
  */

@@ -25,8 +25,8 @@ int luce_qk_norm_rope(const float* qkv, int64_t ld, const luce_seqview* views, i
     REQUIRE(qkv && pos && q && views, LUCE_EINVAL, "%s: null qkv/pos/q/views", who);
     REQUIRE(Hkv >= 1 && Hq >= 1 && Hq <= (1 << 16) && Hkv <= (1 << 16), LUCE_EINVAL, "%s: heads %d/%d", who, Hq, Hkv);
     REQUIRE(D == LUCE_HEAD_DIM, LUCE_EUNSUPPORTED, "%s: head_dim %d (only %d)", who, D, LUCE_HEAD_DIM);
-    REQUIRE(ld >= (int64_t)(Hq + 2 * Hkv) * D && ld % 4 == 0, LUCE_EINVAL,
-            "%s: ld=%lld must be a multiple of 4 that holds %d heads", who, (long long)ld, Hq + 2 * Hkv);
+    REQUIRE(ld >= (int64_t)(Hq + 2 * Hkv) * D && ld % 4 == 0 && ld <= (1 << 28), LUCE_EINVAL,
+            "%s: ld=%lld must be a multiple of 4 that holds %d heads, at most 2^28", who, (long long)ld, Hq + 2 * Hkv);
     REQUIRE(aligned(qkv, 16) && aligned(q, 16) && aligned(q_gamma, 16) && aligned(k_gamma, 16) && aligned(pos, 4), LUCE_EINVAL,
             "%s: qkv, q and the gammas must be 16-byte, pos 4-byte aligned", who);
     REQUIRE(eps >= 0 && isfinite(eps), LUCE_EINVAL, "%s: eps must be finite and >= 0", who);
@@ -103,7 +103,7 @@ int luce_q8kv_seal(const luce_q8kv_slot* slots, int n_seq, int n_layers, int Hkv
     const int64_t heads = (int64_t)n_layers * Hkv;
     for (int s = 0; s < n_seq; ++s) {
         const luce_q8kv_slot& c = slots[s];
-        REQUIRE(c.k && c.v && aligned(c.k, 16) && aligned(c.v, 16), LUCE_EINVAL, "%s: slot %d tail null or not 16-byte aligned", who,
+        REQUIRE(c.k && c.v && aligned(c.k, 32) && aligned(c.v, 32), LUCE_EINVAL, "%s: slot %d tail null or not 32-byte aligned", who,
                 s);
         REQUIRE(c.cap >= 1 && c.len >= 0 && c.len <= c.cap, LUCE_EINVAL, "%s: slot %d len=%d outside [0, cap=%d]", who, s, c.len,
                 c.cap);
@@ -111,7 +111,8 @@ int luce_q8kv_seal(const luce_q8kv_slot* slots, int n_seq, int n_layers, int Hkv
                 c.sealed, LUCE_Q8KV_BLOCK);
         REQUIRE((int64_t)c.sealed + c.len <= LUCE_MAX_KEYS, LUCE_EUNSUPPORTED, "%s: slot %d would hold %lld keys (at most %d)", who, s,
                 (long long)c.sealed + c.len, LUCE_MAX_KEYS);
-        REQUIRE(c.n_pages >= 0, LUCE_EINVAL, "%s: slot %d n_pages=%d", who, s, c.n_pages);
+        REQUIRE(c.n_pages >= 0 && c.n_pages * heads < ((int64_t)1 << 40), LUCE_EINVAL, "%s: slot %d n_pages=%d out of range", who, s,
+                c.n_pages);
         Q8SealSlot& o = b.slot[s];
         o.k = reinterpret_cast<__half*>(c.k);
         o.v = reinterpret_cast<__half*>(c.v);
@@ -196,7 +197,7 @@ int luce_q8kv_attn(const float* q, const luce_q8kv_view* views, int n_seq, int H
     r[nr++] = range_of(ws, (int64_t)need, -1, "workspace", true);
     const int rc = check_apart(r, nr, who);
     if (rc) return rc;
-    return cuda_status(launch_q8kv_attention(q, b, Hq, Hkv, scale, ws, out, nullptr, nullptr, (cudaStream_t)stream), who);
+    return cuda_status(launch_q8kv_attention(q, b, Hq, Hkv, scale, ws, out, (cudaStream_t)stream), who);
 }
 
 int luce::add_q8kv_view(Q8Batch& b, int s, const luce_q8kv_view& v, int Hkv, bool* covered, const char* who)
@@ -236,6 +237,8 @@ int luce::add_q8kv_view(Q8Batch& b, int s, const luce_q8kv_view& v, int Hkv, boo
         const int64_t page = (int64_t)Hkv * kQ8PageBytes;
         REQUIRE(v.page_stride == 0 || (v.page_stride >= page && v.page_stride % kQ8PageBytes == 0 && v.page_stride < ((int64_t)1 << 38)),
                 LUCE_EINVAL, "%s: view %d page_stride must be a multiple of %d and keep the pages apart", who, s, kQ8PageBytes);
+        REQUIRE(v.n_pages <= ((int64_t)1 << 46) / std::max(v.page_stride, page), LUCE_EINVAL, "%s: view %d n_pages=%d out of range", who,
+                s, v.n_pages);
         t.k_codes = v.k_codes;
         t.v_codes = v.v_codes;
         t.scales = v.scales;

@@ -10,6 +10,29 @@
 // into chunks of 128-key tiles; each chunk yields (m, l, sum e^(s - m) v) per row, and
 // the merge adds the chunks in order, then the tail's keys and the path's.  A
 // node's bits follow from its prefix and its path alone.
+//
+// The products.  Codes are whole numbers below 2^8 and so f16 without an error; q and
+// the weights are each two f16 parts, 22 bits, whose products with a code are exact in
+// the tensor cores' f32 sums.  The scales stay out of them: K's multiplies the scores,
+// V's the weights of its 32 keys.  A tree has few rows (8 nodes of 8 heads are 64), so
+// the keys of a tile (for the sums, the dims) are the 128 rows of a product and the
+// tree's rows its columns, 16 to 128 of them: no lane works for a row that is not there.
+// A then is what is turned from 8 bits, and lies in tensor memory: from shared memory a
+// product of 16 columns takes 39 cycles, from there 9, and shared memory would have to
+// hold the turned tile as well.
+//
+// What bounds it.  A tile is 33 KB and 1,430 cycles of an SM's share of the copy rate.
+// Its codes are turned at 4 bytes for 6 instructions: of the 4,700 warp instructions a
+// tile with up to 16 rows costs, 1,900 turn, 400 form weights, 200 issue products.  Warps
+// of a kind share a scheduler with four others and fetch code of their own, and a tile
+// takes 1,700 cycles: long contexts are bound by issue and by instruction fetch, not by
+// memory.  With many rows the weights take over (two 16-bit parts, one exponential and a
+// dozen other instructions each).  Short contexts are bound by the latency of
+// one tile's chain (load, turn, product, weights, product, sums) and of the merge.
+//
+// Measured (HBM reads from memory, L2 flushed): 4 one-token slots of 8 KV heads x 4,096
+// keys @@4x1@@; 4 slots of 4 nodes @@4x4@@; 4 paged one-token slots of 32k to 128k keys @@long@@
+// (197 MB); one slot of 16 nodes x 131k @@16@@; 4 slots of 4 nodes with a window @@win@@.
 #include <limits.h>
 
 #include <algorithm>
@@ -39,11 +62,10 @@ struct Q8Scale {
 };
 
 // Tiles of a chunk for a view of nt tiles, an even number: a step of the kernel takes
-// two.  Of the cuts that fill the kernel's CTAs (kQ8Ctas of them where rows are few, half
-// as many with twice the warps where they are many) 1, 2, 3 or 4 times the cheapest
-// is taken, a chunk costing its steps and about one more (its q, its results).  A
-// function of the tiles and the KV heads alone, so that a row's sums are cut the same
-// way whatever else is in the call.
+// two.  Of the cuts that fill kQ8Ctas CTAs 1, 2, 3 or 4 times the cheapest is taken,
+// a chunk costing its steps and about one more (its q, its results).  A function of the
+// tiles and the KV heads alone, so that a row's sums are cut the same way whatever else
+// is in the call: with many rows, where half as many CTAs run, it is cut alike.
 static int q8_chunk_tiles(int nt, int Hkv)
 {
     const int all = (nt + 1) / 2;
@@ -119,8 +141,8 @@ struct Q8Shape {
     static constexpr int kWarps = 4 * PARTS;
     static constexpr int kThreads = 32 * (kWarps + 12);
     static constexpr int kCtas = PARTS == 1 ? 2 : 1;           // of a multiprocessor
-    // registers of a thread on weights; 32 of a turning one, 48 of the last four warps':
-    // 32,768 of a CTA launched with 64 each, 61,440 with 96
+    // registers of a thread on weights; a turning one has 32, one of the last four warps
+    // 48: together 32,768 of a CTA of 512 launched with 64 each, 61,440 of 640 with 96
     static constexpr int kRegs = PARTS == 1 ? 144 : 184;
     static constexpr int kSlotsK = NG == 3 ? 4 : NG == 4 || NG == 5 || NG == 8 ? 3 : 2;  // tiles in flight
     static constexpr int kSlotsV = NG == 3 ? 3 : NG == 2 ? 1 : 2;
@@ -349,8 +371,9 @@ __device__ __forceinline__ uint4 lds128_at(uint32_t addr)
 }
 
 // One operand's codes, [lane's row][128], into tensor memory as f16, from the row's
-// first piece of 16 in the tile's swizzle.  (Small pieces: few registers, and code
-// that fits the schedulers' first instruction cache.)
+// first piece of 16 in the tile's swizzle.  (A loop of 32 codes a round: unrolled to 64
+// or 128 its code is fetched more slowly than it runs, 57 and 58 us for 55 where 4 slots
+// are longest.)
 __device__ __forceinline__ void q8_turn(uint32_t from, uint32_t to)
 {
 #pragma unroll 1
@@ -1021,7 +1044,7 @@ constexpr int kQ8MaxKeys = kQ8MaxTail + kMaxTree;
 
 __global__ void __launch_bounds__(kQ8MergeThreads, 5)
 q8kv_merge_kernel(const float* q, const __grid_constant__ Q8Batch b, int Hq, int Hkv, Q8Scale scale, const float* part_o,
-                  const float* part_ml, float* __restrict__ out, int8_t* __restrict__ out_q, float* __restrict__ out_d)
+                  const float* part_ml, float* __restrict__ out)
 {
     __shared__ float ps[kQ8MaxKeys];                    // the f16 keys' products
     __shared__ float ms[kQ8MaxChunks], ls[kQ8MaxChunks];  // the chunks' maxima and sums
@@ -1121,18 +1144,11 @@ q8kv_merge_kernel(const float* q, const __grid_constant__ Q8Batch b, int Hq, int
     __syncthreads();
     const float* of = &os[0][0].x + tid;
     const float O = __fadd_rn(__fadd_rn(of[0], of[kHeadDim]), __fadd_rn(of[2 * kHeadDim], of[3 * kHeadDim]));
-    const float val = __fdiv_rn(O, L);
-    out[rh * kHeadDim + tid] = val;
-    if (out_q) {
-        float dd;
-        const int code = q8_quantize_lane(val, &dd);
-        out_q[rh * kHeadDim + tid] = (int8_t)code;
-        if (lane == 0) out_d[(rh * kHeadDim + tid) / 32] = dd;
-    }
+    out[rh * kHeadDim + tid] = __fdiv_rn(O, L);
 }
 
 cudaError_t launch_q8kv_attention(const float* q, const Q8Batch& b, int Hq, int Hkv, float scale, void* part, float* out,
-                                  int8_t* out_q, float* out_d, cudaStream_t s)
+                                  cudaStream_t s)
 {
     int64_t units = 0, n_part = 0;
     bool runs = true;
@@ -1158,7 +1174,7 @@ cudaError_t launch_q8kv_attention(const float* q, const Q8Batch& b, int Hq, int 
         if (e != cudaSuccess) return e;
     }
     const cudaError_t e = launch_pdl(q8kv_merge_kernel, dim3(Hq, b.n_row), dim3(kQ8MergeThreads), s, q, b, Hq, Hkv, sc,
-                                     (const float*)part_o, (const float*)part_ml, out, out_q, out_d);
+                                     (const float*)part_o, (const float*)part_ml, out);
     if (e != cudaSuccess) return e;
     count_launches(1);
     return cudaSuccess;

@@ -63,9 +63,9 @@ int q8kv_max_chunks(int max_sealed, int Hkv);
 // Bytes of n_part rows of partial results.
 size_t q8kv_part_bytes(int64_t n_part);
 
-// out [T][Hq][128]; out_q, out_d (nullable): out's q8_0 codes and scales.
+// out [T][Hq][128].
 cudaError_t launch_q8kv_attention(const float* q, const Q8Batch& b, int Hq, int Hkv, float scale, void* part, float* out,
-                                  int8_t* out_q, float* out_d, cudaStream_t s);
+                                  cudaStream_t s);
 
 // Bounded waits of that attention that expired on the current device.
 cudaError_t read_q8kv_wait_timeouts(uint32_t* count, bool reset);

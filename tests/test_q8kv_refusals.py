@@ -133,3 +133,14 @@ THREE = (ctypes.c_uint8 * 64)(*[i % 3 for i in range(64)])
 ])
 def test_project_refusals(lib, want, kw):
     assert project(lib, **kw) == want and lib.luce_last_error()
+
+
+def test_seal_reads_32_bytes_at_a_time(lib):
+    for kw in (dict(k=P + M + 16), dict(v=P + 2 * M + 16)):
+        assert seal(lib, [slot(**kw)]) == E and b"32-byte" in lib.luce_last_error()
+
+
+def test_sizes_that_pass_64_bits(lib):
+    assert project(lib, ld=1 << 62) == E and b"2^28" in lib.luce_last_error()
+    assert seal(lib, [slot(pages=2 ** 31 - 1)], L=1 << 19) == E and b"out of range" in lib.luce_last_error()
+    assert attn(lib, [view(pages=2 ** 31 - 1, page=1 << 37)]) == E and b"out of range" in lib.luce_last_error()
