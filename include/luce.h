@@ -76,7 +76,7 @@ uint64_t luce_launch_count(void);
  * projection of the decode step on either ring) wait on shared-memory
  * barriers for those copies, and the attention that serves a slot's verify
  * rows together waits on one for its tcgen05 MMAs; the attention of draft trees
- * waits for both.  Every such wait gives up
+ * and the one over caches in 8 bits wait for both.  Every such wait gives up
  * after about one second and adds one to this device counter, so a stalled
  * copy engine or tensor core surfaces here instead of as a hung stream.  A
  * healthy run reads 0 (an attention CTA whose wait expired writes none of its

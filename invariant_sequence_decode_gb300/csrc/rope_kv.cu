@@ -113,20 +113,23 @@ cudaError_t launch_kv_append(const float* k, const float* v, int64_t ld, int Hkv
 // without a gamma), and the pair (y_i, y_(i+64)) rotates by the row's position on
 // the pair's axis times theta^(-i/64); v heads are only rounded.
 // Bound by memory (read once, written once), so what is shared is kept small:
-// a row's 64 cosines and sines are formed once per CTA into shared memory, and
-// 16 lanes take a head, four pairs each as two 16-byte loads.  All loads of a
-// lane's heads are under way before the angles are: kProjectAhead heads of 16
-// at a time.  Sums of squares: a lane's eight in order, then lanes by an xor
+// a row's 64 cosines and sines and the gammas go once per CTA into shared memory, and
+// 16 lanes take a head, four pairs each as two 16-byte loads, kProjectAhead heads at a
+// time.  All loads of the first are under way before the angles (formed in 64-bit
+// arithmetic) and the sums are.  8,192 rows of 40 + 2 x 8 heads take 66.7 us, 6.5 TB/s,
+// 0.96 of a copy's rate; with four heads at a time 70.7, three 73.4, one 75.5, eight CTAs a
+// multiprocessor instead of six 74.1.  One row takes 4.6 us, latency.  Sums of squares: a lane's eight in order, then lanes by an xor
 // butterfly, so a row's bits do not depend on the other rows or the grid; without
 // gammas and with one axis they are those of rope_posvec_kernel and kv_append_kernel.
-constexpr int kProjectAhead = 4;
+constexpr int kProjectAhead = 2;
 
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 6)
 qk_norm_rope_kernel(const float* qkv, int64_t ld, int Hq, int Hkv, const __grid_constant__ AppendViews views,
                     const float* q_gamma, const float* k_gamma, float eps, const int32_t* pos, int T, PairAxes axes,
                     const __grid_constant__ RopeFreq f, float* __restrict__ q)
 {
     __shared__ __align__(16) float cs[2][kHeadDim / 2];
+    __shared__ __align__(16) float gammas[2][kHeadDim];
     pdl_trigger();
     const int t = blockIdx.x, tid = threadIdx.x, part = tid & 15, heads = Hq + 2 * Hkv;
     const int step = 16 * gridDim.y;
@@ -154,19 +157,16 @@ qk_norm_rope_kernel(const float* qkv, int64_t ld, int Hq, int Hkv, const __grid_
                 const float2 x = rope_cs(ld_placed_i(pos + (int64_t)axis * T + t), f.inv[tid]);
                 cs[0][tid] = x.x;
                 cs[1][tid] = x.y;
+            } else if (tid < kHeadDim / 2 + 2 * kHeadDim / 4) {
+                const int i = tid - kHeadDim / 2, at4 = 4 * (i & (kHeadDim / 4 - 1));
+                const float* gamma = i < kHeadDim / 4 ? q_gamma : k_gamma;
+                if (gamma) *reinterpret_cast<float4*>(&gammas[i / (kHeadDim / 4)][at4]) = ld_placed_f4(gamma + at4);
             }
-            __syncthreads();
-            turned = true;
         }
-        const float4 c = *reinterpret_cast<const float4*>(&cs[0][4 * part]);
-        const float4 s = *reinterpret_cast<const float4*>(&cs[1][4 * part]);
+        float inv[kProjectAhead];
 #pragma unroll
         for (int e = 0; e < kProjectAhead; ++e) {
-            const int h = h0 + e * step;
-            if (h - (tid >> 4) >= heads) break;  // (the same for all threads of the CTA)
-            float4 x = a[e], y = b[e];
-            const float* gamma = h < Hq ? q_gamma : h < Hq + Hkv ? k_gamma : nullptr;
-            // (all lanes of the warp come here: the butterfly needs them)
+            const float4 x = a[e], y = b[e];
             float sq = __fmul_rn(x.x, x.x);
             sq = __fmaf_rn(x.y, x.y, sq);
             sq = __fmaf_rn(x.z, x.z, sq);
@@ -177,17 +177,29 @@ qk_norm_rope_kernel(const float* qkv, int64_t ld, int Hq, int Hkv, const __grid_
             sq = __fmaf_rn(y.w, y.w, sq);
 #pragma unroll
             for (int o = 1; o < 16; o <<= 1) sq = __fadd_rn(sq, __shfl_xor_sync(0xffffffffu, sq, o));
+            inv[e] = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fmul_rn(sq, 1.0f / kHeadDim), eps)));
+        }
+        if (!turned) __syncthreads();
+        turned = true;
+        const float4 c = *reinterpret_cast<const float4*>(&cs[0][4 * part]);
+        const float4 s = *reinterpret_cast<const float4*>(&cs[1][4 * part]);
+#pragma unroll
+        for (int e = 0; e < kProjectAhead; ++e) {
+            const int h = h0 + e * step;
+            if (h >= heads) break;
+            float4 x = a[e], y = b[e];
+            const float* gamma = h < Hq ? q_gamma : h < Hq + Hkv ? k_gamma : nullptr;
             if (gamma) {
-                const float inv = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fmul_rn(sq, 1.0f / kHeadDim), eps)));
-                const float4 g0 = ld_placed_f4(gamma + 4 * part), g1 = ld_placed_f4(gamma + kHeadDim / 2 + 4 * part);
-                x.x = __fmul_rn(__fmul_rn(x.x, inv), g0.x);
-                x.y = __fmul_rn(__fmul_rn(x.y, inv), g0.y);
-                x.z = __fmul_rn(__fmul_rn(x.z, inv), g0.z);
-                x.w = __fmul_rn(__fmul_rn(x.w, inv), g0.w);
-                y.x = __fmul_rn(__fmul_rn(y.x, inv), g1.x);
-                y.y = __fmul_rn(__fmul_rn(y.y, inv), g1.y);
-                y.z = __fmul_rn(__fmul_rn(y.z, inv), g1.z);
-                y.w = __fmul_rn(__fmul_rn(y.w, inv), g1.w);
+                const float* gs = gammas[h >= Hq];
+                const float4 g0 = *reinterpret_cast<const float4*>(gs + 4 * part), g1 = *reinterpret_cast<const float4*>(gs + kHeadDim / 2 + 4 * part);
+                x.x = __fmul_rn(__fmul_rn(x.x, inv[e]), g0.x);
+                x.y = __fmul_rn(__fmul_rn(x.y, inv[e]), g0.y);
+                x.z = __fmul_rn(__fmul_rn(x.z, inv[e]), g0.z);
+                x.w = __fmul_rn(__fmul_rn(x.w, inv[e]), g0.w);
+                y.x = __fmul_rn(__fmul_rn(y.x, inv[e]), g1.x);
+                y.y = __fmul_rn(__fmul_rn(y.y, inv[e]), g1.y);
+                y.z = __fmul_rn(__fmul_rn(y.z, inv[e]), g1.z);
+                y.w = __fmul_rn(__fmul_rn(y.w, inv[e]), g1.w);
             }
             if (h < Hq + Hkv) {
                 rope_rotate(x.x, y.x, c.x, s.x);
@@ -195,7 +207,6 @@ qk_norm_rope_kernel(const float* qkv, int64_t ld, int Hq, int Hkv, const __grid_
                 rope_rotate(x.z, y.z, c.z, s.z);
                 rope_rotate(x.w, y.w, c.w, s.w);
             }
-            if (h >= heads) continue;
             if (h < Hq) {
                 float* o = q + ((int64_t)t * Hq + h) * kHeadDim + 4 * part;
                 *reinterpret_cast<float4*>(o) = x;
@@ -216,7 +227,9 @@ cudaError_t launch_qk_norm_rope(const float* qkv, int64_t ld, int T, int Hq, int
                                 const float* q_gamma, const float* k_gamma, float eps, const int32_t* pos,
                                 const PairAxes& axes, const RopeFreq& f, float* q, cudaStream_t s)
 {
-    // few rows: 16 heads a CTA, so that a row's heads go at once; many: a row a CTA, its angles formed once
+    // few rows: 16 heads a CTA, so that a row's heads go at once (40 + 2 x 8 heads, with the
+    // launch: 6.8 us for 8.9 up to 40 rows, 8.9 for 10.9 at 152, no difference up to 456); many: a
+    // row a CTA, its angles formed once (608 rows 13.0 us for 15.0, 8,192 67.6 for 98.1)
     const int groups = T < 152 ? std::min((Hq + 2 * Hkv + 15) / 16, 65535) : 1;
     const cudaError_t e = launch_pdl(qk_norm_rope_kernel, dim3(T, groups), dim3(256), s, qkv, ld, Hq, Hkv, views, q_gamma,
                                      k_gamma, eps, pos, T, axes, f, q);
