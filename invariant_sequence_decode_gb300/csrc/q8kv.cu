@@ -151,7 +151,8 @@ struct Q8Shape {
     // scores of a step's two, and its V, which waits for their weights
     static constexpr int kTurnedV = NG == 2 || NG == 8 ? 1 : 2;
     static constexpr int kWeights = NG == 8 ? 1 : 2;           // tiles of weights in shared memory
-    static constexpr int kHeads = NG == 1 || NG == 3 || NG == 4 ? 2 : 1;  // heads of q in shared memory
+    // heads of q in shared memory: with two the next one's is prepared ahead by a warp of its own
+    static constexpr int kHeads = NG == 1 ? 2 : 1;
     static constexpr bool kTwice = NG == 2 || NG >= 5;                    // scores are read twice, not held while maxima are found
     static constexpr int kPart = kRows * kHeadDim * 2;         // bytes of one part of q, or of the weights
     static constexpr uint32_t kColK = 0, kColV = 64, kColS = kColV + 64 * kTurnedV, kColO = kColS + 2 * kRows;
@@ -503,11 +504,10 @@ __device__ void q8_sums(const Q8Batch& b, int Hkv, const Q8Share& w, uint32_t we
 
 // A head's rows of q, in units of a power of two each, as two f16 parts in the products'
 // layout: 16 lanes a row, rows first, first + step, ..
-template <typename S>
+template <typename S, int kAhead>
 __device__ void q8_prepare(const float* q, const Q8Batch& b, int Hq, int Hkv, const Q8Run& t, const Q8Scale& scale, uint8_t* parts,
                            float (*unit_s)[S::kCols], int (*from_s)[S::kCols], int first, int step)
 {
-    constexpr int kAhead = S::kRows <= 32 ? 2 : 4;
     const Q8View& v = b.view[t.view];
     const int GQ = Hq / Hkv, R = v.n_nodes * GQ, piece = threadIdx.x & 15;
     for (int c0 = first; c0 < S::kRows; c0 += step * kAhead) {
@@ -635,7 +635,7 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
         mbar_init(&bar.o_full, 1);
         mbar_init(&bar.o_free, S::kWarps);
         for (int i = 0; i < S::kHeads; ++i) {
-            mbar_init(&bar.q_full[i], 1);
+            mbar_init(&bar.q_full[i], S::kHeads == 1 ? S::kWarps : 1);
             mbar_init(&bar.q_free[i], 1 + S::kWarps);
         }
         mbar_init(&bar.done[0], 1);
@@ -661,15 +661,17 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (warp == S::kWarps + 8 && lane == 0) q8_produce(maps, b, Hkv, w, tiles, scales, bar);
         if (warp > S::kWarps + 8) {
-            // the first head's q by all three of these warps, which have nothing else to do
-            // before; the others' ahead of time by the last one
-            const int first = (tid - 32 * (S::kWarps + 9)) >> 4;
-            pdl_wait();
-            q8_prepare<S>(q, b, Hq, Hkv, q8_run(b, Hkv, w.u0, w.u0 + 1), scale, qs, unit_s[0], from_s[0], first, 6);
-            asm volatile("bar.sync 15, 96;" ::: "memory");
+            if (S::kHeads > 1) {
+                // the first head's q by all three of these warps, which have nothing else to
+                // do before
+                pdl_wait();
+                q8_prepare<S, 2>(q, b, Hq, Hkv, q8_run(b, Hkv, w.u0, w.u0 + 1), scale, qs, unit_s[0], from_s[0],
+                                 (tid - 32 * (S::kWarps + 9)) >> 4, 6);
+                asm volatile("bar.sync 15, 96;" ::: "memory");
+            }
             if (warp == S::kWarps + 9) q8_scores(b, Hkv, w, smem_addr(qs), tmem, bar);
             if (warp == S::kWarps + 10) q8_sums(b, Hkv, w, smem_addr(ps), tmem, bar);
-            if (warp == S::kWarps + 11) {
+            if (S::kHeads > 1 && warp == S::kWarps + 11) {
                 int head = -1, last = -1;
                 q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
                     if (t.view * Hkv + t.g == last) return true;
@@ -677,7 +679,7 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                     const int to = ++head % S::kHeads;
                     if (head > 0) {
                         if (!__all_sync(0xffffffffu, mbar_wait(&bar.q_free[to], ((head / S::kHeads) & 1) ^ 1, late))) return false;
-                        q8_prepare<S>(q, b, Hq, Hkv, t, scale, qs + to * 2 * S::kPart, unit_s[to], from_s[to], lane >> 4, 2);
+                        q8_prepare<S, 2>(q, b, Hq, Hkv, t, scale, qs + to * 2 * S::kPart, unit_s[to], from_s[to], lane >> 4, 2);
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar.q_full[to]);
@@ -800,8 +802,15 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                 if (last >= 0 && lane == 0) mbar_arrive(&bar.q_free[head % S::kHeads]);  // (its units have been read)
                 last = t.view * Hkv + t.g;
                 ++head;
+                if (head == 0) pdl_wait();  // (q is there, and the results' place is free)
+                // With room for one head's q it is prepared by these warps, which have nothing
+                // else to do by then: each part's rows by its own, all rows at once
+                if (S::kHeads == 1) {
+                    if (head > 0) ok = ok && mbar_wait(&bar.q_free[0], (head & 1) ^ 1, late);
+                    q8_prepare<S, G>(q, b, Hq, Hkv, t, scale, qs, unit_s[0], from_s[0], tid >> 4, 8 * PARTS);
+                    warp_arrive(&bar.q_full[0]);
+                }
                 ok = ok && mbar_wait(&bar.q_full[head % S::kHeads], (head / S::kHeads) & 1, late);
-                if (head == 0) pdl_wait();  // (the results' place is free)
             }
             // (out of the views' table, once)
             const int sealed = v.sealed, front = v.front, skip = v.back - v.front, sinks = v.sinks, chunk = v.chunk, tile0 = t.t0;
