@@ -149,7 +149,7 @@ struct Q8Shape {
     static constexpr int kSlots = kSlotsK + kSlotsV;
     // In tensor memory: one tile of K, which is multiplied as soon as it is there, the
     // scores of a step's two, and its V, which waits for their weights
-    static constexpr int kTurnedV = NG == 2 || NG == 8 ? 1 : 2;
+    static constexpr int kTurnedV = NG == 2 || NG == 5 || NG == 8 ? 1 : 2;
     static constexpr int kWeights = NG == 8 ? 1 : 2;           // tiles of weights in shared memory
     // heads of q in shared memory: with two the next one's is prepared ahead by a warp of its own
     static constexpr int kHeads = NG == 1 ? 2 : 1;
@@ -919,11 +919,12 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                 }
                 __syncwarp();
                 if (i > 0) take(i - 1);  // (behind its products the weights' places are free)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
+#pragma unroll(NG == 2 ? 1 : 2)
+                for (int x = 0; x < 2; ++x) {  // (as a loop where that was faster: less code is fetched)
                     if (x == 1 && two == 1) break;
                     const uint32_t to = smem_addr(ps) + (x % S::kWeights) * 2 * S::kPart + row_at;
-                    const uint64_t iv2 = pair(iv[x], iv[x]);
+                    const float inverse = x ? iv[1] : iv[0];
+                    const uint64_t iv2 = pair(inverse, inverse);
                     if (x == 1 && S::kWeights == 1) ok = ok && mbar_wait(&bar.p_free, freed & 1, late);
 #pragma unroll
                     for (int e = 0; e < G; ++e) {
