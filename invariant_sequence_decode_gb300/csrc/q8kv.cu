@@ -61,6 +61,12 @@ struct Q8Scale {
     float sign, log2;
 };
 
+// Query heads of a KV head, KV heads.
+struct Q8Heads {
+    int group, kv, inverse;  // inverse: 2^16 / group, rounded up
+    __device__ __forceinline__ int node(int c) const { return c * inverse >> 16; }  // c / group, for c < 2^10 and groups up to 8
+};
+
 // Tiles of a chunk for a view of nt tiles, an even number: a step of the kernel takes
 // two.  Of the cuts that fill kQ8Ctas CTAs 1, 2, 3 or 4 times the cheapest is taken,
 // a chunk costing its steps and about one more (its q, its results).  A function of the
@@ -503,49 +509,54 @@ __device__ void q8_sums(const Q8Batch& b, int Hkv, const Q8Share& w, uint32_t we
 }
 
 // A head's rows of q, in units of a power of two each, as two f16 parts in the products'
-// layout: 16 lanes a row, rows first, first + step, ..
-template <typename S, int kAhead>
-__device__ void q8_prepare(const float* q, const Q8Batch& b, int Hq, int Hkv, const Q8Run& t, const Q8Scale& scale, uint8_t* parts,
-                           float (*unit_s)[S::kCols], int (*from_s)[S::kCols], int first, int step)
+// layout: 16 lanes a row, rows first, first + step, ..  A loop with the next row on its
+// way: a kernel's first instructions are fetched more slowly than they run.
+template <typename S>
+__device__ __forceinline__ void q8_prepare(const float* q, const Q8Batch& b, const Q8Heads& heads, const Q8Run& t, const Q8Scale& scale,
+                                           uint8_t* parts, float (*unit_s)[S::kCols], int (*from_s)[S::kCols], int first, int step)
 {
     const Q8View& v = b.view[t.view];
-    const int GQ = Hq / Hkv, R = v.n_nodes * GQ, piece = threadIdx.x & 15;
-    for (int c0 = first; c0 < S::kRows; c0 += step * kAhead) {
-        float4 x[kAhead], y[kAhead];
-#pragma unroll
-        for (int e = 0; e < kAhead; ++e) {
-            const int c = c0 + step * e;
-            x[e] = y[e] = make_float4(0, 0, 0, 0);
-            if (c < R) {
-                const float* p = q + ((int64_t)(v.row0 + c / GQ) * Hq + t.g * GQ + c % GQ) * kHeadDim + 8 * piece;
-                x[e] = ld_placed_f4(p);
-                y[e] = ld_placed_f4(p + 4);
-            }
+    const int R = v.n_nodes * heads.group, piece = threadIdx.x & 15;
+    const float* head_q = q + ((int64_t)v.row0 * heads.kv + t.g) * heads.group * kHeadDim + 8 * piece;
+    const int from = v.sealed + v.tail - v.window;
+    float4 x, y;
+    int path;
+    auto load = [&](int c) {
+        x = y = make_float4(0, 0, 0, 0);
+        path = 0;
+        if (c < R) {
+            const int node = heads.node(c);
+            const float* p = head_q + ((int64_t)node * heads.kv * heads.group + c - node * heads.group) * kHeadDim;
+            x = ld_placed_f4(p);
+            y = ld_placed_f4(p + 4);
+            path = b.row[v.row0 + node].n_path;
         }
+    };
+    load(first);
+#pragma unroll 1
+    for (int c = first; c < S::kRows; c += step) {  // (kRows and step are even: a warp's halves go round as often)
+        const float4 x0 = x, y0 = y;
+        const int from0 = from + path;
+        load(c + step);
+        float big = fmaxf(fmaxf(fmaxf(fabsf(x0.x), fabsf(x0.y)), fmaxf(fabsf(x0.z), fabsf(x0.w))),
+                          fmaxf(fmaxf(fabsf(y0.x), fabsf(y0.y)), fmaxf(fabsf(y0.z), fabsf(y0.w))));
 #pragma unroll
-        for (int e = 0; e < kAhead; ++e) {
-            const int c = c0 + step * e;
-            float big = fmaxf(fmaxf(fmaxf(fabsf(x[e].x), fabsf(x[e].y)), fmaxf(fabsf(x[e].z), fabsf(x[e].w))),
-                              fmaxf(fmaxf(fabsf(y[e].x), fabsf(y[e].y)), fmaxf(fabsf(y[e].z), fabsf(y[e].w))));
-#pragma unroll
-            for (int d = 1; d < 16; d <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
-            if (c >= S::kRows) continue;
-            // the row's unit puts its largest element into [2^14, 2^15)
-            const int exp = max((__float_as_int(big) >> 23) - 127 - 14, -112);
-            const float into = __fmul_rn(scale.sign, __int_as_float((127 - exp) << 23));
-            uint4 hi, lo;
-            tree_split(__fmul_rn(x[e].x, into), __fmul_rn(x[e].y, into), hi.x, lo.x);
-            tree_split(__fmul_rn(x[e].z, into), __fmul_rn(x[e].w, into), hi.y, lo.y);
-            tree_split(__fmul_rn(y[e].x, into), __fmul_rn(y[e].y, into), hi.z, lo.z);
-            tree_split(__fmul_rn(y[e].z, into), __fmul_rn(y[e].w, into), hi.w, lo.w);
-            uint8_t* at = parts + (piece >> 3) * (S::kPart / 2) + (c >> 3) * 1024 + (c & 7) * 128 + (((piece & 7) ^ (c & 7)) << 4);
-            *reinterpret_cast<uint4*>(at) = hi;
-            *reinterpret_cast<uint4*>(at + S::kPart) = lo;
-            if (piece == 0) {
-                const int part = (c >> 3) % S::kParts, col = (c >> 3) / S::kParts * 8 + (c & 7);
-                unit_s[part][col] = __fmul_rn(scale.log2, __int_as_float((127 + exp) << 23));
-                from_s[part][col] = v.sealed + v.tail + b.row[v.row0 + min(c / GQ, v.n_nodes - 1)].n_path - v.window;
-            }
+        for (int d = 1; d < 16; d <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+        // the row's unit puts its largest element into [2^14, 2^15)
+        const int exp = max((__float_as_int(big) >> 23) - 127 - 14, -112);
+        const float into = __fmul_rn(scale.sign, __int_as_float((127 - exp) << 23));
+        uint4 hi, lo;
+        tree_split(__fmul_rn(x0.x, into), __fmul_rn(x0.y, into), hi.x, lo.x);
+        tree_split(__fmul_rn(x0.z, into), __fmul_rn(x0.w, into), hi.y, lo.y);
+        tree_split(__fmul_rn(y0.x, into), __fmul_rn(y0.y, into), hi.z, lo.z);
+        tree_split(__fmul_rn(y0.z, into), __fmul_rn(y0.w, into), hi.w, lo.w);
+        uint8_t* at = parts + (piece >> 3) * (S::kPart / 2) + (c >> 3) * 1024 + (c & 7) * 128 + (((piece & 7) ^ (c & 7)) << 4);
+        *reinterpret_cast<uint4*>(at) = hi;
+        *reinterpret_cast<uint4*>(at + S::kPart) = lo;
+        if (piece == 0) {
+            const int part = (c >> 3) % S::kParts, col = (c >> 3) / S::kParts * 8 + (c & 7);
+            unit_s[part][col] = __fmul_rn(scale.log2, __int_as_float((127 + exp) << 23));
+            from_s[part][col] = from0;
         }
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -586,10 +597,11 @@ constexpr int q8_left(int n, int off = 16) { return off < 4 ? n : q8_left(n % 2 
 // kCtas CTAs an SM, each with its share of all chunks.
 template <int NG, int PARTS>
 __global__ void __launch_bounds__(Q8Shape<NG, PARTS>::kThreads, Q8Shape<NG, PARTS>::kCtas)
-q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __grid_constant__ Q8Batch b, int Hq, int Hkv, int units,
+q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __grid_constant__ Q8Batch b, Q8Heads heads, int units,
                   bool runs, Q8Scale scale, float* __restrict__ part_o, float* __restrict__ part_ml)
 {
     using S = Q8Shape<NG, PARTS>;
+    const int Hkv = heads.kv;
     extern __shared__ uint8_t q8_smem[];
     uint8_t* tiles = q8_smem + ((1024u - (smem_addr(q8_smem) & 1023u)) & 1023u);
     uint8_t* qs = tiles + S::kSlots * kQ8PageBytes;       // q: high and low part, two halves of the dims each
@@ -665,7 +677,7 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                 // the first head's q by all three of these warps, which have nothing else to
                 // do before
                 pdl_wait();
-                q8_prepare<S, 2>(q, b, Hq, Hkv, q8_run(b, Hkv, w.u0, w.u0 + 1), scale, qs, unit_s[0], from_s[0],
+                q8_prepare<S>(q, b, heads, q8_run(b, Hkv, w.u0, w.u0 + 1), scale, qs, unit_s[0], from_s[0],
                                  (tid - 32 * (S::kWarps + 9)) >> 4, 6);
                 asm volatile("bar.sync 15, 96;" ::: "memory");
             }
@@ -679,7 +691,7 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                     const int to = ++head % S::kHeads;
                     if (head > 0) {
                         if (!__all_sync(0xffffffffu, mbar_wait(&bar.q_free[to], ((head / S::kHeads) & 1) ^ 1, late))) return false;
-                        q8_prepare<S, 2>(q, b, Hq, Hkv, t, scale, qs + to * 2 * S::kPart, unit_s[to], from_s[to], lane >> 4, 2);
+                        q8_prepare<S>(q, b, heads, t, scale, qs + to * 2 * S::kPart, unit_s[to], from_s[to], lane >> 4, 2);
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar.q_full[to]);
@@ -796,7 +808,7 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
             for (int c = 0; c < 4; ++c) o[e][c] = 0;
         q8_each_run(b, Hkv, w, [&](const Q8Run& t) {
             const Q8View& v = b.view[t.view];
-            const int R = v.n_nodes * (Hq / Hkv);
+            const int R = v.n_nodes * heads.group;
             if (t.view * Hkv + t.g != last) {
                 __syncwarp();
                 if (last >= 0 && lane == 0) mbar_arrive(&bar.q_free[head % S::kHeads]);  // (its units have been read)
@@ -804,10 +816,10 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                 ++head;
                 if (head == 0) pdl_wait();  // (q is there, and the results' place is free)
                 // With room for one head's q it is prepared by these warps, which have nothing
-                // else to do by then: each part's rows by its own, all rows at once
+                // else to do by then: each part's rows by its own
                 if (S::kHeads == 1) {
                     if (head > 0) ok = ok && mbar_wait(&bar.q_free[0], (head & 1) ^ 1, late);
-                    q8_prepare<S, G>(q, b, Hq, Hkv, t, scale, qs, unit_s[0], from_s[0], tid >> 4, 8 * PARTS);
+                    q8_prepare<S>(q, b, heads, t, scale, qs, unit_s[0], from_s[0], tid >> 4, 8 * PARTS);
                     warp_arrive(&bar.q_full[0]);
                 }
                 ok = ok && mbar_wait(&bar.q_full[head % S::kHeads], (head / S::kHeads) & 1, late);
@@ -1025,13 +1037,14 @@ static cudaError_t launch_chunks(const Q8Maps& maps, const float* q, const Q8Bat
                                  const Q8Scale& scale, float* part_o, float* part_ml, cudaStream_t s)
 {
     using S = Q8Shape<NG, PARTS>;
+    const Q8Heads heads = {Hq / Hkv, Hkv, (65536 + Hq / Hkv - 1) / (Hq / Hkv)};
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     static std::atomic<bool> done[kMaxDevices];
     cudaError_t e = set_smem_once(q8kv_chunk_kernel<NG, PARTS>, S::kBytes, done);
     if (e == cudaSuccess)
         e = launch_pdl_smem(q8kv_chunk_kernel<NG, PARTS>, dim3((unsigned)std::min<int64_t>(sms * S::kCtas, units)), dim3(S::kThreads),
-                            S::kBytes, s, maps, q, b, Hq, Hkv, (int)units, runs, scale, part_o, part_ml);
+                            S::kBytes, s, maps, q, b, heads, (int)units, runs, scale, part_o, part_ml);
     if (e == cudaSuccess) count_launches(1);
     return e;
 }
