@@ -23,16 +23,18 @@
 //
 // What bounds it.  A tile is 33 KB and 1,430 cycles of an SM's share of the copy rate.
 // Its codes are turned at 4 bytes for 6 instructions: of the 4,700 warp instructions a
-// tile with up to 16 rows costs, 1,900 turn, 400 form weights, 200 issue products.  Warps
-// of a kind share a scheduler with four others and fetch code of their own, and a tile
-// takes 1,700 cycles: long contexts are bound by issue and by instruction fetch, not by
-// memory.  With many rows the weights take over (two 16-bit parts, one exponential and a
-// dozen other instructions each).  Short contexts are bound by the latency of
-// one tile's chain (load, turn, product, weights, product, sums) and of the merge.
+// tile with up to 16 rows costs, 1,900 turn, 400 form weights, 200 issue products; issue
+// slots are taken to 59 %, and most of the rest is instruction fetch, as warps of six kinds
+// run code of their own, and latency within the weights' warps, of which a scheduler has one
+// or two.  With many rows the weights take over (two 16-bit parts, one exponential and a
+// dozen other instructions each).  Short contexts are bound by the latency of one tile's
+// chain (load, turn, product, weights, product, sums) and of the merge.
 //
-// Measured (HBM reads from memory, L2 flushed): 4 one-token slots of 8 KV heads x 4,096
-// keys @@4x1@@; 4 slots of 4 nodes @@4x4@@; 4 paged one-token slots of 32k to 128k keys @@long@@
-// (197 MB); one slot of 16 nodes x 131k @@16@@; 4 slots of 4 nodes with a window @@win@@.
+// Measured (L2 flushed; with the merge): 4 one-token slots of 8 KV heads x 2,048 keys 12.6 us;
+// 4 slots of 4 nodes 15.1; 4 paged one-token slots of 16k to 33k keys (197 MB) 52.9, 3.7
+// TB/s; one slot of 16 nodes x 130,784 keys (269 MB, 43 GFLOP) 118, 2.3 TB/s and 0.36
+// PFLOP/s in one f16 part (twice that with both); 4 slots of 4 nodes, a window of 4,096
+// keys, 22.4.
 #include <limits.h>
 
 #include <algorithm>
@@ -1055,14 +1057,17 @@ static cudaError_t launch_chunks(const Q8Maps& maps, const float* q, const Q8Bat
 // path's.  One CTA of 4 warps.  Scores of the f16 keys: 16 lanes a key, eight dims
 // each, key 8 i + 2 warp + lane / 16 in step i.  Sums: four dims a lane, warp w takes
 // chunks w, w + 4, .. in order, then f16 keys w, w + 4, .. in order; the four are added
-// in order.  Bound by latency: K and V of the first 48 f16 keys (a tail that is
-// sealed at every step and the longest path), statistics and the first 20 chunks' sums
-// are all asked for before anything is used.  (Of 640 CTAs, 16 nodes of 40 heads, five
-// fit a multiprocessor.  With 8 warps 160 of them take 1 us less and 640 1 us more;
-// one order of summation serves both, as a row's bits do not depend on the others.)
+// in order.  Bound by latency: K and V of the first 32 f16 keys (a tail that is sealed
+// at every step), statistics and the first 20 chunks' sums are all asked for before
+// anything is used; a warp leaves its loops where its keys end.  Of 640 CTAs, 16 nodes
+// of 40 heads, five fit a multiprocessor.  Measured, 160 and 640 CTAs with the chunks before
+// them: 12.6 and 15.1 us; 64 keys in flight 13.8 and 15.7; loops that run to their full
+// length 13.2 and 15.4; six CTAs a multiprocessor 13.0 and 15.5.  (Eight warps took 1 us
+// less with 160 CTAs and 1 us more with 640; one order of summation serves both, as a row's
+// bits do not depend on the others.)
 constexpr int kQ8MergeWarps = 4, kQ8MergeThreads = 32 * kQ8MergeWarps;
 constexpr int kQ8Ahead = 5;  // chunk sums in flight per warp
-constexpr int kQ8Keys = 48;  // f16 keys in flight
+constexpr int kQ8Keys = 32;  // f16 keys in flight
 constexpr int kQ8MaxKeys = kQ8MaxTail + kMaxTree;
 
 __global__ void __launch_bounds__(kQ8MergeThreads, 5)
@@ -1082,8 +1087,8 @@ q8kv_merge_kernel(const float* q, const __grid_constant__ Q8Batch b, int Hq, int
     // f16 key a: the tail's, then the path's.  It is seen at a position below `sinks` or from `from` on
     const int sinks = v.window ? max(0, v.sinks - v.sealed) : n, from = v.window ? n - v.window : 0;
     const __half *kb = v.k + g * v.head_stride, *vb = v.v + g * v.head_stride;
-    const int64_t tok = v.tok_stride;
-    auto place = [&](int a) { return (int64_t)(a < tail ? a : tail + row.path[a - tail]) * tok; };
+    const uint32_t tok = (uint32_t)v.tok_stride;  // (below 2^32: one multiplication a key)
+    auto place = [&](int a) { return (uint64_t)(uint32_t)(a < tail ? a : tail + row.path[a - tail]) * tok; };
     auto seen = [&](int a) { return a < n && (a < sinks || a >= from); };
     pdl_wait();
     const int part = lane & 15;
@@ -1094,6 +1099,7 @@ q8kv_merge_kernel(const float* q, const __grid_constant__ Q8Batch b, int Hq, int
     auto load_k = [&](int base) {
 #pragma unroll
         for (int i = 0; i < kK; ++i) {
+            if (base + 2 * kQ8MergeWarps * i + 2 * warp >= n) break;  // (the warp as one)
             const int a = base + 2 * kQ8MergeWarps * i + 2 * warp + (lane >> 4);
             kx[i] = make_uint4(0, 0, 0, 0);
             if (seen(a)) kx[i] = ld_placed_u4(kb + place(a) + 8 * part);
@@ -1103,6 +1109,7 @@ q8kv_merge_kernel(const float* q, const __grid_constant__ Q8Batch b, int Hq, int
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
             const int a = base + kQ8MergeWarps * i + warp;
+            if (a >= n) break;
             vx[i] = make_uint2(0, 0);
             if (seen(a)) vx[i] = ld_placed_u2(vb + place(a) + 4 * lane);
         }
@@ -1128,6 +1135,7 @@ q8kv_merge_kernel(const float* q, const __grid_constant__ Q8Batch b, int Hq, int
         if (base > 0) load_k(base);
 #pragma unroll
         for (int i = 0; i < kK; ++i) {
+            if (base + 2 * kQ8MergeWarps * i + 2 * warp >= n) break;
             const int a = base + 2 * kQ8MergeWarps * i + 2 * warp + (lane >> 4);
             const float4 k0 = half4(make_uint2(kx[i].x, kx[i].y)), k1 = half4(make_uint2(kx[i].z, kx[i].w));
             float dot = __fmaf_rn(q0.w, k0.w, __fmaf_rn(q0.z, k0.z, __fmaf_rn(q0.y, k0.y, __fmul_rn(q0.x, k0.x))));
@@ -1160,7 +1168,8 @@ q8kv_merge_kernel(const float* q, const __grid_constant__ Q8Batch b, int Hq, int
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
             const int a = base + kQ8MergeWarps * i + warp;
-            if (a < n) axpy4(o, half4(vx[i]), tree_exp2(__fsub_rn(ps[a], M)));
+            if (a >= n) break;
+            axpy4(o, half4(vx[i]), tree_exp2(__fsub_rn(ps[a], M)));
         }
     }
     os[warp][lane] = o;
