@@ -152,16 +152,24 @@ struct Q8Shape {
     // registers of a thread on weights; a turning one has 32, one of the last four warps
     // 48: together 32,768 of a CTA of 512 launched with 64 each, 61,440 of 640 with 96
     static constexpr int kRegs = PARTS == 1 ? 144 : 184;
-    static constexpr int kSlotsK = NG == 3 ? 4 : NG == 4 || NG == 5 || NG == 8 ? 3 : 2;  // tiles in flight
+    // tiles in flight: what shared memory holds beside q and the weights
+    static constexpr int kSlotsK = NG == 3 ? 4 : NG == 4 || NG == 5 || NG == 8 ? 3 : 2;
     static constexpr int kSlotsV = NG == 3 ? 3 : NG == 2 ? 1 : 2;
     static constexpr int kSlots = kSlotsK + kSlotsV;
     // In tensor memory: one tile of K, which is multiplied as soon as it is there, the
-    // scores of a step's two, and its V, which waits for their weights
+    // scores of a step's two, and its V, which waits for their weights: two tiles where
+    // they fit (one takes 14.1 us for 13.6 with 5 rows of 32 tiles, 98 for 96 with 60 of
+    // 1,015), but for 80 rows, where turning ahead only keeps the weights' warps from their
+    // issue slots (124 us for 119 with 1,022 tiles)
     static constexpr int kTurnedV = NG == 2 || NG == 5 || NG == 8 ? 1 : 2;
     static constexpr int kWeights = NG == 8 ? 1 : 2;           // tiles of weights in shared memory
-    // heads of q in shared memory: with two the next one's is prepared ahead by a warp of its own
+    // heads of q in shared memory: with two the next one's is prepared ahead by a warp of its
+    // own (56.7 us for 53.4 without, at 4 rows of 4 slots), else the weights' many warps prepare
+    // it when its turn comes (27 us for 24 by the one warp at 64 rows, 155 for 124 at 80)
     static constexpr int kHeads = NG == 1 ? 2 : 1;
-    static constexpr bool kTwice = NG == 2 || NG >= 5;                    // scores are read twice, not held while maxima are found
+    // scores are read twice, not held while maxima are found, where registers do not hold both
+    // tiles' (held: 16.3 us for 16.0 with 20 rows, 150 for 119 with 80; read twice by 16: 54.4 for 53.4)
+    static constexpr bool kTwice = NG == 2 || NG >= 5;
     static constexpr int kPart = kRows * kHeadDim * 2;         // bytes of one part of q, or of the weights
     static constexpr uint32_t kColK = 0, kColV = 64, kColS = kColV + 64 * kTurnedV, kColO = kColS + 2 * kRows;
     static constexpr uint32_t kTmem = 512 / kCtas;
@@ -210,7 +218,7 @@ __device__ __forceinline__ Q8Run q8_run(const Q8Batch& b, int Hkv, int u, int en
 
 // The CTA's runs.  Chunks of one step: neighbours u0 .. u1 - 1 (heads change least).
 // Longer ones: of every `step` of them one, from the longest on, back and forth, so
-// that the CTAs' shares are alike.
+// that the CTAs' shares are alike (4 windows of unlike slots 27 us, as neighbours 36).
 struct Q8Share {
     int u0, u1, step;
 };
@@ -934,7 +942,7 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                 __syncwarp();
                 if (i > 0) take(i - 1);  // (behind its products the weights' places are free)
 #pragma unroll(NG == 2 ? 1 : 2)
-                for (int x = 0; x < 2; ++x) {  // (as a loop where that was faster: less code is fetched)
+                for (int x = 0; x < 2; ++x) {  // (as a loop less code is fetched: 15.7 us for 16.0 with 20 rows; with 80, 125 for 119)
                     if (x == 1 && two == 1) break;
                     const uint32_t to = smem_addr(ps) + (x % S::kWeights) * 2 * S::kPart + row_at;
                     const float inverse = x ? iv[1] : iv[0];
@@ -1199,6 +1207,11 @@ cudaError_t launch_q8kv_attention(const float* q, const Q8Batch& b, int Hq, int 
     if (units > 0) {
         Q8Maps maps{};
         if (!q8_maps(b, Hkv, &maps)) return cudaErrorInvalidValue;
+        // The least width that holds the rows of a KV head (a product's time goes with it).  Up to
+        // 32 rows the weights are little work and two CTAs of 16 warps share a multiprocessor, so
+        // that one's chain fills the other's waits (13.7 us for 15.2 with 5 rows, 18.7 for 20.3
+        // with 20, 58 for 67 on long slots); above, one CTA with twice the warps on weights and
+        // all of tensor memory, which holds 48 rows and more only then.
         const auto launch = rows <= 16 ? launch_chunks<1, 1> : rows <= 32 ? launch_chunks<2, 1> : rows <= 48 ? launch_chunks<3, 2>
                             : rows <= 64 ? launch_chunks<4, 2> : rows <= 80 ? launch_chunks<5, 2> : rows <= 96 ? launch_chunks<6, 2>
                                          : launch_chunks<8, 2>;
