@@ -159,9 +159,9 @@ struct Q8Shape {
     // In tensor memory: one tile of K, which is multiplied as soon as it is there, the
     // scores of a step's two, and its V, which waits for their weights: two tiles where
     // they fit (one takes 14.1 us for 13.6 with 5 rows of 32 tiles, 98 for 96 with 60 of
-    // 1,015), but for 80 rows, where turning ahead only keeps the weights' warps from their
-    // issue slots (124 us for 119 with 1,022 tiles)
-    static constexpr int kTurnedV = NG == 2 || NG == 5 || NG == 8 ? 1 : 2;
+    // 1,015), but where rows are so many that turning ahead only keeps the weights' warps from
+    // their issue slots (124 us for 119 with 80 of 1,022 tiles, 112 for 107 with 96 of 782)
+    static constexpr int kTurnedV = NG == 2 || NG >= 5 ? 1 : 2;
     static constexpr int kWeights = NG == 8 ? 1 : 2;           // tiles of weights in shared memory
     // heads of q in shared memory: with two the next one's is prepared ahead by a warp of its
     // own (56.7 us for 53.4 without, at 4 rows of 4 slots), else the weights' many warps prepare
