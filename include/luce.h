@@ -108,6 +108,7 @@ int luce_wait_timeouts(uint32_t* count, int reset);
  */
 int luce_test_wait_expiry(int64_t limit_ns, void* stream);
 int luce_test_tree_wait_expiry(int64_t limit_ns, void* stream); /* the same, counted by the attention of draft trees */
+int luce_test_q8kv_wait_expiry(int64_t limit_ns, void* stream); /* the same, counted by the one over caches in 8 bits */
 
 /*
  * Activation quantization to q8_0 blocks [qfuse, item 2: the consumer's

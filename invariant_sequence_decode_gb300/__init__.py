@@ -151,7 +151,7 @@ EXPORTS = ("luce_last_error", "luce_version", "luce_launch_count", "luce_q8_quan
            "luce_decode_attn_workspace_size", "luce_decode_step_layout", "luce_decode_step",
            "luce_decode_attn_multiseq_noalloc", "luce_decode_attn_noalloc_max_bytes", "luce_decode_attn_paged",
            "luce_decode_step_paged", "luce_wait_timeouts", "luce_decode_step_host",
-           "luce_test_wait_expiry", "luce_test_tree_wait_expiry", "luce_q8_matvec_batch_path", "luce_q8_quantize_act_f16", "luce_rmsnorm_q8",
+           "luce_test_wait_expiry", "luce_test_tree_wait_expiry", "luce_test_q8kv_wait_expiry", "luce_q8_matvec_batch_path", "luce_q8_quantize_act_f16", "luce_rmsnorm_q8",
            "luce_swiglu_q8", "luce_step_graph_create", "luce_step_graph_run", "luce_step_graph_stats",
            "luce_step_graph_destroy", "luce_tree_attn", "luce_tree_attn_paged", "luce_tree_attn_workspace_size",
            "luce_tree_commit", "luce_kv_evict", "luce_decode_step_tree", "luce_decode_step_tree_layout",
@@ -200,6 +200,7 @@ def load_library(path: str = LIB_PATH):
     lib.luce_wait_timeouts.argtypes = [ctypes.POINTER(ctypes.c_uint32), i32]
     lib.luce_test_wait_expiry.argtypes = [i64, vp]
     lib.luce_test_tree_wait_expiry.argtypes = [i64, vp]
+    lib.luce_test_q8kv_wait_expiry.argtypes = [i64, vp]
     lib.luce_decode_step_host.argtypes = [ctypes.POINTER(ModelC), ctypes.POINTER(SlotC), ctypes.POINTER(ctypes.c_int32),
                                           i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.luce_step_graph_create.argtypes = [ctypes.POINTER(ModelC), ctypes.POINTER(SlotC),

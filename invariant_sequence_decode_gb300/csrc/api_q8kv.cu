@@ -200,6 +200,13 @@ int luce_q8kv_attn(const float* q, const luce_q8kv_view* views, int n_seq, int H
     return cuda_status(launch_q8kv_attention(q, b, Hq, Hkv, scale, ws, out, (cudaStream_t)stream), who);
 }
 
+int luce_test_q8kv_wait_expiry(int64_t limit_ns, void* stream)
+{
+    REQUIRE(limit_ns >= 1000 && limit_ns <= 1000000000, LUCE_EINVAL,
+            "test_q8kv_wait_expiry: limit_ns=%lld outside 1 us .. 1 s", (long long)limit_ns);
+    return cuda_status(launch_q8kv_wait_expiry((uint64_t)limit_ns, (cudaStream_t)stream), "test_q8kv_wait_expiry");
+}
+
 int luce::add_q8kv_view(Q8Batch& b, int s, const luce_q8kv_view& v, int Hkv, bool* covered, const char* who)
 {
     REQUIRE(v.k && v.v && aligned(v.k, 16) && aligned(v.v, 16), LUCE_EINVAL, "%s: view %d tail null or not 16-byte aligned", who, s);

@@ -1011,6 +1011,22 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
     if (warp == S::kWarps + 10) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kTmem));
 }
 
+__global__ void q8kv_wait_expiry_kernel(uint64_t limit_ns)
+{
+    __shared__ uint64_t bar;
+    if (threadIdx.x != 0) return;
+    mbar_init(&bar, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    mbar_wait(&bar, 0, &g_q8kv_wait_timeouts, limit_ns);
+}
+
+cudaError_t launch_q8kv_wait_expiry(uint64_t limit_ns, cudaStream_t s)
+{
+    q8kv_wait_expiry_kernel<<<1, 32, 0, s>>>(limit_ns);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
 cudaError_t read_q8kv_wait_timeouts(uint32_t* count, bool reset)
 {
     cudaError_t e = cudaMemcpyFromSymbol(count, g_q8kv_wait_timeouts, sizeof(uint32_t));

@@ -67,8 +67,9 @@ size_t q8kv_part_bytes(int64_t n_part);
 cudaError_t launch_q8kv_attention(const float* q, const Q8Batch& b, int Hq, int Hkv, float scale, void* part, float* out,
                                   cudaStream_t s);
 
-// Bounded waits of that attention that expired on the current device.
+// Bounded waits of that attention that expired on the current device; one that does.
 cudaError_t read_q8kv_wait_timeouts(uint32_t* count, bool reset);
+cudaError_t launch_q8kv_wait_expiry(uint64_t limit_ns, cudaStream_t s);
 
 // A slot whose tail's whole blocks are sealed, in every (layer, KV head) lh: row
 // i of the tail is at (lh * cap + i) * 128, a page's codes at (page * heads + lh) *

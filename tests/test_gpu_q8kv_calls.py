@@ -134,3 +134,13 @@ def test_sealing_then_attending_needs_no_wait_between():
     for i in range(3, 30):
         assert np.array_equal(bits(outs[i]), bits(outs[i % 3]))
     assert not np.array_equal(bits(outs[1]), first)
+
+
+def test_an_expired_wait_is_counted_and_the_context_stays_usable(lib):  # noqa: F811
+    rng = np.random.default_rng(26)
+    s = Cache(rng, 40, 8, 1024, 5, chain(3))
+    want = bits(run([s], [s.flat()], 8))                       # (no wait expired)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert lib.luce_test_q8kv_wait_expiry(1_000_000, stream) == lib.luce_test_tree_wait_expiry(1_000_000, stream) == 0
+    assert luce.wait_timeouts(reset=True) == 2
+    assert np.array_equal(bits(run([s], [s.flat()], 8)), want)

@@ -144,3 +144,8 @@ def test_sizes_that_pass_64_bits(lib):
     assert project(lib, ld=1 << 62) == E and b"2^28" in lib.luce_last_error()
     assert seal(lib, [slot(pages=2 ** 31 - 1)], L=1 << 19) == E and b"out of range" in lib.luce_last_error()
     assert attn(lib, [view(pages=2 ** 31 - 1, page=1 << 37)]) == E and b"out of range" in lib.luce_last_error()
+
+
+def test_wait_expiry_refuses_limits(lib):
+    for bad in (0, 999, 1_000_000_001, -1):
+        assert lib.luce_test_q8kv_wait_expiry(bad, None) == E and b"limit_ns" in lib.luce_last_error()
