@@ -22,7 +22,7 @@
 // hold the turned tile as well.
 //
 // What bounds it.  A tile is 33 KB and 1,430 cycles of an SM's share of the copy rate.
-// Its codes are turned at 4 bytes for 6 instructions: of the 4,700 warp instructions a
+// Its codes are turned at 4 bytes for 6 instructions: of the 4,500 warp instructions a
 // tile with up to 16 rows costs, 1,900 turn, 400 form weights, 200 issue products; issue
 // slots are taken to 59 %, and most of the rest is instruction fetch, as warps of six kinds
 // run code of their own, and latency within the weights' warps, of which a scheduler has one
