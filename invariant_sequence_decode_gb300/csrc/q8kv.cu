@@ -887,8 +887,10 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                     const float ks = valid ? sc[quad] : 0.0f;
                     // V's scale goes into the weights as a power of two: 2^(s + log2 vs - m) is
                     // what multiplies a code, and over vs the weight itself.  (A block of zeros
-                    // weighs as one of the smallest scale, 2^-31.)
-                    const float vs = fmaxf(valid ? sc[4 + quad] : 0.0f, 4.656612873e-10f);
+                    // weighs as one of the smallest scale, 2^-31.  A block that no row sees may have
+                    // any scale: NaN becomes the smallest, infinity the largest, whose logarithm is
+                    // finite, so that its scores of -inf give weights of 0.)
+                    const float vs = fminf(fmaxf(valid ? sc[4 + quad] : 0.0f, 4.656612873e-10f), 3.402823466e38f);
                     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lv[x]) : "f"(vs));
                     if (!valid) lv[x] = -INFINITY;  // (whatever its scores are)
                     iv[x] = __frcp_rn(vs);
