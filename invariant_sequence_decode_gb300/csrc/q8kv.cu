@@ -57,6 +57,14 @@ constexpr int kQ8Ctas = 304;  // the CTAs that a cut aims at
 // reason, f16 has no digits below 2^-24.
 constexpr float kQ8Up = 15.0f, kQ8Down = 1.0f / 32768.0f;
 
+// The smallest scale of V that weights are formed with, 2^-60 (sealing gives 0 or 2^-24 / 127
+// and more): a block of zeros weighs as one of this scale, and next to one of scale 2^40, the
+// largest, a key's weight of 2^-41 of the largest, below which 2^17 keys leave the
+// sum's digits as they are, is 2^(15 - 60 - 40 - 41) = 2^-126, the smallest normal number.
+// (The weights of smaller scales times what is missing, where there are any: 12.6 -> 12.9
+// us on 4x1 serving and 52.9 -> 53.7 on long paged, by the code's size alone.)
+constexpr float kQ8LeastV = 8.673617379884035e-19f;
+
 // Scores in powers of two: e^(s - m) = 2^(log2 dot - max).  The scale's sign goes
 // into q.
 struct Q8Scale {
@@ -887,10 +895,10 @@ q8kv_chunk_kernel(const __grid_constant__ Q8Maps maps, const float* q, const __g
                     const float ks = valid ? sc[quad] : 0.0f;
                     // V's scale goes into the weights as a power of two: 2^(s + log2 vs - m) is
                     // what multiplies a code, and over vs the weight itself.  (A block of zeros
-                    // weighs as one of the smallest scale, 2^-31.  A block that no row sees may have
+                    // weighs as one of the smallest scale.  A block that no row sees may have
                     // any scale: NaN becomes the smallest, infinity the largest, whose logarithm is
                     // finite, so that its scores of -inf give weights of 0.)
-                    const float vs = fminf(fmaxf(valid ? sc[4 + quad] : 0.0f, 4.656612873e-10f), 3.402823466e38f);
+                    const float vs = fminf(fmaxf(valid ? sc[4 + quad] : 0.0f, kQ8LeastV), 3.402823466e38f);
                     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lv[x]) : "f"(vs));
                     if (!valid) lv[x] = -INFINITY;  // (whatever its scores are)
                     iv[x] = __frcp_rn(vs);
