@@ -560,8 +560,9 @@ __device__ __forceinline__ void q8_prepare(const float* q, const Q8Batch& b, con
                           fmaxf(fmaxf(fabsf(y0.x), fabsf(y0.y)), fmaxf(fabsf(y0.z), fabsf(y0.w))));
 #pragma unroll
         for (int d = 1; d < 16; d <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
-        // the row's unit puts its largest element into [2^14, 2^15)
-        const int exp = max((__float_as_int(big) >> 23) - 127 - 14, -112);
+        // the row's unit puts its largest element into [2^14, 2^15), the smallest normal
+        // numbers and what is below them, whose own digits end at 2^-149, into 2^0 and less
+        const int exp = max((__float_as_int(big) >> 23) - 127 - 14, -126);
         const float into = __fmul_rn(scale.sign, __int_as_float((127 - exp) << 23));
         uint4 hi, lo;
         tree_split(__fmul_rn(x0.x, into), __fmul_rn(x0.y, into), hi.x, lo.x);
