@@ -810,7 +810,8 @@ typedef struct luce_q8kv_slot {
  * left as they were.  The caller continues with sealed + len / 32 * 32
  * keys in blocks and a tail of len % 32.  An entry of table outside [0, n_pages):
  * its blocks are not written.  Slots may share pools, no page is named twice
- * at spans that the call writes; other arrays overlap nothing.
+ * at spans that the call writes (LUCE_EINVAL where two slots have the same table, or none, and
+ * would write the same keys); other arrays overlap nothing.
  * sealed + len <= LUCE_MAX_KEYS, D == 128, 1 <= n_seq <= LUCE_MAX_SEQ.
  */
 int luce_q8kv_seal(const luce_q8kv_slot* slots, int n_seq, int n_layers, int Hkv, int D, void* stream);

@@ -134,6 +134,15 @@ int luce_q8kv_seal(const luce_q8kv_slot* slots, int n_seq, int n_layers, int Hkv
         o.scales = c.scales;
         o.table = c.table;
         o.n_pages = c.n_pages;
+        // (of slots that share pools, what the host can see: through one table, or none, a key
+        // has one place)
+        for (int e = 0; e < s; ++e) {
+            const luce_q8kv_slot& d = slots[e];
+            const int end = d.sealed + d.len / LUCE_Q8KV_BLOCK * LUCE_Q8KV_BLOCK;
+            const bool shared = c.table == d.table && (c.k_codes == d.k_codes || c.v_codes == d.v_codes || c.scales == d.scales);
+            REQUIRE(!shared || end == d.sealed || c.sealed >= end || d.sealed >= c.sealed + whole, LUCE_EINVAL,
+                    "%s: slots %d and %d would write the same blocks of one pool", who, e, s);
+        }
         add_pool(r, &nr, c.k_codes, heads * kQ8PageBytes * c.n_pages, s, "K codes");
         add_pool(r, &nr, c.v_codes, heads * kQ8PageBytes * c.n_pages, s, "V codes");
         add_pool(r, &nr, c.scales, heads * kQ8PageScales * 4 * c.n_pages, s, "scales");
