@@ -1475,7 +1475,7 @@ def _page_stride(t, per_page, name):
         raise ValueError(f"{name}: each page of a layer must be contiguous")
     if t.shape[0] <= 1:
         return 0
-    if t.stride(0) % per_page:
+    if t.stride(0) == 0 or t.stride(0) % per_page:  # (0 would mean pages in a row to the library)
         raise ValueError(f"{name}: pages must be apart by a multiple of {per_page} elements")
     return t.stride(0)
 

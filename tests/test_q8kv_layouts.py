@@ -1,0 +1,61 @@
+"""Layouts and numbers that the prepared calls over caches in 8 bits refuse or hand on, seen by a stand-in for
+the library: no device needed, the tensors lie on the host."""
+import ctypes
+
+import pytest
+
+torch = pytest.importorskip("torch")
+import invariant_sequence_decode_gb300 as luce  # noqa: E402
+from test_prepared_calls import library, prepared, record  # noqa: E402,F401
+from test_q8kv_prepared import q8_slot  # noqa: E402
+
+i32 = ctypes.c_int32
+
+
+@pytest.fixture
+def host(prepared, monkeypatch):  # noqa: F811
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True)
+    prepared.luce_q8kv_attn_workspace_size = lambda *a: 1000
+    return prepared
+
+
+def attention(host, fields=("page_stride", "n_pages")):
+    """(make a prepared call of one view, what the library saw)."""
+    seen = []
+
+    def call(q, views, n, Hq, Hkv, D, scale, out, ws, ws_bytes, stream):
+        seen.append(tuple(getattr(views[0], f) for f in fields))
+        return 0
+
+    call.argtypes = [ctypes.c_void_p, None, i32, i32, i32, i32, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+    host.luce_q8kv_attn = call
+    return lambda view: luce.Q8Attention(torch.zeros(1, 4, 128), [view], 2, 0.1), seen
+
+
+def pools(n_pages, layers=1):
+    return [torch.zeros(n_pages, layers, 2, 128, 128, dtype=torch.int8) for _ in range(2)] + [torch.zeros(n_pages, layers, 2, 2, 4)]
+
+
+def view_of(k_codes, v_codes, scales, **kw):
+    tail = torch.zeros(2, 8, 128, dtype=torch.float16)
+    return luce.Q8View(k_codes, v_codes, scales, 32, tail, tail.clone(), **kw)
+
+
+def test_pages_that_lie_on_one_another_are_refused(host):
+    """One page expanded to several has a stride of 0 from page to page, which the library takes as pages in a row."""
+    make, seen = attention(host)
+    one = [p[:, 0] for p in pools(1)]
+    with pytest.raises(ValueError, match="apart"):
+        make(view_of(*(p.expand(3, *p.shape[1:]) for p in one)))
+    with pytest.raises(ValueError, match="apart"):
+        make(view_of(*(p.expand(3, *p.shape[1:]) for p in one), table=torch.zeros(2, dtype=torch.int32)))
+    many = [p[:, 0] for p in pools(3)]
+    with pytest.raises(ValueError, match="apart"):
+        make(view_of(many[0], many[1], one[2].expand(3, -1, -1, -1)))
+    run = make(view_of(*many))
+    run()
+    run = make(view_of(*(p[:, 1] for p in pools(3, layers=4))))
+    run()
+    run = make(view_of(*one))
+    run()
+    assert seen == [(2 * 128 * 128, 3), (4 * 2 * 128 * 128, 3), (0, 1)]
