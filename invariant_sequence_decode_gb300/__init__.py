@@ -1057,6 +1057,8 @@ class TreeAttention(_Prepared):
             if v.k_pool.shape[1:] != page or stride[2] != HEAD_DIM or (Hkv > 1 and stride[1] != PAGE_KEYS * HEAD_DIM):
                 raise ValueError(f"views[{i}]: expected pools [n_pages][{Hkv}][128][128], each page contiguous")
             c.page_stride = stride[0] if v.k_pool.shape[0] > 1 else 0
+            if c.page_stride == 0 and v.k_pool.shape[0] > 1:  # (0 means pages in a row to the library)
+                raise ValueError(f"views[{i}]: the pools' pages lie on one another")
             _same_device(self._q, v.k_pool, v.v_pool, v.table)
             self._caps[i] = min(v.table.numel() * PAGE_KEYS, MAX_KEYS)
             c.k_pool, c.v_pool, c.table, c.n_pages = v.k_pool.data_ptr(), v.v_pool.data_ptr(), v.table.data_ptr(), v.k_pool.shape[0]
