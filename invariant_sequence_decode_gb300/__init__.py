@@ -1553,6 +1553,7 @@ class Q8Attention(_Prepared):
 
     def _take_sizes(self, i, v):
         c, tree = self._items[i], self._trees[i]
+        self._seen[i] = (*self._seen[i][:-1], None)  # (until all is checked)
         kind = v.parent.__class__ if v.parent.__class__ in (int, list, tuple) else None
         if tree is None or kind is None or kind is not tree[0] or v.parent != tree[1]:
             nn, par = _tree(v.parent)
@@ -1760,10 +1761,10 @@ class QkNormRope(_Prepared):
                 now = self._take(i, v)
             if (v.len, v.n_q, v.row0) != now:
                 c = self._items[i]
-                c.len, c.n_q, c.row0 = v.len, v.n_q, v.row0
                 rows = max(x.row0 + x.n_q for x in self.views)
                 if rows != self._T:
                     raise ValueError(f"qkv has {self._T} rows, the views name {rows}")
+                c.len, c.n_q, c.row0 = v.len, v.n_q, v.row0
                 self._seen[i] = (i, v, v.k, v.v, (v.len, v.n_q, v.row0))
         self._call()
         return self.out

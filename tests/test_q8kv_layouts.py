@@ -59,3 +59,46 @@ def test_pages_that_lie_on_one_another_are_refused(host):
     run = make(view_of(*one))
     run()
     assert seen == [(2 * 128 * 128, 3), (4 * 2 * 128 * 128, 3), (0, 1)]
+
+
+def test_a_view_put_right_after_a_refusal_is_taken_again(host):
+    """What a refused call has handed to the library's structs of a view does not stay there."""
+    make, seen = attention(host, ("sealed", "len", "n_nodes", "row0"))
+    view = view_of(*(p[:, 0] for p in pools(3)), len=2)
+    run = make(view)
+    run()
+    view.parent, view.sealed = 4, 4096                   # more keys than the pages hold, and another tree
+    with pytest.raises(ValueError, match="pages hold"):
+        run()
+    view.parent, view.sealed = 1, 32
+    run()
+    view.parent = [-1, 0]                                # a row too many
+    with pytest.raises(ValueError, match="rows"):
+        run()
+    view.parent = 1
+    run()
+    assert seen == [(32, 2, 1, 0)] * 3
+
+
+def test_a_projection_put_right_after_a_refusal_is_taken_again(host):
+    seen = []
+
+    def call(qkv, ld, views, n, *rest):
+        seen.append(tuple((v.len, v.n_q, v.row0) for v in views))
+        return 0
+
+    vp = ctypes.c_void_p
+    call.argtypes = [vp, ctypes.c_int64, None, i32, i32, i32, i32, vp, vp, ctypes.c_float, vp, i32, vp, ctypes.c_double, vp, vp]
+    host.luce_qk_norm_rope = call
+    cache = lambda: torch.zeros(2, 16, 128, dtype=torch.float16)  # noqa: E731
+    views = [luce.SeqView(cache(), cache(), 9, 4, 0), luce.SeqView(cache(), cache(), 5, 5, 4)]
+    run = luce.QkNormRope(torch.zeros(9, 8 * 128), views, 4, torch.zeros(9, dtype=torch.int32), 1e4)
+    run()
+    views[1].n_q = views[1].len = 4                      # a row too few
+    with pytest.raises(ValueError, match="rows"):
+        run()
+    views[1].n_q = views[1].len = 5
+    run()
+    views[0].n_q, views[1].row0, views[1].n_q = 5, 5, 4  # another split of the same rows
+    run()
+    assert seen == [((9, 4, 0), (5, 5, 4))] * 2 + [((9, 5, 0), (5, 4, 5))]
