@@ -913,6 +913,14 @@ def _tree(parent):
     return len(p), (ctypes.c_int32 * max(1, len(p)))(*p)
 
 
+def _int32(values, fields, name):
+    """The numbers as they are; ctypes cuts one that a struct's 32 bits do not hold to its low bits without a word."""
+    if not -2 ** 31 <= min(values) <= max(values) < 2 ** 31:
+        field, v = next((f, v) for f, v in zip(fields, values) if not -2 ** 31 <= v < 2 ** 31)
+        raise ValueError(f"{name}.{field}: {v} does not fit in 32 bits")
+    return values
+
+
 def _same_device(first, *tensors):
     for t in tensors:
         if t is not None and t.device != first.device:
@@ -1557,14 +1565,16 @@ class Q8Attention(_Prepared):
         kind = v.parent.__class__ if v.parent.__class__ in (int, list, tuple) else None
         if tree is None or kind is None or kind is not tree[0] or v.parent != tree[1]:
             nn, par = _tree(v.parent)
+            (c.n_nodes,) = _int32((nn,), ("parent",), f"views[{i}]")
             self._trees[i] = (kind, list(v.parent) if kind is list else v.parent, par)
-            c.n_nodes, c.parent = nn, par
+            c.parent = par
             self._rows = None
         if v.sealed > self._caps[i]:
             raise ValueError(f"views[{i}]: {v.sealed} sealed keys exceed the {self._caps[i]} that its pages hold")
         if v.row0 != c.row0:
             self._rows = None
-        c.sealed, c.len, c.row0, c.window, c.sinks = v.sealed, v.len, v.row0, v.window, v.sinks
+        c.sealed, c.len, c.row0, c.window, c.sinks = _int32((v.sealed, v.len, v.row0, v.window, v.sinks),
+                                                            ("sealed", "len", "row0", "window", "sinks"), f"views[{i}]")
         self._seen[i] = (*self._seen[i][:-1], (v.sealed, v.len, v.row0, v.window, v.sinks, v.parent if kind is int else None))
 
     def _check_rows(self):
@@ -1661,7 +1671,7 @@ class Q8Seal(_Prepared):
         if s.sealed + s.len // Q8_BLOCK * Q8_BLOCK > self._caps[i]:
             raise ValueError(f"slots[{i}]: its pages hold {self._caps[i]} keys, {s.sealed} + {s.len // Q8_BLOCK * Q8_BLOCK} come")
         c = self._items[i]
-        c.len, c.sealed = s.len, s.sealed
+        c.len, c.sealed = _int32((s.len, s.sealed), ("len", "sealed"), f"slots[{i}]")
         self._seen[i] = (*self._seen[i][:-1], (s.len, s.sealed))
 
     def __call__(self):
@@ -1760,11 +1770,11 @@ class QkNormRope(_Prepared):
             if v.k is not k or v.v is not vv:
                 now = self._take(i, v)
             if (v.len, v.n_q, v.row0) != now:
-                c = self._items[i]
                 rows = max(x.row0 + x.n_q for x in self.views)
                 if rows != self._T:
                     raise ValueError(f"qkv has {self._T} rows, the views name {rows}")
-                c.len, c.n_q, c.row0 = v.len, v.n_q, v.row0
+                c = self._items[i]
+                c.len, c.n_q, c.row0 = _int32((v.len, v.n_q, v.row0), ("len", "n_q", "row0"), f"views[{i}]")
                 self._seen[i] = (i, v, v.k, v.v, (v.len, v.n_q, v.row0))
         self._call()
         return self.out

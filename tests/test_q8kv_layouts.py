@@ -102,3 +102,66 @@ def test_a_projection_put_right_after_a_refusal_is_taken_again(host):
     views[0].n_q, views[1].row0, views[1].n_q = 5, 5, 4  # another split of the same rows
     run()
     assert seen == [((9, 4, 0), (5, 5, 4))] * 2 + [((9, 5, 0), (5, 4, 5))]
+
+
+BIG = 2 ** 32
+
+
+@pytest.mark.parametrize("field,value", [("sinks", BIG), ("window", BIG + 4096), ("len", BIG + 2), ("row0", -BIG), ("sealed", -BIG + 32),
+                                         ("parent", BIG + 1), ("window", 2 ** 31)])
+def test_numbers_of_a_view_that_32_bits_do_not_hold_are_refused(host, field, value):
+    """(sinks of 2^32, meant as all keys, would be none)"""
+    make, seen = attention(host, ("sealed", "len", "n_nodes", "row0", "window", "sinks"))
+    view = view_of(*(p[:, 0] for p in pools(3)), len=2, window=100, sinks=3)
+    run = make(view)
+    run()
+    was = getattr(view, field)
+    setattr(view, field, value)
+    for _ in range(2):
+        with pytest.raises(ValueError, match="32 bits"):
+            run()
+    setattr(view, field, was)
+    run()
+    assert seen == [(32, 2, 1, 0, 100, 3)] * 2
+    setattr(view, field, value)
+    with pytest.raises(ValueError, match="32 bits"):
+        make(view)
+
+
+def test_numbers_of_a_slot_that_32_bits_do_not_hold_are_refused(host):
+    seen = record(host, "luce_q8kv_seal", ("len", "sealed"), [None, i32, i32, i32, i32, None])
+    slot = q8_slot(40, 64)
+    seal = luce.Q8Seal([slot])
+    for field, value in (("len", -BIG + 40), ("sealed", -BIG), ("sealed", -BIG + 64)):
+        was = getattr(slot, field)
+        setattr(slot, field, value)
+        for _ in range(2):
+            with pytest.raises(ValueError, match="32 bits"):
+                seal()
+        setattr(slot, field, was)
+    seal()
+    assert seen == [(40, 64)]
+
+
+def test_numbers_of_a_projection_that_32_bits_do_not_hold_are_refused(host):
+    seen = []
+
+    def call(qkv, ld, views, n, *rest):
+        seen.append((views[0].len, views[0].n_q, views[0].row0))
+        return 0
+
+    vp = ctypes.c_void_p
+    call.argtypes = [vp, ctypes.c_int64, None, i32, i32, i32, i32, vp, vp, ctypes.c_float, vp, i32, vp, ctypes.c_double, vp, vp]
+    host.luce_qk_norm_rope = call
+    view = luce.SeqView(*(torch.zeros(2, 16, 128, dtype=torch.float16) for _ in range(2)), 9, 4, 0)
+    run = luce.QkNormRope(torch.zeros(4, 8 * 128), [view], 4, torch.zeros(4, dtype=torch.int32), 1e4)
+    view.len = BIG + 9
+    with pytest.raises(ValueError, match="32 bits"):
+        run()
+    view.len = 9
+    view.n_q, view.row0 = 4 - BIG, BIG                   # 4 rows, by their sum
+    with pytest.raises(ValueError, match="32 bits"):
+        run()
+    view.n_q, view.row0 = 4, 0
+    run()
+    assert seen == [(9, 4, 0)]
