@@ -997,7 +997,7 @@ class _Prepared:
             _check(rc)
 
 
-_NOTHING = (None,) * 8  # what no view holds
+_NOTHING = (object(),) * 8  # what no view holds
 
 
 class TreeAttention(_Prepared):
@@ -1757,7 +1757,7 @@ class QkNormRope(_Prepared):
     def _take(self, i, v):
         """View i's caches."""
         c, name = self._items[i], f"views[{i}]"
-        self._seen[i] = (i, v, None, None, None)  # (until all is checked)
+        self._seen[i] = (i, v, *_NOTHING[:2], None)  # (until all is checked)
         _kv_pair(v.k, v.v, 3, name)
         if v.k.shape[0] != self._Hkv:
             raise ValueError(f"{name}: {v.k.shape[0]} heads, expected {self._Hkv}")
