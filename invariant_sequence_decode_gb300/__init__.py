@@ -1423,7 +1423,7 @@ def q8_cache(n_pages: int, n_layers: int, n_kv_heads: int, device="cuda"):
     shape = (n_pages, n_layers, n_kv_heads)
     return (torch.zeros(*shape, PAGE_KEYS, HEAD_DIM, dtype=torch.int8, device=device),
             torch.zeros(*shape, HEAD_DIM, PAGE_KEYS, dtype=torch.int8, device=device),
-            torch.zeros(*shape, 2, PAGE_KEYS // Q8_BLOCK, device=device))
+            torch.zeros(*shape, 2, PAGE_KEYS // Q8_BLOCK, dtype=torch.float32, device=device))
 
 
 @dataclass
