@@ -885,7 +885,8 @@ size_t luce_q8kv_attn_workspace_size(int n_rows, int Hq, int Hkv, int D, int max
  *   pos (device) int32 [n_axes][T];  pair_axis (host) [D/2], each < n_axes, or
  *       NULL for one axis
  *   q   (device) fp32 [T][Hq][D], 16-byte aligned
- * The views name every row 0 .. T-1 once; nothing written overlaps anything else.
+ * The views name every row 0 .. T-1 once; nothing written overlaps anything else (caches of
+ * the same strides may lie between one another's heads or rows; of unlike strides, side by side).
  * D == 128, 1 <= n_axes <= LUCE_MAX_AXES, 1 <= n_seq <= LUCE_MAX_SEQ.
  */
 #define LUCE_MAX_AXES 4

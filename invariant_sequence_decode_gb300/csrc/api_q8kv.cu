@@ -2,6 +2,7 @@
 // rotates and appends a projection's rows, sealing, attention (see
 // include/luce.h for the contract).
 #include <math.h>
+#include <stdlib.h>
 
 #include <algorithm>
 
@@ -16,6 +17,42 @@ using namespace luce;
 static_assert(LUCE_Q8KV_BLOCK == kQ8Block && LUCE_Q8KV_MAX_TAIL == kQ8MaxTail && LUCE_PAGE_KEYS == kQ8Page, "sizes of the cache");
 
 // ------------------------------------------------------------ projection
+
+namespace {
+
+// What a view's rows write of one cache: n rows of D values in each head.
+struct CacheRows {
+    const __half* at;
+    int64_t head_stride, tok_stride;
+    int heads, n;
+    const char* what;
+
+    ByteRange hull(int slot) const
+    {
+        return range_of(at, (head_stride * (heads - 1) + tok_stride * (n - 1) + LUCE_HEAD_DIM) * 2, slot, what, true);
+    }
+};
+
+// Whether two of them share a value.  Slots' caches may lie between one another's heads (slices
+// of one pool along its tokens) or rows, so where the strides are alike the rows are compared, not
+// what spans them: row (g, i) of a and (h, j) of b lie d + (h - g) head_stride + (j - i) tok_stride
+// apart, and as a head's rows fit its stride only the nearest differences can be small.
+bool rows_meet(const CacheRows& a, const CacheRows& b)
+{
+    const ByteRange x = a.hull(0), y = b.hull(0);
+    if (x.hi <= y.lo || y.hi <= x.lo) return false;
+    if (a.head_stride != b.head_stride || a.tok_stride != b.tok_stride) return true;
+    const int64_t d = ((int64_t)(uintptr_t)b.at - (int64_t)(uintptr_t)a.at) / 2;
+    const int64_t h0 = a.head_stride ? -d / a.head_stride : 0;
+    for (int64_t h = std::max<int64_t>(h0 - 1, 1 - a.heads); h <= std::min<int64_t>(h0 + 1, a.heads - 1); ++h) {
+        const int64_t e = d + h * a.head_stride, t0 = -e / a.tok_stride;
+        for (int64_t t = std::max<int64_t>(t0 - 1, 1 - a.n); t <= std::min<int64_t>(t0 + 1, b.n - 1); ++t)
+            if (std::abs(e + t * a.tok_stride) < LUCE_HEAD_DIM) return true;
+    }
+    return false;
+}
+
+}  // namespace
 
 int luce_qk_norm_rope(const float* qkv, int64_t ld, const luce_seqview* views, int n_seq, int Hq, int Hkv, int D,
                       const float* q_gamma, const float* k_gamma, float eps, const int32_t* pos, int n_axes,
@@ -43,8 +80,7 @@ int luce_qk_norm_rope(const float* qkv, int64_t ld, const luce_seqview* views, i
     AppendViews to{};
     to.n_view = n_seq;
     int64_t T = 0, rows = 0;
-    ByteRange r[2 * LUCE_MAX_SEQ + 5];
-    int nr = 0;
+    CacheRows written[2 * LUCE_MAX_SEQ];
     for (int s = 0; s < n_seq; ++s) {
         const luce_seqview& v = views[s];
         REQUIRE(v.k && v.v && aligned(v.k, 16) && aligned(v.v, 16), LUCE_EINVAL, "%s: view %d cache null or not 16-byte aligned",
@@ -71,18 +107,31 @@ int luce_qk_norm_rope(const float* qkv, int64_t ld, const luce_seqview* views, i
         a.row0 = v.row0;
         a.n = v.n_q;
         a.at0 = v.len - v.n_q;
-        const int64_t first = a.at0 * v.tok_stride, elems = a.head_stride * (Hkv - 1) + (v.n_q - 1) * v.tok_stride + D;
-        r[nr++] = range_of(a.k + first, elems * 2, s, "K cache", true);
-        r[nr++] = range_of(a.v + first, elems * 2, s, "V cache", true);
+        written[2 * s] = CacheRows{a.k + a.at0 * v.tok_stride, a.head_stride, v.tok_stride, Hkv, v.n_q, "K cache"};
+        written[2 * s + 1] = CacheRows{a.v + a.at0 * v.tok_stride, a.head_stride, v.tok_stride, Hkv, v.n_q, "V cache"};
+        for (int e = 0; e < 2 * s + 2; ++e)
+            for (int c = std::max(e + 1, 2 * s); c < 2 * s + 2; ++c)
+                REQUIRE(!rows_meet(written[e], written[c]), LUCE_EINVAL, "%s: the %s of slot %d overlaps the %s of slot %d", who,
+                        written[c].what, s, written[e].what, e / 2);
     }
     // (rows are apart, so as many of them as the highest number says cover all)
     REQUIRE(rows == T, LUCE_EINVAL, "%s: the views name %lld of %lld rows", who, (long long)rows, (long long)T);
+    ByteRange r[5];
+    int nr = 0;
     r[nr++] = range_of(qkv, ((T - 1) * ld + (int64_t)(Hq + 2 * Hkv) * D) * 4, -1, "projection", false);
     r[nr++] = range_of(q, T * Hq * D * 4, -1, "q", true);
     r[nr++] = range_of(pos, T * n_axes * 4, -1, "positions", false);
     if (q_gamma) r[nr++] = range_of(q_gamma, D * 4, -1, "q_gamma", false);
     if (k_gamma) r[nr++] = range_of(k_gamma, D * 4, -1, "k_gamma", false);
-    const int rc = check_apart(r, nr, who);
+    int rc = check_apart(r, nr, who);
+    for (int c = 0; c < 2 * n_seq && !rc; ++c) {
+        const ByteRange h = written[c].hull(c / 2);
+        for (int i = 0; i < nr && !rc; ++i) {
+            if (h.hi <= r[i].lo || r[i].hi <= h.lo) continue;
+            const ByteRange two[2] = {r[i], h};
+            rc = check_apart(two, 2, who);
+        }
+    }
     if (rc) return rc;
     return cuda_status(launch_qk_norm_rope(qkv, ld, (int)T, Hq, Hkv, to, q_gamma, k_gamma, eps, pos, axes, rope_freq(theta), q,
                                            (cudaStream_t)stream),
