@@ -18,10 +18,11 @@ __device__ __forceinline__ uint64_t tree_desc(uint32_t addr, uint32_t lbo, uint3
            (2ull << 61);
 }
 
-// D[128][128] (+)= A (tensor memory, f16) * B (shared memory), one 16-wide
-// step, by the lane whose `elected` is set.  The whole warp comes here: issued
-// from a branch of one thread, each product cost 152 cycles (its descriptor
-// goes through registers that only a converged warp has at hand) against 64.
+// D[128][N] (+)= A (tensor memory, f16) * B (shared memory), one 16-wide step, N
+// from idesc, by the lane whose `elected` is set.  The whole warp comes here: issued
+// from a branch of one thread, each product of the attention of draft trees (N = 128)
+// cost 152 cycles (its descriptor goes through registers that only a converged warp has
+// at hand) against 64.
 __device__ __forceinline__ void tree_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate,
                                          uint32_t elected)
 {
