@@ -1447,7 +1447,8 @@ class Q8View:
     [n_pages][Hkv][128][128], V's transposed) and scales (fp32 [n_pages][Hkv][2][4]), or the layer
     pool[:, l] of ``q8_cache``'s pools; ``len`` keys of the tail (fp16 [Hkv][cap][128]), node j of
     the tree ``parent`` (as in TreeView) at its row len + j.  ``window`` > 0: a row sees itself, the
-    window - 1 keys before it and the first ``sinks`` keys."""
+    window - 1 keys before it and the first ``sinks`` keys.  V's scales are 0 (of blocks of zeros) or
+    2^-60 .. 2^40; sealing's are."""
     k_codes: object
     v_codes: object
     scales: object

@@ -31,10 +31,10 @@
 // chain (load, turn, product, weights, product, sums) and of the merge.
 //
 // Measured (L2 flushed; with the merge): 4 one-token slots of 8 KV heads x 2,048 keys 12.6 us;
-// 4 slots of 4 nodes 15.1; 4 paged one-token slots of 16k to 33k keys (197 MB) 52.9, 3.7
-// TB/s; one slot of 16 nodes x 130,784 keys (269 MB, 43 GFLOP) 118, 2.3 TB/s and 0.36
-// PFLOP/s in one f16 part (twice that with both); 4 slots of 4 nodes, a window of 4,096
-// keys, 22.4.
+// 4 slots of 4 nodes 15.0; 4 paged one-token slots of 16k to 33k keys (197 MB) 53.0, 3.7
+// TB/s; one slot of 16 nodes x 130,784 keys (269 MB, 43 GFLOP) 119, 2.3 TB/s and 0.36
+// PFLOP/s in one f16 part (twice that with both; 102 us over an f16 cache); 4 slots of 4
+// nodes, a window of 4,096 keys, 22.3.
 #include <limits.h>
 
 #include <algorithm>
@@ -61,8 +61,8 @@ constexpr float kQ8Up = 15.0f, kQ8Down = 1.0f / 32768.0f;
 // and more): a block of zeros weighs as one of this scale, and next to one of scale 2^40, the
 // largest, a key's weight of 2^-41 of the largest, below which 2^17 keys leave the
 // sum's digits as they are, is 2^(15 - 60 - 40 - 41) = 2^-126, the smallest normal number.
-// (The weights of smaller scales times what is missing, where there are any: 12.6 -> 12.9
-// us on 4x1 serving and 52.9 -> 53.7 on long paged, by the code's size alone.)
+// (The weights of smaller scales times what is missing, where there are any: 12.6 -> 13.0
+// us on 4x1 serving and 52.8 -> 53.6 on long paged, although these never run that code.)
 constexpr float kQ8LeastV = 8.673617379884035e-19f;
 
 // Scores in powers of two: e^(s - m) = 2^(log2 dot - max).  The scale's sign goes

@@ -116,10 +116,11 @@ cudaError_t launch_kv_append(const float* k, const float* v, int64_t ld, int Hkv
 // a row's 64 cosines and sines and the gammas go once per CTA into shared memory, and
 // 16 lanes take a head, four pairs each as two 16-byte loads, kProjectAhead heads at a
 // time.  All loads of the first are under way before the angles (formed in 64-bit
-// arithmetic) and the sums are.  8,192 rows of 40 + 2 x 8 heads take 66.7 us, 6.5 TB/s,
+// arithmetic) and the sums are.  8,192 rows of 40 + 2 x 8 heads take 67.0 us, 6.5 TB/s,
 // 0.96 of a copy's rate; with four heads at a time 70.7, three 73.4, one 75.5, eight CTAs a
-// multiprocessor instead of six 74.1.  One row takes 4.6 us, latency.  Sums of squares: a lane's eight in order, then lanes by an xor
-// butterfly, so a row's bits do not depend on the other rows or the grid; without
+// multiprocessor instead of six 74.1.  One row takes 2.1 us in a graph, latency; its call
+// 4.6 to 5.0, the host's.  Sums of squares: a lane's eight in order, then lanes by an xor butterfly,
+// so a row's bits do not depend on the other rows or the grid; without
 // gammas and with one axis they are those of rope_posvec_kernel and kv_append_kernel.
 constexpr int kProjectAhead = 2;
 
@@ -229,7 +230,7 @@ cudaError_t launch_qk_norm_rope(const float* qkv, int64_t ld, int T, int Hq, int
 {
     // few rows: 16 heads a CTA, so that a row's heads go at once (40 + 2 x 8 heads, with the
     // launch: 6.8 us for 8.9 up to 40 rows, 8.9 for 10.9 at 152, no difference up to 456); many: a
-    // row a CTA, its angles formed once (608 rows 13.0 us for 15.0, 8,192 67.6 for 98.1)
+    // row a CTA, its angles formed once (608 rows 13.0 us for 15.0, 8,192 67 for 98)
     const int groups = T < 152 ? std::min((Hq + 2 * Hkv + 15) / 16, 65535) : 1;
     const cudaError_t e = launch_pdl(qk_norm_rope_kernel, dim3(T, groups), dim3(256), s, qkv, ld, Hq, Hkv, views, q_gamma,
                                      k_gamma, eps, pos, T, axes, f, q);
