@@ -856,8 +856,8 @@ typedef struct luce_q8kv_view {
  *       initial contents); calls that can overlap on the GPU need scratches of
  *       their own
  * q, scales and the tail's rows that a node sees must be finite, K's scales not negative,
- * V's 0 (of a block whose codes are 0) or 2^-60 .. 2^40, as luce_q8kv_seal's are (0 or 2^-31
- * .. 2^10); one below counts as 2^-60.  What lies where no row sees it is not used, whatever it is.  Sizes as luce_tree_attn, sealed + len
+ * V's 0 (of a block whose codes are 0) or 2^-50 .. 2^35, as luce_q8kv_seal's are (0 or 2^-31
+ * .. 2^10); one below counts as 2^-50.  What lies where no row sees it is not used, whatever it is.  Sizes as luce_tree_attn, sealed + len
  * + n_nodes <= LUCE_MAX_KEYS.  out and ws overlap nothing that the call reads or
  * writes (LUCE_EINVAL), but out may be q itself.
  */

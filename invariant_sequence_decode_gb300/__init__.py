@@ -1448,7 +1448,7 @@ class Q8View:
     pool[:, l] of ``q8_cache``'s pools; ``len`` keys of the tail (fp16 [Hkv][cap][128]), node j of
     the tree ``parent`` (as in TreeView) at its row len + j.  ``window`` > 0: a row sees itself, the
     window - 1 keys before it and the first ``sinks`` keys.  V's scales are 0 (of blocks of zeros) or
-    2^-60 .. 2^40; sealing's are."""
+    2^-50 .. 2^35; sealing's are."""
     k_codes: object
     v_codes: object
     scales: object

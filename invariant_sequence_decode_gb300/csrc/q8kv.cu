@@ -57,13 +57,14 @@ constexpr int kQ8Ctas = 304;  // the CTAs that a cut aims at
 // reason, f16 has no digits below 2^-24.
 constexpr float kQ8Up = 15.0f, kQ8Down = 1.0f / 32768.0f;
 
-// The smallest scale of V that weights are formed with, 2^-60 (sealing gives 0 or 2^-24 / 127
-// and more): a block of zeros weighs as one of this scale, and next to one of scale 2^40, the
+// The smallest scale of V that weights are formed with, 2^-50 (sealing gives 0 or 2^-24 / 127
+// and more): a block of zeros weighs as one of this scale, and next to one of scale 2^35, the
 // largest, a key's weight of 2^-41 of the largest, below which 2^17 keys leave the
-// sum's digits as they are, is 2^(15 - 60 - 40 - 41) = 2^-126, the smallest normal number.
+// sum's digits as they are, is 2^(15 - 50 - 35 - 41) = 2^-111 in a chunk, and its chunk's factor in
+// the merge 2^(-50 - 35 - 41) = 2^-126, the smallest normal number.
 // (The weights of smaller scales times what is missing, where there are any: 12.6 -> 13.0
 // us on 4x1 serving and 52.8 -> 53.6 on long paged, although these never run that code.)
-constexpr float kQ8LeastV = 8.673617379884035e-19f;
+constexpr float kQ8LeastV = 8.881784197001252e-16f;
 
 // Scores in powers of two: e^(s - m) = 2^(log2 dot - max).  The scale's sign goes
 // into q.
@@ -1155,7 +1156,7 @@ q8kv_merge_kernel(const float* q, const __grid_constant__ Q8Batch b, int Hq, int
         const float* ml = part_ml + 8 * (pr0 + c * pstep);
         const float4 x = ld_placed_cg_f4(ml + 4);
         ms[c] = ld_placed_f(ml);
-        ls[c] = __fadd_rn(__fadd_rn(x.x, x.y), __fadd_rn(x.z, x.w));
+        ls[c] = __fmul_rn(__fadd_rn(__fadd_rn(x.x, x.y), __fadd_rn(x.z, x.w)), kQ8Down);  // (here, as the factor may be small)
     }
     float4 ov[kQ8Ahead];
     auto load_o = [&](int j) {
@@ -1186,7 +1187,7 @@ q8kv_merge_kernel(const float* q, const __grid_constant__ Q8Batch b, int Hq, int
     for (int c = lane; c < nch; c += 32) M = fmaxf(M, ms[c]);
     for (int a = lane; a < n; a += 32) M = fmaxf(M, ps[a]);
     M = warp_max(M);  // (a row sees itself: there is one)
-    for (int c = lane; c < nch; c += 32) L = __fmaf_rn(ls[c], __fmul_rn(tree_exp2(__fsub_rn(ms[c], M)), kQ8Down), L);
+    for (int c = lane; c < nch; c += 32) L = __fmaf_rn(ls[c], tree_exp2(__fsub_rn(ms[c], M)), L);
     for (int a = lane; a < n; a += 32) L = __fadd_rn(L, tree_exp2(__fsub_rn(ps[a], M)));
     L = warp_sum_butterfly(L);
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);

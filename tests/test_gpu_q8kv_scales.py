@@ -5,7 +5,7 @@ import pytest
 
 import q8kv_reference as ref
 from cache_reference import chain
-from test_gpu_q8kv import SCALE, Cache, bits, lib, run  # noqa: F401
+from test_gpu_q8kv import D, SCALE, Cache, bits, lib, run  # noqa: F401
 from test_gpu_tree import tree_of
 
 pytest.importorskip("torch")
@@ -45,7 +45,7 @@ def near(s, got):
     assert np.linalg.norm(got - want) <= 1e-5 * np.linalg.norm(want)
 
 
-LEAST, MOST = 2.0 ** -60, 2.0 ** 40  # V's scales but 0
+LEAST, MOST = 2.0 ** -50, 2.0 ** 35  # V's scales but 0
 EDGES = [LEAST, float(np.nextafter(np.float32(LEAST), np.float32(1))), 1e-15, 1e-12, 2.0 ** -32, 2.0 ** -31, 2.0 ** -24 / 127, 1.0, MOST]
 
 
@@ -96,3 +96,27 @@ def test_zero_blocks_beside_large_scales_keep_their_weight(Hq, Hkv, n, large):
     s.vs[:, 1::2] = large
     s.v[:] = 0
     near(s, run([s], [s.flat()], Hkv))
+
+
+@pytest.fixture(scope="module")
+def longest():
+    return Cache(np.random.default_rng(7), 5, 1, 130784, 0, chain(1))
+
+
+@pytest.mark.parametrize("large", [1.0, 2.0 ** 10, MOST])
+@pytest.mark.parametrize("below", [3, 13, 27])
+def test_chunks_of_zeros_beside_a_large_scale_keep_their_weight(longest, below, large):
+    """One key of a large value, 2^below times as heavy as each of 130,783 keys of zeros in other chunks: at 2^27 these are
+    1e-3 of the sum of weights."""
+    s = longest
+    s.kc[:], s.ks[:], s.vc[:], s.vs[:] = 0, 1, 0, 0
+    s.k[:], s.v[:] = 0, 0
+    s.kc[:, 5, 3, 0] = below
+    s.vc[:, 5, 3], s.vs[:, 5] = np.arange(D) - 70, large
+    s.q[:] = 0
+    s.q[:, :, 0] = np.log(2) / SCALE
+    got = run([s], [s.flat()], 1).cpu().numpy().astype(np.float64)
+    w = 2.0 ** (below * float(np.float32(np.log(2) / SCALE)) * float(np.float32(SCALE)) / np.log(2))
+    want = np.repeat(s.vc[:, 5, 3].astype(np.float64) * large * w / (w + 130784), 5, 0)[None]
+    # (the score is one product of a scale's, exact parts: 2^-24 of `below`, and three numbers' roundings as above)
+    assert np.linalg.norm(got - want) <= 1e-5 * np.linalg.norm(want)
