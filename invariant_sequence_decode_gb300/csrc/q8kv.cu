@@ -32,7 +32,7 @@
 //
 // Measured (L2 flushed; with the merge): 4 one-token slots of 8 KV heads x 2,048 keys 12.6 us;
 // 4 slots of 4 nodes 15.0; 4 paged one-token slots of 16k to 33k keys (197 MB) 53.0, 3.7
-// TB/s; one slot of 16 nodes x 130,784 keys (269 MB, 43 GFLOP) 119, 2.3 TB/s and 0.36
+// TB/s; one slot of 16 nodes x 130,784 keys (269 MB, 43 GFLOP) 120, 2.2 TB/s and 0.36
 // PFLOP/s in one f16 part (twice that with both; 102 us over an f16 cache); 4 slots of 4
 // nodes, a window of 4,096 keys, 22.3.
 #include <limits.h>
